@@ -14,7 +14,7 @@ LIB_PATH = os.path.join(_PKG, "_build", "libmoe_gb300.so")
 _lock = threading.Lock()
 _lib = None
 
-P, I, U, SZ, LL = C.c_void_p, C.c_int, C.c_uint, C.c_size_t, C.c_longlong
+P, I, U, SZ, LL, FL = C.c_void_p, C.c_int, C.c_uint, C.c_size_t, C.c_longlong, C.c_float
 
 # name -> (restype, argtypes); names and argument order are those of include/moe_gb300.h
 SIGNATURES = {
@@ -54,6 +54,13 @@ SIGNATURES = {
     "moe_route_probs_bytes": (SZ, [I, I]),
     "moe_ep_recv_expert_ids": (I, [P, I, I, LL, P, P]),
     "moe_host_mapped_pointer": (I, [P, C.POINTER(C.c_void_p)]),
+    "moe_layer_few_tokens_workspace_size": (SZ, [I, I, I, I, I, I]),
+    "moe_layer_few_tokens": (I, [P, I, I, P, I, I, I, P, P, P, P, I, P, I, P, P, U, P, SZ, P]),
+    "moe_layer_norm": (I, [P, P, I, I, I, P, P, I, FL, P, P, P, P, P]),
+    "moe_layer_norm_backward_workspace_size": (SZ, [I, I]),
+    "moe_layer_norm_backward": (I, [P, P, I, I, I, P, I, P, P, P, P, P, P, P, SZ, P]),
+    "moe_grad_norm_workspace_size": (SZ, [I]),
+    "moe_grad_norm_clip": (I, [P, P, P, P, I, FL, FL, P, P, SZ, P]),
 }
 
 

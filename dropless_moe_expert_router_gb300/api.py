@@ -14,7 +14,7 @@ import torch
 
 from . import _lib
 
-MOE_I16, MOE_I32, MOE_BF16, MOE_MXFP8 = 0, 1, 2, 3
+MOE_I16, MOE_I32, MOE_BF16, MOE_MXFP8, MOE_F32 = 0, 1, 2, 3, 4
 MOE_ROUTE_RENORM = 1
 MOE_PERMUTE_FUSE_MXFP8 = 2
 MOE_QUANT_COLWISE = 4
@@ -686,3 +686,194 @@ def moe_grouped_gemm_wgrad(aT: torch.Tensor, aT_scales: Optional[torch.Tensor], 
         R_cap, _ptr(dw), _ptr(dw2 if split else None), _stream(stream))
     _check("moe_grouped_gemm_wgrad", st)
     return (dw, dw2) if split else dw
+
+
+# ---------------------------------------------------------- the layer for a few tokens
+def moe_layer_few_tokens_workspace(w: PackedWeights, T: int, K: int) -> torch.Tensor:
+    """The workspace of moe_layer_few_tokens for up to T tokens (uninitialised, reusable)."""
+    n = _lib.load().moe_layer_few_tokens_workspace_size(T, K, w.E, w.H, w.F, _dt_code(w.precision))
+    return torch.empty(int(n), dtype=torch.uint8, device=w.w13.device)
+
+
+def moe_layer_few_tokens(x: torch.Tensor, logits: Optional[torch.Tensor], w: PackedWeights, K: int, *,
+                         renorm: bool = False, id_dtype=torch.int32, ids: Optional[torch.Tensor] = None,
+                         probs: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """The whole layer for T <= 64 tokens: x [T, H] bf16, logits [T, E] fp32 -> (y [T, H] bf16,
+    ids [T, K], probs [T, K]). With logits None, ids and probs are the caller's routes instead."""
+    _want(x, "x", torch.bfloat16, 2)
+    T, H = x.shape
+    if H != w.H:
+        raise ValueError(f"x must have {w.H} columns")
+    if logits is not None:
+        _want(logits, "logits", torch.float32, 2)
+        if logits.shape[0] != T or logits.shape[1] != w.E:
+            raise ValueError("logits must be [T, E]")
+        if ids is None:
+            ids = torch.empty((T, K), dtype=id_dtype, device=x.device)
+        if probs is None:
+            probs = torch.empty((T, K), dtype=torch.float32, device=x.device)
+    elif ids is None or probs is None:
+        raise ValueError("without logits, ids and probs are inputs")
+    _want(ids, "ids", None, 2)
+    _want(probs, "probs", torch.float32, 2)
+    if tuple(ids.shape) != (T, K) or tuple(probs.shape) != (T, K):
+        raise ValueError("ids and probs must be [T, K]")
+    if y is None:
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    else:
+        _want(y, "y", torch.bfloat16, 2)
+        if tuple(y.shape) != (T, H):
+            raise ValueError("y must be [T, H]")
+    if workspace is None:
+        workspace = moe_layer_few_tokens_workspace(w, T, K)
+    st = _lib.load().moe_layer_few_tokens(
+        x.data_ptr(), T, H, None if logits is None else logits.data_ptr(), K, w.E, w.F, _ptr(w.w13),
+        _ptr(w.w13_scales), _ptr(w.w2), _ptr(w.w2_scales), _dt_code(w.precision), ids.data_ptr(), _id_code(ids.dtype),
+        probs.data_ptr(), y.data_ptr(), MOE_ROUTE_RENORM if renorm else 0, workspace.data_ptr(), workspace.numel(),
+        _stream(stream))
+    _check("moe_layer_few_tokens", st)
+    return y, ids, probs
+
+
+# ----------------------------------------------------------------- layer norm
+def _float_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return MOE_BF16
+    if t.dtype == torch.float32:
+        return MOE_F32
+    raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _like(t: Optional[torch.Tensor], ref: torch.Tensor, name: str, shape=None) -> None:
+    """t, where given, is a contiguous CUDA tensor of ref's type and of the shape (ref's by default)."""
+    if t is None:
+        return
+    _want(t, name, ref.dtype, None)
+    if t.shape != (ref.shape if shape is None else shape):
+        raise ValueError(f"{name} must be {list(ref.shape if shape is None else shape)}")
+
+
+class LayerNormed(NamedTuple):
+    y: torch.Tensor                 # [T, H]
+    sum: torch.Tensor               # [T, H] the normalised stream: x + residual (x itself without one)
+    mean: torch.Tensor              # [T] fp32
+    rstd: torch.Tensor              # [T] fp32
+
+
+def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, eps: float = 1e-5, *,
+                   residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                   sum: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+                   rstd: Optional[torch.Tensor] = None, stream=None) -> LayerNormed:
+    """Layer norm of x (+ residual) [T, H] bf16 or fp32 with weight (and bias) [H] bf16 or fp32."""
+    _want(x, "x", None, 2)
+    T, H = x.shape
+    code, wcode = _float_code(x, "x"), _float_code(weight, "weight")
+    _like(weight, weight, "weight", (H,))
+    _like(bias, weight, "bias", (H,))
+    _like(residual, x, "residual")
+    if residual is None and sum is not None:
+        raise ValueError("sum goes with residual")
+    for t, n in ((y, "y"), (sum, "sum")):
+        _like(t, x, n)
+    for t, n in ((mean, "mean"), (rstd, "rstd")):
+        if t is not None:
+            _want(t, n, torch.float32, 1)
+            if t.numel() != T:
+                raise ValueError(f"{n} must be [T]")
+    if y is None:
+        y = torch.empty_like(x)
+    if sum is None and residual is not None:
+        sum = torch.empty_like(x)
+    if mean is None:
+        mean = torch.empty((T,), dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty((T,), dtype=torch.float32, device=x.device)
+    st = _lib.load().moe_layer_norm(_ptr(x), _ptr(residual), T, H, code, _ptr(weight), _ptr(bias), wcode, eps, _ptr(sum),
+                                    _ptr(y), _ptr(mean), _ptr(rstd), _stream(stream))
+    _check("moe_layer_norm", st)
+    return LayerNormed(y, x if residual is None else sum, mean, rstd)
+
+
+def moe_layer_norm_backward_workspace_size(T: int, H: int) -> int:
+    return int(_lib.load().moe_layer_norm_backward_workspace_size(T, H))
+
+
+def moe_layer_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor,
+                            rstd: torch.Tensor, *, dx_add: Optional[torch.Tensor] = None,
+                            dx: Optional[torch.Tensor] = None, dweight: Optional[torch.Tensor] = None,
+                            dbias: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                            stream=None):
+    """dy, s [T, H] (s: LayerNormed.sum), mean, rstd [T] -> (dx [T, H], dweight [H], dbias [H]);
+    dx_add [T, H]: the gradient that reaches s past the norm, added to dx."""
+    _want(s, "s", None, 2)
+    T, H = s.shape
+    code, wcode = _float_code(s, "s"), _float_code(weight, "weight")
+    _like(weight, weight, "weight", (H,))
+    if dy is None:
+        raise ValueError("dy must be given")
+    for t, n in ((dy, "dy"), (dx_add, "dx_add"), (dx, "dx")):
+        _like(t, s, n)
+    for t, n in ((dweight, "dweight"), (dbias, "dbias")):
+        _like(t, weight, n, (H,))
+    for t, n in ((mean, "mean"), (rstd, "rstd")):
+        _want(t, n, torch.float32, 1)
+        if t.numel() != T:
+            raise ValueError(f"{n} must be [T]")
+    if dx is None:
+        dx = torch.empty_like(s)
+    if dweight is None:
+        dweight = torch.empty_like(weight)
+    if dbias is None:
+        dbias = torch.empty_like(weight)
+    if workspace is None:
+        workspace = torch.empty(moe_layer_norm_backward_workspace_size(T, H), dtype=torch.uint8, device=s.device)
+    st = _lib.load().moe_layer_norm_backward(_ptr(dy), _ptr(s), T, H, code, _ptr(weight), wcode, _ptr(mean), _ptr(rstd),
+                                             _ptr(dx_add), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(workspace),
+                                             workspace.numel(), _stream(stream))
+    _check("moe_layer_norm_backward", st)
+    return dx, dweight, dbias
+
+
+# ------------------------------------------------------- gradient norm, clipping
+def _grad_norm_clip(grads, outs, max_norm, eps, norm, workspace, stream):
+    n = len(grads)
+    for t in grads:
+        _want(t, "a gradient", None, None)
+    codes = [_float_code(t, "a gradient") for t in grads]
+    if outs is not None:
+        if len(outs) != n:
+            raise ValueError("out must have one tensor per gradient")
+        for t, o in zip(grads, outs):
+            if o is not t:
+                _like(o, t, "an output")
+    if norm is None:
+        if n == 0:
+            raise ValueError("no gradients: pass norm, the tensor to write")
+        norm = torch.empty((1,), dtype=torch.float32, device=grads[0].device)
+    else:
+        _want(norm, "norm", torch.float32, None)
+        if norm.numel() != 1:
+            raise ValueError("norm must hold one value")
+    L = _lib.load()
+    if workspace is None:
+        workspace = torch.empty(int(L.moe_grad_norm_workspace_size(n)), dtype=torch.uint8, device=norm.device)
+    ptrs = (C.c_void_p * n)(*[t.data_ptr() for t in grads])
+    outp = None if outs is None else (C.c_void_p * n)(*[t.data_ptr() for t in outs])
+    st = L.moe_grad_norm_clip(ptrs, (C.c_longlong * n)(*[t.numel() for t in grads]), (C.c_int * n)(*codes), outp, n,
+                              max_norm, eps, _ptr(norm), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check("moe_grad_norm_clip", st)
+    return norm
+
+
+def moe_grad_norm(grads, *, norm: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """sqrt of the sum of squares over a list of bf16 / fp32 tensors -> norm [1] fp32 (on the device)."""
+    return _grad_norm_clip(grads, None, 0.0, 0.0, norm, workspace, stream)
+
+
+def moe_grad_clip(grads, max_norm: float, *, eps: float = 1e-6, out=None, norm: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Scale the gradients by min(1, max_norm / (norm + eps)), norm being their global norm: in
+    place, or into the tensors of out. Returns the norm before clipping ([1] fp32, on the device)."""
+    return _grad_norm_clip(grads, grads if out is None else out, max_norm, eps, norm, workspace, stream)

@@ -1,0 +1,178 @@
+// grad_norm.cu -- global gradient norm over many tensors, and clipping by it: moe_grad_norm_clip.
+//
+// norm = sqrt(sum of all g^2), c = min(1, max_norm / (norm + eps)), out = g c. Two kernels a
+// group of tensors: the first sums the squares (a partial sum per CTA), the second adds the
+// partial sums up -- every CTA all of them, in one fixed order -- and scales.
+// The list of tensors travels in the kernels' parameters, cut into pieces of GN_CHUNK elements
+// that the CTAs take in turn, so that ragged lists keep every CTA busy.
+#include "common.cuh"
+
+#include <math.h>
+
+namespace moe {
+namespace {
+
+constexpr int GN_GROUP = 96;          // tensors per launch (the table is a kernel parameter)
+constexpr int GN_CHUNK = 16384;       // elements per piece
+constexpr int GN_THREADS = 256;
+constexpr int GN_CTAS = 1216;         // partial sums per group: the first kernel's grid at most
+
+struct GradTable {
+    const void* in[GN_GROUP];
+    void* out[GN_GROUP];
+    long long count[GN_GROUP];
+    int first[GN_GROUP + 1];          // first piece of each tensor
+    uint8_t f32[GN_GROUP];
+    int n;
+};
+
+__device__ __forceinline__ int tensor_of(const GradTable& g, int piece) {
+    int lo = 0, hi = g.n - 1;         // last tensor that starts at or before the piece (never an empty one)
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (g.first[mid] <= piece) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Sum over the CTA in a fixed order, in thread 0.
+__device__ __forceinline__ double cta_sum(double v, double* red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_down_sync(FULL, v, o);
+    if (lane_id() == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int w = 1; w < GN_THREADS / 32; w++) v += red[w];
+    return v;
+}
+
+__global__ void __launch_bounds__(GN_THREADS) grad_sumsq_kernel(const __grid_constant__ GradTable g, double* partial) {
+    __shared__ double red[GN_THREADS / 32];
+    float acc = 0.0f;
+    for (int piece = blockIdx.x; piece < g.first[g.n]; piece += gridDim.x) {
+        const int i = tensor_of(g, piece);
+        const long long b = (long long)(piece - g.first[i]) * GN_CHUNK;
+        const long long left = g.count[i] - b;
+        const int m = left < GN_CHUNK ? (int)left : GN_CHUNK;
+        for (int j = threadIdx.x; j < m; j += GN_THREADS) {
+            const float v = g.f32[i] ? static_cast<const float*>(g.in[i])[b + j]
+                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(g.in[i])[b + j]);
+            acc = fmaf(v, v, acc);
+        }
+    }
+    const double s = cta_sum((double)acc, red);
+    if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+// partial: n_partial sums; only CTA 0 of the first group writes the norm.
+__global__ void __launch_bounds__(GN_THREADS) grad_scale_kernel(const __grid_constant__ GradTable g,
+                                                                const double* __restrict__ partial, int n_partial,
+                                                                float max_norm, float eps, float* norm_out) {
+    __shared__ double red[GN_THREADS / 32];
+    __shared__ float s_c;
+    double v = 0.0;
+    for (int j = threadIdx.x; j < n_partial; j += GN_THREADS) v += partial[j];
+    v = cta_sum(v, red);
+    if (threadIdx.x == 0) {
+        const float norm = (float)sqrt(v);
+        const float c = max_norm / (norm + eps);
+        s_c = c >= 1.0f ? 1.0f : c;             // (a NaN stays)
+        if (norm_out && blockIdx.x == 0) *norm_out = norm;
+    }
+    __syncthreads();
+    const float c = s_c;
+    for (int piece = blockIdx.x; piece < g.first[g.n]; piece += gridDim.x) {
+        const int i = tensor_of(g, piece);
+        if (c == 1.0f && g.in[i] == g.out[i]) continue;
+        const long long b = (long long)(piece - g.first[i]) * GN_CHUNK;
+        const long long left = g.count[i] - b;
+        const int m = left < GN_CHUNK ? (int)left : GN_CHUNK;
+        for (int j = threadIdx.x; j < m; j += GN_THREADS) {
+            if (g.f32[i]) {
+                static_cast<float*>(g.out[i])[b + j] = static_cast<const float*>(g.in[i])[b + j] * c;
+            } else {
+                const float f = __bfloat162float(static_cast<const __nv_bfloat16*>(g.in[i])[b + j]);
+                static_cast<__nv_bfloat16*>(g.out[i])[b + j] = __float2bfloat16_rn(f * c);
+            }
+        }
+    }
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" size_t moe_grad_norm_workspace_size(int n) {
+    using namespace moe;
+    if (n < 0) return 0;
+    const size_t groups = n == 0 ? 1 : ((size_t)n + GN_GROUP - 1) / GN_GROUP;
+    return groups * GN_CTAS * sizeof(double);
+}
+
+extern "C" moe_status moe_grad_norm_clip(const void* const* grads, const long long* counts, const int* dtypes,
+                                         void* const* outs, int n, float max_norm, float eps, float* norm_out,
+                                         void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+    using namespace moe;
+    if (n < 0 || !(max_norm >= 0.0f) || !(eps >= 0.0f) || !norm_out) return MOE_ERR_INVALID_ARG;
+    if (n > 0 && (!grads || !counts || !dtypes)) return MOE_ERR_INVALID_ARG;
+    for (int i = 0; i < n; i++) {
+        if (counts[i] < 0 || (dtypes[i] != MOE_BF16 && dtypes[i] != MOE_F32)) return MOE_ERR_INVALID_ARG;
+        if (counts[i] > 0 && (!grads[i] || (outs && !outs[i]))) return MOE_ERR_INVALID_ARG;
+        if (counts[i] > ((long long)1 << 38)) return MOE_ERR_UNSUPPORTED;   // (pieces are counted in 32 bits)
+    }
+    if (!workspace || workspace_bytes < moe_grad_norm_workspace_size(n)) return MOE_ERR_WORKSPACE;
+    if (!moe_host::aligned(workspace, 16) || !moe_host::aligned(norm_out, 4)) return MOE_ERR_ALIGNMENT;
+    for (int i = 0; i < n; i++) {
+        const size_t a = dtypes[i] == MOE_F32 ? 4 : 2;
+        if (counts[i] > 0 && (!moe_host::aligned(grads[i], a) || (outs && !moe_host::aligned(outs[i], a))))
+            return MOE_ERR_ALIGNMENT;
+    }
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int most = sms * 8 < GN_CTAS ? sms * 8 : GN_CTAS;
+    const cudaStream_t s = moe_host::as_stream(stream);
+    double* partial = static_cast<double*>(workspace);
+    auto table = [&](int i0) {
+        GradTable g;
+        g.n = 0;
+        int pieces = 0;
+        for (int i = i0; i < n && i < i0 + GN_GROUP; i++) {
+            if (counts[i] == 0) continue;
+            g.in[g.n] = grads[i];
+            g.out[g.n] = outs ? outs[i] : nullptr;
+            g.count[g.n] = counts[i];
+            g.f32[g.n] = dtypes[i] == MOE_F32;
+            g.first[g.n] = pieces;
+            pieces += (int)((counts[i] + GN_CHUNK - 1) / GN_CHUNK);
+            g.n++;
+        }
+        g.first[g.n] = pieces;
+        return g;
+    };
+    int n_partial = 0;
+    for (int i0 = 0; i0 < n; i0 += GN_GROUP) {
+        const GradTable g = table(i0);
+        const int pieces = g.first[g.n];
+        if (!pieces) continue;
+        const int ctas = pieces < most ? pieces : most;
+        grad_sumsq_kernel<<<ctas, GN_THREADS, 0, s>>>(g, partial + n_partial);
+        n_partial += ctas;
+    }
+    bool told = false;
+    for (int i0 = 0; i0 < n && outs; i0 += GN_GROUP) {
+        const GradTable g = table(i0);
+        const int pieces = g.first[g.n];
+        if (!pieces) continue;
+        grad_scale_kernel<<<pieces < most ? pieces : most, GN_THREADS, 0, s>>>(g, partial, n_partial, max_norm, eps,
+                                                                               told ? nullptr : norm_out);
+        told = true;
+    }
+    if (!told) {
+        GradTable g;
+        g.n = 0;
+        g.first[0] = 0;
+        grad_scale_kernel<<<1, GN_THREADS, 0, s>>>(g, partial, n_partial, max_norm, eps, norm_out);
+    }
+    return moe_host::launch_status();
+}

@@ -61,7 +61,8 @@ typedef enum {
     MOE_I16 = 0,   /* int16 expert ids (E <= 32767) */
     MOE_I32 = 1,   /* int32 expert ids */
     MOE_BF16 = 2,  /* bfloat16 operands */
-    MOE_MXFP8 = 3  /* E4M3 payloads with one E8M0 scale byte per 32 elements */
+    MOE_MXFP8 = 3, /* E4M3 payloads with one E8M0 scale byte per 32 elements */
+    MOE_F32 = 4    /* fp32 (layer norm and gradient norm) */
 } moe_dtype;
 
 /* flags */
@@ -502,6 +503,94 @@ moe_status moe_unpermute_combine_backward(const void *dy, const void *y_perm,
  * ------------------------------------------------------------------------ */
 moe_status moe_permute_backward(const void *dx_perm, const int32_t *row_map,
                                 int T, int K, int H, void *dx, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The whole layer for a few tokens (a decoding step): router, expert MLP and
+ * combine in two kernels, on the same packed weights as the grouped GEMMs.
+ * (The pages describe training batches and no such call.)
+ *
+ * x [T, H] bf16, logits [T, E] fp32. ids [T, K] and probs [T, K] as
+ * moe_route_topk gives them (same flags), written; with logits NULL they are
+ * inputs instead (any router's; an id outside [0, E) is an invalid route, outside
+ * [-1, E) it also sets MOE_DEVERR_BAD_ID). For every valid route (t, k), e = ids[t,k]:
+ *   a = x[t] W1[e],  b = x[t] W3[e]                       (fp32 accumulation)
+ *   h = silu(a) * b, rounded to bf16, or (MXFP8) quantised 1x32 along F
+ *   y[t] = bf16( sum over the valid k of probs[t,k] * (h W2[e]) )
+ * with the sums over F and k in fp32 and one rounding at the end (the batched path
+ * rounds every route's row to bf16 before the combine). MXFP8: x is quantised 1x32
+ * along H first, as moe_permute does. A token without a valid route gets zeros.
+ * w13_packed, w2_packed and their scales: moe_prepare_weights, dtype MOE_BF16 or
+ * MOE_MXFP8. Outputs do not depend on the timing of the GPU's blocks.
+ * Requires 0 <= T <= 64, 1 <= K <= min(E, 128), T * K <= 4096, E <= 8192 (above:
+ * MOE_ERR_UNSUPPORTED), H % 128 == 0 and F % 128 == 0 (MXFP8: both % 512), the packed
+ * weights and the workspace 128-byte aligned, x, y and the scales 16-byte, ids and probs
+ * to their element. workspace: moe_layer_few_tokens_workspace_size bytes (0 for sizes
+ * that are refused); its contents need not be initialised, and calls that share one
+ * must not overlap. Every wait inside is bounded (MOE_DEVERR_TIMEOUT).
+ * ------------------------------------------------------------------------ */
+size_t moe_layer_few_tokens_workspace_size(int T, int K, int E, int H, int F, moe_dtype dtype);
+
+moe_status moe_layer_few_tokens(const void *x, int T, int H, const float *logits, int K, int E, int F,
+                                const void *w13_packed, const uint8_t *w13_scales,
+                                const void *w2_packed, const uint8_t *w2_scales, moe_dtype dtype,
+                                void *ids, moe_dtype id_dtype, float *probs, void *y,
+                                unsigned flags, void *workspace, size_t workspace_bytes,
+                                moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm around the layer (the norm of a pre-norm block; the pages do not
+ * describe one). For every row t of x [T, H] (dtype MOE_BF16 or MOE_F32):
+ *   s = x[t], or with residual [T, H]: s = round(x[t] + residual[t]) to dtype, also
+ *       written to sum [T, H] (required with residual, NULL without)
+ *   mean[t] = sum s / H;  rstd[t] = 1 / sqrt(sum (s - mean)^2 / H + eps)   (fp32)
+ *   y[t] = round((s - mean) * rstd * weight + bias)
+ * weight, bias [H] of dtype w_dtype (MOE_BF16 or MOE_F32); bias may be NULL (0). mean, rstd
+ * [T] fp32, NULL to skip. y, sum of dtype; sum may be x or residual itself, y may be any
+ * of them too. Pointers aligned to their elements (16 bytes and a row of whole 16-byte
+ * pieces take the wide path). Requires T >= 0, 1 <= H <= 65536, eps >= 0.
+ * ------------------------------------------------------------------------ */
+moe_status moe_layer_norm(const void *x, const void *residual, int T, int H, moe_dtype dtype,
+                          const void *weight, const void *bias, moe_dtype w_dtype, float eps,
+                          void *sum, void *y, float *mean, float *rstd, moe_stream_t stream);
+
+/* Its backward pass: s [T, H] (the normalised stream: x, or sum), dy [T, H], the forward's
+ * mean and rstd, weight. With xh = (s - mean) rstd and g = dy * weight:
+ *   dx[t] = round( rstd (g - sum(g)/H - xh sum(g xh)/H) + dx_add[t] )
+ *   dweight = round(sum over t of dy xh),  dbias = round(sum over t of dy)
+ * dx_add [T, H] (the gradient that reaches s past the norm) may be NULL, dx may be dy or
+ * dx_add itself. dweight [H] and dbias [H] (each NULL to skip) of w_dtype; T = 0 writes
+ * zeros to them. Sums in fp32, in an order that depends on the sizes and the device only.
+ * workspace: moe_layer_norm_backward_workspace_size bytes, 16-byte aligned, not
+ * initialised. Same limits as the forward. */
+size_t moe_layer_norm_backward_workspace_size(int T, int H);
+
+moe_status moe_layer_norm_backward(const void *dy, const void *s, int T, int H, moe_dtype dtype,
+                                   const void *weight, moe_dtype w_dtype, const float *mean,
+                                   const float *rstd, const void *dx_add, void *dx, void *dweight,
+                                   void *dbias, void *workspace, size_t workspace_bytes,
+                                   moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Global gradient norm over many tensors, and clipping by it (the step between
+ * the layer's backward pass and an optimiser; the pages do not describe it).
+ *   norm = sqrt( sum over the n tensors of sum g^2 )                       (fp32)
+ *   c = min(1, max_norm / (norm + eps));   outs[i] = round(grads[i] * c)
+ * grads, counts, dtypes, outs are host arrays of n entries: device pointers (aligned to
+ * their element), element counts (0 is legal, the pointer is then not used), MOE_BF16 or
+ * MOE_F32. outs NULL: only the norm. outs[i] may be grads[i] (in place: with c = 1 nothing
+ * is written) and has the type of grads[i]. *norm_out (device fp32). A NaN in a gradient
+ * makes norm and every output NaN; an infinite norm gives c = 0 (0 * inf is NaN). Squares
+ * are summed in fp32 per thread (values above about 1e19 overflow to an infinite norm) and
+ * joined in double in a fixed order. The host never reads the norm. Requires n >= 0,
+ * max_norm >= 0, eps >= 0 (not NaN). workspace: moe_grad_norm_workspace_size(n) bytes,
+ * 16-byte aligned, not initialised. The host arrays are read during the call only.
+ * ------------------------------------------------------------------------ */
+size_t moe_grad_norm_workspace_size(int n);
+
+moe_status moe_grad_norm_clip(const void *const *grads, const long long *counts,
+                              const int *dtypes, void *const *outs, int n, float max_norm,
+                              float eps, float *norm_out, void *workspace,
+                              size_t workspace_bytes, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Device error word. Copies the word to *flags_out (synchronising the device)

@@ -1,0 +1,267 @@
+"""The whole layer for a few tokens against a plain 64-bit implementation, through the C ABI.
+
+Bars. ids: equal. probs: 1e-6 absolute (the router's bar). y, with A = sum over the routes of
+p sum |h||W2| (the sum of the magnitudes that y is summed from):
+  2^-8 |y|       the one rounding of y to bf16 (half a unit of the last of 8 significant bits);
+  2^-12 A        bf16 h: where an fp32 sum falls on the other side of a rounding boundary, h
+                 differs by one step, at most 2^-7 of itself; fewer than one in 32 do;
+  2^-10 A        MXFP8 h: a step is at most 2^-3 of the value, fewer than one in 128 differ.
+"""
+import numpy as np
+import pytest
+import torch
+
+from dropless_moe_expert_router_gb300 import api
+from dropless_moe_expert_router_gb300.api import MoeError
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from dropless_moe_expert_router_gb300 import build
+    build.build()
+    api.moe_get_device_errors(clear=True)
+
+
+def _mxfp8(v):
+    """Row-wise 1x32 MXFP8 of a float64 array, as values."""
+    b = v.reshape(v.shape[:-1] + (v.shape[-1] // 32, 32))
+    amax = np.abs(b).max(-1, keepdims=True)
+    with np.errstate(divide="ignore"):
+        e = np.where(amax > 0, np.floor(np.log2(np.where(amax > 0, amax, 1.0))) - 8, 0.0)
+    e = np.clip(e, -127, 127)
+    scaled = np.clip(b / 2.0 ** e, -448, 448)
+    q = torch.from_numpy(scaled.astype(np.float32)).to(torch.float8_e4m3fn).to(torch.float32).numpy()
+    return (q.astype(np.float64) * 2.0 ** e).reshape(v.shape)
+
+
+def _decoded(codes, scales):
+    v = codes.cpu().view(torch.float8_e4m3fn).to(torch.float64).numpy()
+    s = 2.0 ** (scales.cpu().to(torch.float64).numpy() - 127)
+    return (v.reshape(v.shape[:-1] + (-1, 32)) * s[..., None]).reshape(v.shape)
+
+
+def _weights(E, H, F, precision, seed, std=0.05):
+    g = torch.Generator().manual_seed(seed)
+    w1, w3 = ((torch.randn((E, H, F), generator=g) * std).to(torch.bfloat16) for _ in range(2))
+    w2 = (torch.randn((E, F, H), generator=g) * std).to(torch.bfloat16)
+    return (w1, w3, w2), api.moe_prepare_weights(w1.cuda(), w3.cuda(), w2.cuda(), precision)
+
+
+def _reference(x, ids, probs, packed):
+    """(y, A) in 64 bits from bf16 x, integer ids, probs and the packed weights."""
+    fp8 = packed.precision == "mxfp8"
+    T, K = ids.shape
+    E, H, F = packed.E, packed.H, packed.F
+    X = x.double().cpu().numpy()
+    if fp8:
+        X = _mxfp8(X)
+    first = np.arange(F) // 128 * 256 + np.arange(F) % 128
+    y, A = np.zeros((T, H)), np.zeros((T, H))
+    for e in range(E):
+        at = [(t, k) for t in range(T) for k in range(K) if ids[t, k] == e]
+        if not at:
+            continue
+        if fp8:
+            w13 = _decoded(packed.w13[e], packed.w13_scales[e])
+            w2 = _decoded(packed.w2[e], packed.w2_scales[e])
+        else:
+            w13, w2 = packed.w13[e].double().cpu().numpy(), packed.w2[e].double().cpu().numpy()
+        a, b = X[[t for t, _ in at]] @ w13[first].T, X[[t for t, _ in at]] @ w13[first + 128].T
+        h = a / (1 + np.exp(-a)) * b
+        h = _mxfp8(h) if fp8 else torch.from_numpy(h).to(torch.bfloat16).double().numpy()
+        d, m = h @ w2.T, np.abs(h) @ np.abs(w2.T)
+        for i, (t, k) in enumerate(at):
+            y[t] += float(probs[t, k]) * d[i]
+            A[t] += float(probs[t, k]) * m[i]
+    return y, A
+
+
+def _check(y, x, ids, probs, packed):
+    ref, A = _reference(x, ids.cpu().numpy(), probs.cpu().numpy(), packed)
+    got = y.double().cpu().numpy()
+    bar = 2.0 ** -8 * np.abs(ref) + (2.0 ** -10 if packed.precision == "mxfp8" else 2.0 ** -12) * A
+    assert np.isfinite(got).all()
+    assert (np.abs(got - ref) <= bar).all(), float((np.abs(got - ref) / np.maximum(bar, 1e-30)).max())
+
+
+def _inputs(T, H, E, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn((T, H), generator=g).to(torch.bfloat16).cuda(), torch.randn((T, E), generator=g).cuda()
+
+
+CASES = [
+    (1, 256, 8, 2, 512, "bf16", False, torch.int32),
+    (3, 128, 1, 1, 128, "bf16", True, torch.int32),        # one expert
+    (7, 384, 5, 5, 128, "bf16", False, torch.int16),       # K = E
+    (16, 256, 4, 2, 640, "bf16", True, torch.int32),
+    (17, 640, 3, 1, 256, "bf16", False, torch.int32),
+    (64, 256, 33, 3, 384, "bf16", True, torch.int32),
+    (64, 128, 64, 64, 128, "bf16", False, torch.int16),    # T * K = 4096
+    (5, 256, 2304, 36, 128, "bf16", False, torch.int16),
+    (33, 128, 700, 20, 128, "bf16", True, torch.int32),
+    (2, 1152, 2, 1, 2176, "bf16", False, torch.int32),
+    (1, 512, 4, 2, 512, "mxfp8", False, torch.int32),
+    (9, 512, 40, 8, 1024, "mxfp8", True, torch.int32),
+    (64, 1024, 8, 2, 512, "mxfp8", True, torch.int16),
+    (31, 512, 300, 7, 512, "mxfp8", False, torch.int32),
+]
+
+
+@pytest.mark.parametrize("T,H,E,K,F,precision,renorm,idt", CASES)
+def test_few_tokens_matches_plain(T, H, E, K, F, precision, renorm, idt):
+    x, lg = _inputs(T, H, E, seed=T * 31 + E)
+    _, packed = _weights(E, H, F, precision, seed=E + F)
+    y, ids, probs = api.moe_layer_few_tokens(x, lg, packed, K, renorm=renorm, id_dtype=idt)
+    want_ids, want_p = api.moe_route_topk(lg, K, renorm=renorm, id_dtype=idt)
+    assert ids.dtype == idt and torch.equal(ids, want_ids)
+    assert (probs - want_p).abs().max().item() <= 1e-6
+    _check(y, x, ids, probs, packed)
+    assert api.moe_get_device_errors() == 0
+
+
+@pytest.mark.parametrize("E,K", [(200, 17), (256, 128), (257, 100), (1024, 9), (2304, 36), (8192, 40)])
+def test_few_tokens_router_ties(E, K):
+    """Equal logits, a few values only, both zeros and infinities: ties go to the lower index."""
+    T = 8
+    lg = torch.zeros((T, E))
+    g = torch.Generator().manual_seed(E)
+    lg[1] = torch.randint(0, 3, (E,), generator=g).float()
+    lg[2, ::2] = -0.0
+    lg[3] = torch.randint(0, 2, (E,), generator=g).float() * -1e30
+    lg[4] = float("-inf")
+    lg[4, E // 2:] = torch.arange(E - E // 2).float() % 5
+    lg[5] = torch.arange(E).float()
+    lg[6] = -torch.arange(E).float()
+    lg[7] = (torch.arange(E) % 7).float() * 1e-40                   # subnormal
+    _, packed = _weights(1, 128, 128, "bf16", seed=1)
+    w = packed._replace(E=E, w13=packed.w13.expand(E, -1, -1).contiguous(), w2=packed.w2.expand(E, -1, -1).contiguous())
+    x, _ = _inputs(T, 128, 1, seed=3)
+    y, ids, _ = api.moe_layer_few_tokens(x, lg.cuda(), w, K)
+    want = torch.sort(lg.double(), dim=1, descending=True, stable=True).indices[:, :K]
+    assert torch.equal(ids.cpu().long(), want)
+    assert torch.isfinite(y.float()).all()
+
+
+@pytest.mark.parametrize("precision", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("idt", [torch.int16, torch.int32])
+def test_few_tokens_given_routes(precision, idt):
+    """Routes of the caller's: invalid ones, a token with none (zeros), an expert named twice by
+    one token (both weights count), one expert taken by every token."""
+    T, H, E, K, F = 19, 512, 11, 4, 512
+    x, _ = _inputs(T, H, E, seed=5)
+    _, packed = _weights(E, H, F, precision, seed=6)
+    g = torch.Generator().manual_seed(7)
+    ids = torch.randint(0, E, (T, K), generator=g).to(idt)
+    ids[:, 0] = 3
+    ids[0] = -1
+    ids[1, 1:] = -1
+    ids[2] = 9
+    ids[T - 1] = torch.tensor([-1, 4, -1, 4]).to(idt)
+    probs = torch.rand((T, K), generator=g)
+    probs[4] = 0.0
+    ids, probs = ids.cuda(), probs.cuda()
+    keep_i, keep_p = ids.clone(), probs.clone()
+    y, i2, p2 = api.moe_layer_few_tokens(x, None, packed, K, ids=ids, probs=probs)
+    assert i2 is ids and p2 is probs and torch.equal(ids, keep_i) and torch.equal(probs, keep_p)
+    _check(y, x, ids, probs, packed)
+    assert not y[0].any() and not y[4].any()
+    assert api.moe_get_device_errors() == 0
+    ids[5, 2] = E                                                    # outside [-1, E): invalid, and flagged
+    ids[6, 1] = -2
+    y, _, _ = api.moe_layer_few_tokens(x, None, packed, K, ids=ids, probs=probs)
+    _check(y, x, ids, probs, packed)
+    assert api.moe_get_device_errors() == api.MOE_DEVERR_BAD_ID
+
+
+def test_few_tokens_no_valid_route_at_all():
+    x, _ = _inputs(6, 256, 8, seed=1)
+    _, packed = _weights(8, 256, 128, "bf16", seed=2)
+    ids = torch.full((6, 2), -1, dtype=torch.int32, device="cuda")
+    y, _, _ = api.moe_layer_few_tokens(x, None, packed, 2, ids=ids, probs=torch.ones((6, 2), device="cuda"),
+                                       y=torch.full((6, 256), 7.0, dtype=torch.bfloat16, device="cuda"))
+    assert not y.any()
+
+
+@pytest.mark.parametrize("precision", ["bf16", "mxfp8"])
+def test_few_tokens_skewed_to_one_expert(precision):
+    x, lg = _inputs(64, 512, 16, seed=8)
+    lg[:, 7] += 100.0
+    _, packed = _weights(16, 512, 512, precision, seed=9)
+    y, ids, probs = api.moe_layer_few_tokens(x, lg, packed, 1)
+    assert (ids == 7).all()
+    _check(y, x, ids, probs, packed)
+
+
+def test_few_tokens_bad_values_stay_in_their_token():
+    """A NaN and an infinity in two tokens, NaN weights in an expert nobody chose: the other
+    tokens' results are those without them."""
+    T, H, E, K, F = 20, 256, 6, 2, 256
+    x, lg = _inputs(T, H, E, seed=11)
+    lg[:, 5] = -100.0
+    _, packed = _weights(E, H, F, "bf16", seed=12)
+    y0, _, _ = api.moe_layer_few_tokens(x, lg, packed, K)
+    packed.w13[5] = float("nan")
+    packed.w2[5] = float("nan")
+    x2 = x.clone()
+    x2[3, 17] = float("nan")
+    x2[8, 200] = float("inf")
+    y1, _, _ = api.moe_layer_few_tokens(x2, lg, packed, K)
+    clean = [t for t in range(T) if t not in (3, 8)]
+    assert torch.equal(y0[clean], y1[clean])
+    assert not torch.isfinite(y1[3].float()).all() and not torch.isfinite(y1[8].float()).all()
+
+
+@pytest.mark.parametrize("precision", ["bf16", "mxfp8"])
+def test_few_tokens_repeats_bit_for_bit(precision):
+    """The same call on a workspace of any contents, another stream and a graph's replay."""
+    x, lg = _inputs(13, 1024, 24, seed=21)
+    _, packed = _weights(24, 1024, 1024, precision, seed=22)
+    ws = api.moe_layer_few_tokens_workspace(packed, 13, 3)
+    first = api.moe_layer_few_tokens(x, lg, packed, 3, workspace=ws)[0].clone()
+    for fill in (0, 255, 1):
+        ws.fill_(fill)
+        assert torch.equal(api.moe_layer_few_tokens(x, lg, packed, 3, workspace=ws)[0], first)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y = api.moe_layer_few_tokens(x, lg, packed, 3, workspace=ws, stream=s)[0]
+    s.synchronize()
+    assert torch.equal(y, first)
+    y = torch.empty_like(first)
+    ids, probs = torch.empty((13, 3), dtype=torch.int32, device="cuda"), torch.empty((13, 3), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.moe_layer_few_tokens(x, lg, packed, 3, ids=ids, probs=probs, y=y, workspace=ws)
+    for seed in (31, 32):
+        x2, lg2 = _inputs(13, 1024, 24, seed=seed)
+        x.copy_(x2)
+        lg.copy_(lg2)
+        graph.replay()
+        got = y.clone()
+        assert torch.equal(got, api.moe_layer_few_tokens(x2, lg2, packed, 3)[0])
+
+
+def test_few_tokens_zero_tokens_and_refusals():
+    _, packed = _weights(4, 256, 128, "bf16", seed=2)
+    y, ids, probs = api.moe_layer_few_tokens(torch.empty((0, 256), dtype=torch.bfloat16, device="cuda"),
+                                             torch.empty((0, 4), device="cuda"), packed, 2)
+    assert y.shape == (0, 256) and ids.shape == (0, 2) and probs.shape == (0, 2)
+    x, lg = _inputs(3, 256, 4, seed=1)
+    with pytest.raises(MoeError):
+        api.moe_layer_few_tokens(x, lg, packed, 5)                                    # K > E
+    with pytest.raises(MoeError):
+        api.moe_layer_few_tokens(*_inputs(65, 256, 4, seed=1), packed, 2)             # T > 64
+    with pytest.raises(MoeError):
+        api.moe_layer_few_tokens(x, lg, packed, 2, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        api.moe_layer_few_tokens(x, lg[:, :3].contiguous(), packed, 2)
+    with pytest.raises(ValueError):
+        api.moe_layer_few_tokens(x.t(), lg, packed, 2)
+    with pytest.raises(ValueError):
+        api.moe_layer_few_tokens(x.float(), lg, packed, 2)
+    with pytest.raises(ValueError):
+        api.moe_layer_few_tokens(x, None, packed, 2)
+    with pytest.raises(ValueError):
+        api.moe_layer_few_tokens(x.cpu(), lg, packed, 2)
+    assert api.moe_get_device_errors() == 0

@@ -1,0 +1,256 @@
+"""Layer norm forward and backward against a plain 64-bit implementation, through the C ABI.
+
+Bars, with u = 2^-24 and G = (H / 32 + 64) u, the worst relative error of an fp32 sum of H terms
+that 32 threads or more share: every statistic errs by G of the mean magnitude it is summed from,
+every output by the statistics' error carried through its formula, 16 u of the largest term, and
+(bf16) half a unit of the last of its 8 significant bits, 2^-8 of itself.
+"""
+import pytest
+import torch
+
+from dropless_moe_expert_router_gb300 import api
+from dropless_moe_expert_router_gb300.api import MoeError
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from dropless_moe_expert_router_gb300 import build
+    build.build()
+
+
+def _half(dt):
+    return 2.0 ** -8 if dt == BF else U
+
+
+def _inputs(T, H, dt, wdt, seed, mean=0.3):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn((T, H), generator=g) * 1.5 + mean).to(dt).cuda()
+    w = (1 + 0.2 * torch.randn(H, generator=g)).to(wdt).cuda()
+    b = (0.2 * torch.randn(H, generator=g)).to(wdt).cuda()
+    r = torch.randn((T, H), generator=g).to(dt).cuda()
+    dy = torch.randn((T, H), generator=g).to(dt).cuda()
+    return x, w, b, r, dy
+
+
+def _within(got, ref, bar):
+    d = (got.double() - ref).abs()
+    assert bool((d <= bar).all()), float((d / bar.clamp_min(1e-300)).max())
+
+
+def _forward_check(o, s, w, b, eps):
+    S, H = s.double(), s.shape[1]
+    G = (H / 32 + 64) * U
+    mean = S.mean(1)
+    var = (S - mean[:, None]).square().mean(1)
+    rstd = (var + eps).rsqrt()
+    mag = S.abs().mean(1)
+    e_mean = G * mag + 1e-30
+    _within(o.mean, mean, e_mean)
+    # d(rstd)/rstd = d(var + eps) / (2 (var + eps)); (s - mean) errs by u |s| and the mean's error
+    e_rstd = rstd * (0.5 * (G * var + e_mean ** 2 + 4 * U * S.abs().amax(1) * var.sqrt()) * rstd ** 2 + 8 * U)
+    _within(o.rstd, rstd, e_rstd)
+    W, B = w.double(), torch.zeros(H, device=s.device).double() if b is None else b.double()
+    y = (S - mean[:, None]) * rstd[:, None] * W + B
+    e = ((e_mean + 4 * U * S.abs().amax(1)) * rstd)[:, None] * W.abs() + ((y - B).abs() * (e_rstd / rstd)[:, None]) \
+        + 16 * U * (y.abs() + B.abs())
+    _within(o.y, y, e + _half(o.y.dtype) * y.abs() * 1.01 + 1e-38)
+
+
+SHAPES = [(1, 1), (1, 8), (3, 7), (2, 33), (5, 1021), (1, 4096), (130, 256), (33, 4096), (9, 7168), (4, 8192),
+          (3, 8200), (2, 16384), (2, 65536), (1000, 129), (2, 20001)]
+
+
+@pytest.mark.parametrize("dt,wdt", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("T,H", SHAPES)
+def test_forward(T, H, dt, wdt):
+    x, w, b, r, _ = _inputs(T, H, dt, wdt, seed=T + H)
+    eps = 1e-5
+    o = api.moe_layer_norm(x, w, b, eps)
+    assert o.sum is x
+    _forward_check(o, x, w, b, eps)
+    o = api.moe_layer_norm(x, w, None, eps, residual=r)
+    s = (x.float() + r.float()).to(dt)
+    assert torch.equal(o.sum, s)
+    _forward_check(o, s, w, None, eps)
+
+
+def _backward_reference(dy, s, w, mean, rstd, add):
+    DY, S, W = dy.double(), s.double(), w.double()
+    R = rstd.double()[:, None]
+    xh = (S - mean.double()[:, None]) * R
+    g = DY * W
+    a, c = g.mean(1, keepdim=True), (g * xh).mean(1, keepdim=True)
+    dx = R * (g - a - xh * c)
+    if add is not None:
+        dx = dx + add.double()
+    return dx, (DY * xh).sum(0), DY.sum(0), xh, g
+
+
+@pytest.mark.parametrize("dt,wdt", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("T,H", SHAPES + [(2500, 64), (1700, 1000)])
+def test_backward(T, H, dt, wdt):
+    x, w, b, r, dy = _inputs(T, H, dt, wdt, seed=3 * T + H)
+    o = api.moe_layer_norm(x, w, b)
+    G, GT = (H / 32 + 64) * U, (T + 64) * U
+    for add in (None, r):
+        dx, dw, db = api.moe_layer_norm_backward(dy, x, w, o.mean, o.rstd, dx_add=add)
+        rx, rw, rb, xh, g = _backward_reference(dy, x, w, o.mean, o.rstd, add)
+        R = o.rstd.double()[:, None]
+        exh = 4 * U * (x.double().abs() + o.mean.double().abs()[:, None]) * R
+        sums = G * (g.abs().mean(1, keepdim=True) + xh.abs() * (g * xh).abs().mean(1, keepdim=True)) \
+            + xh.abs() * (g.abs() * exh).mean(1, keepdim=True)
+        terms = g.abs() + g.mean(1, keepdim=True).abs() + (xh.abs() + exh) * (g * xh).mean(1, keepdim=True).abs()
+        e = R * (sums + 16 * U * terms + exh * (g * xh).mean(1, keepdim=True).abs())
+        if add is not None:
+            e = e + 2 * U * (add.double().abs() + rx.abs())
+        _within(dx, rx, e + 1.01 * _half(dt) * rx.abs() + 1e-38)
+        D = dy.double().abs()
+        _within(dw, rw, GT * (D * xh.abs()).sum(0) + (D * exh).sum(0) + 1.01 * _half(wdt) * rw.abs() + 1e-38)
+        _within(db, rb, GT * D.sum(0) + 1.01 * _half(wdt) * rb.abs() + 1e-38)
+
+
+def test_backward_against_differences():
+    """<dx, v>, <dw, v>, <db, v> against central differences of L = sum(dy y), y of the fp32 kernel.
+    Step 2^-6 along unit-variance v: truncation 2^-12 / 6 of third derivatives of order 1 per value;
+    rounding 16 u sum|dy y| / 2^-6; both well under 2^-9 of the sum of |terms|."""
+    T, H = 6, 96
+    x, w, b, _, dy = _inputs(T, H, F32, F32, seed=1)
+    g = torch.Generator().manual_seed(2)
+    o = api.moe_layer_norm(x, w, b)
+    dx, dw, db = api.moe_layer_norm_backward(dy, x, w, o.mean, o.rstd)
+    h = 2.0 ** -6
+
+    def loss(x_, w_, b_):
+        return (api.moe_layer_norm(x_, w_, b_).y.double() * dy.double()).sum().item()
+
+    for d, at in ((dx, 0), (dw, 1), (db, 2)):
+        v = torch.randn(d.shape, generator=g).cuda()
+        up, down = [x, w, b], [x, w, b]
+        up[at], down[at] = up[at] + h * v, down[at] - h * v
+        diff = (loss(*up) - loss(*down)) / (2 * h)
+        dot = (d.double() * v.double()).sum().item()
+        assert abs(diff - dot) <= 2.0 ** -9 * (d.double().abs() * v.double().abs()).sum().item()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_in_place(dt):
+    x, w, b, r, dy = _inputs(40, 520, dt, F32, seed=9)
+    want = api.moe_layer_norm(x, w, b, residual=r)
+    x2, r2 = x.clone(), r.clone()
+    got = api.moe_layer_norm(x2, w, b, residual=r2, sum=r2, y=x2)
+    assert torch.equal(got.y, want.y) and torch.equal(r2, want.sum) and got.y is x2
+    x3 = x.clone()
+    assert torch.equal(api.moe_layer_norm(x3, w, b, y=x3).y, api.moe_layer_norm(x, w, b).y)
+    ref = api.moe_layer_norm_backward(dy, want.sum, w, want.mean, want.rstd, dx_add=r)
+    for alias in ("dy", "add"):
+        d2, a2 = dy.clone(), r.clone()
+        got = api.moe_layer_norm_backward(d2, want.sum, w, want.mean, want.rstd, dx_add=a2, dx=d2 if alias == "dy" else a2)
+        assert all(torch.equal(p, q) for p, q in zip(got, ref))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("off", [1, 3, 4])
+def test_unaligned_bases(dt, off):
+    """Contiguous tensors that start off a 16-byte boundary, at a width that is a multiple of 8."""
+    T, H = 37, 512
+    x, w, b, r, dy = _inputs(T, H, dt, dt, seed=off)
+
+    def moved(t):
+        buf = torch.empty(t.numel() + off, dtype=t.dtype, device="cuda")
+        v = buf[off:].view(t.shape)
+        v.copy_(t)
+        return v
+    o = api.moe_layer_norm(moved(x), moved(w), moved(b), residual=moved(r), y=moved(x), sum=moved(x))
+    s = (x.float() + r.float()).to(dt)
+    assert torch.equal(o.sum, s)
+    _forward_check(o, s, w, b, 1e-5)
+    ref = api.moe_layer_norm_backward(dy, s, w, o.mean, o.rstd, dx_add=r)
+    got = api.moe_layer_norm_backward(moved(dy), moved(s), moved(w), o.mean, o.rstd, dx_add=moved(r), dx=moved(x),
+                                      dweight=moved(w), dbias=moved(b))
+    rx, rw, rb, _, _ = _backward_reference(dy, s, w, o.mean, o.rstd, r)
+    for a, c, e in zip(got, ref, (rx, rw, rb)):
+        bar = (2 * _half(dt) + 1e-5) * e.abs() + 1e-4
+        _within(a, e, bar)
+        _within(c, e, bar)
+
+
+def test_degenerate_rows_stay_apart():
+    """Constant rows (variance 0), a NaN row and an infinite one beside ordinary rows."""
+    x, w, b, _, dy = _inputs(8, 640, F32, F32, seed=4)
+    clean = api.moe_layer_norm(x, w, b)
+    x2 = x.clone()
+    x2[1] = 3.0
+    x2[2] = 0.0
+    x2[4, 5] = float("nan")
+    x2[6, 639] = float("inf")
+    o = api.moe_layer_norm(x2, w, b)
+    rows = [0, 3, 5, 7]
+    assert torch.equal(o.y[rows], clean.y[rows]) and torch.equal(o.rstd[rows], clean.rstd[rows])
+    for t, v in ((1, 3.0), (2, 0.0)):
+        assert abs(o.mean[t].item() - v) <= 1e-6 and abs(o.rstd[t].item() - 1e-5 ** -0.5) <= 1e-2
+        assert (o.y[t] - b).abs().max().item() <= 1e-3
+    assert torch.isnan(o.y[4]).all() and torch.isnan(o.y[6]).any()
+    dx, _, _ = api.moe_layer_norm_backward(dy, x2, w, o.mean, o.rstd)
+    ref, _, _ = api.moe_layer_norm_backward(dy, x, w, clean.mean, clean.rstd)
+    assert torch.equal(dx[rows], ref[rows])
+
+
+def test_repeats_bit_for_bit_on_any_workspace_and_stream():
+    x, w, b, r, dy = _inputs(3000, 1000, BF, F32, seed=6)
+    o = api.moe_layer_norm(x, w, b)
+    ref = api.moe_layer_norm_backward(dy, x, w, o.mean, o.rstd)
+    ws = torch.empty(api.moe_layer_norm_backward_workspace_size(3000, 1000), dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    for fill in (0, 255):
+        ws.fill_(fill)
+        s.wait_stream(torch.cuda.current_stream())
+        got = api.moe_layer_norm_backward(dy, x, w, o.mean, o.rstd, workspace=ws, stream=s)
+        s.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, ref))
+    y, sm = torch.empty_like(x), torch.empty_like(x)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(w)
+    mean, rstd = torch.empty(3000, device="cuda"), torch.empty(3000, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.moe_layer_norm(x, w, b, residual=r, y=y, sum=sm, mean=mean, rstd=rstd)
+        api.moe_layer_norm_backward(dy, sm, w, mean, rstd, dx=dx, dweight=dw, dbias=db, workspace=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    o = api.moe_layer_norm(x, w, b, residual=r)
+    assert torch.equal(y, o.y)
+    assert all(torch.equal(p, q) for p, q in
+               zip((dx, dw, db), api.moe_layer_norm_backward(dy, o.sum, w, o.mean, o.rstd)))
+
+
+def test_no_rows_and_refusals():
+    x, w, b, r, dy = _inputs(4, 64, BF, F32, seed=1)
+    z = torch.empty((0, 64), dtype=BF, device="cuda")
+    o = api.moe_layer_norm(z, w, b, residual=z)
+    assert o.y.shape == (0, 64)
+    dx, dw, db = api.moe_layer_norm_backward(z, z, w, o.mean, o.rstd)
+    assert dx.shape == (0, 64) and not dw.any() and not db.any()
+    with pytest.raises(ValueError):
+        api.moe_layer_norm(x.half(), w, b)
+    with pytest.raises(ValueError):
+        api.moe_layer_norm(x, w[:32].contiguous(), b)
+    with pytest.raises(ValueError):
+        api.moe_layer_norm(x, w, b.to(BF))
+    with pytest.raises(ValueError):
+        api.moe_layer_norm(x.t(), w, b)
+    with pytest.raises(ValueError):
+        api.moe_layer_norm(x, w, b, residual=r.float())
+    with pytest.raises(MoeError):
+        api.moe_layer_norm(x, w, b, eps=-1.0)
+    with pytest.raises(MoeError):
+        api.moe_layer_norm(torch.zeros((1, 65537), device="cuda"), torch.zeros(65537, device="cuda"))
+    o = api.moe_layer_norm(x, w, b)
+    with pytest.raises(ValueError):
+        api.moe_layer_norm_backward(dy[:3].contiguous(), x, w, o.mean, o.rstd)
+    with pytest.raises(ValueError):
+        api.moe_layer_norm_backward(dy, x, w, o.mean[:2], o.rstd)
+    with pytest.raises(MoeError):
+        api.moe_layer_norm_backward(dy, x, w, o.mean, o.rstd, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
