@@ -5,6 +5,8 @@
 // Every weight of the chosen experts is read once and used for the few tokens that chose
 // them, so the time is the weights' bytes over the memory's rate.
 #include "common.cuh"
+#include "sm100_ptx.cuh"
+#include "tensor_map.cuh"
 
 #include <math.h>
 
@@ -72,6 +74,8 @@ struct PrepArgs {
     float* probs;
     uint8_t* xq;              // MXFP8: codes [T, H] and scales [T, H / 32] of x; else null
     uint8_t* xs;
+    unsigned* count;          // the second kernel's counters, zeroed here
+    int n_count;
 };
 
 template <int V>
@@ -197,6 +201,8 @@ template <int V>
 __global__ void __launch_bounds__(PREP_THREADS) few_prep_kernel(PrepArgs p) {
     __shared__ PrepSmem sm;
     const int t = blockIdx.x;
+    if (t == 0)
+        for (int i = threadIdx.x; i < p.n_count; i += PREP_THREADS) p.count[i] = 0u;
     if (p.logits) prep_route<V>(p, t, sm);
     if (p.xq) {
         const int lane = (int)lane_id();
@@ -217,122 +223,775 @@ __global__ void __launch_bounds__(PREP_THREADS) few_prep_kernel(PrepArgs p) {
 }
 
 // ---------------------------------------------------------------------------
-// The expert MLP, one warp per dot product.
+// Second kernel: the expert MLP and the combine, one persistent CTA per SM.
+//
+// Every weight row is streamed once, as the A operand (128 rows) of tcgen05.mma; the few tokens
+// are the B operand, so a tile's accumulator is [128 weight rows][tokens] in TMEM. The weights'
+// bytes bound the kernel: a producer warp keeps up to FEW_STAGES 16 KB weight tiles in flight per SM.
+//
+// Up: a tile is 64 columns of W1 and the same 64 of W3 of one expert, over all of H; the tokens
+//   operand is all of x (T rows, zero rows past them), the chosen tokens' columns are read. h goes
+//   to the workspace, the rows of an expert side by side.
+// Down: a tile is 128 output columns of one expert's W2. The walk over (output tile, expert,
+//   k-block) is cut into gridDim.x equal pieces whatever the number of experts, so that few experts
+//   still use every SM; a CTA adds p * (its piece of h W2) up over its experts in shared memory. The
+//   CTAs that share an output tile leave partial sums, and the last to arrive adds them, in the
+//   order of the CTAs: the result does not depend on who is last.
+// Between the two every CTA waits for all of h (a counter, bounded); the first down tiles of weights are
+// already on their way then, as they depend on the routing alone.
+//
+// Warps: 0 TMA producer, 1 TMEM and MMA issue, 2-5 epilogue (one TMEM lane quarter each), 6 (MXFP8)
+// the scales: loads a group of four k-blocks' scale bytes and rearranges them for tcgen05.cp.
 // ---------------------------------------------------------------------------
-// Dot product over n elements of two rows (bf16, or E4M3 codes with a scale byte per 32), by a warp.
-template <bool FP8>
-__device__ __forceinline__ float warp_dot(const void* a, const uint8_t* as, const void* b, const uint8_t* bs, int n) {
-    const int lane = (int)lane_id();
-    float acc = 0.0f;
-    for (int j = lane; j < n / 8; j += 32) {
-        if constexpr (FP8) {
-            const uint2 u = __ldg(static_cast<const uint2*>(a) + j), v = __ldg(static_cast<const uint2*>(b) + j);
-            const uint32_t uw[2] = {u.x, u.y}, vw[2] = {v.x, v.y};
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-                s = fmaf(e4m3_value((uw[i / 4] >> (8 * (i % 4))) & 0xffu), e4m3_value((vw[i / 4] >> (8 * (i % 4))) & 0xffu), s);
-            acc += s * exp2f((float)((int)as[j / 4] - 127)) * exp2f((float)((int)bs[j / 4] - 127));
-        } else {
-            float f[8], g[8];
-            bf16x8_to_f32(__ldg(static_cast<const uint4*>(a) + j), f);
-            bf16x8_to_f32(__ldg(static_cast<const uint4*>(b) + j), g);
-#pragma unroll
-            for (int i = 0; i < 8; i++) acc = fmaf(f[i], g[i], acc);
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(FULL, acc, o);
-    return acc;
-}
+constexpr int FEW_STAGES = 12;             // most ring stages
+constexpr int FEW_A_BYTES = 128 * 128;     // a weight tile: 128 rows of 128 bytes
+constexpr int FEW_ACC_COLS = 64;           // TMEM columns of one accumulator: tokens
+constexpr int FEW_SF_SLOTS = 4;            // MXFP8: groups of scales in flight
+constexpr int FEW_SF_BYTES = 4096;         // a slot: landed 16 bytes a row, rearranged 4 x (A 512 | B 512)
+constexpr int FEW_XCH = 16;                // tokens whose W3 products the epilogue exchanges at a time (tmem_wait16)
+constexpr int FEW_MIN_KB = 2;              // k-blocks of the down walk that a CTA takes at least
+constexpr size_t FEW_SMEM_MAX = 227 * 1024;
 
 struct FewArgs {
-    const void* x;            // [T, H] bf16 or E4M3
-    const uint8_t* xs;
-    const void* w13;
-    const uint8_t* w13s;
-    const void* w2;
-    const uint8_t* w2s;
     const void* ids;
     const float* probs;
     bool i16;
     int T, H, K, E, F;
-    void* h;                  // [T * K, F] bf16 or E4M3
-    uint8_t* hs;
+    int nb;                   // B rows of a stage: T rounded up to 16
+    int stages;
+    int a_max;                // most experts chosen: min(E, T K)
+    void* h;                  // [T K, F] bf16 or E4M3
+    uint8_t* hs;              // MXFP8: [T K, F / 32]
+    float* part;              // [2 gridDim.x][T][128] partial sums of shared output tiles
+    unsigned* count;          // [0] CTAs whose h is written, [1 + r] arrivals at output tile r; zeroed before
     __nv_bfloat16* y;
 };
 
-// h of one route and 32 columns of F per CTA (8 warps, four columns each).
+// Shared memory past the ring.
+struct FewSmem {
+    uint64_t full[FEW_STAGES], empty[FEW_STAGES], tfull[2], tempty[2], done;
+    uint64_t sf_full[FEW_SF_SLOTS], sf_ready[FEW_SF_SLOTS], sf_empty[FEW_SF_SLOTS];
+    uint32_t tmem, abort_flag;
+    int A, slots, routes, ticket;
+    int scan[2][8];
+    float xch[2][FEW_XCH][64];
+};
+
+__host__ __device__ constexpr size_t few_up16(size_t v) { return (v + 15) & ~(size_t)15; }
+
+// Bytes of shared memory past the ring: FewSmem, MXFP8 scale slots, output sums, the plan.
+__host__ __device__ inline size_t few_fixed_smem(int T, int K, int a_max, bool fp8) {
+    return few_up16(sizeof(FewSmem)) + (fp8 ? (size_t)FEW_SF_SLOTS * FEW_SF_BYTES : 0) + (size_t)T * 128 * 4 +
+           few_up16((size_t)a_max * 8) + few_up16((size_t)a_max * 4) + few_up16((size_t)(a_max + 1) * 4) +
+           few_up16((size_t)T * K * 4);
+}
+
+// The chosen experts: id, first row of h, which tokens; and each route's weight.
+struct FewPlan {
+    const unsigned long long* mask;
+    const int* e;
+    const int* off;
+    const float* w;
+    int A;
+    int W;                    // k-blocks of the whole down walk
+    int parts;                // CTAs that take an equal piece of it each (at least FEW_MIN_KB k-blocks)
+
+    // first k-block of CTA c's piece (c = parts: the end)
+    __device__ int begin_of(int c) const { return (int)((long long)W * min(c, parts) / parts); }
+};
+
+// A run of k-blocks of one tile: the unit that all warps walk in the same order.
+struct FewRun {
+    int phase;                // 0 up, 1 down
+    int a;                    // index among the chosen experts
+    int tile;                 // up: 64-column tile of F; down: 128-column tile of H
+    int kb0, nkb;
+    int row0, row1;           // weight rows of the two 64-row halves
+    int brow, bn;             // tokens operand: first row, rows loaded
+};
+
 template <bool FP8>
-__global__ void __launch_bounds__(256) few_up_kernel(FewArgs p) {
-    __shared__ float col[32];
-    const int r = blockIdx.x, f0 = blockIdx.y * 32, warp = threadIdx.x >> 5, lane = (int)lane_id();
-    const int t = r / p.K;
-    const int e = load_id(p.ids, r, p.i16);
-    if (e < 0 || e >= p.E) {
-        if (e != -1 && threadIdx.x == 0 && blockIdx.y == 0) raise_device_error(MOE_DEVERR_BAD_ID);
-        return;
+struct FewWalk {
+    const FewArgs& p;
+    const FewPlan& pl;
+    int u, w, w1;
+    __device__ FewWalk(const FewArgs& p_, const FewPlan& pl_) : p(p_), pl(pl_) {
+        u = blockIdx.x;
+        w = pl.begin_of(blockIdx.x);
+        w1 = pl.begin_of(blockIdx.x + 1);
     }
-    const size_t esz = FP8 ? 1 : 2;
-    const char* x = static_cast<const char*>(p.x) + (size_t)t * p.H * esz;
-    const uint8_t* xs = FP8 ? p.xs + (size_t)t * (p.H / 32) : nullptr;
-    for (int i = 0; i < 4; i++) {
-        const int f = f0 + warp * 4 + i;
-        const size_t row = (size_t)e * 2 * p.F + f / 128 * 256 + f % 128;
-        const char* w = static_cast<const char*>(p.w13);
-        const float a = warp_dot<FP8>(x, xs, w + row * p.H * esz, FP8 ? p.w13s + row * (p.H / 32) : nullptr, p.H);
-        const float b = warp_dot<FP8>(x, xs, w + (row + 128) * p.H * esz,
-                                      FP8 ? p.w13s + (row + 128) * (p.H / 32) : nullptr, p.H);
-        if (lane == 0) col[warp * 4 + i] = a / (1.0f + expf(-a)) * b;
+    __device__ bool next(FewRun& r) {
+        constexpr int BK = FP8 ? 128 : 64;
+        const int ft = p.F / 64;
+        if (u < pl.A * ft) {
+            r.phase = 0;
+            r.a = u / ft;
+            r.tile = u - r.a * ft;
+            r.kb0 = 0;
+            r.nkb = p.H / BK;
+            const int c = r.tile * 64;
+            r.row0 = pl.e[r.a] * 2 * p.F + c / 128 * 256 + c % 128;
+            r.row1 = r.row0 + 128;
+            r.brow = 0;
+            r.bn = p.nb;
+            u += gridDim.x;
+            return true;
+        }
+        if (w >= w1) return false;
+        const int kbs = p.F / BK;
+        const int q = w / kbs;
+        r.phase = 1;
+        r.tile = q / pl.A;
+        r.a = q - r.tile * pl.A;
+        r.kb0 = w - q * kbs;
+        r.nkb = min(kbs - r.kb0, w1 - w);
+        r.row0 = pl.e[r.a] * p.H + r.tile * 128;
+        r.row1 = r.row0 + 64;
+        r.brow = pl.off[r.a];
+        r.bn = (pl.off[r.a + 1] - r.brow + 15) & ~15;
+        w += r.nkb;
+        return true;
+    }
+};
+
+// Whether all CTAs have written their h (then the loads that follow, TMA's, see it).
+__device__ __forceinline__ bool few_h_ready(const unsigned* count) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+    if (v < gridDim.x) return false;
+    asm volatile("fence.proxy.async;" ::: "memory");
+    return true;
+}
+
+// Bounded wait for it.
+__device__ __forceinline__ bool few_wait_h(const unsigned* count, volatile uint32_t* abort_flag) {
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!few_h_ready(count)) {
+        if (*abort_flag) return false;
+        if (ptx::globaltimer_ns() - t0 > ptx::WAIT_LIMIT_NS) {
+            *abort_flag = 1u;
+            raise_device_error(MOE_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// Whether all 128 epilogue threads say yes: what they decide on is the same in all of them.
+__device__ __forceinline__ bool epi_all(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred P, Q;\n setp.ne.b32 P, %1, 0;\n barrier.cta.red.and.pred Q, 1, 128, P;\n"
+        " selp.u32 %0, 1, 0, Q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)ok)
+        : "memory");
+    return r != 0;
+}
+
+// A warp's bounded wait: the same answer in all of its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
+    return __all_sync(FULL, ptx::wait_parity(bar, parity, abort_flag));
+}
+
+// One TMEM column (dynamic) of this warp's lane quarter.
+__device__ __forceinline__ uint32_t tmem_ld_x1(uint32_t taddr) {
+    uint32_t v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr));
+    return v;
+}
+
+// 16 consecutive TMEM columns of this warp's lane quarter.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// The loads into r have completed (r passes through, so that no use of it moves ahead of the wait).
+__device__ __forceinline__ void tmem_wait16(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+template <bool FP8>
+constexpr int few_threads() { return FP8 ? 224 : 192; }
+
+// The plan, the same in every CTA: experts in ascending order, an expert's tokens in ascending order.
+// scratch: 8 E bytes (token masks) and 2 E bytes (an expert's index among the chosen), in the ring.
+template <int THREADS>
+__device__ void few_plan(const FewArgs& p, FewSmem& sm, uint8_t* scratch, unsigned long long* s_mask, int* s_e,
+                         int* s_off, float* s_w) {
+    unsigned long long* mask = reinterpret_cast<unsigned long long*>(scratch);
+    uint16_t* index = reinterpret_cast<uint16_t*>(scratch + (size_t)p.E * 8);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int e = tid; e < p.E; e += THREADS) mask[e] = 0ull;
+    if (tid == 0) sm.routes = 0;
+    __syncthreads();
+    pdl_wait();               // the routes are the first kernel's
+    const int R = p.T * p.K;
+    int valid = 0;
+    for (int r = tid; r < R; r += THREADS) {
+        const int e = load_id(p.ids, r, p.i16);
+        if (e >= 0 && e < p.E) {
+            atomicOr(&mask[e], 1ull << (r / p.K));
+            valid++;
+        } else if (e != -1 && blockIdx.x == 0) {
+            raise_device_error(MOE_DEVERR_BAD_ID);
+        }
+    }
+    if (valid) atomicAdd(&sm.routes, valid);
+    __syncthreads();
+    // exclusive scan of (chosen, tokens) over the experts, a stretch of them per thread
+    const int per = (p.E + THREADS - 1) / THREADS;
+    const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
+    int n = 0, m = 0;
+    for (int e = e0; e < e1; e++) {
+        const unsigned long long b = mask[e];
+        n += b != 0ull;
+        m += __popcll(b);
+    }
+    int sn = n, sm_ = m;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int a = __shfl_up_sync(FULL, sn, d), c = __shfl_up_sync(FULL, sm_, d);
+        if (lane >= d) {
+            sn += a;
+            sm_ += c;
+        }
+    }
+    if (lane == 31) {
+        sm.scan[0][warp] = sn;
+        sm.scan[1][warp] = sm_;
     }
     __syncthreads();
-    if (warp == 0) {
-        const float h = col[lane];
-        const size_t o = (size_t)r * p.F + f0 + lane;
-        if constexpr (FP8) {
-            float amax = fabsf(h);
-#pragma unroll
-            for (int o2 = 16; o2 > 0; o2 >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o2));
-            const int sb = e8m0_scale_byte(amax);
-            static_cast<uint8_t*>(p.h)[o] = (uint8_t)f32x2_to_e4m3x2(h * e8m0_inv_scale(sb), 0.0f);
-            if (lane == 0) p.hs[o / 32] = (uint8_t)sb;
-        } else {
-            static_cast<__nv_bfloat16*>(p.h)[o] = __float2bfloat16_rn(h);
-        }
+    int a = sn - n, o = sm_ - m;
+    for (int i = 0; i < warp; i++) {
+        a += sm.scan[0][i];
+        o += sm.scan[1][i];
     }
+    for (int e = e0; e < e1; e++) {
+        const unsigned long long b = mask[e];
+        if (!b) continue;
+        s_mask[a] = b;
+        s_e[a] = e;
+        s_off[a] = o;
+        index[e] = (uint16_t)a;
+        a++;
+        o += __popcll(b);
+    }
+    if (tid == THREADS - 1) {
+        sm.A = a;
+        sm.slots = o;
+        s_off[a] = o;
+    }
+    __syncthreads();
+    // each route's weight at its row of h; an expert that a token names more than once has one row,
+    // weighted with the sum (in ascending k)
+    const bool repeated = sm.slots != sm.routes;
+    for (int r = tid; r < R; r += THREADS) {
+        const int e = load_id(p.ids, r, p.i16);
+        if (e < 0 || e >= p.E) continue;
+        const int t = r / p.K;
+        float w = p.probs[r];
+        if (repeated) {
+            bool first = true;
+            for (int j = t * p.K; j < r; j++) first = first && load_id(p.ids, j, p.i16) != e;
+            if (!first) continue;
+            for (int j = r + 1; j < (t + 1) * p.K; j++)
+                if (load_id(p.ids, j, p.i16) == e) w += p.probs[j];
+        }
+        s_w[s_off[index[e]] + __popcll(mask[e] & ((1ull << t) - 1))] = w;
+    }
+    ptx::fence_proxy_async_smem();     // the ring, used as scratch here, is TMA's from now on
 }
 
-// y of one token and 32 columns of H per CTA (8 warps, four columns each).
 template <bool FP8>
-__global__ void __launch_bounds__(256) few_down_kernel(FewArgs p) {
-    const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = (int)lane_id();
-    const size_t esz = FP8 ? 1 : 2;
-    for (int i = 0; i < 4; i++) {
-        const int c = blockIdx.y * 32 + warp * 4 + i;
-        float acc = 0.0f;
-        for (int k = 0; k < p.K; k++) {
-            const int r = t * p.K + k, e = load_id(p.ids, r, p.i16);
-            if (e < 0 || e >= p.E) continue;
-            const size_t row = (size_t)e * p.H + c;
-            const float d = warp_dot<FP8>(static_cast<const char*>(p.h) + (size_t)r * p.F * esz,
-                                          FP8 ? p.hs + (size_t)r * (p.F / 32) : nullptr,
-                                          static_cast<const char*>(p.w2) + row * p.F * esz,
-                                          FP8 ? p.w2s + row * (p.F / 32) : nullptr, p.F);
-            acc = fmaf(__ldg(p.probs + r), d, acc);
+__global__ void __launch_bounds__(few_threads<FP8>(), 1)
+    few_layer_kernel(const __grid_constant__ CUtensorMap tmW13, const __grid_constant__ CUtensorMap tmW2,
+                     const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmH,
+                     const __grid_constant__ CUtensorMap tmSW13, const __grid_constant__ CUtensorMap tmSW2,
+                     const __grid_constant__ CUtensorMap tmSX, const __grid_constant__ CUtensorMap tmSH,
+                     const FewArgs p) {
+    constexpr int THREADS = few_threads<FP8>();
+    constexpr int BK = FP8 ? 128 : 64;
+    constexpr int TMEM_COLS = FP8 ? 256 : 128;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int stages = p.stages;
+    const int stage_bytes = FEW_A_BYTES + p.nb * 128;
+    uint8_t* at = ring + (size_t)stages * stage_bytes;
+    uint8_t* sfring = at;                                            // MXFP8
+    at += FP8 ? FEW_SF_SLOTS * FEW_SF_BYTES : 0;
+    FewSmem& sm = *reinterpret_cast<FewSmem*>(at);
+    at += few_up16(sizeof(FewSmem));
+    float* acc = reinterpret_cast<float*>(at);                       // [T][128] output sums
+    at += (size_t)p.T * 512;
+    unsigned long long* s_mask = reinterpret_cast<unsigned long long*>(at);
+    at += few_up16((size_t)p.a_max * 8);
+    int* s_e = reinterpret_cast<int*>(at);
+    at += few_up16((size_t)p.a_max * 4);
+    int* s_off = reinterpret_cast<int*>(at);
+    at += few_up16((size_t)(p.a_max + 1) * 4);
+    float* s_w = reinterpret_cast<float*>(at);
+    volatile uint32_t* s_abort = &sm.abort_flag;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < FEW_STAGES; s++) {
+            ptx::mbar_init(&sm.full[s], 1);
+            ptx::mbar_init(&sm.empty[s], 1);
         }
-        if (lane == 0) p.y[(size_t)t * p.H + c] = __float2bfloat16_rn(acc);
+        for (int s = 0; s < 2; s++) {
+            ptx::mbar_init(&sm.tfull[s], 1);
+            ptx::mbar_init(&sm.tempty[s], 4);
+        }
+        for (int s = 0; s < FEW_SF_SLOTS; s++) {
+            ptx::mbar_init(&sm.sf_full[s], 1);
+            ptx::mbar_init(&sm.sf_ready[s], 1);
+            ptx::mbar_init(&sm.sf_empty[s], 1);
+        }
+        ptx::mbar_init(&sm.done, 1);
+        sm.abort_flag = 0u;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tmap(&tmW13);
+        ptx::prefetch_tmap(&tmW2);
+        ptx::prefetch_tmap(&tmX);
+        ptx::prefetch_tmap(&tmH);
+        if constexpr (FP8) {
+            ptx::prefetch_tmap(&tmSW13);
+            ptx::prefetch_tmap(&tmSW2);
+            ptx::prefetch_tmap(&tmSX);
+            ptx::prefetch_tmap(&tmSH);
+        }
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(&sm.tmem, TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    few_plan<THREADS>(p, sm, ring, s_mask, s_e, s_off, s_w);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    FewPlan pl{s_mask, s_e, s_off, s_w, sm.A, 0, 1};
+    pl.W = (p.H / 128) * pl.A * (p.F / BK);
+    pl.parts = max(1, min((int)gridDim.x, pl.W / FEW_MIN_KB));
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        FewWalk<FP8> wk(p, pl);
+        FewRun r;
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true, have = wk.next(r);
+        int kb = 0;
+        auto load_a = [&](int st, const FewRun& q, int k) {
+            if (lane == 0) {
+                uint8_t* sa = ring + (size_t)st * stage_bytes;
+                ptx::mbar_arrive_expect_tx(&sm.full[st], FEW_A_BYTES + q.bn * 128);
+                const CUtensorMap* tm = q.phase ? &tmW2 : &tmW13;
+                ptx::tma_load_2d(sa, tm, &sm.full[st], (q.kb0 + k) * BK, q.row0);
+                ptx::tma_load_2d(sa + FEW_A_BYTES / 2, tm, &sm.full[st], (q.kb0 + k) * BK, q.row1);
+            }
+        };
+        auto load_b = [&](int st, const FewRun& q, int k) {
+            if (lane == 0) {
+                uint8_t* sb = ring + (size_t)st * stage_bytes + FEW_A_BYTES;
+                if (q.phase == 0) {
+                    ptx::tma_load_2d(sb, &tmX, &sm.full[st], k * BK, 0);
+                } else {
+                    for (int i = 0; i < q.bn; i += 16)
+                        ptx::tma_load_2d(sb + i * 128, &tmH, &sm.full[st], (q.kb0 + k) * BK, q.brow + i);
+                }
+            }
+        };
+        auto step = [&]() {
+            __syncwarp();
+            issued++;
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
+            if (++kb == r.nkb) { kb = 0; have = wk.next(r); }
+        };
+        while (ok && have && r.phase == 0) {
+            ok = warp_wait(&sm.empty[stage], phase ^ 1u, s_abort);
+            if (!ok) break;
+            load_a(stage, r, kb);
+            load_b(stage, r, kb);
+            step();
+        }
+        if (ok && have) {
+            // the ring's worth of down weights, then (once all of h is written) their tokens operand
+            FewWalk<FP8> wb = wk;
+            FewRun rb = r;
+            int sb = stage, kbb = kb, n = 0;
+            while (have && n < stages) {
+                ok = warp_wait(&sm.empty[stage], phase ^ 1u, s_abort);
+                if (!ok) break;
+                load_a(stage, r, kb);
+                step();
+                n++;
+            }
+            ok = __all_sync(FULL, few_wait_h(p.count, s_abort)) && ok;
+            for (int i = 0; i < n; i++) {    // (also when giving up: the stages' loads have to complete)
+                load_b(sb, rb, kbb);
+                if (++sb == stages) sb = 0;
+                if (++kbb == rb.nkb) { kbb = 0; wb.next(rb); }
+            }
+            while (ok && have) {
+                ok = warp_wait(&sm.empty[stage], phase ^ 1u, s_abort);
+                if (!ok) break;
+                load_a(stage, r, kb);
+                load_b(stage, r, kb);
+                step();
+            }
+        }
+        if (!ok) {
+            // give the loads already issued a bounded chance to land before the CTA exits
+            for (int i = 0; i < stages && i < issued; i++) {
+                if (--stage < 0) { stage = stages - 1; phase ^= 1u; }
+                volatile uint32_t never = 0u;
+                ptx::wait_parity(&sm.full[stage], phase, &never, 100000000ull);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        FewWalk<FP8> wk(p, pl);
+        FewRun r;
+        int stage = 0, buf = 0, sslot = 0;
+        uint32_t phase = 0, tphase = 0, sphase = 0;
+        bool ok = true;
+        while (ok && wk.next(r)) {
+            if (!warp_wait(&sm.tempty[buf], tphase ^ 1u, s_abort)) break;
+            ptx::tc_fence_after();
+            const uint32_t d = tmem + (uint32_t)(buf * FEW_ACC_COLS);
+            for (int kb = 0; kb < r.nkb; kb++) {
+                const int gk = r.kb0 + kb;
+                ok = warp_wait(&sm.full[stage], phase, s_abort);
+                if (!ok) break;
+                if (FP8 && (kb == 0 || (gk & 3) == 0)) {
+                    ok = warp_wait(&sm.sf_ready[sslot], sphase, s_abort);
+                    if (!ok) break;
+                }
+                ptx::tc_fence_after();
+                const bool group_end = kb == r.nkb - 1 || (gk & 3) == 3;
+                if (lane == 0) {
+                    const uint32_t a0 = ptx::smem_addr(ring + (size_t)stage * stage_bytes);
+                    const uint32_t b0 = a0 + FEW_A_BYTES;
+                    if constexpr (FP8) {
+                        const uint32_t sf_t = tmem + (uint32_t)(2 * FEW_ACC_COLS + stage * 8);
+                        const uint32_t sf_s = ptx::smem_addr(sfring + (size_t)sslot * FEW_SF_BYTES + (gk & 3) * 1024);
+                        ptx::tc_cp_32x128b_warpx4(sf_t, ptx::sdesc_plain(sf_s));
+                        ptx::tc_cp_32x128b_warpx4(sf_t + 4, ptx::sdesc_plain(sf_s + 512));
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            ptx::mma_mxf8(d, ptx::sdesc_k_sw128(a0 + k * 32), ptx::sdesc_k_sw128(b0 + k * 32),
+                                          ptx::idesc_mxf8(128, r.bn, k, k), sf_t, sf_t + 4, (kb | k) != 0);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            ptx::mma_f16(d, ptx::sdesc_k_sw128(a0 + k * 32), ptx::sdesc_k_sw128(b0 + k * 32),
+                                         ptx::idesc_bf16(128, r.bn), (kb | k) != 0);
+                    }
+                    ptx::tc_commit(&sm.empty[stage]);
+                    if (FP8 && group_end) ptx::tc_commit(&sm.sf_empty[sslot]);
+                }
+                __syncwarp();
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
+                if (FP8 && group_end && ++sslot == FEW_SF_SLOTS) { sslot = 0; sphase ^= 1u; }
+            }
+            if (!ok) break;
+            if (lane == 0) ptx::tc_commit(&sm.tfull[buf]);
+            __syncwarp();
+            buf ^= 1;
+            if (buf == 0) tphase ^= 1u;
+        }
+        // every MMA issued has completed before TMEM is released
+        if (lane == 0) ptx::tc_commit(&sm.done);
+        __syncwarp();
+        volatile uint32_t never = 0u;
+        ptx::wait_parity(&sm.done, 0u, &never, 100000000ull);
+    } else if (FP8 && warp == 6) {
+        // ------------------------------------------------------------ scales (MXFP8)
+        // A group is the 16 scale bytes (four k-blocks) of every row of a tile: 128 weight rows, bn
+        // token rows. Landed, it is rearranged in place into four chunks for tcgen05.cp .32x128b:
+        // chunk w has k-block w's words, the word of row 32 j + lane at lane * 4 + j; first the weights'
+        // 512 bytes, then the tokens'. Loads and rearranging do not wait for one another.
+        if constexpr (FP8) {
+            struct Cursor {
+                FewWalk<FP8> wk;
+                FewRun r;
+                int kb;
+                bool have;
+            };
+            auto advance = [](Cursor& c) {
+                c.kb += 4 - ((c.r.kb0 + c.kb) & 3);
+                if (c.kb >= c.r.nkb) {
+                    c.kb = 0;
+                    c.have = c.wk.next(c.r);
+                }
+            };
+            Cursor ld{FewWalk<FP8>(p, pl), FewRun{}, 0, false};
+            ld.have = ld.wk.next(ld.r);
+            int ld_slot = 0, pr_slot = 0, loaded = 0;
+            uint32_t ld_phase = 0, pr_phase = 0;
+            bool h_seen = false;
+            uint64_t t_idle = ptx::globaltimer_ns();
+            while (ld.have || loaded > 0) {
+                bool progress = false;
+                // (down scales: once h's are written; the groups landed meanwhile are not held up)
+                if (ld.have && ld.r.phase == 1 && !h_seen) h_seen = __all_sync(FULL, few_h_ready(p.count));
+                if (ld.have && (ld.r.phase == 0 || h_seen) && loaded < FEW_SF_SLOTS &&
+                    __all_sync(FULL, ptx::mbar_test_wait(&sm.sf_empty[ld_slot], ld_phase ^ 1u))) {
+                    if (lane == 0) {
+                        uint8_t* sf = sfring + (size_t)ld_slot * FEW_SF_BYTES;
+                        const int kx = ((ld.r.kb0 + ld.kb) >> 2) * 16;
+                        const CUtensorMap* tm = ld.r.phase ? &tmSW2 : &tmSW13;
+                        ptx::mbar_arrive_expect_tx(&sm.sf_full[ld_slot], (128 + ld.r.bn) * 16);
+                        ptx::tma_load_2d(sf, tm, &sm.sf_full[ld_slot], kx, ld.r.row0);
+                        ptx::tma_load_2d(sf + 1024, tm, &sm.sf_full[ld_slot], kx, ld.r.row1);
+                        if (ld.r.phase == 0) {
+                            ptx::tma_load_2d(sf + 2048, &tmSX, &sm.sf_full[ld_slot], kx, 0);
+                        } else {
+                            for (int i = 0; i < ld.r.bn; i += 16)
+                                ptx::tma_load_2d(sf + 2048 + i * 16, &tmSH, &sm.sf_full[ld_slot], kx, ld.r.brow + i);
+                        }
+                    }
+                    __syncwarp();
+                    loaded++;
+                    advance(ld);
+                    if (++ld_slot == FEW_SF_SLOTS) { ld_slot = 0; ld_phase ^= 1u; }
+                    progress = true;
+                }
+                if (loaded > 0 && __all_sync(FULL, ptx::mbar_test_wait(&sm.sf_full[pr_slot], pr_phase))) {
+                    uint8_t* sf = sfring + (size_t)pr_slot * FEW_SF_BYTES;
+                    const uint4* l = reinterpret_cast<const uint4*>(sf);
+                    uint4 v[6];
+#pragma unroll
+                    for (int j = 0; j < 6; j++) v[j] = l[32 * j + lane];
+                    __syncwarp();
+                    uint4* out = reinterpret_cast<uint4*>(sf);
+#pragma unroll
+                    for (int w = 0; w < 4; w++) {
+                        auto word = [w](const uint4& q) { return w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w; };
+                        out[w * 64 + lane] = make_uint4(word(v[0]), word(v[1]), word(v[2]), word(v[3]));
+                        out[w * 64 + 32 + lane] = make_uint4(word(v[4]), word(v[5]), 0u, 0u);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&sm.sf_ready[pr_slot]);
+                    loaded--;
+                    if (++pr_slot == FEW_SF_SLOTS) { pr_slot = 0; pr_phase ^= 1u; }
+                    progress = true;
+                }
+                if (progress) {
+                    t_idle = ptx::globaltimer_ns();
+                } else if (__any_sync(FULL, *s_abort != 0u)) {
+                    break;
+                } else if (__any_sync(FULL, ptx::globaltimer_ns() - t_idle > ptx::WAIT_LIMIT_NS)) {
+                    *s_abort = 1u;
+                    raise_device_error(MOE_DEVERR_TIMEOUT);
+                    break;
+                }
+            }
+            for (int i = 0; i < loaded; i++) {     // loads in flight land before the CTA exits
+                volatile uint32_t never = 0u;
+                ptx::wait_parity(&sm.sf_full[pr_slot], pr_phase, &never, 100000000ull);
+                if (++pr_slot == FEW_SF_SLOTS) { pr_slot = 0; pr_phase ^= 1u; }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue (4 warps)
+        const int q = warp & 3;                         // TMEM lane quarter
+        const int row = q * 32 + lane;                  // weight row of the tile
+        const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
+        FewWalk<FP8> wk(p, pl);
+        FewRun r;
+        int buf = 0, xb = 0;
+        uint32_t tphase = 0;
+        bool ok = true, have = wk.next(r);
+        auto release = [&]() {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sm.tempty[buf]);
+            buf ^= 1;
+            if (buf == 0) tphase ^= 1u;
+        };
+        // up: lanes 0-63 hold the gate products, 64-127 the same columns' linear ones; those go over
+        // through shared memory, FEW_XCH tokens at a time, two buffers in turn
+        while (ok && have && r.phase == 0) {
+            ok = ptx::wait_parity(&sm.tfull[buf], tphase, s_abort);
+            ok = epi_all(ok);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            unsigned long long m = pl.mask[r.a];
+            int slot = pl.off[r.a];
+            while (m) {
+                uint32_t v[FEW_XCH];
+                int n = 0;
+                unsigned long long mm = m;
+#pragma unroll
+                for (int i = 0; i < FEW_XCH; i++) {
+                    v[i] = 0u;
+                    if (mm) {                            // uniform
+                        v[i] = tmem_ld_x1(tq + (uint32_t)(buf * FEW_ACC_COLS + __ffsll((long long)mm) - 1));
+                        mm &= mm - 1;
+                        n++;
+                    }
+                }
+                tmem_wait16(v);
+                m = mm;
+                if (q >= 2) {
+#pragma unroll
+                    for (int i = 0; i < FEW_XCH; i++)
+                        if (i < n) sm.xch[xb][i][row - 64] = __uint_as_float(v[i]);
+                }
+                epi_sync();
+                if (q < 2) {
+#pragma unroll
+                    for (int i = 0; i < FEW_XCH; i++) {
+                        if (i >= n) break;
+                        const float ga = __uint_as_float(v[i]);
+                        const float h = ga / (1.0f + expf(-ga)) * sm.xch[xb][i][row];
+                        const size_t o = (size_t)(slot + i) * p.F + r.tile * 64 + row;
+                        if constexpr (FP8) {
+                            const float amax = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(fabsf(h))));
+                            const int sbyte = e8m0_scale_byte(amax);
+                            static_cast<uint8_t*>(p.h)[o] = (uint8_t)f32x2_to_e4m3x2(h * e8m0_inv_scale(sbyte), 0.0f);
+                            if (lane == 0) p.hs[o >> 5] = (uint8_t)sbyte;
+                        } else {
+                            static_cast<__nv_bfloat16*>(p.h)[o] = __float2bfloat16_rn(h);
+                        }
+                    }
+                }
+                slot += n;
+                xb ^= 1;
+            }
+            release();
+            have = wk.next(r);
+        }
+        // this CTA's h is written: made visible to the other CTAs' TMA loads, then counted
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __threadfence();
+        epi_sync();
+        if (threadIdx.x == 64) {
+            __threadfence();
+            asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p.count), "r"(1u) : "memory");
+        }
+        // down
+        const int per_tile = pl.A * (p.F / BK);         // k-blocks of an output tile
+        int tile = -1;
+        const int first_tile = have ? r.tile : -1;
+        auto owner = [&](int w) {                       // the CTA whose piece has k-block w
+            int c = (int)((long long)w * pl.parts / pl.W);
+            while (pl.begin_of(c) > w) c--;
+            while (pl.begin_of(c + 1) <= w) c++;
+            return c;
+        };
+        auto flush = [&]() {
+            const int c0 = owner(tile * per_tile), c1 = owner((tile + 1) * per_tile - 1);
+            __nv_bfloat16* y = p.y + tile * 128 + row;
+            if (c0 == c1) {
+                for (int t = 0; t < p.T; t++) y[(size_t)t * p.H] = __float2bfloat16_rn(acc[t * 128 + row]);
+                return;
+            }
+            float* mine = p.part + ((size_t)2 * blockIdx.x + (tile != first_tile)) * p.T * 128 + row;
+            for (int t = 0; t < p.T; t++) __stcg(mine + t * 128, acc[t * 128 + row]);
+            __threadfence();
+            epi_sync();
+            if (threadIdx.x == 64) sm.ticket = (int)atomicAdd(p.count + 1 + tile, 1u);
+            epi_sync();
+            if (sm.ticket != c1 - c0) return;
+            __threadfence();
+            for (int t0 = 0; t0 < p.T; t0 += 4) {
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int c = c0; c <= c1; c++) {
+                    const int which = pl.begin_of(c) / per_tile != tile;
+                    const float* src = p.part + ((size_t)2 * c + which) * p.T * 128 + row;
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        if (t0 + i < p.T) v[i] += __ldcg(src + (t0 + i) * 128);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    if (t0 + i < p.T) y[(size_t)(t0 + i) * p.H] = __float2bfloat16_rn(v[i]);
+            }
+        };
+        while (ok && have) {
+            if (r.tile != tile) {
+                if (tile >= 0) flush();
+                tile = r.tile;
+                for (int t = 0; t < p.T; t++) acc[t * 128 + row] = 0.0f;
+            }
+            ok = ptx::wait_parity(&sm.tfull[buf], tphase, s_abort);
+            ok = epi_all(ok);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            unsigned long long m = pl.mask[r.a];
+            const int m_a = pl.off[r.a + 1] - pl.off[r.a];
+            const float* wt = pl.w + pl.off[r.a];
+            for (int i0 = 0; i0 < m_a; i0 += 16) {
+                uint32_t v[16];
+                tmem_ld_x16(tq + (uint32_t)(buf * FEW_ACC_COLS + i0), v);
+                tmem_wait16(v);
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    if (i0 + i >= m_a) break;
+                    const int t = __ffsll((long long)m) - 1;
+                    m &= m - 1;
+                    acc[t * 128 + row] = fmaf(wt[i0 + i], __uint_as_float(v[i]), acc[t * 128 + row]);
+                }
+            }
+            release();
+            have = wk.next(r);
+        }
+        if (ok && tile >= 0) flush();
+        if (pl.A == 0) {
+            // no valid route at all: zeros
+            for (long long i = (long long)blockIdx.x * 128 + row; i < (long long)p.T * p.H; i += (long long)gridDim.x * 128)
+                p.y[i] = __float2bfloat16_rn(0.0f);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, TMEM_COLS);
     }
 }
 
-// Workspace: x's codes and scales (MXFP8), h (and its scales), each region 128-byte aligned.
+// Workspace: counters, x's codes and scales (MXFP8), h (and its scales), partial sums; each region
+// 128-byte aligned.
 struct FewLayout {
-    size_t xq, xs, h, hs, bytes;
+    size_t count, xq, xs, h, hs, part, bytes;
 };
+
+int few_sms() {
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+constexpr int FEW_GRID_MAX = 256;          // CTAs that the workspace has room for
 
 FewLayout few_layout(int T, int K, int H, int F, bool fp8) {
     auto up = [](size_t v) { return (v + 127) & ~(size_t)127; };
     FewLayout l{};
     size_t o = 0;
+    l.count = o;
+    o += up((size_t)(1 + H / 128) * 4);
     l.xq = o;
     o += fp8 ? up((size_t)T * H) : 0;
     l.xs = o;
@@ -341,6 +1000,8 @@ FewLayout few_layout(int T, int K, int H, int F, bool fp8) {
     o += up((size_t)T * K * F * (fp8 ? 1 : 2));
     l.hs = o;
     o += fp8 ? up((size_t)T * K * (F / 32)) : 0;
+    l.part = o;
+    o += (size_t)2 * FEW_GRID_MAX * T * 128 * 4;
     l.bytes = o;
     return l;
 }
@@ -356,16 +1017,59 @@ moe_status few_sizes(int T, int K, int E, int H, int F, moe_dtype dtype) {
 }
 
 template <bool FP8>
-moe_status few_launch(FewArgs a, const PrepArgs& p, cudaStream_t s) {
-    if (p.logits || p.xq) {
-        const int V = p.logits ? (p.E + PREP_THREADS - 1) / PREP_THREADS : 1;
-        if (V <= 1) few_prep_kernel<1><<<a.T, PREP_THREADS, 0, s>>>(p);
-        else if (V <= 4) few_prep_kernel<4><<<a.T, PREP_THREADS, 0, s>>>(p);
-        else if (V <= 12) few_prep_kernel<12><<<a.T, PREP_THREADS, 0, s>>>(p);
-        else few_prep_kernel<32><<<a.T, PREP_THREADS, 0, s>>>(p);
+moe_status few_launch(FewArgs a, const PrepArgs& p, const void* x, const uint8_t* xs, const void* w13,
+                      const uint8_t* w13s, const void* w2, const uint8_t* w2s, cudaStream_t s) {
+    // shared memory: as many ring stages as fit beside the plan and the output sums
+    const size_t fixed = 1024 + few_fixed_smem(a.T, a.K, a.a_max, FP8);
+    const int stage_bytes = FEW_A_BYTES + a.nb * 128;
+    if (fixed + 4 * (size_t)stage_bytes > FEW_SMEM_MAX) return MOE_ERR_UNSUPPORTED;
+    a.stages = (int)((FEW_SMEM_MAX - fixed) / stage_bytes);
+    if (a.stages > FEW_STAGES) a.stages = FEW_STAGES;
+    if ((size_t)a.stages * stage_bytes < (size_t)a.E * 10) return MOE_ERR_UNSUPPORTED;   // the plan's scratch
+    const size_t smem = fixed + (size_t)a.stages * stage_bytes;
+    CUtensorMap tw13, tw2, tx, th, ts13, ts2, tsx, tsh;
+    using moe_host::make_operand_map;
+    using moe_host::make_scale_map;
+    const uint64_t r13 = (uint64_t)a.E * 2 * a.F, r2 = (uint64_t)a.E * a.H, rh = (uint64_t)a.T * a.K;
+    if (!make_operand_map(&tw13, w13, FP8, a.H, r13, 64) || !make_operand_map(&tw2, w2, FP8, a.F, r2, 64) ||
+        !make_operand_map(&tx, x, FP8, a.H, a.T, a.nb) || !make_operand_map(&th, a.h, FP8, a.F, rh, 16))
+        return MOE_ERR_CUDA;
+    if (FP8) {
+        if (!make_scale_map(&ts13, w13s, a.H / 32, r13, 64) || !make_scale_map(&ts2, w2s, a.F / 32, r2, 64) ||
+            !make_scale_map(&tsx, xs, a.H / 32, a.T, a.nb) || !make_scale_map(&tsh, a.hs, a.F / 32, rh, 16))
+            return MOE_ERR_CUDA;
+    } else {
+        ts13 = ts2 = tsx = tsh = tw13;
     }
-    few_up_kernel<FP8><<<dim3(a.T * a.K, a.F / 32), 256, 0, s>>>(a);
-    few_down_kernel<FP8><<<dim3(a.T, a.H / 32), 256, 0, s>>>(a);
+    auto kern = few_layer_kernel<FP8>;
+    static size_t configured = 0;
+    if (smem > configured) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FEW_SMEM_MAX) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        configured = FEW_SMEM_MAX;
+    }
+    const int V = p.logits ? (p.E + PREP_THREADS - 1) / PREP_THREADS : 1;
+    if (V <= 1) few_prep_kernel<1><<<a.T, PREP_THREADS, 0, s>>>(p);
+    else if (V <= 4) few_prep_kernel<4><<<a.T, PREP_THREADS, 0, s>>>(p);
+    else if (V <= 12) few_prep_kernel<12><<<a.T, PREP_THREADS, 0, s>>>(p);
+    else few_prep_kernel<32><<<a.T, PREP_THREADS, 0, s>>>(p);
+    if (cudaPeekAtLastError() != cudaSuccess) return moe_host::launch_status();
+    int grid = few_sms();
+    if (grid > FEW_GRID_MAX) grid = FEW_GRID_MAX;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(few_threads<FP8>());
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;      // the CTAs wait for one another: all resident, or none
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, tw13, tw2, tx, th, ts13, ts2, tsx, tsh, a) != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
     return moe_host::launch_status();
 }
 
@@ -412,13 +1116,9 @@ extern "C" moe_status moe_layer_few_tokens(const void* x, int T, int H, const fl
     p.probs = probs;
     p.xq = fp8 ? ws + l.xq : nullptr;
     p.xs = fp8 ? ws + l.xs : nullptr;
+    p.count = reinterpret_cast<unsigned*>(ws + l.count);
+    p.n_count = 1 + H / 128;
     FewArgs a{};
-    a.x = fp8 ? p.xq : x;
-    a.xs = p.xs;
-    a.w13 = w13_packed;
-    a.w13s = w13_scales;
-    a.w2 = w2_packed;
-    a.w2s = w2_scales;
     a.ids = ids;
     a.probs = probs;
     a.i16 = p.i16;
@@ -427,9 +1127,14 @@ extern "C" moe_status moe_layer_few_tokens(const void* x, int T, int H, const fl
     a.K = K;
     a.E = E;
     a.F = F;
+    a.nb = (T + 15) / 16 * 16;
+    a.a_max = E < T * K ? E : T * K;
     a.h = ws + l.h;
     a.hs = fp8 ? ws + l.hs : nullptr;
+    a.part = reinterpret_cast<float*>(ws + l.part);
+    a.count = p.count;
     a.y = static_cast<__nv_bfloat16*>(y);
     const cudaStream_t s = moe_host::as_stream(stream);
-    return fp8 ? few_launch<true>(a, p, s) : few_launch<false>(a, p, s);
+    return fp8 ? few_launch<true>(a, p, p.xq, p.xs, w13_packed, w13_scales, w2_packed, w2_scales, s)
+               : few_launch<false>(a, p, x, nullptr, w13_packed, nullptr, w2_packed, nullptr, s);
 }
