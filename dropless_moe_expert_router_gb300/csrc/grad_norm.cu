@@ -47,21 +47,113 @@ __device__ __forceinline__ double cta_sum(double v, double* red) {
     return v;
 }
 
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+// 16 bytes as floats and back
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[4], const float*) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[8], const __nv_bfloat16*) { bf16x8_to_f32(v, f); }
+__device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) { return f32_to_bf16x8(f); }
+
+// Elements before the first 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ int head_of(const T* p, int m) {
+    const int h = (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int)sizeof(T);
+    return h < m ? h : m;
+}
+
+// Squares of the m elements at p added to eight sums per thread: 16-byte pieces, four in flight, the
+// elements before the first boundary and after the last one singly.
+template <typename T>
+__device__ __forceinline__ void sumsq_piece(const T* p, int m, float (&acc)[8]) {
+    constexpr int VEC = 16 / sizeof(T);
+    const int h = head_of(p, m), n = (m - h) / VEC;
+    const uint4* q = reinterpret_cast<const uint4*>(p + h);
+    int j = threadIdx.x;
+    for (; j + 3 * GN_THREADS < n; j += 4 * GN_THREADS) {
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) v[u] = __ldg(q + j + u * GN_THREADS);
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            float f[VEC];
+            unpack(v[u], f, p);
+#pragma unroll
+            for (int k = 0; k < VEC; k++) acc[(u & 1) * (8 - VEC) + k] = fmaf(f[k], f[k], acc[(u & 1) * (8 - VEC) + k]);
+        }
+    }
+    for (; j < n; j += GN_THREADS) {
+        float f[VEC];
+        unpack(__ldg(q + j), f, p);
+#pragma unroll
+        for (int k = 0; k < VEC; k++) acc[k] = fmaf(f[k], f[k], acc[k]);
+    }
+    const int tail = h + n * VEC, rest = h + m - tail;      // (both below VEC: one element a thread)
+    if ((int)threadIdx.x < rest) {
+        const int k = (int)threadIdx.x < h ? (int)threadIdx.x : tail + (int)threadIdx.x - h;
+        const float f = to_f(p[k]);
+        acc[0] = fmaf(f, f, acc[0]);
+    }
+}
+
+// out = in * c; in and out may be the same. Pieces of 16 bytes where both are aligned alike.
+template <typename T>
+__device__ __forceinline__ void scale_piece(const T* p, T* o, int m, float c) {
+    constexpr int VEC = 16 / sizeof(T);
+    if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) {
+        for (int j = threadIdx.x; j < m; j += GN_THREADS) put(o + j, to_f(p[j]) * c);
+        return;
+    }
+    const int h = head_of(p, m), n = (m - h) / VEC;
+    const uint4* q = reinterpret_cast<const uint4*>(p + h);
+    uint4* d = reinterpret_cast<uint4*>(o + h);
+    auto one = [&](const uint4& v) {
+        float f[VEC];
+        unpack(v, f, p);
+#pragma unroll
+        for (int k = 0; k < VEC; k++) f[k] *= c;
+        return pack(f);
+    };
+    int j = threadIdx.x;
+    for (; j + 3 * GN_THREADS < n; j += 4 * GN_THREADS) {
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) v[u] = __ldcs(q + j + u * GN_THREADS);
+#pragma unroll
+        for (int u = 0; u < 4; u++) __stcs(d + j + u * GN_THREADS, one(v[u]));
+    }
+    for (; j < n; j += GN_THREADS) d[j] = one(q[j]);
+    const int tail = h + n * VEC, rest = h + m - tail;
+    if ((int)threadIdx.x < rest) {
+        const int k = (int)threadIdx.x < h ? (int)threadIdx.x : tail + (int)threadIdx.x - h;
+        put(o + k, to_f(p[k]) * c);
+    }
+}
+
 __global__ void __launch_bounds__(GN_THREADS) grad_sumsq_kernel(const __grid_constant__ GradTable g, double* partial) {
     __shared__ double red[GN_THREADS / 32];
-    float acc = 0.0f;
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     for (int piece = blockIdx.x; piece < g.first[g.n]; piece += gridDim.x) {
         const int i = tensor_of(g, piece);
         const long long b = (long long)(piece - g.first[i]) * GN_CHUNK;
         const long long left = g.count[i] - b;
         const int m = left < GN_CHUNK ? (int)left : GN_CHUNK;
-        for (int j = threadIdx.x; j < m; j += GN_THREADS) {
-            const float v = g.f32[i] ? static_cast<const float*>(g.in[i])[b + j]
-                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(g.in[i])[b + j]);
-            acc = fmaf(v, v, acc);
-        }
+        if (g.f32[i]) sumsq_piece(static_cast<const float*>(g.in[i]) + b, m, acc);
+        else sumsq_piece(static_cast<const __nv_bfloat16*>(g.in[i]) + b, m, acc);
     }
-    const double s = cta_sum((double)acc, red);
+    double s = 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; k++) s += (double)acc[k];
+    s = cta_sum(s, red);
     if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
@@ -88,14 +180,9 @@ __global__ void __launch_bounds__(GN_THREADS) grad_scale_kernel(const __grid_con
         const long long b = (long long)(piece - g.first[i]) * GN_CHUNK;
         const long long left = g.count[i] - b;
         const int m = left < GN_CHUNK ? (int)left : GN_CHUNK;
-        for (int j = threadIdx.x; j < m; j += GN_THREADS) {
-            if (g.f32[i]) {
-                static_cast<float*>(g.out[i])[b + j] = static_cast<const float*>(g.in[i])[b + j] * c;
-            } else {
-                const float f = __bfloat162float(static_cast<const __nv_bfloat16*>(g.in[i])[b + j]);
-                static_cast<__nv_bfloat16*>(g.out[i])[b + j] = __float2bfloat16_rn(f * c);
-            }
-        }
+        if (g.f32[i]) scale_piece(static_cast<const float*>(g.in[i]) + b, static_cast<float*>(g.out[i]) + b, m, c);
+        else
+            scale_piece(static_cast<const __nv_bfloat16*>(g.in[i]) + b, static_cast<__nv_bfloat16*>(g.out[i]) + b, m, c);
     }
 }
 

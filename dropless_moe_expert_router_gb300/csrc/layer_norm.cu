@@ -7,6 +7,8 @@
 // Each operand is read once and each output written once: the bytes bound both directions.
 #include "common.cuh"
 
+#include <initializer_list>
+
 namespace moe {
 namespace {
 
@@ -19,28 +21,142 @@ template <typename T> __device__ __forceinline__ T from_f(float v);
 template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// Sum over the CTA, the same in every thread; red: 32 floats, free again after the next barrier.
-__device__ __forceinline__ float cta_sum(float v, float* red) {
+// VEC consecutive elements, moved in pieces of 16 bytes at most; bf16 pairs stay packed in registers.
+template <typename T, int VEC>
+struct alignas(VEC * sizeof(T) < 16 ? VEC * sizeof(T) : 16) Vec {
+    T v[VEC];
+    __device__ __forceinline__ float get(int j) const { return to_f(v[j]); }
+    __device__ __forceinline__ void set(const float* f) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
-    if (lane_id() == 0) red[threadIdx.x >> 5] = v;
+        for (int j = 0; j < VEC; j++) v[j] = from_f<T>(f[j]);
+    }
+};
+template <int VEC>
+struct alignas(VEC * 2 < 16 ? VEC * 2 : 16) VecBf16 {
+    uint32_t v[VEC / 2];
+    __device__ __forceinline__ float get(int j) const {
+        return __uint_as_float(j & 1 ? v[j / 2] & 0xffff0000u : v[j / 2] << 16);
+    }
+    __device__ __forceinline__ void set(const float* f) {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(f[j], f[j + 1]);
+            v[j / 2] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+    }
+};
+template <>
+struct Vec<__nv_bfloat16, 8> : VecBf16<8> {};
+template <>
+struct Vec<__nv_bfloat16, 4> : VecBf16<4> {};
+
+// Sums of N values over a row's threads (a warp, or the CTA), the same in every thread. red: 32 N floats,
+// free again once every thread has passed another such sum through other memory.
+template <int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], bool warp_row, float* red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int n = 0; n < N; n++) v[n] += __shfl_xor_sync(FULL, v[n], o);
+    if (warp_row) return;
+    const int warps = blockDim.x >> 5, lane = (int)lane_id();
+    if (lane == 0)
+#pragma unroll
+        for (int n = 0; n < N; n++) red[n * 32 + (threadIdx.x >> 5)] = v[n];
     __syncthreads();
-    v = lane_id() < (unsigned)warps ? red[lane_id()] : 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
-    return v;
+    for (int n = 0; n < N; n++) v[n] = lane < warps ? red[n * 32 + lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int n = 0; n < N; n++) v[n] += __shfl_xor_sync(FULL, v[n], o);
 }
 
-// One CTA per row; a row that does not fit in registers is read again for each sum.
+// ---------------------------------------------------------------------------
+// Forward, the row in registers: a row belongs to a warp (warp_row: 8 rows a CTA) or to a CTA, NV
+// pieces of VEC elements per thread, piece i at i * threads + thread. CTAs walk the rows with the
+// grid's stride; weight and bias come from L1.
+// ---------------------------------------------------------------------------
+template <typename T, typename W, int VEC, int NV>
+__global__ void __launch_bounds__(512) ln_forward_kernel(const T* x, const T* residual, int rows, int H, bool warp_row,
+                                                         const W* __restrict__ w, const W* __restrict__ b, float eps,
+                                                         T* sum, T* y, float* mean_out, float* rstd_out) {
+    __shared__ float red[2][32];
+    const int tpr = warp_row ? 32 : blockDim.x;
+    const int me = threadIdx.x % tpr, groups = blockDim.x / tpr;
+    const int n = H / VEC;
+    for (long long t = (long long)blockIdx.x * groups + threadIdx.x / tpr; t < rows; t += (long long)gridDim.x * groups) {
+        const Vec<T, VEC>* xr = reinterpret_cast<const Vec<T, VEC>*>(x + t * H);
+        Vec<T, VEC> xv[NV], rv[NV];
+        float f[NV][VEC];
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = me + i * tpr;
+            if (c < n) {
+                xv[i] = xr[c];
+                if (residual) rv[i] = reinterpret_cast<const Vec<T, VEC>*>(residual + t * H)[c];
+            }
+        }
+        float m[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = me + i * tpr;
+            if (c >= n) continue;
+            if (residual) {
+#pragma unroll
+                for (int j = 0; j < VEC; j++) f[i][j] = xv[i].get(j) + rv[i].get(j);
+                xv[i].set(f[i]);
+                reinterpret_cast<Vec<T, VEC>*>(sum + t * H)[c] = xv[i];
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; j++) {
+                f[i][j] = xv[i].get(j);
+                m[0] += f[i][j];
+            }
+        }
+        row_sum(m, warp_row, red[0]);
+        const float mean = m[0] / (float)H;
+        float q[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (me + i * tpr < n)
+#pragma unroll
+                for (int j = 0; j < VEC; j++) {
+                    f[i][j] -= mean;
+                    q[0] = fmaf(f[i][j], f[i][j], q[0]);
+                }
+        row_sum(q, warp_row, red[1]);
+        const float rstd = 1.0f / sqrtf(q[0] / (float)H + eps);
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = me + i * tpr;
+            if (c < n) {
+                const Vec<W, VEC> wv = reinterpret_cast<const Vec<W, VEC>*>(w)[c];
+                Vec<W, VEC> bv;
+                if (b) bv = reinterpret_cast<const Vec<W, VEC>*>(b)[c];
+                Vec<T, VEC> o;
+#pragma unroll
+                for (int j = 0; j < VEC; j++) f[i][j] = fmaf(f[i][j] * rstd, wv.get(j), b ? bv.get(j) : 0.0f);
+                o.set(f[i]);
+                reinterpret_cast<Vec<T, VEC>*>(y + t * H)[c] = o;
+            }
+        }
+        if (me == 0) {
+            if (mean_out) mean_out[t] = mean;
+            if (rstd_out) rstd_out[t] = rstd;
+        }
+    }
+}
+
+// Forward for rows too long for registers: the row is read again for each sum.
 template <typename T, typename W>
-__global__ void __launch_bounds__(256) ln_forward_kernel(const T* x, const T* residual, int H, const W* __restrict__ w,
-                                                         const W* __restrict__ b, float eps, T* sum, T* y,
-                                                         float* mean_out, float* rstd_out) {
+__global__ void __launch_bounds__(512) ln_forward_long_kernel(const T* x, const T* residual, int H,
+                                                              const W* __restrict__ w, const W* __restrict__ b,
+                                                              float eps, T* sum, T* y, float* mean_out,
+                                                              float* rstd_out) {
     __shared__ float red[2][32];
     const long long base = (long long)blockIdx.x * H;
-    float a = 0.0f;
+    float a[1] = {0.0f};
     for (int i = threadIdx.x; i < H; i += blockDim.x) {
         float v = to_f(x[base + i]);
         if (residual) {
@@ -48,16 +164,18 @@ __global__ void __launch_bounds__(256) ln_forward_kernel(const T* x, const T* re
             sum[base + i] = r;
             v = to_f(r);
         }
-        a += v;
+        a[0] += v;
     }
     const T* s = residual ? sum : x;
-    const float mean = cta_sum(a, red[0]) / (float)H;
-    a = 0.0f;
+    row_sum(a, false, red[0]);
+    const float mean = a[0] / (float)H;
+    a[0] = 0.0f;
     for (int i = threadIdx.x; i < H; i += blockDim.x) {
         const float d = to_f(s[base + i]) - mean;
-        a = fmaf(d, d, a);
+        a[0] = fmaf(d, d, a[0]);
     }
-    const float rstd = 1.0f / sqrtf(cta_sum(a, red[1]) / (float)H + eps);
+    row_sum(a, false, red[1]);
+    const float rstd = 1.0f / sqrtf(a[0] / (float)H + eps);
     for (int i = threadIdx.x; i < H; i += blockDim.x)
         y[base + i] = from_f<T>(fmaf((to_f(s[base + i]) - mean) * rstd, to_f(w[i]), b ? to_f(b[i]) : 0.0f));
     if (threadIdx.x == 0) {
@@ -66,68 +184,295 @@ __global__ void __launch_bounds__(256) ln_forward_kernel(const T* x, const T* re
     }
 }
 
-// dx, one CTA per row.
+// ---------------------------------------------------------------------------
+// Backward, the row in registers (laid out as in the forward). A thread's columns are the same in
+// every row, so dweight and dbias add up in its registers over the CTA's rows and leave as one
+// partial sum per CTA: part [gridDim.x][2][H]. The next row's loads are issued before this row's
+// sums (PRE), so that a CTA that fills its SM has a row in flight at all times.
+// ---------------------------------------------------------------------------
+template <typename T, typename W, int VEC, int NV, bool PRE>
+__global__ void __launch_bounds__(512, 1) ln_backward_kernel(const T* dy, const T* __restrict__ s, int rows, int H,
+                                                             bool warp_row, const W* __restrict__ w,
+                                                             const float* __restrict__ mean,
+                                                             const float* __restrict__ rstd, const T* add, T* dx,
+                                                             float* part) {
+    extern __shared__ float cols[];       // warp_row: [2][H], the CTA's sums
+    __shared__ float red[2][64];
+    using V = Vec<T, VEC>;
+    const int tpr = warp_row ? 32 : blockDim.x;
+    const int me = threadIdx.x % tpr, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
+    const int n = H / VEC;
+    Vec<W, VEC> wv[NV];
+    float dw[NV][VEC], db[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        if (me + i * tpr < n) wv[i] = reinterpret_cast<const Vec<W, VEC>*>(w)[me + i * tpr];
+#pragma unroll
+        for (int j = 0; j < VEC; j++) dw[i][j] = db[i][j] = 0.0f;
+    }
+    V gv[NV], sv[NV], av[NV];
+    float m = 0.0f, r = 0.0f;
+    auto load = [&](long long t, V* g_, V* s_, V* a_, float& m_, float& r_) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = me + i * tpr;
+            if (c < n) {
+                g_[i] = reinterpret_cast<const V*>(dy + t * H)[c];
+                s_[i] = reinterpret_cast<const V*>(s + t * H)[c];
+                if (add) a_[i] = reinterpret_cast<const V*>(add + t * H)[c];
+            }
+        }
+        m_ = __ldg(mean + t);
+        r_ = __ldg(rstd + t);
+    };
+    const long long step = (long long)gridDim.x * groups;
+    long long t = (long long)blockIdx.x * groups + group;
+    if (PRE && t < rows) load(t, gv, sv, av, m, r);
+    for (int buf = 0; t < rows; t += step, buf ^= 1) {
+        V gn[NV], sn[NV], an[NV];
+        float mn = 0.0f, rn = 0.0f;
+        if (PRE) {
+            if (t + step < rows) load(t + step, gn, sn, an, mn, rn);
+        } else {
+            load(t, gv, sv, av, m, r);
+        }
+        float sums[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (me + i * tpr < n)
+#pragma unroll
+                for (int j = 0; j < VEC; j++) {
+                    const float d = gv[i].get(j), xh = (sv[i].get(j) - m) * r, g = d * wv[i].get(j);
+                    sums[0] += g;
+                    sums[1] = fmaf(g, xh, sums[1]);
+                    dw[i][j] = fmaf(d, xh, dw[i][j]);
+                    db[i][j] += d;
+                }
+        row_sum(sums, warp_row, red[buf]);
+        const float a = sums[0] / (float)H, c2 = sums[1] / (float)H;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = me + i * tpr;
+            if (c < n) {
+                V o;
+                float f[VEC];
+#pragma unroll
+                for (int j = 0; j < VEC; j++) {
+                    const float xh = (sv[i].get(j) - m) * r, g = gv[i].get(j) * wv[i].get(j);
+                    f[j] = r * (g - a - xh * c2);
+                    if (add) f[j] += av[i].get(j);
+                }
+                o.set(f);
+                reinterpret_cast<V*>(dx + t * H)[c] = o;
+            }
+        }
+        if (PRE) {
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                gv[i] = gn[i];
+                sv[i] = sn[i];
+                av[i] = an[i];
+            }
+            m = mn;
+            r = rn;
+        }
+    }
+    if (!part) return;
+    float* out = part + (size_t)blockIdx.x * 2 * H;
+    if (warp_row) {
+        // the warps' sums one after the other, in a fixed order
+        for (int k = 0; k < groups; k++) {
+            if (group == k)
+#pragma unroll
+                for (int i = 0; i < NV; i++)
+                    if (me + i * tpr < n)
+#pragma unroll
+                        for (int j = 0; j < VEC; j++) {
+                            const int c = (me + i * tpr) * VEC + j;
+                            cols[c] = k ? cols[c] + dw[i][j] : dw[i][j];
+                            cols[H + c] = k ? cols[H + c] + db[i][j] : db[i][j];
+                        }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < 2 * H; c += blockDim.x) out[c] = cols[c];
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (me + i * tpr < n) {
+                const int c = (me + i * tpr) * VEC;
+                Vec<float, VEC> o;
+                o.set(dw[i]);
+                *reinterpret_cast<Vec<float, VEC>*>(out + c) = o;
+                o.set(db[i]);
+                *reinterpret_cast<Vec<float, VEC>*>(out + H + c) = o;
+            }
+    }
+}
+
+// Backward for rows too long for registers: dx with the row read twice ...
 template <typename T, typename W>
-__global__ void __launch_bounds__(256) ln_backward_dx_kernel(const T* dy, const T* __restrict__ s, int H,
-                                                             const W* __restrict__ w, const float* __restrict__ mean,
-                                                             const float* __restrict__ rstd, const T* dx_add, T* dx) {
-    __shared__ float red[2][32];
+__global__ void __launch_bounds__(512) ln_backward_long_kernel(const T* dy, const T* __restrict__ s, int H,
+                                                               const W* __restrict__ w, const float* __restrict__ mean,
+                                                               const float* __restrict__ rstd, const T* add, T* dx) {
+    __shared__ float red[64];
     const long long base = (long long)blockIdx.x * H;
     const float m = mean[blockIdx.x], r = rstd[blockIdx.x];
-    float a = 0.0f, c = 0.0f;
+    float sums[2] = {0.0f, 0.0f};
     for (int i = threadIdx.x; i < H; i += blockDim.x) {
         const float g = to_f(dy[base + i]) * to_f(w[i]);
-        a += g;
-        c = fmaf(g, (to_f(s[base + i]) - m) * r, c);
+        sums[0] += g;
+        sums[1] = fmaf(g, (to_f(s[base + i]) - m) * r, sums[1]);
     }
-    a = cta_sum(a, red[0]) / (float)H;
-    c = cta_sum(c, red[1]) / (float)H;
+    row_sum(sums, false, red);
+    const float a = sums[0] / (float)H, c = sums[1] / (float)H;
     for (int i = threadIdx.x; i < H; i += blockDim.x) {
         const float g = to_f(dy[base + i]) * to_f(w[i]);
         float v = r * (g - a - (to_f(s[base + i]) - m) * r * c);
-        if (dx_add) v += to_f(dx_add[base + i]);
+        if (add) v += to_f(add[base + i]);
         dx[base + i] = from_f<T>(v);
     }
 }
 
-// dweight and dbias, one thread per column.
-template <typename T, typename W>
-__global__ void __launch_bounds__(32) ln_backward_w_kernel(const T* dy, const T* __restrict__ s, int rows, int H,
-                                                           const float* __restrict__ mean, const float* __restrict__ rstd,
-                                                           W* dw, W* db) {
-    const int i = blockIdx.x * 32 + threadIdx.x;
+// ... and the partial sums of dweight and dbias, a slice of the rows per blockIdx.y.
+template <typename T>
+__global__ void __launch_bounds__(256) ln_backward_long_w_kernel(const T* dy, const T* __restrict__ s, int rows, int H,
+                                                                 const float* __restrict__ mean,
+                                                                 const float* __restrict__ rstd, float* part) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
     if (i >= H) return;
     float a = 0.0f, c = 0.0f;
-    for (int t = 0; t < rows; t++) {
-        const float g = to_f(dy[(long long)t * H + i]);
-        a = fmaf(g, (to_f(s[(long long)t * H + i]) - mean[t]) * rstd[t], a);
+    for (long long t = blockIdx.y; t < rows; t += gridDim.y) {
+        const float g = to_f(dy[t * H + i]);
+        a = fmaf(g, (to_f(s[t * H + i]) - mean[t]) * rstd[t], a);
         c += g;
     }
-    if (dw) dw[i] = from_f<W>(a);
-    if (db) db[i] = from_f<W>(c);
+    part[(size_t)blockIdx.y * 2 * H + i] = a;
+    part[((size_t)blockIdx.y * 2 + 1) * H + i] = c;
+}
+
+// dweight and dbias from n partial sums, 32 columns per CTA: thread row y adds partials y, y + 32, ...
+template <typename W>
+__global__ void __launch_bounds__(1024) ln_columns_kernel(const float* __restrict__ part, int n, int H, W* dw, W* db) {
+    __shared__ float red[2][32][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
+    float a = 0.0f, b = 0.0f;
+    if (c < H) {
+#pragma unroll 4
+        for (int i = y; i < n; i += 32) {
+            a += part[(size_t)i * 2 * H + c];
+            b += part[((size_t)i * 2 + 1) * H + c];
+        }
+    }
+    red[0][y][x] = a;
+    red[1][y][x] = b;
+    __syncthreads();
+    if (y < 2 && c < H) {
+        float v = 0.0f;
+        for (int i = 0; i < 32; i++) v += red[y][i][x];
+        W* out = y ? db : dw;
+        if (out) out[c] = from_f<W>(v);
+    }
 }
 
 bool ln_type(int d) { return d == MOE_BF16 || d == MOE_F32; }
 size_t ln_size(int d) { return d == MOE_BF16 ? 2 : 4; }
 
+int ln_sms() {
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+constexpr int LN_PARTS = 1024;            // most partial sums of dweight and dbias
+
+// How a row is spread over threads: VEC elements a piece, NV pieces a thread, a warp or a CTA per
+// row. nv = 0: it does not fit in registers. wide: rows and pointers allow 16-byte pieces.
+struct LnShape {
+    int nv, threads;
+    bool warp_row;
+};
+
+LnShape ln_shape(int H, int vec, bool wide, bool forward) {
+    const int n = H / vec;
+    auto cta = [&](int nv) { return LnShape{nv, (((n + nv - 1) / nv) + 31) / 32 * 32, false}; };
+    if (wide) {
+        if (n <= 32) return {1, 256, true};
+        if (n <= 128 && (forward || vec == 4)) return {4, 256, true};
+        if (n <= 64) return {2, 256, true};
+        if (n <= 1024) return cta(2);
+        if (n <= 2048 && (forward || vec == 4)) return cta(4);
+        return {0, 512, false};
+    }
+    if (n <= 128) return {4, 256, true};
+    if (n <= 2048) return cta(4);
+    if (n <= 8192) return cta(16);
+    return {0, 512, false};
+}
+
 template <typename T, typename W>
 moe_status ln_forward(const void* x, const void* residual, int rows, int H, const void* w, const void* b, float eps,
                       void* sum, void* y, float* mean, float* rstd, cudaStream_t s) {
-    ln_forward_kernel<T, W><<<rows, 256, 0, s>>>((const T*)x, (const T*)residual, H, (const W*)w, (const W*)b, eps,
-                                                 (T*)sum, (T*)y, mean, rstd);
+    constexpr int VEC = 16 / sizeof(T);
+    bool wide = H % VEC == 0;
+    for (const void* q : {x, residual, w, b, (const void*)sum, (const void*)y}) wide = wide && moe_host::aligned(q, 16);
+    const LnShape l = ln_shape(H, wide ? VEC : 1, wide, true);
+    const long long ctas = l.warp_row ? ((long long)rows + 7) / 8 : rows;
+    // as many CTAs as are resident at 2048 threads an SM: a CTA's rows share its weights
+    const long long most = (long long)ln_sms() * (2048 / l.threads);
+    const int grid = (int)(ctas < most ? ctas : most);
+#define MOE_LN_F(vec, nv)                                                                                             \
+    ln_forward_kernel<T, W, vec, nv><<<grid, l.threads, 0, s>>>((const T*)x, (const T*)residual, rows, H, l.warp_row, \
+                                                                (const W*)w, (const W*)b, eps, (T*)sum, (T*)y, mean, rstd)
+    if (l.nv == 0)
+        ln_forward_long_kernel<T, W><<<rows, 512, 0, s>>>((const T*)x, (const T*)residual, H, (const W*)w, (const W*)b,
+                                                          eps, (T*)sum, (T*)y, mean, rstd);
+    else if (wide && l.nv == 1) MOE_LN_F(VEC, 1);
+    else if (wide && l.nv == 2) MOE_LN_F(VEC, 2);
+    else if (wide) MOE_LN_F(VEC, 4);
+    else if (l.nv == 4) MOE_LN_F(1, 4);
+    else MOE_LN_F(1, 16);
+#undef MOE_LN_F
     return moe_host::launch_status();
 }
 
 template <typename T, typename W>
 moe_status ln_backward(const void* dy, const void* sv, int rows, int H, const void* w, const float* mean,
-                       const float* rstd, const void* dx_add, void* dx, void* dw, void* db, cudaStream_t s) {
-    // (before dx, which may be dy)
-    if (dw || db)
-        ln_backward_w_kernel<T, W><<<(H + 31) / 32, 32, 0, s>>>((const T*)dy, (const T*)sv, rows, H, mean, rstd, (W*)dw,
-                                                                (W*)db);
-    if (rows)
-        ln_backward_dx_kernel<T, W><<<rows, 256, 0, s>>>((const T*)dy, (const T*)sv, H, (const W*)w, mean, rstd,
-                                                         (const T*)dx_add, (T*)dx);
+                       const float* rstd, const void* add, void* dx, void* dw, void* db, float* part, cudaStream_t s) {
+    constexpr int VEC = 16 / sizeof(T);
+    bool wide = H % VEC == 0;
+    for (const void* q : {dy, sv, w, add, (const void*)dx}) wide = wide && moe_host::aligned(q, 16);
+    const LnShape l = ln_shape(H, wide ? VEC : 1, wide, false);
+    const bool sums = dw || db;
+    int n_part = 0;
+    if (rows == 0) {
+    } else if (l.nv == 0) {
+        if (sums) {      // (before dx, which may be dy)
+            n_part = rows < 64 ? rows : 64;
+            ln_backward_long_w_kernel<T><<<dim3((H + 255) / 256, n_part), 256, 0, s>>>((const T*)dy, (const T*)sv, rows, H,
+                                                                                       mean, rstd, part);
+        }
+        ln_backward_long_kernel<T, W><<<rows, 512, 0, s>>>((const T*)dy, (const T*)sv, H, (const W*)w, mean, rstd,
+                                                           (const T*)add, (T*)dx);
+    } else {
+        const long long ctas = l.warp_row ? ((long long)rows + 7) / 8 : rows;
+        long long most = (long long)ln_sms() * (512 / l.threads > 1 ? 512 / l.threads : 1);
+        if (most > LN_PARTS) most = LN_PARTS;
+        n_part = (int)(ctas < most ? ctas : most);
+        const size_t smem = l.warp_row ? (size_t)H * 8 : 0;
+#define MOE_LN_B(vec, nv, pre)                                                                                        \
+    ln_backward_kernel<T, W, vec, nv, pre><<<n_part, l.threads, smem, s>>>((const T*)dy, (const T*)sv, rows, H,       \
+                                                                           l.warp_row, (const W*)w, mean, rstd,       \
+                                                                           (const T*)add, (T*)dx, sums ? part : nullptr)
+        if (wide && l.nv == 1) MOE_LN_B(VEC, 1, true);
+        else if (wide && l.nv == 2) MOE_LN_B(VEC, 2, true);
+        else if (wide) {
+            if constexpr (VEC == 4) MOE_LN_B(VEC, 4, false);
+        } else if (l.nv == 4) MOE_LN_B(1, 4, true);
+        else MOE_LN_B(1, 16, false);
+#undef MOE_LN_B
+    }
+    if (sums) ln_columns_kernel<W><<<(H + 31) / 32, 1024, 0, s>>>(part, n_part, H, (W*)dw, (W*)db);
     return moe_host::launch_status();
 }
 
@@ -161,7 +506,7 @@ extern "C" moe_status moe_layer_norm(const void* x, const void* residual, int T,
 
 extern "C" size_t moe_layer_norm_backward_workspace_size(int T, int H) {
     if (T < 0 || H < 1 || H > moe::LN_HMAX) return 0;
-    return 16;
+    return (size_t)moe::LN_PARTS * 2 * H * sizeof(float);
 }
 
 extern "C" moe_status moe_layer_norm_backward(const void* dy, const void* s, int T, int H, moe_dtype dtype,
@@ -181,7 +526,7 @@ extern "C" moe_status moe_layer_norm_backward(const void* dy, const void* s, int
         !moe_host::aligned(workspace, 16))
         return MOE_ERR_ALIGNMENT;
     const cudaStream_t st = moe_host::as_stream(stream);
-#define MOE_LNB(T_, W_) return ln_backward<T_, W_>(dy, s, T, H, weight, mean, rstd, dx_add, dx, dweight, dbias, st)
+#define MOE_LNB(T_, W_) return ln_backward<T_, W_>(dy, s, T, H, weight, mean, rstd, dx_add, dx, dweight, dbias, (float*)workspace, st)
     if (dtype == MOE_BF16) {
         if (w_dtype == MOE_BF16) MOE_LNB(__nv_bfloat16, __nv_bfloat16);
         MOE_LNB(__nv_bfloat16, float);
