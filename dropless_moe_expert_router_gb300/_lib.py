@@ -71,6 +71,8 @@ class MoeLibraryMissing(RuntimeError):
 def load():
     """Load the library (once) and declare every exported entry point."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

@@ -8,6 +8,7 @@ the library. Every step of the computation runs in the library's kernels.
 from __future__ import annotations
 
 import ctypes as C
+from array import array
 from typing import NamedTuple, Optional
 
 import torch
@@ -41,6 +42,15 @@ def _ptr(t: Optional[torch.Tensor]):
 def _stream(stream: Optional[torch.cuda.Stream]):
     s = stream if stream is not None else torch.cuda.current_stream()
     return C.c_void_p(s.cuda_stream)
+
+
+def _raw_stream(stream: Optional[torch.cuda.Stream], t: torch.Tensor) -> int:
+    """The stream's handle: the given one's, or that of the current stream of t's device."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _want(t: torch.Tensor, name: str, dtype=None, ndim=None):
@@ -709,40 +719,40 @@ def moe_layer_few_tokens(x: torch.Tensor, logits: Optional[torch.Tensor], w: Pac
         _want(logits, "logits", torch.float32, 2)
         if logits.shape[0] != T or logits.shape[1] != w.E:
             raise ValueError("logits must be [T, E]")
-        if ids is None:
-            ids = torch.empty((T, K), dtype=id_dtype, device=x.device)
-        if probs is None:
-            probs = torch.empty((T, K), dtype=torch.float32, device=x.device)
     elif ids is None or probs is None:
         raise ValueError("without logits, ids and probs are inputs")
-    _want(ids, "ids", None, 2)
-    _want(probs, "probs", torch.float32, 2)
-    if tuple(ids.shape) != (T, K) or tuple(probs.shape) != (T, K):
-        raise ValueError("ids and probs must be [T, K]")
+    for t, n, dt in ((ids, "ids", None), (probs, "probs", torch.float32)):
+        if t is not None:
+            _want(t, n, dt, 2)
+            if t.shape != (T, K):
+                raise ValueError(f"{n} must be [T, K]")
+    if ids is None:
+        ids = x.new_empty((T, K), dtype=id_dtype)
+    if probs is None:
+        probs = x.new_empty((T, K), dtype=torch.float32)
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        y = torch.empty_like(x)
     else:
-        _want(y, "y", torch.bfloat16, 2)
-        if tuple(y.shape) != (T, H):
-            raise ValueError("y must be [T, H]")
+        _like(y, x, "y")
     if workspace is None:
         workspace = moe_layer_few_tokens_workspace(w, T, K)
     st = _lib.load().moe_layer_few_tokens(
-        x.data_ptr(), T, H, None if logits is None else logits.data_ptr(), K, w.E, w.F, _ptr(w.w13),
-        _ptr(w.w13_scales), _ptr(w.w2), _ptr(w.w2_scales), _dt_code(w.precision), ids.data_ptr(), _id_code(ids.dtype),
-        probs.data_ptr(), y.data_ptr(), MOE_ROUTE_RENORM if renorm else 0, workspace.data_ptr(), workspace.numel(),
-        _stream(stream))
+        x.data_ptr(), T, H, _at(logits), K, w.E, w.F, w.w13.data_ptr(), _at(w.w13_scales), w.w2.data_ptr(),
+        _at(w.w2_scales), _dt_code(w.precision), ids.data_ptr(), _id_code(ids.dtype), probs.data_ptr(), y.data_ptr(),
+        MOE_ROUTE_RENORM if renorm else 0, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, x))
     _check("moe_layer_few_tokens", st)
     return y, ids, probs
 
 
 # ----------------------------------------------------------------- layer norm
+_FLOAT_CODES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+
+
 def _float_code(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.bfloat16:
-        return MOE_BF16
-    if t.dtype == torch.float32:
-        return MOE_F32
-    raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    code = _FLOAT_CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return code
 
 
 def _like(t: Optional[torch.Tensor], ref: torch.Tensor, name: str, shape=None) -> None:
@@ -752,6 +762,13 @@ def _like(t: Optional[torch.Tensor], ref: torch.Tensor, name: str, shape=None) -
     _want(t, name, ref.dtype, None)
     if t.shape != (ref.shape if shape is None else shape):
         raise ValueError(f"{name} must be {list(ref.shape if shape is None else shape)}")
+
+
+def _stat(t: Optional[torch.Tensor], name: str, T: int) -> None:
+    if t is not None:
+        _want(t, name, torch.float32, 1)
+        if t.numel() != T:
+            raise ValueError(f"{name} must be [T]")
 
 
 class LayerNormed(NamedTuple):
@@ -772,25 +789,23 @@ def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     _like(weight, weight, "weight", (H,))
     _like(bias, weight, "bias", (H,))
     _like(residual, x, "residual")
-    if residual is None and sum is not None:
-        raise ValueError("sum goes with residual")
-    for t, n in ((y, "y"), (sum, "sum")):
-        _like(t, x, n)
-    for t, n in ((mean, "mean"), (rstd, "rstd")):
-        if t is not None:
-            _want(t, n, torch.float32, 1)
-            if t.numel() != T:
-                raise ValueError(f"{n} must be [T]")
+    _like(y, x, "y")
+    _like(sum, x, "sum")
+    _stat(mean, "mean", T)
+    _stat(rstd, "rstd", T)
     if y is None:
         y = torch.empty_like(x)
-    if sum is None and residual is not None:
+    if residual is None:
+        if sum is not None:
+            raise ValueError("sum goes with residual")
+    elif sum is None:
         sum = torch.empty_like(x)
     if mean is None:
-        mean = torch.empty((T,), dtype=torch.float32, device=x.device)
+        mean = x.new_empty(T, dtype=torch.float32)
     if rstd is None:
-        rstd = torch.empty((T,), dtype=torch.float32, device=x.device)
-    st = _lib.load().moe_layer_norm(_ptr(x), _ptr(residual), T, H, code, _ptr(weight), _ptr(bias), wcode, eps, _ptr(sum),
-                                    _ptr(y), _ptr(mean), _ptr(rstd), _stream(stream))
+        rstd = x.new_empty(T, dtype=torch.float32)
+    st = _lib.load().moe_layer_norm(x.data_ptr(), _at(residual), T, H, code, weight.data_ptr(), _at(bias), wcode, eps,
+                                    _at(sum), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, x))
     _check("moe_layer_norm", st)
     return LayerNormed(y, x if residual is None else sum, mean, rstd)
 
@@ -810,16 +825,15 @@ def moe_layer_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Ten
     T, H = s.shape
     code, wcode = _float_code(s, "s"), _float_code(weight, "weight")
     _like(weight, weight, "weight", (H,))
-    if dy is None:
-        raise ValueError("dy must be given")
-    for t, n in ((dy, "dy"), (dx_add, "dx_add"), (dx, "dx")):
-        _like(t, s, n)
-    for t, n in ((dweight, "dweight"), (dbias, "dbias")):
-        _like(t, weight, n, (H,))
-    for t, n in ((mean, "mean"), (rstd, "rstd")):
-        _want(t, n, torch.float32, 1)
-        if t.numel() != T:
-            raise ValueError(f"{n} must be [T]")
+    if dy is None or mean is None or rstd is None:
+        raise ValueError("dy, mean and rstd must be given")
+    _like(dy, s, "dy")
+    _like(dx_add, s, "dx_add")
+    _like(dx, s, "dx")
+    _like(dweight, weight, "dweight", (H,))
+    _like(dbias, weight, "dbias", (H,))
+    _stat(mean, "mean", T)
+    _stat(rstd, "rstd", T)
     if dx is None:
         dx = torch.empty_like(s)
     if dweight is None:
@@ -828,40 +842,55 @@ def moe_layer_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Ten
         dbias = torch.empty_like(weight)
     if workspace is None:
         workspace = torch.empty(moe_layer_norm_backward_workspace_size(T, H), dtype=torch.uint8, device=s.device)
-    st = _lib.load().moe_layer_norm_backward(_ptr(dy), _ptr(s), T, H, code, _ptr(weight), wcode, _ptr(mean), _ptr(rstd),
-                                             _ptr(dx_add), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(workspace),
-                                             workspace.numel(), _stream(stream))
+    st = _lib.load().moe_layer_norm_backward(dy.data_ptr(), s.data_ptr(), T, H, code, weight.data_ptr(), wcode,
+                                             mean.data_ptr(), rstd.data_ptr(), _at(dx_add), dx.data_ptr(),
+                                             dweight.data_ptr(), dbias.data_ptr(), workspace.data_ptr(),
+                                             workspace.numel(), _raw_stream(stream, s))
     _check("moe_layer_norm_backward", st)
     return dx, dweight, dbias
 
 
 # ------------------------------------------------------- gradient norm, clipping
 def _grad_norm_clip(grads, outs, max_norm, eps, norm, workspace, stream):
+    # (the lists can be long: each check is one pass over them)
     n = len(grads)
-    for t in grads:
-        _want(t, "a gradient", None, None)
-    codes = [_float_code(t, "a gradient") for t in grads]
-    if outs is not None:
+    if not all([t.is_cuda for t in grads]):
+        raise ValueError("gradients must be CUDA tensors")
+    if not all([t.is_contiguous() for t in grads]):
+        raise ValueError("gradients must be contiguous")
+    dtypes = [t.dtype for t in grads]
+    codes = [_FLOAT_CODES.get(d) for d in dtypes]
+    if None in codes:
+        raise ValueError("gradients must be bfloat16 or float32")
+    counts = [t.numel() for t in grads]
+    ptrs = array("q", [t.data_ptr() for t in grads])
+    out_at = None
+    if outs is grads:
+        out_at = ptrs.buffer_info()[0]
+    elif outs is not None:
         if len(outs) != n:
             raise ValueError("out must have one tensor per gradient")
-        for t, o in zip(grads, outs):
-            if o is not t:
-                _like(o, t, "an output")
+        if [t.numel() for t in outs] != counts or [t.dtype for t in outs] != dtypes:
+            raise ValueError("outputs must have the gradients' sizes and types")
+        if not all([t.is_cuda for t in outs]) or not all([t.is_contiguous() for t in outs]):
+            raise ValueError("outputs must be contiguous CUDA tensors")
+        optrs = array("q", [t.data_ptr() for t in outs])
+        out_at = optrs.buffer_info()[0]
     if norm is None:
         if n == 0:
             raise ValueError("no gradients: pass norm, the tensor to write")
-        norm = torch.empty((1,), dtype=torch.float32, device=grads[0].device)
+        norm = grads[0].new_empty(1, dtype=torch.float32)
     else:
         _want(norm, "norm", torch.float32, None)
         if norm.numel() != 1:
             raise ValueError("norm must hold one value")
     L = _lib.load()
     if workspace is None:
-        workspace = torch.empty(int(L.moe_grad_norm_workspace_size(n)), dtype=torch.uint8, device=norm.device)
-    ptrs = (C.c_void_p * n)(*[t.data_ptr() for t in grads])
-    outp = None if outs is None else (C.c_void_p * n)(*[t.data_ptr() for t in outs])
-    st = L.moe_grad_norm_clip(ptrs, (C.c_longlong * n)(*[t.numel() for t in grads]), (C.c_int * n)(*codes), outp, n,
-                              max_norm, eps, _ptr(norm), _ptr(workspace), workspace.numel(), _stream(stream))
+        workspace = norm.new_empty(L.moe_grad_norm_workspace_size(n), dtype=torch.uint8)
+    counts, codes = array("q", counts), array("i", codes)
+    st = L.moe_grad_norm_clip(ptrs.buffer_info()[0], counts.buffer_info()[0], codes.buffer_info()[0], out_at, n,
+                              max_norm, eps, norm.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                              _raw_stream(stream, norm))
     _check("moe_grad_norm_clip", st)
     return norm
 

@@ -201,6 +201,7 @@ template <int V>
 __global__ void __launch_bounds__(PREP_THREADS) few_prep_kernel(PrepArgs p) {
     __shared__ PrepSmem sm;
     const int t = blockIdx.x;
+    pdl_trigger();            // the second kernel sets up meanwhile (and waits for this one's end)
     if (t == 0)
         for (int i = threadIdx.x; i < p.n_count; i += PREP_THREADS) p.count[i] = 0u;
     if (p.logits) prep_route<V>(p, t, sm);
@@ -363,18 +364,41 @@ __device__ __forceinline__ bool few_h_ready(const unsigned* count) {
     return true;
 }
 
-// Bounded wait for it.
+// Bounded wait for it by a warp (one lane polls: the counter's line is every CTA's).
 __device__ __forceinline__ bool few_wait_h(const unsigned* count, volatile uint32_t* abort_flag) {
-    const uint64_t t0 = ptx::globaltimer_ns();
-    while (!few_h_ready(count)) {
-        if (*abort_flag) return false;
-        if (ptx::globaltimer_ns() - t0 > ptx::WAIT_LIMIT_NS) {
-            *abort_flag = 1u;
-            raise_device_error(MOE_DEVERR_TIMEOUT);
-            return false;
+    uint32_t ok = 1u;
+    if (lane_id() == 0) {
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while (!few_h_ready(count)) {
+            if (*abort_flag) {
+                ok = 0u;
+                break;
+            }
+            if (ptx::globaltimer_ns() - t0 > ptx::WAIT_LIMIT_NS) {
+                *abort_flag = 1u;
+                raise_device_error(MOE_DEVERR_TIMEOUT);
+                ok = 0u;
+                break;
+            }
         }
     }
-    return true;
+    return __shfl_sync(FULL, ok, 0) != 0u;
+}
+
+// A weight tile, read once by the whole GPU: first to leave L2, so that what the next call needs again
+// (the kernels' code, x, the workspace) stays.
+__device__ __forceinline__ uint64_t evict_first_policy() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void tma_load_weights(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1,
+                                                 uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+        "{%3, %4}], [%2], %5;" ::"r"(ptx::smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(ptx::smem_addr(bar)), "r"(c0), "r"(c1), "l"(policy)
+        : "memory");
 }
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -594,6 +618,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
         // ------------------------------------------------------------ producer
         FewWalk<FP8> wk(p, pl);
         FewRun r;
+        const uint64_t policy = evict_first_policy();
         int stage = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true, have = wk.next(r);
@@ -603,8 +628,8 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                 uint8_t* sa = ring + (size_t)st * stage_bytes;
                 ptx::mbar_arrive_expect_tx(&sm.full[st], FEW_A_BYTES + q.bn * 128);
                 const CUtensorMap* tm = q.phase ? &tmW2 : &tmW13;
-                ptx::tma_load_2d(sa, tm, &sm.full[st], (q.kb0 + k) * BK, q.row0);
-                ptx::tma_load_2d(sa + FEW_A_BYTES / 2, tm, &sm.full[st], (q.kb0 + k) * BK, q.row1);
+                tma_load_weights(sa, tm, &sm.full[st], (q.kb0 + k) * BK, q.row0, policy);
+                tma_load_weights(sa + FEW_A_BYTES / 2, tm, &sm.full[st], (q.kb0 + k) * BK, q.row1, policy);
             }
         };
         auto load_b = [&](int st, const FewRun& q, int k) {
@@ -643,7 +668,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                 step();
                 n++;
             }
-            ok = __all_sync(FULL, few_wait_h(p.count, s_abort)) && ok;
+            ok = few_wait_h(p.count, s_abort) && ok;
             for (int i = 0; i < n; i++) {    // (also when giving up: the stages' loads have to complete)
                 load_b(sb, rb, kbb);
                 if (++sb == stages) sb = 0;
@@ -751,7 +776,8 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             while (ld.have || loaded > 0) {
                 bool progress = false;
                 // (down scales: once h's are written; the groups landed meanwhile are not held up)
-                if (ld.have && ld.r.phase == 1 && !h_seen) h_seen = __all_sync(FULL, few_h_ready(p.count));
+                if (ld.have && ld.r.phase == 1 && !h_seen)
+                    h_seen = __shfl_sync(FULL, (uint32_t)(lane == 0 && few_h_ready(p.count)), 0) != 0u;
                 if (ld.have && (ld.r.phase == 0 || h_seen) && loaded < FEW_SF_SLOTS &&
                     __all_sync(FULL, ptx::mbar_test_wait(&sm.sf_empty[ld_slot], ld_phase ^ 1u))) {
                     if (lane == 0) {
@@ -906,7 +932,10 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                 for (int t = 0; t < p.T; t++) y[(size_t)t * p.H] = __float2bfloat16_rn(acc[t * 128 + row]);
                 return;
             }
-            float* mine = p.part + ((size_t)2 * blockIdx.x + (tile != first_tile)) * p.T * 128 + row;
+            // a CTA's partial sums: slot 0 for the first tile that it works on, slot 1 for the last; only the
+            // first of a tile's CTAs can have it as its last
+            const size_t slot = (size_t)p.T * 128;
+            float* mine = p.part + ((size_t)2 * blockIdx.x + (tile != first_tile)) * slot + row;
             for (int t = 0; t < p.T; t++) __stcg(mine + t * 128, acc[t * 128 + row]);
             __threadfence();
             epi_sync();
@@ -914,18 +943,36 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             epi_sync();
             if (sm.ticket != c1 - c0) return;
             __threadfence();
-            for (int t0 = 0; t0 < p.T; t0 += 4) {
-                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                for (int c = c0; c <= c1; c++) {
-                    const int which = pl.begin_of(c) / per_tile != tile;
-                    const float* src = p.part + ((size_t)2 * c + which) * p.T * 128 + row;
+            // a warp per token, four rows a lane; eight tokens' loads in flight per warp
+            const float4* src = reinterpret_cast<const float4*>(
+                p.part + ((size_t)2 * c0 + (pl.begin_of(c0) / per_tile != tile)) * slot) + lane;
+            const float4* rest = reinterpret_cast<const float4*>(p.part + (size_t)2 * (c0 + 1) * slot) + lane;
+            const int n = c1 - c0;
+            for (int t0 = q; t0 < p.T; t0 += 32) {
+                float4 v[8];
 #pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        if (t0 + i < p.T) v[i] += __ldcg(src + (t0 + i) * 128);
+                for (int j = 0; j < 8; j++) {
+                    v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (t0 + 4 * j < p.T) v[j] = __ldcg(src + (t0 + 4 * j) * 32);
                 }
+#pragma unroll 4
+                for (int i = 0; i < n; i++)
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    if (t0 + i < p.T) y[(size_t)(t0 + i) * p.H] = __float2bfloat16_rn(v[i]);
+                    for (int j = 0; j < 8; j++)
+                        if (t0 + 4 * j < p.T) {
+                            const float4 u = __ldcg(rest + (slot / 2) * i + (t0 + 4 * j) * 32);
+                            v[j].x += u.x;
+                            v[j].y += u.y;
+                            v[j].z += u.z;
+                            v[j].w += u.w;
+                        }
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    if (t0 + 4 * j < p.T) {
+                        __nv_bfloat162 o[2] = {__floats2bfloat162_rn(v[j].x, v[j].y), __floats2bfloat162_rn(v[j].z, v[j].w)};
+                        *reinterpret_cast<uint2*>(p.y + (size_t)(t0 + 4 * j) * p.H + tile * 128 + 4 * lane) =
+                            *reinterpret_cast<uint2*>(o);
+                    }
             }
         };
         while (ok && have) {
@@ -1061,11 +1108,13 @@ moe_status few_launch(FewArgs a, const PrepArgs& p, const void* x, const uint8_t
     cfg.blockDim = dim3(few_threads<FP8>());
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;      // the CTAs wait for one another: all resident, or none
     attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, kern, tw13, tw2, tx, th, ts13, ts2, tsx, tsh, a) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
