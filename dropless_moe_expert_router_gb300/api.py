@@ -727,9 +727,9 @@ def moe_layer_few_tokens(x: torch.Tensor, logits: Optional[torch.Tensor], w: Pac
             if t.shape != (T, K):
                 raise ValueError(f"{n} must be [T, K]")
     if ids is None:
-        ids = x.new_empty((T, K), dtype=id_dtype)
+        ids = torch.empty((T, K), dtype=id_dtype, device=x.device)
     if probs is None:
-        probs = x.new_empty((T, K), dtype=torch.float32)
+        probs = torch.empty((T, K), dtype=torch.float32, device=x.device)
     if y is None:
         y = torch.empty_like(x)
     else:
@@ -801,9 +801,9 @@ def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     elif sum is None:
         sum = torch.empty_like(x)
     if mean is None:
-        mean = x.new_empty(T, dtype=torch.float32)
+        mean = torch.empty(T, dtype=torch.float32, device=x.device)
     if rstd is None:
-        rstd = x.new_empty(T, dtype=torch.float32)
+        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
     st = _lib.load().moe_layer_norm(x.data_ptr(), _at(residual), T, H, code, weight.data_ptr(), _at(bias), wcode, eps,
                                     _at(sum), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, x))
     _check("moe_layer_norm", st)
@@ -879,14 +879,14 @@ def _grad_norm_clip(grads, outs, max_norm, eps, norm, workspace, stream):
     if norm is None:
         if n == 0:
             raise ValueError("no gradients: pass norm, the tensor to write")
-        norm = grads[0].new_empty(1, dtype=torch.float32)
+        norm = torch.empty(1, dtype=torch.float32, device=grads[0].device)
     else:
         _want(norm, "norm", torch.float32, None)
         if norm.numel() != 1:
             raise ValueError("norm must hold one value")
     L = _lib.load()
     if workspace is None:
-        workspace = norm.new_empty(L.moe_grad_norm_workspace_size(n), dtype=torch.uint8)
+        workspace = torch.empty(L.moe_grad_norm_workspace_size(n), dtype=torch.uint8, device=norm.device)
     counts, codes = array("q", counts), array("i", codes)
     st = L.moe_grad_norm_clip(ptrs.buffer_info()[0], counts.buffer_info()[0], codes.buffer_info()[0], out_at, n,
                               max_norm, eps, norm.data_ptr(), workspace.data_ptr(), workspace.numel(),

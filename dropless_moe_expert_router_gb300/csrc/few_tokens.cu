@@ -19,22 +19,26 @@ constexpr int FEW_ROUTES = 4096;     // T * K
 constexpr int FEW_EMAX = 8192;       // experts
 
 // ---------------------------------------------------------------------------
-// First kernel, one CTA per token: the router's selection (unless the caller gave ids and
-// probs), and for MXFP8 the token's row-wise 1x32 quantisation.
+// First kernel. CTA t < T: token t's selection (unless the caller gave ids and probs). MXFP8: the CTAs
+// after those quantise x row-wise 1x32, PREP_QUANT elements of a row each.
 //
-// Selection: a thread holds V logits as order-preserving keys (expert i * 256 + thread). Up to
-// 256 experts, each logit's rank is counted directly against the row. Above, the K-th largest
-// key is found by a search over its 32 bits, two bits a step (three counts of keys at or above a
-// bound per step), then the keys above it and the lowest-index ones equal to it are ranked among
-// themselves.
+// Selection: a thread holds V logits as order-preserving keys (expert i * 256 + thread). Up to 256
+// experts, each logit's rank is counted directly against the row. Above, the K-th largest of the
+// threads' own largest keys bounds the row's K-th largest from below; the keys at or above it,
+// normally a few more than K, are listed and ranked among themselves. A row with more than PREP_CAND
+// of them (many equal logits) takes an exact search instead: the K-th largest key by its 32 bits, two a
+// step, then the keys above it and the lowest-index ones equal to it.
 // ---------------------------------------------------------------------------
 constexpr int PREP_THREADS = 256;
 constexpr int PREP_WARPS = PREP_THREADS / 32;
+constexpr int PREP_CAND = 256;
+constexpr int PREP_QUANT = PREP_THREADS * 8;
 
 struct PrepSmem {
     unsigned key[PREP_THREADS];
-    unsigned list_key[FEW_KMAX];
-    int list_idx[FEW_KMAX];
+    unsigned list_key[PREP_CAND];
+    int list_idx[PREP_CAND];
+    unsigned bound;
     unsigned cnt[2][3];
     float red[2][PREP_WARPS];
     int n;
@@ -68,7 +72,7 @@ __device__ __forceinline__ float prep_reduce(float v, float* red) {
 struct PrepArgs {
     const __nv_bfloat16* x;
     const float* logits;      // null: ids and probs are the caller's
-    int H, E, K;
+    int T, H, E, K;
     void* ids;
     bool i16, renorm;
     float* probs;
@@ -78,9 +82,80 @@ struct PrepArgs {
     int n_count;
 };
 
+// The K largest keys of the row (lower index first among equals) into the list, whatever the ties.
+template <int V>
+__device__ __noinline__ void prep_exact(const PrepArgs& p, const unsigned (&key)[V], PrepSmem& sm) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    __syncthreads();                  // (every thread has read the list's length)
+    if (tid < 6) sm.cnt[tid / 3][tid % 3] = 0u;
+    if (tid == 0) sm.n = 0;
+    __syncthreads();
+    // the largest bound with at least K keys at or above it: the K-th largest key
+    unsigned kth = 0u;
+    for (int sh = 30, step = 0; sh >= 0; sh -= 2, step ^= 1) {
+        unsigned c[3] = {0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < V; i++)
+#pragma unroll
+            for (int j = 0; j < 3; j++) c[j] += key[i] >= kth + ((unsigned)(j + 1) << sh);
+#pragma unroll
+        for (int j = 0; j < 3; j++) {
+            c[j] = __reduce_add_sync(FULL, c[j]);
+            if (lane == 0 && c[j]) atomicAdd(&sm.cnt[step][j], c[j]);
+        }
+        __syncthreads();
+        unsigned d = 0u;
+#pragma unroll
+        for (int j = 0; j < 3; j++) d += sm.cnt[step][j] >= (unsigned)p.K;
+        kth += d << sh;
+        if (tid < 3) sm.cnt[step ^ 1][tid] = 0u;
+        __syncthreads();
+    }
+    // how many of the keys equal to it belong to the K largest
+    {
+        unsigned c = 0u;
+#pragma unroll
+        for (int i = 0; i < V; i++) c += key[i] > kth;
+        c = __reduce_add_sync(FULL, c);
+        if (lane == 0 && c) atomicAdd(&sm.cnt[0][0], c);   // (cleared by the search's last step)
+        if (tid == 0) sm.cnt[1][1] = 0u;
+        __syncthreads();
+    }
+    const unsigned ties = (unsigned)p.K - sm.cnt[0][0];
+    // those with the lowest expert indices: the index bound by bisection
+    int lo = 0, hi = p.E - 1;         // smallest b with at least `ties` equal keys at indices <= b
+    int step = 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (tid == 0) sm.cnt[step ^ 1][1] = 0u;
+        unsigned c = 0u;
+#pragma unroll
+        for (int i = 0; i < V; i++) c += key[i] == kth && i * PREP_THREADS + tid <= mid;
+        c = __reduce_add_sync(FULL, c);
+        if (lane == 0 && c) atomicAdd(&sm.cnt[step][1], c);
+        __syncthreads();
+        if (sm.cnt[step][1] >= ties) hi = mid;
+        else lo = mid + 1;
+        step ^= 1;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+        const int e = i * PREP_THREADS + tid;
+        if (e < p.E && (key[i] > kth || (key[i] == kth && e <= lo))) {
+            const int pos = atomicAdd(&sm.n, 1);
+            if (pos < PREP_CAND) {        // (NaN logits aside, exactly K keys come here)
+                sm.list_key[pos] = key[i];
+                sm.list_idx[pos] = e;
+            }
+        }
+    }
+    __syncthreads();
+}
+
 template <int V>
 __device__ void prep_route(const PrepArgs& p, int t, PrepSmem& sm) {
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x;
     const float* row = p.logits + (long long)t * p.E;
     unsigned key[V];
     float m = -INFINITY;
@@ -94,8 +169,10 @@ __device__ void prep_route(const PrepArgs& p, int t, PrepSmem& sm) {
             m = fmaxf(m, f);
         }
     }
-    if (tid == 0) sm.n = 0;
-    if (tid < 6) sm.cnt[tid / 3][tid % 3] = 0u;
+    if (tid == 0) {
+        sm.n = 0;
+        sm.bound = 0u;
+    }
     m = prep_reduce<true>(m, sm.red[0]);
     float den = 0.0f;
     if (!p.renorm) {
@@ -104,96 +181,63 @@ __device__ void prep_route(const PrepArgs& p, int t, PrepSmem& sm) {
             if (key[i]) den += expf(key_value(key[i]) - m);
         den = prep_reduce<false>(den, sm.red[1]);
     }
+    // the row's largest key of each thread (V = 1: its only one), ranked against the others'
+    unsigned top = key[0];
+#pragma unroll
+    for (int i = 1; i < V; i++) top = max(top, key[i]);
+    sm.key[tid] = top;
+    __syncthreads();
+    int r = 0;
+    const int others = min(p.E, PREP_THREADS);
+#pragma unroll 8
+    for (int j = 0; j < others; j++) r += (sm.key[j] > top) || (sm.key[j] == top && j < tid);
+    int n = p.K;              // length of the list
     if (V == 1) {
-        sm.key[tid] = key[0];
-        __syncthreads();
-        int r = 0;
-        for (int j = 0; j < p.E; j++) r += (sm.key[j] > key[0]) || (sm.key[j] == key[0] && j < tid);
         if (tid < p.E && r < p.K) {
-            sm.list_key[r] = key[0];
+            sm.list_key[r] = top;
             sm.list_idx[r] = tid;
         }
         __syncthreads();
     } else {
-        // the largest bound with at least K keys at or above it: the K-th largest key
-        unsigned kth = 0u, above = 0u;    // above: keys > kth, once the search is done
-        for (int sh = 30, step = 0; sh >= 0; sh -= 2, step ^= 1) {
-            unsigned c[3] = {0u, 0u, 0u};
+        if (r == p.K - 1) sm.bound = top;
+        __syncthreads();
+        const unsigned bound = sm.bound;
 #pragma unroll
-            for (int i = 0; i < V; i++)
-#pragma unroll
-                for (int j = 0; j < 3; j++) c[j] += key[i] >= kth + ((unsigned)(j + 1) << sh);
-#pragma unroll
-            for (int j = 0; j < 3; j++) {
-                c[j] = __reduce_add_sync(FULL, c[j]);
-                if (lane == 0 && c[j]) atomicAdd(&sm.cnt[step][j], c[j]);
-            }
-            __syncthreads();
-            unsigned d = 0u;
-#pragma unroll
-            for (int j = 0; j < 3; j++) d += sm.cnt[step][j] >= (unsigned)p.K;
-            kth += d << sh;
-            if (tid < 3) sm.cnt[step ^ 1][tid] = 0u;
-            __syncthreads();
-        }
-        // how many of the keys equal to it belong to the K largest
-        {
-            unsigned c = 0u;
-#pragma unroll
-            for (int i = 0; i < V; i++) c += key[i] > kth;
-            c = __reduce_add_sync(FULL, c);
-            if (lane == 0 && c) atomicAdd(&sm.cnt[0][0], c);   // (cleared by the search's last step)
-            if (tid == 0) sm.cnt[1][1] = 0u;
-            __syncthreads();
-            above = sm.cnt[0][0];
-        }
-        const unsigned ties = (unsigned)p.K - above;
-        // the keys equal to kth with the lowest expert indices: the index bound by bisection
-        int lo = 0, hi = p.E - 1;         // smallest b with at least `ties` equal keys at indices <= b
-        int step = 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (tid == 0) sm.cnt[step ^ 1][1] = 0u;
-            unsigned c = 0u;
-#pragma unroll
-            for (int i = 0; i < V; i++) c += key[i] == kth && i * PREP_THREADS + tid <= mid;
-            c = __reduce_add_sync(FULL, c);
-            if (lane == 0 && c) atomicAdd(&sm.cnt[step][1], c);
-            __syncthreads();
-            if (sm.cnt[step][1] >= ties) hi = mid;
-            else lo = mid + 1;
-            step ^= 1;
-            __syncthreads();
-        }
-#pragma unroll
-        for (int i = 0; i < V; i++) {
-            const int e = i * PREP_THREADS + tid;
-            if (e < p.E && (key[i] > kth || (key[i] == kth && e <= lo))) {
+        for (int i = 0; i < V; i++)
+            if (key[i] >= bound && i * PREP_THREADS + tid < p.E) {
                 const int pos = atomicAdd(&sm.n, 1);
-                if (pos < FEW_KMAX) {     // (NaN logits aside, exactly K keys come here)
+                if (pos < PREP_CAND) {
                     sm.list_key[pos] = key[i];
-                    sm.list_idx[pos] = e;
+                    sm.list_idx[pos] = i * PREP_THREADS + tid;
                 }
             }
-        }
         __syncthreads();
-    }
-    if (p.renorm) {
-        for (int j = tid; j < p.K; j += PREP_THREADS) den += expf(key_value(sm.list_key[j]) - m);
-        den = prep_reduce<false>(den, sm.red[1]);
-    }
-    for (int j = tid; j < p.K; j += PREP_THREADS) {
-        const unsigned k = sm.list_key[j];
-        const int e = sm.list_idx[j];
-        int r = j;
-        if (V > 1) {
-            r = 0;
-            for (int i = 0; i < p.K; i++) r += sm.list_key[i] > k || (sm.list_key[i] == k && sm.list_idx[i] < e);
+        n = sm.n;
+        if (n > PREP_CAND) {
+            prep_exact<V>(p, key, sm);
+            n = p.K;
         }
-        const long long o = (long long)t * p.K + r;
+    }
+    // ranks within the list; the first K are the selection
+    int rank = tid, e = 0;
+    unsigned k = 0u;
+    if (tid < n) {
+        k = sm.list_key[tid];
+        e = sm.list_idx[tid];
+        if (V > 1) {
+            rank = 0;
+#pragma unroll 4
+            for (int i = 0; i < n; i++) rank += sm.list_key[i] > k || (sm.list_key[i] == k && sm.list_idx[i] < e);
+        }
+    }
+    const bool chosen = tid < n && rank < p.K;
+    const float num = chosen ? expf(key_value(k) - m) : 0.0f;
+    if (p.renorm) den = prep_reduce<false>(num, sm.red[1]);
+    if (chosen) {
+        const long long o = (long long)t * p.K + rank;
         if (p.i16) static_cast<int16_t*>(p.ids)[o] = (int16_t)e;
         else static_cast<int32_t*>(p.ids)[o] = e;
-        p.probs[o] = expf(key_value(k) - m) / den;
+        p.probs[o] = num / den;
     }
 }
 
@@ -201,25 +245,22 @@ template <int V>
 __global__ void __launch_bounds__(PREP_THREADS) few_prep_kernel(PrepArgs p) {
     __shared__ PrepSmem sm;
     const int t = blockIdx.x;
-    pdl_trigger();            // the second kernel sets up meanwhile (and waits for this one's end)
-    if (t == 0)
-        for (int i = threadIdx.x; i < p.n_count; i += PREP_THREADS) p.count[i] = 0u;
-    if (p.logits) prep_route<V>(p, t, sm);
-    if (p.xq) {
-        const int lane = (int)lane_id();
-        const uint4* src = reinterpret_cast<const uint4*>(p.x + (long long)t * p.H);
-        const int H8 = p.H >> 3;
-        for (int j0 = threadIdx.x & ~31; j0 < H8; j0 += PREP_THREADS) {     // warp-uniform
-            const int j = j0 + lane;
-            float f[8];
-            bf16x8_to_f32(j < H8 ? __ldg(src + j) : make_uint4(0, 0, 0, 0), f);
-            int sb;
-            const uint2 code = quant8_in_quad(f, &sb);
-            if (j < H8) {
-                reinterpret_cast<uint2*>(p.xq)[(long long)t * H8 + j] = code;
-                if ((lane & 3) == 0) p.xs[(long long)t * (p.H >> 5) + (j >> 2)] = (uint8_t)sb;
-            }
-        }
+    if (t < p.T) {
+        if (t == 0)
+            for (int i = threadIdx.x; i < p.n_count; i += PREP_THREADS) p.count[i] = 0u;
+        if (p.logits) prep_route<V>(p, t, sm);
+        return;
+    }
+    const int per = (p.H + PREP_QUANT - 1) / PREP_QUANT;
+    const int row = (t - p.T) / per, j = ((t - p.T) % per) * PREP_THREADS + threadIdx.x;
+    const int H8 = p.H >> 3;
+    float f[8];
+    bf16x8_to_f32(j < H8 ? __ldg(reinterpret_cast<const uint4*>(p.x + (long long)row * p.H) + j) : make_uint4(0, 0, 0, 0), f);
+    int sb;
+    const uint2 code = quant8_in_quad(f, &sb);
+    if (j < H8) {
+        reinterpret_cast<uint2*>(p.xq)[(long long)row * H8 + j] = code;
+        if ((threadIdx.x & 3) == 0) p.xs[(long long)row * (p.H >> 5) + (j >> 2)] = (uint8_t)sb;
     }
 }
 
@@ -360,29 +401,22 @@ __device__ __forceinline__ bool few_h_ready(const unsigned* count) {
     unsigned v;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
     if (v < gridDim.x) return false;
-    asm volatile("fence.proxy.async;" ::: "memory");
+    asm volatile("fence.proxy.async.global;" ::: "memory");
     return true;
 }
 
-// Bounded wait for it by a warp (one lane polls: the counter's line is every CTA's).
+// Bounded wait for it, by one lane (the counter's line is every CTA's).
 __device__ __forceinline__ bool few_wait_h(const unsigned* count, volatile uint32_t* abort_flag) {
-    uint32_t ok = 1u;
-    if (lane_id() == 0) {
-        const uint64_t t0 = ptx::globaltimer_ns();
-        while (!few_h_ready(count)) {
-            if (*abort_flag) {
-                ok = 0u;
-                break;
-            }
-            if (ptx::globaltimer_ns() - t0 > ptx::WAIT_LIMIT_NS) {
-                *abort_flag = 1u;
-                raise_device_error(MOE_DEVERR_TIMEOUT);
-                ok = 0u;
-                break;
-            }
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!few_h_ready(count)) {
+        if (*abort_flag) return false;
+        if (ptx::globaltimer_ns() - t0 > ptx::WAIT_LIMIT_NS) {
+            *abort_flag = 1u;
+            raise_device_error(MOE_DEVERR_TIMEOUT);
+            return false;
         }
     }
-    return __shfl_sync(FULL, ok, 0) != 0u;
+    return true;
 }
 
 // A weight tile, read once by the whole GPU: first to leave L2, so that what the next call needs again
@@ -413,11 +447,6 @@ __device__ __forceinline__ bool epi_all(bool ok) {
         : "r"((uint32_t)ok)
         : "memory");
     return r != 0;
-}
-
-// A warp's bounded wait: the same answer in all of its lanes.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
-    return __all_sync(FULL, ptx::wait_parity(bar, parity, abort_flag));
 }
 
 // One TMEM column (dynamic) of this warp's lane quarter.
@@ -460,11 +489,12 @@ __device__ void few_plan(const FewArgs& p, FewSmem& sm, uint8_t* scratch, unsign
     for (int e = tid; e < p.E; e += THREADS) mask[e] = 0ull;
     if (tid == 0) sm.routes = 0;
     __syncthreads();
-    pdl_wait();               // the routes are the first kernel's
     const int R = p.T * p.K;
     int valid = 0;
+    const int e_own = tid < R ? load_id(p.ids, tid, p.i16) : -1;      // (in flight together)
+    const float w_own = tid < R ? p.probs[tid] : 0.0f;
     for (int r = tid; r < R; r += THREADS) {
-        const int e = load_id(p.ids, r, p.i16);
+        const int e = r == tid ? e_own : load_id(p.ids, r, p.i16);
         if (e >= 0 && e < p.E) {
             atomicOr(&mask[e], 1ull << (r / p.K));
             valid++;
@@ -522,10 +552,10 @@ __device__ void few_plan(const FewArgs& p, FewSmem& sm, uint8_t* scratch, unsign
     // weighted with the sum (in ascending k)
     const bool repeated = sm.slots != sm.routes;
     for (int r = tid; r < R; r += THREADS) {
-        const int e = load_id(p.ids, r, p.i16);
+        const int e = r == tid ? e_own : load_id(p.ids, r, p.i16);
         if (e < 0 || e >= p.E) continue;
         const int t = r / p.K;
-        float w = p.probs[r];
+        float w = r == tid ? w_own : p.probs[r];
         if (repeated) {
             bool first = true;
             for (int j = t * p.K; j < r; j++) first = first && load_id(p.ids, j, p.i16) != e;
@@ -615,25 +645,22 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
     pl.parts = max(1, min((int)gridDim.x, pl.W / FEW_MIN_KB));
 
     if (warp == 0) {
-        // ------------------------------------------------------------ producer
-        FewWalk<FP8> wk(p, pl);
-        FewRun r;
-        const uint64_t policy = evict_first_policy();
-        int stage = 0, issued = 0;
-        uint32_t phase = 0;
-        bool ok = true, have = wk.next(r);
-        int kb = 0;
-        auto load_a = [&](int st, const FewRun& q, int k) {
-            if (lane == 0) {
+        // ------------------------------------------------------------ producer (one lane)
+        if (lane == 0) {
+            FewWalk<FP8> wk(p, pl);
+            FewRun r;
+            const uint64_t policy = evict_first_policy();
+            int stage = 0, issued = 0, kb = 0;
+            uint32_t phase = 0;
+            bool ok = true, have = wk.next(r);
+            auto load_a = [&](int st, const FewRun& q, int k) {
                 uint8_t* sa = ring + (size_t)st * stage_bytes;
                 ptx::mbar_arrive_expect_tx(&sm.full[st], FEW_A_BYTES + q.bn * 128);
                 const CUtensorMap* tm = q.phase ? &tmW2 : &tmW13;
                 tma_load_weights(sa, tm, &sm.full[st], (q.kb0 + k) * BK, q.row0, policy);
                 tma_load_weights(sa + FEW_A_BYTES / 2, tm, &sm.full[st], (q.kb0 + k) * BK, q.row1, policy);
-            }
-        };
-        auto load_b = [&](int st, const FewRun& q, int k) {
-            if (lane == 0) {
+            };
+            auto load_b = [&](int st, const FewRun& q, int k) {
                 uint8_t* sb = ring + (size_t)st * stage_bytes + FEW_A_BYTES;
                 if (q.phase == 0) {
                     ptx::tma_load_2d(sb, &tmX, &sm.full[st], k * BK, 0);
@@ -641,112 +668,118 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                     for (int i = 0; i < q.bn; i += 16)
                         ptx::tma_load_2d(sb + i * 128, &tmH, &sm.full[st], (q.kb0 + k) * BK, q.brow + i);
                 }
-            }
-        };
-        auto step = [&]() {
-            __syncwarp();
-            issued++;
-            if (++stage == stages) { stage = 0; phase ^= 1u; }
-            if (++kb == r.nkb) { kb = 0; have = wk.next(r); }
-        };
-        while (ok && have && r.phase == 0) {
-            ok = warp_wait(&sm.empty[stage], phase ^ 1u, s_abort);
-            if (!ok) break;
-            load_a(stage, r, kb);
-            load_b(stage, r, kb);
-            step();
-        }
-        if (ok && have) {
-            // the ring's worth of down weights, then (once all of h is written) their tokens operand
-            FewWalk<FP8> wb = wk;
-            FewRun rb = r;
-            int sb = stage, kbb = kb, n = 0;
-            while (have && n < stages) {
-                ok = warp_wait(&sm.empty[stage], phase ^ 1u, s_abort);
-                if (!ok) break;
-                load_a(stage, r, kb);
-                step();
-                n++;
-            }
-            ok = few_wait_h(p.count, s_abort) && ok;
-            for (int i = 0; i < n; i++) {    // (also when giving up: the stages' loads have to complete)
-                load_b(sb, rb, kbb);
-                if (++sb == stages) sb = 0;
-                if (++kbb == rb.nkb) { kbb = 0; wb.next(rb); }
-            }
-            while (ok && have) {
-                ok = warp_wait(&sm.empty[stage], phase ^ 1u, s_abort);
+            };
+            auto step = [&]() {
+                issued++;
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
+                if (++kb == r.nkb) { kb = 0; have = wk.next(r); }
+            };
+            while (have && r.phase == 0) {
+                ok = ptx::wait_parity(&sm.empty[stage], phase ^ 1u, s_abort);
                 if (!ok) break;
                 load_a(stage, r, kb);
                 load_b(stage, r, kb);
                 step();
             }
-        }
-        if (!ok) {
-            // give the loads already issued a bounded chance to land before the CTA exits
-            for (int i = 0; i < stages && i < issued; i++) {
-                if (--stage < 0) { stage = stages - 1; phase ^= 1u; }
-                volatile uint32_t never = 0u;
-                ptx::wait_parity(&sm.full[stage], phase, &never, 100000000ull);
+            if (ok && have) {
+                // the ring's worth of down weights, then (once all of h is written) their tokens operand
+                FewWalk<FP8> wb = wk;
+                FewRun rb = r;
+                int sb = stage, kbb = kb, n = 0;
+                while (have && n < stages) {
+                    ok = ptx::wait_parity(&sm.empty[stage], phase ^ 1u, s_abort);
+                    if (!ok) break;
+                    load_a(stage, r, kb);
+                    step();
+                    n++;
+                }
+                ok = few_wait_h(p.count, s_abort) && ok;
+                for (int i = 0; i < n; i++) {    // (also when giving up: the stages' loads have to complete)
+                    load_b(sb, rb, kbb);
+                    if (++sb == stages) sb = 0;
+                    if (++kbb == rb.nkb) { kbb = 0; wb.next(rb); }
+                }
+                while (ok && have) {
+                    ok = ptx::wait_parity(&sm.empty[stage], phase ^ 1u, s_abort);
+                    if (!ok) break;
+                    load_a(stage, r, kb);
+                    load_b(stage, r, kb);
+                    step();
+                }
+            }
+            if (!ok) {
+                // give the loads already issued a bounded chance to land before the CTA exits
+                for (int i = 0; i < stages && i < issued; i++) {
+                    if (--stage < 0) { stage = stages - 1; phase ^= 1u; }
+                    volatile uint32_t never = 0u;
+                    ptx::wait_parity(&sm.full[stage], phase, &never, 100000000ull);
+                }
             }
         }
+        __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        FewWalk<FP8> wk(p, pl);
-        FewRun r;
-        int stage = 0, buf = 0, sslot = 0;
-        uint32_t phase = 0, tphase = 0, sphase = 0;
-        bool ok = true;
-        while (ok && wk.next(r)) {
-            if (!warp_wait(&sm.tempty[buf], tphase ^ 1u, s_abort)) break;
-            ptx::tc_fence_after();
-            const uint32_t d = tmem + (uint32_t)(buf * FEW_ACC_COLS);
-            for (int kb = 0; kb < r.nkb; kb++) {
-                const int gk = r.kb0 + kb;
-                ok = warp_wait(&sm.full[stage], phase, s_abort);
+        // ------------------------------------------------------------ MMA issuer (one lane)
+        // The four MMAs of a k-block take the tensor pipe about 400 cycles at these shapes, most of
+        // the 690 that a 16 KB tile takes to arrive at an SM's share of the memory's rate: the issuing
+        // thread does nothing else.
+        if (lane == 0) {
+            FewWalk<FP8> wk(p, pl);
+            FewRun r;
+            int stage = 0, buf = 0, sslot = 0;
+            uint32_t phase = 0, tphase = 0, sphase = 0;
+            const uint64_t a_desc = ptx::sdesc_k_sw128(ptx::smem_addr(ring));
+            const uint64_t sf_desc = ptx::sdesc_plain(ptx::smem_addr(sfring));
+            bool ok = true;
+            while (ok && wk.next(r)) {
+                ok = ptx::wait_parity(&sm.tempty[buf], tphase ^ 1u, s_abort);
                 if (!ok) break;
-                if (FP8 && (kb == 0 || (gk & 3) == 0)) {
-                    ok = warp_wait(&sm.sf_ready[sslot], sphase, s_abort);
-                    if (!ok) break;
-                }
                 ptx::tc_fence_after();
-                const bool group_end = kb == r.nkb - 1 || (gk & 3) == 3;
-                if (lane == 0) {
-                    const uint32_t a0 = ptx::smem_addr(ring + (size_t)stage * stage_bytes);
-                    const uint32_t b0 = a0 + FEW_A_BYTES;
-                    if constexpr (FP8) {
-                        const uint32_t sf_t = tmem + (uint32_t)(2 * FEW_ACC_COLS + stage * 8);
-                        const uint32_t sf_s = ptx::smem_addr(sfring + (size_t)sslot * FEW_SF_BYTES + (gk & 3) * 1024);
-                        ptx::tc_cp_32x128b_warpx4(sf_t, ptx::sdesc_plain(sf_s));
-                        ptx::tc_cp_32x128b_warpx4(sf_t + 4, ptx::sdesc_plain(sf_s + 512));
+                const uint32_t d = tmem + (uint32_t)(buf * FEW_ACC_COLS);
+                const uint32_t idesc = FP8 ? ptx::idesc_mxf8(128, r.bn, 0, 0) : ptx::idesc_bf16(128, r.bn);
+                for (int kb = 0; kb < r.nkb; kb++) {
+                    const int gk = r.kb0 + kb;
+                    const uint32_t sf_t = tmem + (uint32_t)(2 * FEW_ACC_COLS + sslot * 32);
+                    if (FP8 && (kb == 0 || (gk & 3) == 0)) {
+                        // a group's scales to TMEM at once; the slot in shared memory is free after that
+                        ok = ptx::wait_parity(&sm.sf_ready[sslot], sphase, s_abort);
+                        if (!ok) break;
+                        const uint64_t sd = sf_desc + (uint64_t)(sslot * (FEW_SF_BYTES / 16));
 #pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            ptx::mma_mxf8(d, ptx::sdesc_k_sw128(a0 + k * 32), ptx::sdesc_k_sw128(b0 + k * 32),
-                                          ptx::idesc_mxf8(128, r.bn, k, k), sf_t, sf_t + 4, (kb | k) != 0);
+                        for (int w = 0; w < 4; w++) {
+                            ptx::tc_cp_32x128b_warpx4(sf_t + 8 * w, sd + 64 * w);
+                            ptx::tc_cp_32x128b_warpx4(sf_t + 8 * w + 4, sd + 64 * w + 32);
+                        }
+                        ptx::tc_commit(&sm.sf_empty[sslot]);
+                    }
+                    ok = ptx::wait_parity(&sm.full[stage], phase, s_abort);
+                    if (!ok) break;
+                    const uint64_t ad = a_desc + (uint64_t)(stage * (stage_bytes / 16));
+                    const uint64_t bd = ad + FEW_A_BYTES / 16;
+                    if constexpr (FP8) {
+                        const uint32_t sf = sf_t + (uint32_t)(gk & 3) * 8;
+#pragma unroll
+                        for (int k = 0; k < 4; k++)      // (scale ids k: bits 29-30 of A's, 4-5 of B's)
+                            ptx::mma_mxf8(d, ad + 2 * k, bd + 2 * k, idesc | (uint32_t)(k << 29) | (uint32_t)(k << 4), sf,
+                                          sf + 4, (kb | k) != 0);
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            ptx::mma_f16(d, ptx::sdesc_k_sw128(a0 + k * 32), ptx::sdesc_k_sw128(b0 + k * 32),
-                                         ptx::idesc_bf16(128, r.bn), (kb | k) != 0);
+                        for (int k = 0; k < 4; k++) ptx::mma_f16(d, ad + 2 * k, bd + 2 * k, idesc, (kb | k) != 0);
                     }
                     ptx::tc_commit(&sm.empty[stage]);
-                    if (FP8 && group_end) ptx::tc_commit(&sm.sf_empty[sslot]);
+                    if (++stage == stages) { stage = 0; phase ^= 1u; }
+                    if (FP8 && (kb == r.nkb - 1 || (gk & 3) == 3) && ++sslot == FEW_SF_SLOTS) { sslot = 0; sphase ^= 1u; }
                 }
-                __syncwarp();
-                if (++stage == stages) { stage = 0; phase ^= 1u; }
-                if (FP8 && group_end && ++sslot == FEW_SF_SLOTS) { sslot = 0; sphase ^= 1u; }
+                if (!ok) break;
+                ptx::tc_commit(&sm.tfull[buf]);
+                buf ^= 1;
+                if (buf == 0) tphase ^= 1u;
             }
-            if (!ok) break;
-            if (lane == 0) ptx::tc_commit(&sm.tfull[buf]);
-            __syncwarp();
-            buf ^= 1;
-            if (buf == 0) tphase ^= 1u;
+            // every MMA issued has completed before TMEM is released
+            ptx::tc_commit(&sm.done);
+            volatile uint32_t never = 0u;
+            ptx::wait_parity(&sm.done, 0u, &never, 100000000ull);
         }
-        // every MMA issued has completed before TMEM is released
-        if (lane == 0) ptx::tc_commit(&sm.done);
         __syncwarp();
-        volatile uint32_t never = 0u;
-        ptx::wait_parity(&sm.done, 0u, &never, 100000000ull);
     } else if (FP8 && warp == 6) {
         // ------------------------------------------------------------ scales (MXFP8)
         // A group is the 16 scale bytes (four k-blocks) of every row of a tile: 128 weight rows, bn
@@ -907,14 +940,12 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             release();
             have = wk.next(r);
         }
-        // this CTA's h is written: made visible to the other CTAs' TMA loads, then counted
-        asm volatile("fence.proxy.async;" ::: "memory");
-        __threadfence();
+        // this CTA's h is written: made visible to the other CTAs' TMA loads, then counted (the barrier
+        // orders the four warps' stores before the one release)
+        asm volatile("fence.proxy.async.global;" ::: "memory");
         epi_sync();
-        if (threadIdx.x == 64) {
-            __threadfence();
+        if (threadIdx.x == 64)
             asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p.count), "r"(1u) : "memory");
-        }
         // down
         const int per_tile = pl.A * (p.F / BK);         // k-blocks of an output tile
         int tile = -1;
@@ -937,12 +968,17 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             const size_t slot = (size_t)p.T * 128;
             float* mine = p.part + ((size_t)2 * blockIdx.x + (tile != first_tile)) * slot + row;
             for (int t = 0; t < p.T; t++) __stcg(mine + t * 128, acc[t * 128 + row]);
-            __threadfence();
             epi_sync();
-            if (threadIdx.x == 64) sm.ticket = (int)atomicAdd(p.count + 1 + tile, 1u);
+            if (threadIdx.x == 64) {
+                unsigned n;      // releases this CTA's sums (all four warps', by the barrier), acquires the others'
+                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;"
+                             : "=r"(n)
+                             : "l"(p.count + 1 + tile), "r"(1u)
+                             : "memory");
+                sm.ticket = (int)n;
+            }
             epi_sync();
             if (sm.ticket != c1 - c0) return;
-            __threadfence();
             // a warp per token, four rows a lane; eight tokens' loads in flight per warp
             const float4* src = reinterpret_cast<const float4*>(
                 p.part + ((size_t)2 * c0 + (pl.begin_of(c0) / per_tile != tile)) * slot) + lane;
@@ -1096,10 +1132,11 @@ moe_status few_launch(FewArgs a, const PrepArgs& p, const void* x, const uint8_t
         configured = FEW_SMEM_MAX;
     }
     const int V = p.logits ? (p.E + PREP_THREADS - 1) / PREP_THREADS : 1;
-    if (V <= 1) few_prep_kernel<1><<<a.T, PREP_THREADS, 0, s>>>(p);
-    else if (V <= 4) few_prep_kernel<4><<<a.T, PREP_THREADS, 0, s>>>(p);
-    else if (V <= 12) few_prep_kernel<12><<<a.T, PREP_THREADS, 0, s>>>(p);
-    else few_prep_kernel<32><<<a.T, PREP_THREADS, 0, s>>>(p);
+    const int ctas = a.T + (FP8 ? a.T * ((a.H + PREP_QUANT - 1) / PREP_QUANT) : 0);
+    if (V <= 1) few_prep_kernel<1><<<ctas, PREP_THREADS, 0, s>>>(p);
+    else if (V <= 4) few_prep_kernel<4><<<ctas, PREP_THREADS, 0, s>>>(p);
+    else if (V <= 12) few_prep_kernel<12><<<ctas, PREP_THREADS, 0, s>>>(p);
+    else few_prep_kernel<32><<<ctas, PREP_THREADS, 0, s>>>(p);
     if (cudaPeekAtLastError() != cudaSuccess) return moe_host::launch_status();
     int grid = few_sms();
     if (grid > FEW_GRID_MAX) grid = FEW_GRID_MAX;
@@ -1108,13 +1145,11 @@ moe_status few_launch(FewArgs a, const PrepArgs& p, const void* x, const uint8_t
     cfg.blockDim = dim3(few_threads<FP8>());
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;      // the CTAs wait for one another: all resident, or none
     attr[0].val.cooperative = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kern, tw13, tw2, tx, th, ts13, ts2, tsx, tsh, a) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
@@ -1156,6 +1191,7 @@ extern "C" moe_status moe_layer_few_tokens(const void* x, int T, int H, const fl
     PrepArgs p{};
     p.x = static_cast<const __nv_bfloat16*>(x);
     p.logits = logits;
+    p.T = T;
     p.H = H;
     p.E = E;
     p.K = K;
