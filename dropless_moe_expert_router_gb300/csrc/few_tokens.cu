@@ -283,13 +283,15 @@ __global__ void __launch_bounds__(PREP_THREADS) few_prep_kernel(PrepArgs p) {
 // already on their way then, as they depend on the routing alone.
 //
 // Warps: 0 TMA producer, 1 TMEM and MMA issue, 2-5 epilogue (one TMEM lane quarter each), 6 (MXFP8)
-// the scales: loads a group of four k-blocks' scale bytes and rearranges them for tcgen05.cp.
+// the scales: loads a group of 16 k-blocks' scale bytes and rearranges them for tcgen05.cp.
 // ---------------------------------------------------------------------------
-constexpr int FEW_STAGES = 12;             // most ring stages
+constexpr int FEW_STAGES = 6;              // most ring stages
+constexpr int FEW_KPS = 2;                 // k-blocks in a stage
 constexpr int FEW_A_BYTES = 128 * 128;     // a weight tile: 128 rows of 128 bytes
 constexpr int FEW_ACC_COLS = 64;           // TMEM columns of one accumulator: tokens
-constexpr int FEW_SF_SLOTS = 4;            // MXFP8: groups of scales in flight
-constexpr int FEW_SF_BYTES = 4096;         // a slot: landed 16 bytes a row, rearranged 4 x (A 512 | B 512)
+constexpr int FEW_SF_KB = 16;              // MXFP8: k-blocks in a group of scales, and a row's bytes of it / 4
+constexpr int FEW_SF_SLOTS = 2;            // groups of scales in flight
+constexpr int FEW_SF_BYTES = FEW_SF_KB * 1024;   // a slot: landed 64 bytes a row, rearranged 16 x (A 512 | B 512)
 constexpr int FEW_XCH = 16;                // tokens whose W3 products the epilogue exchanges at a time (tmem_wait16)
 constexpr int FEW_MIN_KB = 2;              // k-blocks of the down walk that a CTA takes at least
 constexpr size_t FEW_SMEM_MAX = 227 * 1024;
@@ -581,7 +583,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int stages = p.stages;
-    const int stage_bytes = FEW_A_BYTES + p.nb * 128;
+    const int stage_bytes = FEW_KPS * (FEW_A_BYTES + p.nb * 128);      // FEW_KPS weight tiles, then tokens
     uint8_t* at = ring + (size_t)stages * stage_bytes;
     uint8_t* sfring = at;                                            // MXFP8
     at += FP8 ? FEW_SF_SLOTS * FEW_SF_BYTES : 0;
@@ -653,26 +655,33 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             int stage = 0, issued = 0, kb = 0;
             uint32_t phase = 0;
             bool ok = true, have = wk.next(r);
+            // a stage: k-blocks k and, if the run has it, k + 1
             auto load_a = [&](int st, const FewRun& q, int k) {
                 uint8_t* sa = ring + (size_t)st * stage_bytes;
-                ptx::mbar_arrive_expect_tx(&sm.full[st], FEW_A_BYTES + q.bn * 128);
+                const int n = min(FEW_KPS, q.nkb - k);
+                ptx::mbar_arrive_expect_tx(&sm.full[st], n * (FEW_A_BYTES + q.bn * 128));
                 const CUtensorMap* tm = q.phase ? &tmW2 : &tmW13;
-                tma_load_weights(sa, tm, &sm.full[st], (q.kb0 + k) * BK, q.row0, policy);
-                tma_load_weights(sa + FEW_A_BYTES / 2, tm, &sm.full[st], (q.kb0 + k) * BK, q.row1, policy);
+                for (int i = 0; i < n; i++, sa += FEW_A_BYTES) {
+                    tma_load_weights(sa, tm, &sm.full[st], (q.kb0 + k + i) * BK, q.row0, policy);
+                    tma_load_weights(sa + FEW_A_BYTES / 2, tm, &sm.full[st], (q.kb0 + k + i) * BK, q.row1, policy);
+                }
             };
             auto load_b = [&](int st, const FewRun& q, int k) {
-                uint8_t* sb = ring + (size_t)st * stage_bytes + FEW_A_BYTES;
-                if (q.phase == 0) {
-                    ptx::tma_load_2d(sb, &tmX, &sm.full[st], k * BK, 0);
-                } else {
-                    for (int i = 0; i < q.bn; i += 16)
-                        ptx::tma_load_2d(sb + i * 128, &tmH, &sm.full[st], (q.kb0 + k) * BK, q.brow + i);
+                uint8_t* sb = ring + (size_t)st * stage_bytes + FEW_KPS * FEW_A_BYTES;
+                const int n = min(FEW_KPS, q.nkb - k);
+                for (int i = 0; i < n; i++, sb += p.nb * 128) {
+                    if (q.phase == 0) {
+                        ptx::tma_load_2d(sb, &tmX, &sm.full[st], (k + i) * BK, 0);
+                    } else {
+                        for (int j = 0; j < q.bn; j += 16)
+                            ptx::tma_load_2d(sb + j * 128, &tmH, &sm.full[st], (q.kb0 + k + i) * BK, q.brow + j);
+                    }
                 }
             };
             auto step = [&]() {
                 issued++;
                 if (++stage == stages) { stage = 0; phase ^= 1u; }
-                if (++kb == r.nkb) { kb = 0; have = wk.next(r); }
+                if ((kb += FEW_KPS) >= r.nkb) { kb = 0; have = wk.next(r); }
             };
             while (have && r.phase == 0) {
                 ok = ptx::wait_parity(&sm.empty[stage], phase ^ 1u, s_abort);
@@ -697,7 +706,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                 for (int i = 0; i < n; i++) {    // (also when giving up: the stages' loads have to complete)
                     load_b(sb, rb, kbb);
                     if (++sb == stages) sb = 0;
-                    if (++kbb == rb.nkb) { kbb = 0; wb.next(rb); }
+                    if ((kbb += FEW_KPS) >= rb.nkb) { kbb = 0; wb.next(rb); }
                 }
                 while (ok && have) {
                     ok = ptx::wait_parity(&sm.empty[stage], phase ^ 1u, s_abort);
@@ -719,9 +728,9 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (one lane)
-        // The four MMAs of a k-block take the tensor pipe about 400 cycles at these shapes, most of
-        // the 690 that a 16 KB tile takes to arrive at an SM's share of the memory's rate: the issuing
-        // thread does nothing else.
+        // An SM's share of the memory's rate brings a 16 KB tile about every 690 cycles; a k-block's four
+        // MMAs take 320, its two copies of scales 160, and a stage's wait and commit 350, one after the
+        // other: hence two k-blocks a stage, and one lane that does nothing else.
         if (lane == 0) {
             FewWalk<FP8> wk(p, pl);
             FewRun r;
@@ -736,38 +745,45 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * FEW_ACC_COLS);
                 const uint32_t idesc = FP8 ? ptx::idesc_mxf8(128, r.bn, 0, 0) : ptx::idesc_bf16(128, r.bn);
-                for (int kb = 0; kb < r.nkb; kb++) {
-                    const int gk = r.kb0 + kb;
-                    const uint32_t sf_t = tmem + (uint32_t)(2 * FEW_ACC_COLS + sslot * 32);
-                    if (FP8 && (kb == 0 || (gk & 3) == 0)) {
-                        // a group's scales to TMEM at once; the slot in shared memory is free after that
-                        ok = ptx::wait_parity(&sm.sf_ready[sslot], sphase, s_abort);
-                        if (!ok) break;
-                        const uint64_t sd = sf_desc + (uint64_t)(sslot * (FEW_SF_BYTES / 16));
-#pragma unroll
-                        for (int w = 0; w < 4; w++) {
-                            ptx::tc_cp_32x128b_warpx4(sf_t + 8 * w, sd + 64 * w);
-                            ptx::tc_cp_32x128b_warpx4(sf_t + 8 * w + 4, sd + 64 * w + 32);
-                        }
-                        ptx::tc_commit(&sm.sf_empty[sslot]);
-                    }
+                for (int k0 = 0; k0 < r.nkb; k0 += FEW_KPS) {
+                    const uint64_t ad0 = a_desc + (uint64_t)(stage * (stage_bytes / 16));
+                    const uint64_t bd0 = ad0 + FEW_KPS * FEW_A_BYTES / 16;
                     ok = ptx::wait_parity(&sm.full[stage], phase, s_abort);
                     if (!ok) break;
-                    const uint64_t ad = a_desc + (uint64_t)(stage * (stage_bytes / 16));
-                    const uint64_t bd = ad + FEW_A_BYTES / 16;
-                    if constexpr (FP8) {
-                        const uint32_t sf = sf_t + (uint32_t)(gk & 3) * 8;
 #pragma unroll
-                        for (int k = 0; k < 4; k++)      // (scale ids k: bits 29-30 of A's, 4-5 of B's)
-                            ptx::mma_mxf8(d, ad + 2 * k, bd + 2 * k, idesc | (uint32_t)(k << 29) | (uint32_t)(k << 4), sf,
-                                          sf + 4, (kb | k) != 0);
-                    } else {
+                    for (int u = 0; u < FEW_KPS; u++) {
+                        const int kb = k0 + u;
+                        if (kb >= r.nkb) break;
+                        const uint64_t ad = ad0 + u * FEW_A_BYTES / 16, bd = bd0 + (uint64_t)(u * p.nb * 8);
+                        if constexpr (FP8) {
+                            const int gw = (r.kb0 + kb) & (FEW_SF_KB - 1);
+                            const uint32_t sf_t = tmem + (uint32_t)(2 * FEW_ACC_COLS);
+                            if (kb == 0 || gw == 0) {
+                                // a group's scales to TMEM at once; the slot in shared memory is free after that
+                                ok = ptx::wait_parity(&sm.sf_ready[sslot], sphase, s_abort);
+                                if (!ok) break;
+                                const uint64_t sd = sf_desc + (uint64_t)(sslot * (FEW_SF_BYTES / 16));
+                                const int end = min(FEW_SF_KB, gw + r.nkb - kb);
+                                for (int w = gw; w < end; w++) {
+                                    ptx::tc_cp_32x128b_warpx4(sf_t + 8 * w, sd + 64 * w);
+                                    ptx::tc_cp_32x128b_warpx4(sf_t + 8 * w + 4, sd + 64 * w + 32);
+                                }
+                                ptx::tc_commit(&sm.sf_empty[sslot]);
+                                if (++sslot == FEW_SF_SLOTS) { sslot = 0; sphase ^= 1u; }
+                            }
+                            const uint32_t sf = sf_t + (uint32_t)gw * 8;
 #pragma unroll
-                        for (int k = 0; k < 4; k++) ptx::mma_f16(d, ad + 2 * k, bd + 2 * k, idesc, (kb | k) != 0);
+                            for (int k = 0; k < 4; k++)      // (scale ids k: bits 29-30 of A's, 4-5 of B's)
+                                ptx::mma_mxf8(d, ad + 2 * k, bd + 2 * k, idesc | (uint32_t)(k << 29) | (uint32_t)(k << 4),
+                                              sf, sf + 4, (kb | k) != 0);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; k++) ptx::mma_f16(d, ad + 2 * k, bd + 2 * k, idesc, (kb | k) != 0);
+                        }
                     }
+                    if (!ok) break;
                     ptx::tc_commit(&sm.empty[stage]);
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
-                    if (FP8 && (kb == r.nkb - 1 || (gk & 3) == 3) && ++sslot == FEW_SF_SLOTS) { sslot = 0; sphase ^= 1u; }
                 }
                 if (!ok) break;
                 ptx::tc_commit(&sm.tfull[buf]);
@@ -782,10 +798,10 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
         __syncwarp();
     } else if (FP8 && warp == 6) {
         // ------------------------------------------------------------ scales (MXFP8)
-        // A group is the 16 scale bytes (four k-blocks) of every row of a tile: 128 weight rows, bn
-        // token rows. Landed, it is rearranged in place into four chunks for tcgen05.cp .32x128b:
-        // chunk w has k-block w's words, the word of row 32 j + lane at lane * 4 + j; first the weights'
-        // 512 bytes, then the tokens'. Loads and rearranging do not wait for one another.
+        // A group is 64 scale bytes (16 k-blocks) of every row of a tile: 128 weight rows, bn token
+        // rows. Landed, it is rearranged in place into 16 chunks for tcgen05.cp .32x128b: chunk w
+        // has k-block w's words, the word of row 32 j + lane at lane * 4 + j; first the weights' 512
+        // bytes, then the tokens'. Loads and rearranging do not wait for one another.
         if constexpr (FP8) {
             struct Cursor {
                 FewWalk<FP8> wk;
@@ -794,7 +810,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                 bool have;
             };
             auto advance = [](Cursor& c) {
-                c.kb += 4 - ((c.r.kb0 + c.kb) & 3);
+                c.kb += FEW_SF_KB - ((c.r.kb0 + c.kb) & (FEW_SF_KB - 1));
                 if (c.kb >= c.r.nkb) {
                     c.kb = 0;
                     c.have = c.wk.next(c.r);
@@ -815,16 +831,16 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                     __all_sync(FULL, ptx::mbar_test_wait(&sm.sf_empty[ld_slot], ld_phase ^ 1u))) {
                     if (lane == 0) {
                         uint8_t* sf = sfring + (size_t)ld_slot * FEW_SF_BYTES;
-                        const int kx = ((ld.r.kb0 + ld.kb) >> 2) * 16;
+                        const int kx = (ld.r.kb0 + ld.kb) / FEW_SF_KB * 64;
                         const CUtensorMap* tm = ld.r.phase ? &tmSW2 : &tmSW13;
-                        ptx::mbar_arrive_expect_tx(&sm.sf_full[ld_slot], (128 + ld.r.bn) * 16);
+                        ptx::mbar_arrive_expect_tx(&sm.sf_full[ld_slot], (128 + ld.r.bn) * 64);
                         ptx::tma_load_2d(sf, tm, &sm.sf_full[ld_slot], kx, ld.r.row0);
-                        ptx::tma_load_2d(sf + 1024, tm, &sm.sf_full[ld_slot], kx, ld.r.row1);
+                        ptx::tma_load_2d(sf + 4096, tm, &sm.sf_full[ld_slot], kx, ld.r.row1);
                         if (ld.r.phase == 0) {
-                            ptx::tma_load_2d(sf + 2048, &tmSX, &sm.sf_full[ld_slot], kx, 0);
+                            ptx::tma_load_2d(sf + 8192, &tmSX, &sm.sf_full[ld_slot], kx, 0);
                         } else {
                             for (int i = 0; i < ld.r.bn; i += 16)
-                                ptx::tma_load_2d(sf + 2048 + i * 16, &tmSH, &sm.sf_full[ld_slot], kx, ld.r.brow + i);
+                                ptx::tma_load_2d(sf + 8192 + i * 64, &tmSH, &sm.sf_full[ld_slot], kx, ld.r.brow + i);
                         }
                     }
                     __syncwarp();
@@ -836,14 +852,19 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                 if (loaded > 0 && __all_sync(FULL, ptx::mbar_test_wait(&sm.sf_full[pr_slot], pr_phase))) {
                     uint8_t* sf = sfring + (size_t)pr_slot * FEW_SF_BYTES;
                     const uint4* l = reinterpret_cast<const uint4*>(sf);
-                    uint4 v[6];
+                    uint4 v[6][4];                   // row 32 j + lane: words of k-blocks 4 i ..
 #pragma unroll
-                    for (int j = 0; j < 6; j++) v[j] = l[32 * j + lane];
+                    for (int j = 0; j < 6; j++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) v[j][i] = l[(32 * j + lane) * 4 + i];
                     __syncwarp();
                     uint4* out = reinterpret_cast<uint4*>(sf);
 #pragma unroll
-                    for (int w = 0; w < 4; w++) {
-                        auto word = [w](const uint4& q) { return w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w; };
+                    for (int w = 0; w < FEW_SF_KB; w++) {
+                        auto word = [w](const uint4 (&q)[4]) {
+                            const uint4& u = q[w / 4];
+                            return w % 4 == 0 ? u.x : w % 4 == 1 ? u.y : w % 4 == 2 ? u.z : u.w;
+                        };
                         out[w * 64 + lane] = make_uint4(word(v[0]), word(v[1]), word(v[2]), word(v[3]));
                         out[w * 64 + 32 + lane] = make_uint4(word(v[4]), word(v[5]), 0u, 0u);
                     }
@@ -1104,8 +1125,8 @@ moe_status few_launch(FewArgs a, const PrepArgs& p, const void* x, const uint8_t
                       const uint8_t* w13s, const void* w2, const uint8_t* w2s, cudaStream_t s) {
     // shared memory: as many ring stages as fit beside the plan and the output sums
     const size_t fixed = 1024 + few_fixed_smem(a.T, a.K, a.a_max, FP8);
-    const int stage_bytes = FEW_A_BYTES + a.nb * 128;
-    if (fixed + 4 * (size_t)stage_bytes > FEW_SMEM_MAX) return MOE_ERR_UNSUPPORTED;
+    const int stage_bytes = FEW_KPS * (FEW_A_BYTES + a.nb * 128);
+    if (fixed + 2 * (size_t)stage_bytes > FEW_SMEM_MAX) return MOE_ERR_UNSUPPORTED;
     a.stages = (int)((FEW_SMEM_MAX - fixed) / stage_bytes);
     if (a.stages > FEW_STAGES) a.stages = FEW_STAGES;
     if ((size_t)a.stages * stage_bytes < (size_t)a.E * 10) return MOE_ERR_UNSUPPORTED;   // the plan's scratch
@@ -1118,8 +1139,8 @@ moe_status few_launch(FewArgs a, const PrepArgs& p, const void* x, const uint8_t
         !make_operand_map(&tx, x, FP8, a.H, a.T, a.nb) || !make_operand_map(&th, a.h, FP8, a.F, rh, 16))
         return MOE_ERR_CUDA;
     if (FP8) {
-        if (!make_scale_map(&ts13, w13s, a.H / 32, r13, 64) || !make_scale_map(&ts2, w2s, a.F / 32, r2, 64) ||
-            !make_scale_map(&tsx, xs, a.H / 32, a.T, a.nb) || !make_scale_map(&tsh, a.hs, a.F / 32, rh, 16))
+        if (!make_scale_map(&ts13, w13s, a.H / 32, r13, 64, 64) || !make_scale_map(&ts2, w2s, a.F / 32, r2, 64, 64) ||
+            !make_scale_map(&tsx, xs, a.H / 32, a.T, a.nb, 64) || !make_scale_map(&tsh, a.hs, a.F / 32, rh, 16, 64))
             return MOE_ERR_CUDA;
     } else {
         ts13 = ts2 = tsx = tsh = tw13;

@@ -39,13 +39,14 @@ inline bool make_operand_map(CUtensorMap* m, const void* base, bool fp8, uint64_
     return r == CUDA_SUCCESS;
 }
 
-// MXFP8 scales [rows][row_bytes] (bytes), box {16 bytes, box_rows}, no swizzle.
-inline bool make_scale_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows) {
+// MXFP8 scales [rows][row_bytes] (bytes), box {box_bytes, box_rows}, no swizzle.
+inline bool make_scale_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows,
+                           uint32_t box_bytes = 16) {
     auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[2] = {row_bytes, rows};
     cuuint64_t strides[1] = {row_bytes};
-    cuuint32_t box[2] = {16u, box_rows};
+    cuuint32_t box[2] = {box_bytes, box_rows};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
