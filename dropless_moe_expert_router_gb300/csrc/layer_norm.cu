@@ -6,6 +6,7 @@
 // dx = rstd (g - sum(g) / H - xh sum(g xh) / H) (+ dx_add), dw = sum_t dy xh, db = sum_t dy.
 // Each operand is read once and each output written once: the bytes bound both directions.
 #include "common.cuh"
+#include "sm100_ptx.cuh"
 
 #include <initializer_list>
 
@@ -13,6 +14,8 @@ namespace moe {
 namespace {
 
 constexpr int LN_HMAX = 65536;
+constexpr int LN_STAGES = 4;              // most ring stages of the kernels that go through shared memory
+constexpr size_t LN_SMEM = 220 * 1024;    // their dynamic shared memory at most
 
 template <typename T> __device__ __forceinline__ float to_f(T v);
 template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
@@ -309,6 +312,340 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const T* dy, const 
     }
 }
 
+// ---------------------------------------------------------------------------
+// Rows through shared memory. A CTA takes R consecutive rows at a time; their operands arrive by
+// bulk copies, a ring of stages ahead, so that enough bytes are in flight without holding them in
+// registers, and one barrier per R rows joins the warps' sums (it also says that everybody has
+// read the stage before: thread 0 refills it then). Thread pieces as above: piece i at
+// i * threads + thread.
+// ---------------------------------------------------------------------------
+struct LnRing {
+    uint64_t full[LN_STAGES];
+    uint32_t abort_flag;
+};
+
+__device__ __forceinline__ void ring_init(LnRing& ring, int stages) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; i++) ptx::mbar_init(&ring.full[i], 1);
+        ring.abort_flag = 0u;
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+}
+
+// After a wait that gave up: the copies in flight get a bounded chance to land (`done` groups were begun).
+__device__ __forceinline__ void ring_drain(LnRing& ring, int stages, int done) {
+    if (threadIdx.x == 0 && *(volatile uint32_t*)&ring.abort_flag) {
+        volatile uint32_t never = 0u;
+        for (int i = 0; i < stages && i < done; i++)
+            ptx::wait_parity(&ring.full[(done - 1 - i) % stages], (uint32_t)(((done - 1 - i) / stages) & 1), &never, 100000000ull);
+    }
+}
+
+// Forward. The variance is joined from each warp's sum of squares about its own mean (no cancellation,
+// one barrier): sum (s - mean)^2 = sum over warps of (their M2 + n_w (mean_w - mean)^2).
+template <typename T, typename W, int VEC, int NV, int R>
+__global__ void __launch_bounds__(512, NV == 2 && R == 1 ? 2 : 1) ln_forward_ring_kernel(const T* x, const T* residual, int rows, int H,
+                                                              const W* __restrict__ w, const W* __restrict__ b,
+                                                              float eps, T* sum, T* y, float* mean_out, float* rstd_out,
+                                                              int stages) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ LnRing ring;
+    __shared__ float2 red[2][16 * R];         // (mean, M2) of every warp and row
+    __shared__ float count[16];               // elements of a row that a warp has
+    using V = Vec<T, VEC>;
+    const int tpr = blockDim.x, me = threadIdx.x, n = H / VEC, lane = (int)lane_id();
+    const uint32_t rb = (uint32_t)(H * sizeof(T));
+    const int entry = lane & (16 * R - 1);    // this lane's of red: warp entry / R, row entry % R
+    const int nt = residual ? 2 : 1;
+    const uint32_t stage_bytes = nt * R * rb;
+    const long long groups = ((long long)rows + R - 1) / R, step = gridDim.x;
+    auto issue = [&](long long g, int st) {
+        uint8_t* d = smem + (size_t)st * stage_bytes;
+        const long long t = g * R;
+        const uint32_t nb = (uint32_t)(rows - t < R ? rows - t : R) * rb;
+        ptx::mbar_arrive_expect_tx(&ring.full[st], nt * nb);
+        ptx::bulk_load(d, x + t * H, nb, &ring.full[st]);
+        if (residual) ptx::bulk_load(d + R * rb, residual + t * H, nb, &ring.full[st]);
+    };
+    ring_init(ring, stages);
+    if (me == 0)
+        for (int i = 0; i < stages; i++)
+            if (blockIdx.x + i * step < groups) issue(blockIdx.x + i * step, i);
+    Vec<W, VEC> wv[NV], bv[NV];
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        const int c = me + i * tpr;
+        if (c < n) {
+            mine += VEC;
+            wv[i] = reinterpret_cast<const Vec<W, VEC>*>(w)[c];
+            if (b) bv[i] = reinterpret_cast<const Vec<W, VEC>*>(b)[c];
+        }
+    }
+    const int nw = __reduce_add_sync(FULL, mine);
+    if (me < 16) count[me] = 0.0f;
+    for (int i = me; i < 2 * 16 * R; i += tpr) (&red[0][0])[i] = make_float2(0.0f, 0.0f);
+    __syncthreads();
+    if (lane == 0) count[me >> 5] = (float)nw;
+    const float per_nw = nw ? 1.0f / (float)nw : 0.0f, per_h = 1.0f / (float)H;
+    int st = 0, done = 0;
+    uint32_t phase = 0;
+    for (long long g = blockIdx.x; g < groups; g += step, done++) {
+        ptx::wait_parity(&ring.full[st], phase, &ring.abort_flag);
+        const uint8_t* base = smem + (size_t)st * stage_bytes;
+        const int nr = (int)(rows - g * R < R ? rows - g * R : R);
+        float2* rd = red[done & 1];
+        V xv[R][NV];
+        float sw[R], qw[R];
+#pragma unroll
+        for (int k = 0; k < R; k++) {
+            sw[k] = 0.0f;
+            if (k >= nr) continue;
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const int c = me + i * tpr;
+                if (c >= n) continue;
+                xv[k][i] = reinterpret_cast<const V*>(base + (size_t)k * rb)[c];
+                if (residual) {
+                    const V rv = reinterpret_cast<const V*>(base + (size_t)(R + k) * rb)[c];
+                    float f[VEC];
+#pragma unroll
+                    for (int j = 0; j < VEC; j++) f[j] = xv[k][i].get(j) + rv.get(j);
+                    xv[k][i].set(f);
+                    reinterpret_cast<V*>(sum + (g * R + k) * H)[c] = xv[k][i];
+                }
+#pragma unroll
+                for (int j = 0; j < VEC; j++) sw[k] += xv[k][i].get(j);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < R; k++) sw[k] += __shfl_xor_sync(FULL, sw[k], o);
+#pragma unroll
+        for (int k = 0; k < R; k++) {
+            qw[k] = 0.0f;
+            sw[k] *= per_nw;                            // the warp's mean
+            if (k >= nr) continue;
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                if (me + i * tpr < n)
+#pragma unroll
+                    for (int j = 0; j < VEC; j++) {
+                        const float d = xv[k][i].get(j) - sw[k];
+                        qw[k] = fmaf(d, d, qw[k]);
+                    }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < R; k++) qw[k] += __shfl_xor_sync(FULL, qw[k], o);
+        if (lane == 0)
+#pragma unroll
+            for (int k = 0; k < R; k++) {
+                rd[(me >> 5) * R + k] = make_float2(sw[k], qw[k]);
+            }
+        __syncthreads();
+        if (me == 0 && done > 0 && g + (stages - 1) * step < groups)
+            issue(g + (stages - 1) * step, st == 0 ? stages - 1 : st - 1);      // the stage before this one
+        // every warp joins the warps' sums, an entry a lane
+        const float2 e = rd[entry];
+        const float ce = count[entry / R];
+        float sum_e = ce * e.x;
+#pragma unroll
+        for (int o = R; o < 16 * R; o <<= 1) sum_e += __shfl_xor_sync(FULL, sum_e, o);
+        const float mean_e = sum_e * per_h, d_e = e.x - mean_e;
+        float m2_e = fmaf(ce * d_e, d_e, e.y);
+#pragma unroll
+        for (int o = R; o < 16 * R; o <<= 1) m2_e += __shfl_xor_sync(FULL, m2_e, o);
+        const float rstd_e = rsqrtf(fmaf(m2_e, per_h, eps));
+#pragma unroll
+        for (int k = 0; k < R; k++) {
+            const float mean = __shfl_sync(FULL, mean_e, k), rstd = __shfl_sync(FULL, rstd_e, k);
+            if (k >= nr) continue;
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const int c = me + i * tpr;
+                if (c >= n) continue;
+                V o;
+                float f[VEC];
+#pragma unroll
+                for (int j = 0; j < VEC; j++)
+                    f[j] = fmaf((xv[k][i].get(j) - mean) * rstd, wv[i].get(j), b ? bv[i].get(j) : 0.0f);
+                o.set(f);
+                reinterpret_cast<V*>(y + (g * R + k) * H)[c] = o;
+            }
+            if (me == 0) {
+                if (mean_out) mean_out[g * R + k] = mean;
+                if (rstd_out) rstd_out[g * R + k] = rstd;
+            }
+        }
+        if (++st == stages) { st = 0; phase ^= 1u; }
+    }
+    ring_drain(ring, stages, done);
+}
+
+// Sums of 2 R values over the CTA (512 threads at most), one barrier, the same in every thread. The first
+// step hands half of the values to either half of a warp; then every warp joins the warps' sums, two
+// values a lane. red: 16 R pairs, zero where there is no warp.
+template <int R>
+__device__ __forceinline__ void cta_sums(float (&v)[2 * R], float2* red) {
+    const int lane = (int)lane_id();
+#pragma unroll
+    for (int k = 0; k < R; k++) {
+        const float mine = lane < 16 ? v[2 * k] : v[2 * k + 1], other = lane < 16 ? v[2 * k + 1] : v[2 * k];
+        v[2 * k] = mine + __shfl_xor_sync(FULL, other, 16);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < R; k++) v[2 * k] += __shfl_xor_sync(FULL, v[2 * k], o);
+    if ((lane & 15) == 0)
+#pragma unroll
+        for (int k = 0; k < R; k++) reinterpret_cast<float*>(red)[((threadIdx.x >> 5) * R + k) * 2 + (lane >> 4)] = v[2 * k];
+    __syncthreads();
+    float2 e = red[lane & (16 * R - 1)];
+#pragma unroll
+    for (int o = R; o < 16 * R; o <<= 1) {
+        e.x += __shfl_xor_sync(FULL, e.x, o);
+        e.y += __shfl_xor_sync(FULL, e.y, o);
+    }
+#pragma unroll
+    for (int k = 0; k < R; k++) {
+        v[2 * k] = __shfl_sync(FULL, e.x, k);
+        v[2 * k + 1] = __shfl_sync(FULL, e.y, k);
+    }
+}
+
+// Backward. dweight and dbias add up in the threads' registers over the CTA's rows and leave as one
+// partial sum per CTA: part [gridDim.x][2][H].
+template <typename T, typename W, int VEC, int NV, int R>
+__global__ void __launch_bounds__(512) ln_backward_ring_kernel(const T* dy, const T* s, int rows, int H,
+                                                               const W* __restrict__ w, const float* __restrict__ mean,
+                                                               const float* __restrict__ rstd, const T* add, T* dx,
+                                                               float* part, int stages) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ LnRing ring;
+    __shared__ float2 red[2][16 * R];
+    using V = Vec<T, VEC>;
+    const int tpr = blockDim.x, me = threadIdx.x, n = H / VEC;
+    const uint32_t rb = (uint32_t)(H * sizeof(T));
+    const int nt = add ? 3 : 2;
+    const uint32_t stage_bytes = nt * R * rb;
+    const long long groups = ((long long)rows + R - 1) / R, step = gridDim.x;
+    auto issue = [&](long long g, int st) {
+        uint8_t* d = smem + (size_t)st * stage_bytes;
+        const long long t = g * R;
+        const uint32_t nb = (uint32_t)(rows - t < R ? rows - t : R) * rb;
+        ptx::mbar_arrive_expect_tx(&ring.full[st], nt * nb);
+        ptx::bulk_load(d, dy + t * H, nb, &ring.full[st]);
+        ptx::bulk_load(d + R * rb, s + t * H, nb, &ring.full[st]);
+        if (add) ptx::bulk_load(d + 2 * R * rb, add + t * H, nb, &ring.full[st]);
+    };
+    for (int i = me; i < 2 * 16 * R; i += tpr) (&red[0][0])[i] = make_float2(0.0f, 0.0f);
+    ring_init(ring, stages);
+    if (me == 0)
+        for (int i = 0; i < stages; i++)
+            if (blockIdx.x + i * step < groups) issue(blockIdx.x + i * step, i);
+    Vec<W, VEC> wv[NV];
+    float dw[NV][VEC], db[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        if (me + i * tpr < n) wv[i] = reinterpret_cast<const Vec<W, VEC>*>(w)[me + i * tpr];
+#pragma unroll
+        for (int j = 0; j < VEC; j++) dw[i][j] = db[i][j] = 0.0f;
+    }
+    // the rows' statistics, one group ahead
+    const float per_h = 1.0f / (float)H;
+    float m[R], r[R], mn[R], rn[R];
+    auto stats = [&](long long g, float* a, float* c) {
+#pragma unroll
+        for (int k = 0; k < R; k++) {
+            const long long t = g * R + k < rows ? g * R + k : rows - 1;
+            a[k] = __ldg(mean + t);
+            c[k] = __ldg(rstd + t);
+        }
+    };
+    if (blockIdx.x < groups) stats(blockIdx.x, m, r);
+    int st = 0, done = 0;
+    uint32_t phase = 0;
+    for (long long g = blockIdx.x; g < groups; g += step, done++) {
+        if (g + step < groups) stats(g + step, mn, rn);
+        ptx::wait_parity(&ring.full[st], phase, &ring.abort_flag);
+        const uint8_t* base = smem + (size_t)st * stage_bytes;
+        const int nr = (int)(rows - g * R < R ? rows - g * R : R);
+        float sums[2 * R];
+#pragma unroll
+        for (int k = 0; k < R; k++) {
+            sums[2 * k] = sums[2 * k + 1] = 0.0f;
+            if (k >= nr) continue;
+            const V* gr = reinterpret_cast<const V*>(base + (size_t)k * rb);
+            const V* sr = reinterpret_cast<const V*>(base + (size_t)(R + k) * rb);
+            const float nm = -m[k] * r[k];
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const int c = me + i * tpr;
+                if (c >= n) continue;
+                const V gv = gr[c], sv = sr[c];
+#pragma unroll
+                for (int j = 0; j < VEC; j++) {
+                    const float d = gv.get(j), xh = fmaf(sv.get(j), r[k], nm), q = d * wv[i].get(j);
+                    sums[2 * k] += q;
+                    sums[2 * k + 1] = fmaf(q, xh, sums[2 * k + 1]);
+                    dw[i][j] = fmaf(d, xh, dw[i][j]);
+                    db[i][j] += d;
+                }
+            }
+        }
+        cta_sums<R>(sums, red[done & 1]);
+        if (me == 0 && done > 0 && g + (stages - 1) * step < groups)
+            issue(g + (stages - 1) * step, st == 0 ? stages - 1 : st - 1);
+#pragma unroll
+        for (int k = 0; k < R; k++) {
+            if (k >= nr) continue;
+            const V* gr = reinterpret_cast<const V*>(base + (size_t)k * rb);
+            const V* sr = reinterpret_cast<const V*>(base + (size_t)(R + k) * rb);
+            const V* ar = reinterpret_cast<const V*>(base + (size_t)(2 * R + k) * rb);
+            // r (g - a - xh c) = r w dy + ks s + k0
+            const float ks = -(sums[2 * k + 1] * per_h) * r[k] * r[k], k0 = -fmaf(ks, m[k], r[k] * (sums[2 * k] * per_h));
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const int c = me + i * tpr;
+                if (c >= n) continue;
+                const V gv = gr[c], sv = sr[c];
+                V av, o;
+                if (add) av = ar[c];
+                float f[VEC];
+#pragma unroll
+                for (int j = 0; j < VEC; j++) {
+                    f[j] = fmaf(gv.get(j), r[k] * wv[i].get(j), fmaf(sv.get(j), ks, k0));
+                    if (add) f[j] += av.get(j);
+                }
+                o.set(f);
+                reinterpret_cast<V*>(dx + (g * R + k) * H)[c] = o;
+            }
+            m[k] = mn[k];
+            r[k] = rn[k];
+        }
+        if (++st == stages) { st = 0; phase ^= 1u; }
+    }
+    pdl_trigger();
+    ring_drain(ring, stages, done);
+    if (!part) return;
+    float* out = part + (size_t)blockIdx.x * 2 * H;
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+        if (me + i * tpr < n) {
+            const int c = (me + i * tpr) * VEC;
+            Vec<float, VEC> o;
+            o.set(dw[i]);
+            *reinterpret_cast<Vec<float, VEC>*>(out + c) = o;
+            o.set(db[i]);
+            *reinterpret_cast<Vec<float, VEC>*>(out + H + c) = o;
+        }
+}
+
 // Backward for rows too long for registers: dx with the row read twice ...
 template <typename T, typename W>
 __global__ void __launch_bounds__(512) ln_backward_long_kernel(const T* dy, const T* __restrict__ s, int H,
@@ -354,6 +691,7 @@ __global__ void __launch_bounds__(256) ln_backward_long_w_kernel(const T* dy, co
 template <typename W>
 __global__ void __launch_bounds__(1024) ln_columns_kernel(const float* __restrict__ part, int n, int H, W* dw, W* db) {
     __shared__ float red[2][32][33];
+    pdl_wait();
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
     float a = 0.0f, b = 0.0f;
     if (c < H) {
@@ -387,27 +725,53 @@ int ln_sms() {
 constexpr int LN_PARTS = 1024;            // most partial sums of dweight and dbias
 
 // How a row is spread over threads: VEC elements a piece, NV pieces a thread, a warp or a CTA per
-// row. nv = 0: it does not fit in registers. wide: rows and pointers allow 16-byte pieces.
+// row. nv = 0: it does not fit. ring: it goes through shared memory. wide: rows and pointers allow
+// 16-byte pieces.
 struct LnShape {
     int nv, threads;
-    bool warp_row;
+    bool warp_row, ring;
 };
 
 LnShape ln_shape(int H, int vec, bool wide, bool forward) {
     const int n = H / vec;
-    auto cta = [&](int nv) { return LnShape{nv, (((n + nv - 1) / nv) + 31) / 32 * 32, false}; };
+    auto cta = [&](int nv, bool ring) { return LnShape{nv, (((n + nv - 1) / nv) + 31) / 32 * 32, false, ring}; };
     if (wide) {
-        if (n <= 32) return {1, 256, true};
-        if (n <= 128 && (forward || vec == 4)) return {4, 256, true};
-        if (n <= 64) return {2, 256, true};
-        if (n <= 1024) return cta(2);
-        if (n <= 2048 && (forward || vec == 4)) return cta(4);
-        return {0, 512, false};
+        if (n <= 32) return {1, 256, true, false};
+        if (n <= 128 && (forward || vec == 4)) return {4, 256, true, false};
+        if (n <= 64) return {2, 256, true, false};
+        if (n <= 1024) return cta(2, true);
+        if (n <= 2048 && (forward || vec == 4)) return cta(4, true);
+        return {0, 512, false, false};
     }
-    if (n <= 128) return {4, 256, true};
-    if (n <= 2048) return cta(4);
-    if (n <= 8192) return cta(16);
-    return {0, 512, false};
+    if (n <= 128) return {4, 256, true, false};
+    if (n <= 2048) return cta(4, false);
+    if (n <= 8192) return cta(16, false);
+    return {0, 512, false, false};
+}
+
+// Rows per group, stages and CTAs per SM of a ring kernel, row_bytes of operands per row. Two rows a
+// group where two such CTAs fit an SM (and a lone CTA cannot hide its barriers otherwise); three stages
+// where they fit, else two.
+struct LnRingShape {
+    int rows, stages, ctas;
+    size_t smem;
+};
+
+LnRingShape ln_ring(size_t row_bytes, const LnShape& l, int most_threads, bool forward) {
+    LnRingShape r;
+    r.rows = l.nv == 4 || (forward && 2 * 3 * 2 * row_bytes > LN_SMEM) || 2 * 2 * row_bytes > LN_SMEM ? 1 : 2;
+    r.stages = forward && 3 * r.rows * row_bytes <= LN_SMEM ? 3 : 2;
+    r.smem = r.stages * r.rows * row_bytes;
+    r.ctas = most_threads / l.threads;
+    if (r.ctas > (int)(LN_SMEM / (r.smem + 2048))) r.ctas = (int)(LN_SMEM / (r.smem + 2048));
+    if (r.ctas < 1) r.ctas = 1;
+    return r;
+}
+
+template <typename K>
+bool ln_allow_smem(K kernel, bool& done) {
+    if (!done) done = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LN_SMEM) == cudaSuccess;
+    return done;
 }
 
 template <typename T, typename W>
@@ -417,6 +781,24 @@ moe_status ln_forward(const void* x, const void* residual, int rows, int H, cons
     bool wide = H % VEC == 0;
     for (const void* q : {x, residual, w, b, (const void*)sum, (const void*)y}) wide = wide && moe_host::aligned(q, 16);
     const LnShape l = ln_shape(H, wide ? VEC : 1, wide, true);
+    if (l.ring) {
+        const LnRingShape r = ln_ring((size_t)(residual ? 2 : 1) * H * sizeof(T), l, 1024, true);
+        const long long groups = ((long long)rows + r.rows - 1) / r.rows, most = (long long)ln_sms() * r.ctas;
+        const int grid = (int)(groups < most ? groups : most);
+#define MOE_LN_FR(nv, R)                                                                                              \
+    {                                                                                                                 \
+        static bool allowed = false;                                                                                  \
+        auto kern = ln_forward_ring_kernel<T, W, VEC, nv, R>;                                                         \
+        if (!ln_allow_smem(kern, allowed)) return MOE_ERR_CUDA;                                                       \
+        kern<<<grid, l.threads, r.smem, s>>>((const T*)x, (const T*)residual, rows, H, (const W*)w, (const W*)b, eps, \
+                                             (T*)sum, (T*)y, mean, rstd, r.stages);                                   \
+    }
+        if (l.nv == 2 && r.rows == 2) MOE_LN_FR(2, 2)
+        else if (l.nv == 2) MOE_LN_FR(2, 1)
+        else MOE_LN_FR(4, 1)
+#undef MOE_LN_FR
+        return moe_host::launch_status();
+    }
     const long long ctas = l.warp_row ? ((long long)rows + 7) / 8 : rows;
     // as many CTAs as are resident at 2048 threads an SM: a CTA's rows share its weights
     const long long most = (long long)ln_sms() * (2048 / l.threads);
@@ -428,7 +810,6 @@ moe_status ln_forward(const void* x, const void* residual, int rows, int H, cons
         ln_forward_long_kernel<T, W><<<rows, 512, 0, s>>>((const T*)x, (const T*)residual, H, (const W*)w, (const W*)b,
                                                           eps, (T*)sum, (T*)y, mean, rstd);
     else if (wide && l.nv == 1) MOE_LN_F(VEC, 1);
-    else if (wide && l.nv == 2) MOE_LN_F(VEC, 2);
     else if (wide) MOE_LN_F(VEC, 4);
     else if (l.nv == 4) MOE_LN_F(1, 4);
     else MOE_LN_F(1, 16);
@@ -454,6 +835,25 @@ moe_status ln_backward(const void* dy, const void* sv, int rows, int H, const vo
         }
         ln_backward_long_kernel<T, W><<<rows, 512, 0, s>>>((const T*)dy, (const T*)sv, H, (const W*)w, mean, rstd,
                                                            (const T*)add, (T*)dx);
+    } else if (l.ring) {
+        const LnRingShape r = ln_ring((size_t)(add ? 3 : 2) * H * sizeof(T), l, 512, false);
+        if (r.smem > LN_SMEM) return MOE_ERR_UNSUPPORTED;
+        const long long groups = ((long long)rows + r.rows - 1) / r.rows, most = (long long)ln_sms() * r.ctas;
+        n_part = (int)(groups < most ? groups : most);
+        if (n_part > LN_PARTS) n_part = LN_PARTS;
+#define MOE_LN_BR(nv, R)                                                                                            \
+    {                                                                                                               \
+        static bool allowed = false;                                                                                \
+        auto kern = ln_backward_ring_kernel<T, W, VEC, nv, R>;                                                      \
+        if (!ln_allow_smem(kern, allowed)) return MOE_ERR_CUDA;                                                     \
+        kern<<<n_part, l.threads, r.smem, s>>>((const T*)dy, (const T*)sv, rows, H, (const W*)w, mean, rstd,        \
+                                               (const T*)add, (T*)dx, sums ? part : nullptr, r.stages);             \
+    }
+        if (l.nv == 4) {
+            if constexpr (VEC == 4) MOE_LN_BR(4, 1)
+        } else if (r.rows == 2) MOE_LN_BR(2, 2)
+        else MOE_LN_BR(2, 1)
+#undef MOE_LN_BR
     } else {
         const long long ctas = l.warp_row ? ((long long)rows + 7) / 8 : rows;
         long long most = (long long)ln_sms() * (512 / l.threads > 1 ? 512 / l.threads : 1);
@@ -467,12 +867,14 @@ moe_status ln_backward(const void* dy, const void* sv, int rows, int H, const vo
         if (wide && l.nv == 1) MOE_LN_B(VEC, 1, true);
         else if (wide && l.nv == 2) MOE_LN_B(VEC, 2, true);
         else if (wide) {
-            if constexpr (VEC == 4) MOE_LN_B(VEC, 4, false);
+            if constexpr (VEC == 4) MOE_LN_B(VEC, 4, false);      // (bf16 rows of this length take the ring)
         } else if (l.nv == 4) MOE_LN_B(1, 4, true);
         else MOE_LN_B(1, 16, false);
 #undef MOE_LN_B
     }
-    if (sums) ln_columns_kernel<W><<<(H + 31) / 32, 1024, 0, s>>>(part, n_part, H, (W*)dw, (W*)db);
+    if (sums && moe_host::launch_pdl(ln_columns_kernel<W>, dim3((H + 31) / 32), dim3(1024), 0, s, (const float*)part, n_part,
+                                     H, (W*)dw, (W*)db) != cudaSuccess)
+        return MOE_ERR_CUDA;
     return moe_host::launch_status();
 }
 
