@@ -14,7 +14,7 @@ namespace moe {
 namespace {
 
 constexpr int LN_HMAX = 65536;
-constexpr int LN_STAGES = 4;              // most ring stages of the kernels that go through shared memory
+constexpr int LN_STAGES = 6;              // most ring stages of the kernels that go through shared memory
 constexpr size_t LN_SMEM = 220 * 1024;    // their dynamic shared memory at most
 
 template <typename T> __device__ __forceinline__ float to_f(T v);
@@ -486,11 +486,11 @@ __global__ void __launch_bounds__(512, NV == 2 && R == 1 ? 2 : 1) ln_forward_rin
     ring_drain(ring, stages, done);
 }
 
-// Sums of 2 R values over the CTA (512 threads at most), one barrier, the same in every thread. The first
+// Sums of 2 R values over the first `threads` (512 at most) threads of the CTA, one barrier, the same in each. The first
 // step hands half of the values to either half of a warp; then every warp joins the warps' sums, two
 // values a lane. red: 16 R pairs, zero where there is no warp.
 template <int R>
-__device__ __forceinline__ void cta_sums(float (&v)[2 * R], float2* red) {
+__device__ __forceinline__ void cta_sums(float (&v)[2 * R], float2* red, int threads) {
     const int lane = (int)lane_id();
 #pragma unroll
     for (int k = 0; k < R; k++) {
@@ -504,7 +504,7 @@ __device__ __forceinline__ void cta_sums(float (&v)[2 * R], float2* red) {
     if ((lane & 15) == 0)
 #pragma unroll
         for (int k = 0; k < R; k++) reinterpret_cast<float*>(red)[((threadIdx.x >> 5) * R + k) * 2 + (lane >> 4)] = v[2 * k];
-    __syncthreads();
+    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
     float2 e = red[lane & (16 * R - 1)];
 #pragma unroll
     for (int o = R; o < 16 * R; o <<= 1) {
@@ -518,36 +518,62 @@ __device__ __forceinline__ void cta_sums(float (&v)[2 * R], float2* red) {
     }
 }
 
-// Backward. dweight and dbias add up in the threads' registers over the CTA's rows and leave as one
-// partial sum per CTA: part [gridDim.x][2][H].
+// Backward. A warp of its own fills the ring, a stage per row, as soon as the computing warps have let go of
+// the row that was there; those take R rows at a time. dweight and dbias add up in the threads' registers
+// over the CTA's rows and leave as one partial sum per CTA: part [gridDim.x][2][H].
 template <typename T, typename W, int VEC, int NV, int R>
-__global__ void __launch_bounds__(512) ln_backward_ring_kernel(const T* dy, const T* s, int rows, int H,
+__global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, const T* s, int rows, int H,
                                                                const W* __restrict__ w, const float* __restrict__ mean,
                                                                const float* __restrict__ rstd, const T* add, T* dx,
                                                                float* part, int stages) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ LnRing ring;
+    __shared__ uint64_t full[LN_STAGES], empty[LN_STAGES];
+    __shared__ uint32_t abort_flag;
     __shared__ float2 red[2][16 * R];
     using V = Vec<T, VEC>;
-    const int tpr = blockDim.x, me = threadIdx.x, n = H / VEC;
+    const int tpr = blockDim.x - 32, me = threadIdx.x, n = H / VEC;
     const uint32_t rb = (uint32_t)(H * sizeof(T));
     const int nt = add ? 3 : 2;
-    const uint32_t stage_bytes = nt * R * rb;
+    const uint32_t stage_bytes = nt * rb;
     const long long groups = ((long long)rows + R - 1) / R, step = gridDim.x;
-    auto issue = [&](long long g, int st) {
-        uint8_t* d = smem + (size_t)st * stage_bytes;
-        const long long t = g * R;
-        const uint32_t nb = (uint32_t)(rows - t < R ? rows - t : R) * rb;
-        ptx::mbar_arrive_expect_tx(&ring.full[st], nt * nb);
-        ptx::bulk_load(d, dy + t * H, nb, &ring.full[st]);
-        ptx::bulk_load(d + R * rb, s + t * H, nb, &ring.full[st]);
-        if (add) ptx::bulk_load(d + 2 * R * rb, add + t * H, nb, &ring.full[st]);
-    };
-    for (int i = me; i < 2 * 16 * R; i += tpr) (&red[0][0])[i] = make_float2(0.0f, 0.0f);
-    ring_init(ring, stages);
-    if (me == 0)
-        for (int i = 0; i < stages; i++)
-            if (blockIdx.x + i * step < groups) issue(blockIdx.x + i * step, i);
+    for (int i = me; i < 2 * 16 * R; i += blockDim.x) (&red[0][0])[i] = make_float2(0.0f, 0.0f);
+    if (me == 0) {
+        for (int i = 0; i < stages; i++) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], tpr >> 5);
+        }
+        abort_flag = 0u;
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    int st = 0;
+    uint32_t phase = 0;
+    if (me >= tpr) {
+        if (me == tpr) {
+            int issued = 0;
+            bool ok = true;
+            for (long long g = blockIdx.x; g < groups && ok; g += step)
+                for (long long t = g * R; t < rows && t < (g + 1) * R; t++) {
+                    ok = ptx::wait_parity(&empty[st], phase ^ 1u, &abort_flag);
+                    if (!ok) break;
+                    uint8_t* d = smem + (size_t)st * stage_bytes;
+                    ptx::mbar_arrive_expect_tx(&full[st], stage_bytes);
+                    ptx::bulk_load(d, dy + t * H, rb, &full[st]);
+                    ptx::bulk_load(d + rb, s + t * H, rb, &full[st]);
+                    if (add) ptx::bulk_load(d + 2 * rb, add + t * H, rb, &full[st]);
+                    issued++;
+                    if (++st == stages) { st = 0; phase ^= 1u; }
+                }
+            if (!ok) {       // the copies in flight get a bounded chance to land
+                for (int i = 0; i < stages && i < issued; i++) {
+                    if (--st < 0) { st = stages - 1; phase ^= 1u; }
+                    volatile uint32_t never = 0u;
+                    ptx::wait_parity(&full[st], phase, &never, 100000000ull);
+                }
+            }
+        }
+        return;
+    }
     Vec<W, VEC> wv[NV];
     float dw[NV][VEC], db[NV][VEC];
 #pragma unroll
@@ -568,20 +594,21 @@ __global__ void __launch_bounds__(512) ln_backward_ring_kernel(const T* dy, cons
         }
     };
     if (blockIdx.x < groups) stats(blockIdx.x, m, r);
-    int st = 0, done = 0;
-    uint32_t phase = 0;
-    for (long long g = blockIdx.x; g < groups; g += step, done++) {
+    int buf = 0;
+    for (long long g = blockIdx.x; g < groups; g += step, buf ^= 1) {
         if (g + step < groups) stats(g + step, mn, rn);
-        ptx::wait_parity(&ring.full[st], phase, &ring.abort_flag);
-        const uint8_t* base = smem + (size_t)st * stage_bytes;
         const int nr = (int)(rows - g * R < R ? rows - g * R : R);
         float sums[2 * R];
+        int at[R];
 #pragma unroll
         for (int k = 0; k < R; k++) {
             sums[2 * k] = sums[2 * k + 1] = 0.0f;
+            at[k] = st;
             if (k >= nr) continue;
-            const V* gr = reinterpret_cast<const V*>(base + (size_t)k * rb);
-            const V* sr = reinterpret_cast<const V*>(base + (size_t)(R + k) * rb);
+            ptx::wait_parity(&full[st], phase, &abort_flag);
+            if (++st == stages) { st = 0; phase ^= 1u; }
+            const V* gr = reinterpret_cast<const V*>(smem + (size_t)at[k] * stage_bytes);
+            const V* sr = reinterpret_cast<const V*>(smem + (size_t)at[k] * stage_bytes + rb);
             const float nm = -m[k] * r[k];
 #pragma unroll
             for (int i = 0; i < NV; i++) {
@@ -598,15 +625,13 @@ __global__ void __launch_bounds__(512) ln_backward_ring_kernel(const T* dy, cons
                 }
             }
         }
-        cta_sums<R>(sums, red[done & 1]);
-        if (me == 0 && done > 0 && g + (stages - 1) * step < groups)
-            issue(g + (stages - 1) * step, st == 0 ? stages - 1 : st - 1);
+        cta_sums<R>(sums, red[buf], tpr);
 #pragma unroll
         for (int k = 0; k < R; k++) {
             if (k >= nr) continue;
-            const V* gr = reinterpret_cast<const V*>(base + (size_t)k * rb);
-            const V* sr = reinterpret_cast<const V*>(base + (size_t)(R + k) * rb);
-            const V* ar = reinterpret_cast<const V*>(base + (size_t)(2 * R + k) * rb);
+            const V* gr = reinterpret_cast<const V*>(smem + (size_t)at[k] * stage_bytes);
+            const V* sr = reinterpret_cast<const V*>(smem + (size_t)at[k] * stage_bytes + rb);
+            const V* ar = reinterpret_cast<const V*>(smem + (size_t)at[k] * stage_bytes + 2 * rb);
             // r (g - a - xh c) = r w dy + ks s + k0
             const float ks = -(sums[2 * k + 1] * per_h) * r[k] * r[k], k0 = -fmaf(ks, m[k], r[k] * (sums[2 * k] * per_h));
 #pragma unroll
@@ -625,13 +650,13 @@ __global__ void __launch_bounds__(512) ln_backward_ring_kernel(const T* dy, cons
                 o.set(f);
                 reinterpret_cast<V*>(dx + (g * R + k) * H)[c] = o;
             }
+            __syncwarp();
+            if (lane_id() == 0) ptx::mbar_arrive(&empty[at[k]]);
             m[k] = mn[k];
             r[k] = rn[k];
         }
-        if (++st == stages) { st = 0; phase ^= 1u; }
     }
     pdl_trigger();
-    ring_drain(ring, stages, done);
     if (!part) return;
     float* out = part + (size_t)blockIdx.x * 2 * H;
 #pragma unroll
@@ -749,22 +774,33 @@ LnShape ln_shape(int H, int vec, bool wide, bool forward) {
     return {0, 512, false, false};
 }
 
-// Rows per group, stages and CTAs per SM of a ring kernel, row_bytes of operands per row. Two rows a
-// group where two such CTAs fit an SM (and a lone CTA cannot hide its barriers otherwise); three stages
-// where they fit, else two.
+// Rows per group, ring stages and CTAs per SM of the ring kernels, row_bytes of operands per row.
 struct LnRingShape {
     int rows, stages, ctas;
     size_t smem;
 };
 
-LnRingShape ln_ring(size_t row_bytes, const LnShape& l, int most_threads, bool forward) {
+// Forward: a stage is a group of two rows where two CTAs of three such stages fit an SM, else one row.
+LnRingShape ln_forward_ring(size_t row_bytes, const LnShape& l) {
     LnRingShape r;
-    r.rows = l.nv == 4 || (forward && 2 * 3 * 2 * row_bytes > LN_SMEM) || 2 * 2 * row_bytes > LN_SMEM ? 1 : 2;
-    r.stages = forward && 3 * r.rows * row_bytes <= LN_SMEM ? 3 : 2;
+    r.rows = l.nv == 4 || 2 * 3 * 2 * row_bytes > LN_SMEM ? 1 : 2;
+    r.stages = 3 * r.rows * row_bytes <= LN_SMEM ? 3 : 2;
     r.smem = r.stages * r.rows * row_bytes;
-    r.ctas = most_threads / l.threads;
-    if (r.ctas > (int)(LN_SMEM / (r.smem + 2048))) r.ctas = (int)(LN_SMEM / (r.smem + 2048));
-    if (r.ctas < 1) r.ctas = 1;
+    const int fit = (int)(LN_SMEM / (r.smem + 2048)), most = 1024 / l.threads;
+    r.ctas = fit < most ? (fit < 1 ? 1 : fit) : most;
+    return r;
+}
+
+// Backward: a stage is a row; two rows a group where three fit (long fp32 rows go singly).
+LnRingShape ln_backward_ring(size_t row_bytes, const LnShape& l) {
+    LnRingShape r;
+    const int most = l.threads > 256 ? 1 : 512 / l.threads;     // (128 registers a thread)
+    r.ctas = most;
+    while (r.ctas > 1 && r.ctas * (4 * row_bytes + 2048) > LN_SMEM) r.ctas--;
+    r.stages = (int)((LN_SMEM / r.ctas - 2048) / row_bytes);
+    if (r.stages > LN_STAGES) r.stages = LN_STAGES;
+    r.rows = l.nv == 4 || r.stages < 3 ? 1 : 2;
+    r.smem = r.stages * row_bytes;
     return r;
 }
 
@@ -782,7 +818,7 @@ moe_status ln_forward(const void* x, const void* residual, int rows, int H, cons
     for (const void* q : {x, residual, w, b, (const void*)sum, (const void*)y}) wide = wide && moe_host::aligned(q, 16);
     const LnShape l = ln_shape(H, wide ? VEC : 1, wide, true);
     if (l.ring) {
-        const LnRingShape r = ln_ring((size_t)(residual ? 2 : 1) * H * sizeof(T), l, 1024, true);
+        const LnRingShape r = ln_forward_ring((size_t)(residual ? 2 : 1) * H * sizeof(T), l);
         const long long groups = ((long long)rows + r.rows - 1) / r.rows, most = (long long)ln_sms() * r.ctas;
         const int grid = (int)(groups < most ? groups : most);
 #define MOE_LN_FR(nv, R)                                                                                              \
@@ -836,8 +872,7 @@ moe_status ln_backward(const void* dy, const void* sv, int rows, int H, const vo
         ln_backward_long_kernel<T, W><<<rows, 512, 0, s>>>((const T*)dy, (const T*)sv, H, (const W*)w, mean, rstd,
                                                            (const T*)add, (T*)dx);
     } else if (l.ring) {
-        const LnRingShape r = ln_ring((size_t)(add ? 3 : 2) * H * sizeof(T), l, 512, false);
-        if (r.smem > LN_SMEM) return MOE_ERR_UNSUPPORTED;
+        const LnRingShape r = ln_backward_ring((size_t)(add ? 3 : 2) * H * sizeof(T), l);
         const long long groups = ((long long)rows + r.rows - 1) / r.rows, most = (long long)ln_sms() * r.ctas;
         n_part = (int)(groups < most ? groups : most);
         if (n_part > LN_PARTS) n_part = LN_PARTS;
@@ -846,7 +881,7 @@ moe_status ln_backward(const void* dy, const void* sv, int rows, int H, const vo
         static bool allowed = false;                                                                                \
         auto kern = ln_backward_ring_kernel<T, W, VEC, nv, R>;                                                      \
         if (!ln_allow_smem(kern, allowed)) return MOE_ERR_CUDA;                                                     \
-        kern<<<n_part, l.threads, r.smem, s>>>((const T*)dy, (const T*)sv, rows, H, (const W*)w, mean, rstd,        \
+        kern<<<n_part, l.threads + 32, r.smem, s>>>((const T*)dy, (const T*)sv, rows, H, (const W*)w, mean, rstd,        \
                                                (const T*)add, (T*)dx, sums ? part : nullptr, r.stages);             \
     }
         if (l.nv == 4) {
