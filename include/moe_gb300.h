@@ -580,8 +580,8 @@ moe_status moe_layer_norm_backward(const void *dy, const void *s, int T, int H, 
  * MOE_F32. outs NULL: only the norm. outs[i] may be grads[i] (in place: with c = 1 nothing
  * is written) and has the type of grads[i]. *norm_out (device fp32). A NaN in a gradient
  * makes norm and every output NaN; an infinite norm gives c = 0 (0 * inf is NaN). Squares
- * are summed in fp32 per thread (values above about 1e19 overflow to an infinite norm) and
- * joined in double in a fixed order. The host never reads the norm. Requires n >= 0,
+ * are summed in fp32 (values above about 1e19 overflow to an infinite norm) in an order that
+ * depends on the sizes and the device only. The host never reads the norm. Requires n >= 0,
  * max_norm >= 0, eps >= 0 (not NaN). workspace: moe_grad_norm_workspace_size(n) bytes,
  * 16-byte aligned, not initialised. The host arrays are read during the call only.
  * ------------------------------------------------------------------------ */

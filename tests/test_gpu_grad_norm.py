@@ -1,7 +1,7 @@
 """Global gradient norm and clipping against a plain 64-bit implementation, through the C ABI.
 
 Bars, u = 2^-24: a thread adds at most n squares in fp32, so the norm errs by less than (n / 2 + 8) u of
-itself; n <= 2^11 holds for every size here (the rest is joined in double): 2^-14. Outputs: the scale's
+itself; n <= 2^11 holds for every size here (the rest is a tree): 2^-14. Outputs: the scale's
 error, and half a unit of the last place (2^-8 of a bf16 value, u of an fp32 one)."""
 import pytest
 import torch
