@@ -30,6 +30,7 @@ class MoELayer:
         self._w = (w1, w3, w2)
         self._slice_layers = None
         self._slots = None
+        self._few_workspace = None  # forward_few's, made at its first call
         self.host_event = None      # set by forward_host: y_host holds the result once it completes
         self.E, self.H, self.F, self.T, self.K = E, H, F, T, K
         self.precision = precision
@@ -178,6 +179,26 @@ class MoELayer:
         self.stage_gemm_down(stream)
         self.stage_combine(stream)
         return self.y
+
+    def forward_few(self, x: torch.Tensor, logits: torch.Tensor, stream=None) -> torch.Tensor:
+        """The layer for a few tokens (a decoding step): x [t, H] bf16 and logits [t, E] fp32 with
+        t <= 64 (and t * K <= 4096), whatever the layer's T -> y [t, H] bf16, a new tensor. The same
+        packed weights and router as ``forward``; its buffers are not touched. Calls on one layer share
+        a workspace and must not overlap on the GPU. The expert outputs are not rounded to bf16 before the combine, so y may differ from ``forward``'s in its last bit."""
+        if self.nv4:
+            raise ValueError("the few-token path wants bf16 or MXFP8 weights")
+        w, K = self.weights, self.K
+        if self._few_workspace is None:
+            self._few_workspace = api.moe_layer_few_tokens_workspace(w, min(64, 4096 // K), K)
+        if self.score == "sigmoid":
+            ids, probs = api.moe_route_sigmoid_topk(logits, K, expert_bias=self.expert_bias, renorm=self.renorm,
+                                                    id_dtype=self.ids.dtype, stream=stream)
+            y, _, _ = api.moe_layer_few_tokens(x, None, w, K, ids=ids, probs=probs, workspace=self._few_workspace,
+                                               stream=stream)
+        else:
+            y, _, _ = api.moe_layer_few_tokens(x, logits, w, K, renorm=self.renorm, id_dtype=self.ids.dtype,
+                                               workspace=self._few_workspace, stream=stream)
+        return y
 
     # ------------------------------------------------------------ backward
     # library launches of the expert-MLP backward: dgrad 1, dx 1, transposes 4, wgrad 2 (+ dy's
