@@ -1,4 +1,5 @@
-// few_tokens.cu -- the whole MoE layer for a few tokens (a decoding step): moe_layer_few_tokens.
+// few_tokens.cu -- the whole MoE layer for a few tokens (a decoding step): moe_layer_few_tokens. Three
+// kernels: routing (and x's quantisation), up projection, down projection and combine.
 //
 // For every valid route (t, k) with expert e = ids[t,k]:
 //   h = silu(x[t] W1[e]) * (x[t] W3[e]);   y[t] = bf16( sum_k p[t,k] (h W2[e]) )
@@ -35,11 +36,10 @@ constexpr int PREP_CAND = 256;
 constexpr int PREP_QUANT = PREP_THREADS * 8;
 
 struct PrepSmem {
-    unsigned key[PREP_THREADS];
-    unsigned list_key[PREP_CAND];
-    int list_idx[PREP_CAND];
+    uint4 key[PREP_THREADS / 4];            // each thread's largest key
+    unsigned long long list[PREP_CAND];     // key, then the complement of the expert's index
     unsigned bound;
-    unsigned cnt[2][3];
+    unsigned cnt[2];
     float red[2][PREP_WARPS];
     int n;
 };
@@ -52,6 +52,10 @@ __device__ __forceinline__ unsigned order_key(float f) {
 }
 __device__ __forceinline__ float key_value(unsigned k) {
     return (k & 0x80000000u) ? __uint_as_float(k & 0x7fffffffu) : __uint_as_float(~k);
+}
+
+__device__ __forceinline__ unsigned long long list_entry(unsigned key, int e) {
+    return ((unsigned long long)key << 32) | (unsigned)~e;
 }
 
 template <bool MAX>
@@ -83,71 +87,52 @@ struct PrepArgs {
 };
 
 // The K largest keys of the row (lower index first among equals) into the list, whatever the ties.
-template <int V>
-__device__ __noinline__ void prep_exact(const PrepArgs& p, const unsigned (&key)[V], PrepSmem& sm) {
+__device__ __noinline__ void prep_exact(const float* row, int E, int K, PrepSmem& sm) {
     const int tid = threadIdx.x, lane = tid & 31;
+    // (few rows come here: the keys are made anew in each step)
+    auto count = [&](unsigned* to, auto pred) {
+        unsigned c = 0u;
+        for (int e = tid; e < E; e += PREP_THREADS) c += pred(order_key(__ldg(row + e)), e);
+        c = __reduce_add_sync(FULL, c);
+        if (lane == 0 && c) atomicAdd(to, c);
+    };
     __syncthreads();                  // (every thread has read the list's length)
-    if (tid < 6) sm.cnt[tid / 3][tid % 3] = 0u;
+    if (tid < 2) sm.cnt[tid] = 0u;
     if (tid == 0) sm.n = 0;
     __syncthreads();
     // the largest bound with at least K keys at or above it: the K-th largest key
     unsigned kth = 0u;
-    for (int sh = 30, step = 0; sh >= 0; sh -= 2, step ^= 1) {
-        unsigned c[3] = {0u, 0u, 0u};
-#pragma unroll
-        for (int i = 0; i < V; i++)
-#pragma unroll
-            for (int j = 0; j < 3; j++) c[j] += key[i] >= kth + ((unsigned)(j + 1) << sh);
-#pragma unroll
-        for (int j = 0; j < 3; j++) {
-            c[j] = __reduce_add_sync(FULL, c[j]);
-            if (lane == 0 && c[j]) atomicAdd(&sm.cnt[step][j], c[j]);
-        }
+    int step = 0;
+    for (int sh = 31; sh >= 0; sh--, step ^= 1) {
+        const unsigned bound = kth | (1u << sh);
+        count(&sm.cnt[step], [&](unsigned k, int) { return k >= bound; });
         __syncthreads();
-        unsigned d = 0u;
-#pragma unroll
-        for (int j = 0; j < 3; j++) d += sm.cnt[step][j] >= (unsigned)p.K;
-        kth += d << sh;
-        if (tid < 3) sm.cnt[step ^ 1][tid] = 0u;
+        if (sm.cnt[step] >= (unsigned)K) kth = bound;
+        if (tid == 0) sm.cnt[step ^ 1] = 0u;
         __syncthreads();
     }
-    // how many of the keys equal to it belong to the K largest
-    {
-        unsigned c = 0u;
-#pragma unroll
-        for (int i = 0; i < V; i++) c += key[i] > kth;
-        c = __reduce_add_sync(FULL, c);
-        if (lane == 0 && c) atomicAdd(&sm.cnt[0][0], c);   // (cleared by the search's last step)
-        if (tid == 0) sm.cnt[1][1] = 0u;
-        __syncthreads();
-    }
-    const unsigned ties = (unsigned)p.K - sm.cnt[0][0];
-    // those with the lowest expert indices: the index bound by bisection
-    int lo = 0, hi = p.E - 1;         // smallest b with at least `ties` equal keys at indices <= b
-    int step = 1;
+    // how many of the keys equal to it belong to the K largest: those with the lowest expert
+    // indices, the index bound by bisection
+    count(&sm.cnt[step], [&](unsigned k, int) { return k > kth; });
+    __syncthreads();
+    const unsigned ties = (unsigned)K - sm.cnt[step];
+    int lo = 0, hi = E - 1;           // smallest b with at least `ties` equal keys at indices <= b
     while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (tid == 0) sm.cnt[step ^ 1][1] = 0u;
-        unsigned c = 0u;
-#pragma unroll
-        for (int i = 0; i < V; i++) c += key[i] == kth && i * PREP_THREADS + tid <= mid;
-        c = __reduce_add_sync(FULL, c);
-        if (lane == 0 && c) atomicAdd(&sm.cnt[step][1], c);
-        __syncthreads();
-        if (sm.cnt[step][1] >= ties) hi = mid;
-        else lo = mid + 1;
         step ^= 1;
         __syncthreads();
+        if (tid == 0) sm.cnt[step] = 0u;
+        __syncthreads();
+        const int mid = (lo + hi) >> 1;
+        count(&sm.cnt[step], [&](unsigned k, int e) { return k == kth && e <= mid; });
+        __syncthreads();
+        if (sm.cnt[step] >= ties) hi = mid;
+        else lo = mid + 1;
     }
-#pragma unroll
-    for (int i = 0; i < V; i++) {
-        const int e = i * PREP_THREADS + tid;
-        if (e < p.E && (key[i] > kth || (key[i] == kth && e <= lo))) {
+    for (int e = tid; e < E; e += PREP_THREADS) {
+        const unsigned k = order_key(__ldg(row + e));
+        if (k > kth || (k == kth && e <= lo)) {
             const int pos = atomicAdd(&sm.n, 1);
-            if (pos < PREP_CAND) {        // (NaN logits aside, exactly K keys come here)
-                sm.list_key[pos] = key[i];
-                sm.list_idx[pos] = e;
-            }
+            if (pos < PREP_CAND) sm.list[pos] = list_entry(k, e);     // (NaN logits aside, exactly K come here)
         }
     }
     __syncthreads();
@@ -185,52 +170,50 @@ __device__ void prep_route(const PrepArgs& p, int t, PrepSmem& sm) {
     unsigned top = key[0];
 #pragma unroll
     for (int i = 1; i < V; i++) top = max(top, key[i]);
-    sm.key[tid] = top;
+    reinterpret_cast<unsigned*>(sm.key)[tid] = top;
     __syncthreads();
-    int r = 0;
-    const int others = min(p.E, PREP_THREADS);
-#pragma unroll 8
-    for (int j = 0; j < others; j++) r += (sm.key[j] > top) || (sm.key[j] == top && j < tid);
-    int n = p.K;              // length of the list
-    if (V == 1) {
-        if (tid < p.E && r < p.K) {
-            sm.list_key[r] = top;
-            sm.list_idx[r] = tid;
+    int above = 0, equal = 0;             // V = 1: equal keys before this one; else all of them
+#pragma unroll 4
+    for (int j = 0; j < (min(p.E, PREP_THREADS) + 3) / 4; j++) {      // (keys past E are 0, below all)
+        const uint4 q = sm.key[j];
+        const unsigned k[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            above += k[u] > top;
+            equal += k[u] == top && (V > 1 || 4 * j + u < tid);
         }
-        __syncthreads();
-    } else {
-        if (r == p.K - 1) sm.bound = top;
+    }
+    int n = p.K;              // length of the list
+    int rank = above + equal;
+    unsigned long long mine = list_entry(top, tid);
+    bool chosen = V == 1 && tid < p.E && rank < p.K;
+    if (V > 1) {
+        if (above < p.K && p.K <= above + equal) sm.bound = top;      // (the same from every such thread)
         __syncthreads();
         const unsigned bound = sm.bound;
 #pragma unroll
         for (int i = 0; i < V; i++)
             if (key[i] >= bound && i * PREP_THREADS + tid < p.E) {
                 const int pos = atomicAdd(&sm.n, 1);
-                if (pos < PREP_CAND) {
-                    sm.list_key[pos] = key[i];
-                    sm.list_idx[pos] = i * PREP_THREADS + tid;
-                }
+                if (pos < PREP_CAND) sm.list[pos] = list_entry(key[i], i * PREP_THREADS + tid);
             }
         __syncthreads();
         n = sm.n;
         if (n > PREP_CAND) {
-            prep_exact<V>(p, key, sm);
+            prep_exact(row, p.E, p.K, sm);
             n = p.K;
         }
-    }
-    // ranks within the list; the first K are the selection
-    int rank = tid, e = 0;
-    unsigned k = 0u;
-    if (tid < n) {
-        k = sm.list_key[tid];
-        e = sm.list_idx[tid];
-        if (V > 1) {
+        // ranks within the list; the first K are the selection
+        if (tid < n) {
+            mine = sm.list[tid];
             rank = 0;
-#pragma unroll 4
-            for (int i = 0; i < n; i++) rank += sm.list_key[i] > k || (sm.list_key[i] == k && sm.list_idx[i] < e);
+#pragma unroll 8
+            for (int i = 0; i < n; i++) rank += sm.list[i] > mine;
+            chosen = rank < p.K;
         }
     }
-    const bool chosen = tid < n && rank < p.K;
+    const unsigned k = (unsigned)(mine >> 32);
+    const int e = (int)~(unsigned)mine;
     const float num = chosen ? expf(key_value(k) - m) : 0.0f;
     if (p.renorm) den = prep_reduce<false>(num, sm.red[1]);
     if (chosen) {
@@ -244,6 +227,7 @@ __device__ void prep_route(const PrepArgs& p, int t, PrepSmem& sm) {
 template <int V>
 __global__ void __launch_bounds__(PREP_THREADS) few_prep_kernel(PrepArgs p) {
     __shared__ PrepSmem sm;
+    pdl_trigger();            // the second kernel sets up meanwhile
     const int t = blockIdx.x;
     if (t < p.T) {
         if (t == 0)
@@ -265,11 +249,12 @@ __global__ void __launch_bounds__(PREP_THREADS) few_prep_kernel(PrepArgs p) {
 }
 
 // ---------------------------------------------------------------------------
-// Second kernel: the expert MLP and the combine, one persistent CTA per SM.
+// The expert MLP and the combine: two kernels, one persistent CTA per SM each.
 //
 // Every weight row is streamed once, as the A operand (128 rows) of tcgen05.mma; the few tokens
 // are the B operand, so a tile's accumulator is [128 weight rows][tokens] in TMEM. The weights'
-// bytes bound the kernel: a producer warp keeps up to FEW_STAGES 16 KB weight tiles in flight per SM.
+// bytes bound the kernels: a producer warp keeps a ring of up to FEW_STAGES stages of two 16 KB weight
+// tiles in flight per SM.
 //
 // Up: a tile is 64 columns of W1 and the same 64 of W3 of one expert, over all of H; the tokens
 //   operand is all of x (T rows, zero rows past them), the chosen tokens' columns are read. h goes
@@ -279,8 +264,10 @@ __global__ void __launch_bounds__(PREP_THREADS) few_prep_kernel(PrepArgs p) {
 //   still use every SM; a CTA adds p * (its piece of h W2) up over its experts in shared memory. The
 //   CTAs that share an output tile leave partial sums, and the last to arrive adds them, in the
 //   order of the CTAs: the result does not depend on who is last.
-// Between the two every CTA waits for all of h (a counter, bounded); the first down tiles of weights are
-// already on their way then, as they depend on the routing alone.
+// The down kernel is launched while the up kernel runs: its CTAs start as SMs fall free, make the
+// plan and fill their rings with weights, which depend on the routing alone, and only then wait for h. (One
+// kernel with a barrier between the two halves was slower: it has to be launched cooperatively, which
+// alone took 3 us longer.)
 //
 // Warps: 0 TMA producer, 1 TMEM and MMA issue, 2-5 epilogue (one TMEM lane quarter each), 6 (MXFP8)
 // the scales: loads a group of 16 k-blocks' scale bytes and rearranges them for tcgen05.cp.
@@ -307,7 +294,7 @@ struct FewArgs {
     void* h;                  // [T K, F] bf16 or E4M3
     uint8_t* hs;              // MXFP8: [T K, F / 32]
     float* part;              // [2 gridDim.x][T][128] partial sums of shared output tiles
-    unsigned* count;          // [0] CTAs whose h is written, [1 + r] arrivals at output tile r; zeroed before
+    unsigned* count;          // arrivals at each output tile; zeroed before
     __nv_bfloat16* y;
 };
 
@@ -346,7 +333,6 @@ struct FewPlan {
 
 // A run of k-blocks of one tile: the unit that all warps walk in the same order.
 struct FewRun {
-    int phase;                // 0 up, 1 down
     int a;                    // index among the chosen experts
     int tile;                 // up: 64-column tile of F; down: 128-column tile of H
     int kb0, nkb;
@@ -354,23 +340,34 @@ struct FewRun {
     int brow, bn;             // tokens operand: first row, rows loaded
 };
 
-template <bool FP8>
+template <bool FP8, bool DOWN>
 struct FewWalk {
     const FewArgs& p;
     const FewPlan& pl;
-    int u, w, w1;
+    int at, end;              // up: tiles, gridDim.x apart; down: k-blocks
     __device__ FewWalk(const FewArgs& p_, const FewPlan& pl_) : p(p_), pl(pl_) {
-        u = blockIdx.x;
-        w = pl.begin_of(blockIdx.x);
-        w1 = pl.begin_of(blockIdx.x + 1);
+        at = DOWN ? pl.begin_of(blockIdx.x) : (int)blockIdx.x;
+        end = DOWN ? pl.begin_of(blockIdx.x + 1) : pl.A * (p.F / 64);
     }
     __device__ bool next(FewRun& r) {
         constexpr int BK = FP8 ? 128 : 64;
-        const int ft = p.F / 64;
-        if (u < pl.A * ft) {
-            r.phase = 0;
-            r.a = u / ft;
-            r.tile = u - r.a * ft;
+        if (at >= end) return false;
+        if constexpr (DOWN) {
+            const int kbs = p.F / BK;
+            const int q = at / kbs;
+            r.tile = q / pl.A;
+            r.a = q - r.tile * pl.A;
+            r.kb0 = at - q * kbs;
+            r.nkb = min(kbs - r.kb0, end - at);
+            r.row0 = pl.e[r.a] * p.H + r.tile * 128;
+            r.row1 = r.row0 + 64;
+            r.brow = pl.off[r.a];
+            r.bn = (pl.off[r.a + 1] - r.brow + 15) & ~15;
+            at += r.nkb;
+        } else {
+            const int ft = p.F / 64;
+            r.a = at / ft;
+            r.tile = at - r.a * ft;
             r.kb0 = 0;
             r.nkb = p.H / BK;
             const int c = r.tile * 64;
@@ -378,48 +375,11 @@ struct FewWalk {
             r.row1 = r.row0 + 128;
             r.brow = 0;
             r.bn = p.nb;
-            u += gridDim.x;
-            return true;
+            at += gridDim.x;
         }
-        if (w >= w1) return false;
-        const int kbs = p.F / BK;
-        const int q = w / kbs;
-        r.phase = 1;
-        r.tile = q / pl.A;
-        r.a = q - r.tile * pl.A;
-        r.kb0 = w - q * kbs;
-        r.nkb = min(kbs - r.kb0, w1 - w);
-        r.row0 = pl.e[r.a] * p.H + r.tile * 128;
-        r.row1 = r.row0 + 64;
-        r.brow = pl.off[r.a];
-        r.bn = (pl.off[r.a + 1] - r.brow + 15) & ~15;
-        w += r.nkb;
         return true;
     }
 };
-
-// Whether all CTAs have written their h (then the loads that follow, TMA's, see it).
-__device__ __forceinline__ bool few_h_ready(const unsigned* count) {
-    unsigned v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
-    if (v < gridDim.x) return false;
-    asm volatile("fence.proxy.async.global;" ::: "memory");
-    return true;
-}
-
-// Bounded wait for it, by one lane (the counter's line is every CTA's).
-__device__ __forceinline__ bool few_wait_h(const unsigned* count, volatile uint32_t* abort_flag) {
-    const uint64_t t0 = ptx::globaltimer_ns();
-    while (!few_h_ready(count)) {
-        if (*abort_flag) return false;
-        if (ptx::globaltimer_ns() - t0 > ptx::WAIT_LIMIT_NS) {
-            *abort_flag = 1u;
-            raise_device_error(MOE_DEVERR_TIMEOUT);
-            return false;
-        }
-    }
-    return true;
-}
 
 // A weight tile, read once by the whole GPU: first to leave L2, so that what the next call needs again
 // (the kernels' code, x, the workspace) stays.
@@ -480,9 +440,15 @@ __device__ __forceinline__ void tmem_wait16(uint32_t* r) {
 template <bool FP8>
 constexpr int few_threads() { return FP8 ? 224 : 192; }
 
+__device__ __forceinline__ int few_id(const FewArgs& p, int r) {
+    return p.i16 ? (int)__ldcg(static_cast<const short*>(p.ids) + r) : __ldcg(static_cast<const int*>(p.ids) + r);
+}
+
 // The plan, the same in every CTA: experts in ascending order, an expert's tokens in ascending order.
 // scratch: 8 E bytes (token masks) and 2 E bytes (an expert's index among the chosen), in the ring.
-template <int THREADS>
+// Up: waits for the first kernel, whose the routes are, and then lets the down kernel start, which therefore
+// finds them written. (Routes are read past L1, which is not kept in line with the other kernels.)
+template <int THREADS, bool DOWN>
 __device__ void few_plan(const FewArgs& p, FewSmem& sm, uint8_t* scratch, unsigned long long* s_mask, int* s_e,
                          int* s_off, float* s_w) {
     unsigned long long* mask = reinterpret_cast<unsigned long long*>(scratch);
@@ -491,16 +457,20 @@ __device__ void few_plan(const FewArgs& p, FewSmem& sm, uint8_t* scratch, unsign
     for (int e = tid; e < p.E; e += THREADS) mask[e] = 0ull;
     if (tid == 0) sm.routes = 0;
     __syncthreads();
+    if constexpr (!DOWN) {
+        pdl_wait();
+        pdl_trigger();
+    }
     const int R = p.T * p.K;
     int valid = 0;
-    const int e_own = tid < R ? load_id(p.ids, tid, p.i16) : -1;      // (in flight together)
-    const float w_own = tid < R ? p.probs[tid] : 0.0f;
+    const int e_own = tid < R ? few_id(p, tid) : -1;                  // (in flight together)
+    const float w_own = DOWN && tid < R ? __ldcg(p.probs + tid) : 0.0f;
     for (int r = tid; r < R; r += THREADS) {
-        const int e = r == tid ? e_own : load_id(p.ids, r, p.i16);
+        const int e = r == tid ? e_own : few_id(p, r);
         if (e >= 0 && e < p.E) {
             atomicOr(&mask[e], 1ull << (r / p.K));
             valid++;
-        } else if (e != -1 && blockIdx.x == 0) {
+        } else if (!DOWN && e != -1 && blockIdx.x == 0) {
             raise_device_error(MOE_DEVERR_BAD_ID);
         }
     }
@@ -550,33 +520,35 @@ __device__ void few_plan(const FewArgs& p, FewSmem& sm, uint8_t* scratch, unsign
         s_off[a] = o;
     }
     __syncthreads();
+    if (!DOWN) {
+        ptx::fence_proxy_async_smem();
+        return;
+    }
     // each route's weight at its row of h; an expert that a token names more than once has one row,
     // weighted with the sum (in ascending k)
     const bool repeated = sm.slots != sm.routes;
     for (int r = tid; r < R; r += THREADS) {
-        const int e = r == tid ? e_own : load_id(p.ids, r, p.i16);
+        const int e = r == tid ? e_own : few_id(p, r);
         if (e < 0 || e >= p.E) continue;
         const int t = r / p.K;
-        float w = r == tid ? w_own : p.probs[r];
+        float w = r == tid ? w_own : __ldcg(p.probs + r);
         if (repeated) {
             bool first = true;
-            for (int j = t * p.K; j < r; j++) first = first && load_id(p.ids, j, p.i16) != e;
+            for (int j = t * p.K; j < r; j++) first = first && few_id(p, j) != e;
             if (!first) continue;
             for (int j = r + 1; j < (t + 1) * p.K; j++)
-                if (load_id(p.ids, j, p.i16) == e) w += p.probs[j];
+                if (few_id(p, j) == e) w += __ldcg(p.probs + j);
         }
         s_w[s_off[index[e]] + __popcll(mask[e] & ((1ull << t) - 1))] = w;
     }
     ptx::fence_proxy_async_smem();     // the ring, used as scratch here, is TMA's from now on
 }
 
-template <bool FP8>
+template <bool FP8, bool DOWN>
 __global__ void __launch_bounds__(few_threads<FP8>(), 1)
-    few_layer_kernel(const __grid_constant__ CUtensorMap tmW13, const __grid_constant__ CUtensorMap tmW2,
-                     const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmH,
-                     const __grid_constant__ CUtensorMap tmSW13, const __grid_constant__ CUtensorMap tmSW2,
-                     const __grid_constant__ CUtensorMap tmSX, const __grid_constant__ CUtensorMap tmSH,
-                     const FewArgs p) {
+    few_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT,
+                    const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmST,
+                    const FewArgs p) {
     constexpr int THREADS = few_threads<FP8>();
     constexpr int BK = FP8 ? 128 : 64;
     constexpr int TMEM_COLS = FP8 ? 256 : 128;
@@ -622,22 +594,18 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
         ptx::fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        ptx::prefetch_tmap(&tmW13);
-        ptx::prefetch_tmap(&tmW2);
-        ptx::prefetch_tmap(&tmX);
-        ptx::prefetch_tmap(&tmH);
+        ptx::prefetch_tmap(&tmW);
+        ptx::prefetch_tmap(&tmT);
         if constexpr (FP8) {
-            ptx::prefetch_tmap(&tmSW13);
-            ptx::prefetch_tmap(&tmSW2);
-            ptx::prefetch_tmap(&tmSX);
-            ptx::prefetch_tmap(&tmSH);
+            ptx::prefetch_tmap(&tmSW);
+            ptx::prefetch_tmap(&tmST);
         }
     }
     if (warp == 1) {
         ptx::tmem_alloc(&sm.tmem, TMEM_COLS);
         ptx::tmem_relinquish();
     }
-    few_plan<THREADS>(p, sm, ring, s_mask, s_e, s_off, s_w);
+    few_plan<THREADS, DOWN>(p, sm, ring, s_mask, s_e, s_off, s_w);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -649,7 +617,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
     if (warp == 0) {
         // ------------------------------------------------------------ producer (one lane)
         if (lane == 0) {
-            FewWalk<FP8> wk(p, pl);
+            FewWalk<FP8, DOWN> wk(p, pl);
             FewRun r;
             const uint64_t policy = evict_first_policy();
             int stage = 0, issued = 0, kb = 0;
@@ -660,21 +628,20 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                 uint8_t* sa = ring + (size_t)st * stage_bytes;
                 const int n = min(FEW_KPS, q.nkb - k);
                 ptx::mbar_arrive_expect_tx(&sm.full[st], n * (FEW_A_BYTES + q.bn * 128));
-                const CUtensorMap* tm = q.phase ? &tmW2 : &tmW13;
                 for (int i = 0; i < n; i++, sa += FEW_A_BYTES) {
-                    tma_load_weights(sa, tm, &sm.full[st], (q.kb0 + k + i) * BK, q.row0, policy);
-                    tma_load_weights(sa + FEW_A_BYTES / 2, tm, &sm.full[st], (q.kb0 + k + i) * BK, q.row1, policy);
+                    tma_load_weights(sa, &tmW, &sm.full[st], (q.kb0 + k + i) * BK, q.row0, policy);
+                    tma_load_weights(sa + FEW_A_BYTES / 2, &tmW, &sm.full[st], (q.kb0 + k + i) * BK, q.row1, policy);
                 }
             };
             auto load_b = [&](int st, const FewRun& q, int k) {
                 uint8_t* sb = ring + (size_t)st * stage_bytes + FEW_KPS * FEW_A_BYTES;
                 const int n = min(FEW_KPS, q.nkb - k);
                 for (int i = 0; i < n; i++, sb += p.nb * 128) {
-                    if (q.phase == 0) {
-                        ptx::tma_load_2d(sb, &tmX, &sm.full[st], (k + i) * BK, 0);
-                    } else {
+                    if constexpr (DOWN) {
                         for (int j = 0; j < q.bn; j += 16)
-                            ptx::tma_load_2d(sb + j * 128, &tmH, &sm.full[st], (q.kb0 + k + i) * BK, q.brow + j);
+                            ptx::tma_load_2d(sb + j * 128, &tmT, &sm.full[st], (q.kb0 + k + i) * BK, q.brow + j);
+                    } else {
+                        ptx::tma_load_2d(sb, &tmT, &sm.full[st], (k + i) * BK, 0);
                     }
                 }
             };
@@ -683,38 +650,27 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                 if (++stage == stages) { stage = 0; phase ^= 1u; }
                 if ((kb += FEW_KPS) >= r.nkb) { kb = 0; have = wk.next(r); }
             };
-            while (have && r.phase == 0) {
+            if constexpr (DOWN) {
+                // the ring's worth of weights, then (once h is written) their tokens operand
+                FewWalk<FP8, DOWN> wb = wk;
+                FewRun rb = r;
+                int sb = 0, kbb = 0, n = 0;
+                for (; have && n < stages; n++) {
+                    load_a(stage, r, kb);
+                    step();
+                }
+                pdl_wait();
+                for (int i = 0; i < n; i++) {
+                    load_b(sb++, rb, kbb);
+                    if ((kbb += FEW_KPS) >= rb.nkb) { kbb = 0; wb.next(rb); }
+                }
+            }
+            while (have) {
                 ok = ptx::wait_parity(&sm.empty[stage], phase ^ 1u, s_abort);
                 if (!ok) break;
                 load_a(stage, r, kb);
                 load_b(stage, r, kb);
                 step();
-            }
-            if (ok && have) {
-                // the ring's worth of down weights, then (once all of h is written) their tokens operand
-                FewWalk<FP8> wb = wk;
-                FewRun rb = r;
-                int sb = stage, kbb = kb, n = 0;
-                while (have && n < stages) {
-                    ok = ptx::wait_parity(&sm.empty[stage], phase ^ 1u, s_abort);
-                    if (!ok) break;
-                    load_a(stage, r, kb);
-                    step();
-                    n++;
-                }
-                ok = few_wait_h(p.count, s_abort) && ok;
-                for (int i = 0; i < n; i++) {    // (also when giving up: the stages' loads have to complete)
-                    load_b(sb, rb, kbb);
-                    if (++sb == stages) sb = 0;
-                    if ((kbb += FEW_KPS) >= rb.nkb) { kbb = 0; wb.next(rb); }
-                }
-                while (ok && have) {
-                    ok = ptx::wait_parity(&sm.empty[stage], phase ^ 1u, s_abort);
-                    if (!ok) break;
-                    load_a(stage, r, kb);
-                    load_b(stage, r, kb);
-                    step();
-                }
             }
             if (!ok) {
                 // give the loads already issued a bounded chance to land before the CTA exits
@@ -732,7 +688,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
         // MMAs take 320, its two copies of scales 160, and a stage's wait and commit 350, one after the
         // other: hence two k-blocks a stage, and one lane that does nothing else.
         if (lane == 0) {
-            FewWalk<FP8> wk(p, pl);
+            FewWalk<FP8, DOWN> wk(p, pl);
             FewRun r;
             int stage = 0, buf = 0, sslot = 0;
             uint32_t phase = 0, tphase = 0, sphase = 0;
@@ -804,7 +760,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
         // bytes, then the tokens'. Loads and rearranging do not wait for one another.
         if constexpr (FP8) {
             struct Cursor {
-                FewWalk<FP8> wk;
+                FewWalk<FP8, DOWN> wk;
                 FewRun r;
                 int kb;
                 bool have;
@@ -816,31 +772,27 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                     c.have = c.wk.next(c.r);
                 }
             };
-            Cursor ld{FewWalk<FP8>(p, pl), FewRun{}, 0, false};
+            Cursor ld{FewWalk<FP8, DOWN>(p, pl), FewRun{}, 0, false};
             ld.have = ld.wk.next(ld.r);
             int ld_slot = 0, pr_slot = 0, loaded = 0;
             uint32_t ld_phase = 0, pr_phase = 0;
-            bool h_seen = false;
+            if constexpr (DOWN) pdl_wait();       // (h's scales; the weights' wait with them)
             uint64_t t_idle = ptx::globaltimer_ns();
             while (ld.have || loaded > 0) {
                 bool progress = false;
-                // (down scales: once h's are written; the groups landed meanwhile are not held up)
-                if (ld.have && ld.r.phase == 1 && !h_seen)
-                    h_seen = __shfl_sync(FULL, (uint32_t)(lane == 0 && few_h_ready(p.count)), 0) != 0u;
-                if (ld.have && (ld.r.phase == 0 || h_seen) && loaded < FEW_SF_SLOTS &&
+                if (ld.have && loaded < FEW_SF_SLOTS &&
                     __all_sync(FULL, ptx::mbar_test_wait(&sm.sf_empty[ld_slot], ld_phase ^ 1u))) {
                     if (lane == 0) {
                         uint8_t* sf = sfring + (size_t)ld_slot * FEW_SF_BYTES;
                         const int kx = (ld.r.kb0 + ld.kb) / FEW_SF_KB * 64;
-                        const CUtensorMap* tm = ld.r.phase ? &tmSW2 : &tmSW13;
                         ptx::mbar_arrive_expect_tx(&sm.sf_full[ld_slot], (128 + ld.r.bn) * 64);
-                        ptx::tma_load_2d(sf, tm, &sm.sf_full[ld_slot], kx, ld.r.row0);
-                        ptx::tma_load_2d(sf + 4096, tm, &sm.sf_full[ld_slot], kx, ld.r.row1);
-                        if (ld.r.phase == 0) {
-                            ptx::tma_load_2d(sf + 8192, &tmSX, &sm.sf_full[ld_slot], kx, 0);
-                        } else {
+                        ptx::tma_load_2d(sf, &tmSW, &sm.sf_full[ld_slot], kx, ld.r.row0);
+                        ptx::tma_load_2d(sf + 4096, &tmSW, &sm.sf_full[ld_slot], kx, ld.r.row1);
+                        if constexpr (DOWN) {
                             for (int i = 0; i < ld.r.bn; i += 16)
-                                ptx::tma_load_2d(sf + 8192 + i * 64, &tmSH, &sm.sf_full[ld_slot], kx, ld.r.brow + i);
+                                ptx::tma_load_2d(sf + 8192 + i * 64, &tmST, &sm.sf_full[ld_slot], kx, ld.r.brow + i);
+                        } else {
+                            ptx::tma_load_2d(sf + 8192, &tmST, &sm.sf_full[ld_slot], kx, 0);
                         }
                     }
                     __syncwarp();
@@ -896,9 +848,9 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
         const int q = warp & 3;                         // TMEM lane quarter
         const int row = q * 32 + lane;                  // weight row of the tile
         const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
-        FewWalk<FP8> wk(p, pl);
+        FewWalk<FP8, DOWN> wk(p, pl);
         FewRun r;
-        int buf = 0, xb = 0;
+        int buf = 0;
         uint32_t tphase = 0;
         bool ok = true, have = wk.next(r);
         auto release = [&]() {
@@ -908,9 +860,11 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             buf ^= 1;
             if (buf == 0) tphase ^= 1u;
         };
-        // up: lanes 0-63 hold the gate products, 64-127 the same columns' linear ones; those go over
+        if constexpr (!DOWN) {
+        // lanes 0-63 hold the gate products, 64-127 the same columns' linear ones; those go over
         // through shared memory, FEW_XCH tokens at a time, two buffers in turn
-        while (ok && have && r.phase == 0) {
+        int xb = 0;
+        while (have) {
             ok = ptx::wait_parity(&sm.tfull[buf], tphase, s_abort);
             ok = epi_all(ok);
             if (!ok) break;
@@ -961,13 +915,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             release();
             have = wk.next(r);
         }
-        // this CTA's h is written: made visible to the other CTAs' TMA loads, then counted (the barrier
-        // orders the four warps' stores before the one release)
-        asm volatile("fence.proxy.async.global;" ::: "memory");
-        epi_sync();
-        if (threadIdx.x == 64)
-            asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p.count), "r"(1u) : "memory");
-        // down
+        } else {
         const int per_tile = pl.A * (p.F / BK);         // k-blocks of an output tile
         int tile = -1;
         const int first_tile = have ? r.tile : -1;
@@ -994,7 +942,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                 unsigned n;      // releases this CTA's sums (all four warps', by the barrier), acquires the others'
                 asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;"
                              : "=r"(n)
-                             : "l"(p.count + 1 + tile), "r"(1u)
+                             : "l"(p.count + tile), "r"(1u)
                              : "memory");
                 sm.ticket = (int)n;
             }
@@ -1032,7 +980,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                     }
             }
         };
-        while (ok && have) {
+        while (have) {
             if (r.tile != tile) {
                 if (tile >= 0) flush();
                 tile = r.tile;
@@ -1066,6 +1014,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             for (long long i = (long long)blockIdx.x * 128 + row; i < (long long)p.T * p.H; i += (long long)gridDim.x * 128)
                 p.y[i] = __float2bfloat16_rn(0.0f);
         }
+        }
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -1095,7 +1044,7 @@ FewLayout few_layout(int T, int K, int H, int F, bool fp8) {
     FewLayout l{};
     size_t o = 0;
     l.count = o;
-    o += up((size_t)(1 + H / 128) * 4);
+    o += up((size_t)(H / 128) * 4);
     l.xq = o;
     o += fp8 ? up((size_t)T * H) : 0;
     l.xs = o;
@@ -1145,12 +1094,14 @@ moe_status few_launch(FewArgs a, const PrepArgs& p, const void* x, const uint8_t
     } else {
         ts13 = ts2 = tsx = tsh = tw13;
     }
-    auto kern = few_layer_kernel<FP8>;
-    static size_t configured = 0;
-    if (smem > configured) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FEW_SMEM_MAX) != cudaSuccess)
+    static bool allowed = false;
+    if (!allowed) {
+        if (cudaFuncSetAttribute(few_gemm_kernel<FP8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FEW_SMEM_MAX) !=
+                cudaSuccess ||
+            cudaFuncSetAttribute(few_gemm_kernel<FP8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FEW_SMEM_MAX) !=
+                cudaSuccess)
             return MOE_ERR_CUDA;
-        configured = FEW_SMEM_MAX;
+        allowed = true;
     }
     const int V = p.logits ? (p.E + PREP_THREADS - 1) / PREP_THREADS : 1;
     const int ctas = a.T + (FP8 ? a.T * ((a.H + PREP_QUANT - 1) / PREP_QUANT) : 0);
@@ -1161,17 +1112,11 @@ moe_status few_launch(FewArgs a, const PrepArgs& p, const void* x, const uint8_t
     if (cudaPeekAtLastError() != cudaSuccess) return moe_host::launch_status();
     int grid = few_sms();
     if (grid > FEW_GRID_MAX) grid = FEW_GRID_MAX;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(few_threads<FP8>());
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;      // the CTAs wait for one another: all resident, or none
-    attr[0].val.cooperative = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, tw13, tw2, tx, th, ts13, ts2, tsx, tsh, a) != cudaSuccess) {
+    const dim3 block(few_threads<FP8>());
+    if (moe_host::launch_pdl(few_gemm_kernel<FP8, false>, dim3((unsigned)grid), block, smem, s, tw13, tx, ts13, tsx, a) !=
+            cudaSuccess ||
+        moe_host::launch_pdl(few_gemm_kernel<FP8, true>, dim3((unsigned)grid), block, smem, s, tw2, th, ts2, tsh, a) !=
+            cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
@@ -1223,7 +1168,7 @@ extern "C" moe_status moe_layer_few_tokens(const void* x, int T, int H, const fl
     p.xq = fp8 ? ws + l.xq : nullptr;
     p.xs = fp8 ? ws + l.xs : nullptr;
     p.count = reinterpret_cast<unsigned*>(ws + l.count);
-    p.n_count = 1 + H / 128;
+    p.n_count = H / 128;
     FewArgs a{};
     a.ids = ids;
     a.probs = probs;
