@@ -259,11 +259,12 @@ __global__ void __launch_bounds__(PREP_THREADS) few_prep_kernel(PrepArgs p) {
 // Up: a tile is 64 columns of W1 and the same 64 of W3 of one expert, over all of H; the tokens
 //   operand is all of x (T rows, zero rows past them), the chosen tokens' columns are read. h goes
 //   to the workspace, the rows of an expert side by side.
-// Down: a tile is 128 output columns of one expert's W2. The walk over (output tile, expert,
-//   k-block) is cut into gridDim.x equal pieces whatever the number of experts, so that few experts
-//   still use every SM; a CTA adds p * (its piece of h W2) up over its experts in shared memory. The
-//   CTAs that share an output tile leave partial sums, and the last to arrive adds them, in the
-//   order of the CTAs: the result does not depend on who is last.
+// Down: a tile is 128 output columns of W2, over all chosen experts one after the other; a CTA adds
+//   p * (its part of h W2) up over the experts in shared memory.
+// Either walk (tile, expert, k-block) is cut into gridDim.x equal pieces wherever that beats whole
+// tiles, so that any number of experts and tiles keeps every SM busy to the end. CTAs that share a tile
+// leave partial sums, and the last to arrive adds them, in the order of the CTAs: the result does
+// not depend on who is last.
 // The down kernel is launched while the up kernel runs: its CTAs start as SMs fall free, make the
 // plan and fill their rings with weights, which depend on the routing alone, and only then wait for h. (One
 // kernel with a barrier between the two halves was slower: it has to be launched cooperatively, which
@@ -280,7 +281,8 @@ constexpr int FEW_SF_KB = 16;              // MXFP8: k-blocks in a group of scal
 constexpr int FEW_SF_SLOTS = 2;            // groups of scales in flight
 constexpr int FEW_SF_BYTES = FEW_SF_KB * 1024;   // a slot: landed 64 bytes a row, rearranged 16 x (A 512 | B 512)
 constexpr int FEW_XCH = 16;                // tokens whose W3 products the epilogue exchanges at a time (tmem_wait16)
-constexpr int FEW_MIN_KB = 2;              // k-blocks of the down walk that a CTA takes at least
+constexpr int FEW_MIN_KB = 2;              // down: k-blocks that a CTA takes at least
+constexpr int FEW_JOIN_KB = 8;             // joining partial sums costs about as much as this many k-blocks
 constexpr size_t FEW_SMEM_MAX = 227 * 1024;
 
 struct FewArgs {
@@ -294,7 +296,7 @@ struct FewArgs {
     void* h;                  // [T K, F] bf16 or E4M3
     uint8_t* hs;              // MXFP8: [T K, F / 32]
     float* part;              // [2 gridDim.x][T][128] partial sums of shared output tiles
-    unsigned* count;          // arrivals at each output tile; zeroed before
+    unsigned* count;          // arrivals at shared tiles (down: by tile, H / 128; up: by first CTA); zeroed before
     __nv_bfloat16* y;
 };
 
@@ -324,17 +326,29 @@ struct FewPlan {
     const int* off;
     const float* w;
     int A;
-    int W;                    // k-blocks of the whole down walk
-    int parts;                // CTAs that take an equal piece of it each (at least FEW_MIN_KB k-blocks)
+    int kbs;                  // k-blocks of a tile (down: of all its experts)
+    int W;                    // k-blocks of the whole walk
+    int unit;                 // it is cut at multiples of this many
+    int parts;                // CTAs that take an equal piece each
 
     // first k-block of CTA c's piece (c = parts: the end)
-    __device__ int begin_of(int c) const { return (int)((long long)W * min(c, parts) / parts); }
+    __device__ int begin_of(int c) const { return unit * (int)((long long)(W / unit) * min(c, parts) / parts); }
+    // the CTA whose piece has k-block w
+    __device__ int owner(int w) const {
+        int c = (int)((long long)w * parts / W);
+        while (begin_of(c) > w) c--;
+        while (begin_of(c + 1) <= w) c++;
+        return c;
+    }
+    // Partial sums have two slots per CTA: 0 for the first tile that it works on, 1 for its last. Of a
+    // tile's CTAs only the first (c0) can have it as its last.
+    __device__ int slot_of(int c, int tile) const { return 2 * c + (begin_of(c) / kbs != tile); }
 };
 
 // A run of k-blocks of one tile: the unit that all warps walk in the same order.
 struct FewRun {
     int a;                    // index among the chosen experts
-    int tile;                 // up: 64-column tile of F; down: 128-column tile of H
+    int tile;                 // up: expert * (F / 64) + 64-column tile of F; down: 128-column tile of H
     int kb0, nkb;
     int row0, row1;           // weight rows of the two 64-row halves
     int brow, bn;             // tokens operand: first row, rows loaded
@@ -344,38 +358,35 @@ template <bool FP8, bool DOWN>
 struct FewWalk {
     const FewArgs& p;
     const FewPlan& pl;
-    int at, end;              // up: tiles, gridDim.x apart; down: k-blocks
+    int at, end;              // k-blocks
     __device__ FewWalk(const FewArgs& p_, const FewPlan& pl_) : p(p_), pl(pl_) {
-        at = DOWN ? pl.begin_of(blockIdx.x) : (int)blockIdx.x;
-        end = DOWN ? pl.begin_of(blockIdx.x + 1) : pl.A * (p.F / 64);
+        at = pl.begin_of(blockIdx.x);
+        end = pl.begin_of(blockIdx.x + 1);
     }
     __device__ bool next(FewRun& r) {
         constexpr int BK = FP8 ? 128 : 64;
         if (at >= end) return false;
+        const int kbs = (DOWN ? p.F : p.H) / BK;      // of a tile and expert
+        const int q = at / kbs;
+        r.kb0 = at - q * kbs;
+        r.nkb = min(kbs - r.kb0, end - at);
+        at += r.nkb;
         if constexpr (DOWN) {
-            const int kbs = p.F / BK;
-            const int q = at / kbs;
             r.tile = q / pl.A;
             r.a = q - r.tile * pl.A;
-            r.kb0 = at - q * kbs;
-            r.nkb = min(kbs - r.kb0, end - at);
             r.row0 = pl.e[r.a] * p.H + r.tile * 128;
             r.row1 = r.row0 + 64;
             r.brow = pl.off[r.a];
             r.bn = (pl.off[r.a + 1] - r.brow + 15) & ~15;
-            at += r.nkb;
         } else {
             const int ft = p.F / 64;
-            r.a = at / ft;
-            r.tile = at - r.a * ft;
-            r.kb0 = 0;
-            r.nkb = p.H / BK;
-            const int c = r.tile * 64;
+            r.tile = q;
+            r.a = q / ft;
+            const int c = (q - r.a * ft) * 64;
             r.row0 = pl.e[r.a] * 2 * p.F + c / 128 * 256 + c % 128;
             r.row1 = r.row0 + 128;
             r.brow = 0;
             r.bn = p.nb;
-            at += gridDim.x;
         }
         return true;
     }
@@ -610,9 +621,20 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    FewPlan pl{s_mask, s_e, s_off, s_w, sm.A, 0, 1};
-    pl.W = (p.H / 128) * pl.A * (p.F / BK);
-    pl.parts = max(1, min((int)gridDim.x, pl.W / FEW_MIN_KB));
+    FewPlan pl{s_mask, s_e, s_off, s_w, sm.A, 0, 0, 1, 1};
+    if constexpr (DOWN) {
+        pl.kbs = pl.A * (p.F / BK);
+        pl.W = (p.H / 128) * pl.kbs;
+        pl.parts = max(1, min((int)gridDim.x, pl.W / FEW_MIN_KB));
+    } else {
+        const int tiles = pl.A * (p.F / 64), G = gridDim.x;
+        pl.kbs = p.H / BK;
+        pl.W = tiles * pl.kbs;
+        // whole tiles, or equal pieces with the shared tiles joined: whichever ends first
+        const bool whole = (tiles + G - 1) / G * pl.kbs <= (pl.W + G - 1) / G + FEW_JOIN_KB;
+        pl.unit = whole ? pl.kbs : 1;
+        pl.parts = max(1, min(G, pl.W / pl.unit));
+    }
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer (one lane)
@@ -641,7 +663,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                         for (int j = 0; j < q.bn; j += 16)
                             ptx::tma_load_2d(sb + j * 128, &tmT, &sm.full[st], (q.kb0 + k + i) * BK, q.brow + j);
                     } else {
-                        ptx::tma_load_2d(sb, &tmT, &sm.full[st], (k + i) * BK, 0);
+                        ptx::tma_load_2d(sb, &tmT, &sm.full[st], (q.kb0 + k + i) * BK, 0);
                     }
                 }
             };
@@ -860,6 +882,18 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             buf ^= 1;
             if (buf == 0) tphase ^= 1u;
         };
+        // Counts this CTA's partial sums as written (all four warps', by the barrier) and makes those counted
+        // before visible: how many these are.
+        auto arrive = [&](unsigned* count) {
+            epi_sync();
+            if (threadIdx.x == 64) {
+                unsigned n;
+                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(n) : "l"(count), "r"(1u) : "memory");
+                sm.ticket = (int)n;
+            }
+            epi_sync();
+            return sm.ticket;
+        };
         if constexpr (!DOWN) {
         // lanes 0-63 hold the gate products, 64-127 the same columns' linear ones; those go over
         // through shared memory, FEW_XCH tokens at a time, two buffers in turn
@@ -869,88 +903,103 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             ok = epi_all(ok);
             if (!ok) break;
             ptx::tc_fence_after();
-            unsigned long long m = pl.mask[r.a];
-            int slot = pl.off[r.a];
-            while (m) {
-                uint32_t v[FEW_XCH];
-                int n = 0;
-                unsigned long long mm = m;
+            const unsigned long long tokens = pl.mask[r.a];
+            const int m_a = pl.off[r.a + 1] - pl.off[r.a];
+            const size_t slot = (size_t)p.T * 128;
+            // the next up to 16 tokens' columns of the accumulator
+            auto load16 = [&](unsigned long long& m, uint32_t* v) {
 #pragma unroll
                 for (int i = 0; i < FEW_XCH; i++) {
                     v[i] = 0u;
-                    if (mm) {                            // uniform
-                        v[i] = tmem_ld_x1(tq + (uint32_t)(buf * FEW_ACC_COLS + __ffsll((long long)mm) - 1));
-                        mm &= mm - 1;
-                        n++;
+                    if (m) {                             // uniform
+                        v[i] = tmem_ld_x1(tq + (uint32_t)(buf * FEW_ACC_COLS + __ffsll((long long)m) - 1));
+                        m &= m - 1;
                     }
                 }
                 tmem_wait16(v);
-                m = mm;
-                if (q >= 2) {
+            };
+            const bool whole = r.nkb == pl.kbs;
+            bool mine = true;
+            int c0 = 0, c1 = 0;
+            if (!whole) {
+                c0 = pl.owner(r.tile * pl.kbs);
+                c1 = pl.owner((r.tile + 1) * pl.kbs - 1);
+                float* to = p.part + pl.slot_of(blockIdx.x, r.tile) * slot + row;
+                unsigned long long m = tokens;
+                for (int i0 = 0; i0 < m_a; i0 += FEW_XCH) {
+                    uint32_t v[FEW_XCH];
+                    load16(m, v);
 #pragma unroll
                     for (int i = 0; i < FEW_XCH; i++)
-                        if (i < n) sm.xch[xb][i][row - 64] = __uint_as_float(v[i]);
+                        if (i0 + i < m_a) __stcg(to + (i0 + i) * 128, __uint_as_float(v[i]));
                 }
-                epi_sync();
-                if (q < 2) {
+                release();
+                mine = arrive(p.count + p.H / 128 + c0) == c1 - c0;
+            }
+            if (mine) {
+                unsigned long long m = tokens;
+                for (int i0 = 0; i0 < m_a; i0 += FEW_XCH) {
+                    uint32_t v[FEW_XCH];
+                    const int n = min(FEW_XCH, m_a - i0);
+                    if (whole) {
+                        load16(m, v);
+                    } else {
+                        float f[FEW_XCH];
 #pragma unroll
-                    for (int i = 0; i < FEW_XCH; i++) {
-                        if (i >= n) break;
-                        const float ga = __uint_as_float(v[i]);
-                        const float h = ga / (1.0f + expf(-ga)) * sm.xch[xb][i][row];
-                        const size_t o = (size_t)(slot + i) * p.F + r.tile * 64 + row;
-                        if constexpr (FP8) {
-                            const float amax = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(fabsf(h))));
-                            const int sbyte = e8m0_scale_byte(amax);
-                            static_cast<uint8_t*>(p.h)[o] = (uint8_t)f32x2_to_e4m3x2(h * e8m0_inv_scale(sbyte), 0.0f);
-                            if (lane == 0) p.hs[o >> 5] = (uint8_t)sbyte;
-                        } else {
-                            static_cast<__nv_bfloat16*>(p.h)[o] = __float2bfloat16_rn(h);
+                        for (int i = 0; i < FEW_XCH; i++) f[i] = 0.0f;
+                        for (int c = c0; c <= c1; c++) {
+                            const float* from = p.part + pl.slot_of(c, r.tile) * slot + i0 * 128 + row;
+#pragma unroll
+                            for (int i = 0; i < FEW_XCH; i++)
+                                if (i < n) f[i] += __ldcg(from + i * 128);
+                        }
+#pragma unroll
+                        for (int i = 0; i < FEW_XCH; i++) v[i] = __float_as_uint(f[i]);
+                    }
+                    if (q >= 2) {
+#pragma unroll
+                        for (int i = 0; i < FEW_XCH; i++)
+                            if (i < n) sm.xch[xb][i][row - 64] = __uint_as_float(v[i]);
+                    }
+                    epi_sync();
+                    if (q < 2) {
+#pragma unroll
+                        for (int i = 0; i < FEW_XCH; i++) {
+                            if (i >= n) break;
+                            const float ga = __uint_as_float(v[i]);
+                            const float h = ga / (1.0f + expf(-ga)) * sm.xch[xb][i][row];
+                            const size_t o = (size_t)(pl.off[r.a] + i0 + i) * p.F + r.tile % (p.F / 64) * 64 + row;
+                            if constexpr (FP8) {
+                                const float amax = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(fabsf(h))));
+                                const int sbyte = e8m0_scale_byte(amax);
+                                static_cast<uint8_t*>(p.h)[o] = (uint8_t)f32x2_to_e4m3x2(h * e8m0_inv_scale(sbyte), 0.0f);
+                                if (lane == 0) p.hs[o >> 5] = (uint8_t)sbyte;
+                            } else {
+                                static_cast<__nv_bfloat16*>(p.h)[o] = __float2bfloat16_rn(h);
+                            }
                         }
                     }
+                    xb ^= 1;
                 }
-                slot += n;
-                xb ^= 1;
             }
-            release();
+            if (whole) release();
             have = wk.next(r);
         }
         } else {
-        const int per_tile = pl.A * (p.F / BK);         // k-blocks of an output tile
         int tile = -1;
-        const int first_tile = have ? r.tile : -1;
-        auto owner = [&](int w) {                       // the CTA whose piece has k-block w
-            int c = (int)((long long)w * pl.parts / pl.W);
-            while (pl.begin_of(c) > w) c--;
-            while (pl.begin_of(c + 1) <= w) c++;
-            return c;
-        };
         auto flush = [&]() {
-            const int c0 = owner(tile * per_tile), c1 = owner((tile + 1) * per_tile - 1);
+            const int c0 = pl.owner(tile * pl.kbs), c1 = pl.owner((tile + 1) * pl.kbs - 1);
             __nv_bfloat16* y = p.y + tile * 128 + row;
             if (c0 == c1) {
                 for (int t = 0; t < p.T; t++) y[(size_t)t * p.H] = __float2bfloat16_rn(acc[t * 128 + row]);
                 return;
             }
-            // a CTA's partial sums: slot 0 for the first tile that it works on, slot 1 for the last; only the
-            // first of a tile's CTAs can have it as its last
             const size_t slot = (size_t)p.T * 128;
-            float* mine = p.part + ((size_t)2 * blockIdx.x + (tile != first_tile)) * slot + row;
-            for (int t = 0; t < p.T; t++) __stcg(mine + t * 128, acc[t * 128 + row]);
-            epi_sync();
-            if (threadIdx.x == 64) {
-                unsigned n;      // releases this CTA's sums (all four warps', by the barrier), acquires the others'
-                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;"
-                             : "=r"(n)
-                             : "l"(p.count + tile), "r"(1u)
-                             : "memory");
-                sm.ticket = (int)n;
-            }
-            epi_sync();
-            if (sm.ticket != c1 - c0) return;
+            float* to = p.part + pl.slot_of(blockIdx.x, tile) * slot + row;
+            for (int t = 0; t < p.T; t++) __stcg(to + t * 128, acc[t * 128 + row]);
+            if (arrive(p.count + tile) != c1 - c0) return;
             // a warp per token, four rows a lane; eight tokens' loads in flight per warp
-            const float4* src = reinterpret_cast<const float4*>(
-                p.part + ((size_t)2 * c0 + (pl.begin_of(c0) / per_tile != tile)) * slot) + lane;
+            const float4* src = reinterpret_cast<const float4*>(p.part + pl.slot_of(c0, tile) * slot) + lane;
             const float4* rest = reinterpret_cast<const float4*>(p.part + (size_t)2 * (c0 + 1) * slot) + lane;
             const int n = c1 - c0;
             for (int t0 = q; t0 < p.T; t0 += 32) {
@@ -1044,7 +1093,7 @@ FewLayout few_layout(int T, int K, int H, int F, bool fp8) {
     FewLayout l{};
     size_t o = 0;
     l.count = o;
-    o += up((size_t)(H / 128) * 4);
+    o += up((size_t)(H / 128 + FEW_GRID_MAX) * 4);
     l.xq = o;
     o += fp8 ? up((size_t)T * H) : 0;
     l.xs = o;
@@ -1168,7 +1217,7 @@ extern "C" moe_status moe_layer_few_tokens(const void* x, int T, int H, const fl
     p.xq = fp8 ? ws + l.xq : nullptr;
     p.xs = fp8 ? ws + l.xs : nullptr;
     p.count = reinterpret_cast<unsigned*>(ws + l.count);
-    p.n_count = H / 128;
+    p.n_count = H / 128 + FEW_GRID_MAX;
     FewArgs a{};
     a.ids = ids;
     a.probs = probs;

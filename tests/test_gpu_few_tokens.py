@@ -49,8 +49,9 @@ def _weights(E, H, F, precision, seed, std=0.05):
     return (w1, w3, w2), api.moe_prepare_weights(w1.cuda(), w3.cuda(), w2.cuda(), precision)
 
 
-def _reference(x, ids, probs, packed):
-    """(y, A) in 64 bits from bf16 x, integer ids, probs and the packed weights."""
+def _reference(x, ids, probs, packed, largest=False):
+    """(y, A) in 64 bits from bf16 x, integer ids, probs and the packed weights; largest: A is the largest of
+    the magnitudes that y is summed from, not their sum."""
     fp8 = packed.precision == "mxfp8"
     T, K = ids.shape
     E, H, F = packed.E, packed.H, packed.F
@@ -71,10 +72,11 @@ def _reference(x, ids, probs, packed):
         a, b = X[[t for t, _ in at]] @ w13[first].T, X[[t for t, _ in at]] @ w13[first + 128].T
         h = a / (1 + np.exp(-a)) * b
         h = _mxfp8(h) if fp8 else torch.from_numpy(h).to(torch.bfloat16).double().numpy()
-        d, m = h @ w2.T, np.abs(h) @ np.abs(w2.T)
+        d = h @ w2.T
+        m = np.stack([(np.abs(r) * np.abs(w2)).max(1) for r in h]) if largest else np.abs(h) @ np.abs(w2.T)
         for i, (t, k) in enumerate(at):
             y[t] += float(probs[t, k]) * d[i]
-            A[t] += float(probs[t, k]) * m[i]
+            A[t] = np.maximum(A[t], float(probs[t, k]) * m[i]) if largest else A[t] + float(probs[t, k]) * m[i]
     return y, A
 
 
@@ -118,6 +120,31 @@ def test_few_tokens_matches_plain(T, H, E, K, F, precision, renorm, idt):
     assert ids.dtype == idt and torch.equal(ids, want_ids)
     assert (probs - want_p).abs().max().item() <= 1e-6
     _check(y, x, ids, probs, packed)
+    assert api.moe_get_device_errors() == 0
+
+
+@pytest.mark.parametrize("T,H,E,K,F,precision", [
+    (1, 4096, 2, 1, 128, "bf16"),          # two tiles, each by dozens of blocks
+    (64, 2048, 3, 2, 512, "bf16"),         # few tiles, many tokens
+    (40, 7168, 1, 1, 128, "bf16"),
+    (5, 4096, 3, 2, 512, "mxfp8"),
+    (64, 7168, 2, 2, 512, "mxfp8"),
+    (17, 1024, 21, 4, 2048, "mxfp8"),      # more tiles than blocks, shared ones among them
+    (6, 1536, 30, 6, 1280, "bf16"),
+])
+def test_few_tokens_shared_tiles(T, H, E, K, F, precision):
+    """Sizes whose tiles are shared between the GPU's blocks and joined from partial sums. With F as
+    small as 128 a single step of h weighs more than the bars' share of all terms: they are joined
+    by two steps (2^-7 each, MXFP8 2^-3) of the largest term."""
+    x, lg = _inputs(T, H, E, seed=T + H)
+    _, packed = _weights(E, H, F, precision, seed=E + F, std=0.02)
+    y, ids, probs = api.moe_layer_few_tokens(x, lg, packed, K)
+    ref, A = _reference(x, ids.cpu().numpy(), probs.cpu().numpy(), packed)
+    _, M = _reference(x, ids.cpu().numpy(), probs.cpu().numpy(), packed, largest=True)
+    fp8 = precision == "mxfp8"
+    bar = 2.0 ** -8 * np.abs(ref) + 2.0 ** (-10 if fp8 else -12) * A + 2.0 ** (-2 if fp8 else -6) * M
+    assert (np.abs(y.double().cpu().numpy() - ref) <= bar).all()
+    assert torch.equal(y, api.moe_layer_few_tokens(x, lg, packed, K)[0])
     assert api.moe_get_device_errors() == 0
 
 
