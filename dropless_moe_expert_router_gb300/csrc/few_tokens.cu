@@ -329,16 +329,20 @@ struct FewPlan {
     int kbs;                  // k-blocks of a tile (down: of all its experts)
     int W;                    // k-blocks of the whole walk
     int unit;                 // it is cut at multiples of this many
-    int parts;                // CTAs that take an equal piece each
+    int parts;                // CTAs that take a piece each: base units, the first `more` of them one more
+    int base, more;
 
-    // first k-block of CTA c's piece (c = parts: the end)
-    __device__ int begin_of(int c) const { return unit * (int)((long long)(W / unit) * min(c, parts) / parts); }
+    __device__ void cut(int n) {
+        parts = n;
+        base = W / unit / n;
+        more = W / unit - base * n;
+    }
+    // first k-block of CTA c's piece (c >= parts: the end)
+    __device__ int begin_of(int c) const { return c >= parts ? W : unit * (base * c + min(c, more)); }
     // the CTA whose piece has k-block w
     __device__ int owner(int w) const {
-        int c = (int)((long long)w * parts / W);
-        while (begin_of(c) > w) c--;
-        while (begin_of(c + 1) <= w) c++;
-        return c;
+        const int u = w / unit, longer = more * (base + 1);
+        return u < longer ? u / (base + 1) : more + (u - longer) / base;
     }
     // Partial sums have two slots per CTA: 0 for the first tile that it works on, 1 for its last. Of a
     // tile's CTAs only the first (c0) can have it as its last.
@@ -456,7 +460,7 @@ __device__ __forceinline__ int few_id(const FewArgs& p, int r) {
 }
 
 // The plan, the same in every CTA: experts in ascending order, an expert's tokens in ascending order.
-// scratch: 8 E bytes (token masks) and 2 E bytes (an expert's index among the chosen), in the ring.
+// scratch: 8 E bytes (token masks), 2 E (an expert's index among the chosen) and 2 T K (the routes), in the ring.
 // Up: waits for the first kernel, whose the routes are, and then lets the down kernel start, which therefore
 // finds them written. (Routes are read past L1, which is not kept in line with the other kernels.)
 template <int THREADS, bool DOWN>
@@ -464,6 +468,9 @@ __device__ void few_plan(const FewArgs& p, FewSmem& sm, uint8_t* scratch, unsign
                          int* s_off, float* s_w) {
     unsigned long long* mask = reinterpret_cast<unsigned long long*>(scratch);
     uint16_t* index = reinterpret_cast<uint16_t*>(scratch + (size_t)p.E * 8);
+    uint16_t* id = index + p.E;
+    constexpr uint16_t NONE = 0xffff;
+    constexpr int B = 8;              // routes a thread has in flight
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int e = tid; e < p.E; e += THREADS) mask[e] = 0ull;
     if (tid == 0) sm.routes = 0;
@@ -474,15 +481,27 @@ __device__ void few_plan(const FewArgs& p, FewSmem& sm, uint8_t* scratch, unsign
     }
     const int R = p.T * p.K;
     int valid = 0;
-    const int e_own = tid < R ? few_id(p, tid) : -1;                  // (in flight together)
-    const float w_own = DOWN && tid < R ? __ldcg(p.probs + tid) : 0.0f;
-    for (int r = tid; r < R; r += THREADS) {
-        const int e = r == tid ? e_own : few_id(p, r);
-        if (e >= 0 && e < p.E) {
-            atomicOr(&mask[e], 1ull << (r / p.K));
-            valid++;
-        } else if (!DOWN && e != -1 && blockIdx.x == 0) {
-            raise_device_error(MOE_DEVERR_BAD_ID);
+    float w_own[B];                   // (down) its first routes' weights
+    for (int r0 = tid; r0 < R; r0 += B * THREADS) {
+        int e[B];
+#pragma unroll
+        for (int u = 0; u < B; u++) {
+            const int r = r0 + u * THREADS;
+            e[u] = r < R ? few_id(p, r) : -1;
+            if (DOWN && r0 == tid) w_own[u] = r < R ? __ldcg(p.probs + r) : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < B; u++) {
+            const int r = r0 + u * THREADS;
+            if (r >= R) break;
+            const bool ok = e[u] >= 0 && e[u] < p.E;
+            id[r] = ok ? (uint16_t)e[u] : NONE;
+            if (ok) {
+                atomicOr(&mask[e[u]], 1ull << (r / p.K));
+                valid++;
+            } else if (!DOWN && e[u] != -1 && blockIdx.x == 0) {
+                raise_device_error(MOE_DEVERR_BAD_ID);
+            }
         }
     }
     if (valid) atomicAdd(&sm.routes, valid);
@@ -538,19 +557,27 @@ __device__ void few_plan(const FewArgs& p, FewSmem& sm, uint8_t* scratch, unsign
     // each route's weight at its row of h; an expert that a token names more than once has one row,
     // weighted with the sum (in ascending k)
     const bool repeated = sm.slots != sm.routes;
-    for (int r = tid; r < R; r += THREADS) {
-        const int e = r == tid ? e_own : few_id(p, r);
-        if (e < 0 || e >= p.E) continue;
-        const int t = r / p.K;
-        float w = r == tid ? w_own : __ldcg(p.probs + r);
-        if (repeated) {
-            bool first = true;
-            for (int j = t * p.K; j < r; j++) first = first && few_id(p, j) != e;
-            if (!first) continue;
-            for (int j = r + 1; j < (t + 1) * p.K; j++)
-                if (few_id(p, j) == e) w += __ldcg(p.probs + j);
+    for (int r0 = tid; r0 < R; r0 += B * THREADS) {
+        float w[B];
+#pragma unroll
+        for (int u = 0; u < B; u++) {
+            const int r = r0 + u * THREADS;
+            w[u] = r0 == tid ? w_own[u] : r < R ? __ldcg(p.probs + r) : 0.0f;
         }
-        s_w[s_off[index[e]] + __popcll(mask[e] & ((1ull << t) - 1))] = w;
+#pragma unroll
+        for (int u = 0; u < B; u++) {
+            const int r = r0 + u * THREADS;
+            if (r >= R || id[r] == NONE) continue;
+            const int e = id[r], t = r / p.K;
+            if (repeated) {
+                bool first = true;
+                for (int j = t * p.K; j < r; j++) first = first && id[j] != e;
+                if (!first) continue;
+                for (int j = r + 1; j < (t + 1) * p.K; j++)
+                    if (id[j] == e) w[u] += __ldcg(p.probs + j);
+            }
+            s_w[s_off[index[e]] + __popcll(mask[e] & ((1ull << t) - 1))] = w[u];
+        }
     }
     ptx::fence_proxy_async_smem();     // the ring, used as scratch here, is TMA's from now on
 }
@@ -621,19 +648,20 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    FewPlan pl{s_mask, s_e, s_off, s_w, sm.A, 0, 0, 1, 1};
+    FewPlan pl{s_mask, s_e, s_off, s_w, sm.A, 0, 0, 1, 1, 0, 0};
     if constexpr (DOWN) {
         pl.kbs = pl.A * (p.F / BK);
         pl.W = (p.H / 128) * pl.kbs;
-        pl.parts = max(1, min((int)gridDim.x, pl.W / FEW_MIN_KB));
+        pl.cut(max(1, min((int)gridDim.x, pl.W / FEW_MIN_KB)));
     } else {
         const int tiles = pl.A * (p.F / 64), G = gridDim.x;
         pl.kbs = p.H / BK;
         pl.W = tiles * pl.kbs;
         // whole tiles, or equal pieces with the shared tiles joined: whichever ends first
-        const bool whole = (tiles + G - 1) / G * pl.kbs <= (pl.W + G - 1) / G + FEW_JOIN_KB;
+        const int join = FEW_JOIN_KB + sm.slots / (2 * max(pl.A, 1));       // (and half of one for each token)
+        const bool whole = (tiles + G - 1) / G * pl.kbs <= (pl.W + G - 1) / G + join;
         pl.unit = whole ? pl.kbs : 1;
-        pl.parts = max(1, min(G, pl.W / pl.unit));
+        pl.cut(max(1, min(G, pl.W / pl.unit)));
     }
 
     if (warp == 0) {
@@ -947,11 +975,13 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                         float f[FEW_XCH];
 #pragma unroll
                         for (int i = 0; i < FEW_XCH; i++) f[i] = 0.0f;
+                        const float* from = p.part + pl.slot_of(c0, r.tile) * slot + i0 * 128 + row;
+#pragma unroll 2
                         for (int c = c0; c <= c1; c++) {
-                            const float* from = p.part + pl.slot_of(c, r.tile) * slot + i0 * 128 + row;
 #pragma unroll
                             for (int i = 0; i < FEW_XCH; i++)
                                 if (i < n) f[i] += __ldcg(from + i * 128);
+                            from = p.part + (2 * (c + 1)) * slot + i0 * 128 + row;
                         }
 #pragma unroll
                         for (int i = 0; i < FEW_XCH; i++) v[i] = __float_as_uint(f[i]);
@@ -1127,7 +1157,8 @@ moe_status few_launch(FewArgs a, const PrepArgs& p, const void* x, const uint8_t
     if (fixed + 2 * (size_t)stage_bytes > FEW_SMEM_MAX) return MOE_ERR_UNSUPPORTED;
     a.stages = (int)((FEW_SMEM_MAX - fixed) / stage_bytes);
     if (a.stages > FEW_STAGES) a.stages = FEW_STAGES;
-    if ((size_t)a.stages * stage_bytes < (size_t)a.E * 10) return MOE_ERR_UNSUPPORTED;   // the plan's scratch
+    if ((size_t)a.stages * stage_bytes < (size_t)a.E * 10 + (size_t)a.T * a.K * 2)      // the plan's scratch
+        return MOE_ERR_UNSUPPORTED;
     const size_t smem = fixed + (size_t)a.stages * stage_bytes;
     CUtensorMap tw13, tw2, tx, th, ts13, ts2, tsx, tsh;
     using moe_host::make_operand_map;
