@@ -281,7 +281,8 @@ constexpr int FEW_SF_KB = 16;              // MXFP8: k-blocks in a group of scal
 constexpr int FEW_SF_SLOTS = 2;            // groups of scales in flight
 constexpr int FEW_SF_BYTES = FEW_SF_KB * 1024;   // a slot: landed 64 bytes a row, rearranged 16 x (A 512 | B 512)
 constexpr int FEW_XCH = 16;                // tokens whose W3 products the epilogue exchanges at a time (tmem_wait16)
-constexpr int FEW_MIN_KB = 2;              // down: k-blocks that a CTA takes at least
+constexpr int FEW_MIN_KB = 2;              // k-blocks that a CTA takes at least
+constexpr int FEW_SHARE = 32;              // CTAs that share a tile at most (the last to arrive reads all their sums)
 constexpr int FEW_JOIN_KB = 8;             // joining partial sums costs about as much as this many k-blocks
 constexpr size_t FEW_SMEM_MAX = 227 * 1024;
 
@@ -450,6 +451,35 @@ __device__ __forceinline__ void tmem_wait16(uint32_t* r) {
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
                  : "memory");
+}
+
+// v[j] = the sum over the CTAs i = i0, i0 + di, ... < n of their partial sums of token t0 + j dt (< T): the
+// first CTA's at `first`, the others' at `rest`, `stride` apart. UN CTAs' loads in flight.
+template <int NT, int UN>
+__device__ __forceinline__ void few_add_parts(float4 (&v)[NT], const float4* first, const float4* rest, size_t stride,
+                                              int i0, int di, int n, int t0, int dt, int T) {
+#pragma unroll
+    for (int j = 0; j < NT; j++) v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (; i0 < n; i0 += UN * di) {
+        float4 u[UN][NT];
+#pragma unroll
+        for (int k = 0; k < UN; k++) {
+            const int i = i0 + k * di;
+            const float4* from = i == 0 ? first : rest + stride * (i - 1);
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+                u[k][j] = i < n && t0 + j * dt < T ? __ldcg(from + (t0 + j * dt) * 32) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int k = 0; k < UN; k++)
+#pragma unroll
+            for (int j = 0; j < NT; j++) {
+                v[j].x += u[k][j].x;
+                v[j].y += u[k][j].y;
+                v[j].z += u[k][j].z;
+                v[j].w += u[k][j].w;
+            }
+    }
 }
 
 template <bool FP8>
@@ -652,16 +682,17 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
     if constexpr (DOWN) {
         pl.kbs = pl.A * (p.F / BK);
         pl.W = (p.H / 128) * pl.kbs;
-        pl.cut(max(1, min((int)gridDim.x, pl.W / FEW_MIN_KB)));
+        pl.cut(max(1, min(min((int)gridDim.x, pl.W / FEW_MIN_KB), p.H / 128 * FEW_SHARE)));
     } else {
         const int tiles = pl.A * (p.F / 64), G = gridDim.x;
         pl.kbs = p.H / BK;
         pl.W = tiles * pl.kbs;
         // whole tiles, or equal pieces with the shared tiles joined: whichever ends first
         const int join = FEW_JOIN_KB + sm.slots / (2 * max(pl.A, 1));       // (and half of one for each token)
-        const bool whole = (tiles + G - 1) / G * pl.kbs <= (pl.W + G - 1) / G + join;
+        const int pieces = max(1, min(min(G, pl.W / FEW_MIN_KB), tiles * FEW_SHARE));
+        const bool whole = (tiles + G - 1) / G * pl.kbs <= (pl.W + pieces - 1) / pieces + join;
         pl.unit = whole ? pl.kbs : 1;
-        pl.cut(max(1, min(G, pl.W / pl.unit)));
+        pl.cut(whole ? max(1, min(G, tiles)) : pieces);
     }
 
     if (warp == 0) {
@@ -1028,35 +1059,47 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             float* to = p.part + pl.slot_of(blockIdx.x, tile) * slot + row;
             for (int t = 0; t < p.T; t++) __stcg(to + t * 128, acc[t * 128 + row]);
             if (arrive(p.count + tile) != c1 - c0) return;
-            // a warp per token, four rows a lane; eight tokens' loads in flight per warp
-            const float4* src = reinterpret_cast<const float4*>(p.part + pl.slot_of(c0, tile) * slot) + lane;
+            // four rows a lane; up to 32 loads in flight per warp
+            const float4* first = reinterpret_cast<const float4*>(p.part + pl.slot_of(c0, tile) * slot) + lane;
             const float4* rest = reinterpret_cast<const float4*>(p.part + (size_t)2 * (c0 + 1) * slot) + lane;
-            const int n = c1 - c0;
-            for (int t0 = q; t0 < p.T; t0 += 32) {
-                float4 v[8];
+            const int n = c1 - c0 + 1;
+            auto put = [&](int t, const float4& v) {
+                __nv_bfloat162 o[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+                *reinterpret_cast<uint2*>(p.y + (size_t)t * p.H + tile * 128 + 4 * lane) = *reinterpret_cast<uint2*>(o);
+            };
+            if (p.T <= 4) {
+                // a quarter of the CTAs' sums per warp, then the four warps' in order
+                float4 v[4];
+                few_add_parts<4, 8>(v, first, rest, slot / 2, q, 4, n, 0, 1, p.T);
+                float4* x = reinterpret_cast<float4*>(sm.xch);      // [warp][token][lane]
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (t0 + 4 * j < p.T) v[j] = __ldcg(src + (t0 + 4 * j) * 32);
+                for (int t = 0; t < 4; t++) x[(q * 4 + t) * 32 + lane] = v[t];
+                epi_sync();
+                if (q < p.T) {
+                    float4 a = x[q * 32 + lane];
+#pragma unroll
+                    for (int w = 1; w < 4; w++) {
+                        const float4 b = x[(w * 4 + q) * 32 + lane];
+                        a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+                    }
+                    put(q, a);
                 }
-#pragma unroll 4
-                for (int i = 0; i < n; i++)
+                epi_sync();
+            } else if (p.T <= 16) {
+                // a warp per token
+                float4 v[4];
+                few_add_parts<4, 8>(v, first, rest, slot / 2, 0, 1, n, q, 4, p.T);
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    if (q + 4 * j < p.T) put(q + 4 * j, v[j]);
+            } else {
+                for (int t0 = q; t0 < p.T; t0 += 32) {
+                    float4 v[8];
+                    few_add_parts<8, 4>(v, first, rest, slot / 2, 0, 1, n, t0, 4, p.T);
 #pragma unroll
                     for (int j = 0; j < 8; j++)
-                        if (t0 + 4 * j < p.T) {
-                            const float4 u = __ldcg(rest + (slot / 2) * i + (t0 + 4 * j) * 32);
-                            v[j].x += u.x;
-                            v[j].y += u.y;
-                            v[j].z += u.z;
-                            v[j].w += u.w;
-                        }
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-                    if (t0 + 4 * j < p.T) {
-                        __nv_bfloat162 o[2] = {__floats2bfloat162_rn(v[j].x, v[j].y), __floats2bfloat162_rn(v[j].z, v[j].w)};
-                        *reinterpret_cast<uint2*>(p.y + (size_t)(t0 + 4 * j) * p.H + tile * 128 + 4 * lane) =
-                            *reinterpret_cast<uint2*>(o);
-                    }
+                        if (t0 + 4 * j < p.T) put(t0 + 4 * j, v[j]);
+                }
             }
         };
         while (have) {
