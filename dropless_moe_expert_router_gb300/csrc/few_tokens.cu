@@ -271,18 +271,18 @@ __global__ void __launch_bounds__(PREP_THREADS) few_prep_kernel(PrepArgs p) {
 // alone took 3 us longer.)
 //
 // Warps: 0 TMA producer, 1 TMEM and MMA issue, 2-5 epilogue (one TMEM lane quarter each), 6 (MXFP8)
-// the scales: loads a group of 16 k-blocks' scale bytes and rearranges them for tcgen05.cp.
+// the scales: loads a group of k-blocks' scale bytes and rearranges them for tcgen05.cp.
 // ---------------------------------------------------------------------------
 constexpr int FEW_STAGES = 6;              // most ring stages
 constexpr int FEW_KPS = 2;                 // k-blocks in a stage
 constexpr int FEW_A_BYTES = 128 * 128;     // a weight tile: 128 rows of 128 bytes
 constexpr int FEW_ACC_COLS = 64;           // TMEM columns of one accumulator: tokens
-constexpr int FEW_SF_KB = 16;              // MXFP8: k-blocks in a group of scales, and a row's bytes of it / 4
-constexpr int FEW_SF_SLOTS = 2;            // groups of scales in flight
-constexpr int FEW_SF_BYTES = FEW_SF_KB * 1024;   // a slot: landed 64 bytes a row, rearranged 16 x (A 512 | B 512)
+constexpr int FEW_SF_KB = 8;               // MXFP8: k-blocks in a group of scales (4 bytes a row each)
+constexpr int FEW_SF_SLOTS = 4;            // groups of scales in flight (short tiles have a group each)
+constexpr int FEW_SF_BYTES = FEW_SF_KB * 1024;   // a slot: landed 4 FEW_SF_KB bytes a row, rearranged FEW_SF_KB x (A 512 | B 512)
 constexpr int FEW_XCH = 16;                // tokens whose W3 products the epilogue exchanges at a time (tmem_wait16)
 constexpr int FEW_MIN_KB = 2;              // k-blocks that a CTA takes at least
-constexpr int FEW_SHARE = 32;              // CTAs that share a tile at most (the last to arrive reads all their sums)
+constexpr int FEW_SHARE = 32;              // up: CTAs that share a tile at most (the last to arrive reads all their sums)
 constexpr int FEW_JOIN_KB = 8;             // joining partial sums costs about as much as this many k-blocks
 constexpr size_t FEW_SMEM_MAX = 227 * 1024;
 
@@ -527,7 +527,8 @@ __device__ void few_plan(const FewArgs& p, FewSmem& sm, uint8_t* scratch, unsign
             const bool ok = e[u] >= 0 && e[u] < p.E;
             id[r] = ok ? (uint16_t)e[u] : NONE;
             if (ok) {
-                atomicOr(&mask[e[u]], 1ull << (r / p.K));
+                // (by words: 64-bit atomics on shared memory retry where routes meet)
+                atomicOr(reinterpret_cast<unsigned*>(mask + e[u]) + (r / p.K >> 5), 1u << (r / p.K & 31));
                 valid++;
             } else if (!DOWN && e[u] != -1 && blockIdx.x == 0) {
                 raise_device_error(MOE_DEVERR_BAD_ID);
@@ -682,7 +683,10 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
     if constexpr (DOWN) {
         pl.kbs = pl.A * (p.F / BK);
         pl.W = (p.H / 128) * pl.kbs;
-        pl.cut(max(1, min(min((int)gridDim.x, pl.W / FEW_MIN_KB), p.H / 128 * FEW_SHARE)));
+        // n CTAs take W / n k-blocks of about 0.36 us each, then the last of a tile reads n / (H / 128) sums
+        // of about 0.1 us each, 5 ns a token where that is more: the n that makes the sum least
+        const float least = sqrtf((float)pl.W * (float)(p.H / 128) * (p.T <= 20 ? 3.6f : 72.0f / (float)p.T));
+        pl.cut(max(1, min(min((int)gridDim.x, pl.W / FEW_MIN_KB), (int)least)));
     } else {
         const int tiles = pl.A * (p.F / 64), G = gridDim.x;
         pl.kbs = p.H / BK;
@@ -835,10 +839,10 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
         __syncwarp();
     } else if (FP8 && warp == 6) {
         // ------------------------------------------------------------ scales (MXFP8)
-        // A group is 64 scale bytes (16 k-blocks) of every row of a tile: 128 weight rows, bn token
-        // rows. Landed, it is rearranged in place into 16 chunks for tcgen05.cp .32x128b: chunk w
-        // has k-block w's words, the word of row 32 j + lane at lane * 4 + j; first the weights' 512
-        // bytes, then the tokens'. Loads and rearranging do not wait for one another.
+        // A group is the scale bytes of FEW_SF_KB k-blocks of every row of a tile: 128 weight rows, bn token
+        // rows. Landed, it is rearranged in place into a chunk per k-block for tcgen05.cp .32x128b: the
+        // word of row 32 j + lane at lane * 4 + j; first the weights' 512 bytes, then the tokens'. Loads
+        // and rearranging do not wait for one another.
         if constexpr (FP8) {
             struct Cursor {
                 FewWalk<FP8, DOWN> wk;
@@ -865,15 +869,16 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                     __all_sync(FULL, ptx::mbar_test_wait(&sm.sf_empty[ld_slot], ld_phase ^ 1u))) {
                     if (lane == 0) {
                         uint8_t* sf = sfring + (size_t)ld_slot * FEW_SF_BYTES;
-                        const int kx = (ld.r.kb0 + ld.kb) / FEW_SF_KB * 64;
-                        ptx::mbar_arrive_expect_tx(&sm.sf_full[ld_slot], (128 + ld.r.bn) * 64);
+                        constexpr int RB = FEW_SF_KB * 4;            // bytes of a row
+                        const int kx = (ld.r.kb0 + ld.kb) / FEW_SF_KB * RB;
+                        ptx::mbar_arrive_expect_tx(&sm.sf_full[ld_slot], (128 + ld.r.bn) * RB);
                         ptx::tma_load_2d(sf, &tmSW, &sm.sf_full[ld_slot], kx, ld.r.row0);
-                        ptx::tma_load_2d(sf + 4096, &tmSW, &sm.sf_full[ld_slot], kx, ld.r.row1);
+                        ptx::tma_load_2d(sf + 64 * RB, &tmSW, &sm.sf_full[ld_slot], kx, ld.r.row1);
                         if constexpr (DOWN) {
                             for (int i = 0; i < ld.r.bn; i += 16)
-                                ptx::tma_load_2d(sf + 8192 + i * 64, &tmST, &sm.sf_full[ld_slot], kx, ld.r.brow + i);
+                                ptx::tma_load_2d(sf + (128 + i) * RB, &tmST, &sm.sf_full[ld_slot], kx, ld.r.brow + i);
                         } else {
-                            ptx::tma_load_2d(sf + 8192, &tmST, &sm.sf_full[ld_slot], kx, 0);
+                            ptx::tma_load_2d(sf + 128 * RB, &tmST, &sm.sf_full[ld_slot], kx, 0);
                         }
                     }
                     __syncwarp();
@@ -885,16 +890,17 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                 if (loaded > 0 && __all_sync(FULL, ptx::mbar_test_wait(&sm.sf_full[pr_slot], pr_phase))) {
                     uint8_t* sf = sfring + (size_t)pr_slot * FEW_SF_BYTES;
                     const uint4* l = reinterpret_cast<const uint4*>(sf);
-                    uint4 v[6][4];                   // row 32 j + lane: words of k-blocks 4 i ..
+                    constexpr int Q = FEW_SF_KB / 4;
+                    uint4 v[6][Q];                   // row 32 j + lane: words of k-blocks 4 i ..
 #pragma unroll
                     for (int j = 0; j < 6; j++)
 #pragma unroll
-                        for (int i = 0; i < 4; i++) v[j][i] = l[(32 * j + lane) * 4 + i];
+                        for (int i = 0; i < Q; i++) v[j][i] = l[(32 * j + lane) * Q + i];
                     __syncwarp();
                     uint4* out = reinterpret_cast<uint4*>(sf);
 #pragma unroll
                     for (int w = 0; w < FEW_SF_KB; w++) {
-                        auto word = [w](const uint4 (&q)[4]) {
+                        auto word = [w](const uint4 (&q)[Q]) {
                             const uint4& u = q[w / 4];
                             return w % 4 == 0 ? u.x : w % 4 == 1 ? u.y : w % 4 == 2 ? u.z : u.w;
                         };
@@ -954,8 +960,8 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             return sm.ticket;
         };
         if constexpr (!DOWN) {
-        // lanes 0-63 hold the gate products, 64-127 the same columns' linear ones; those go over
-        // through shared memory, FEW_XCH tokens at a time, two buffers in turn
+        // lanes 0-63 hold the gate products, 64-127 the same columns' linear ones; FEW_XCH tokens at a
+        // time, two exchange buffers in turn
         int xb = 0;
         while (have) {
             ok = ptx::wait_parity(&sm.tfull[buf], tphase, s_abort);
@@ -968,12 +974,12 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             // the next up to 16 tokens' columns of the accumulator
             auto load16 = [&](unsigned long long& m, uint32_t* v) {
 #pragma unroll
+                for (int i = 0; i < FEW_XCH; i++) v[i] = 0u;
+#pragma unroll
                 for (int i = 0; i < FEW_XCH; i++) {
-                    v[i] = 0u;
-                    if (m) {                             // uniform
-                        v[i] = tmem_ld_x1(tq + (uint32_t)(buf * FEW_ACC_COLS + __ffsll((long long)m) - 1));
-                        m &= m - 1;
-                    }
+                    if (!m) break;                       // uniform
+                    v[i] = tmem_ld_x1(tq + (uint32_t)(buf * FEW_ACC_COLS + __ffsll((long long)m) - 1));
+                    m &= m - 1;
                 }
                 tmem_wait16(v);
             };
@@ -1017,27 +1023,31 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
 #pragma unroll
                         for (int i = 0; i < FEW_XCH; i++) v[i] = __float_as_uint(f[i]);
                     }
-                    if (q >= 2) {
+                    // gate and linear lanes each finish every other token: the other half's value comes through
+                    // shared memory
+                    const int col = row & 63;
+                    const bool gate = q < 2;
+                    const int other = gate ? 1 : 0;          // parity of the tokens that go over
 #pragma unroll
-                        for (int i = 0; i < FEW_XCH; i++)
-                            if (i < n) sm.xch[xb][i][row - 64] = __uint_as_float(v[i]);
+                    for (int i = 0; i < FEW_XCH; i += 2) {
+                        if (i + other >= n) break;
+                        sm.xch[xb][i + other][col] = __uint_as_float(gate ? v[i + 1] : v[i]);
                     }
                     epi_sync();
-                    if (q < 2) {
+                    size_t o = (size_t)(pl.off[r.a] + i0 + 1 - other) * p.F + r.tile % (p.F / 64) * 64 + col;
 #pragma unroll
-                        for (int i = 0; i < FEW_XCH; i++) {
-                            if (i >= n) break;
-                            const float ga = __uint_as_float(v[i]);
-                            const float h = ga / (1.0f + expf(-ga)) * sm.xch[xb][i][row];
-                            const size_t o = (size_t)(pl.off[r.a] + i0 + i) * p.F + r.tile % (p.F / 64) * 64 + row;
-                            if constexpr (FP8) {
-                                const float amax = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(fabsf(h))));
-                                const int sbyte = e8m0_scale_byte(amax);
-                                static_cast<uint8_t*>(p.h)[o] = (uint8_t)f32x2_to_e4m3x2(h * e8m0_inv_scale(sbyte), 0.0f);
-                                if (lane == 0) p.hs[o >> 5] = (uint8_t)sbyte;
-                            } else {
-                                static_cast<__nv_bfloat16*>(p.h)[o] = __float2bfloat16_rn(h);
-                            }
+                    for (int i = 0; i < FEW_XCH; i += 2, o += 2 * p.F) {
+                        if (i + 1 - other >= n) break;
+                        const float here = __uint_as_float(gate ? v[i] : v[i + 1]), there = sm.xch[xb][i + 1 - other][col];
+                        const float ga = gate ? here : there, li = gate ? there : here;
+                        const float h = __fdividef(ga, 1.0f + __expf(-ga)) * li;
+                        if constexpr (FP8) {
+                            const float amax = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(fabsf(h))));
+                            const int sbyte = e8m0_scale_byte(amax);
+                            static_cast<uint8_t*>(p.h)[o] = (uint8_t)f32x2_to_e4m3x2(h * e8m0_inv_scale(sbyte), 0.0f);
+                            if (lane == 0) p.hs[o >> 5] = (uint8_t)sbyte;
+                        } else {
+                            static_cast<__nv_bfloat16*>(p.h)[o] = __float2bfloat16_rn(h);
                         }
                     }
                     xb ^= 1;
@@ -1211,8 +1221,8 @@ moe_status few_launch(FewArgs a, const PrepArgs& p, const void* x, const uint8_t
         !make_operand_map(&tx, x, FP8, a.H, a.T, a.nb) || !make_operand_map(&th, a.h, FP8, a.F, rh, 16))
         return MOE_ERR_CUDA;
     if (FP8) {
-        if (!make_scale_map(&ts13, w13s, a.H / 32, r13, 64, 64) || !make_scale_map(&ts2, w2s, a.F / 32, r2, 64, 64) ||
-            !make_scale_map(&tsx, xs, a.H / 32, a.T, a.nb, 64) || !make_scale_map(&tsh, a.hs, a.F / 32, rh, 16, 64))
+        if (!make_scale_map(&ts13, w13s, a.H / 32, r13, 64, FEW_SF_KB * 4) || !make_scale_map(&ts2, w2s, a.F / 32, r2, 64, FEW_SF_KB * 4) ||
+            !make_scale_map(&tsx, xs, a.H / 32, a.T, a.nb, FEW_SF_KB * 4) || !make_scale_map(&tsh, a.hs, a.F / 32, rh, 16, FEW_SF_KB * 4))
             return MOE_ERR_CUDA;
     } else {
         ts13 = ts2 = tsx = tsh = tw13;
