@@ -856,25 +856,25 @@ def _grad_norm_clip(grads, outs, max_norm, eps, norm, workspace, stream):
     n = len(grads)
     if not all([t.is_cuda for t in grads]):
         raise ValueError("gradients must be CUDA tensors")
-    if not all([t.is_contiguous() for t in grads]):
+    if not all(map(torch.Tensor.is_contiguous, grads)):
         raise ValueError("gradients must be contiguous")
     dtypes = [t.dtype for t in grads]
     codes = [_FLOAT_CODES.get(d) for d in dtypes]
     if None in codes:
         raise ValueError("gradients must be bfloat16 or float32")
-    counts = [t.numel() for t in grads]
-    ptrs = array("q", [t.data_ptr() for t in grads])
+    counts = list(map(torch.Tensor.numel, grads))
+    ptrs = array("q", map(torch.Tensor.data_ptr, grads))
     out_at = None
     if outs is grads:
         out_at = ptrs.buffer_info()[0]
     elif outs is not None:
         if len(outs) != n:
             raise ValueError("out must have one tensor per gradient")
-        if [t.numel() for t in outs] != counts or [t.dtype for t in outs] != dtypes:
+        if list(map(torch.Tensor.numel, outs)) != counts or [t.dtype for t in outs] != dtypes:
             raise ValueError("outputs must have the gradients' sizes and types")
-        if not all([t.is_cuda for t in outs]) or not all([t.is_contiguous() for t in outs]):
+        if not all([t.is_cuda for t in outs]) or not all(map(torch.Tensor.is_contiguous, outs)):
             raise ValueError("outputs must be contiguous CUDA tensors")
-        optrs = array("q", [t.data_ptr() for t in outs])
+        optrs = array("q", map(torch.Tensor.data_ptr, outs))
         out_at = optrs.buffer_info()[0]
     if norm is None:
         if n == 0:

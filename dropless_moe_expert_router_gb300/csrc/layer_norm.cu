@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(1024) ln_columns_kernel(const float* __restric
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
     float a = 0.0f, b = 0.0f;
     if (c < H) {
-#pragma unroll 4
+#pragma unroll 8
         for (int i = y; i < n; i += 32) {
             a += part[(size_t)i * 2 * H + c];
             b += part[((size_t)i * 2 + 1) * H + c];
