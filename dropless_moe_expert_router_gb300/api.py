@@ -64,6 +64,11 @@ def _want(t: torch.Tensor, name: str, dtype=None, ndim=None):
         raise ValueError(f"{name} must have {ndim} dims")
 
 
+def _scratch(t: torch.Tensor) -> None:
+    if not (t.is_cuda and t.dtype is torch.uint8 and t.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
+
+
 def _id_code(dtype: torch.dtype) -> int:
     if dtype == torch.int16:
         return MOE_I16
@@ -716,26 +721,25 @@ def moe_layer_few_tokens(x: torch.Tensor, logits: Optional[torch.Tensor], w: Pac
     if H != w.H:
         raise ValueError(f"x must have {w.H} columns")
     if logits is not None:
-        _want(logits, "logits", torch.float32, 2)
-        if logits.shape[0] != T or logits.shape[1] != w.E:
-            raise ValueError("logits must be [T, E]")
+        _like(logits, "logits", torch.float32, (T, w.E))
     elif ids is None or probs is None:
         raise ValueError("without logits, ids and probs are inputs")
-    for t, n, dt in ((ids, "ids", None), (probs, "probs", torch.float32)):
-        if t is not None:
-            _want(t, n, dt, 2)
-            if t.shape != (T, K):
-                raise ValueError(f"{n} must be [T, K]")
     if ids is None:
         ids = torch.empty((T, K), dtype=id_dtype, device=x.device)
+    else:
+        _like(ids, "ids", ids.dtype, (T, K))
     if probs is None:
         probs = torch.empty((T, K), dtype=torch.float32, device=x.device)
+    else:
+        _like(probs, "probs", torch.float32, (T, K))
     if y is None:
         y = torch.empty_like(x)
     else:
-        _like(y, x, "y")
+        _like(y, "y", torch.bfloat16, (T, H))
     if workspace is None:
         workspace = moe_layer_few_tokens_workspace(w, T, K)
+    else:
+        _scratch(workspace)
     st = _lib.load().moe_layer_few_tokens(
         x.data_ptr(), T, H, _at(logits), K, w.E, w.F, w.w13.data_ptr(), _at(w.w13_scales), w.w2.data_ptr(),
         _at(w.w2_scales), _dt_code(w.precision), ids.data_ptr(), _id_code(ids.dtype), probs.data_ptr(), y.data_ptr(),
@@ -755,20 +759,12 @@ def _float_code(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _like(t: Optional[torch.Tensor], ref: torch.Tensor, name: str, shape=None) -> None:
-    """t, where given, is a contiguous CUDA tensor of ref's type and of the shape (ref's by default)."""
-    if t is None:
+def _like(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape) -> None:
+    """t, where given, is a contiguous CUDA tensor of this type and shape."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
         return
-    _want(t, name, ref.dtype, None)
-    if t.shape != (ref.shape if shape is None else shape):
-        raise ValueError(f"{name} must be {list(ref.shape if shape is None else shape)}")
-
-
-def _stat(t: Optional[torch.Tensor], name: str, T: int) -> None:
-    if t is not None:
-        _want(t, name, torch.float32, 1)
-        if t.numel() != T:
-            raise ValueError(f"{name} must be [T]")
+    _want(t, name, dtype, None)
+    raise ValueError(f"{name} must be {list(shape)}")
 
 
 class LayerNormed(NamedTuple):
@@ -784,26 +780,30 @@ def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
                    rstd: Optional[torch.Tensor] = None, stream=None) -> LayerNormed:
     """Layer norm of x (+ residual) [T, H] bf16 or fp32 with weight (and bias) [H] bf16 or fp32."""
     _want(x, "x", None, 2)
-    T, H = x.shape
+    shape, dtype = x.shape, x.dtype
+    T, H = shape
     code, wcode = _float_code(x, "x"), _float_code(weight, "weight")
-    _like(weight, weight, "weight", (H,))
-    _like(bias, weight, "bias", (H,))
-    _like(residual, x, "residual")
-    _like(y, x, "y")
-    _like(sum, x, "sum")
-    _stat(mean, "mean", T)
-    _stat(rstd, "rstd", T)
+    _like(weight, "weight", weight.dtype, (H,))
+    _like(bias, "bias", weight.dtype, (H,))
+    _like(residual, "residual", dtype, shape)
     if y is None:
         y = torch.empty_like(x)
-    if residual is None:
-        if sum is not None:
+    else:
+        _like(y, "y", dtype, shape)
+    if sum is not None:
+        if residual is None:
             raise ValueError("sum goes with residual")
-    elif sum is None:
+        _like(sum, "sum", dtype, shape)
+    elif residual is not None:
         sum = torch.empty_like(x)
     if mean is None:
         mean = torch.empty(T, dtype=torch.float32, device=x.device)
+    else:
+        _like(mean, "mean", torch.float32, (T,))
     if rstd is None:
         rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    else:
+        _like(rstd, "rstd", torch.float32, (T,))
     st = _lib.load().moe_layer_norm(x.data_ptr(), _at(residual), T, H, code, weight.data_ptr(), _at(bias), wcode, eps,
                                     _at(sum), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, x))
     _check("moe_layer_norm", st)
@@ -822,26 +822,32 @@ def moe_layer_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Ten
     """dy, s [T, H] (s: LayerNormed.sum), mean, rstd [T] -> (dx [T, H], dweight [H], dbias [H]);
     dx_add [T, H]: the gradient that reaches s past the norm, added to dx."""
     _want(s, "s", None, 2)
-    T, H = s.shape
+    shape, dtype, wdtype = s.shape, s.dtype, weight.dtype
+    T, H = shape
     code, wcode = _float_code(s, "s"), _float_code(weight, "weight")
-    _like(weight, weight, "weight", (H,))
     if dy is None or mean is None or rstd is None:
         raise ValueError("dy, mean and rstd must be given")
-    _like(dy, s, "dy")
-    _like(dx_add, s, "dx_add")
-    _like(dx, s, "dx")
-    _like(dweight, weight, "dweight", (H,))
-    _like(dbias, weight, "dbias", (H,))
-    _stat(mean, "mean", T)
-    _stat(rstd, "rstd", T)
+    _like(weight, "weight", wdtype, (H,))
+    _like(dy, "dy", dtype, shape)
+    _like(mean, "mean", torch.float32, (T,))
+    _like(rstd, "rstd", torch.float32, (T,))
+    _like(dx_add, "dx_add", dtype, shape)
     if dx is None:
         dx = torch.empty_like(s)
+    else:
+        _like(dx, "dx", dtype, shape)
     if dweight is None:
         dweight = torch.empty_like(weight)
+    else:
+        _like(dweight, "dweight", wdtype, (H,))
     if dbias is None:
         dbias = torch.empty_like(weight)
+    else:
+        _like(dbias, "dbias", wdtype, (H,))
     if workspace is None:
         workspace = torch.empty(moe_layer_norm_backward_workspace_size(T, H), dtype=torch.uint8, device=s.device)
+    else:
+        _scratch(workspace)
     st = _lib.load().moe_layer_norm_backward(dy.data_ptr(), s.data_ptr(), T, H, code, weight.data_ptr(), wcode,
                                              mean.data_ptr(), rstd.data_ptr(), _at(dx_add), dx.data_ptr(),
                                              dweight.data_ptr(), dbias.data_ptr(), workspace.data_ptr(),
@@ -887,6 +893,8 @@ def _grad_norm_clip(grads, outs, max_norm, eps, norm, workspace, stream):
     L = _lib.load()
     if workspace is None:
         workspace = torch.empty(L.moe_grad_norm_workspace_size(n), dtype=torch.uint8, device=norm.device)
+    else:
+        _scratch(workspace)
     counts, codes = array("q", counts), array("i", codes)
     st = L.moe_grad_norm_clip(ptrs.buffer_info()[0], counts.buffer_info()[0], codes.buffer_info()[0], out_at, n,
                               max_norm, eps, norm.data_ptr(), workspace.data_ptr(), workspace.numel(),

@@ -109,3 +109,22 @@ def test_block_refusals():
         _block(dict(p, router=p["router"][:2]), 8, 2)
     with pytest.raises(api.MoeError):
         blk.step(torch.zeros((65, 256), dtype=torch.bfloat16, device="cuda"))
+
+
+def test_workspaces_of_another_kind_are_refused():
+    """A workspace on the host, of another type, or with gaps never reaches a kernel."""
+    p = _params(4, 256, 128, seed=5)
+    blk = _block(p, 8, 2)
+    x = torch.zeros((2, 256), dtype=torch.bfloat16, device="cuda")
+    lg = torch.zeros((2, 4), device="cuda")
+    w = torch.ones(256, device="cuda")
+    o = api.moe_layer_norm(x, w)
+    n = 1 << 22
+    for ws in (torch.empty(n, dtype=torch.uint8), torch.empty(n, device="cuda"),
+               torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            api.moe_layer_few_tokens(x, lg, blk.layer.weights, 2, workspace=ws)
+        with pytest.raises(ValueError):
+            api.moe_layer_norm_backward(x, x, w, o.mean, o.rstd, workspace=ws)
+        with pytest.raises(ValueError):
+            api.moe_grad_norm([x], workspace=ws)
