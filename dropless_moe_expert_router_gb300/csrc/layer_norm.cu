@@ -4,7 +4,8 @@
 // Forward, per row: s = x (+ residual), mean = sum s / H, rstd = 1 / sqrt(sum (s - mean)^2 / H + eps),
 // y = (s - mean) rstd w + b. Backward, with xh = (s - mean) rstd and g = dy w:
 // dx = rstd (g - sum(g) / H - xh sum(g xh) / H) (+ dx_add), dw = sum_t dy xh, db = sum_t dy.
-// Each operand is read once and each output written once: the bytes bound both directions.
+// Each operand is read once and each output written once: the bytes bound both directions. A single row
+// is latency: 3.8 us at 1 x 4096.
 #include "common.cuh"
 #include "sm100_ptx.cuh"
 
@@ -78,7 +79,9 @@ __device__ __forceinline__ void row_sum(float (&v)[N], bool warp_row, float* red
 // ---------------------------------------------------------------------------
 // Forward, the row in registers: a row belongs to a warp (warp_row: 8 rows a CTA) or to a CTA, NV
 // pieces of VEC elements per thread, piece i at i * threads + thread. CTAs walk the rows with the
-// grid's stride; weight and bias come from L1.
+// grid's stride; weight and bias come from L1. For short rows, and for rows off the 16-byte boundary where
+// they are short or few or not off it alike; the others take the ring below (ln_shape has the rules; 8192 x 4096
+// with a residual took 57 us this way, 47 us by the ring).
 // ---------------------------------------------------------------------------
 template <typename T, typename W, int VEC, int NV>
 __global__ void __launch_bounds__(512) ln_forward_kernel(const T* x, const T* residual, int rows, int H, bool warp_row,
@@ -316,9 +319,54 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const T* dy, const 
 // Rows through shared memory. A CTA takes R consecutive rows at a time; their operands arrive by
 // bulk copies, a ring of stages ahead, so that enough bytes are in flight without holding them in
 // registers, and one barrier per R rows joins the warps' sums (it also says that everybody has
-// read the stage before: thread 0 refills it then). Thread pieces as above: piece i at
+// read the stage before: in the forward thread 0 refills it then). Thread pieces as above: piece i at
 // i * threads + thread.
 // ---------------------------------------------------------------------------
+// Rows of a CTA and their parts. Where every row starts on a 16-byte boundary, piece c is its elements c * VEC
+// ... and a CTA takes R consecutive rows at a time. Else (ODD; every row tensor is off the boundary alike) a row
+// is `head` elements up to its first boundary, n pieces, which the bulk copies bring, and `tail` elements past the
+// last one; a lane for each of those, in the CTA's last warp, moves them itself, a group of rows ahead. Rows t and
+// t + period start alike: a CTA takes only rows of one head, so that a thread's columns are the same in all.
+template <bool ODD>
+struct LnRows {
+    int n, head;
+    int edge;                         // the column of this thread's single element, or -1
+    int period, first;                // row(u) = u * period + first
+    long long count;                  // rows of this head
+    __device__ LnRows(const void* base, int size, int rows, int H, int period_, int tpr) : n(H * size / 16), head(0), edge(-1), period(1), first(0), count(rows) {
+        if constexpr (ODD) {
+            const int vec = 16 / size;
+            period = period_;
+            first = (int)(blockIdx.x % period);
+            count = ((long long)rows - first + period - 1) / period;
+            head = vec - 1 - (int)(((reinterpret_cast<uintptr_t>(base) & 15) / size + (long long)first * H + vec - 1) % vec);
+            n = (H - head) / vec;
+            const int q = tpr - 1 - (int)threadIdx.x, tail = H - head - n * vec;
+            if (q >= 0 && q < head) edge = q;
+            else if (q >= 8 && q - 8 < tail) edge = head + n * vec + q - 8;
+        }
+    }
+    __device__ long long row(long long u) const { return ODD ? u * period + first : u; }
+    __device__ long long begin() const { return ODD ? blockIdx.x / period : blockIdx.x; }
+    __device__ long long step() const { return ODD ? gridDim.x / period : gridDim.x; }
+    __device__ bool single() const { return ODD && edge >= 0; }
+};
+
+// Columns of weight or bias that belong to piece c.
+template <typename W, int VEC, bool ODD>
+__device__ __forceinline__ Vec<W, VEC> ln_column(const LnRows<ODD>& l, const W* w, int c) {
+    if constexpr (ODD) {
+        Vec<W, VEC> v;
+        float f[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; j++) f[j] = to_f(w[l.head + c * VEC + j]);
+        v.set(f);
+        return v;
+    } else {
+        return reinterpret_cast<const Vec<W, VEC>*>(w)[c];
+    }
+}
+
 struct LnRing {
     uint64_t full[LN_STAGES];
     uint32_t abort_flag;
@@ -343,35 +391,49 @@ __device__ __forceinline__ void ring_drain(LnRing& ring, int stages, int done) {
 }
 
 // Forward. The variance is joined from each warp's sum of squares about its own mean (no cancellation,
-// one barrier): sum (s - mean)^2 = sum over warps of (their M2 + n_w (mean_w - mean)^2).
-template <typename T, typename W, int VEC, int NV, int R>
+// one barrier): sum (s - mean)^2 = sum over warps of (their M2 + n_w (mean_w - mean)^2). 8192 x 4096 bf16
+// with a residual, 268 MB: 47-48 us, 5.6-5.7 TB/s; a device-to-device copy of as many bytes takes 48 us.
+template <typename T, typename W, int VEC, int NV, int R, bool ODD>
 __global__ void __launch_bounds__(512, NV == 2 && R == 1 ? 2 : 1) ln_forward_ring_kernel(const T* x, const T* residual, int rows, int H,
                                                               const W* __restrict__ w, const W* __restrict__ b,
                                                               float eps, T* sum, T* y, float* mean_out, float* rstd_out,
-                                                              int stages) {
+                                                              int stages, int period, uint32_t rb) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ LnRing ring;
     __shared__ float2 red[2][16 * R];         // (mean, M2) of every warp and row
     __shared__ float count[16];               // elements of a row that a warp has
     using V = Vec<T, VEC>;
-    const int tpr = blockDim.x, me = threadIdx.x, n = H / VEC, lane = (int)lane_id();
-    const uint32_t rb = (uint32_t)(H * sizeof(T));
+    const LnRows<ODD> l(x, sizeof(T), rows, H, period, blockDim.x);
+    const int tpr = blockDim.x, me = threadIdx.x, n = l.n, lane = (int)lane_id();
     const int entry = lane & (16 * R - 1);    // this lane's of red: warp entry / R, row entry % R
     const int nt = residual ? 2 : 1;
     const uint32_t stage_bytes = nt * R * rb;
-    const long long groups = ((long long)rows + R - 1) / R, step = gridDim.x;
+    const long long groups = (l.count + R - 1) / R, step = l.step();
     auto issue = [&](long long g, int st) {
         uint8_t* d = smem + (size_t)st * stage_bytes;
-        const long long t = g * R;
-        const uint32_t nb = (uint32_t)(rows - t < R ? rows - t : R) * rb;
-        ptx::mbar_arrive_expect_tx(&ring.full[st], nt * nb);
-        ptx::bulk_load(d, x + t * H, nb, &ring.full[st]);
-        if (residual) ptx::bulk_load(d + R * rb, residual + t * H, nb, &ring.full[st]);
+        const long long u = g * R;
+        const int nr = (int)(l.count - u < R ? l.count - u : R);
+        if constexpr (ODD) {
+            const uint32_t nb = (uint32_t)l.n * 16u;
+            ptx::mbar_arrive_expect_tx(&ring.full[st], nt * nr * nb);
+#pragma unroll
+            for (int k = 0; k < R; k++) {
+                if (k >= nr) continue;
+                const long long at = l.row(u + k) * H + l.head;
+                ptx::bulk_load(d + k * rb, x + at, nb, &ring.full[st]);
+                if (residual) ptx::bulk_load(d + (R + k) * rb, residual + at, nb, &ring.full[st]);
+            }
+        } else {
+            const uint32_t nb = (uint32_t)nr * rb;
+            ptx::mbar_arrive_expect_tx(&ring.full[st], nt * nb);
+            ptx::bulk_load(d, x + u * H, nb, &ring.full[st]);
+            if (residual) ptx::bulk_load(d + R * rb, residual + u * H, nb, &ring.full[st]);
+        }
     };
     ring_init(ring, stages);
     if (me == 0)
         for (int i = 0; i < stages; i++)
-            if (blockIdx.x + i * step < groups) issue(blockIdx.x + i * step, i);
+            if (l.begin() + i * step < groups) issue(l.begin() + i * step, i);
     Vec<W, VEC> wv[NV], bv[NV];
     int mine = 0;
 #pragma unroll
@@ -379,9 +441,26 @@ __global__ void __launch_bounds__(512, NV == 2 && R == 1 ? 2 : 1) ln_forward_rin
         const int c = me + i * tpr;
         if (c < n) {
             mine += VEC;
-            wv[i] = reinterpret_cast<const Vec<W, VEC>*>(w)[c];
-            if (b) bv[i] = reinterpret_cast<const Vec<W, VEC>*>(b)[c];
+            wv[i] = ln_column<W, VEC>(l, w, c);
+            if (b) bv[i] = ln_column<W, VEC>(l, b, c);
         }
+    }
+    // single elements: (x, residual) of the group to come
+    float ew = 0.0f, eb = 0.0f, ex[R], er[R];
+    auto fetch = [&](long long g) {
+#pragma unroll
+        for (int k = 0; k < R; k++)
+            if (l.single() && g * R + k < l.count) {
+                const long long at = l.row(g * R + k) * H + l.edge;
+                ex[k] = to_f(x[at]);
+                if (residual) er[k] = to_f(residual[at]);
+            }
+    };
+    if (l.single()) {
+        mine++;
+        ew = to_f(w[l.edge]);
+        if (b) eb = to_f(b[l.edge]);
+        fetch(l.begin());
     }
     const int nw = __reduce_add_sync(FULL, mine);
     if (me < 16) count[me] = 0.0f;
@@ -391,13 +470,13 @@ __global__ void __launch_bounds__(512, NV == 2 && R == 1 ? 2 : 1) ln_forward_rin
     const float per_nw = nw ? 1.0f / (float)nw : 0.0f, per_h = 1.0f / (float)H;
     int st = 0, done = 0;
     uint32_t phase = 0;
-    for (long long g = blockIdx.x; g < groups; g += step, done++) {
+    for (long long g = l.begin(); g < groups; g += step, done++) {
         ptx::wait_parity(&ring.full[st], phase, &ring.abort_flag);
         const uint8_t* base = smem + (size_t)st * stage_bytes;
-        const int nr = (int)(rows - g * R < R ? rows - g * R : R);
+        const int nr = (int)(l.count - g * R < R ? l.count - g * R : R);
         float2* rd = red[done & 1];
         V xv[R][NV];
-        float sw[R], qw[R];
+        float sw[R], qw[R], es[R];
 #pragma unroll
         for (int k = 0; k < R; k++) {
             sw[k] = 0.0f;
@@ -413,12 +492,22 @@ __global__ void __launch_bounds__(512, NV == 2 && R == 1 ? 2 : 1) ln_forward_rin
 #pragma unroll
                     for (int j = 0; j < VEC; j++) f[j] = xv[k][i].get(j) + rv.get(j);
                     xv[k][i].set(f);
-                    reinterpret_cast<V*>(sum + (g * R + k) * H)[c] = xv[k][i];
+                    reinterpret_cast<V*>(sum + l.row(g * R + k) * H + l.head)[c] = xv[k][i];
                 }
 #pragma unroll
                 for (int j = 0; j < VEC; j++) sw[k] += xv[k][i].get(j);
             }
+            if (l.single()) {
+                es[k] = ex[k];
+                if (residual) {
+                    const T v = from_f<T>(ex[k] + er[k]);
+                    sum[l.row(g * R + k) * H + l.edge] = v;
+                    es[k] = to_f(v);
+                }
+                sw[k] += es[k];
+            }
         }
+        if (l.single()) fetch(g + step);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
@@ -436,6 +525,7 @@ __global__ void __launch_bounds__(512, NV == 2 && R == 1 ? 2 : 1) ln_forward_rin
                         const float d = xv[k][i].get(j) - sw[k];
                         qw[k] = fmaf(d, d, qw[k]);
                     }
+            if (l.single()) qw[k] = fmaf(es[k] - sw[k], es[k] - sw[k], qw[k]);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -474,11 +564,12 @@ __global__ void __launch_bounds__(512, NV == 2 && R == 1 ? 2 : 1) ln_forward_rin
                 for (int j = 0; j < VEC; j++)
                     f[j] = fmaf((xv[k][i].get(j) - mean) * rstd, wv[i].get(j), b ? bv[i].get(j) : 0.0f);
                 o.set(f);
-                reinterpret_cast<V*>(y + (g * R + k) * H)[c] = o;
+                reinterpret_cast<V*>(y + l.row(g * R + k) * H + l.head)[c] = o;
             }
+            if (l.single()) y[l.row(g * R + k) * H + l.edge] = from_f<T>(fmaf((es[k] - mean) * rstd, ew, eb));
             if (me == 0) {
-                if (mean_out) mean_out[g * R + k] = mean;
-                if (rstd_out) rstd_out[g * R + k] = rstd;
+                if (mean_out) mean_out[l.row(g * R + k)] = mean;
+                if (rstd_out) rstd_out[l.row(g * R + k)] = rstd;
             }
         }
         if (++st == stages) { st = 0; phase ^= 1u; }
@@ -520,22 +611,25 @@ __device__ __forceinline__ void cta_sums(float (&v)[2 * R], float2* red, int thr
 
 // Backward. A warp of its own fills the ring, a stage per row, as soon as the computing warps have let go of
 // the row that was there; those take R rows at a time. dweight and dbias add up in the threads' registers
-// over the CTA's rows and leave as one partial sum per CTA: part [gridDim.x][2][H].
-template <typename T, typename W, int VEC, int NV, int R>
+// over the CTA's rows and leave as one partial sum per CTA: part [gridDim.x][2][H]. 8192 x 7168 bf16 with
+// dx_add, 470 MB: 86-88 us with the columns' kernel, 5.4 TB/s; a copy of as many bytes takes 77 us. (Refilled by
+// thread 0 between the barriers, as in the forward, it took 98 us.)
+template <typename T, typename W, int VEC, int NV, int R, bool ODD>
 __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, const T* s, int rows, int H,
                                                                const W* __restrict__ w, const float* __restrict__ mean,
                                                                const float* __restrict__ rstd, const T* add, T* dx,
-                                                               float* part, int stages) {
+                                                               float* part, int stages, int period, uint32_t rb) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[LN_STAGES], empty[LN_STAGES];
     __shared__ uint32_t abort_flag;
     __shared__ float2 red[2][16 * R];
+    __shared__ float4 own[ODD ? R : 1][ODD ? 16 : 1];     // single elements of the group at hand, each its own thread's
     using V = Vec<T, VEC>;
-    const int tpr = blockDim.x - 32, me = threadIdx.x, n = H / VEC;
-    const uint32_t rb = (uint32_t)(H * sizeof(T));
+    const LnRows<ODD> l(s, sizeof(T), rows, H, period, blockDim.x - 32);
+    const int tpr = blockDim.x - 32, me = threadIdx.x, n = l.n;
     const int nt = add ? 3 : 2;
     const uint32_t stage_bytes = nt * rb;
-    const long long groups = ((long long)rows + R - 1) / R, step = gridDim.x;
+    const long long groups = (l.count + R - 1) / R, step = l.step();
     for (int i = me; i < 2 * 16 * R; i += blockDim.x) (&red[0][0])[i] = make_float2(0.0f, 0.0f);
     if (me == 0) {
         for (int i = 0; i < stages; i++) {
@@ -552,15 +646,17 @@ __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, cons
         if (me == tpr) {
             int issued = 0;
             bool ok = true;
-            for (long long g = blockIdx.x; g < groups && ok; g += step)
-                for (long long t = g * R; t < rows && t < (g + 1) * R; t++) {
+            for (long long g = l.begin(); g < groups && ok; g += step)
+                for (long long u = g * R; u < l.count && u < (g + 1) * R; u++) {
                     ok = ptx::wait_parity(&empty[st], phase ^ 1u, &abort_flag);
                     if (!ok) break;
                     uint8_t* d = smem + (size_t)st * stage_bytes;
-                    ptx::mbar_arrive_expect_tx(&full[st], stage_bytes);
-                    ptx::bulk_load(d, dy + t * H, rb, &full[st]);
-                    ptx::bulk_load(d + rb, s + t * H, rb, &full[st]);
-                    if (add) ptx::bulk_load(d + 2 * rb, add + t * H, rb, &full[st]);
+                    const long long at = l.row(u) * H + l.head;
+                    const uint32_t nb = ODD ? (uint32_t)l.n * 16u : rb;
+                    ptx::mbar_arrive_expect_tx(&full[st], nt * nb);
+                    ptx::bulk_load(d, dy + at, nb, &full[st]);
+                    ptx::bulk_load(d + rb, s + at, nb, &full[st]);
+                    if (add) ptx::bulk_load(d + 2 * rb, add + at, nb, &full[st]);
                     issued++;
                     if (++st == stages) { st = 0; phase ^= 1u; }
                 }
@@ -578,7 +674,7 @@ __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, cons
     float dw[NV][VEC], db[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-        if (me + i * tpr < n) wv[i] = reinterpret_cast<const Vec<W, VEC>*>(w)[me + i * tpr];
+        if (me + i * tpr < n) wv[i] = ln_column<W, VEC>(l, w, me + i * tpr);
 #pragma unroll
         for (int j = 0; j < VEC; j++) dw[i][j] = db[i][j] = 0.0f;
     }
@@ -588,16 +684,32 @@ __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, cons
     auto stats = [&](long long g, float* a, float* c) {
 #pragma unroll
         for (int k = 0; k < R; k++) {
-            const long long t = g * R + k < rows ? g * R + k : rows - 1;
+            const long long t = l.row(g * R + k < l.count ? g * R + k : l.count - 1);
             a[k] = __ldg(mean + t);
             c[k] = __ldg(rstd + t);
         }
     };
-    if (blockIdx.x < groups) stats(blockIdx.x, m, r);
+    // single elements: (dy, s, add) of the group to come
+    float ew = 0.0f, edw = 0.0f, edb = 0.0f, eg[R], es[R], ea[R];
+    auto fetch = [&](long long g) {
+#pragma unroll
+        for (int k = 0; k < R; k++)
+            if (l.single() && g * R + k < l.count) {
+                const long long at = l.row(g * R + k) * H + l.edge;
+                eg[k] = to_f(dy[at]);
+                es[k] = to_f(s[at]);
+                if (add) ea[k] = to_f(add[at]);
+            }
+    };
+    if (l.single()) {
+        ew = to_f(w[l.edge]);
+        fetch(l.begin());
+    }
+    if (l.begin() < groups) stats(l.begin(), m, r);
     int buf = 0;
-    for (long long g = blockIdx.x; g < groups; g += step, buf ^= 1) {
+    for (long long g = l.begin(); g < groups; g += step, buf ^= 1) {
         if (g + step < groups) stats(g + step, mn, rn);
-        const int nr = (int)(rows - g * R < R ? rows - g * R : R);
+        const int nr = (int)(l.count - g * R < R ? l.count - g * R : R);
         float sums[2 * R];
         int at[R];
 #pragma unroll
@@ -625,6 +737,19 @@ __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, cons
                 }
             }
         }
+        if (l.single()) {
+#pragma unroll
+            for (int k = 0; k < R; k++) {
+                if (k >= nr) continue;
+                const float xh = fmaf(es[k], r[k], -m[k] * r[k]), q = eg[k] * ew;
+                sums[2 * k] += q;
+                sums[2 * k + 1] = fmaf(q, xh, sums[2 * k + 1]);
+                edw = fmaf(eg[k], xh, edw);
+                edb += eg[k];
+                own[k][tpr - 1 - me] = make_float4(eg[k], es[k], add ? ea[k] : 0.0f, 0.0f);
+            }
+            fetch(g + step);
+        }
         cta_sums<R>(sums, red[buf], tpr);
 #pragma unroll
         for (int k = 0; k < R; k++) {
@@ -648,7 +773,11 @@ __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, cons
                     if (add) f[j] += av.get(j);
                 }
                 o.set(f);
-                reinterpret_cast<V*>(dx + (g * R + k) * H)[c] = o;
+                reinterpret_cast<V*>(dx + l.row(g * R + k) * H + l.head)[c] = o;
+            }
+            if (l.single()) {
+                const float4 e = own[k][tpr - 1 - me];
+                dx[l.row(g * R + k) * H + l.edge] = from_f<T>(fmaf(e.x, r[k] * ew, fmaf(e.y, ks, k0)) + e.z);
             }
             __syncwarp();
             if (lane_id() == 0) ptx::mbar_arrive(&empty[at[k]]);
@@ -659,16 +788,43 @@ __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, cons
     pdl_trigger();
     if (!part) return;
     float* out = part + (size_t)blockIdx.x * 2 * H;
+    if constexpr (ODD) {
+        // by way of the ring, for whole lines (the computing warps have read all of it)
+        float* o = reinterpret_cast<float*>(smem);
+        const int np = n * VEC;
+        asm volatile("bar.sync 1, %0;" ::"r"(tpr) : "memory");
 #pragma unroll
-    for (int i = 0; i < NV; i++)
-        if (me + i * tpr < n) {
-            const int c = (me + i * tpr) * VEC;
-            Vec<float, VEC> o;
-            o.set(dw[i]);
-            *reinterpret_cast<Vec<float, VEC>*>(out + c) = o;
-            o.set(db[i]);
-            *reinterpret_cast<Vec<float, VEC>*>(out + H + c) = o;
+        for (int i = 0; i < NV; i++)
+            if (me + i * tpr < n) {
+                const int c = (me + i * tpr) * VEC;
+#pragma unroll
+                for (int j = 0; j < VEC; j += 4) {
+                    *reinterpret_cast<float4*>(o + c + j) = make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
+                    *reinterpret_cast<float4*>(o + np + c + j) = make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]);
+                }
+            }
+        if (l.single()) {
+            out[l.edge] = edw;
+            out[H + l.edge] = edb;
         }
+        asm volatile("bar.sync 1, %0;" ::"r"(tpr) : "memory");
+#pragma unroll 4
+        for (int i = me; i < np; i += tpr) {
+            out[l.head + i] = o[i];
+            out[H + l.head + i] = o[np + i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (me + i * tpr < n) {
+                const int c = (me + i * tpr) * VEC;
+                Vec<float, VEC> o;
+                o.set(dw[i]);
+                *reinterpret_cast<Vec<float, VEC>*>(out + c) = o;
+                o.set(db[i]);
+                *reinterpret_cast<Vec<float, VEC>*>(out + H + c) = o;
+            }
+    }
 }
 
 // Backward for rows too long for registers: dx with the row read twice ...
@@ -713,6 +869,7 @@ __global__ void __launch_bounds__(256) ln_backward_long_w_kernel(const T* dy, co
 }
 
 // dweight and dbias from n partial sums, 32 columns per CTA: thread row y adds partials y, y + 32, ...
+// Latency, mostly: 8.7 MB in 7.4-8 us (152 partial sums of 7168 columns).
 template <typename W>
 __global__ void __launch_bounds__(1024) ln_columns_kernel(const float* __restrict__ part, int n, int H, W* dw, W* db) {
     __shared__ float red[2][32][33];
@@ -720,10 +877,21 @@ __global__ void __launch_bounds__(1024) ln_columns_kernel(const float* __restric
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
     float a = 0.0f, b = 0.0f;
     if (c < H) {
-#pragma unroll 8
-        for (int i = y; i < n; i += 32) {
-            a += part[(size_t)i * 2 * H + c];
-            b += part[((size_t)i * 2 + 1) * H + c];
+        constexpr int B = 8;                           // of either in flight, the last ones too
+        const float* p = part + (size_t)y * 2 * H + c;
+        const size_t step = (size_t)64 * H;
+        for (int left = n - y; left > 0; left -= 32 * B) {
+            float u[B], v[B];
+#pragma unroll
+            for (int k = 0; k < B; k++, p += step) {
+                u[k] = left > 32 * k ? p[0] : 0.0f;
+                v[k] = left > 32 * k ? p[H] : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < B; k++) {
+                a += u[k];
+                b += v[k];
+            }
         }
     }
     red[0][y][x] = a;
@@ -749,29 +917,60 @@ int ln_sms() {
 
 constexpr int LN_PARTS = 1024;            // most partial sums of dweight and dbias
 
-// How a row is spread over threads: VEC elements a piece, NV pieces a thread, a warp or a CTA per
-// row. nv = 0: it does not fit. ring: it goes through shared memory. wide: rows and pointers allow
-// 16-byte pieces.
-struct LnShape {
-    int nv, threads;
-    bool warp_row, ring;
+// The row tensors (null: not there) and the columns' (weight, bias) against 16 bytes. alike: the rows' are
+// off the boundary alike; wide: every row and column starts on it.
+struct LnAlign {
+    bool alike = true, wide = true;
+    LnAlign(std::initializer_list<const void*> row_tensors, std::initializer_list<const void*> columns, int H, int vec) {
+        const uintptr_t first = reinterpret_cast<uintptr_t>(*row_tensors.begin()) & 15;
+        for (const void* q : row_tensors) alike = alike && (!q || (reinterpret_cast<uintptr_t>(q) & 15) == first);
+        wide = alike && first == 0 && H % vec == 0;
+        for (const void* q : columns) wide = wide && moe_host::aligned(q, 16);
+    }
 };
 
-LnShape ln_shape(int H, int vec, bool wide, bool forward) {
-    const int n = H / vec;
-    auto cta = [&](int nv, bool ring) { return LnShape{nv, (((n + nv - 1) / nv) + 31) / 32 * 32, false, ring}; };
-    if (wide) {
-        if (n <= 32) return {1, 256, true, false};
-        if (n <= 128 && (forward || vec == 4)) return {4, 256, true, false};
-        if (n <= 64) return {2, 256, true, false};
-        if (n <= 1024) return cta(2, true);
-        if (n <= 2048 && (forward || vec == 4)) return cta(4, true);
-        return {0, 512, false, false};
+// How a row is spread over threads: pieces of vec elements, nv a thread, a warp or a CTA per row. nv = 0: it
+// does not fit. ring: it goes through shared memory; odd: with rows off the 16-byte boundary.
+// Both sides of the rules, in us (bf16 unless said; forward with a residual, backward with dx_add):
+//   on the boundary, a warp per row up to 32 pieces: forward 8192 x 256 5.0 (ring 7.3), but 8192 x 512 9.8
+//     (7.1); backward 8192 x 256 11.5 (13.4) but 1000 x 256 9.1 (7.5) and 64 x 256 7.8 (5.0)
+//   off it, forward, element by element: 777 x 511 3.9 (ring 6.1), 8192 x 255 10.7 (11.8), but 777 x 777 6.5
+//     (5.7), 8192 x 1021 42 (18), 777 x 5001 25 (11.7)
+//   off it, backward, element by element: 2000 x 1021 13.4 (15.3), 8192 x 511 22.5 (24.8), 777 x 1021 fp32 8.4
+//     (9.1), but 8192 x 1021 46 (29), 2000 x 777 fp32 12.1 (11.1), 777 x 5001 36 (19.4)
+struct LnShape {
+    int nv, threads;
+    bool warp_row, ring, odd;
+    int period;               // rows t and t + period start alike on the 16-byte boundary
+    uint32_t row_bytes;       // of a row in the ring
+};
+
+LnShape ln_shape(int H, int size, const LnAlign& a, bool forward, int rows) {
+    const int vec = 16 / size;
+    auto cta = [&](int n, int nv) { return LnShape{nv, (((n + nv - 1) / nv) + 31) / 32 * 32, false, false, false, 1, 0u}; };
+    auto ring = [&](int n, bool odd) {
+        LnShape l = cta(n, n <= 1024 ? 2 : 4);
+        l.ring = true;
+        l.odd = odd;
+        while (odd && (long long)l.period * H % vec) l.period *= 2;
+        l.row_bytes = odd ? (uint32_t)n * 16u : (uint32_t)(H * size);
+        return l;
+    };
+    const int most = forward || vec == 4 ? 2048 : 1024;      // pieces
+    if (a.wide) {
+        const int n = H / vec;
+        if (n <= 32 && (forward || rows > 2000)) return {1, 256, true, false, false, 1, 0u};
+        return n <= most ? ring(n, false) : LnShape{0, 512, false, false, false, 1, 0u};
     }
-    if (n <= 128) return {4, 256, true, false};
-    if (n <= 2048) return cta(4, false);
-    if (n <= 8192) return cta(16, false);
-    return {0, 512, false, false};
+    // Element by element while that fits a few registers a thread and the rows are short or few, else whole
+    // pieces by the ring where they are off the boundary alike.
+    if (H <= 128) return {4, 256, true, false, false, 1, 0u};
+    const long long all = (long long)rows * H;
+    const bool little = forward ? H * size <= 512 || all <= 1 << 19 : H * size <= 1024 || all * size <= 1 << 22;
+    if (a.alike && H / vec <= most && !(little && H <= 2048)) return ring(H / vec, true);
+    if (H <= 2048) return cta(H, 4);
+    if (H <= 8192) return cta(H, 16);
+    return {0, 512, false, false, false, 1, 0u};
 }
 
 // Rows per group, ring stages and CTAs per SM of the ring kernels, row_bytes of operands per row.
@@ -780,18 +979,20 @@ struct LnRingShape {
     size_t smem;
 };
 
-// Forward: a stage is a group of two rows where two CTAs of three such stages fit an SM, else one row.
+// Forward: a stage is a group of two rows where two CTAs of three such stages fit an SM, else one row. Not
+// 32 CTAs of one warp, whose starts cost more than they hide: 8192 x 264 bf16 8.2 us, with 16 of them 6.9.
 LnRingShape ln_forward_ring(size_t row_bytes, const LnShape& l) {
     LnRingShape r;
     r.rows = l.nv == 4 || 2 * 3 * 2 * row_bytes > LN_SMEM ? 1 : 2;
     r.stages = 3 * r.rows * row_bytes <= LN_SMEM ? 3 : 2;
     r.smem = r.stages * r.rows * row_bytes;
-    const int fit = (int)(LN_SMEM / (r.smem + 2048)), most = 1024 / l.threads;
+    const int fit = (int)(LN_SMEM / (r.smem + 2048)), most = l.threads < 64 ? 16 : 1024 / l.threads;
     r.ctas = fit < most ? (fit < 1 ? 1 : fit) : most;
     return r;
 }
 
-// Backward: a stage is a row; two rows a group where three fit (long fp32 rows go singly).
+// Backward: a stage is a row; two rows a group where three fit (long fp32 rows go singly, and rows off the
+// boundary of more than 4 KB, whose two would spill: 3000 x 8191 61 us, singly 56.6; 777 x 1021 fp32 8.7 and 9.8).
 LnRingShape ln_backward_ring(size_t row_bytes, const LnShape& l) {
     LnRingShape r;
     const int most = l.threads > 256 ? 1 : 512 / l.threads;     // (128 registers a thread)
@@ -799,9 +1000,16 @@ LnRingShape ln_backward_ring(size_t row_bytes, const LnShape& l) {
     while (r.ctas > 1 && r.ctas * (4 * row_bytes + 2048) > LN_SMEM) r.ctas--;
     r.stages = (int)((LN_SMEM / r.ctas - 2048) / row_bytes);
     if (r.stages > LN_STAGES) r.stages = LN_STAGES;
-    r.rows = l.nv == 4 || r.stages < 3 ? 1 : 2;
+    r.rows = l.nv == 4 || r.stages < 3 || (l.odd && l.row_bytes > 4096) ? 1 : 2;
     r.smem = r.stages * row_bytes;
     return r;
+}
+
+// CTAs of a ring kernel: the same number for each of the period's rows.
+int ln_ring_grid(int rows, int group, int period, long long most) {
+    const long long of_one = (((long long)rows + period - 1) / period + group - 1) / group;
+    most /= period;
+    return (int)(of_one < most ? of_one : most) * period;
 }
 
 template <typename K>
@@ -814,24 +1022,30 @@ template <typename T, typename W>
 moe_status ln_forward(const void* x, const void* residual, int rows, int H, const void* w, const void* b, float eps,
                       void* sum, void* y, float* mean, float* rstd, cudaStream_t s) {
     constexpr int VEC = 16 / sizeof(T);
-    bool wide = H % VEC == 0;
-    for (const void* q : {x, residual, w, b, (const void*)sum, (const void*)y}) wide = wide && moe_host::aligned(q, 16);
-    const LnShape l = ln_shape(H, wide ? VEC : 1, wide, true);
+    const LnAlign align({x, residual, sum, y}, {w, b}, H, VEC);
+    const bool wide = align.wide;
+    const LnShape l = ln_shape(H, sizeof(T), align, true, rows);
     if (l.ring) {
-        const LnRingShape r = ln_forward_ring((size_t)(residual ? 2 : 1) * H * sizeof(T), l);
-        const long long groups = ((long long)rows + r.rows - 1) / r.rows, most = (long long)ln_sms() * r.ctas;
-        const int grid = (int)(groups < most ? groups : most);
-#define MOE_LN_FR(nv, R)                                                                                              \
+        const LnRingShape r = ln_forward_ring((size_t)(residual ? 2 : 1) * l.row_bytes, l);
+        const int grid = ln_ring_grid(rows, r.rows, l.period, (long long)ln_sms() * r.ctas);
+#define MOE_LN_FR(nv, R, odd)                                                                                         \
     {                                                                                                                 \
         static bool allowed = false;                                                                                  \
-        auto kern = ln_forward_ring_kernel<T, W, VEC, nv, R>;                                                         \
+        auto kern = ln_forward_ring_kernel<T, W, VEC, nv, R, odd>;                                                    \
         if (!ln_allow_smem(kern, allowed)) return MOE_ERR_CUDA;                                                       \
         kern<<<grid, l.threads, r.smem, s>>>((const T*)x, (const T*)residual, rows, H, (const W*)w, (const W*)b, eps, \
-                                             (T*)sum, (T*)y, mean, rstd, r.stages);                                   \
+                                             (T*)sum, (T*)y, mean, rstd, r.stages, l.period, l.row_bytes);            \
     }
-        if (l.nv == 2 && r.rows == 2) MOE_LN_FR(2, 2)
-        else if (l.nv == 2) MOE_LN_FR(2, 1)
-        else MOE_LN_FR(4, 1)
+        if (l.nv == 2 && r.rows == 2) {
+            if (l.odd) MOE_LN_FR(2, 2, true)
+            else MOE_LN_FR(2, 2, false)
+        } else if (l.nv == 2) {
+            if (l.odd) MOE_LN_FR(2, 1, true)
+            else MOE_LN_FR(2, 1, false)
+        } else {
+            if (l.odd) MOE_LN_FR(4, 1, true)
+            else MOE_LN_FR(4, 1, false)
+        }
 #undef MOE_LN_FR
         return moe_host::launch_status();
     }
@@ -845,8 +1059,7 @@ moe_status ln_forward(const void* x, const void* residual, int rows, int H, cons
     if (l.nv == 0)
         ln_forward_long_kernel<T, W><<<rows, 512, 0, s>>>((const T*)x, (const T*)residual, H, (const W*)w, (const W*)b,
                                                           eps, (T*)sum, (T*)y, mean, rstd);
-    else if (wide && l.nv == 1) MOE_LN_F(VEC, 1);
-    else if (wide) MOE_LN_F(VEC, 4);
+    else if (wide) MOE_LN_F(VEC, 1);
     else if (l.nv == 4) MOE_LN_F(1, 4);
     else MOE_LN_F(1, 16);
 #undef MOE_LN_F
@@ -857,9 +1070,9 @@ template <typename T, typename W>
 moe_status ln_backward(const void* dy, const void* sv, int rows, int H, const void* w, const float* mean,
                        const float* rstd, const void* add, void* dx, void* dw, void* db, float* part, cudaStream_t s) {
     constexpr int VEC = 16 / sizeof(T);
-    bool wide = H % VEC == 0;
-    for (const void* q : {dy, sv, w, add, (const void*)dx}) wide = wide && moe_host::aligned(q, 16);
-    const LnShape l = ln_shape(H, wide ? VEC : 1, wide, false);
+    const LnAlign align({dy, sv, add, dx}, {w}, H, VEC);
+    const bool wide = align.wide;
+    const LnShape l = ln_shape(H, sizeof(T), align, false, rows);
     const bool sums = dw || db;
     int n_part = 0;
     if (rows == 0) {
@@ -872,22 +1085,32 @@ moe_status ln_backward(const void* dy, const void* sv, int rows, int H, const vo
         ln_backward_long_kernel<T, W><<<rows, 512, 0, s>>>((const T*)dy, (const T*)sv, H, (const W*)w, mean, rstd,
                                                            (const T*)add, (T*)dx);
     } else if (l.ring) {
-        const LnRingShape r = ln_backward_ring((size_t)(add ? 3 : 2) * H * sizeof(T), l);
-        const long long groups = ((long long)rows + r.rows - 1) / r.rows, most = (long long)ln_sms() * r.ctas;
-        n_part = (int)(groups < most ? groups : most);
-        if (n_part > LN_PARTS) n_part = LN_PARTS;
-#define MOE_LN_BR(nv, R)                                                                                            \
+        LnRingShape r = ln_backward_ring((size_t)(add ? 3 : 2) * l.row_bytes, l);
+        if (l.odd && r.smem < (size_t)H * 8) r.smem = (size_t)H * 8;       // (its partial sums leave by it)
+        const int sms = ln_sms();
+        if (sms * r.ctas > LN_PARTS) r.ctas = LN_PARTS / sms;
+        n_part = ln_ring_grid(rows, r.rows, l.period, (long long)sms * r.ctas);
+#define MOE_LN_BR(nv, R, odd)                                                                                       \
     {                                                                                                               \
         static bool allowed = false;                                                                                \
-        auto kern = ln_backward_ring_kernel<T, W, VEC, nv, R>;                                                      \
+        auto kern = ln_backward_ring_kernel<T, W, VEC, nv, R, odd>;                                                 \
         if (!ln_allow_smem(kern, allowed)) return MOE_ERR_CUDA;                                                     \
         kern<<<n_part, l.threads + 32, r.smem, s>>>((const T*)dy, (const T*)sv, rows, H, (const W*)w, mean, rstd,        \
-                                               (const T*)add, (T*)dx, sums ? part : nullptr, r.stages);             \
+                                               (const T*)add, (T*)dx, sums ? part : nullptr, r.stages, l.period,    \
+                                               l.row_bytes);                                                        \
     }
         if (l.nv == 4) {
-            if constexpr (VEC == 4) MOE_LN_BR(4, 1)
-        } else if (r.rows == 2) MOE_LN_BR(2, 2)
-        else MOE_LN_BR(2, 1)
+            if constexpr (VEC == 4) {
+                if (l.odd) MOE_LN_BR(4, 1, true)
+                else MOE_LN_BR(4, 1, false)
+            }
+        } else if (r.rows == 2) {
+            if (l.odd) MOE_LN_BR(2, 2, true)
+            else MOE_LN_BR(2, 2, false)
+        } else {
+            if (l.odd) MOE_LN_BR(2, 1, true)
+            else MOE_LN_BR(2, 1, false)
+        }
 #undef MOE_LN_BR
     } else {
         const long long ctas = l.warp_row ? ((long long)rows + 7) / 8 : rows;
@@ -899,11 +1122,8 @@ moe_status ln_backward(const void* dy, const void* sv, int rows, int H, const vo
     ln_backward_kernel<T, W, vec, nv, pre><<<n_part, l.threads, smem, s>>>((const T*)dy, (const T*)sv, rows, H,       \
                                                                            l.warp_row, (const W*)w, mean, rstd,       \
                                                                            (const T*)add, (T*)dx, sums ? part : nullptr)
-        if (wide && l.nv == 1) MOE_LN_B(VEC, 1, true);
-        else if (wide && l.nv == 2) MOE_LN_B(VEC, 2, true);
-        else if (wide) {
-            if constexpr (VEC == 4) MOE_LN_B(VEC, 4, false);      // (bf16 rows of this length take the ring)
-        } else if (l.nv == 4) MOE_LN_B(1, 4, true);
+        if (wide) MOE_LN_B(VEC, 1, true);
+        else if (l.nv == 4) MOE_LN_B(1, 4, true);
         else MOE_LN_B(1, 16, false);
 #undef MOE_LN_B
     }

@@ -254,3 +254,92 @@ def test_no_rows_and_refusals():
         api.moe_layer_norm_backward(dy, x, w, o.mean[:2], o.rstd)
     with pytest.raises(MoeError):
         api.moe_layer_norm_backward(dy, x, w, o.mean, o.rstd, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+
+
+def _backward_check(got, dy, s, w, mean, rstd, add):
+    T, H = s.shape
+    G, GT = (H / 32 + 64) * U, (T + 64) * U
+    dx, dw, db = got
+    rx, rw, rb, xh, g = _backward_reference(dy, s, w, mean, rstd, add)
+    R = rstd.double()[:, None]
+    exh = 4 * U * (s.double().abs() + mean.double().abs()[:, None]) * R
+    sums = G * (g.abs().mean(1, keepdim=True) + xh.abs() * (g * xh).abs().mean(1, keepdim=True)) \
+        + xh.abs() * (g.abs() * exh).mean(1, keepdim=True)
+    terms = g.abs() + g.mean(1, keepdim=True).abs() + (xh.abs() + exh) * (g * xh).mean(1, keepdim=True).abs()
+    e = R * (sums + 16 * U * terms + exh * (g * xh).mean(1, keepdim=True).abs())
+    if add is not None:
+        e = e + 2 * U * (add.double().abs() + rx.abs())
+    _within(dx, rx, e + 1.01 * _half(s.dtype) * rx.abs() + 1e-38)
+    D = dy.double().abs()
+    _within(dw, rw, GT * (D * xh.abs()).sum(0) + (D * exh).sum(0) + 1.01 * _half(w.dtype) * rw.abs() + 1e-38)
+    _within(db, rb, GT * D.sum(0) + 1.01 * _half(w.dtype) * rb.abs() + 1e-38)
+
+
+class _Fenced:
+    """Contiguous tensors `off` elements past a 16-byte boundary, NaN before and behind them."""
+
+    def __init__(self, off):
+        self.off, self.all = off, []
+
+    def __call__(self, t):
+        n, pre = t.numel(), 64 + self.off
+        buf = torch.full((pre + n + 64,), float("nan"), dtype=t.dtype, device="cuda")
+        v = buf[pre:pre + n].view(t.shape)
+        v.copy_(t)
+        self.all.append((buf, pre, n))
+        return v
+
+    def intact(self):
+        return all(bool(torch.isnan(b[:p]).all()) and bool(torch.isnan(b[p + n:]).all()) for b, p, n in self.all)
+
+
+@pytest.mark.parametrize("dt,wdt,off", [(BF, BF, 0), (BF, F32, 3), (BF, BF, 7), (F32, F32, 0), (F32, BF, 1)])
+@pytest.mark.parametrize("T,H", [(1, 129), (2, 131), (7, 258), (8, 33), (9, 255), (40, 100), (3000, 33), (777, 1021), (23, 2047), (500, 4099),
+                                 (5, 8185), (2, 8191), (3, 8193), (2, 16383), (6, 1024), (3000, 1024), (2100, 1021), (4200, 513),
+                                 (8300, 257)])
+def test_rows_off_the_boundary(T, H, dt, wdt, off):
+    """Rows that start anywhere against 16 bytes: nothing beside a row or a tensor is used or written."""
+    x, w, b, r, dy = _inputs(T, H, dt, wdt, seed=T + 5 * H)
+    at = _Fenced(off)
+    for res in (None, r):
+        s = x if res is None else (x.float() + r.float()).to(dt)
+        o = api.moe_layer_norm(at(x), w, b, residual=None if res is None else at(res), y=at(dy),
+                               sum=None if res is None else at(dy))
+        _forward_check(o, s, w, b, 1e-5)
+        assert res is None or torch.equal(o.sum, s)
+        got = api.moe_layer_norm_backward(at(dy), at(s), w, o.mean, o.rstd, dx_add=None if res is None else at(res), dx=at(x))
+        _backward_check(got, dy, s, w, o.mean, o.rstd, res)
+    assert at.intact()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_rows_off_the_boundary_in_place(dt):
+    x, w, b, r, dy = _inputs(400, 1021, dt, F32, seed=11)
+    want = api.moe_layer_norm(x, w, b, residual=r)
+    x2, r2 = x.clone(), r.clone()
+    got = api.moe_layer_norm(x2, w, b, residual=r2, sum=r2, y=x2)
+    assert torch.equal(got.y, want.y) and torch.equal(r2, want.sum)
+    ref = api.moe_layer_norm_backward(dy, want.sum, w, want.mean, want.rstd, dx_add=r)
+    for alias in ("dy", "add"):
+        d2, a2 = dy.clone(), r.clone()
+        got = api.moe_layer_norm_backward(d2, want.sum, w, want.mean, want.rstd, dx_add=a2, dx=d2 if alias == "dy" else a2)
+        assert all(torch.equal(p, q) for p, q in zip(got, ref))
+
+
+def test_non_finite_rows_off_the_boundary_stay_apart():
+    """A NaN row and an infinite one, whose elements share 16-byte pieces with their neighbours'."""
+    x, w, b, _, dy = _inputs(40, 1021, BF, F32, seed=4)
+    clean = api.moe_layer_norm(x, w, b)
+    x2 = x.clone()
+    x2[4] = float("nan")
+    x2[6] = float("inf")
+    o = api.moe_layer_norm(x2, w, b)
+    rows = [t for t in range(40) if t not in (4, 6)]
+    assert torch.equal(o.y[rows], clean.y[rows]) and torch.equal(o.rstd[rows], clean.rstd[rows])
+    assert torch.isnan(o.y[4]).all() and torch.isnan(o.y[6]).all()
+    d2 = dy.clone()
+    d2[9] = float("nan")
+    dx, _, _ = api.moe_layer_norm_backward(d2, x2, w, o.mean, o.rstd)
+    ref, _, _ = api.moe_layer_norm_backward(dy, x, w, clean.mean, clean.rstd)
+    rows.remove(9)
+    assert torch.equal(dx[rows], ref[rows]) and torch.isnan(dx[9]).all()
