@@ -4,7 +4,14 @@
 // For every valid route (t, k) with expert e = ids[t,k]:
 //   h = silu(x[t] W1[e]) * (x[t] W3[e]);   y[t] = bf16( sum_k p[t,k] (h W2[e]) )
 // Every weight of the chosen experts is read once and used for the few tokens that chose
-// them, so the time is the weights' bytes over the memory's rate.
+// them, so the time is the weights' bytes over the memory's rate plus a fixed part: 12 to 15 us from the
+// routing through two dependent kernels' starts and joins. Measured on a GPU that copies 6.78 TB/s (whole
+// layer, SM clock 2070 MHz; the share is that of the weights' bytes at that rate):
+//   1 token, 8 experts, top-2, 4096 x 14336, bf16         116-119 us   0.88-0.90   (0.70 GB)
+//   32 tokens of the same (all experts)                   413-425 us   0.98-1.0    (2.8 GB)
+//   8 tokens, 32 experts, top-4, 7168 x 2048, MXFP8       156-166 us   0.85-0.90   (0.95 GB)
+//   5 tokens, 2,304 experts, top-36, 512 x 512, bf16        64-66 us   0.61-0.63   (0.27 GB)
+//   1 token, 8 experts, top-2, 256 x 512, bf16                 15 us   the fixed part (1.6 MB)
 #include "common.cuh"
 #include "sm100_ptx.cuh"
 #include "tensor_map.cuh"
@@ -21,7 +28,8 @@ constexpr int FEW_EMAX = 8192;       // experts
 
 // ---------------------------------------------------------------------------
 // First kernel. CTA t < T: token t's selection (unless the caller gave ids and probs). MXFP8: the CTAs
-// after those quantise x row-wise 1x32, PREP_QUANT elements of a row each.
+// after those quantise x row-wise 1x32, PREP_QUANT elements of a row each. 4 to 5 us, all of it latency:
+// hence counting and ranking, a fixed number of steps, in place of K rounds of a maximum each.
 //
 // Selection: a thread holds V logits as order-preserving keys (expert i * 256 + thread). Up to 256
 // experts, each logit's rank is counted directly against the row. Above, the K-th largest of the
@@ -252,9 +260,13 @@ __global__ void __launch_bounds__(PREP_THREADS) few_prep_kernel(PrepArgs p) {
 // The expert MLP and the combine: two kernels, one persistent CTA per SM each.
 //
 // Every weight row is streamed once, as the A operand (128 rows) of tcgen05.mma; the few tokens
-// are the B operand, so a tile's accumulator is [128 weight rows][tokens] in TMEM. The weights'
-// bytes bound the kernels: a producer warp keeps a ring of up to FEW_STAGES stages of two 16 KB weight
-// tiles in flight per SM.
+// are the B operand, so a tile's accumulator is [128 weight rows][tokens] in TMEM (with the weights as
+// B the M = 128 rows of A would be padding, and a token's worth of MMA would cost as much as 128). The
+// weights' bytes bound the kernels: a producer warp keeps a ring of up to FEW_STAGES stages of two 16 KB
+// weight tiles in flight per SM. By themselves, from a cold L2: up 470 MB in 80 us (5.9 TB/s; tensor pipe
+// 4 % busy at 1 token, 8 % at 32), down 235 MB in 53 us (its start and its joins weigh more), MXFP8 up 424 MB in 76 us.
+// MXFP8 comes near a second bound: the MMA warp spends 324 cycles on a k-block's MMAs, 160 on its scale
+// copies and about 175 on barriers, 0.33 us per 16 KB, 7.5 TB/s over 152 SMs.
 //
 // Up: a tile is 64 columns of W1 and the same 64 of W3 of one expert, over all of H; the tokens
 //   operand is all of x (T rows, zero rows past them), the chosen tokens' columns are read. h goes

@@ -4,7 +4,8 @@
 // group of tensors: the first sums the squares (a partial sum per CTA), the second adds the
 // partial sums up -- every CTA all of them, in one fixed order -- and scales. The scale depends on every
 // gradient, so what does not stay in L2 is read twice: three passes over the bytes bound large lists,
-// two launches small ones.
+// two launches small ones. Measured: 2.8 GB of bf16 in six tensors 1274-1284 us, 6.6 TB/s over the three
+// passes (a copy runs at 6.78); 40 tensors of 24 M elements in all, bf16 and fp32, 32.5 us; six tensors of a small layer 8-9 us.
 // The list of tensors travels in the kernels' parameters. Its elements, in blocks of GN_BLOCK, are cut
 // into one equal stretch per CTA whatever the tensors' sizes, so ragged lists keep every CTA busy. The
 // second kernel walks each stretch from its end: what the first one read last is in L2 still.

@@ -505,8 +505,9 @@ moe_status moe_permute_backward(const void *dx_perm, const int32_t *row_map,
                                 int T, int K, int H, void *dx, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
- * The whole layer for a few tokens (a decoding step): router, expert MLP and
- * combine in two kernels, on the same packed weights as the grouped GEMMs.
+ * The whole layer for a few tokens (a decoding step): router, up projection, and down
+ * projection with the combine, three kernels that overlap, on the same packed weights
+ * as the grouped GEMMs.
  * (The pages describe training batches and no such call.)
  *
  * x [T, H] bf16, logits [T, E] fp32. ids [T, K] and probs [T, K] as
