@@ -154,36 +154,60 @@ __global__ void __launch_bounds__(512) ln_forward_kernel(const T* x, const T* re
     }
 }
 
-// Forward for rows too long for registers: the row is read again for each sum.
-template <typename T, typename W>
+// Forward for rows too long for the ring: a CTA per row, which is read again for each sum (from L2). 1000 x 40000 bf16
+// with a residual 76 us (floor 47; element by element 200).
+template <typename T, typename W, int VEC>
 __global__ void __launch_bounds__(512) ln_forward_long_kernel(const T* x, const T* residual, int H,
                                                               const W* __restrict__ w, const W* __restrict__ b,
                                                               float eps, T* sum, T* y, float* mean_out,
                                                               float* rstd_out) {
     __shared__ float red[2][32];
+    using V = Vec<T, VEC>;
     const long long base = (long long)blockIdx.x * H;
+    const int n = H / VEC;
     float a[1] = {0.0f};
-    for (int i = threadIdx.x; i < H; i += blockDim.x) {
-        float v = to_f(x[base + i]);
+#pragma unroll(VEC == 1 ? 1 : 2)
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        V v = reinterpret_cast<const V*>(x + base)[i];
         if (residual) {
-            const T r = from_f<T>(v + to_f(residual[base + i]));
-            sum[base + i] = r;
-            v = to_f(r);
+            const V r = reinterpret_cast<const V*>(residual + base)[i];
+            float f[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; j++) f[j] = v.get(j) + r.get(j);
+            v.set(f);
+            reinterpret_cast<V*>(sum + base)[i] = v;
         }
-        a[0] += v;
+#pragma unroll
+        for (int j = 0; j < VEC; j++) a[0] += v.get(j);
     }
     const T* s = residual ? sum : x;
     row_sum(a, false, red[0]);
     const float mean = a[0] / (float)H;
     a[0] = 0.0f;
-    for (int i = threadIdx.x; i < H; i += blockDim.x) {
-        const float d = to_f(s[base + i]) - mean;
-        a[0] = fmaf(d, d, a[0]);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const V v = reinterpret_cast<const V*>(s + base)[i];
+#pragma unroll
+        for (int j = 0; j < VEC; j++) {
+            const float d = v.get(j) - mean;
+            a[0] = fmaf(d, d, a[0]);
+        }
     }
     row_sum(a, false, red[1]);
     const float rstd = 1.0f / sqrtf(a[0] / (float)H + eps);
-    for (int i = threadIdx.x; i < H; i += blockDim.x)
-        y[base + i] = from_f<T>(fmaf((to_f(s[base + i]) - mean) * rstd, to_f(w[i]), b ? to_f(b[i]) : 0.0f));
+#pragma unroll(VEC == 1 ? 1 : 2)
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const V v = reinterpret_cast<const V*>(s + base)[i];
+        const Vec<W, VEC> wv = reinterpret_cast<const Vec<W, VEC>*>(w)[i];
+        Vec<W, VEC> bv;
+        if (b) bv = reinterpret_cast<const Vec<W, VEC>*>(b)[i];
+        V o;
+        float f[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; j++) f[j] = fmaf((v.get(j) - mean) * rstd, wv.get(j), b ? bv.get(j) : 0.0f);
+        o.set(f);
+        reinterpret_cast<V*>(y + base)[i] = o;
+    }
     if (threadIdx.x == 0) {
         if (mean_out) mean_out[blockIdx.x] = mean;
         if (rstd_out) rstd_out[blockIdx.x] = rstd;
@@ -827,45 +851,77 @@ __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, cons
     }
 }
 
-// Backward for rows too long for registers: dx with the row read twice ...
-template <typename T, typename W>
+// Backward for rows too long for the ring (bf16 above 8192 columns): dx with the row read twice (from L2 the second
+// time) ... Together with the kernel below 3000 x 16384 bf16 with dx_add takes 128 us (floor 58; two more reads of
+// the operands than that; element by element 264).
+template <typename T, typename W, int VEC>
 __global__ void __launch_bounds__(512) ln_backward_long_kernel(const T* dy, const T* __restrict__ s, int H,
                                                                const W* __restrict__ w, const float* __restrict__ mean,
                                                                const float* __restrict__ rstd, const T* add, T* dx) {
     __shared__ float red[64];
+    using V = Vec<T, VEC>;
     const long long base = (long long)blockIdx.x * H;
+    const int n = H / VEC;
     const float m = mean[blockIdx.x], r = rstd[blockIdx.x];
     float sums[2] = {0.0f, 0.0f};
-    for (int i = threadIdx.x; i < H; i += blockDim.x) {
-        const float g = to_f(dy[base + i]) * to_f(w[i]);
-        sums[0] += g;
-        sums[1] = fmaf(g, (to_f(s[base + i]) - m) * r, sums[1]);
+#pragma unroll(VEC == 1 ? 1 : 2)
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const V gv = reinterpret_cast<const V*>(dy + base)[i], sv = reinterpret_cast<const V*>(s + base)[i];
+        const Vec<W, VEC> wv = reinterpret_cast<const Vec<W, VEC>*>(w)[i];
+#pragma unroll
+        for (int j = 0; j < VEC; j++) {
+            const float g = gv.get(j) * wv.get(j);
+            sums[0] += g;
+            sums[1] = fmaf(g, (sv.get(j) - m) * r, sums[1]);
+        }
     }
     row_sum(sums, false, red);
     const float a = sums[0] / (float)H, c = sums[1] / (float)H;
-    for (int i = threadIdx.x; i < H; i += blockDim.x) {
-        const float g = to_f(dy[base + i]) * to_f(w[i]);
-        float v = r * (g - a - (to_f(s[base + i]) - m) * r * c);
-        if (add) v += to_f(add[base + i]);
-        dx[base + i] = from_f<T>(v);
+#pragma unroll(VEC == 1 ? 1 : 2)
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const V gv = reinterpret_cast<const V*>(dy + base)[i], sv = reinterpret_cast<const V*>(s + base)[i];
+        const Vec<W, VEC> wv = reinterpret_cast<const Vec<W, VEC>*>(w)[i];
+        V av, o;
+        if (add) av = reinterpret_cast<const V*>(add + base)[i];
+        float f[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; j++) {
+            f[j] = r * (gv.get(j) * wv.get(j) - a - (sv.get(j) - m) * r * c);
+            if (add) f[j] += av.get(j);
+        }
+        o.set(f);
+        reinterpret_cast<V*>(dx + base)[i] = o;
     }
 }
 
-// ... and the partial sums of dweight and dbias, a slice of the rows per blockIdx.y.
-template <typename T>
+// ... and the partial sums of dweight and dbias, a slice of the rows per blockIdx.y, VEC columns a thread, four rows
+// of loads in flight.
+template <typename T, int VEC>
 __global__ void __launch_bounds__(256) ln_backward_long_w_kernel(const T* dy, const T* __restrict__ s, int rows, int H,
                                                                  const float* __restrict__ mean,
                                                                  const float* __restrict__ rstd, float* part) {
+    using V = Vec<T, VEC>;
     const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= H) return;
-    float a = 0.0f, c = 0.0f;
+    if (i >= H / VEC) return;
+    float a[VEC], c[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; j++) a[j] = c[j] = 0.0f;
+#pragma unroll 4
     for (long long t = blockIdx.y; t < rows; t += gridDim.y) {
-        const float g = to_f(dy[t * H + i]);
-        a = fmaf(g, (to_f(s[t * H + i]) - mean[t]) * rstd[t], a);
-        c += g;
+        const V gv = reinterpret_cast<const V*>(dy + t * H)[i], sv = reinterpret_cast<const V*>(s + t * H)[i];
+        const float m = mean[t], r = rstd[t];
+#pragma unroll
+        for (int j = 0; j < VEC; j++) {
+            a[j] = fmaf(gv.get(j), (sv.get(j) - m) * r, a[j]);
+            c[j] += gv.get(j);
+        }
     }
-    part[(size_t)blockIdx.y * 2 * H + i] = a;
-    part[((size_t)blockIdx.y * 2 + 1) * H + i] = c;
+    float* out = part + (size_t)blockIdx.y * 2 * H + (size_t)i * VEC;
+#pragma unroll
+    for (int j = 0; j < VEC; j++) {
+        out[j] = a[j];
+        out[H + j] = c[j];
+    }
 }
 
 // dweight and dbias from n partial sums, 32 columns per CTA: thread row y adds partials y, y + 32, ...
@@ -1056,13 +1112,16 @@ moe_status ln_forward(const void* x, const void* residual, int rows, int H, cons
 #define MOE_LN_F(vec, nv)                                                                                             \
     ln_forward_kernel<T, W, vec, nv><<<grid, l.threads, 0, s>>>((const T*)x, (const T*)residual, rows, H, l.warp_row, \
                                                                 (const W*)w, (const W*)b, eps, (T*)sum, (T*)y, mean, rstd)
-    if (l.nv == 0)
-        ln_forward_long_kernel<T, W><<<rows, 512, 0, s>>>((const T*)x, (const T*)residual, H, (const W*)w, (const W*)b,
-                                                          eps, (T*)sum, (T*)y, mean, rstd);
+#define MOE_LN_FL(vec)                                                                                              \
+    ln_forward_long_kernel<T, W, vec><<<rows, 512, 0, s>>>((const T*)x, (const T*)residual, H, (const W*)w, (const W*)b, \
+                                                           eps, (T*)sum, (T*)y, mean, rstd)
+    if (l.nv == 0 && wide) MOE_LN_FL(VEC);
+    else if (l.nv == 0) MOE_LN_FL(1);
     else if (wide) MOE_LN_F(VEC, 1);
     else if (l.nv == 4) MOE_LN_F(1, 4);
     else MOE_LN_F(1, 16);
 #undef MOE_LN_F
+#undef MOE_LN_FL
     return moe_host::launch_status();
 }
 
@@ -1077,13 +1136,22 @@ moe_status ln_backward(const void* dy, const void* sv, int rows, int H, const vo
     int n_part = 0;
     if (rows == 0) {
     } else if (l.nv == 0) {
-        if (sums) {      // (before dx, which may be dy)
-            n_part = rows < 64 ? rows : 64;
-            ln_backward_long_w_kernel<T><<<dim3((H + 255) / 256, n_part), 256, 0, s>>>((const T*)dy, (const T*)sv, rows, H,
-                                                                                       mean, rstd, part);
-        }
-        ln_backward_long_kernel<T, W><<<rows, 512, 0, s>>>((const T*)dy, (const T*)sv, H, (const W*)w, mean, rstd,
-                                                           (const T*)add, (T*)dx);
+#define MOE_LN_BL(vec)                                                                                              \
+    {                                                                                                               \
+        if (sums) { /* (before dx, which may be dy) */                                                              \
+            /* eight rows a CTA at least; four CTAs an SM, more of the narrow ones */                               \
+            const int cols = (H / vec + 255) / 256, most = (vec == 1 ? 24 : 4) * ln_sms() / cols + 1;               \
+            n_part = (rows + 7) / 8 < most ? (rows + 7) / 8 : most;                                                 \
+            if (n_part > LN_PARTS) n_part = LN_PARTS;                                                               \
+            ln_backward_long_w_kernel<T, vec><<<dim3(cols, n_part), 256, 0, s>>>((const T*)dy, (const T*)sv, rows, H, \
+                                                                                 mean, rstd, part);                 \
+        }                                                                                                           \
+        ln_backward_long_kernel<T, W, vec><<<rows, 512, 0, s>>>((const T*)dy, (const T*)sv, H, (const W*)w, mean, rstd, \
+                                                                (const T*)add, (T*)dx);                             \
+    }
+        if (wide) MOE_LN_BL(VEC)
+        else MOE_LN_BL(1)
+#undef MOE_LN_BL
     } else if (l.ring) {
         LnRingShape r = ln_backward_ring((size_t)(add ? 3 : 2) * l.row_bytes, l);
         if (l.odd && r.smem < (size_t)H * 8) r.smem = (size_t)H * 8;       // (its partial sums leave by it)

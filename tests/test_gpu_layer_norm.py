@@ -343,3 +343,19 @@ def test_non_finite_rows_off_the_boundary_stay_apart():
     ref, _, _ = api.moe_layer_norm_backward(dy, x, w, clean.mean, clean.rstd)
     rows.remove(9)
     assert torch.equal(dx[rows], ref[rows]) and torch.isnan(dx[9]).all()
+
+
+@pytest.mark.parametrize("dt,wdt", [(BF, F32), (F32, BF)])
+@pytest.mark.parametrize("T,H", [(300, 8264), (33, 16392), (9, 40000), (70, 9001)])
+def test_long_rows_by_the_dozen(T, H, dt, wdt):
+    """Rows that do not fit the ring, enough of them for several partial sums a column."""
+    x, w, b, r, dy = _inputs(T, H, dt, wdt, seed=T * 3 + H)
+    s = (x.float() + r.float()).to(dt)
+    o = api.moe_layer_norm(x, w, b, residual=r)
+    assert torch.equal(o.sum, s)
+    _forward_check(o, s, w, b, 1e-5)
+    got = api.moe_layer_norm_backward(dy, s, w, o.mean, o.rstd, dx_add=r)
+    _backward_check(got, dy, s, w, o.mean, o.rstd, r)
+    d2 = dy.clone()
+    again = api.moe_layer_norm_backward(d2, s, w, o.mean, o.rstd, dx_add=r, dx=d2)
+    assert all(torch.equal(p, q) for p, q in zip(got, again))
