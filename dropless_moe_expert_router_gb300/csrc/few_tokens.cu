@@ -1203,6 +1203,16 @@ FewLayout few_layout(int T, int K, int H, int F, bool fp8) {
     return l;
 }
 
+// Ring stages that fit beside the plan and the output sums, 0 where too few do, or where the plan's
+// scratch does not fit them.
+int few_stages(int T, int K, int E, bool fp8) {
+    const size_t fixed = 1024 + few_fixed_smem(T, K, E < T * K ? E : T * K, fp8);
+    const size_t stage = FEW_KPS * (FEW_A_BYTES + (size_t)((T + 15) & ~15) * 128);
+    if (fixed + 2 * stage > FEW_SMEM_MAX) return 0;
+    const int n = (int)((FEW_SMEM_MAX - fixed) / stage), stages = n < FEW_STAGES ? n : FEW_STAGES;
+    return stages * stage < (size_t)E * 10 + (size_t)T * K * 2 ? 0 : stages;
+}
+
 moe_status few_sizes(int T, int K, int E, int H, int F, moe_dtype dtype) {
     if (dtype != MOE_BF16 && dtype != MOE_MXFP8) return MOE_ERR_INVALID_ARG;
     if (T < 0 || K < 1 || E < 1 || K > E || H < 128 || F < 128) return MOE_ERR_INVALID_ARG;
@@ -1210,21 +1220,15 @@ moe_status few_sizes(int T, int K, int E, int H, int F, moe_dtype dtype) {
     if (H % step || F % step) return MOE_ERR_UNSUPPORTED;
     if (T > FEW_TMAX || K > FEW_KMAX || (long long)T * K > FEW_ROUTES || E > FEW_EMAX) return MOE_ERR_UNSUPPORTED;
     if ((long long)E * 2 * F > 0x7fffffffLL || (long long)E * H > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+    if (T > 0 && !few_stages(T, K, E, dtype == MOE_MXFP8)) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
 template <bool FP8>
 moe_status few_launch(FewArgs a, const PrepArgs& p, const void* x, const uint8_t* xs, const void* w13,
                       const uint8_t* w13s, const void* w2, const uint8_t* w2s, cudaStream_t s) {
-    // shared memory: as many ring stages as fit beside the plan and the output sums
-    const size_t fixed = 1024 + few_fixed_smem(a.T, a.K, a.a_max, FP8);
-    const int stage_bytes = FEW_KPS * (FEW_A_BYTES + a.nb * 128);
-    if (fixed + 2 * (size_t)stage_bytes > FEW_SMEM_MAX) return MOE_ERR_UNSUPPORTED;
-    a.stages = (int)((FEW_SMEM_MAX - fixed) / stage_bytes);
-    if (a.stages > FEW_STAGES) a.stages = FEW_STAGES;
-    if ((size_t)a.stages * stage_bytes < (size_t)a.E * 10 + (size_t)a.T * a.K * 2)      // the plan's scratch
-        return MOE_ERR_UNSUPPORTED;
-    const size_t smem = fixed + (size_t)a.stages * stage_bytes;
+    a.stages = few_stages(a.T, a.K, a.E, FP8);
+    const size_t smem = 1024 + few_fixed_smem(a.T, a.K, a.a_max, FP8) + (size_t)a.stages * FEW_KPS * (FEW_A_BYTES + a.nb * 128);
     CUtensorMap tw13, tw2, tx, th, ts13, ts2, tsx, tsh;
     using moe_host::make_operand_map;
     using moe_host::make_scale_map;

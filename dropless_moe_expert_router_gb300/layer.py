@@ -184,12 +184,17 @@ class MoELayer:
         """The layer for a few tokens (a decoding step): x [t, H] bf16 and logits [t, E] fp32 with
         t <= 64 (and t * K <= 4096), whatever the layer's T -> y [t, H] bf16, a new tensor. The same
         packed weights and router as ``forward``; its buffers are not touched. Calls on one layer share
-        a workspace and must not overlap on the GPU. The expert outputs are not rounded to bf16 before the combine, so y may differ from ``forward``'s in its last bit."""
+        a workspace and must not overlap on the GPU. The expert outputs are not rounded to bf16 before
+        the combine, so y may differ from ``forward``'s in its last bit."""
         if self.nv4:
             raise ValueError("the few-token path wants bf16 or MXFP8 weights")
         w, K = self.weights, self.K
         if self._few_workspace is None:
-            self._few_workspace = api.moe_layer_few_tokens_workspace(w, min(64, 4096 // K), K)
+            t = min(64, 4096 // K)        # the most tokens that the sizes allow
+            self._few_workspace = api.moe_layer_few_tokens_workspace(w, t, K)
+            while t > 1 and not self._few_workspace.numel():
+                t -= 1
+                self._few_workspace = api.moe_layer_few_tokens_workspace(w, t, K)
         if self.score == "sigmoid":
             ids, probs = api.moe_route_sigmoid_topk(logits, K, expert_bias=self.expert_bias, renorm=self.renorm,
                                                     id_dtype=self.ids.dtype, stream=stream)

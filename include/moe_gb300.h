@@ -522,10 +522,10 @@ moe_status moe_permute_backward(const void *dx_perm, const int32_t *row_map,
  * along H first, as moe_permute does. A token without a valid route gets zeros.
  * w13_packed, w2_packed and their scales: moe_prepare_weights, dtype MOE_BF16 or
  * MOE_MXFP8. Outputs do not depend on the timing of the GPU's blocks.
- * Requires 0 <= T <= 64, 1 <= K <= min(E, 128), T * K <= 4096, E <= 8192 (above:
- * MOE_ERR_UNSUPPORTED), H % 128 == 0 and F % 128 == 0 (MXFP8: both % 512), the packed
- * weights and the workspace 128-byte aligned, x, y and the scales 16-byte, ids and probs
- * to their element. workspace: moe_layer_few_tokens_workspace_size bytes (0 for sizes
+ * Requires 0 <= T <= 64, 1 <= K <= min(E, 128), T * K <= 4096, E <= 8192 (MXFP8: with
+ * E > 2304, T * K above 2048 may not fit shared memory; above: MOE_ERR_UNSUPPORTED),
+ * H % 128 == 0 and F % 128 == 0 (MXFP8: both % 512), the packed weights and the workspace
+ * 128-byte aligned, x, y and the scales 16-byte, ids and probs to their element. workspace: moe_layer_few_tokens_workspace_size bytes (0 for sizes
  * that are refused); its contents need not be initialised, and calls that share one
  * must not overlap. Every wait inside is bounded (MOE_DEVERR_TIMEOUT).
  * ------------------------------------------------------------------------ */

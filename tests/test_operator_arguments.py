@@ -42,6 +42,16 @@ def test_few_tokens(lib):
     assert lib.moe_layer_few_tokens_workspace_size(4, 2, 8, 512, 512, F32) == 0
 
 
+def test_few_tokens_sizes_that_do_not_fit_shared_memory(lib):
+    """The plan of very many routes and experts beside MXFP8's scales: refused with the workspace's size, not later."""
+    size = lib.moe_layer_few_tokens_workspace_size
+    assert size(64, 64, 8192, 512, 512, MXFP8) == 0 and _few(lib, T=64, K=64, E=8192, dtype=MXFP8) == 2
+    for T, K, E in ((64, 32, 8192), (16, 128, 8192), (64, 64, 2304), (32, 128, 2304)):
+        assert size(T, K, E, 512, 512, MXFP8) > 0
+    for T, K in ((64, 64), (32, 128)):
+        assert size(T, K, 8192, 512, 512, BF16) > 0
+
+
 def _ln(lib, T=4, H=64, dtype=BF16, x=P, res=None, w=P, b=P, wdt=F32, eps=1e-5, sm=None, y=P, mean=P, rstd=P):
     return lib.moe_layer_norm(x, res, T, H, dtype, w, b, wdt, eps, sm, y, mean, rstd, None)
 
