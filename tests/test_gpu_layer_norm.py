@@ -359,3 +359,18 @@ def test_long_rows_by_the_dozen(T, H, dt, wdt):
     d2 = dy.clone()
     again = api.moe_layer_norm_backward(d2, s, w, o.mean, o.rstd, dx_add=r, dx=d2)
     assert all(torch.equal(p, q) for p, q in zip(got, again))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,H", [(700, 3001), (40, 8000), (9, 2048), (3, 9001), (300, 100)])
+def test_tensors_off_the_boundary_differently(T, H, dt):
+    """Each tensor starts elsewhere against 16 bytes, so no piece of one is a piece of the others."""
+    x, w, b, r, dy = _inputs(T, H, dt, F32, seed=T + 7 * H)
+    s = (x.float() + r.float()).to(dt)
+    a0, a1, a2 = _Fenced(0), _Fenced(1), _Fenced(2)
+    o = api.moe_layer_norm(a0(x), w, b, residual=a1(r), y=a2(dy), sum=a1(dy))
+    assert torch.equal(o.sum, s)
+    _forward_check(o, s, w, b, 1e-5)
+    got = api.moe_layer_norm_backward(a1(dy), a0(s), w, o.mean, o.rstd, dx_add=a2(r), dx=a1(x))
+    _backward_check(got, dy, s, w, o.mean, o.rstd, r)
+    assert a0.intact() and a1.intact() and a2.intact()
