@@ -294,6 +294,10 @@ constexpr int FEW_SF_SLOTS = 4;            // groups of scales in flight (short 
 constexpr int FEW_SF_BYTES = FEW_SF_KB * 1024;   // a slot: landed 4 FEW_SF_KB bytes a row, rearranged FEW_SF_KB x (A 512 | B 512)
 constexpr int FEW_XCH = 16;                // tokens whose W3 products the epilogue exchanges at a time (tmem_wait16)
 constexpr int FEW_MIN_KB = 2;              // k-blocks that a CTA takes at least
+constexpr int FEW_GRID_MAX = 256;          // CTAs that the workspace has room for
+constexpr int FEW_ONE_JOIN = 512;          // down: most CTAs of a tile x tokens that are joined in one step: one SM reads
+                                           // them all (64 tokens, H = 256, 64 experts, F = 1024: 50 us, in two steps 45;
+                                           // at 1024 24 tokens, H = 512, F = 2048 take 39.9 us instead of 36.4)
 constexpr int FEW_SHARE = 32;              // up: CTAs that share a tile at most (the last to arrive reads all their sums)
 constexpr int FEW_JOIN_KB = 8;             // joining partial sums costs about as much as this many k-blocks
 constexpr size_t FEW_SMEM_MAX = 227 * 1024;
@@ -309,7 +313,8 @@ struct FewArgs {
     void* h;                  // [T K, F] bf16 or E4M3
     uint8_t* hs;              // MXFP8: [T K, F / 32]
     float* part;              // [2 gridDim.x][T][128] partial sums of shared output tiles
-    unsigned* count;          // arrivals at shared tiles (down: by tile, H / 128; up: by first CTA); zeroed before
+    unsigned* count;          // arrivals at shared tiles (down: by tile, H / 128; up: by first CTA, FEW_GRID_MAX) and
+                              // at a tile's groups of CTAs (down: by the first one's slot, 2 FEW_GRID_MAX); zeroed before
     __nv_bfloat16* y;
 };
 
@@ -1080,16 +1085,34 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             const size_t slot = (size_t)p.T * 128;
             float* to = p.part + pl.slot_of(blockIdx.x, tile) * slot + row;
             for (int t = 0; t < p.T; t++) __stcg(to + t * 128, acc[t * 128 + row]);
-            if (arrive(p.count + tile) != c1 - c0) return;
-            // four rows a lane; up to 32 loads in flight per warp
-            const float4* first = reinterpret_cast<const float4*>(p.part + pl.slot_of(c0, tile) * slot) + lane;
-            const float4* rest = reinterpret_cast<const float4*>(p.part + (size_t)2 * (c0 + 1) * slot) + lane;
-            const int n = c1 - c0 + 1;
             auto put = [&](int t, const float4& v) {
                 __nv_bfloat162 o[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
                 *reinterpret_cast<uint2*>(p.y + (size_t)t * p.H + tile * 128 + 4 * lane) = *reinterpret_cast<uint2*>(o);
             };
-            if (p.T <= 4) {
+            // four rows a lane; up to 32 loads in flight per warp
+            const float4* first = reinterpret_cast<const float4*>(p.part + pl.slot_of(c0, tile) * slot) + lane;
+            int n = c1 - c0 + 1, apart = 1;            // sums to add: of every apart-th CTA
+            if (n * p.T > FEW_ONE_JOIN) {
+                // in two steps: the last of a group of CTAs adds the group's sums up into its first one's
+                apart = (int)ceilf(sqrtf((float)n));
+                const int g = ((int)blockIdx.x - c0) / apart, m0 = c0 + g * apart, m = min(apart, c1 + 1 - m0);
+                const int own = pl.slot_of(m0, tile);
+                if (arrive(p.count + p.H / 128 + FEW_GRID_MAX + own) != m - 1) return;
+                float4* sum = reinterpret_cast<float4*>(p.part + own * slot) + lane;
+                const float4* others = reinterpret_cast<const float4*>(p.part + (size_t)2 * (m0 + 1) * slot) + lane;
+                for (int t0 = q; t0 < p.T; t0 += 32) {
+                    float4 v[8];
+                    few_add_parts<8, 4>(v, sum, others, slot / 2, 0, 1, m, t0, 4, p.T);
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        if (t0 + 4 * j < p.T) __stcg(sum + (t0 + 4 * j) * 32, v[j]);
+                }
+                n = (n + apart - 1) / apart;
+            }
+            if (arrive(p.count + tile) != n - 1) return;
+            const float4* rest = reinterpret_cast<const float4*>(p.part + (size_t)2 * (c0 + apart) * slot) + lane;
+            const size_t stride = apart * (slot / 2);
+            if (apart == 1 && p.T <= 4) {
                 // a quarter of the CTAs' sums per warp, then the four warps' in order
                 float4 v[4];
                 few_add_parts<4, 8>(v, first, rest, slot / 2, q, 4, n, 0, 1, p.T);
@@ -1107,7 +1130,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
                     put(q, a);
                 }
                 epi_sync();
-            } else if (p.T <= 16) {
+            } else if (apart == 1 && p.T <= 16) {
                 // a warp per token
                 float4 v[4];
                 few_add_parts<4, 8>(v, first, rest, slot / 2, 0, 1, n, q, 4, p.T);
@@ -1117,7 +1140,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
             } else {
                 for (int t0 = q; t0 < p.T; t0 += 32) {
                     float4 v[8];
-                    few_add_parts<8, 4>(v, first, rest, slot / 2, 0, 1, n, t0, 4, p.T);
+                    few_add_parts<8, 4>(v, first, rest, stride, 0, 1, n, t0, 4, p.T);
 #pragma unroll
                     for (int j = 0; j < 8; j++)
                         if (t0 + 4 * j < p.T) put(t0 + 4 * j, v[j]);
@@ -1181,14 +1204,13 @@ int few_sms() {
     return sms;
 }
 
-constexpr int FEW_GRID_MAX = 256;          // CTAs that the workspace has room for
 
 FewLayout few_layout(int T, int K, int H, int F, bool fp8) {
     auto up = [](size_t v) { return (v + 127) & ~(size_t)127; };
     FewLayout l{};
     size_t o = 0;
     l.count = o;
-    o += up((size_t)(H / 128 + FEW_GRID_MAX) * 4);
+    o += up((size_t)(H / 128 + 3 * FEW_GRID_MAX) * 4);
     l.xq = o;
     o += fp8 ? up((size_t)T * H) : 0;
     l.xs = o;
@@ -1317,7 +1339,7 @@ extern "C" moe_status moe_layer_few_tokens(const void* x, int T, int H, const fl
     p.xq = fp8 ? ws + l.xq : nullptr;
     p.xs = fp8 ? ws + l.xs : nullptr;
     p.count = reinterpret_cast<unsigned*>(ws + l.count);
-    p.n_count = H / 128 + FEW_GRID_MAX;
+    p.n_count = H / 128 + 3 * FEW_GRID_MAX;
     FewArgs a{};
     a.ids = ids;
     a.probs = probs;

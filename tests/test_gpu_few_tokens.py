@@ -292,3 +292,18 @@ def test_few_tokens_zero_tokens_and_refusals():
     with pytest.raises(ValueError):
         api.moe_layer_few_tokens(x.cpu(), lg, packed, 2)
     assert api.moe_get_device_errors() == 0
+
+
+@pytest.mark.parametrize("T,H,E,K,F,precision", [
+    (64, 256, 40, 4, 1024, "bf16"), (33, 512, 16, 2, 2048, "bf16"), (17, 128, 64, 4, 1024, "bf16"),
+    (64, 512, 16, 4, 2048, "mxfp8"), (9, 128, 128, 16, 512, "bf16"), (50, 384, 100, 3, 640, "bf16")])
+def test_few_tokens_joined_in_two_steps(T, H, E, K, F, precision):
+    """Few output tiles and many tokens: a tile's many blocks are joined in groups first. The tokens'
+    results do not depend on when the blocks arrive."""
+    x, lg = _inputs(T, H, E, seed=2 * T + H)
+    _, packed = _weights(E, H, F, precision, seed=E + 3 * F)
+    y, ids, probs = api.moe_layer_few_tokens(x, lg, packed, K)
+    _check(y, x, ids, probs, packed)
+    for _ in range(5):
+        assert torch.equal(y, api.moe_layer_few_tokens(x, lg, packed, K)[0])
+    assert api.moe_get_device_errors() == 0
