@@ -710,7 +710,12 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
         pl.W = tiles * pl.kbs;
         // whole tiles, or equal pieces with the shared tiles joined: whichever ends first
         const int join = FEW_JOIN_KB + sm.slots / (2 * max(pl.A, 1));       // (and half of one for each token)
-        const int pieces = max(1, min(min(G, pl.W / FEW_MIN_KB), tiles * FEW_SHARE));
+        // n pieces of W / n k-blocks of about 0.36 us each, then the last of a tile reads n / tiles sums of about
+        // 0.02 us a token each (of 8 tokens at least): the n that makes the sum least (64 tokens of one expert, H =
+        // 7168, F = 128: 84 us with 32 CTAs a tile, 37 so; 1 token, F = 256: 28 and 20)
+        const float m = (float)sm.slots / (float)max(pl.A, 1);
+        const int least = (int)sqrtf(18.0f * (float)pl.W * (float)tiles / fmaxf(m, 8.0f));
+        const int pieces = max(1, min(min(G, pl.W / FEW_MIN_KB), min(tiles * FEW_SHARE, max(tiles, least))));
         const bool whole = (tiles + G - 1) / G * pl.kbs <= (pl.W + pieces - 1) / pieces + join;
         pl.unit = whole ? pl.kbs : 1;
         pl.cut(whole ? max(1, min(G, tiles)) : pieces);
@@ -1030,7 +1035,7 @@ __global__ void __launch_bounds__(few_threads<FP8>(), 1)
 #pragma unroll
                         for (int i = 0; i < FEW_XCH; i++) f[i] = 0.0f;
                         const float* from = p.part + pl.slot_of(c0, r.tile) * slot + i0 * 128 + row;
-#pragma unroll 2
+#pragma unroll 4
                         for (int c = c0; c <= c1; c++) {
 #pragma unroll
                             for (int i = 0; i < FEW_XCH; i++)
