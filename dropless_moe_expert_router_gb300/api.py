@@ -2,8 +2,9 @@
 
 Each function has the name of its C entry point and only marshals arguments:
 it checks devices and dtypes, allocates outputs with torch when the caller did
-not pass them, and hands raw pointers, sizes and the current CUDA stream to
-the library. Every step of the computation runs in the library's kernels.
+not pass them (from the memory of the call's stream), and hands raw pointers, sizes
+and that stream, the current one unless given, to the library. Every step of the
+computation runs in the library's kernels.
 """
 from __future__ import annotations
 
@@ -49,6 +50,20 @@ def _raw_stream(stream: Optional[torch.cuda.Stream], t: torch.Tensor) -> int:
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
+def _empty(shape, dtype: torch.dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Uninitialised memory for a call on `stream` (None: the current one). It comes from that stream's
+    memory, which follows the order of the kernels that use it: whoever gets it next, or had it before, runs
+    on the same stream. What the caller enqueues on the current stream is waited for too before it goes back."""
+    if stream is not None:
+        current = torch.cuda.current_stream(device)
+        if stream != current:
+            with torch.cuda.stream(stream):
+                t = torch.empty(shape, dtype=dtype, device=device)
+            t.record_stream(current)
+            return t
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _at(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -85,9 +100,9 @@ def moe_route_topk(logits: torch.Tensor, K: int, *, id_dtype=torch.int32, renorm
     _want(logits, "logits", torch.float32, 2)
     T, E = logits.shape
     if ids is None:
-        ids = torch.empty((T, K), dtype=id_dtype, device=logits.device)
+        ids = _empty((T, K), id_dtype, logits.device, stream)
     if probs is None:
-        probs = torch.empty((T, K), dtype=torch.float32, device=logits.device)
+        probs = _empty((T, K), torch.float32, logits.device, stream)
     _want(ids, "ids", None, 2)
     _want(probs, "probs", torch.float32, 2)
     st = _lib.load().moe_route_topk(_ptr(logits), T, E, K, _ptr(ids), _id_code(ids.dtype), _ptr(probs),
@@ -108,9 +123,9 @@ def moe_route_sigmoid_topk(logits: torch.Tensor, K: int, *, expert_bias: Optiona
         if expert_bias.numel() != E:
             raise ValueError("expert_bias must have E entries")
     if ids is None:
-        ids = torch.empty((T, K), dtype=id_dtype, device=logits.device)
+        ids = _empty((T, K), id_dtype, logits.device, stream)
     if probs is None:
-        probs = torch.empty((T, K), dtype=torch.float32, device=logits.device)
+        probs = _empty((T, K), torch.float32, logits.device, stream)
     _want(ids, "ids", None, 2)
     _want(probs, "probs", torch.float32, 2)
     st = _lib.load().moe_route_sigmoid_topk(_ptr(logits), _ptr(expert_bias), T, E, K, _ptr(ids),
@@ -130,7 +145,7 @@ def moe_route_sigmoid_topk_backward(logits: torch.Tensor, ids: torch.Tensor, dpr
     T, E = logits.shape
     K = ids.shape[1]
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=torch.float32, device=logits.device)
+        dlogits = _empty((T, E), torch.float32, logits.device, stream)
     _want(dlogits, "dlogits", torch.float32, 2)
     st = _lib.load().moe_route_sigmoid_topk_backward(_ptr(logits), _ptr(ids), _id_code(ids.dtype), _ptr(dprobs),
                                                      T, E, K, MOE_ROUTE_RENORM if renorm else 0, _ptr(dlogits),
@@ -158,22 +173,22 @@ def moe_permute_kernel_launches(T: int, K: int, E: int) -> int:
 
 
 def permute_buffers(T: int, H: int, K: int, E: int, device, fuse_mxfp8: bool = False,
-                    nvfp4: bool = False) -> Permuted:
+                    nvfp4: bool = False, stream=None) -> Permuted:
     R_cap = T * K
     dev = torch.device(device)
     if nvfp4:
-        xp = torch.empty((R_cap, H // 2), dtype=torch.uint8, device=dev)
-        xs = torch.empty((R_cap, H // 16), dtype=torch.uint8, device=dev)
+        xp = _empty((R_cap, H // 2), torch.uint8, dev, stream)
+        xs = _empty((R_cap, H // 16), torch.uint8, dev, stream)
     elif fuse_mxfp8:
-        xp = torch.empty((R_cap, H), dtype=torch.uint8, device=dev)
-        xs = torch.empty((R_cap, H // 32), dtype=torch.uint8, device=dev)
+        xp = _empty((R_cap, H), torch.uint8, dev, stream)
+        xs = _empty((R_cap, H // 32), torch.uint8, dev, stream)
     else:
-        xp = torch.empty((R_cap, H), dtype=torch.bfloat16, device=dev)
+        xp = _empty((R_cap, H), torch.bfloat16, dev, stream)
         xs = None
-    return Permuted(xp, xs, torch.empty(E, dtype=torch.int32, device=dev),
-                    torch.empty(E + 1, dtype=torch.int32, device=dev),
-                    torch.empty((T, K), dtype=torch.int32, device=dev),
-                    torch.empty(R_cap, dtype=torch.int32, device=dev))
+    return Permuted(xp, xs, _empty(E, torch.int32, dev, stream),
+                    _empty(E + 1, torch.int32, dev, stream),
+                    _empty((T, K), torch.int32, dev, stream),
+                    _empty(R_cap, torch.int32, dev, stream))
 
 
 def moe_permute(x: torch.Tensor, ids: torch.Tensor, E: int, *, fuse_mxfp8: bool = False,
@@ -185,10 +200,10 @@ def moe_permute(x: torch.Tensor, ids: torch.Tensor, E: int, *, fuse_mxfp8: bool 
     T, H = x.shape
     K = ids.shape[1]
     if out is None:
-        out = permute_buffers(T, H, K, E, x.device, fuse_mxfp8)
+        out = permute_buffers(T, H, K, E, x.device, fuse_mxfp8, stream=stream)
     ws_bytes = moe_permute_workspace_size(T, K, E)
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+        workspace = _empty(ws_bytes, torch.uint8, x.device, stream)
     st = _lib.load().moe_permute(
         _ptr(x), T, H, _ptr(ids), _id_code(ids.dtype), K, E, _ptr(out.x_perm), _ptr(out.x_perm_scales),
         _ptr(out.group_sizes), _ptr(out.group_offsets), _ptr(out.row_map), _ptr(out.perm_src),
@@ -208,12 +223,12 @@ def moe_permute_nvfp4(x: torch.Tensor, ids: torch.Tensor, E: int, *, amax: Optio
     T, H = x.shape
     K = ids.shape[1]
     if out is None:
-        out = permute_buffers(T, H, K, E, x.device, nvfp4=True)
+        out = permute_buffers(T, H, K, E, x.device, nvfp4=True, stream=stream)
     if amax is None:
-        amax = torch.empty((1,), dtype=torch.float32, device=x.device)
+        amax = _empty((1,), torch.float32, x.device, stream)
     ws_bytes = moe_permute_workspace_size(T, K, E)
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+        workspace = _empty(ws_bytes, torch.uint8, x.device, stream)
     st = _lib.load().moe_permute_nvfp4(
         _ptr(x), T, H, _ptr(ids), _id_code(ids.dtype), K, E, _ptr(amax), _ptr(out.x_perm), _ptr(out.x_perm_scales),
         _ptr(out.group_sizes), _ptr(out.group_offsets), _ptr(out.row_map), _ptr(out.perm_src), _ptr(workspace),
@@ -231,7 +246,7 @@ def moe_permute_noalloc(x: torch.Tensor, ids: torch.Tensor, E: int, *, fuse_mxfp
     T, H = x.shape
     K = ids.shape[1]
     if out is None:
-        out = permute_buffers(T, H, K, E, x.device, fuse_mxfp8)
+        out = permute_buffers(T, H, K, E, x.device, fuse_mxfp8, stream=stream)
     st = _lib.load().moe_permute_noalloc(
         _ptr(x), T, H, _ptr(ids), _id_code(ids.dtype), K, E, _ptr(out.x_perm), _ptr(out.x_perm_scales),
         _ptr(out.group_sizes), _ptr(out.group_offsets), _ptr(out.row_map), _ptr(out.perm_src),
@@ -258,10 +273,10 @@ def moe_quant_mxfp8_grouped(x: torch.Tensor, group_offsets: torch.Tensor, *, col
     R_cap, H = x.shape
     E = group_offsets.numel() - 1
     if q is None:
-        q = torch.empty((R_cap, H), dtype=torch.uint8, device=x.device)
+        q = _empty((R_cap, H), torch.uint8, x.device, stream)
     if scales is None:
         shape = (colwise_scale_rows(R_cap, E), H) if colwise else (R_cap, H // 32)
-        scales = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        scales = _empty(shape, torch.uint8, x.device, stream)
     st = _lib.load().moe_quant_mxfp8_grouped(_ptr(x), R_cap, H, _ptr(group_offsets), E, _ptr(q),
                                              _ptr(scales), MOE_QUANT_COLWISE if colwise else 0,
                                              _stream(stream))
@@ -279,7 +294,7 @@ def moe_unpermute_combine(y_perm: torch.Tensor, row_map: torch.Tensor, probs: to
     T, K = row_map.shape
     H = y_perm.shape[1]
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=y_perm.device)
+        y = _empty((T, H), torch.bfloat16, y_perm.device, stream)
     st = _lib.load().moe_unpermute_combine(_ptr(y_perm), _ptr(row_map), _ptr(probs), T, K, H, _ptr(y),
                                            _stream(stream))
     _check("moe_unpermute_combine", st)
@@ -297,7 +312,7 @@ def moe_route_topk_backward(logits: torch.Tensor, ids: torch.Tensor, dprobs: tor
     T, E = logits.shape
     K = ids.shape[1]
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=torch.float32, device=logits.device)
+        dlogits = _empty((T, E), torch.float32, logits.device, stream)
     _want(dlogits, "dlogits", torch.float32, 2)
     st = _lib.load().moe_route_topk_backward(_ptr(logits), _ptr(ids), _id_code(ids.dtype), _ptr(dprobs), T, E, K,
                                              MOE_ROUTE_RENORM if renorm else 0, _ptr(dlogits), _stream(stream))
@@ -320,9 +335,9 @@ def moe_unpermute_combine_backward(dy: torch.Tensor, y_perm: torch.Tensor, row_m
     T, K = row_map.shape
     H = y_perm.shape[1]
     if dy_perm is None:
-        dy_perm = torch.empty_like(y_perm)    # rows no route maps to are not written
+        dy_perm = _empty(y_perm.shape, y_perm.dtype, y_perm.device, stream)    # rows no route maps to are not written
     if dprobs is None:
-        dprobs = torch.empty((T, K), dtype=torch.float32, device=dy.device)
+        dprobs = _empty((T, K), torch.float32, dy.device, stream)
     _want(dy_perm, "dy_perm", torch.bfloat16, 2)
     _want(dprobs, "dprobs", torch.float32, 2)
     if (dy_perm_q is None) != (dy_perm_scales is None):
@@ -347,7 +362,7 @@ def moe_permute_backward(dx_perm: torch.Tensor, row_map: torch.Tensor, *, dx: Op
     T, K = row_map.shape
     H = dx_perm.shape[1]
     if dx is None:
-        dx = torch.empty((T, H), dtype=torch.bfloat16, device=dx_perm.device)
+        dx = _empty((T, H), torch.bfloat16, dx_perm.device, stream)
     _want(dx, "dx", torch.bfloat16, 2)
     st = _lib.load().moe_permute_backward(_ptr(dx_perm), _ptr(row_map), T, K, H, _ptr(dx), _stream(stream))
     _check("moe_permute_backward", st)
@@ -362,7 +377,7 @@ def moe_ep_recv_expert_ids(recv_counts: torch.Tensor, R_cap: int, *, ids: Option
     _want(recv_counts, "recv_counts", torch.int32, 2)
     G, E_loc = recv_counts.shape
     if ids is None:
-        ids = torch.empty((R_cap,), dtype=torch.int32, device=recv_counts.device)
+        ids = _empty((R_cap,), torch.int32, recv_counts.device, stream)
     _want(ids, "ids", torch.int32, 1)
     st = _lib.load().moe_ep_recv_expert_ids(_ptr(recv_counts), G, E_loc, R_cap, _ptr(ids), _stream(stream))
     _check("moe_ep_recv_expert_ids", st)
@@ -431,10 +446,10 @@ def moe_prepare_weights(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, pr
     dev = w1.device
     fp8 = precision == "mxfp8"
     pdt = torch.uint8 if fp8 else torch.bfloat16
-    w13 = torch.empty((E, 2 * F, H), dtype=pdt, device=dev)
-    w2p = torch.empty((E, H, F), dtype=pdt, device=dev)
-    s13 = torch.empty((E, 2 * F, H // 32), dtype=torch.uint8, device=dev) if fp8 else None
-    s2 = torch.empty((E, H, F // 32), dtype=torch.uint8, device=dev) if fp8 else None
+    w13 = _empty((E, 2 * F, H), pdt, dev, stream)
+    w2p = _empty((E, H, F), pdt, dev, stream)
+    s13 = _empty((E, 2 * F, H // 32), torch.uint8, dev, stream) if fp8 else None
+    s2 = _empty((E, H, F // 32), torch.uint8, dev, stream) if fp8 else None
     st = _lib.load().moe_prepare_weights(_ptr(w1), _ptr(w3), _ptr(w2), E, H, F, _dt_code(precision),
                                          _ptr(w13), _ptr(s13), _ptr(w2p), _ptr(s2), _stream(stream))
     _check("moe_prepare_weights", st)
@@ -452,11 +467,11 @@ def moe_grouped_swiglu_gemm(x_perm: torch.Tensor, x_scales: Optional[torch.Tenso
     R_cap = x_perm.shape[0]
     dev = x_perm.device
     if h is None:
-        h = torch.empty((R_cap, w.F), dtype=torch.uint8 if fp8 else torch.bfloat16, device=dev)
+        h = _empty((R_cap, w.F), torch.uint8 if fp8 else torch.bfloat16, dev, stream)
     if fp8 and h_scales is None:
-        h_scales = torch.empty((R_cap, w.F // 32), dtype=torch.uint8, device=dev)
+        h_scales = _empty((R_cap, w.F // 32), torch.uint8, dev, stream)
     if y_perm is None:
-        y_perm = torch.empty((R_cap, w.H), dtype=torch.bfloat16, device=dev)
+        y_perm = _empty((R_cap, w.H), torch.bfloat16, dev, stream)
     st = _lib.load().moe_grouped_swiglu_gemm(
         _ptr(x_perm), _ptr(x_scales), _ptr(w.w13), _ptr(w.w13_scales), _ptr(w.w2), _ptr(w.w2_scales),
         _dt_code(w.precision), _ptr(group_offsets), w.E, w.H, w.F, R_cap, _ptr(h), _ptr(h_scales),
@@ -474,9 +489,9 @@ def moe_grouped_gemm_up(x_perm: torch.Tensor, x_scales: Optional[torch.Tensor], 
     R_cap = x_perm.shape[0]
     dev = x_perm.device
     if h is None:
-        h = torch.empty((R_cap, w.F), dtype=torch.uint8 if fp8 else torch.bfloat16, device=dev)
+        h = _empty((R_cap, w.F), torch.uint8 if fp8 else torch.bfloat16, dev, stream)
     if fp8 and h_scales is None:
-        h_scales = torch.empty((R_cap, w.F // 32), dtype=torch.uint8, device=dev)
+        h_scales = _empty((R_cap, w.F // 32), torch.uint8, dev, stream)
     st = _lib.load().moe_grouped_gemm_up(
         _ptr(x_perm), _ptr(x_scales), _ptr(w.w13), _ptr(w.w13_scales), _dt_code(w.precision),
         _ptr(group_offsets), w.E, w.H, w.F, R_cap, _ptr(h), _ptr(h_scales), _ptr(ab), _ptr(h_bf16),
@@ -494,7 +509,7 @@ def moe_grouped_gemm_down(h: torch.Tensor, h_scales: Optional[torch.Tensor], w: 
     _want(group_offsets, "group_offsets", torch.int32, 1)
     R_cap = h.shape[0]
     if y_perm is None:
-        y_perm = torch.empty((R_cap, w.H), dtype=torch.bfloat16, device=h.device)
+        y_perm = _empty((R_cap, w.H), torch.bfloat16, h.device, stream)
     st = _lib.load().moe_grouped_gemm_down(
         _ptr(h), _ptr(h_scales), _ptr(w.w2), _ptr(w.w2_scales), _dt_code(w.precision), _ptr(group_offsets),
         w.E, w.H, w.F, R_cap, _ptr(y_perm), _stream(stream))
@@ -510,7 +525,7 @@ def moe_amax_bf16(x: torch.Tensor, *, valid_rows: Optional[torch.Tensor] = None,
     _want(x, "x", torch.bfloat16, None)
     x2 = x.reshape(-1, x.shape[-1])
     if amax is None:
-        amax = torch.empty((1,), dtype=torch.float32, device=x.device)
+        amax = _empty((1,), torch.float32, x.device, stream)
     st = _lib.load().moe_amax_bf16(_ptr(x2), x2.shape[0], x2.shape[1], _ptr(valid_rows), _ptr(amax), _stream(stream))
     _check("moe_amax_bf16", st)
     return amax
@@ -523,9 +538,9 @@ def moe_quant_nvfp4(x: torch.Tensor, amax: torch.Tensor, *, valid_rows: Optional
     _want(x, "x", torch.bfloat16, None)
     C_ = x.shape[-1]
     if q is None:
-        q = torch.empty(x.shape[:-1] + (C_ // 2,), dtype=torch.uint8, device=x.device)
+        q = _empty(x.shape[:-1] + (C_ // 2,), torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty(x.shape[:-1] + (C_ // 16,), dtype=torch.uint8, device=x.device)
+        scales = _empty(x.shape[:-1] + (C_ // 16,), torch.uint8, x.device, stream)
     rows = x.numel() // C_
     st = _lib.load().moe_quant_nvfp4(_ptr(x), rows, C_, _ptr(valid_rows), _ptr(amax), _ptr(q), _ptr(scales),
                                      _stream(stream))
@@ -563,9 +578,9 @@ def moe_grouped_gemm_up_nvfp4(x_q: torch.Tensor, x_scales: torch.Tensor, x_amax:
     """NVFP4 x [R_cap, H/2] -> (h [R_cap, F] bf16 = silu(x W1) * (x W3), h_amax [1] fp32)."""
     R_cap = x_q.shape[0]
     if h is None:
-        h = torch.empty((R_cap, w.F), dtype=torch.bfloat16, device=x_q.device)
+        h = _empty((R_cap, w.F), torch.bfloat16, x_q.device, stream)
     if h_amax is None:
-        h_amax = torch.empty((1,), dtype=torch.float32, device=x_q.device)
+        h_amax = _empty((1,), torch.float32, x_q.device, stream)
     st = _lib.load().moe_grouped_gemm_up_nvfp4(
         _ptr(x_q), _ptr(x_scales), _ptr(x_amax), _ptr(w.w13), _ptr(w.w13_scales), _ptr(w.w13_amax),
         _ptr(group_offsets), w.E, w.H, w.F, R_cap, _ptr(h), _ptr(h_amax), _ptr(ab), _stream(stream))
@@ -579,7 +594,7 @@ def moe_grouped_gemm_down_nvfp4(h_q: torch.Tensor, h_scales: torch.Tensor, h_ama
     """NVFP4 h [R_cap, F/2] -> y_perm [R_cap, H] bf16 = h W2."""
     R_cap = h_q.shape[0]
     if y_perm is None:
-        y_perm = torch.empty((R_cap, w.H), dtype=torch.bfloat16, device=h_q.device)
+        y_perm = _empty((R_cap, w.H), torch.bfloat16, h_q.device, stream)
     st = _lib.load().moe_grouped_gemm_down_nvfp4(
         _ptr(h_q), _ptr(h_scales), _ptr(h_amax), _ptr(w.w2), _ptr(w.w2_scales), _ptr(w.w2_amax),
         _ptr(group_offsets), w.E, w.H, w.F, R_cap, _ptr(y_perm), _stream(stream))
@@ -607,10 +622,10 @@ def moe_prepare_weights_bwd(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor
     dev = w1.device
     fp8 = precision == "mxfp8"
     pdt = torch.uint8 if fp8 else torch.bfloat16
-    w2b = torch.empty((E, F, H), dtype=pdt, device=dev)
-    w13t = torch.empty((E, H, 2 * F), dtype=pdt, device=dev)
-    s2 = torch.empty((E, F, H // 32), dtype=torch.uint8, device=dev) if fp8 else None
-    s13 = torch.empty((E, H, 2 * F // 32), dtype=torch.uint8, device=dev) if fp8 else None
+    w2b = _empty((E, F, H), pdt, dev, stream)
+    w13t = _empty((E, H, 2 * F), pdt, dev, stream)
+    s2 = _empty((E, F, H // 32), torch.uint8, dev, stream) if fp8 else None
+    s13 = _empty((E, H, 2 * F // 32), torch.uint8, dev, stream) if fp8 else None
     st = _lib.load().moe_prepare_weights_bwd(_ptr(w1), _ptr(w3), _ptr(w2), E, H, F, _dt_code(precision),
                                              _ptr(w2b), _ptr(s2), _ptr(w13t), _ptr(s13), _stream(stream))
     _check("moe_prepare_weights_bwd", st)
@@ -626,7 +641,7 @@ def moe_grouped_swiglu_dgrad(dy: torch.Tensor, dy_scales: Optional[torch.Tensor]
     writes the row-wise MXFP8 codes and scales of dab into them."""
     R_cap = dy.shape[0]
     if dab is None:
-        dab = torch.empty((R_cap, 2 * bw.F), dtype=torch.bfloat16, device=dy.device)
+        dab = _empty((R_cap, 2 * bw.F), torch.bfloat16, dy.device, stream)
     if (dab_q is None) != (dab_scales is None):
         raise ValueError("dab_q and dab_scales go together")
     if dab_q is not None:
@@ -647,7 +662,7 @@ def moe_grouped_gemm_dx(dab: torch.Tensor, dab_scales: Optional[torch.Tensor], b
     """dab [R_cap, 2F] (bf16 or MXFP8 codes) -> dx [R_cap, H] bf16."""
     R_cap = dab.shape[0]
     if dx is None:
-        dx = torch.empty((R_cap, bw.H), dtype=torch.bfloat16, device=dab.device)
+        dx = _empty((R_cap, bw.H), torch.bfloat16, dab.device, stream)
     st = _lib.load().moe_grouped_gemm_dx(
         _ptr(dab), _ptr(dab_scales), _ptr(bw.w13t), _ptr(bw.w13t_scales), _dt_code(bw.precision),
         _ptr(group_offsets), bw.E, bw.H, bw.F, R_cap, _ptr(dx), _stream(stream))
@@ -672,9 +687,9 @@ def moe_grouped_transpose(x: torch.Tensor, group_offsets: torch.Tensor, precisio
     kpad = moe_grouped_transpose_kpad(R_cap, E)
     fp8 = precision == "mxfp8"
     if xT is None:
-        xT = torch.empty((C, kpad), dtype=torch.uint8 if fp8 else torch.bfloat16, device=x.device)
+        xT = _empty((C, kpad), torch.uint8 if fp8 else torch.bfloat16, x.device, stream)
     if fp8 and xT_scales is None:
-        xT_scales = torch.empty((C, kpad // 32), dtype=torch.uint8, device=x.device)
+        xT_scales = _empty((C, kpad // 32), torch.uint8, x.device, stream)
     st = _lib.load().moe_grouped_transpose(_ptr(x), _ptr(src_rows), R_cap, C, _ptr(group_offsets), E,
                                            _dt_code(precision), _ptr(xT), _ptr(xT_scales), _stream(stream))
     _check("moe_grouped_transpose", st)
@@ -691,11 +706,11 @@ def moe_grouped_gemm_wgrad(aT: torch.Tensor, aT_scales: Optional[torch.Tensor], 
     dev = aT.device
     if split:
         if dw is None:
-            dw = torch.empty((E, M, N // 2), dtype=torch.bfloat16, device=dev)
+            dw = _empty((E, M, N // 2), torch.bfloat16, dev, stream)
         if dw2 is None:
-            dw2 = torch.empty((E, M, N // 2), dtype=torch.bfloat16, device=dev)
+            dw2 = _empty((E, M, N // 2), torch.bfloat16, dev, stream)
     elif dw is None:
-        dw = torch.empty((E, M, N), dtype=torch.bfloat16, device=dev)
+        dw = _empty((E, M, N), torch.bfloat16, dev, stream)
     st = _lib.load().moe_grouped_gemm_wgrad(
         _ptr(aT), _ptr(aT_scales), _ptr(bT), _ptr(bT_scales), _dt_code(precision), _ptr(group_offsets), E, M, N,
         R_cap, _ptr(dw), _ptr(dw2 if split else None), _stream(stream))
@@ -704,10 +719,11 @@ def moe_grouped_gemm_wgrad(aT: torch.Tensor, aT_scales: Optional[torch.Tensor], 
 
 
 # ---------------------------------------------------------- the layer for a few tokens
-def moe_layer_few_tokens_workspace(w: PackedWeights, T: int, K: int) -> torch.Tensor:
-    """The workspace of moe_layer_few_tokens for up to T tokens (uninitialised, reusable)."""
+def moe_layer_few_tokens_workspace(w: PackedWeights, T: int, K: int, stream=None) -> torch.Tensor:
+    """The workspace of moe_layer_few_tokens for up to T tokens (uninitialised, reusable; stream: the one of
+    the first call that uses it)."""
     n = _lib.load().moe_layer_few_tokens_workspace_size(T, K, w.E, w.H, w.F, _dt_code(w.precision))
-    return torch.empty(int(n), dtype=torch.uint8, device=w.w13.device)
+    return _empty(int(n), torch.uint8, w.w13.device, stream)
 
 
 def moe_layer_few_tokens(x: torch.Tensor, logits: Optional[torch.Tensor], w: PackedWeights, K: int, *,
@@ -725,19 +741,19 @@ def moe_layer_few_tokens(x: torch.Tensor, logits: Optional[torch.Tensor], w: Pac
     elif ids is None or probs is None:
         raise ValueError("without logits, ids and probs are inputs")
     if ids is None:
-        ids = torch.empty((T, K), dtype=id_dtype, device=x.device)
+        ids = _empty((T, K), id_dtype, x.device, stream)
     else:
         _like(ids, "ids", ids.dtype, (T, K))
     if probs is None:
-        probs = torch.empty((T, K), dtype=torch.float32, device=x.device)
+        probs = _empty((T, K), torch.float32, x.device, stream)
     else:
         _like(probs, "probs", torch.float32, (T, K))
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, x.dtype, x.device, stream)
     else:
         _like(y, "y", torch.bfloat16, (T, H))
     if workspace is None:
-        workspace = moe_layer_few_tokens_workspace(w, T, K)
+        workspace = moe_layer_few_tokens_workspace(w, T, K, stream)
     else:
         _scratch(workspace)
     st = _lib.load().moe_layer_few_tokens(
@@ -787,7 +803,7 @@ def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     _like(bias, "bias", weight.dtype, (H,))
     _like(residual, "residual", dtype, shape)
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, x.dtype, x.device, stream)
     else:
         _like(y, "y", dtype, shape)
     if sum is not None:
@@ -795,13 +811,13 @@ def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
             raise ValueError("sum goes with residual")
         _like(sum, "sum", dtype, shape)
     elif residual is not None:
-        sum = torch.empty_like(x)
+        sum = _empty(x.shape, x.dtype, x.device, stream)
     if mean is None:
-        mean = torch.empty(T, dtype=torch.float32, device=x.device)
+        mean = _empty(T, torch.float32, x.device, stream)
     else:
         _like(mean, "mean", torch.float32, (T,))
     if rstd is None:
-        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+        rstd = _empty(T, torch.float32, x.device, stream)
     else:
         _like(rstd, "rstd", torch.float32, (T,))
     st = _lib.load().moe_layer_norm(x.data_ptr(), _at(residual), T, H, code, weight.data_ptr(), _at(bias), wcode, eps,
@@ -833,19 +849,19 @@ def moe_layer_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Ten
     _like(rstd, "rstd", torch.float32, (T,))
     _like(dx_add, "dx_add", dtype, shape)
     if dx is None:
-        dx = torch.empty_like(s)
+        dx = _empty(s.shape, s.dtype, s.device, stream)
     else:
         _like(dx, "dx", dtype, shape)
     if dweight is None:
-        dweight = torch.empty_like(weight)
+        dweight = _empty(weight.shape, weight.dtype, weight.device, stream)
     else:
         _like(dweight, "dweight", wdtype, (H,))
     if dbias is None:
-        dbias = torch.empty_like(weight)
+        dbias = _empty(weight.shape, weight.dtype, weight.device, stream)
     else:
         _like(dbias, "dbias", wdtype, (H,))
     if workspace is None:
-        workspace = torch.empty(moe_layer_norm_backward_workspace_size(T, H), dtype=torch.uint8, device=s.device)
+        workspace = _empty(moe_layer_norm_backward_workspace_size(T, H), torch.uint8, s.device, stream)
     else:
         _scratch(workspace)
     st = _lib.load().moe_layer_norm_backward(dy.data_ptr(), s.data_ptr(), T, H, code, weight.data_ptr(), wcode,
@@ -885,14 +901,14 @@ def _grad_norm_clip(grads, outs, max_norm, eps, norm, workspace, stream):
     if norm is None:
         if n == 0:
             raise ValueError("no gradients: pass norm, the tensor to write")
-        norm = torch.empty(1, dtype=torch.float32, device=grads[0].device)
+        norm = _empty(1, torch.float32, grads[0].device, stream)
     else:
         _want(norm, "norm", torch.float32, None)
         if norm.numel() != 1:
             raise ValueError("norm must hold one value")
     L = _lib.load()
     if workspace is None:
-        workspace = torch.empty(L.moe_grad_norm_workspace_size(n), dtype=torch.uint8, device=norm.device)
+        workspace = _empty(L.moe_grad_norm_workspace_size(n), torch.uint8, norm.device, stream)
     else:
         _scratch(workspace)
     counts, codes = array("q", counts), array("i", codes)

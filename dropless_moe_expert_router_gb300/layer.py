@@ -191,10 +191,10 @@ class MoELayer:
         w, K = self.weights, self.K
         if self._few_workspace is None:
             t = min(64, 4096 // K)        # the most tokens that the sizes allow
-            self._few_workspace = api.moe_layer_few_tokens_workspace(w, t, K)
+            self._few_workspace = api.moe_layer_few_tokens_workspace(w, t, K, stream)
             while t > 1 and not self._few_workspace.numel():
                 t -= 1
-                self._few_workspace = api.moe_layer_few_tokens_workspace(w, t, K)
+                self._few_workspace = api.moe_layer_few_tokens_workspace(w, t, K, stream)
         if self.score == "sigmoid":
             ids, probs = api.moe_route_sigmoid_topk(logits, K, expert_bias=self.expert_bias, renorm=self.renorm,
                                                     id_dtype=self.ids.dtype, stream=stream)
