@@ -637,7 +637,8 @@ __device__ __forceinline__ void cta_sums(float (&v)[2 * R], float2* red, int thr
 // the row that was there; those take R rows at a time. dweight and dbias add up in the threads' registers
 // over the CTA's rows and leave as one partial sum per CTA: part [gridDim.x][2][H]. 8192 x 7168 bf16 with
 // dx_add, 470 MB: 86-88 us with the columns' kernel, 5.4 TB/s; a copy of as many bytes takes 77 us. (Refilled by
-// thread 0 between the barriers, as in the forward, it took 98 us.)
+// thread 0 between the barriers, as in the forward, it took 98 us.) xh is (s - mean) rstd in both passes: one fma
+// s rstd - mean rstd would save 1 us of that and lose |mean| rstd units of xh's last place.
 template <typename T, typename W, int VEC, int NV, int R, bool ODD>
 __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, const T* s, int rows, int H,
                                                                const W* __restrict__ w, const float* __restrict__ mean,
@@ -745,7 +746,6 @@ __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, cons
             if (++st == stages) { st = 0; phase ^= 1u; }
             const V* gr = reinterpret_cast<const V*>(smem + (size_t)at[k] * stage_bytes);
             const V* sr = reinterpret_cast<const V*>(smem + (size_t)at[k] * stage_bytes + rb);
-            const float nm = -m[k] * r[k];
 #pragma unroll
             for (int i = 0; i < NV; i++) {
                 const int c = me + i * tpr;
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, cons
                 const V gv = gr[c], sv = sr[c];
 #pragma unroll
                 for (int j = 0; j < VEC; j++) {
-                    const float d = gv.get(j), xh = fmaf(sv.get(j), r[k], nm), q = d * wv[i].get(j);
+                    const float d = gv.get(j), xh = (sv.get(j) - m[k]) * r[k], q = d * wv[i].get(j);
                     sums[2 * k] += q;
                     sums[2 * k + 1] = fmaf(q, xh, sums[2 * k + 1]);
                     dw[i][j] = fmaf(d, xh, dw[i][j]);
@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, cons
 #pragma unroll
             for (int k = 0; k < R; k++) {
                 if (k >= nr) continue;
-                const float xh = fmaf(es[k], r[k], -m[k] * r[k]), q = eg[k] * ew;
+                const float xh = (es[k] - m[k]) * r[k], q = eg[k] * ew;
                 sums[2 * k] += q;
                 sums[2 * k + 1] = fmaf(q, xh, sums[2 * k + 1]);
                 edw = fmaf(eg[k], xh, edw);
@@ -781,8 +781,7 @@ __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, cons
             const V* gr = reinterpret_cast<const V*>(smem + (size_t)at[k] * stage_bytes);
             const V* sr = reinterpret_cast<const V*>(smem + (size_t)at[k] * stage_bytes + rb);
             const V* ar = reinterpret_cast<const V*>(smem + (size_t)at[k] * stage_bytes + 2 * rb);
-            // r (g - a - xh c) = r w dy + ks s + k0
-            const float ks = -(sums[2 * k + 1] * per_h) * r[k] * r[k], k0 = -fmaf(ks, m[k], r[k] * (sums[2 * k] * per_h));
+            const float a = sums[2 * k] * per_h, c2 = sums[2 * k + 1] * per_h;
 #pragma unroll
             for (int i = 0; i < NV; i++) {
                 const int c = me + i * tpr;
@@ -793,7 +792,8 @@ __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, cons
                 float f[VEC];
 #pragma unroll
                 for (int j = 0; j < VEC; j++) {
-                    f[j] = fmaf(gv.get(j), r[k] * wv[i].get(j), fmaf(sv.get(j), ks, k0));
+                    const float xh = (sv.get(j) - m[k]) * r[k];
+                    f[j] = r[k] * fmaf(-xh, c2, fmaf(gv.get(j), wv[i].get(j), -a));
                     if (add) f[j] += av.get(j);
                 }
                 o.set(f);
@@ -801,7 +801,8 @@ __global__ void __launch_bounds__(544) ln_backward_ring_kernel(const T* dy, cons
             }
             if (l.single()) {
                 const float4 e = own[k][tpr - 1 - me];
-                dx[l.row(g * R + k) * H + l.edge] = from_f<T>(fmaf(e.x, r[k] * ew, fmaf(e.y, ks, k0)) + e.z);
+                const float xh = (e.y - m[k]) * r[k];
+                dx[l.row(g * R + k) * H + l.edge] = from_f<T>(r[k] * fmaf(-xh, c2, fmaf(e.x, ew, -a)) + e.z);
             }
             __syncwarp();
             if (lane_id() == 0) ptx::mbar_arrive(&empty[at[k]]);

@@ -374,3 +374,61 @@ def test_tensors_off_the_boundary_differently(T, H, dt):
     got = api.moe_layer_norm_backward(a1(dy), a0(s), w, o.mean, o.rstd, dx_add=a2(r), dx=a1(x))
     _backward_check(got, dy, s, w, o.mean, o.rstd, r)
     assert a0.intact() and a1.intact() and a2.intact()
+
+
+def _large_mean_check(dy, s, w, add, dx=None):
+    """The backward of rows whose mean is many standard deviations, from statistics exact to fp32. The
+    bars take xh to 4 u of itself, two roundings with room, whatever the mean: s - mean loses nothing."""
+    S = s.double()
+    mean64 = S.mean(1)
+    mean = mean64.float()
+    rstd = ((S - mean64[:, None]).square().mean(1) + 1e-5).rsqrt().float()
+    got = api.moe_layer_norm_backward(dy, s, w, mean, rstd, dx_add=add, dx=dx)
+    T, H = s.shape
+    G, GT = (H / 32 + 64) * U, (T + 64) * U
+    rx, rw, rb, xh, g = _backward_reference(dy, s, w, mean, rstd, add)
+    R = rstd.double()[:, None]
+    exh = 4 * U * xh.abs()
+    c = (g * xh).mean(1, keepdim=True).abs()
+    sums = G * (g.abs().mean(1, keepdim=True) + xh.abs() * (g * xh).abs().mean(1, keepdim=True)) \
+        + xh.abs() * (g.abs() * exh).mean(1, keepdim=True)
+    terms = g.abs() + g.mean(1, keepdim=True).abs() + xh.abs() * c
+    e = R * (sums + 16 * U * terms + exh * c)
+    if add is not None:
+        e = e + 2 * U * (add.double().abs() + rx.abs())
+    _within(got[0], rx, e + 1.01 * _half(s.dtype) * rx.abs() + 1e-38)
+    D = dy.double().abs()
+    _within(got[1], rw, GT * (D * xh.abs()).sum(0) + (D * exh).sum(0) + 1.01 * _half(w.dtype) * rw.abs() + 1e-38)
+    _within(got[2], rb, GT * D.sum(0) + 1.01 * _half(w.dtype) * rb.abs() + 1e-38)
+
+
+@pytest.mark.parametrize("ratio", [1e2, 1e3, 1e4])
+@pytest.mark.parametrize("T,H", [(2500, 128), (40, 1024), (200, 4096), (9, 8192), (40, 1021), (1100, 1021), (40, 2001),
+                                 (9, 8001), (20, 9001), (20, 12288)])
+def test_backward_of_rows_with_a_large_mean(T, H, ratio):
+    """Every kernel of the backward: rows in registers, through the ring (on and off the boundary), long ones."""
+    x, w, _, r, dy = _inputs(T, H, F32, F32, seed=T + H, mean=1.5 * ratio)
+    for add in (None, r):
+        _large_mean_check(dy, x, w, add)
+
+
+@pytest.mark.parametrize("dt,wdt,ratio", [(F32, BF, 1e3), (BF, BF, 1e2), (BF, F32, 1e2)])
+@pytest.mark.parametrize("T,H", [(40, 2048), (33, 8184), (1500, 1021), (20, 8193)])
+def test_backward_of_rows_with_a_large_mean_other_types(T, H, dt, wdt, ratio):
+    x, w, _, r, dy = _inputs(T, H, dt, wdt, seed=T + H, mean=1.5 * ratio)
+    _large_mean_check(dy, x, w, r)
+
+
+def test_backward_of_rows_with_a_large_mean_elsewhere_against_16_bytes():
+    x, w, _, r, dy = _inputs(40, 3001, F32, F32, seed=1, mean=1.5e3)
+    _large_mean_check(dy, x, w, r, dx=_Fenced(1)(x))
+
+
+@pytest.mark.parametrize("T,H", [(40, 1024), (9, 8192), (1100, 1021), (20, 12288)])
+def test_backward_of_constant_rows(T, H):
+    """s = mean in every place: xh is 0, so no weight gradient comes of it."""
+    _, w, _, _, dy = _inputs(T, H, F32, F32, seed=3)
+    s = torch.full((T, H), 1000.1, device="cuda")
+    mean, rstd = s[:, 0].contiguous(), torch.full((T,), 1e-5 ** -0.5, device="cuda")
+    _, dw, db = api.moe_layer_norm_backward(dy, s, w, mean, rstd)
+    assert not dw.any() and db.any()
