@@ -146,6 +146,15 @@ __device__ __noinline__ void prep_exact(const float* row, int E, int K, PrepSmem
     __syncthreads();
 }
 
+// The sum of num over the chosen (rank >= 0) in the order of their ranks: which thread has which entry of the list is
+// chance. (Inlined, with its barrier, it made the whole kernel slower: the 2,304-expert layer 63.5 -> 66.4 us.)
+__device__ __noinline__ float prep_ordered_sum(float num, int rank, int K, PrepSmem& sm) {
+    float* by_rank = reinterpret_cast<float*>(sm.key);        // (every thread is done with the keys)
+    if (rank >= 0) by_rank[rank] = num;
+    __syncthreads();
+    return prep_reduce<false>((int)threadIdx.x < K ? by_rank[threadIdx.x] : 0.0f, sm.red[1]);
+}
+
 template <int V>
 __device__ void prep_route(const PrepArgs& p, int t, PrepSmem& sm) {
     const int tid = threadIdx.x;
@@ -223,7 +232,7 @@ __device__ void prep_route(const PrepArgs& p, int t, PrepSmem& sm) {
     const unsigned k = (unsigned)(mine >> 32);
     const int e = (int)~(unsigned)mine;
     const float num = chosen ? expf(key_value(k) - m) : 0.0f;
-    if (p.renorm) den = prep_reduce<false>(num, sm.red[1]);
+    if (p.renorm) den = V > 1 ? prep_ordered_sum(num, chosen ? rank : -1, p.K, sm) : prep_reduce<false>(num, sm.red[1]);
     if (chosen) {
         const long long o = (long long)t * p.K + rank;
         if (p.i16) static_cast<int16_t*>(p.ids)[o] = (int16_t)e;

@@ -307,3 +307,19 @@ def test_few_tokens_joined_in_two_steps(T, H, E, K, F, precision):
     for _ in range(5):
         assert torch.equal(y, api.moe_layer_few_tokens(x, lg, packed, K)[0])
     assert api.moe_get_device_errors() == 0
+
+
+@pytest.mark.parametrize("T,E,K", [(64, 2304, 36), (40, 1024, 100), (64, 8192, 16)])
+def test_few_tokens_renormalised_probs_repeat_bit_for_bit(T, E, K):
+    """Above 256 experts the chosen logits are listed in the order in which the threads find them; the sum
+    over them is not in that order."""
+    _, packed = _weights(1, 128, 128, "bf16", seed=1)
+    w = packed._replace(E=E, w13=packed.w13.expand(E, -1, -1).contiguous(), w2=packed.w2.expand(E, -1, -1).contiguous())
+    x, lg = _inputs(T, 128, E, seed=E + K)
+    ws = api.moe_layer_few_tokens_workspace(w, T, K)
+    y, ids, probs = api.moe_layer_few_tokens(x, lg, w, K, renorm=True, workspace=ws)
+    chosen = torch.gather(lg.double(), 1, ids.long())
+    assert (probs.double() - torch.softmax(chosen, 1)).abs().max().item() <= 1e-6
+    for _ in range(200):
+        y2, ids2, probs2 = api.moe_layer_few_tokens(x, lg, w, K, renorm=True, workspace=ws)
+        assert torch.equal(ids, ids2) and torch.equal(probs, probs2) and torch.equal(y, y2)
