@@ -437,23 +437,45 @@ class PackedWeights(NamedTuple):
     w2_scales: Optional[torch.Tensor]   # [E, H, F/32] uint8 (MXFP8)
 
 
+def _want_packed(out, kind, shapes) -> None:
+    """out is a kind of packed weights with these scalars first and these shapes (None: no tensor) after them."""
+    n = len(out) - len(shapes[1])
+    if type(out) is not kind or tuple(out[:n]) != shapes[0]:
+        raise ValueError(f"out must be the {kind.__name__} of weights of this precision and size")
+    for t, name, want in zip(out[n:], kind._fields[n:], shapes[1]):
+        if want is None:
+            continue
+        if t is None:
+            raise ValueError(f"out has no {name}")
+        _like(t, name, want[0], want[1])
+
+
 def moe_prepare_weights(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, precision: str = "bf16",
-                        stream=None) -> PackedWeights:
-    """Pack logical W1, W3 [E, H, F] and W2 [E, F, H] (bf16) for the grouped GEMMs (one-time)."""
+                        stream=None, out: Optional[PackedWeights] = None) -> PackedWeights:
+    """Pack logical W1, W3 [E, H, F] and W2 [E, F, H] (bf16) for the grouped GEMMs: into new buffers, or
+    into those of out (packed before from weights of the same sizes that have changed since)."""
     for t, n in ((w1, "w1"), (w3, "w3"), (w2, "w2")):
         _want(t, n, torch.bfloat16, 3)
     E, H, F = w1.shape
     dev = w1.device
     fp8 = precision == "mxfp8"
     pdt = torch.uint8 if fp8 else torch.bfloat16
-    w13 = _empty((E, 2 * F, H), pdt, dev, stream)
-    w2p = _empty((E, H, F), pdt, dev, stream)
-    s13 = _empty((E, 2 * F, H // 32), torch.uint8, dev, stream) if fp8 else None
-    s2 = _empty((E, H, F // 32), torch.uint8, dev, stream) if fp8 else None
+    if out is None:
+        w13 = _empty((E, 2 * F, H), pdt, dev, stream)
+        w2p = _empty((E, H, F), pdt, dev, stream)
+        s13 = _empty((E, 2 * F, H // 32), torch.uint8, dev, stream) if fp8 else None
+        s2 = _empty((E, H, F // 32), torch.uint8, dev, stream) if fp8 else None
+        out = PackedWeights(precision, E, H, F, w13, s13, w2p, s2)
+    else:
+        u8 = torch.uint8
+        _want_packed(out, PackedWeights, ((precision, E, H, F), (
+            (pdt, (E, 2 * F, H)), (u8, (E, 2 * F, H // 32)) if fp8 else None,
+            (pdt, (E, H, F)), (u8, (E, H, F // 32)) if fp8 else None)))
     st = _lib.load().moe_prepare_weights(_ptr(w1), _ptr(w3), _ptr(w2), E, H, F, _dt_code(precision),
-                                         _ptr(w13), _ptr(s13), _ptr(w2p), _ptr(s2), _stream(stream))
+                                         _ptr(out.w13), _ptr(out.w13_scales), _ptr(out.w2), _ptr(out.w2_scales),
+                                         _stream(stream))
     _check("moe_prepare_weights", st)
-    return PackedWeights(precision, E, H, F, w13, s13, w2p, s2)
+    return out
 
 
 def moe_grouped_swiglu_gemm(x_perm: torch.Tensor, x_scales: Optional[torch.Tensor], w: PackedWeights,
@@ -560,15 +582,23 @@ class Nvfp4Weights(NamedTuple):
     w2_amax: torch.Tensor      # [1] fp32
 
 
-def moe_prepare_weights_nvfp4(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, stream=None) -> Nvfp4Weights:
-    """One-time: pack the logical weights (bf16) into the grouped GEMMs' layouts and quantise each
-    stacked tensor row-wise to NVFP4 along its contraction dimension, with its own amax."""
+def moe_prepare_weights_nvfp4(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, stream=None,
+                              out: Optional[Nvfp4Weights] = None) -> Nvfp4Weights:
+    """Pack the logical weights (bf16) into the grouped GEMMs' layouts and quantise each stacked tensor
+    row-wise to NVFP4 along its contraction dimension, with its own amax: into new buffers, or into those of out."""
     pw = moe_prepare_weights(w1, w3, w2, "bf16", stream=stream)
-    a13 = moe_amax_bf16(pw.w13, stream=stream)
-    q13, s13 = moe_quant_nvfp4(pw.w13, a13, stream=stream)
-    a2 = moe_amax_bf16(pw.w2, stream=stream)
-    q2, s2 = moe_quant_nvfp4(pw.w2, a2, stream=stream)
-    return Nvfp4Weights(pw.E, pw.H, pw.F, q13, s13, a13, q2, s2, a2)
+    E, H, F = pw.E, pw.H, pw.F
+    o = Nvfp4Weights(E, H, F, *[None] * 6) if out is None else out
+    if out is not None:
+        u8, f32 = torch.uint8, torch.float32
+        _want_packed(out, Nvfp4Weights, ((E, H, F), (
+            (u8, (E, 2 * F, H // 2)), (u8, (E, 2 * F, H // 16)), (f32, (1,)),
+            (u8, (E, H, F // 2)), (u8, (E, H, F // 16)), (f32, (1,)))))
+    a13 = moe_amax_bf16(pw.w13, amax=o.w13_amax, stream=stream)
+    q13, s13 = moe_quant_nvfp4(pw.w13, a13, q=o.w13, scales=o.w13_scales, stream=stream)
+    a2 = moe_amax_bf16(pw.w2, amax=o.w2_amax, stream=stream)
+    q2, s2 = moe_quant_nvfp4(pw.w2, a2, q=o.w2, scales=o.w2_scales, stream=stream)
+    return Nvfp4Weights(E, H, F, q13, s13, a13, q2, s2, a2)
 
 
 def moe_grouped_gemm_up_nvfp4(x_q: torch.Tensor, x_scales: torch.Tensor, x_amax: torch.Tensor, w: Nvfp4Weights,
@@ -614,22 +644,30 @@ class BwdWeights(NamedTuple):
 
 
 def moe_prepare_weights_bwd(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, precision: str = "bf16",
-                            stream=None) -> BwdWeights:
-    """Pack logical W1, W3 [E, H, F] and W2 [E, F, H] for the backward GEMMs (one-time)."""
+                            stream=None, out: Optional[BwdWeights] = None) -> BwdWeights:
+    """Pack logical W1, W3 [E, H, F] and W2 [E, F, H] for the backward GEMMs: into new buffers, or into those of out."""
     for t, n in ((w1, "w1"), (w3, "w3"), (w2, "w2")):
         _want(t, n, torch.bfloat16, 3)
     E, H, F = w1.shape
     dev = w1.device
     fp8 = precision == "mxfp8"
     pdt = torch.uint8 if fp8 else torch.bfloat16
-    w2b = _empty((E, F, H), pdt, dev, stream)
-    w13t = _empty((E, H, 2 * F), pdt, dev, stream)
-    s2 = _empty((E, F, H // 32), torch.uint8, dev, stream) if fp8 else None
-    s13 = _empty((E, H, 2 * F // 32), torch.uint8, dev, stream) if fp8 else None
+    if out is None:
+        w2b = _empty((E, F, H), pdt, dev, stream)
+        w13t = _empty((E, H, 2 * F), pdt, dev, stream)
+        s2 = _empty((E, F, H // 32), torch.uint8, dev, stream) if fp8 else None
+        s13 = _empty((E, H, 2 * F // 32), torch.uint8, dev, stream) if fp8 else None
+        out = BwdWeights(precision, E, H, F, w2b, s2, w13t, s13)
+    else:
+        u8 = torch.uint8
+        _want_packed(out, BwdWeights, ((precision, E, H, F), (
+            (pdt, (E, F, H)), (u8, (E, F, H // 32)) if fp8 else None,
+            (pdt, (E, H, 2 * F)), (u8, (E, H, 2 * F // 32)) if fp8 else None)))
     st = _lib.load().moe_prepare_weights_bwd(_ptr(w1), _ptr(w3), _ptr(w2), E, H, F, _dt_code(precision),
-                                             _ptr(w2b), _ptr(s2), _ptr(w13t), _ptr(s13), _stream(stream))
+                                             _ptr(out.w2b), _ptr(out.w2b_scales), _ptr(out.w13t),
+                                             _ptr(out.w13t_scales), _stream(stream))
     _check("moe_prepare_weights_bwd", st)
-    return BwdWeights(precision, E, H, F, w2b, s2, w13t, s13)
+    return out
 
 
 def moe_grouped_swiglu_dgrad(dy: torch.Tensor, dy_scales: Optional[torch.Tensor], bw: BwdWeights,

@@ -4,8 +4,8 @@
 
 The block keeps the residual stream and the update apart, as a stack of blocks hands them on:
 ``forward`` takes (x, delta) and gives (s, delta'), and the next block's norm adds them. A
-training step is ``forward``, ``backward`` and ``clip_gradients``; serving calls ``step`` with
-the few tokens of a decoding step. The router's projection is an ordinary dense product and is
+training step is ``forward``, ``backward``, ``clip_gradients``, an optimiser's update of the parameters
+in place, and ``repack``; serving calls ``step`` with the few tokens of a decoding step. The router's projection is an ordinary dense product and is
 left to torch; the norm, the layer, their backward passes and the clipping are the library's.
 """
 from __future__ import annotations
@@ -23,7 +23,8 @@ class MoEBlock:
                  norm_weight: torch.Tensor, norm_bias: Optional[torch.Tensor] = None, *, T: int, K: int,
                  eps: float = 1e-5, **layer_args):
         """Expert weights as MoELayer takes them, router [E, H] fp32, norm_weight and norm_bias [H];
-        the remaining arguments are MoELayer's (precision, renorm, training, score, ...)."""
+        the remaining arguments are MoELayer's (precision, renorm, training, score, ...). The block keeps
+        the tensors themselves; the layer also keeps packed copies of w1, w3 and w2 (``repack``)."""
         E, H, _ = w1.shape
         if tuple(router.shape) != (E, H) or router.dtype != torch.float32:
             raise ValueError("router must be [E, H] float32")
@@ -63,6 +64,10 @@ class MoEBlock:
         if self.norm_bias is not None:
             self.gradients["norm_bias"] = dnb
         return dsum
+
+    def repack(self, stream=None) -> None:
+        """After an update of w1, w3 or w2 in place: without it the kernels compute with the weights from before."""
+        self.layer.repack(stream)
 
     def clip_gradients(self, max_norm: float) -> torch.Tensor:
         """Scale the gradients in place to a global norm of at most max_norm; the norm they had ([1] fp32

@@ -104,6 +104,18 @@ class MoELayer:
             self.dW3 = torch.empty((E, H, F), dtype=bf, device=dev)
             self.dW2 = torch.empty((E, F, H), dtype=bf, device=dev)
 
+    def repack(self, stream=None) -> None:
+        """Pack w1, w3 and w2 (the tensors that the layer was made with, changed in place) again: every
+        later call computes with them. The kernels read packed copies, so this follows each update of the
+        weights. It writes the buffers that are there, packed_weights of another layer's among them, so
+        captured graphs and the layers that share them follow; it is not to overlap with calls that read them."""
+        if self.nv4:
+            api.moe_prepare_weights_nvfp4(*self._w, stream=stream, out=self.weights)
+        else:
+            api.moe_prepare_weights(*self._w, self.precision, stream=stream, out=self.weights)
+        if self.training:
+            api.moe_prepare_weights_bwd(*self._w, self.precision, stream=stream, out=self.bwd_weights)
+
     # number of library kernel launches one forward enqueues: router 1, permute 2 or 3
     # (rank, [scan,] scatter), GEMM 2, combine 1
     @property

@@ -9,6 +9,7 @@ import torch
 
 from dropless_moe_expert_router_gb300 import api
 from dropless_moe_expert_router_gb300.block import MoEBlock
+from dropless_moe_expert_router_gb300.layer import MoELayer
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +129,82 @@ def test_workspaces_of_another_kind_are_refused():
             api.moe_layer_norm_backward(x, x, w, o.mean, o.rstd, workspace=ws)
         with pytest.raises(ValueError):
             api.moe_grad_norm([x], workspace=ws)
+
+
+@pytest.mark.parametrize("precision", ["bf16", "mxfp8"])
+def test_two_training_steps(precision):
+    """Forward, backward, an update of every parameter in place, and again: the second step and the
+    few-token step compute with the updated weights. MXFP8 rounds each operand by up to 2^-4, and with it
+    every product of the forward by that much of one of many independent terms: its bar is 8e-2."""
+    T, H, E, K, F = 128, 512, 8, 2, 512
+    p = _params(E, H, F, seed=21)
+    blk = _block(p, T, K, renorm=True, training=True, precision=precision)
+    mine = dict(w1=blk.layer._w[0], w3=blk.layer._w[1], w2=blk.layer._w[2], router=blk.router,
+                norm_weight=blk.norm_weight, norm_bias=blk.norm_bias)
+    g = torch.Generator().manual_seed(22)
+    x, ds, dd = ((torch.randn((T, H), generator=g) * k).to(torch.bfloat16) for k in (1.0, 0.1, 0.1))
+    bar, gbar = (1e-2, 3e-2) if precision == "bf16" else (8e-2, 2e-1)
+    for step in range(2):
+        _, out = blk.forward(x.cuda())
+        ids = blk.layer.ids.cpu().long()
+        q = {k: v.detach().cpu().double().requires_grad_() for k, v in mine.items()}
+        xs = x.double().requires_grad_()
+        rs, ro = _plain(q, xs, torch.zeros_like(xs), ids, K)
+        assert _rel(out, ro.detach()) <= bar
+        assert _rel(blk.step(x[:24].cuda())[1], ro.detach()[:24]) <= bar
+        dx = blk.backward(ds.cuda(), dd.cuda())
+        torch.autograd.backward([rs, ro], [ds.double(), dd.double()])
+        assert _rel(dx, xs.grad) <= gbar
+        for k, v in blk.gradients.items():
+            assert _rel(v, q[k].grad) <= gbar, k
+        before = {k: v.clone() for k, v in mine.items()}
+        for k, v in blk.gradients.items():                       # a step that changes every weight by about itself
+            scale = mine[k].float().abs().mean() / v.float().abs().mean().clamp_min(1e-30)
+            mine[k].copy_((mine[k].float() - scale * v.float()).to(v.dtype))
+        assert all(not torch.equal(before[k], v) for k, v in mine.items())
+        blk.repack()
+    assert api.moe_get_device_errors() == 0
+
+
+@pytest.mark.parametrize("precision", ["bf16", "mxfp8", "nvfp4"])
+def test_repack_gives_what_a_new_layer_gives(precision):
+    """In the buffers that were there: a captured graph and layers that share them see the new weights."""
+    p = _params(4, 512, 512, seed=31)
+    w = [p[k].cuda() for k in ("w1", "w3", "w2")]
+    L = MoELayer(*w, T=40, K=2, precision=precision)
+    shared = MoELayer(*w, T=40, K=2, precision=precision, packed_weights=L.weights)
+    g = torch.Generator().manual_seed(32)
+    x, lg = torch.randn((40, 512), generator=g).to(torch.bfloat16).cuda(), torch.randn((40, 4), generator=g).cuda()
+    L.forward(x, lg)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.forward(x, lg)
+    at = [t.data_ptr() for t in L.weights if torch.is_tensor(t)]
+    for t, seed in zip(w, (33, 34, 35)):
+        t.copy_((torch.randn(t.shape, generator=torch.Generator().manual_seed(seed)) * 0.06).to(torch.bfloat16))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    L.repack(stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    new = MoELayer(*w, T=40, K=2, precision=precision)
+    for a, b in zip(L.weights, new.weights):
+        assert torch.equal(a, b) if torch.is_tensor(a) else a == b
+    assert at == [t.data_ptr() for t in L.weights if torch.is_tensor(t)]
+    want = new.forward(x, lg).clone()
+    graph.replay()
+    assert torch.equal(L.y, want) and torch.equal(shared.forward(x, lg), want)
+
+
+def test_repack_into_other_weights_is_refused():
+    p = _params(4, 512, 512, seed=41)
+    w = [p[k].cuda() for k in ("w1", "w3", "w2")]
+    packed, bwd = api.moe_prepare_weights(*w), api.moe_prepare_weights_bwd(*w)
+    small = [t[:2].contiguous() for t in w]
+    for bad in (lambda: api.moe_prepare_weights(*w, "mxfp8", out=packed), lambda: api.moe_prepare_weights(*small, out=packed),
+                lambda: api.moe_prepare_weights(*w, out=bwd), lambda: api.moe_prepare_weights_bwd(*w, out=packed),
+                lambda: api.moe_prepare_weights_bwd(*small, out=bwd), lambda: api.moe_prepare_weights_nvfp4(*w, out=packed),
+                lambda: api.moe_prepare_weights(*w, out=packed._replace(w2=packed.w2[:, :, 8:])),
+                lambda: api.moe_prepare_weights(*w, out=packed._replace(w13=packed.w13.cpu())),
+                lambda: api.moe_prepare_weights(*w, out=packed._replace(w13=None))):
+        with pytest.raises(ValueError):
+            bad()
