@@ -965,6 +965,6 @@ def moe_grad_norm(grads, *, norm: Optional[torch.Tensor] = None, workspace: Opti
 
 def moe_grad_clip(grads, max_norm: float, *, eps: float = 1e-6, out=None, norm: Optional[torch.Tensor] = None,
                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """Scale the gradients by min(1, max_norm / (norm + eps)), norm being their global norm: in
-    place, or into the tensors of out. Returns the norm before clipping ([1] fp32, on the device)."""
+    """Scale the gradients by min(1, max_norm / (norm + eps)), norm being their global norm (1 where
+    norm + eps is within max_norm, 0 and inf included): in place, or into the tensors of out. Returns the norm before clipping ([1] fp32, on the device)."""
     return _grad_norm_clip(grads, grads if out is None else out, max_norm, eps, norm, workspace, stream)

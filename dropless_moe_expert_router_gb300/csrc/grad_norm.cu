@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(GN_THREADS) grad_scale_kernel(const __grid_con
     float v = 0.0f;
     for (int j = threadIdx.x; j < n_partial; j += GN_THREADS) v += __ldcg(partial + j);
     const float norm = sqrtf(cta_sum(v, red));
-    float c = max_norm / (norm + eps);
-    if (c >= 1.0f) c = 1.0f;                    // (a NaN stays)
+    // (within the bound nothing is divided: 0 / 0 and inf / inf are no scale. A NaN norm is within no bound, and stays.)
+    const float c = norm + eps <= max_norm ? 1.0f : max_norm / (norm + eps);
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
     for (int i = last; b > begin; i--) {
         const int start = max(begin, g.first[i]);

@@ -575,13 +575,15 @@ moe_status moe_layer_norm_backward(const void *dy, const void *s, int T, int H, 
  * Global gradient norm over many tensors, and clipping by it (the step between
  * the layer's backward pass and an optimiser; the pages do not describe it).
  *   norm = sqrt( sum over the n tensors of sum g^2 )                       (fp32)
- *   c = min(1, max_norm / (norm + eps));   outs[i] = round(grads[i] * c)
+ *   c = 1 if norm + eps <= max_norm, else max_norm / (norm + eps);   outs[i] = round(grads[i] * c)
  * grads, counts, dtypes, outs are host arrays of n entries: device pointers (aligned to
  * their element), element counts (0 is legal, the pointer is then not used), MOE_BF16 or
  * MOE_F32. outs NULL: only the norm. outs[i] may be grads[i] (in place: with c = 1 nothing
  * is written) and has the type of grads[i]. *norm_out (device fp32). A NaN in a gradient
- * makes norm and every output NaN; an infinite norm gives c = 0 (0 * inf is NaN). Squares
- * are summed in fp32 (values above about 1e19 overflow to an infinite norm) in an order that
+ * makes norm and every output NaN; an infinite norm gives c = 0 (0 * inf is NaN), but with
+ * max_norm infinite too c = 1: such a bound only measures. The tensors must not overlap. Squares
+ * are summed in fp32 (values above about 1e19 overflow to an infinite norm, those below
+ * about 1e-19 lose bits and below 1e-23 vanish) in an order that
  * depends on the sizes and the device only. The host never reads the norm. Requires n >= 0,
  * max_norm >= 0, eps >= 0 (not NaN). workspace: moe_grad_norm_workspace_size(n) bytes,
  * 16-byte aligned, not initialised. The host arrays are read during the call only.

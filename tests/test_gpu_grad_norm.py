@@ -141,3 +141,30 @@ def test_refusals():
         api.moe_grad_norm([])
     with pytest.raises(MoeError):
         api.moe_grad_norm(g, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_zero_gradients_and_no_room_at_all_stay_zero(dt):
+    """max_norm = 0, eps = 0 and a norm of 0: nothing to clip, not 0 / 0."""
+    z = [torch.zeros(3000, dtype=dt, device="cuda"), torch.zeros(5, device="cuda")]
+    outs = [torch.full_like(t, 3.0) for t in z]
+    assert api.moe_grad_clip(z, 0.0, eps=0.0, out=outs).item() == 0.0
+    assert not any(o.any() for o in outs)
+    assert api.moe_grad_clip(z, 0.0, eps=0.0).item() == 0.0
+    assert not any(t.any() for t in z)
+
+
+def test_an_infinite_bound_clips_nothing():
+    """max_norm = inf only measures, also where the squares overflow fp32."""
+    for value in (0.5, 1e25):
+        g = [torch.full((2000,), value, device="cuda"), torch.full((70,), -1.0, dtype=BF, device="cuda")]
+        keep = [t.clone() for t in g]
+        outs = [torch.empty_like(t) for t in g]
+        norm = api.moe_grad_clip(g, float("inf"), out=outs).item()
+        assert norm == float("inf") if value > 1 else abs(norm - _norm(keep)) <= NORM_BAR * _norm(keep)
+        assert all(torch.equal(a, b) for a, b in zip(outs, keep))
+        api.moe_grad_clip(g, float("inf"))
+        assert all(torch.equal(a, b) for a, b in zip(g, keep))
+    g = [torch.tensor([1.0, float("nan")], device="cuda")]
+    api.moe_grad_clip(g, float("inf"))
+    assert torch.isnan(g[0]).all()                                       # a NaN still reaches every output
