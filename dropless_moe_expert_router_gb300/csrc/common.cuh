@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "moe_gb300.h"
+#include "per_device.h"
 
 namespace moe {
 
@@ -200,6 +201,17 @@ inline moe_status launch_status() {
 }
 
 inline cudaStream_t as_stream(moe_stream_t s) { return (cudaStream_t)s; }
+
+// Let the kernel have this much dynamic shared memory on the current device (set once per device and
+// larger size: not a stream operation, but captured launches stay free of other API calls).
+template <typename K>
+inline bool allow_smem(K kernel, size_t bytes, PerDevice& done) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    return done.reach(dev, (int)bytes, [&](int n) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, n) == cudaSuccess;
+    });
+}
 
 // Launch with programmatic stream serialization: the kernel may start before the previous
 // kernel on the stream completes, so it must call moe::pdl_wait() before reading anything that

@@ -1279,15 +1279,10 @@ moe_status few_launch(FewArgs a, const PrepArgs& p, const void* x, const uint8_t
     } else {
         ts13 = ts2 = tsx = tsh = tw13;
     }
-    static bool allowed = false;
-    if (!allowed) {
-        if (cudaFuncSetAttribute(few_gemm_kernel<FP8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FEW_SMEM_MAX) !=
-                cudaSuccess ||
-            cudaFuncSetAttribute(few_gemm_kernel<FP8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FEW_SMEM_MAX) !=
-                cudaSuccess)
-            return MOE_ERR_CUDA;
-        allowed = true;
-    }
+    static moe_host::PerDevice up_smem, down_smem;
+    if (!moe_host::allow_smem(few_gemm_kernel<FP8, false>, FEW_SMEM_MAX, up_smem) ||
+        !moe_host::allow_smem(few_gemm_kernel<FP8, true>, FEW_SMEM_MAX, down_smem))
+        return MOE_ERR_CUDA;
     const int V = p.logits ? (p.E + PREP_THREADS - 1) / PREP_THREADS : 1;
     const int ctas = a.T + (FP8 ? a.T * ((a.H + PREP_QUANT - 1) / PREP_QUANT) : 0);
     if (V <= 1) few_prep_kernel<1><<<ctas, PREP_THREADS, 0, s>>>(p);

@@ -844,14 +844,8 @@ moe_status launch_gemm(const void* A, uint64_t a_rows, const void* B, uint64_t b
     }
     const size_t smem = smem_bytes_for<FP8, PAIR>(a.E);
     auto kern = grouped_gemm_kernel<MODE, FP8, PAIR, NV4>;
-    // raise the kernel's dynamic shared-memory limit once per process and size (not a stream operation,
-    // but keeping it out of repeated calls keeps captured launches free of other API calls)
-    static int configured_smem = 0;
-    if ((int)smem > configured_smem) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-            return MOE_ERR_CUDA;
-        configured_smem = (int)smem;
-    }
+    static moe_host::PerDevice allowed;
+    if (!moe_host::allow_smem(kern, smem, allowed)) return MOE_ERR_CUDA;
     const int sms = device_sms();
     if (!PAIR) {
         kern<<<sms, C::THREADS, smem, s>>>(tmA, tmB, tmSA, tmSB, a);

@@ -1069,12 +1069,6 @@ int ln_ring_grid(int rows, int group, int period, long long most) {
     return (int)(of_one < most ? of_one : most) * period;
 }
 
-template <typename K>
-bool ln_allow_smem(K kernel, bool& done) {
-    if (!done) done = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LN_SMEM) == cudaSuccess;
-    return done;
-}
-
 template <typename T, typename W>
 moe_status ln_forward(const void* x, const void* residual, int rows, int H, const void* w, const void* b, float eps,
                       void* sum, void* y, float* mean, float* rstd, cudaStream_t s) {
@@ -1087,9 +1081,9 @@ moe_status ln_forward(const void* x, const void* residual, int rows, int H, cons
         const int grid = ln_ring_grid(rows, r.rows, l.period, (long long)ln_sms() * r.ctas);
 #define MOE_LN_FR(nv, R, odd)                                                                                         \
     {                                                                                                                 \
-        static bool allowed = false;                                                                                  \
+        static moe_host::PerDevice allowed;                                                                           \
         auto kern = ln_forward_ring_kernel<T, W, VEC, nv, R, odd>;                                                    \
-        if (!ln_allow_smem(kern, allowed)) return MOE_ERR_CUDA;                                                       \
+        if (!moe_host::allow_smem(kern, LN_SMEM, allowed)) return MOE_ERR_CUDA;                                       \
         kern<<<grid, l.threads, r.smem, s>>>((const T*)x, (const T*)residual, rows, H, (const W*)w, (const W*)b, eps, \
                                              (T*)sum, (T*)y, mean, rstd, r.stages, l.period, l.row_bytes);            \
     }
@@ -1161,9 +1155,9 @@ moe_status ln_backward(const void* dy, const void* sv, int rows, int H, const vo
         n_part = ln_ring_grid(rows, r.rows, l.period, (long long)sms * r.ctas);
 #define MOE_LN_BR(nv, R, odd)                                                                                       \
     {                                                                                                               \
-        static bool allowed = false;                                                                                \
+        static moe_host::PerDevice allowed;                                                                         \
         auto kern = ln_backward_ring_kernel<T, W, VEC, nv, R, odd>;                                                 \
-        if (!ln_allow_smem(kern, allowed)) return MOE_ERR_CUDA;                                                     \
+        if (!moe_host::allow_smem(kern, LN_SMEM, allowed)) return MOE_ERR_CUDA;                                     \
         kern<<<n_part, l.threads + 32, r.smem, s>>>((const T*)dy, (const T*)sv, rows, H, (const W*)w, mean, rstd,        \
                                                (const T*)add, (T*)dx, sums ? part : nullptr, r.stages, l.period,    \
                                                l.row_bytes);                                                        \

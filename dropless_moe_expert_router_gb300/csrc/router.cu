@@ -738,17 +738,19 @@ template <int NV4, int G, bool FULL>
 cudaError_t launch_filter(const float* logits, int T, int E, int K, void* ids, bool i16, float* probs,
                           bool renorm, cudaStream_t s) {
     constexpr size_t smem = filter_smem_bytes<NV4>();
-    static int resident = 0;                      // one wave of CTAs: SMs x resident CTAs per SM
-    if (!resident) {
-        int dev = 0, sms = 0, per = 0;
-        cudaGetDevice(&dev);
+    static moe_host::PerDevice waves;             // CTAs in one wave: SMs x resident CTAs per SM
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const int resident = e != cudaSuccess ? 0 : waves.get(dev, [&] {
+        int sms = 0, per = 0;
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        cudaError_t e = cudaFuncSetAttribute(route_filter_kernel<NV4, G, FULL>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(route_filter_kernel<NV4, G, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return 0;
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, route_filter_kernel<NV4, G, FULL>, FW * 32, smem);
-        resident = sms * (per > 0 ? per : 1);
-    }
+        return sms * (per > 0 ? per : 1);
+    });
+    if (e != cudaSuccess) return e;
+    if (resident == 0) return cudaErrorUnknown;
     const long long need = ((long long)T + FW - 1) / FW;
     const int blocks = (int)(need < resident ? need : resident);
     route_filter_kernel<NV4, G, FULL><<<blocks, FW * 32, smem, s>>>(logits, T, E, K, ids, i16, probs, renorm);
