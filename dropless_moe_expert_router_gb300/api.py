@@ -46,8 +46,16 @@ def _stream(stream: Optional[torch.cuda.Stream]):
 
 
 def _raw_stream(stream: Optional[torch.cuda.Stream], t: torch.Tensor) -> int:
-    """The stream's handle: the given one's, or that of the current stream of t's device."""
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
+    """The stream's handle: the given one's, or that of the current stream of t's device, which has to be the
+    current device: the launch is its own."""
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device (torch.cuda.device)")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the tensors are on cuda:{dev}, the stream on cuda:{stream.device_index}")
+    return stream.cuda_stream
 
 
 def _empty(shape, dtype: torch.dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
@@ -79,9 +87,17 @@ def _want(t: torch.Tensor, name: str, dtype=None, ndim=None):
         raise ValueError(f"{name} must have {ndim} dims")
 
 
-def _scratch(t: torch.Tensor) -> None:
+def _scratch(t: torch.Tensor, dev: int) -> None:
     if not (t.is_cuda and t.dtype is torch.uint8 and t.is_contiguous()):
         raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
+    _on(dev, workspace=t)
+
+
+def _on(dev: int, **tensors) -> None:
+    """The tensors (None: not there) are on this CUDA device."""
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on cuda:{dev}, the other tensors' device")
 
 
 def _id_code(dtype: torch.dtype) -> int:
@@ -437,8 +453,9 @@ class PackedWeights(NamedTuple):
     w2_scales: Optional[torch.Tensor]   # [E, H, F/32] uint8 (MXFP8)
 
 
-def _want_packed(out, kind, shapes) -> None:
-    """out is a kind of packed weights with these scalars first and these shapes (None: no tensor) after them."""
+def _want_packed(out, kind, shapes, dev: int) -> None:
+    """out is a kind of packed weights on this device, with these scalars first and these shapes (None: no
+    tensor) after them."""
     n = len(out) - len(shapes[1])
     if type(out) is not kind or tuple(out[:n]) != shapes[0]:
         raise ValueError(f"out must be the {kind.__name__} of weights of this precision and size")
@@ -447,7 +464,7 @@ def _want_packed(out, kind, shapes) -> None:
             continue
         if t is None:
             raise ValueError(f"out has no {name}")
-        _like(t, name, want[0], want[1])
+        _like(t, name, want[0], want[1], dev)
 
 
 def moe_prepare_weights(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, precision: str = "bf16",
@@ -470,7 +487,7 @@ def moe_prepare_weights(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, pr
         u8 = torch.uint8
         _want_packed(out, PackedWeights, ((precision, E, H, F), (
             (pdt, (E, 2 * F, H)), (u8, (E, 2 * F, H // 32)) if fp8 else None,
-            (pdt, (E, H, F)), (u8, (E, H, F // 32)) if fp8 else None)))
+            (pdt, (E, H, F)), (u8, (E, H, F // 32)) if fp8 else None)), w1.get_device())
     st = _lib.load().moe_prepare_weights(_ptr(w1), _ptr(w3), _ptr(w2), E, H, F, _dt_code(precision),
                                          _ptr(out.w13), _ptr(out.w13_scales), _ptr(out.w2), _ptr(out.w2_scales),
                                          _stream(stream))
@@ -593,7 +610,7 @@ def moe_prepare_weights_nvfp4(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tens
         u8, f32 = torch.uint8, torch.float32
         _want_packed(out, Nvfp4Weights, ((E, H, F), (
             (u8, (E, 2 * F, H // 2)), (u8, (E, 2 * F, H // 16)), (f32, (1,)),
-            (u8, (E, H, F // 2)), (u8, (E, H, F // 16)), (f32, (1,)))))
+            (u8, (E, H, F // 2)), (u8, (E, H, F // 16)), (f32, (1,)))), w1.get_device())
     a13 = moe_amax_bf16(pw.w13, amax=o.w13_amax, stream=stream)
     q13, s13 = moe_quant_nvfp4(pw.w13, a13, q=o.w13, scales=o.w13_scales, stream=stream)
     a2 = moe_amax_bf16(pw.w2, amax=o.w2_amax, stream=stream)
@@ -662,7 +679,7 @@ def moe_prepare_weights_bwd(w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor
         u8 = torch.uint8
         _want_packed(out, BwdWeights, ((precision, E, H, F), (
             (pdt, (E, F, H)), (u8, (E, F, H // 32)) if fp8 else None,
-            (pdt, (E, H, 2 * F)), (u8, (E, H, 2 * F // 32)) if fp8 else None)))
+            (pdt, (E, H, 2 * F)), (u8, (E, H, 2 * F // 32)) if fp8 else None)), w1.get_device())
     st = _lib.load().moe_prepare_weights_bwd(_ptr(w1), _ptr(w3), _ptr(w2), E, H, F, _dt_code(precision),
                                              _ptr(out.w2b), _ptr(out.w2b_scales), _ptr(out.w13t),
                                              _ptr(out.w13t_scales), _stream(stream))
@@ -772,28 +789,30 @@ def moe_layer_few_tokens(x: torch.Tensor, logits: Optional[torch.Tensor], w: Pac
     ids [T, K], probs [T, K]). With logits None, ids and probs are the caller's routes instead."""
     _want(x, "x", torch.bfloat16, 2)
     T, H = x.shape
+    dev = x.get_device()
     if H != w.H:
         raise ValueError(f"x must have {w.H} columns")
     if logits is not None:
-        _like(logits, "logits", torch.float32, (T, w.E))
+        _like(logits, "logits", torch.float32, (T, w.E), dev)
     elif ids is None or probs is None:
         raise ValueError("without logits, ids and probs are inputs")
     if ids is None:
         ids = _empty((T, K), id_dtype, x.device, stream)
     else:
-        _like(ids, "ids", ids.dtype, (T, K))
+        _like(ids, "ids", ids.dtype, (T, K), dev)
     if probs is None:
         probs = _empty((T, K), torch.float32, x.device, stream)
     else:
-        _like(probs, "probs", torch.float32, (T, K))
+        _like(probs, "probs", torch.float32, (T, K), dev)
     if y is None:
         y = _empty(x.shape, x.dtype, x.device, stream)
     else:
-        _like(y, "y", torch.bfloat16, (T, H))
+        _like(y, "y", torch.bfloat16, (T, H), dev)
     if workspace is None:
         workspace = moe_layer_few_tokens_workspace(w, T, K, stream)
     else:
-        _scratch(workspace)
+        _scratch(workspace, dev)
+    _on(dev, w13=w.w13, w13_scales=w.w13_scales, w2=w.w2, w2_scales=w.w2_scales)
     st = _lib.load().moe_layer_few_tokens(
         x.data_ptr(), T, H, _at(logits), K, w.E, w.F, w.w13.data_ptr(), _at(w.w13_scales), w.w2.data_ptr(),
         _at(w.w2_scales), _dt_code(w.precision), ids.data_ptr(), _id_code(ids.dtype), probs.data_ptr(), y.data_ptr(),
@@ -813,11 +832,12 @@ def _float_code(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _like(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape) -> None:
-    """t, where given, is a contiguous CUDA tensor of this type and shape."""
-    if t is None or (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+def _like(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, dev: int) -> None:
+    """t, where given, is a contiguous tensor of this type and shape on this CUDA device."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
         return
     _want(t, name, dtype, None)
+    _on(dev, **{name: t})
     raise ValueError(f"{name} must be {list(shape)}")
 
 
@@ -836,28 +856,29 @@ def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     _want(x, "x", None, 2)
     shape, dtype = x.shape, x.dtype
     T, H = shape
+    dev = x.get_device()
     code, wcode = _float_code(x, "x"), _float_code(weight, "weight")
-    _like(weight, "weight", weight.dtype, (H,))
-    _like(bias, "bias", weight.dtype, (H,))
-    _like(residual, "residual", dtype, shape)
+    _like(weight, "weight", weight.dtype, (H,), dev)
+    _like(bias, "bias", weight.dtype, (H,), dev)
+    _like(residual, "residual", dtype, shape, dev)
     if y is None:
         y = _empty(x.shape, x.dtype, x.device, stream)
     else:
-        _like(y, "y", dtype, shape)
+        _like(y, "y", dtype, shape, dev)
     if sum is not None:
         if residual is None:
             raise ValueError("sum goes with residual")
-        _like(sum, "sum", dtype, shape)
+        _like(sum, "sum", dtype, shape, dev)
     elif residual is not None:
         sum = _empty(x.shape, x.dtype, x.device, stream)
     if mean is None:
         mean = _empty(T, torch.float32, x.device, stream)
     else:
-        _like(mean, "mean", torch.float32, (T,))
+        _like(mean, "mean", torch.float32, (T,), dev)
     if rstd is None:
         rstd = _empty(T, torch.float32, x.device, stream)
     else:
-        _like(rstd, "rstd", torch.float32, (T,))
+        _like(rstd, "rstd", torch.float32, (T,), dev)
     st = _lib.load().moe_layer_norm(x.data_ptr(), _at(residual), T, H, code, weight.data_ptr(), _at(bias), wcode, eps,
                                     _at(sum), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, x))
     _check("moe_layer_norm", st)
@@ -878,30 +899,31 @@ def moe_layer_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Ten
     _want(s, "s", None, 2)
     shape, dtype, wdtype = s.shape, s.dtype, weight.dtype
     T, H = shape
+    dev = s.get_device()
     code, wcode = _float_code(s, "s"), _float_code(weight, "weight")
     if dy is None or mean is None or rstd is None:
         raise ValueError("dy, mean and rstd must be given")
-    _like(weight, "weight", wdtype, (H,))
-    _like(dy, "dy", dtype, shape)
-    _like(mean, "mean", torch.float32, (T,))
-    _like(rstd, "rstd", torch.float32, (T,))
-    _like(dx_add, "dx_add", dtype, shape)
+    _like(weight, "weight", wdtype, (H,), dev)
+    _like(dy, "dy", dtype, shape, dev)
+    _like(mean, "mean", torch.float32, (T,), dev)
+    _like(rstd, "rstd", torch.float32, (T,), dev)
+    _like(dx_add, "dx_add", dtype, shape, dev)
     if dx is None:
         dx = _empty(s.shape, s.dtype, s.device, stream)
     else:
-        _like(dx, "dx", dtype, shape)
+        _like(dx, "dx", dtype, shape, dev)
     if dweight is None:
         dweight = _empty(weight.shape, weight.dtype, weight.device, stream)
     else:
-        _like(dweight, "dweight", wdtype, (H,))
+        _like(dweight, "dweight", wdtype, (H,), dev)
     if dbias is None:
         dbias = _empty(weight.shape, weight.dtype, weight.device, stream)
     else:
-        _like(dbias, "dbias", wdtype, (H,))
+        _like(dbias, "dbias", wdtype, (H,), dev)
     if workspace is None:
         workspace = _empty(moe_layer_norm_backward_workspace_size(T, H), torch.uint8, s.device, stream)
     else:
-        _scratch(workspace)
+        _scratch(workspace, dev)
     st = _lib.load().moe_layer_norm_backward(dy.data_ptr(), s.data_ptr(), T, H, code, weight.data_ptr(), wcode,
                                              mean.data_ptr(), rstd.data_ptr(), _at(dx_add), dx.data_ptr(),
                                              dweight.data_ptr(), dbias.data_ptr(), workspace.data_ptr(),
@@ -914,8 +936,12 @@ def moe_layer_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Ten
 def _grad_norm_clip(grads, outs, max_norm, eps, norm, workspace, stream):
     # (the lists can be long: each check is one pass over them)
     n = len(grads)
-    if not all([t.is_cuda for t in grads]):
+    devices = set(map(torch.Tensor.get_device, grads))
+    if -1 in devices:
         raise ValueError("gradients must be CUDA tensors")
+    dev = norm.get_device() if norm is not None else grads[0].get_device() if n else -1
+    if devices and devices != {dev}:
+        raise ValueError("gradients and norm must be on one device")
     if not all(map(torch.Tensor.is_contiguous, grads)):
         raise ValueError("gradients must be contiguous")
     dtypes = [t.dtype for t in grads]
@@ -932,8 +958,8 @@ def _grad_norm_clip(grads, outs, max_norm, eps, norm, workspace, stream):
             raise ValueError("out must have one tensor per gradient")
         if list(map(torch.Tensor.numel, outs)) != counts or [t.dtype for t in outs] != dtypes:
             raise ValueError("outputs must have the gradients' sizes and types")
-        if not all([t.is_cuda for t in outs]) or not all(map(torch.Tensor.is_contiguous, outs)):
-            raise ValueError("outputs must be contiguous CUDA tensors")
+        if set(map(torch.Tensor.get_device, outs)) - {dev} or not all(map(torch.Tensor.is_contiguous, outs)):
+            raise ValueError("outputs must be contiguous CUDA tensors on the gradients' device")
         optrs = array("q", map(torch.Tensor.data_ptr, outs))
         out_at = optrs.buffer_info()[0]
     if norm is None:
@@ -948,7 +974,7 @@ def _grad_norm_clip(grads, outs, max_norm, eps, norm, workspace, stream):
     if workspace is None:
         workspace = _empty(L.moe_grad_norm_workspace_size(n), torch.uint8, norm.device, stream)
     else:
-        _scratch(workspace)
+        _scratch(workspace, dev)
     counts, codes = array("q", counts), array("i", codes)
     st = L.moe_grad_norm_clip(ptrs.buffer_info()[0], counts.buffer_info()[0], codes.buffer_info()[0], out_at, n,
                               max_norm, eps, norm.data_ptr(), workspace.data_ptr(), workspace.numel(),
