@@ -32,6 +32,7 @@ class MoEBlock:
         self.router = router
         self.norm_weight, self.norm_bias, self.eps = norm_weight, norm_bias, eps
         self._saved = None
+        self.gradients = None       # of every parameter, by name, after a backward
 
     def _norm(self, x, delta):
         o = api.moe_layer_norm(x, self.norm_weight, self.norm_bias, self.eps, residual=delta)
@@ -46,7 +47,8 @@ class MoEBlock:
         return o.sum, out
 
     def step(self, x: torch.Tensor, delta: Optional[torch.Tensor] = None):
-        """The block for the few tokens of a decoding step: x (and delta) [t, H], t <= 64."""
+        """The block for the few tokens of a decoding step: x (and delta) [t, H], t <= 64. Steps share a
+        workspace (MoELayer.forward_few) and must not overlap on the GPU."""
         o, logits = self._norm(x, delta)
         return o.sum, self.layer.forward_few(o.y, logits)
 
@@ -72,4 +74,6 @@ class MoEBlock:
     def clip_gradients(self, max_norm: float) -> torch.Tensor:
         """Scale the gradients in place to a global norm of at most max_norm; the norm they had ([1] fp32
         on the device)."""
+        if self.gradients is None:
+            raise ValueError("clip_gradients wants a backward first")
         return api.moe_grad_clip(list(self.gradients.values()), max_norm)

@@ -208,3 +208,13 @@ def test_repack_into_other_weights_is_refused():
                 lambda: api.moe_prepare_weights(*w, out=packed._replace(w13=None))):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_clip_before_backward_is_refused():
+    p = _params(4, 256, 128, seed=5)
+    blk = _block(p, 8, 2, training=True)
+    with pytest.raises(ValueError):
+        blk.clip_gradients(1.0)
+    blk.forward(torch.zeros((8, 256), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        blk.clip_gradients(1.0)
