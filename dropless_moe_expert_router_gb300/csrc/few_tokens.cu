@@ -4,14 +4,16 @@
 // For every valid route (t, k) with expert e = ids[t,k]:
 //   h = silu(x[t] W1[e]) * (x[t] W3[e]);   y[t] = bf16( sum_k p[t,k] (h W2[e]) )
 // Every weight of the chosen experts is read once and used for the few tokens that chose
-// them, so the time is the weights' bytes over the memory's rate plus a fixed part: 12 to 15 us from the
-// routing through two dependent kernels' starts and joins. Measured on a GPU that copies 6.78 TB/s (whole
-// layer, SM clock 2070 MHz; the share is that of the weights' bytes at that rate):
-//   1 token, 8 experts, top-2, 4096 x 14336, bf16         116-119 us   0.88-0.90   (0.70 GB)
-//   32 tokens of the same (all experts)                   413-425 us   0.98-1.0    (2.8 GB)
-//   8 tokens, 32 experts, top-4, 7168 x 2048, MXFP8       156-166 us   0.85-0.90   (0.95 GB)
-//   5 tokens, 2,304 experts, top-36, 512 x 512, bf16        64-66 us   0.61-0.63   (0.27 GB)
-//   1 token, 8 experts, top-2, 256 x 512, bf16                 15 us   the fixed part (1.6 MB)
+// them, so the time is the weights' bytes over the memory's rate plus a part that does not shrink with them: 10 to
+// 15 us from the routing through two dependent kernels' starts and joins with few experts, about 23 us with 2,304
+// (routing takes 9 us of its own there, against 4 to 5; how the rest divides between the plans, the kernels' change
+// and the joins is not measured). Measured on a GPU that copies 6.78 TB/s (whole layer, SM clock 2070 MHz; the
+// share is that of the weights' bytes at that rate):
+//   1 token, 8 experts, top-2, 4096 x 14336, bf16         114-120 us   0.87-0.91   (0.70 GB)
+//   32 tokens of the same (all experts)                   408-425 us   0.98-1.0    (2.8 GB)
+//   8 tokens, 32 experts, top-4, 7168 x 2048, MXFP8       151-168 us   0.84-0.93   (0.95 GB)
+//   5 tokens, 2,304 experts, top-36, 512 x 512, bf16        62-66 us   0.61-0.65   (0.27 GB)
+//   1 token, 8 experts, top-2, 256 x 512, bf16              14-15 us   starts and joins (1.6 MB)
 #include "common.cuh"
 #include "sm100_ptx.cuh"
 #include "tensor_map.cuh"
@@ -28,8 +30,8 @@ constexpr int FEW_EMAX = 8192;       // experts
 
 // ---------------------------------------------------------------------------
 // First kernel. CTA t < T: token t's selection (unless the caller gave ids and probs). MXFP8: the CTAs
-// after those quantise x row-wise 1x32, PREP_QUANT elements of a row each. 4 to 5 us, all of it latency:
-// hence counting and ranking, a fixed number of steps, in place of K rounds of a maximum each.
+// after those quantise x row-wise 1x32, PREP_QUANT elements of a row each. 4 to 5 us (9 with 2,304 experts), all
+// of it latency: hence counting and ranking, a fixed number of steps, in place of K rounds of a maximum each.
 //
 // Selection: a thread holds V logits as order-preserving keys (expert i * 256 + thread). Up to 256
 // experts, each logit's rank is counted directly against the row. Above, the K-th largest of the

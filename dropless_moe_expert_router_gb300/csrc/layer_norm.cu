@@ -636,7 +636,7 @@ __device__ __forceinline__ void cta_sums(float (&v)[2 * R], float2* red, int thr
 // Backward. A warp of its own fills the ring, a stage per row, as soon as the computing warps have let go of
 // the row that was there; those take R rows at a time. dweight and dbias add up in the threads' registers
 // over the CTA's rows and leave as one partial sum per CTA: part [gridDim.x][2][H]. 8192 x 7168 bf16 with
-// dx_add, 470 MB: 86-88 us with the columns' kernel, 5.4 TB/s; a copy of as many bytes takes 77 us. (Refilled by
+// dx_add, 470 MB: 86-89 us with the columns' kernel, 5.4 TB/s; a copy of as many bytes takes 77 us. (Refilled by
 // thread 0 between the barriers, as in the forward, it took 98 us.) xh is (s - mean) rstd in both passes: one fma
 // s rstd - mean rstd would save 1 us of that and lose |mean| rstd units of xh's last place.
 template <typename T, typename W, int VEC, int NV, int R, bool ODD>
@@ -1049,7 +1049,8 @@ LnRingShape ln_forward_ring(size_t row_bytes, const LnShape& l) {
 }
 
 // Backward: a stage is a row; two rows a group where three fit (long fp32 rows go singly, and rows off the
-// boundary of more than 4 KB, whose two would spill: 3000 x 8191 61 us, singly 56.6; 777 x 1021 fp32 8.7 and 9.8).
+// boundary of more than 4 KB: 3000 x 8191 61 us by twos, singly 56.6, but 777 x 1021 fp32 8.7 and 9.8. Off the
+// boundary the bf16 instance spills 44 to 52 bytes with two rows, 20 with one).
 LnRingShape ln_backward_ring(size_t row_bytes, const LnShape& l) {
     LnRingShape r;
     const int most = l.threads > 256 ? 1 : 512 / l.threads;     // (128 registers a thread)
