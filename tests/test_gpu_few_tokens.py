@@ -323,3 +323,39 @@ def test_few_tokens_renormalised_probs_repeat_bit_for_bit(T, E, K):
     for _ in range(200):
         y2, ids2, probs2 = api.moe_layer_few_tokens(x, lg, w, K, renorm=True, workspace=ws)
         assert torch.equal(ids, ids2) and torch.equal(probs, probs2) and torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("T,K,E,precision", [(64, 64, 8192, "bf16"), (32, 128, 8192, "bf16"), (63, 65, 4097, "bf16"),
+                                             (64, 64, 2304, "mxfp8"), (32, 128, 2304, "mxfp8"), (64, 32, 8192, "mxfp8")])
+def test_few_tokens_largest_plans(T, K, E, precision):
+    """As many routes and experts as are taken. Expert e's W3 and W2 are one expert's times powers of two,
+    by which h and its products scale exactly, so a token's output is that expert's output times
+    sum p 2^(a(e) + b(e)). A step of h is the same for all of a token's experts: the bars join it from the
+    largest term of the sum as in the test of shared tiles."""
+    fp8 = precision == "mxfp8"
+    H = F = 512 if fp8 else 128
+    _, one = _weights(1, H, F, precision, seed=K)
+    e = torch.arange(E, device="cuda")
+    a, b = e % 3 - 1, e % 5 - 2
+    linear = torch.arange(2 * F, device="cuda") // 128 % 2 == 1
+    by = torch.where(linear[None], a[:, None], 0)
+    w13, w2 = one.w13.expand(E, -1, -1).contiguous(), one.w2.expand(E, -1, -1).contiguous()
+    s13 = s2 = None
+    if fp8:
+        s13 = (one.w13_scales.int() + by[..., None]).to(torch.uint8)
+        s2 = (one.w2_scales.int() + b[:, None, None]).to(torch.uint8)
+    else:
+        w13.mul_(torch.exp2(by.float()).to(torch.bfloat16)[..., None])
+        w2.mul_(torch.exp2(b.float()).to(torch.bfloat16)[:, None, None])
+    w = one._replace(E=E, w13=w13, w13_scales=s13, w2=w2, w2_scales=s2)
+    x, lg = _inputs(T, H, E, seed=E + K)
+    y, ids, probs = api.moe_layer_few_tokens(x, lg, w, K, renorm=True)
+    assert torch.equal(ids.long(), torch.sort(lg, dim=1, descending=True, stable=True).indices[:, :K])
+    zeros, ones = np.zeros((T, 1), dtype=np.int64), np.ones((T, 1))
+    d, A = _reference(x, zeros, ones, one)
+    _, M = _reference(x, zeros, ones, one, largest=True)
+    c = (probs.double() * torch.exp2((a + b).double())[ids.long()]).sum(1, keepdim=True).cpu().numpy()
+    bar = c * (2.0 ** -8 * np.abs(d) + 2.0 ** (-10 if fp8 else -12) * A + 2.0 ** (-2 if fp8 else -6) * M)
+    assert (np.abs(y.double().cpu().numpy() - c * d) <= bar).all()
+    assert torch.equal(y, api.moe_layer_few_tokens(x, lg, w, K, renorm=True)[0])
+    assert api.moe_get_device_errors() == 0
