@@ -62,14 +62,20 @@ def _empty(shape, dtype: torch.dtype, device, stream: Optional[torch.cuda.Stream
     """Uninitialised memory for a call on `stream` (None: the current one). It comes from that stream's
     memory, which follows the order of the kernels that use it: whoever gets it next, or had it before, runs
     on the same stream. What the caller enqueues on the current stream is waited for too before it goes back."""
-    if stream is not None:
-        current = torch.cuda.current_stream(device)
-        if stream != current:
-            with torch.cuda.stream(stream):
-                t = torch.empty(shape, dtype=dtype, device=device)
-            t.record_stream(current)
-            return t
-    return torch.empty(shape, dtype=dtype, device=device)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream == current:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
+def _empty_like(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """_empty of t's shape, type and device."""
+    return torch.empty_like(t) if stream is None else _empty(t.shape, t.dtype, t.device, stream)
 
 
 def _at(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -88,16 +94,14 @@ def _want(t: torch.Tensor, name: str, dtype=None, ndim=None):
 
 
 def _scratch(t: torch.Tensor, dev: int) -> None:
-    if not (t.is_cuda and t.dtype is torch.uint8 and t.is_contiguous()):
-        raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
-    _on(dev, workspace=t)
+    if not (t.get_device() == dev and t.dtype is torch.uint8 and t.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{dev}, the other tensors' device")
 
 
-def _on(dev: int, **tensors) -> None:
-    """The tensors (None: not there) are on this CUDA device."""
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be on cuda:{dev}, the other tensors' device")
+def _on(dev: int, t: Optional[torch.Tensor], name: str) -> None:
+    """t, where given, is on this CUDA device."""
+    if t is not None and t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, the other tensors' device")
 
 
 def _id_code(dtype: torch.dtype) -> int:
@@ -351,7 +355,7 @@ def moe_unpermute_combine_backward(dy: torch.Tensor, y_perm: torch.Tensor, row_m
     T, K = row_map.shape
     H = y_perm.shape[1]
     if dy_perm is None:
-        dy_perm = _empty(y_perm.shape, y_perm.dtype, y_perm.device, stream)    # rows no route maps to are not written
+        dy_perm = _empty_like(y_perm, stream)    # rows no route maps to are not written
     if dprobs is None:
         dprobs = _empty((T, K), torch.float32, dy.device, stream)
     _want(dy_perm, "dy_perm", torch.bfloat16, 2)
@@ -805,17 +809,20 @@ def moe_layer_few_tokens(x: torch.Tensor, logits: Optional[torch.Tensor], w: Pac
     else:
         _like(probs, "probs", torch.float32, (T, K), dev)
     if y is None:
-        y = _empty(x.shape, x.dtype, x.device, stream)
+        y = _empty_like(x, stream)
     else:
         _like(y, "y", torch.bfloat16, (T, H), dev)
     if workspace is None:
         workspace = moe_layer_few_tokens_workspace(w, T, K, stream)
     else:
         _scratch(workspace, dev)
-    _on(dev, w13=w.w13, w13_scales=w.w13_scales, w2=w.w2, w2_scales=w.w2_scales)
+    w13, s13, w2, s2 = w.w13, w.w13_scales, w.w2, w.w2_scales
+    if w13.get_device() != dev or w2.get_device() != dev or not (
+            s13 is None or s13.get_device() == dev) or not (s2 is None or s2.get_device() == dev):
+        raise ValueError(f"the weights must be on cuda:{dev}, x's device")
     st = _lib.load().moe_layer_few_tokens(
-        x.data_ptr(), T, H, _at(logits), K, w.E, w.F, w.w13.data_ptr(), _at(w.w13_scales), w.w2.data_ptr(),
-        _at(w.w2_scales), _dt_code(w.precision), ids.data_ptr(), _id_code(ids.dtype), probs.data_ptr(), y.data_ptr(),
+        x.data_ptr(), T, H, _at(logits), K, w.E, w.F, w13.data_ptr(), _at(s13), w2.data_ptr(), _at(s2),
+        _dt_code(w.precision), ids.data_ptr(), _id_code(ids.dtype), probs.data_ptr(), y.data_ptr(),
         MOE_ROUTE_RENORM if renorm else 0, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, x))
     _check("moe_layer_few_tokens", st)
     return y, ids, probs
@@ -837,7 +844,7 @@ def _like(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, dev: 
     if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
         return
     _want(t, name, dtype, None)
-    _on(dev, **{name: t})
+    _on(dev, t, name)
     raise ValueError(f"{name} must be {list(shape)}")
 
 
@@ -862,7 +869,7 @@ def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     _like(bias, "bias", weight.dtype, (H,), dev)
     _like(residual, "residual", dtype, shape, dev)
     if y is None:
-        y = _empty(x.shape, x.dtype, x.device, stream)
+        y = _empty_like(x, stream)
     else:
         _like(y, "y", dtype, shape, dev)
     if sum is not None:
@@ -870,7 +877,7 @@ def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
             raise ValueError("sum goes with residual")
         _like(sum, "sum", dtype, shape, dev)
     elif residual is not None:
-        sum = _empty(x.shape, x.dtype, x.device, stream)
+        sum = _empty_like(x, stream)
     if mean is None:
         mean = _empty(T, torch.float32, x.device, stream)
     else:
@@ -909,15 +916,15 @@ def moe_layer_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Ten
     _like(rstd, "rstd", torch.float32, (T,), dev)
     _like(dx_add, "dx_add", dtype, shape, dev)
     if dx is None:
-        dx = _empty(s.shape, s.dtype, s.device, stream)
+        dx = _empty_like(s, stream)
     else:
         _like(dx, "dx", dtype, shape, dev)
     if dweight is None:
-        dweight = _empty(weight.shape, weight.dtype, weight.device, stream)
+        dweight = _empty_like(weight, stream)
     else:
         _like(dweight, "dweight", wdtype, (H,), dev)
     if dbias is None:
-        dbias = _empty(weight.shape, weight.dtype, weight.device, stream)
+        dbias = _empty_like(weight, stream)
     else:
         _like(dbias, "dbias", wdtype, (H,), dev)
     if workspace is None:

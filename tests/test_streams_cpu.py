@@ -45,7 +45,7 @@ def test_every_call_with_a_stream_allocates_there():
     tree = ast.parse(inspect.getsource(api))
     seen = 0
     for f in tree.body:
-        if not isinstance(f, ast.FunctionDef) or f.name == "_empty":
+        if not isinstance(f, ast.FunctionDef) or f.name in ("_empty", "_empty_like"):
             continue
         takes = "stream" in [a.arg for a in f.args.args + f.args.kwonlyargs]
         for c in ast.walk(f):
@@ -53,7 +53,7 @@ def test_every_call_with_a_stream_allocates_there():
                 continue
             name = ast.unparse(c.func)
             assert not (takes and name.startswith("torch.") and name.split(".")[-1].startswith(("empty", "zeros", "full"))), f.name
-            if name in ("_empty", "permute_buffers", "moe_layer_few_tokens_workspace"):
+            if name in ("_empty", "_empty_like", "permute_buffers", "moe_layer_few_tokens_workspace"):
                 seen += 1
                 given = [ast.unparse(a) for a in c.args[-1:]] + [ast.unparse(k.value) for k in c.keywords if k.arg == "stream"]
                 assert "stream" in given, f.name
