@@ -61,6 +61,16 @@ SIGNATURES = {
     "moe_layer_norm_backward": (I, [P, P, I, I, I, P, I, P, P, P, P, P, P, P, SZ, P]),
     "moe_grad_norm_workspace_size": (SZ, [I]),
     "moe_grad_norm_clip": (I, [P, P, P, P, I, FL, FL, P, P, SZ, P]),
+    "moe_cache_append": (I, [P, P, LL, LL, I, P, P, P, I, I, I, I, I, I, I, P, P, P, P, P]),
+    "moe_cache_gather": (I, [P, P, I, P, P, P, I, I, I, I, I, I, I, P, P, P, P, P]),
+    "moe_paged_attention_workspace_size": (SZ, [I, I, I, I]),
+    "moe_paged_attention": (I, [P, LL, I, I, P, P, P, P, I, I, I, I, I, P, I, P, FL, I, P, P, P, SZ, P]),
+    "moe_cache_pages_workspace_size": (SZ, [I, I]),
+    "moe_cache_fork": (I, [P, P, I, I, P, I, I, I, I, P, P, P, P, P, P, P, SZ, P]),
+    "moe_cache_compact": (I, [P, I, I, I, P, P, P, P, P, SZ, P]),
+    "moe_cache_copy_pages": (I, [P, P, I, P, P, I, I, P]),
+    "moe_beam_select_workspace_size": (SZ, [I, I, I, I]),
+    "moe_beam_select": (I, [P, I, P, P, I, I, I, I, I, P, P, P, P, SZ, P]),
 }
 
 

@@ -22,6 +22,7 @@ MOE_PERMUTE_FUSE_MXFP8 = 2
 MOE_QUANT_COLWISE = 4
 MOE_DEVERR_BAD_ID = 1
 MOE_DEVERR_TIMEOUT = 2
+MOE_DEVERR_NO_PAGE = 4
 
 
 class MoeError(RuntimeError):
@@ -1001,3 +1002,324 @@ def moe_grad_clip(grads, max_norm: float, *, eps: float = 1e-6, out=None, norm: 
     """Scale the gradients by min(1, max_norm / (norm + eps)), norm being their global norm (1 where
     norm + eps is within max_norm, 0 and inf included): in place, or into the tensors of out. Returns the norm before clipping ([1] fp32, on the device)."""
     return _grad_norm_clip(grads, grads if out is None else out, max_norm, eps, norm, workspace, stream)
+
+
+# ------------------------------------------------------- paged key-value cache
+class PagedCache(NamedTuple):
+    """One layer's keys and values in pages; the pages of a sequence are a row of a table [S, M] int32."""
+    precision: str                    # "bf16" or "mxfp8"
+    pages: int
+    heads: int                        # key heads
+    page_size: int
+    dim: int
+    k: torch.Tensor                   # [pages, heads, page_size, dim] bf16 or uint8 (E4M3)
+    k_scales: Optional[torch.Tensor]  # [pages, heads, page_size, dim/32] uint8 (MXFP8)
+    v: torch.Tensor
+    v_scales: Optional[torch.Tensor]
+
+
+def cache_buffers(pages: int, heads: int, page_size: int, dim: int, device, precision: str = "bf16",
+                  stream=None) -> PagedCache:
+    """Pools of this many pages (uninitialised: what no position was written to is not read)."""
+    fp8 = _dt_code(precision) == MOE_MXFP8
+    shape, dev = (pages, heads, page_size, dim), torch.device(device)
+
+    def side():
+        if fp8:
+            return (_empty(shape, torch.uint8, dev, stream),
+                    _empty(shape[:3] + (dim // 32,), torch.uint8, dev, stream))
+        return _empty(shape, torch.bfloat16, dev, stream), None
+    return PagedCache(precision, pages, heads, page_size, dim, *side(), *side())
+
+
+def _want_cache(c: PagedCache, dev: int) -> int:
+    """The pools have the shape that the cache says, on this device; its type's code."""
+    code = _dt_code(c.precision)
+    fp8 = code == MOE_MXFP8
+    shape, dtype = (c.pages, c.heads, c.page_size, c.dim), torch.uint8 if fp8 else torch.bfloat16
+    if c.k is None or c.v is None or (fp8 and (c.k_scales is None or c.v_scales is None)):
+        raise ValueError("the cache has no pools")
+    _like(c.k, "cache.k", dtype, shape, dev)
+    _like(c.v, "cache.v", dtype, shape, dev)
+    if fp8:
+        shape = shape[:3] + (c.dim // 32,)
+        _like(c.k_scales, "cache.k_scales", torch.uint8, shape, dev)
+        _like(c.v_scales, "cache.v_scales", torch.uint8, shape, dev)
+    return code
+
+
+def _table(table: torch.Tensor, dev: int):
+    _like(table, "table", torch.int32, table.shape, dev)
+    if table.dim() != 2:
+        raise ValueError("table must have 2 dims")
+    return table.shape
+
+
+def _tokens(t: torch.Tensor, name: str, shape, dev: int) -> int:
+    """t is bf16 of this shape on this device, the last two dimensions without gaps: the stride between tokens
+    in elements (0 where there is one)."""
+    if not (t.is_cuda and t.get_device() == dev):
+        raise ValueError(f"{name} must be on cuda:{dev}, the other tensors' device")
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    n, h, d = shape
+    if tuple(t.shape) != (n, h, d):
+        raise ValueError(f"{name} must be {[n, h, d]}")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+        raise ValueError(f"{name}'s heads must be contiguous (tokens may be apart)")
+    return s0 if n > 1 else 0
+
+
+def moe_cache_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, table: torch.Tensor, positions: torch.Tensor, *,
+                     rows: Optional[torch.Tensor] = None, stream=None) -> None:
+    """k, v [n, heads, dim] bf16 (slices of one projection, say) to position positions[i] of sequence rows[i] (None:
+    of sequence i); tokens with a negative position or row are skipped."""
+    dev = k.get_device()
+    n = k.shape[0]
+    shape = (n, cache.heads, cache.dim)
+    ks, vs = _tokens(k, "k", shape, dev), _tokens(v, "v", shape, dev)
+    code = _want_cache(cache, dev)
+    S, M = _table(table, dev)
+    _like(positions, "positions", torch.int32, (n,), dev)
+    _like(rows, "rows", torch.int32, (n,), dev)
+    st = _lib.load().moe_cache_append(
+        k.data_ptr(), v.data_ptr(), ks, vs, n, _at(rows), positions.data_ptr(), table.data_ptr(), S, M, code, cache.pages,
+        cache.heads, cache.page_size, cache.dim, cache.k.data_ptr(), _at(cache.k_scales), cache.v.data_ptr(),
+        _at(cache.v_scales), _raw_stream(stream, k))
+    _check("moe_cache_append", st)
+
+
+def moe_cache_gather(cache: PagedCache, table: torch.Tensor, positions: torch.Tensor, *,
+                     rows: Optional[torch.Tensor] = None, k: Optional[torch.Tensor] = None,
+                     v: Optional[torch.Tensor] = None, stream=None):
+    """The keys and values at positions (of sequences rows) -> k, v [n, heads, dim] bf16; zeros where a position or
+    row is negative."""
+    dev = cache.k.get_device()
+    code = _want_cache(cache, dev)
+    S, M = _table(table, dev)
+    _want(positions, "positions", torch.int32, 1)
+    n = positions.shape[0]
+    _like(positions, "positions", torch.int32, (n,), dev)
+    _like(rows, "rows", torch.int32, (n,), dev)
+    shape = (n, cache.heads, cache.dim)
+    if k is None:
+        k = _empty(shape, torch.bfloat16, cache.k.device, stream)
+    else:
+        _like(k, "k", torch.bfloat16, shape, dev)
+    if v is None:
+        v = _empty(shape, torch.bfloat16, cache.k.device, stream)
+    else:
+        _like(v, "v", torch.bfloat16, shape, dev)
+    st = _lib.load().moe_cache_gather(
+        k.data_ptr(), v.data_ptr(), n, _at(rows), positions.data_ptr(), table.data_ptr(), S, M, code, cache.pages,
+        cache.heads, cache.page_size, cache.dim, cache.k.data_ptr(), _at(cache.k_scales), cache.v.data_ptr(),
+        _at(cache.v_scales), _raw_stream(stream, cache.k))
+    _check("moe_cache_gather", st)
+    return k, v
+
+
+def moe_paged_attention_workspace(cache: PagedCache, B: int, q_heads: int, stream=None) -> torch.Tensor:
+    """The workspace of moe_paged_attention for up to B sequences (uninitialised, reusable; stream: the one of the
+    first call that uses it)."""
+    n = _lib.load().moe_paged_attention_workspace_size(B, q_heads, cache.heads, cache.dim)
+    return _empty(int(n), torch.uint8, cache.k.device, stream)
+
+
+def moe_paged_attention(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lengths: torch.Tensor, *,
+                        scale: Optional[float] = None, window: int = 0, out: Optional[torch.Tensor] = None,
+                        lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """One new token's attention per sequence: q [B, q_heads, dim] bf16 (sequences may be apart), table [B, M],
+    lengths [B] int32 (the new token's own position included) -> (out [B, q_heads, dim] bf16, lse [B, q_heads]
+    fp32). scale: 1 / sqrt(dim) unless given; window > 0: only the last so many positions. A sequence of length 0
+    gives out 0 and lse -inf."""
+    dev = q.get_device()
+    if q.dim() != 3:
+        raise ValueError("q must have 3 dims")
+    B, heads, dim = q.shape
+    if dim != cache.dim or heads % cache.heads:
+        raise ValueError(f"q must be [B, a multiple of {cache.heads}, {cache.dim}]")
+    qs = _tokens(q, "q", (B, heads, dim), dev)
+    code = _want_cache(cache, dev)
+    S, M = _table(table, dev)
+    if S != B:
+        raise ValueError(f"table must have {B} rows")
+    _like(lengths, "lengths", torch.int32, (B,), dev)
+    if out is None:
+        out = _empty((B, heads, dim), torch.bfloat16, q.device, stream)
+    else:
+        _like(out, "out", torch.bfloat16, (B, heads, dim), dev)
+    if lse is None:
+        lse = _empty((B, heads), torch.float32, q.device, stream)
+    else:
+        _like(lse, "lse", torch.float32, (B, heads), dev)
+    if workspace is None:
+        workspace = moe_paged_attention_workspace(cache, B, heads, stream)
+    else:
+        _scratch(workspace, dev)
+    st = _lib.load().moe_paged_attention(
+        q.data_ptr(), qs, B, heads, cache.k.data_ptr(), _at(cache.k_scales), cache.v.data_ptr(), _at(cache.v_scales), code,
+        cache.pages, cache.heads, cache.page_size, dim, table.data_ptr(), M, lengths.data_ptr(),
+        dim ** -0.5 if scale is None else scale, window, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _raw_stream(stream, q))
+    _check("moe_paged_attention", st)
+    return out, lse
+
+
+def moe_cache_pages_workspace(pages: int, rows: int, device, stream=None) -> torch.Tensor:
+    """The workspace of moe_cache_fork (rows: of the new table) and moe_cache_compact."""
+    n = _lib.load().moe_cache_pages_workspace_size(pages, rows)
+    return _empty(int(n), torch.uint8, torch.device(device), stream)
+
+
+class CacheFork(NamedTuple):
+    table: torch.Tensor               # [S_new, M] int32
+    lengths: torch.Tensor             # [S_new] int32
+    src: torch.Tensor                 # [S_new] int32: the page to copy for each row, -1: none
+    dst: torch.Tensor                 # [S_new] int32: where to
+    used: torch.Tensor                # [1] int32: pages in use, those that were missing among them
+
+
+def moe_cache_fork(table: torch.Tensor, lengths: torch.Tensor, parents: Optional[torch.Tensor], pages: int, page_size: int, *,
+                   room=1, out: Optional[CacheFork] = None, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> CacheFork:
+    """Sequences that go on from parents [S_new] int32 (rows of table; -1: none, its pages become free; None: each
+    from itself), each with room for `room` more positions (an int, or [S_new] int32) in pages of its own. The
+    pairs (src, dst) are to be copied in every layer's pools (moe_cache_copy_pages) before they are written."""
+    dev = table.get_device()
+    S, M = _table(table, dev)
+    _like(lengths, "lengths", torch.int32, (S,), dev)
+    n = S
+    if parents is not None:
+        _want(parents, "parents", torch.int32, 1)
+        n = parents.shape[0]
+        _like(parents, "parents", torch.int32, (n,), dev)
+    rooms = None
+    if isinstance(room, torch.Tensor):
+        rooms, room = room, 0
+        _like(rooms, "room", torch.int32, (n,), dev)
+    elif not 0 <= room < 1 << 31:
+        raise ValueError("room must be at least 0")
+    i32 = torch.int32
+    if out is None:
+        new = [_empty(shape, i32, table.device, stream) for shape in ((n, M), (n,), (n,), (n,), (1,))]
+        out = CacheFork(*new)
+    else:
+        for t, name, shape in zip(out, CacheFork._fields, ((n, M), (n,), (n,), (n,), (1,))):
+            _like(t, name, i32, shape, dev)
+        if out.table.data_ptr() == table.data_ptr() and table.numel():
+            raise ValueError("the new table must not be the old one")
+    if workspace is None:
+        workspace = moe_cache_pages_workspace(pages, n, table.device, stream)
+    else:
+        _scratch(workspace, dev)
+    st = _lib.load().moe_cache_fork(
+        table.data_ptr(), lengths.data_ptr(), S, M, _at(parents), n, pages, page_size, room, _at(rooms),
+        out.table.data_ptr(), out.lengths.data_ptr(), out.src.data_ptr(), out.dst.data_ptr(), out.used.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, table))
+    _check("moe_cache_fork", st)
+    return out
+
+
+class CacheCompact(NamedTuple):
+    table: torch.Tensor               # [S, M] int32
+    src: torch.Tensor                 # [pages / 2] int32: pages to move, -1 behind the last
+    dst: torch.Tensor                 # [pages / 2] int32: where to
+    used: torch.Tensor                # [1] int32: pages in use, 0 .. used - 1 after the moves
+
+
+def moe_cache_compact(table: torch.Tensor, pages: int, *, out: Optional[CacheCompact] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> CacheCompact:
+    """The pages that the table names renumbered to the lowest numbers; the pairs (src, dst) are to be copied in
+    every layer's pools (moe_cache_copy_pages) before the new table is used. out.table may be the table itself."""
+    dev = table.get_device()
+    S, M = _table(table, dev)
+    shapes = ((S, M), (pages // 2,), (pages // 2,), (1,))
+    if out is None:
+        out = CacheCompact(*[_empty(shape, torch.int32, table.device, stream) for shape in shapes])
+    else:
+        for t, name, shape in zip(out, CacheCompact._fields, shapes):
+            _like(t, name, torch.int32, shape, dev)
+    if workspace is None:
+        workspace = moe_cache_pages_workspace(pages, 0, table.device, stream)
+    else:
+        _scratch(workspace, dev)
+    st = _lib.load().moe_cache_compact(table.data_ptr(), S, M, pages, out.table.data_ptr(), out.src.data_ptr(),
+                                       out.dst.data_ptr(), out.used.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                       _raw_stream(stream, table))
+    _check("moe_cache_compact", st)
+    return out
+
+
+def moe_cache_copy_pages(caches, src: torch.Tensor, dst: torch.Tensor, *, stream=None) -> None:
+    """Page dst[i] = page src[i] (int32 lists on the device; pairs with -1 are skipped) in a PagedCache, or in each
+    of a list of them (a model's layers) with the same number of pages."""
+    if isinstance(caches, PagedCache):
+        caches = [caches]
+    dev = src.get_device()
+    n = src.numel()
+    _like(src, "src", torch.int32, (n,), dev)
+    _like(dst, "dst", torch.int32, (n,), dev)
+    if dev < 0:
+        raise ValueError("src must be a CUDA tensor")
+    pools, sizes = array("q"), array("q")
+    pages = caches[0].pages if caches else 1
+    for c in caches:
+        fp8 = _want_cache(c, dev) == MOE_MXFP8
+        if c.pages != pages:
+            raise ValueError("the caches must have the same number of pages")
+        rows = c.heads * c.page_size
+        pools.extend((c.k.data_ptr(), c.v.data_ptr()))
+        size = rows * c.dim * (1 if fp8 else 2)
+        sizes.extend((size, size))
+        if fp8:
+            pools.extend((c.k_scales.data_ptr(), c.v_scales.data_ptr()))
+            size = rows * (c.dim // 32)
+            sizes.extend((size, size))
+    st = _lib.load().moe_cache_copy_pages(pools.buffer_info()[0], sizes.buffer_info()[0], len(pools), src.data_ptr(),
+                                          dst.data_ptr(), n, pages, _raw_stream(stream, src))
+    _check("moe_cache_copy_pages", st)
+
+
+# -------------------------------------------------------------- beam selection
+class BeamSelected(NamedTuple):
+    scores: torch.Tensor              # [N, K] fp32
+    parents: torch.Tensor             # [N, K] int32: rows n * W + w of the beams that go on
+    tokens: torch.Tensor              # [N, K] int32
+
+
+def moe_beam_select_workspace(logits: torch.Tensor, K: int, stream=None) -> torch.Tensor:
+    """The workspace of moe_beam_select for logits of this shape (uninitialised, reusable)."""
+    N, W, V = logits.shape
+    return _empty(int(_lib.load().moe_beam_select_workspace_size(N, W, V, K)), torch.uint8, logits.device, stream)
+
+
+def moe_beam_select(logits: torch.Tensor, scores: torch.Tensor, K: int, *, done: Optional[torch.Tensor] = None, pad: int = 0,
+                    out: Optional[BeamSelected] = None, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> BeamSelected:
+    """The K best of scores [N, W] fp32 + log_softmax(logits [N, W, V] bf16 or fp32) over beams and tokens, ties to
+    the lower beam, then the lower token. A beam that is done ([N, W] bool) goes on with `pad` alone and its score as
+    it is; one whose score is -inf has no candidates."""
+    _want(logits, "logits", None, 3)
+    N, W, V = logits.shape
+    dev = logits.get_device()
+    code = _float_code(logits, "logits")
+    _like(scores, "scores", torch.float32, (N, W), dev)
+    _like(done, "done", torch.bool, (N, W), dev)
+    if out is None:
+        out = BeamSelected(_empty((N, K), torch.float32, logits.device, stream),
+                           _empty((N, K), torch.int32, logits.device, stream),
+                           _empty((N, K), torch.int32, logits.device, stream))
+    else:
+        _like(out.scores, "scores", torch.float32, (N, K), dev)
+        _like(out.parents, "parents", torch.int32, (N, K), dev)
+        _like(out.tokens, "tokens", torch.int32, (N, K), dev)
+    if workspace is None:
+        workspace = moe_beam_select_workspace(logits, K, stream)
+    else:
+        _scratch(workspace, dev)
+    st = _lib.load().moe_beam_select(logits.data_ptr(), code, scores.data_ptr(), _at(done), pad, N, W, V, K,
+                                     out.scores.data_ptr(), out.parents.data_ptr(), out.tokens.data_ptr(),
+                                     workspace.data_ptr(), workspace.numel(), _raw_stream(stream, logits))
+    _check("moe_beam_select", st)
+    return out

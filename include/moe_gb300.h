@@ -62,7 +62,7 @@ typedef enum {
     MOE_I32 = 1,   /* int32 expert ids */
     MOE_BF16 = 2,  /* bfloat16 operands */
     MOE_MXFP8 = 3, /* E4M3 payloads with one E8M0 scale byte per 32 elements */
-    MOE_F32 = 4    /* fp32 (layer norm and gradient norm) */
+    MOE_F32 = 4    /* fp32 (layer norm, gradient norm, beam selection) */
 } moe_dtype;
 
 /* flags */
@@ -73,6 +73,7 @@ typedef enum {
 /* device error bits */
 #define MOE_DEVERR_BAD_ID 1u       /* an expert id outside [-1, E) was seen (treated as invalid) */
 #define MOE_DEVERR_TIMEOUT 2u      /* a bounded wait inside a kernel gave up */
+#define MOE_DEVERR_NO_PAGE 4u      /* the cache's pool had fewer free pages than its sequences needed */
 
 /* ------------------------------------------------------------------------
  * Router top-K ([SPARSER] "Preserve a compact route": radix/threshold
@@ -594,6 +595,124 @@ moe_status moe_grad_norm_clip(const void *const *grads, const long long *counts,
                               const int *dtypes, void *const *outs, int n, float max_norm,
                               float eps, float *norm_out, void *workspace,
                               size_t workspace_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged key-value cache (a decoding step's attention around the layer; the pages
+ * do not describe one). One layer's cache is two pools of pages, keys and values
+ * [pages, heads, page_size, dim], of dtype MOE_BF16, or MOE_MXFP8 with scales
+ * [pages, heads, page_size, dim/32] (the row rule of moe_permute along dim). A table
+ * [S, M] int32 gives the pages of S sequences: position p of sequence s is offset
+ * p % page_size of page table[s, p / page_size]. -1 marks no page. A page id outside
+ * [-1, pages) where a position is read or written, or -1 there, sets MOE_DEVERR_BAD_ID;
+ * the position is then left out. Many rows may name one page. The calls below require
+ * 1 <= pages, heads, dim % 16 == 0 (MXFP8: % 32), dim <= 256, 1 <= page_size <= 4096,
+ * 1 <= M, M * page_size < 2^31; tables, lengths and positions 4-byte aligned, everything
+ * else 16-byte (scales: to the largest power of two that divides dim / 32, 8 at most).
+ *
+ * moe_cache_append: k, v [n, heads, dim] bf16, tokens k_stride and v_stride elements apart
+ * (multiples of 8; slices of one projection), to position positions[i] of sequence rows[i]
+ * (rows NULL: of sequence i, n <= S). A negative position or row is skipped (padding); a
+ * position at or past M * page_size or a row >= S is a bad id. The (page, offset) pairs of one
+ * call must be distinct. MXFP8 quantises on the way.
+ * moe_cache_gather: the same positions read back, k, v [n, heads, dim] bf16 contiguous
+ * (MXFP8: code times scale, exact), zeros for the positions that are skipped or bad.
+ * ------------------------------------------------------------------------ */
+moe_status moe_cache_append(const void *k, const void *v, long long k_stride, long long v_stride,
+                            int n, const int32_t *rows, const int32_t *positions,
+                            const int32_t *table, int S, int M, moe_dtype dtype, int pages,
+                            int heads, int page_size, int dim, void *k_pages, uint8_t *k_scales,
+                            void *v_pages, uint8_t *v_scales, moe_stream_t stream);
+
+moe_status moe_cache_gather(void *k, void *v, int n, const int32_t *rows, const int32_t *positions,
+                            const int32_t *table, int S, int M, moe_dtype dtype, int pages,
+                            int heads, int page_size, int dim, const void *k_pages,
+                            const uint8_t *k_scales, const void *v_pages,
+                            const uint8_t *v_scales, moe_stream_t stream);
+
+/* Attention of one new token per sequence over the cache. q [B, q_heads, dim] bf16, sequences
+ * q_stride elements apart (a multiple of 8); q_heads a multiple of heads, query head h reads
+ * key head h / (q_heads / heads). With n = lengths[b] (negative: 0; above M * page_size: that, and
+ * MOE_DEVERR_BAD_ID) and first = window > 0 ? max(0, n - window) : 0, over first <= j < n:
+ *   s_j = scale q.k_j;  m = max s;  l = sum exp(s_j - m);  out = round(sum exp(s_j - m) v_j / l)
+ *   lse = m + ln l
+ * out [B, q_heads, dim] bf16, lse [B, q_heads] fp32 (NULL to skip). Without a position: out 0,
+ * lse -inf. What lies in the pages beside these positions does not matter (NaN among it). Sums,
+ * maxima and the joined parts are fp32; the weights exp(s - m) are rounded to 16 bits (bf16
+ * beside bf16 values, fp16 beside MXFP8 ones) before they meet the values, l before
+ * that. Outputs depend on the sizes, lengths and the device, not on timing. Requires B <= 65535,
+ * q_heads / heads <= 1024, finite scale, window >= 0. workspace:
+ * moe_paged_attention_workspace_size bytes (0 for refused sizes), 16-byte aligned, not
+ * initialised; calls that share one must not overlap. */
+size_t moe_paged_attention_workspace_size(int B, int q_heads, int heads, int dim);
+
+moe_status moe_paged_attention(const void *q, long long q_stride, int B, int q_heads,
+                               const void *k_pages, const uint8_t *k_scales, const void *v_pages,
+                               const uint8_t *v_scales, moe_dtype dtype, int pages, int heads,
+                               int page_size, int dim, const int32_t *table, int M,
+                               const int32_t *lengths, float scale, int window, void *out,
+                               float *lse, void *workspace, size_t workspace_bytes,
+                               moe_stream_t stream);
+
+/* Page bookkeeping on the device: no counts of pages are kept, a page is free when no row of the
+ * table names it.
+ *
+ * moe_cache_fork: S_new sequences that go on from parents [S_new] (NULL: each from itself, S_new
+ * = S). Row i of new_table [S_new, M] is row parents[i] of table, cut to the pages that
+ * lengths[parents[i]] positions take; new_lengths[i] is that length; parent -1 (or outside
+ * [-1, S): a bad id) gives an empty row of length 0. Then every row with a parent gets room
+ * for `room` more positions (rooms [S_new], where given, instead; negative: 0): a page that it
+ * would write in but shares is replaced by a free one and (src[i], dst[i]) says what to copy (-1, -1 where
+ * nothing is); the row that keeps a shared page is the one with most positions in it, then the
+ * first. The pages behind are free ones too (up to M). Free pages go out in ascending order, to
+ * rows in ascending order, the copied page first. Pages that no row names any more are free.
+ * *used: the pages named in the end, and those that were missing (then *used > pages,
+ * MOE_DEVERR_NO_PAGE is set and the entries stay -1). Outputs must not overlap inputs.
+ * Requires page_size * S_new < 2^31.
+ *
+ * moe_cache_compact: the named pages renumbered to 0 .. *used - 1: the i-th page at or above
+ * *used goes to the i-th hole below it. new_table: the rows with the new numbers; src, dst
+ * [pages / 2]: the moves, in order, -1 behind the last. A bad id in the table becomes -1. new_table
+ * may be table.
+ *
+ * moe_cache_copy_pages: page dst[i] = page src[i] for n pairs, in n_tensors pools (host arrays of
+ * device pointers and bytes a page); pairs with -1 are skipped, ids outside [-1, pages) are
+ * skipped and bad. No page may be the destination of two pairs, nor of one and the source of
+ * another (the lists of the two calls above are so). The host arrays are read during the call only.
+ *
+ * workspace: moe_cache_pages_workspace_size bytes (rows: of the new table), 16-byte aligned, not
+ * initialised; calls that share one must not overlap. */
+size_t moe_cache_pages_workspace_size(int pages, int rows);
+
+moe_status moe_cache_fork(const int32_t *table, const int32_t *lengths, int S, int M,
+                          const int32_t *parents, int S_new, int pages, int page_size, int room,
+                          const int32_t *rooms, int32_t *new_table, int32_t *new_lengths,
+                          int32_t *src, int32_t *dst, int32_t *used, void *workspace,
+                          size_t workspace_bytes, moe_stream_t stream);
+
+moe_status moe_cache_compact(const int32_t *table, int S, int M, int pages, int32_t *new_table,
+                             int32_t *src, int32_t *dst, int32_t *used, void *workspace,
+                             size_t workspace_bytes, moe_stream_t stream);
+
+moe_status moe_cache_copy_pages(void *const *tensors, const long long *page_bytes, int n_tensors,
+                                const int32_t *src, const int32_t *dst, int n, int pages,
+                                moe_stream_t stream);
+
+/* Selection of a beam search's step. logits [N, W, V] (MOE_F32 or MOE_BF16), scores [N, W] fp32.
+ * Candidate (w, t) of search n: scores[n,w] + (logits[n,w,t] - lse), lse = ln sum exp(logits[n,w]); of a
+ * beam whose score or lse is not finite: -inf. done [N, W] bytes (NULL: none): a beam that is
+ * done has one candidate, token pad with its score as it is, and -inf elsewhere. The K largest in
+ * order, ties to the lower w, then the lower t: out_scores [N, K] fp32, parents [N, K] = n * W + w,
+ * tokens [N, K]. lse is summed in fp32 over each thread's share and in 64 bits above, the
+ * candidates are compared in 64 bits and rounded once. Requires 1 <= W <= 64, 1 <= V < 2^24,
+ * N * W < 2^24, 1 <= K <= 64, K <= W * V, 0 <= pad < V with done. workspace:
+ * moe_beam_select_workspace_size bytes (0 for refused sizes), 16-byte aligned, not initialised; calls that
+ * share one must not overlap. */
+size_t moe_beam_select_workspace_size(int N, int W, int V, int K);
+
+moe_status moe_beam_select(const void *logits, moe_dtype dtype, const float *scores,
+                           const uint8_t *done, int pad, int N, int W, int V, int K,
+                           float *out_scores, int32_t *parents, int32_t *tokens, void *workspace,
+                           size_t workspace_bytes, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Device error word. Copies the word to *flags_out (synchronising the device)

@@ -1,0 +1,190 @@
+"""Selection of a beam search's step against a plain 64-bit implementation, through the C ABI.
+
+Bars. The sum under a beam's logarithm is of at most 2^11 terms a thread in fp32, each off by 2^-22 of itself
+(exp), and in 64 bits above that; so lse errs by 2^-12 at most. What is compared is ids: they have to be the
+reference's wherever its candidates are further apart than that, and everywhere in one beam, whose candidates
+all have the same error, and where nothing is rounded (equal beams, finished beams, -inf)."""
+import pytest
+import torch
+
+from dropless_moe_expert_router_gb300 import api
+from dropless_moe_expert_router_gb300.api import MoeError
+
+pytestmark = pytest.mark.gpu
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+INF = float("inf")
+BAR = 2.0 ** -12
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from dropless_moe_expert_router_gb300 import build
+    build.build()
+
+
+def _plain(logits, scores, K, done=None, pad=0):
+    x, s = logits.double().cpu(), scores.double().cpu()
+    N, W, V = x.shape
+    lse = torch.logsumexp(x, -1)
+    alive = torch.isfinite(lse) & torch.isfinite(s)
+    c = s[..., None] + (x - torch.where(torch.isfinite(lse), lse, torch.zeros_like(lse))[..., None])
+    c = torch.where(alive[..., None], c, torch.full_like(c, -INF))
+    if done is not None:
+        only = torch.full((V,), -INF, dtype=torch.float64)
+        only[pad] = 0.0
+        fin = torch.where(torch.isfinite(s), s, torch.full_like(s, -INF))[..., None] + only
+        c = torch.where(done.cpu()[..., None], fin, c)
+    v, at = torch.sort(c.view(N, -1), dim=1, descending=True, stable=True)
+    return c.view(N, -1), v[:, :K], at[:, :K]
+
+
+def _check(logits, scores, K, done=None, pad=0, exact=False, **kw):
+    N, W, V = logits.shape
+    o = api.moe_beam_select(logits, scores, K, done=done, pad=pad, **kw)
+    c, v, at = _plain(logits, scores, K, done, pad)
+    assert o.scores.dtype == F32 and o.parents.dtype == I32 and o.tokens.dtype == I32
+    rows, tok = o.parents.cpu().long(), o.tokens.cpu().long()
+    base = torch.arange(N)[:, None] * W
+    assert bool(((rows >= base) & (rows < base + W) & (tok >= 0) & (tok < V)).all())
+    got = (rows - base) * V + tok
+    val = torch.gather(c, 1, got)
+    # no candidate twice, their own values in order, and as good as the reference's
+    assert all(len(set(r)) == K for r in got.tolist())
+    fin = torch.isfinite(v)
+    assert torch.equal(fin, torch.isfinite(val)) and torch.equal(fin, torch.isfinite(o.scores.cpu()))
+    err = BAR + 2.0 ** -23 * v[fin].abs()
+    assert bool(((val - v)[fin].abs() <= 2 * err).all())
+    assert bool(((o.scores.cpu().double() - val)[fin].abs() <= err).all())
+    assert torch.equal(got[~fin], at[~fin])                          # -inf: the lowest indices
+    if exact or W == 1:
+        assert torch.equal(got, at)
+    else:
+        # where the reference's neighbours are further apart than the bar, the ids are its own
+        gap = torch.full((N, K + 1), INF, dtype=torch.float64)
+        gap[:, 1:K] = v[:, :-1] - v[:, 1:]
+        nxt = torch.sort(c, 1, descending=True).values
+        if c.shape[1] > K:
+            gap[:, K] = v[:, -1] - nxt[:, K]
+        sure = torch.minimum(gap[:, :-1], gap[:, 1:]) > 2 * BAR
+        assert torch.equal(got[sure & fin], at[sure & fin])
+    assert api.moe_get_device_errors() == 0
+    return o
+
+
+def _inputs(N, W, V, dtype, seed, std=2.5):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return ((torch.randn((N, W, V), generator=g, device="cuda") * std).to(dtype),
+            -8 * torch.rand((N, W), generator=g, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N,W,V,K", [(1, 1, 1, 1), (1, 1, 7, 7), (2, 3, 5, 15), (1, 4, 32000, 8), (5, 5, 1001, 10), (3, 2, 4096, 64),
+                                     (2, 8, 50021, 16), (1, 1, 200_003, 32), (40, 4, 513, 4), (1, 64, 257, 64), (2, 16, 8192, 1),
+                                     (1, 3, 31, 64), (300, 1, 100, 3), (2, 7, 33333, 33)])
+def test_selection(N, W, V, K, dtype):
+    logits, scores = _inputs(N, W, V, dtype, seed=V + K)
+    _check(logits, scores, K)
+    done = torch.rand((N, W), generator=torch.Generator().manual_seed(V)) < 0.4
+    _check(logits, scores, K, done=done.cuda(), pad=V // 2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_first_step_and_dead_beams(dtype):
+    logits, scores = _inputs(3, 4, 2000, dtype, seed=1)
+    scores[:, 1:] = -INF
+    _check(logits, scores, 8)
+    scores[1] = -INF                                                  # no beam lives: -inf, lowest indices
+    _check(logits, scores, 8)
+    done = torch.ones((3, 4), dtype=torch.bool, device="cuda")
+    _check(logits, scores, 8, done=done, pad=1999)                    # fewer candidates than K
+    scores[0, 2], scores[2, 1] = float("nan"), INF
+    _check(logits, scores, 8)
+    _check(logits, scores, 8, done=done, pad=3)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_masked_and_bad_logits(dtype):
+    """Forbidden tokens (-inf, the type's lowest), rows that forbid everything, NaN and +inf rows."""
+    logits, scores = _inputs(4, 3, 777, dtype, seed=2)
+    logits[0, :, 5:] = -INF                                           # 15 candidates are left
+    logits[1, 1] = -INF
+    logits[2, 0] = torch.finfo(dtype).min
+    logits[2, 1, 100:] = torch.finfo(dtype).min
+    logits[3, 0, 50], logits[3, 1, 51] = float("nan"), INF
+    _check(logits, scores, 12)
+    _check(logits, scores, 20)
+
+
+def test_ties_go_to_the_lowest_beam_then_token():
+    for dtype in (F32, BF):
+        logits = torch.zeros((2, 4, 3000), device="cuda", dtype=dtype)
+        scores = torch.zeros((2, 4), device="cuda")
+        o = _check(logits, scores, 40, exact=True)
+        assert o.tokens[0].tolist() == list(range(40)) and o.parents[1].tolist() == [4] * 40
+        one, _ = _inputs(1, 1, 3000, BF, seed=3, std=1.0)             # a few hundred values: many ties
+        logits = one.to(dtype).expand(2, 4, 3000).contiguous()
+        _check(logits, scores, 64, exact=True)
+        logits = torch.full((1, 2, 70_000), -3.0, device="cuda", dtype=dtype)
+        logits[0, :, 69_990:] = 2.0
+        o = _check(logits, scores[:1, :2].contiguous(), 30, exact=True)
+        assert o.tokens[0].tolist() == list(range(69_990, 70_000)) * 2 + list(range(10))
+
+
+def test_ascending_and_descending_rows():
+    """The best at the end, where every element beats those before it, and at the start."""
+    for flip in (False, True):
+        row = torch.linspace(-5, 5, 60_000, device="cuda")
+        logits = (row.flip(0) if flip else row).expand(1, 2, 60_000).contiguous()
+        _check(logits, torch.tensor([[0.0, -0.5]], device="cuda"), 64)
+
+
+def test_repeats_on_any_workspace_stream_and_graph():
+    logits, scores = _inputs(3, 6, 40_000, F32, seed=9)
+    ref = _check(logits, scores, 12)
+    ws = api.moe_beam_select_workspace(logits, 12)
+    s = torch.cuda.Stream()
+    for fill in (0, 255):
+        ws.fill_(fill)
+        s.wait_stream(torch.cuda.current_stream())
+        got = api.moe_beam_select(logits, scores, 12, workspace=ws, stream=s)
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    out = api.BeamSelected(*[torch.empty_like(t) for t in ref])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.moe_beam_select(logits, scores, 12, workspace=ws, out=out)
+    ws.fill_(255)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ref, out))
+    logits.copy_(logits.flip(2))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out.tokens, 39_999 - ref.tokens)
+
+
+def test_refusals():
+    logits, scores = _inputs(2, 3, 50, F32, seed=1)
+    with pytest.raises(ValueError):
+        api.moe_beam_select(logits.half(), scores, 4)
+    with pytest.raises(ValueError):
+        api.moe_beam_select(logits.transpose(1, 2), scores, 4)
+    with pytest.raises(ValueError):
+        api.moe_beam_select(logits, scores[:1], 4)
+    with pytest.raises(ValueError):
+        api.moe_beam_select(logits, scores.double(), 4)
+    with pytest.raises(ValueError):
+        api.moe_beam_select(logits, scores, 4, done=torch.zeros((2, 3), device="cuda"))
+    with pytest.raises(ValueError):
+        api.moe_beam_select(logits.cpu(), scores, 4)
+    for K in (0, 65, 151):
+        with pytest.raises(MoeError):
+            api.moe_beam_select(logits, scores, K)
+    done = torch.zeros((2, 3), dtype=torch.bool, device="cuda")
+    for pad in (-1, 50):
+        with pytest.raises(MoeError):
+            api.moe_beam_select(logits, scores, 4, done=done, pad=pad)
+    with pytest.raises(MoeError):
+        api.moe_beam_select(logits, scores, 4, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    assert api.moe_beam_select(logits[:0], scores[:0], 4).tokens.shape == (0, 4)
