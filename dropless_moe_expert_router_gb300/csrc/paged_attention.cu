@@ -1,4 +1,28 @@
 // paged_attention.cu -- attention of one new token per sequence over a paged key-value cache: moe_paged_attention.
+//
+// For every sequence and key head, with its group of query heads: s = scale q.k over the cached positions,
+// out = sum exp(s - m) v / sum exp(s - m), in one pass with a running maximum m. Each cached byte is used by the
+// group's heads only (a multiply-add per head and element), so DRAM bounds it: what matters is that every block
+// has loads in flight all the time and that all blocks end together.
+//
+// Split: the positions of all (sequence, key head) pairs, in units of 64, are laid end to end and cut into one
+// equal stretch per block (two blocks an SM), whatever the lengths. A pair that lies in one stretch is finished there; of one
+// that is cut, each block leaves m, l and the unnormalised output in the workspace, and a second kernel, set up
+// while the first one runs, joins them in the blocks' order. So outputs do not depend on timing.
+//
+// A block's four warps work alone, 16 positions of a unit each: a ring of three tiles or more per warp is filled by 16-byte
+// asynchronous copies (rows anywhere, so pages may end inside a tile; absent rows are filled with zeros).
+// The products take the cache as the 16-row operand and the heads as the 8 columns, S^T = K Q^T and
+// O^T = V^T P^T, so that a key or value passes through one fragment once, whatever the group, and the running
+// maximum and scale of a head sit in the lanes that hold its column. P^T is the transpose of the fragment that S^T comes
+// out in (movmatrix). These are mma.sync products: a tcgen05 tile of 128 rows would want the softmax
+// across 128 lanes of tensor memory and the weights back through shared memory, for a product that DRAM bounds.
+//
+// MXFP8: codes are converted to halves on the way to the fragments (exact). A block of 32 keys' elements is one
+// partial product, scaled by the key's power of two in fp32; q is scaled per head by a power of two to fill fp16's
+// range. Values' scales go into the weights, relative to the largest scale that the warp has met, which the sums are
+// kept relative to; fp16 weights are scaled by 2^15, so that one loses bits only below 2^-29 of the largest. A tile
+// whose scales span more than 2^6 below that takes bf16 values and weights, which have fp32's range.
 #include "common.cuh"
 #include "paged_cache.cuh"
 
@@ -7,7 +31,13 @@
 namespace moe {
 namespace {
 
-constexpr int PA_WARPS = 8;
+constexpr int PA_WARPS = 4;
+constexpr int PA_THREADS = 32 * PA_WARPS;
+constexpr int PA_TILE = 16;                       // positions of a warp's tile
+constexpr int PA_UNIT = PA_WARPS * PA_TILE;       // positions of a block's unit
+constexpr int PA_MAX_CTAS = 512;                  // blocks at most: what the workspace has room for
+constexpr int PA_MIN_UNITS = 2;                   // of a block's stretch: a shorter one costs more to join than it saves
+constexpr int PA_SPREAD = 6;                      // exponents below the largest scale that fp16 weights take
 
 struct AttnArgs {
     const __nv_bfloat16* q;
@@ -19,77 +49,739 @@ struct AttnArgs {
     float scale;
     __nv_bfloat16* out;
     float* lse;
+    float* part;                                  // [2 * ctas][8 NB][DP] unnormalised outputs
+    float2* part_ml;                              // [2 * ctas][8 NB]
+    int4* cut;                                    // [ctas] the pair that a block begins and does not end
+    int tiles_of_heads;                           // tiles of 8 NB query heads in a group
+    int whole;                                    // pairs are not cut: a stretch is of pairs, not of units
 };
 
-// One element of a row of the cache.
-template <bool FP8>
-__device__ __forceinline__ float element(const void* pool, const uint8_t* scales, long long line, int dim, int d) {
-    if (!FP8) return __bfloat162float(static_cast<const __nv_bfloat16*>(pool)[line * dim + d]);
-    return e4m3_value(static_cast<const uint8_t*>(pool)[line * dim + d]) * e8m0_value(scales[line * (dim / 32) + d / 32]);
+template <bool FP8, int DP, int NB>
+struct Cfg {
+    static constexpr int ROW = DP * (FP8 ? 1 : 2);             // bytes of a row in shared memory
+    static constexpr int CHUNKS = ROW / 16;
+    static constexpr int KV = 2 * PA_TILE * ROW;
+    static constexpr int STAGE = KV + (FP8 ? 2 * PA_TILE * 16 : 0);   // and a 16-byte slot for each row's scales
+    static constexpr int STAGES = DP == 256 && !FP8 ? 3 : (96 * 1024 / PA_WARPS) / STAGE > 6 ? 6 : (96 * 1024 / PA_WARPS) / STAGE;
+    static constexpr int PREP = FP8 ? DP / 32 * PA_TILE * (4 + 2) : 0;  // a tile's scales as the products take them
+    static constexpr int HALF = DP / 2;                        // elements joined at a time
+    static constexpr int JOIN = PA_WARPS * 8 * (HALF + 4) * 4;
+    static constexpr int ML = PA_WARPS * 8 * NB * 2 * 4;
+    static constexpr int SMEM = PA_WARPS * (STAGES * STAGE + PREP + 64) + JOIN + ML;
+    static constexpr int CTAS = SMEM + 1024 <= 114 * 1024 ? 2 : 1;
+    static constexpr int SLOT = 8 * NB * DP;                   // floats of a partial output
+};
+
+// ---------------------------------------------------------------- instructions
+__device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// 16 bytes (0: zeros instead) to shared memory.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void* from, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_t(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float pow2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+    uint2 r;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(at) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
+    return r;
+}
+__device__ __forceinline__ void sts32(uint32_t at, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
+__device__ __forceinline__ void sts16(uint32_t at, uint32_t v) {
+    asm volatile("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n st.shared.b16 [%0], l;\n}" ::"r"(at), "r"(v) : "memory");
+}
+// Codes 0 and 1 of a word, codes 2 and 3, as two halves each (exact).
+__device__ __forceinline__ void halves(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+        : "=r"(lo), "=r"(hi) : "r"(codes));
+}
+// Two halves that came from codes as two bf16 (exact).
+__device__ __forceinline__ uint32_t to_bf16x2(uint32_t h) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    if (F16) {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t times2(uint32_t x, uint32_t y) {
+    if (F16) {
+        const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// A block per sequence and query head; its warps take the positions in turn, a lane every 32nd element.
-template <bool FP8>
-__global__ void __launch_bounds__(32 * PA_WARPS) attention_kernel(const __grid_constant__ AttnArgs a) {
-    __shared__ float part[PA_WARPS][MOE_CACHE_MAX_DIM];
-    __shared__ float part_m[PA_WARPS], part_l[PA_WARPS];
-    const int h = blockIdx.x, b = blockIdx.y, dim = a.c.dim, lane = lane_id(), warp = threadIdx.x / 32;
-    const int kv = h / (a.q_heads / a.c.heads);
-    int n = a.lengths[b];
-    if (n > (long long)a.M * a.c.page_size) {
-        n = a.M * a.c.page_size;
+// ---------------------------------------------------------------- the walk over units
+// Positions [first, n) of sequence b.
+__device__ __forceinline__ void range_of(const AttnArgs& a, int b, int& first, int& n) {
+    n = max(0, __ldg(a.lengths + b));
+    const long long most = (long long)a.M * a.c.page_size;
+    if (n > most) {
+        n = (int)most;
         if (threadIdx.x == 0) raise_device_error(MOE_DEVERR_BAD_ID);
     }
-    const int first = a.window > 0 && n > a.window ? n - a.window : 0;
-    float q[8], acc[8], m = -INFINITY, l = 0.0f;
-    for (int i = 0; i < 8; i++) {
-        const int d = lane + 32 * i;
-        q[i] = d < dim ? __bfloat162float(a.q[b * a.q_stride + (long long)h * dim + d]) * a.scale : 0.0f;
-        acc[i] = 0.0f;
+    first = a.window > 0 && n > a.window ? n - a.window : 0;
+}
+// Units of a pair of sequence b: one at least, which writes the output of a sequence without positions.
+__device__ __forceinline__ int units_of(int first, int n) { return max(1, (n - first + PA_UNIT - 1) / PA_UNIT); }
+
+struct Walk {
+    int b, pair, first, n, units, u, u1;          // pair: of a sequence's key heads and tiles of query heads; [u, u1) to do
+    long long left;                               // units (whole: pairs) of the stretch from this segment on
+
+    __device__ __forceinline__ void cut(const AttnArgs& a) {
+        u1 = a.whole ? units : (int)min((long long)units, u + left);
     }
-    for (int j = first + warp; j < n; j += PA_WARPS) {
-        const int page = a.table[(long long)b * a.M + j / a.c.page_size];
-        if ((unsigned)page >= (unsigned)a.c.pages) {
-            if (lane == 0) raise_device_error(MOE_DEVERR_BAD_ID);
-            continue;
+    __device__ __forceinline__ void next(const AttnArgs& a, int pairs) {
+        left -= a.whole ? 1 : u1 - u;             // (u: where the segment began)
+        u = 0;
+        if (++pair == pairs) {
+            pair = 0;
+            if (++b < a.B && left > 0) {
+                range_of(a, b, first, n);
+                units = units_of(first, n);
+            }
         }
-        const long long line = ((long long)page * a.c.heads + kv) * a.c.page_size + j % a.c.page_size;
-        float s = 0.0f;
-        for (int i = 0; i < 8; i++)
-            if (lane + 32 * i < dim) s += q[i] * element<FP8>(a.c.k, a.c.k_scales, line, dim, lane + 32 * i);
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-        const float top = fmaxf(m, s), keep = m == -INFINITY ? 0.0f : expf(m - top), p = expf(s - top);
-        m = top;
-        l = l * keep + p;
-        for (int i = 0; i < 8; i++)
-            if (lane + 32 * i < dim) acc[i] = acc[i] * keep + p * element<FP8>(a.c.v, a.c.v_scales, line, dim, lane + 32 * i);
+        cut(a);
     }
-    for (int i = 0; i < 8; i++) part[warp][lane + 32 * i] = acc[i];
-    if (lane == 0) {
-        part_m[warp] = m;
-        part_l[warp] = l;
+};
+
+// The first segment of this block's stretch, and in total the units (whole: pairs) of all. Every thread calls it.
+__device__ __forceinline__ Walk walk_begin(const AttnArgs& a, int pairs, long long* red, long long& total, int& ctas) {
+    const int per = (a.B + PA_THREADS - 1) / PA_THREADS, b0 = min(a.B, per * (int)threadIdx.x), b1 = min(a.B, b0 + per);
+    const int warp = threadIdx.x / 32;
+    long long mine = 0;
+    int first, n;
+    for (int b = b0; b < b1; b++) {
+        if (!a.whole) range_of(a, b, first, n);
+        mine += (long long)pairs * (a.whole ? 1 : units_of(first, n));
+    }
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(FULL, upto, o);
+        if ((int)lane_id() >= o) upto += v;
+    }
+    if (lane_id() == 31) red[warp] = upto;
+    __syncthreads();
+    total = 0;
+    long long before = 0;
+#pragma unroll
+    for (int w = 0; w < PA_WARPS; w++) {
+        if (w < warp) before += red[w];
+        total += red[w];
+    }
+    // (a short total is left to fewer blocks; whole pairs to as many as there are)
+    const long long fill = a.whole ? total : (total + PA_MIN_UNITS - 1) / PA_MIN_UNITS;
+    ctas = (int)min((long long)gridDim.x, fill);
+    Walk w;
+    w.b = a.B;
+    w.left = 0;
+    if ((int)blockIdx.x >= ctas) return w;
+    const long long from = total * blockIdx.x / ctas;
+    w.left = total * (blockIdx.x + 1) / ctas - from;
+    // the thread whose sequences hold the first unit finds it
+    long long at = before + upto - mine;
+    __syncthreads();
+    if (from >= at && from < at + mine) {
+        for (int b = b0; b < b1; b++) {
+            range_of(a, b, first, n);
+            const int units = units_of(first, n);
+            const long long here = (long long)pairs * (a.whole ? 1 : units);
+            if (from < at + here) {
+                red[0] = b;
+                red[1] = a.whole ? from - at : (from - at) / units;
+                red[2] = a.whole ? 0 : (from - at) % units;
+                break;
+            }
+            at += here;
+        }
     }
     __syncthreads();
-    float top = -INFINITY, total = 0.0f;
-    for (int w = 0; w < PA_WARPS; w++) top = fmaxf(top, part_m[w]);
-    for (int w = 0; w < PA_WARPS; w++)
-        if (part_l[w] != 0.0f) total += part_l[w] * expf(part_m[w] - top);
-    const long long o = (long long)b * a.q_heads + h;
-    for (int d = threadIdx.x; d < dim; d += 32 * PA_WARPS) {
-        float v = 0.0f;
-        for (int w = 0; w < PA_WARPS; w++)
-            if (part_l[w] != 0.0f) v += part[w][d] * expf(part_m[w] - top);
-        a.out[o * dim + d] = __float2bfloat16_rn(total != 0.0f ? v / total : 0.0f);
+    w.b = (int)red[0];
+    w.pair = (int)red[1];
+    w.u = (int)red[2];
+    range_of(a, w.b, w.first, w.n);
+    w.units = units_of(w.first, w.n);
+    w.cut(a);
+    __syncthreads();
+    return w;
+}
+
+// ---------------------------------------------------------------- the kernel
+template <bool FP8, int DP, int NB>
+__global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attention_kernel(const __grid_constant__ AttnArgs a) {
+    using C = Cfg<FP8, DP, NB>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x / 32, lane = lane_id(), j = lane & 3, r8 = lane >> 2;
+    const int dim = a.c.dim, group = a.q_heads / a.c.heads, pairs = a.c.heads * a.tiles_of_heads;
+    const int row_bytes = dim * (FP8 ? 1 : 2), row_scales = dim / 32;
+    const uint32_t ring = saddr(smem) + warp * (C::STAGES * C::STAGE);
+    const uint32_t prep = saddr(smem) + PA_WARPS * C::STAGES * C::STAGE + warp * C::PREP;    // fp32 [DP/32][16], then 16-bit [DP/32][16]
+    uint32_t* const seen = reinterpret_cast<uint32_t*>(smem + PA_WARPS * (C::STAGES * C::STAGE + C::PREP)) + warp * 16;  // of a stage's rows
+    float* const join = reinterpret_cast<float*>(smem + PA_WARPS * (C::STAGES * C::STAGE + C::PREP + 64));
+    float2* const ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(join) + C::JOIN);
+    if (FP8) {
+        for (int i = lane; i < C::PREP / 4; i += 32) sts32(prep + 4 * i, 0u);
+        for (int i = lane; i < C::STAGES * C::STAGE / 4; i += 32) sts32(ring + 4 * i, 0u);
+        __syncwarp();
     }
-    if (a.lse && threadIdx.x == 0) a.lse[o] = total != 0.0f ? top + logf(total) : -INFINITY;
+    long long total;
+    int ctas;
+    Walk w = walk_begin(a, pairs, reinterpret_cast<long long*>(join), total, ctas);
+    if (threadIdx.x == 0 && !a.whole) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    pdl_trigger();
+    if (w.left <= 0) return;
+
+    // -------- the loading walk, a tile ahead of the copies: its rows' pages are on their way
+    Walk ld = w;
+    int ld_u = w.u, ld_page = -1, ld_off = 0, ld_kv = 0;
+    bool ld_in = false, ld_more = true;
+    auto look = [&]() {                            // finds the next tile of this warp that has a position
+        ld_more = false;
+        while (ld.left > 0) {
+            if (ld_u == ld.u1) {
+                ld.next(a, pairs);
+                ld_u = ld.u;
+                continue;
+            }
+            const int t = ld.first + ld_u * PA_UNIT + warp * PA_TILE;
+            ld_u++;
+            if (t >= ld.n) continue;
+            const int p = t + (lane & 15);
+            ld_in = p < ld.n;
+            const int col = p / a.c.page_size;
+            ld_off = p - col * a.c.page_size;
+            ld_kv = ld.pair / a.tiles_of_heads;
+            ld_page = ld_in ? __ldg(a.table + (long long)ld.b * a.M + col) : -1;
+            ld_more = true;
+            return;
+        }
+    };
+    int fill = 0;                                  // the stage that is filled next
+    auto issue = [&]() {
+        if (ld_more) {
+            const bool ok = ld_in && (unsigned)ld_page < (unsigned)a.c.pages;
+            if (ld_in && !ok) raise_device_error(MOE_DEVERR_BAD_ID);
+            const long long line = ok ? ((long long)ld_page * a.c.heads + ld_kv) * a.c.page_size + ld_off : 0;
+            const unsigned rows = __ballot_sync(FULL, ok) & 0xffffu;
+            const uint32_t at = ring + fill * C::STAGE;
+            constexpr int PER = 32 / C::CHUNKS > 0 ? 32 / C::CHUNKS : 1;      // rows that an instruction of the warp copies
+            const int chunk = lane % C::CHUNKS;
+            const bool in_row = chunk * 16 < row_bytes;
+#pragma unroll
+            for (int i = 0; i < PA_TILE / PER; i++) {
+                const int row = i * PER + lane / C::CHUNKS;
+                const long long from = __shfl_sync(FULL, line, row) * row_bytes + (in_row ? chunk * 16 : 0);
+                const bool there = in_row && ((rows >> row) & 1);
+                int kx, vx;                        // the chunk's place, so that the fragments' reads meet all banks
+                if (!FP8) {
+                    kx = vx = chunk ^ (row & 7);
+                } else if (DP == 64) {
+                    kx = vx = chunk ^ (((row >> 1) & 1) << 1);
+                } else {
+                    kx = chunk ^ ((row & 3) << 1);
+                    vx = chunk ^ (((row >> 1) & 3) << 1);
+                }
+                copy16(at + row * C::ROW + kx * 16, static_cast<const char*>(a.c.k) + from, there);
+                copy16(at + PA_TILE * C::ROW + row * C::ROW + vx * 16, static_cast<const char*>(a.c.v) + from, there);
+            }
+            if (FP8) {
+                // a lane per row and side: the words that hold the row's scales, and where in them they begin
+                const uint8_t* const base = (lane < 16 ? a.c.k_scales : a.c.v_scales) + line * row_scales;
+                const int skip = (int)(reinterpret_cast<uintptr_t>(base) & 3);
+                const uint32_t slot = at + C::KV + lane * 16;
+                const int words = (skip + row_scales + 3) / 4;
+#pragma unroll
+                for (int i = 0; i < (DP / 32 + 6) / 4; i++)
+                    if (i < words) copy4(slot + 4 * i, base - skip + 4 * i, ok);
+                sts32(slot + 12, ok ? 8u * skip : 0u);
+            }
+            if (lane == 0) seen[fill] = rows;
+            look();
+        }
+        copies_commit();
+        fill = fill + 1 == C::STAGES ? 0 : fill + 1;
+    };
+    look();
+#pragma unroll 1
+    for (int i = 0; i < C::STAGES; i++) issue();
+
+    const float log2_scale = a.scale * 1.44269504088896340736f;
+    int take = 0;
+    while (w.left > 0) {
+        // -------- the heads of this segment
+        const int kv = w.pair / a.tiles_of_heads, h0 = (w.pair - kv * a.tiles_of_heads) * 8 * NB;
+        uint32_t qf[NB][DP / 16][2];
+        float to_s[NB][2];                         // from the products to scores in powers of two, of columns 2j and 2j + 1
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            const int h = h0 + nb * 8 + r8;
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + w.b * a.q_stride + (long long)(kv * group + h) * dim);
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ks++) {
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    // (MXFP8: a lane's elements of a 32-element block are its eight codes of a row)
+                    const int d = FP8 ? (ks / 2) * 32 + j * 8 + (ks % 2) * 4 + e * 2 : ks * 16 + j * 2 + e * 8;
+                    qf[nb][ks][e] = h < group && d < dim ? __ldg(src + d / 2) : 0u;
+                }
+            }
+            to_s[nb][0] = to_s[nb][1] = log2_scale;
+            if (FP8) {
+                float top = 0.0f;
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ks++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const float2 f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&qf[nb][ks][e]));
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
+                // by 2^shift the largest element is in [2^14, 2^15); two steps, for either may leave fp32's exponents
+                int shift = 14 + 127 - (int)(__float_as_uint(top) >> 23);
+                if (!(top > 0.0f) || isinf(top)) shift = 0;
+                const float f1 = __uint_as_float((uint32_t)(127 + shift / 2) << 23), f2 = __uint_as_float((uint32_t)(127 + shift - shift / 2) << 23);
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ks++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const float2 f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&qf[nb][ks][e]));
+                        qf[nb][ks][e] = pack2<true>(f.x * f1 * f2, f.y * f1 * f2);
+                    }
+                const float i1 = __uint_as_float((uint32_t)(127 - shift / 2) << 23), i2 = __uint_as_float((uint32_t)(127 - shift + shift / 2) << 23);
+                const float back = log2_scale * i1 * i2;
+                to_s[nb][0] = __shfl_sync(FULL, back, j * 8);
+                to_s[nb][1] = __shfl_sync(FULL, back, j * 8 + 4);
+            }
+        }
+        float m[NB][2], l[NB][2], o[NB][DP / 16][4];
+        int vref = 0;                              // o is relative to 2^(vref - 127) (MXFP8)
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            m[nb][0] = m[nb][1] = -INFINITY;
+            l[nb][0] = l[nb][1] = 0.0f;
+#pragma unroll
+            for (int d = 0; d < DP / 16; d++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) o[nb][d][e] = 0.0f;
+        }
+        const int my_end = min(w.u1, (max(0, w.n - w.first - warp * PA_TILE) + PA_UNIT - 1) / PA_UNIT);
+#pragma unroll 1
+        for (int u = w.u; u < my_end; u++) {
+            copies_wait<C::STAGES - 1>();
+            __syncwarp();
+            const uint32_t kt = ring + take * C::STAGE, vt = kt + PA_TILE * C::ROW;
+            const uint32_t rows = seen[take];
+            bool wide = false;                     // (MXFP8) this tile's scales span more than fp16 weights take
+            if (FP8) {
+                // the tile's scales: a lane per row and side
+                const uint4 slot = lds128(kt + C::KV + lane * 16);
+                const uint32_t s0 = __funnelshift_r(slot.x, slot.y, slot.w), s1 = __funnelshift_r(slot.y, slot.z, slot.w);
+                const bool is_v = lane >= 16, here = (rows >> (lane & 15)) & 1;
+                uint32_t most = 0u, least = 255u;
+                uint32_t byte[DP / 32];
+#pragma unroll
+                for (int i = 0; i < DP / 32; i++) {
+                    byte[i] = ((i < 4 ? s0 : s1) >> (8 * (i & 3))) & 0xffu;
+                    if (is_v && here && i < row_scales) {
+                        if (byte[i] != 255u) most = max(most, byte[i]);
+                        least = min(least, byte[i]);
+                    }
+                }
+                most = __reduce_max_sync(FULL, most);
+                least = __reduce_min_sync(FULL, least);
+                if ((int)most > vref) {
+                    const float f = pow2((float)(vref - (int)most));
+#pragma unroll
+                    for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                        for (int d = 0; d < DP / 16; d++)
+#pragma unroll
+                            for (int e = 0; e < 4; e++) o[nb][d][e] *= f;
+                    vref = (int)most;
+                }
+                wide = vref - (int)least > PA_SPREAD;
+                __syncwarp();                      // (nobody reads the last tile's scales any more)
+#pragma unroll
+                for (int i = 0; i < DP / 32; i++) {
+                    if (i >= row_scales) continue;
+                    if (!is_v) {
+                        sts32(prep + (i * PA_TILE + lane) * 4, __float_as_uint(e8m0_value(byte[i])));
+                    } else {
+                        const int x = (int)byte[i] - vref;
+                        uint32_t f = wide ? (uint32_t)max(0, 127 + x) << 7 : (uint32_t)max(0, 15 + x) << 10;
+                        if (byte[i] == 255u) f = wide ? 0x7fc0u : 0x7e00u;
+                        sts16(prep + DP / 32 * PA_TILE * 4 + (i * PA_TILE + (lane - 16)) * 2, f);
+                    }
+                }
+                __syncwarp();
+            }
+            // S^T = K Q^T
+            float s[NB][4];
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) s[nb][e] = 0.0f;
+            if (!FP8) {
+                const int row = lane & 15;
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ks++) {
+                    uint32_t f[4];
+                    ldmatrix(f, kt + row * C::ROW + (((2 * ks + (lane >> 4)) ^ (row & 7)) * 16));
+#pragma unroll
+                    for (int nb = 0; nb < NB; nb++) mma<false>(s[nb], f, qf[nb][ks][0], qf[nb][ks][1]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < DP / 32; i++) {
+                    const int sw = DP == 64 ? ((r8 >> 1) & 1) << 1 : (r8 & 3) << 1;           // (row r8 + 8 has the same)
+                    const uint32_t at = kt + r8 * C::ROW + (((2 * i + (j >> 1)) ^ sw) * 16) + (j & 1) * 8;
+                    const uint2 top = lds64(at), bot = lds64(at + 8 * C::ROW);
+                    float part[NB][4];
+                    uint32_t f[4], g[4];
+                    halves(top.x, f[0], f[2]);
+                    halves(bot.x, f[1], f[3]);
+                    halves(top.y, g[0], g[2]);
+                    halves(bot.y, g[1], g[3]);
+                    const float k0 = __uint_as_float(lds32(prep + (i * PA_TILE + r8) * 4));
+                    const float k1 = __uint_as_float(lds32(prep + (i * PA_TILE + r8 + 8) * 4));
+#pragma unroll
+                    for (int nb = 0; nb < NB; nb++) {
+                        part[nb][0] = part[nb][1] = part[nb][2] = part[nb][3] = 0.0f;
+                        mma<true>(part[nb], f, qf[nb][2 * i][0], qf[nb][2 * i][1]);
+                        mma<true>(part[nb], g, qf[nb][2 * i + 1][0], qf[nb][2 * i + 1][1]);
+                        s[nb][0] = fmaf(k0, part[nb][0], s[nb][0]);
+                        s[nb][1] = fmaf(k0, part[nb][1], s[nb][1]);
+                        s[nb][2] = fmaf(k1, part[nb][2], s[nb][2]);
+                        s[nb][3] = fmaf(k1, part[nb][3], s[nb][3]);
+                    }
+                }
+            }
+            // weights
+            const bool in0 = (rows >> r8) & 1, in1 = (rows >> (r8 + 8)) & 1;
+            bool rises = false;
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    s[nb][e] = in0 ? s[nb][e] * to_s[nb][e] : -INFINITY;
+                    s[nb][2 + e] = in1 ? s[nb][2 + e] * to_s[nb][e] : -INFINITY;
+                    rises = rises || fmaxf(s[nb][e], s[nb][2 + e]) > m[nb][e];
+                }
+            if (__any_sync(FULL, rises)) {
+#pragma unroll
+                for (int nb = 0; nb < NB; nb++) {
+                    float keep[2];
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        float top = fmaxf(s[nb][e], s[nb][2 + e]);
+                        top = fmaxf(top, __shfl_xor_sync(FULL, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(FULL, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(FULL, top, 16));
+                        top = fmaxf(top, m[nb][e]);
+                        keep[e] = top == -INFINITY ? 1.0f : pow2(m[nb][e] - top);
+                        m[nb][e] = top;
+                        l[nb][e] *= keep[e];
+                    }
+#pragma unroll
+                    for (int d = 0; d < DP / 16; d++) {
+                        o[nb][d][0] *= keep[0];
+                        o[nb][d][1] *= keep[1];
+                        o[nb][d][2] *= keep[0];
+                        o[nb][d][3] *= keep[1];
+                    }
+                }
+            }
+            float p[NB][4];
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const float sub = m[nb][e] == -INFINITY ? 0.0f : FP8 ? m[nb][e] - 15.0f : m[nb][e];
+                    p[nb][e] = pow2(s[nb][e] - sub);
+                    p[nb][2 + e] = pow2(s[nb][2 + e] - sub);
+                    l[nb][e] += p[nb][e] + p[nb][2 + e];
+                }
+            // O^T += V^T P^T
+            if (!FP8) {
+                uint32_t b0[NB], b1[NB];
+#pragma unroll
+                for (int nb = 0; nb < NB; nb++) {
+                    b0[nb] = transposed(pack2<false>(p[nb][0], p[nb][1]));
+                    b1[nb] = transposed(pack2<false>(p[nb][2], p[nb][3]));
+                }
+                const int row = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+                for (int d = 0; d < DP / 16; d++) {
+                    uint32_t f[4];
+                    ldmatrix_t(f, vt + row * C::ROW + (((2 * d + ((lane >> 3) & 1)) ^ (row & 7)) * 16));
+#pragma unroll
+                    for (int nb = 0; nb < NB; nb++) mma<false>(o[nb][d], f, b0[nb], b1[nb]);
+                }
+            } else {
+                auto values = [&](auto wide_tag) {
+                    constexpr bool F16 = !decltype(wide_tag)::value;
+                    uint32_t b0[NB], b1[NB];
+#pragma unroll
+                    for (int nb = 0; nb < NB; nb++) {
+                        b0[nb] = transposed(pack2<F16>(p[nb][0], p[nb][1]));
+                        b1[nb] = transposed(pack2<F16>(p[nb][2], p[nb][3]));
+                    }
+#pragma unroll
+                    for (int i = 0; i < DP / 32; i++) {
+                        const uint32_t fac = prep + DP / 32 * PA_TILE * 4 + (i * PA_TILE + 2 * j) * 2;
+                        const uint32_t f0 = lds32(fac), f1 = lds32(fac + 16);
+                        uint32_t c[4];             // codes 4 r8 .. 4 r8 + 3 of the block, rows 2j, 2j + 1, 2j + 8, 2j + 9
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            const int row = 2 * j + (e & 1) + (e >> 1) * 8;
+                            const int sw = DP == 64 ? ((row >> 1) & 1) << 1 : ((row >> 1) & 3) << 1;
+                            c[e] = lds32(vt + row * C::ROW + (((2 * i + (r8 >> 2)) ^ sw) * 16) + (r8 & 3) * 4);
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {      // codes 4 r8 + 2h and 4 r8 + 2h + 1: rows r8 and r8 + 8 of the operand
+                            uint32_t f[4];
+                            const uint32_t sel = h ? 0x7362u : 0x5140u;
+                            halves(__byte_perm(c[0], c[1], sel), f[0], f[1]);
+                            halves(__byte_perm(c[2], c[3], sel), f[2], f[3]);
+                            if (!F16) {
+#pragma unroll
+                                for (int e = 0; e < 4; e++) f[e] = to_bf16x2(f[e]);
+                            }
+#pragma unroll
+                            for (int nb = 0; nb < NB; nb++)
+                                mma<F16>(o[nb][2 * i + h], f, times2<F16>(b0[nb], f0), times2<F16>(b1[nb], f1));
+                        }
+                    }
+                };
+                if (wide) values(std::true_type());
+                else values(std::false_type());
+            }
+            __syncwarp();
+            take = take + 1 == C::STAGES ? 0 : take + 1;
+            issue();
+        }
+
+        // -------- the warps' sums joined
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                l[nb][e] += __shfl_xor_sync(FULL, l[nb][e], 4);
+                l[nb][e] += __shfl_xor_sync(FULL, l[nb][e], 8);
+                l[nb][e] += __shfl_xor_sync(FULL, l[nb][e], 16);
+                if (r8 == 0) ml[warp * 8 * NB + nb * 8 + 2 * j + e] = make_float2(m[nb][e], l[nb][e]);
+            }
+        __syncthreads();
+        const bool cut = w.u > 0 || w.u1 < w.units;
+        const int slot = 2 * blockIdx.x + (w.u > 0 ? 0 : 1);
+        const float o_scale = FP8 ? pow2((float)(vref - 127)) : 1.0f;
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            float f[2], f2[2];
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int v = 0; v < PA_WARPS; v++) top = fmaxf(top, ml[v * 8 * NB + nb * 8 + 2 * j + e].x);
+                f[e] = top == -INFINITY ? 1.0f : pow2(m[nb][e] - top);
+                f2[e] = o_scale;
+            }
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+                float* const mine = join + warp * 8 * (C::HALF + 4);
+#pragma unroll
+                for (int d = 0; d < C::HALF / 16; d++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int at = FP8 ? (d / 2) * 32 + r8 * 4 + (d % 2) * 2 + (e >> 1) : d * 16 + r8 + (e >> 1) * 8;
+                        mine[(2 * j + (e & 1)) * (C::HALF + 4) + at] = o[nb][half * (C::HALF / 16) + d][e] * f[e & 1] * f2[e & 1];
+                    }
+                __syncthreads();
+                // eight elements of a head a thread and turn
+                for (int i = threadIdx.x; i < 8 * C::HALF / 8; i += PA_THREADS) {
+                    const int h = i / (C::HALF / 8), d = (i - h * (C::HALF / 8)) * 8;
+                    float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+                    for (int v = 0; v < PA_WARPS; v++) top = fmaxf(top, ml[v * 8 * NB + nb * 8 + h].x);
+#pragma unroll
+                    for (int v = 0; v < PA_WARPS; v++) {
+                        const float2 x = ml[v * 8 * NB + nb * 8 + h];
+                        sum += top == -INFINITY ? x.y : x.y * pow2(x.x - top);
+                    }
+                    float v8[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e++) v8[e] = 0.0f;
+#pragma unroll
+                    for (int v = 0; v < PA_WARPS; v++)
+#pragma unroll
+                        for (int e = 0; e < 8; e++) v8[e] += join[(v * 8 + h) * (C::HALF + 4) + d + e];
+                    const int head = h0 + nb * 8 + h, at = half * C::HALF + d;
+                    if (head < group && at < dim) {
+                        if (!cut) {
+                            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+                            for (int e = 0; e < 8; e++) v8[e] *= inv;
+                            const long long row = (long long)w.b * a.q_heads + kv * group + head;
+                            *reinterpret_cast<uint4*>(a.out + row * dim + at) = f32_to_bf16x8(v8);
+                            if (a.lse && at == 0)
+                                a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum) - (FP8 ? 15.0f : 0.0f)) * 0.69314718055994530942f;
+                        } else {
+                            float* const to = a.part + (long long)slot * C::SLOT + (nb * 8 + h) * DP + at;
+                            *reinterpret_cast<float4*>(to) = make_float4(v8[0], v8[1], v8[2], v8[3]);
+                            *reinterpret_cast<float4*>(to + 4) = make_float4(v8[4], v8[5], v8[6], v8[7]);
+                            if (at == 0) a.part_ml[slot * 8 * NB + nb * 8 + h] = make_float2(top, sum);
+                        }
+                    }
+                }
+                __syncthreads();
+            }
+        }
+        if (w.u == 0 && w.u1 < w.units && threadIdx.x == 0) {
+            // the block that has the pair's last unit: the largest whose stretch begins at or before it
+            const long long from = total * (blockIdx.x + 1) / ctas - (w.u1 - w.u), end = from + w.units - 1;
+            const int last = (int)(((end + 1) * ctas - 1) / total);
+            a.cut[blockIdx.x] = make_int4(w.b, w.pair, last - (int)blockIdx.x, 0);
+        }
+        w.next(a, pairs);
+    }
+    copies_wait<0>();
+}
+
+// Pairs that were cut: block (i, h) joins head h of the one that begins in block i of the first kernel.
+template <bool FP8, int DP, int NB>
+__global__ void __launch_bounds__(DP) attention_join_kernel(const __grid_constant__ AttnArgs a) {
+    using C = Cfg<FP8, DP, NB>;
+    pdl_wait();
+    const int4 cut = __ldcg(a.cut + blockIdx.x);
+    if (cut.x < 0) return;
+    const int kv = cut.y / a.tiles_of_heads, group = a.q_heads / a.c.heads, h = blockIdx.y;
+    const int head = (cut.y - kv * a.tiles_of_heads) * 8 * NB + h, d = threadIdx.x;
+    if (head >= group) return;
+    const int first = 2 * blockIdx.x + 1;           // its slot; the blocks after it have theirs at 2 (i + k)
+    float top = -INFINITY;
+    for (int k = 0; k <= cut.z; k++) top = fmaxf(top, __ldcg(a.part_ml + (k ? 2 * (blockIdx.x + k) : first) * 8 * NB + h).x);
+    float sum = 0.0f, v = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k <= cut.z; k++) {
+        const long long slot = k ? 2 * (blockIdx.x + k) : first;
+        const float2 x = __ldcg(a.part_ml + slot * 8 * NB + h);
+        const float y = d < a.c.dim ? __ldcg(a.part + slot * C::SLOT + h * DP + d) : 0.0f;
+        const float f = top == -INFINITY ? 1.0f : pow2(x.x - top);
+        sum += x.y * f;
+        v += y * f;
+    }
+    const long long row = (long long)cut.x * a.q_heads + kv * group + head;
+    if (d < a.c.dim) a.out[row * a.c.dim + d] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : v / sum);
+    if (a.lse && d == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum) - (FP8 ? 15.0f : 0.0f)) * 0.69314718055994530942f;
+}
+
+// Blocks of 8 query heads that a warp holds at once, by the group: what does not fit is another pass over the cache.
+int head_blocks(int group, int dim) { return group <= 8 ? 1 : group <= 16 || dim > 128 ? 2 : 4; }
+int padded(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+size_t part_bytes(int nb, int dp) { return (size_t)2 * PA_MAX_CTAS * 8 * nb * dp * sizeof(float); }
+size_t ml_bytes(int nb) { return (size_t)2 * PA_MAX_CTAS * 8 * nb * sizeof(float2); }
+
+template <bool FP8, int DP, int NB>
+moe_status launch(const AttnArgs& a, cudaStream_t s) {
+    using C = Cfg<FP8, DP, NB>;
+    static moe_host::PerDevice smem, sms_of;
+    if (!moe_host::allow_smem(attention_kernel<FP8, DP, NB>, C::SMEM, smem)) return MOE_ERR_CUDA;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    const int sms = sms_of.get(dev, [&] {
+        int n = 0;
+        return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
+    });
+    if (sms == 0) return MOE_ERR_CUDA;
+    // stretches of at least PA_MIN_UNITS units, as far as the table's room for positions tells
+    const long long room = (long long)a.M * a.c.page_size, pairs = (long long)a.B * a.c.heads * a.tiles_of_heads;
+    const long long units = (((a.window > 0 && a.window < room ? a.window : room) + PA_UNIT - 1) / PA_UNIT) * pairs;
+    const long long fill = a.whole ? pairs : (units + PA_MIN_UNITS - 1) / PA_MIN_UNITS;
+    long long ctas = (long long)sms * C::CTAS;
+    if (ctas > PA_MAX_CTAS) ctas = PA_MAX_CTAS;
+    if (ctas > fill) ctas = fill;
+    attention_kernel<FP8, DP, NB><<<(unsigned)ctas, PA_THREADS, C::SMEM, s>>>(a);
+    const moe_status st = moe_host::launch_status();
+    if (st != MOE_OK || a.whole) return st;
+    if (moe_host::launch_pdl(attention_join_kernel<FP8, DP, NB>, dim3((unsigned)ctas, 8 * NB), dim3(DP), 0, s, a) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return moe_host::launch_status();
+}
+
+template <bool FP8>
+moe_status launch_of(const AttnArgs& a, int nb, cudaStream_t s) {
+    switch (padded(a.c.dim)) {
+        case 64: return nb == 1 ? launch<FP8, 64, 1>(a, s) : nb == 2 ? launch<FP8, 64, 2>(a, s) : launch<FP8, 64, 4>(a, s);
+        case 128: return nb == 1 ? launch<FP8, 128, 1>(a, s) : nb == 2 ? launch<FP8, 128, 2>(a, s) : launch<FP8, 128, 4>(a, s);
+        default: return nb == 1 ? launch<FP8, 256, 1>(a, s) : launch<FP8, 256, 2>(a, s);
+    }
 }
 
 }  // namespace
 }  // namespace moe
 
 extern "C" size_t moe_paged_attention_workspace_size(int B, int q_heads, int heads, int dim) {
-    if (B < 0 || B > 65535 || heads < 1 || q_heads < 1 || q_heads % heads || dim < 1 || dim > MOE_CACHE_MAX_DIM) return 0;
-    return 256;
+    using namespace moe;
+    if (B < 0 || B > 65535 || heads < 1 || q_heads < 1 || q_heads % heads || q_heads / heads > 1024 || dim < 1 ||
+        dim > MOE_CACHE_MAX_DIM)
+        return 0;
+    const int nb = head_blocks(q_heads / heads, dim);
+    return part_bytes(nb, padded(dim)) + ml_bytes(nb) + PA_MAX_CTAS * sizeof(int4);
 }
 
 extern "C" moe_status moe_paged_attention(const void* q, long long q_stride, int B, int q_heads, const void* k_pages,
@@ -111,10 +803,16 @@ extern "C" moe_status moe_paged_attention(const void* q, long long q_stride, int
         !moe_host::aligned(table, 4) || !moe_host::aligned(lengths, 4) || !moe_host::aligned(workspace, 16))
         return MOE_ERR_ALIGNMENT;
     if (B == 0) return MOE_OK;
-    const AttnArgs a = {static_cast<const __nv_bfloat16*>(q), q_stride, B, q_heads, M, window, c, table, lengths, scale,
-                        static_cast<__nv_bfloat16*>(out), lse};
-    const dim3 grid(q_heads, B);
-    if (dtype == MOE_MXFP8) attention_kernel<true><<<grid, 32 * PA_WARPS, 0, moe_host::as_stream(stream)>>>(a);
-    else attention_kernel<false><<<grid, 32 * PA_WARPS, 0, moe_host::as_stream(stream)>>>(a);
-    return moe_host::launch_status();
+    const int nb = head_blocks(q_heads / heads, dim), dp = padded(dim);
+    AttnArgs a = {static_cast<const __nv_bfloat16*>(q), q_stride, B, q_heads, M, window, c, table, lengths, scale,
+                  static_cast<__nv_bfloat16*>(out), lse, nullptr, nullptr, nullptr, 0, 0};
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.part = reinterpret_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(ws + part_bytes(nb, dp));
+    a.cut = reinterpret_cast<int4*>(ws + part_bytes(nb, dp) + ml_bytes(nb));
+    a.tiles_of_heads = (q_heads / heads + 8 * nb - 1) / (8 * nb);
+    const long long room = (long long)M * page_size, most = window > 0 && window < room ? window : room;
+    a.whole = most <= 4 * PA_UNIT;
+    const cudaStream_t s = moe_host::as_stream(stream);
+    return dtype == MOE_MXFP8 ? launch_of<true>(a, nb, s) : launch_of<false>(a, nb, s);
 }
