@@ -33,10 +33,10 @@ namespace {
 
 constexpr int PA_WARPS = 4;
 constexpr int PA_THREADS = 32 * PA_WARPS;
-constexpr int PA_TILE = 16;                       // positions of a warp's tile
-constexpr int PA_UNIT = PA_WARPS * PA_TILE;       // positions of a block's unit
 constexpr int PA_MAX_CTAS = 512;                  // blocks at most: what the workspace has room for
-constexpr int PA_MIN_UNITS = 2;                   // of a block's stretch: a shorter one costs more to join than it saves
+constexpr int PA_BEGIN = 2;                       // units that beginning and ending a pair takes as long as
+constexpr int PA_MIN_UNITS = 4;                   // of a block's stretch: a shorter one costs more to join than it saves
+constexpr int PA_WHOLE = 256;                     // positions that a pair is not cut for
 constexpr int PA_SPREAD = 6;                      // exponents below the largest scale that fp16 weights take
 
 struct AttnArgs {
@@ -54,16 +54,20 @@ struct AttnArgs {
     int4* cut;                                    // [ctas] the pair that a block begins and does not end
     int tiles_of_heads;                           // tiles of 8 NB query heads in a group
     int whole;                                    // pairs are not cut: a stretch is of pairs, not of units
+    uint32_t page_mul, page_shift;                // p / page_size = (p page_mul >> 32) >> page_shift (0: pages of one)
 };
 
 template <bool FP8, int DP, int NB>
 struct Cfg {
     static constexpr int ROW = DP * (FP8 ? 1 : 2);             // bytes of a row in shared memory
     static constexpr int CHUNKS = ROW / 16;
-    static constexpr int KV = 2 * PA_TILE * ROW;
-    static constexpr int STAGE = KV + (FP8 ? 2 * PA_TILE * 16 : 0);   // and a 16-byte slot for each row's scales
+    static constexpr int SUB = ROW <= 128 && NB < 4 ? 2 : 1;   // 16-row operands of a tile: short rows go two at a time
+    static constexpr int TILE = 16 * SUB;                      // positions of a warp's tile
+    static constexpr int UNIT = PA_WARPS * TILE;               // positions of a block's unit
+    static constexpr int KV = 2 * TILE * ROW;
+    static constexpr int STAGE = KV + (FP8 ? 2 * TILE * 16 : 0);   // and a 16-byte slot for each row's scales
     static constexpr int STAGES = DP == 256 && !FP8 ? 3 : (96 * 1024 / PA_WARPS) / STAGE > 6 ? 6 : (96 * 1024 / PA_WARPS) / STAGE;
-    static constexpr int PREP = FP8 ? DP / 32 * PA_TILE * (4 + 2) : 0;  // a tile's scales as the products take them
+    static constexpr int PREP = FP8 ? DP / 32 * TILE * (4 + 2) : 0;  // a tile's scales as the products take them
     static constexpr int HALF = DP / 2;                        // elements joined at a time
     static constexpr int JOIN = PA_WARPS * 8 * (HALF + 4) * 4;
     static constexpr int ML = PA_WARPS * 8 * NB * 2 * 4;
@@ -78,6 +82,9 @@ __device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cv
 // 16 bytes (0: zeros instead) to shared memory.
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t to, const void* from, bool there) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
@@ -173,39 +180,45 @@ __device__ __forceinline__ void range_of(const AttnArgs& a, int b, int& first, i
     }
     first = a.window > 0 && n > a.window ? n - a.window : 0;
 }
-// Units of a pair of sequence b: one at least, which writes the output of a sequence without positions.
-__device__ __forceinline__ int units_of(int first, int n) { return max(1, (n - first + PA_UNIT - 1) / PA_UNIT); }
+// A pair's units: one at least, which writes the output of a sequence without positions. On the line that is cut into
+// stretches PA_BEGIN steps stand before them: what a block takes for a pair however few units it has of it.
+__device__ __forceinline__ int units_of(int first, int n, int unit) { return max(1, (n - first + unit - 1) / unit); }
 
 struct Walk {
-    int b, pair, first, n, units, u, u1;          // pair: of a sequence's key heads and tiles of query heads; [u, u1) to do
-    long long left;                               // units (whole: pairs) of the stretch from this segment on
+    int b, pair, first, n, units;                 // pair: of a sequence's key heads and tiles of query heads
+    int at, u, u1;                                // the segment's first step of the pair; its units [u, u1)
+    long long left;                               // steps (whole: pairs) of the stretch from this segment on
 
     __device__ __forceinline__ void cut(const AttnArgs& a) {
-        u1 = a.whole ? units : (int)min((long long)units, u + left);
+        u = a.whole ? 0 : max(0, at - PA_BEGIN);
+        u1 = a.whole ? units : (int)max(0ll, min((long long)units, at + left - PA_BEGIN));
     }
-    __device__ __forceinline__ void next(const AttnArgs& a, int pairs) {
-        left -= a.whole ? 1 : u1 - u;             // (u: where the segment began)
-        u = 0;
-        if (++pair == pairs) {
-            pair = 0;
-            if (++b < a.B && left > 0) {
+    // The next segment with a unit in it (left is 0 behind the last).
+    __device__ __forceinline__ void next(const AttnArgs& a, int pairs, int unit) {
+        do {
+            left -= a.whole ? 1 : min((long long)units + PA_BEGIN - at, left);
+            at = 0;
+            if (left <= 0) return;
+            if (++pair == pairs) {
+                pair = 0;
+                b++;
                 range_of(a, b, first, n);
-                units = units_of(first, n);
+                units = units_of(first, n, unit);
             }
-        }
-        cut(a);
+            cut(a);
+        } while (u1 <= u);
     }
 };
 
-// The first segment of this block's stretch, and in total the units (whole: pairs) of all. Every thread calls it.
-__device__ __forceinline__ Walk walk_begin(const AttnArgs& a, int pairs, long long* red, long long& total, int& ctas) {
+// The first segment of this block's stretch, and in total the steps (whole: pairs) of all. Every thread calls it.
+__device__ __forceinline__ Walk walk_begin(const AttnArgs& a, int pairs, int unit, long long* red, long long& total, int& ctas) {
     const int per = (a.B + PA_THREADS - 1) / PA_THREADS, b0 = min(a.B, per * (int)threadIdx.x), b1 = min(a.B, b0 + per);
     const int warp = threadIdx.x / 32;
     long long mine = 0;
     int first, n;
     for (int b = b0; b < b1; b++) {
         if (!a.whole) range_of(a, b, first, n);
-        mine += (long long)pairs * (a.whole ? 1 : units_of(first, n));
+        mine += (long long)pairs * (a.whole ? 1 : PA_BEGIN + units_of(first, n, unit));
     }
     long long upto = mine;
 #pragma unroll
@@ -237,12 +250,12 @@ __device__ __forceinline__ Walk walk_begin(const AttnArgs& a, int pairs, long lo
     if (from >= at && from < at + mine) {
         for (int b = b0; b < b1; b++) {
             range_of(a, b, first, n);
-            const int units = units_of(first, n);
-            const long long here = (long long)pairs * (a.whole ? 1 : units);
+            const int steps = a.whole ? 1 : PA_BEGIN + units_of(first, n, unit);
+            const long long here = (long long)pairs * steps;
             if (from < at + here) {
                 red[0] = b;
-                red[1] = a.whole ? from - at : (from - at) / units;
-                red[2] = a.whole ? 0 : (from - at) % units;
+                red[1] = (from - at) / steps;
+                red[2] = (from - at) % steps;
                 break;
             }
             at += here;
@@ -251,10 +264,11 @@ __device__ __forceinline__ Walk walk_begin(const AttnArgs& a, int pairs, long lo
     __syncthreads();
     w.b = (int)red[0];
     w.pair = (int)red[1];
-    w.u = (int)red[2];
+    w.at = (int)red[2];
     range_of(a, w.b, w.first, w.n);
-    w.units = units_of(w.first, w.n);
+    w.units = units_of(w.first, w.n, unit);
     w.cut(a);
+    if (w.u1 <= w.u) w.next(a, pairs, unit);
     __syncthreads();
     return w;
 }
@@ -274,79 +288,94 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
     float2* const ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(join) + C::JOIN);
     if (FP8) {
         for (int i = lane; i < C::PREP / 4; i += 32) sts32(prep + 4 * i, 0u);
-        for (int i = lane; i < C::STAGES * C::STAGE / 4; i += 32) sts32(ring + 4 * i, 0u);
         __syncwarp();
     }
     long long total;
     int ctas;
-    Walk w = walk_begin(a, pairs, reinterpret_cast<long long*>(join), total, ctas);
+    Walk w = walk_begin(a, pairs, C::UNIT, reinterpret_cast<long long*>(join), total, ctas);
     if (threadIdx.x == 0 && !a.whole) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
     pdl_trigger();
     if (w.left <= 0) return;
 
     // -------- the loading walk, a tile ahead of the copies: its rows' pages are on their way
     Walk ld = w;
-    int ld_u = w.u, ld_page = -1, ld_off = 0, ld_kv = 0;
+    int ld_u = w.u, ld_page = -1, ld_off = 0, ld_kv = w.pair / a.tiles_of_heads;
     bool ld_in = false, ld_more = true;
     auto look = [&]() {                            // finds the next tile of this warp that has a position
         ld_more = false;
         while (ld.left > 0) {
             if (ld_u == ld.u1) {
-                ld.next(a, pairs);
+                ld.next(a, pairs, C::UNIT);
                 ld_u = ld.u;
+                ld_kv = ld.pair / a.tiles_of_heads;
                 continue;
             }
-            const int t = ld.first + ld_u * PA_UNIT + warp * PA_TILE;
+            const int t = ld.first + ld_u * C::UNIT + warp * C::TILE;
             ld_u++;
             if (t >= ld.n) continue;
-            const int p = t + (lane & 15);
+            const int p = t + (lane & (C::TILE - 1));
             ld_in = p < ld.n;
-            const int col = p / a.c.page_size;
+            const int col = a.page_mul ? (int)(__umulhi((uint32_t)p, a.page_mul) >> a.page_shift) : p;
             ld_off = p - col * a.c.page_size;
-            ld_kv = ld.pair / a.tiles_of_heads;
             ld_page = ld_in ? __ldg(a.table + (long long)ld.b * a.M + col) : -1;
             ld_more = true;
             return;
         }
     };
+    const int ld_chunk = lane % C::CHUNKS, ld_row = lane / C::CHUNKS;
     int fill = 0;                                  // the stage that is filled next
     auto issue = [&]() {
         if (ld_more) {
             const bool ok = ld_in && (unsigned)ld_page < (unsigned)a.c.pages;
             if (ld_in && !ok) raise_device_error(MOE_DEVERR_BAD_ID);
             const long long line = ok ? ((long long)ld_page * a.c.heads + ld_kv) * a.c.page_size + ld_off : 0;
-            const unsigned rows = __ballot_sync(FULL, ok) & 0xffffu;
+            const long long row_at = line * row_bytes;
+            const unsigned rows = __ballot_sync(FULL, ok) & (C::TILE == 32 ? FULL : 0xffffu);
             const uint32_t at = ring + fill * C::STAGE;
-            constexpr int PER = 32 / C::CHUNKS > 0 ? 32 / C::CHUNKS : 1;      // rows that an instruction of the warp copies
-            const int chunk = lane % C::CHUNKS;
-            const bool in_row = chunk * 16 < row_bytes;
+            constexpr int PER = 32 / C::CHUNKS;    // rows that an instruction of the warp copies
+            const char* const kp = static_cast<const char*>(a.c.k) + ld_chunk * 16;
+            const char* const vp = static_cast<const char*>(a.c.v) + ld_chunk * 16;
+            const bool all = rows == (C::TILE == 32 ? FULL : 0xffffu) && row_bytes == C::ROW;
+            const unsigned mine = ld_chunk * 16 < row_bytes ? rows >> ld_row : 0u;
 #pragma unroll
-            for (int i = 0; i < PA_TILE / PER; i++) {
-                const int row = i * PER + lane / C::CHUNKS;
-                const long long from = __shfl_sync(FULL, line, row) * row_bytes + (in_row ? chunk * 16 : 0);
-                const bool there = in_row && ((rows >> row) & 1);
+            for (int i = 0; i < C::TILE / PER; i++) {
+                const int row = i * PER + ld_row;
+                const long long from = __shfl_sync(FULL, row_at, row);
                 int kx, vx;                        // the chunk's place, so that the fragments' reads meet all banks
                 if (!FP8) {
-                    kx = vx = chunk ^ (row & 7);
+                    kx = vx = ld_chunk ^ (row & 7);
                 } else if (DP == 64) {
-                    kx = vx = chunk ^ (((row >> 1) & 1) << 1);
+                    kx = vx = ld_chunk ^ (((row >> 1) & 1) << 1);
                 } else {
-                    kx = chunk ^ ((row & 3) << 1);
-                    vx = chunk ^ (((row >> 1) & 3) << 1);
+                    kx = ld_chunk ^ ((row & 3) << 1);
+                    vx = ld_chunk ^ (((row >> 1) & 3) << 1);
                 }
-                copy16(at + row * C::ROW + kx * 16, static_cast<const char*>(a.c.k) + from, there);
-                copy16(at + PA_TILE * C::ROW + row * C::ROW + vx * 16, static_cast<const char*>(a.c.v) + from, there);
+                const uint32_t kt = at + row * C::ROW + kx * 16, vt = at + (C::TILE + row) * C::ROW + vx * 16;
+                if (all) {
+                    copy16(kt, kp + from);
+                    copy16(vt, vp + from);
+                } else {
+                    // (a chunk that is not there is zeros, and its address the pool's first)
+                    const bool there = (mine >> (i * PER)) & 1;
+                    copy16(kt, there ? kp + from : static_cast<const char*>(a.c.k), there);
+                    copy16(vt, there ? vp + from : static_cast<const char*>(a.c.v), there);
+                }
             }
             if (FP8) {
-                // a lane per row and side: the words that hold the row's scales, and where in them they begin
-                const uint8_t* const base = (lane < 16 ? a.c.k_scales : a.c.v_scales) + line * row_scales;
-                const int skip = (int)(reinterpret_cast<uintptr_t>(base) & 3);
-                const uint32_t slot = at + C::KV + lane * 16;
-                const int words = (skip + row_scales + 3) / 4;
+                // a lane's row: the words that hold its scales, and where in them they begin
+                const long long scales_at = line * row_scales;
 #pragma unroll
-                for (int i = 0; i < (DP / 32 + 6) / 4; i++)
-                    if (i < words) copy4(slot + 4 * i, base - skip + 4 * i, ok);
-                sts32(slot + 12, ok ? 8u * skip : 0u);
+                for (int x = 0; x < C::SUB; x++) {
+                    const bool is_v = C::SUB == 2 ? x == 1 : lane >= 16;
+                    const uint8_t* const base = (is_v ? a.c.v_scales : a.c.k_scales) + scales_at;
+                    const int skip = (int)(reinterpret_cast<uintptr_t>(base) & 3);
+                    const uint32_t slot = at + C::KV + (x * 32 + lane) * 16;
+                    const int words = (skip + row_scales + 3) / 4;
+#pragma unroll
+                    for (int i = 0; i < (DP / 32 + 6) / 4; i++)
+                        if (i < words) copy4(slot + 4 * i, base - skip + 4 * i, ok);
+                    sts32(slot + 12, ok ? 8u * skip : 0u);
+                }
             }
             if (lane == 0) seen[fill] = rows;
             look();
@@ -359,12 +388,9 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
     for (int i = 0; i < C::STAGES; i++) issue();
 
     const float log2_scale = a.scale * 1.44269504088896340736f;
-    int take = 0;
-    while (w.left > 0) {
-        // -------- the heads of this segment
+    uint32_t qf[NB][DP / 16][2];
+    auto load_q = [&]() {                          // the heads of a segment
         const int kv = w.pair / a.tiles_of_heads, h0 = (w.pair - kv * a.tiles_of_heads) * 8 * NB;
-        uint32_t qf[NB][DP / 16][2];
-        float to_s[NB][2];                         // from the products to scores in powers of two, of columns 2j and 2j + 1
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
             const int h = h0 + nb * 8 + r8;
@@ -378,6 +404,14 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                     qf[nb][ks][e] = h < group && d < dim ? __ldg(src + d / 2) : 0u;
                 }
             }
+        }
+    };
+    load_q();
+    int take = 0;
+    while (w.left > 0) {
+        float to_s[NB][2];                         // from the products to scores in powers of two, of columns 2j and 2j + 1
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
             to_s[nb][0] = to_s[nb][1] = log2_scale;
             if (FP8) {
                 float top = 0.0f;
@@ -418,27 +452,31 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
 #pragma unroll
                 for (int e = 0; e < 4; e++) o[nb][d][e] = 0.0f;
         }
-        const int my_end = min(w.u1, (max(0, w.n - w.first - warp * PA_TILE) + PA_UNIT - 1) / PA_UNIT);
+        const int my_end = min(w.u1, (max(0, w.n - w.first - warp * C::TILE) + C::UNIT - 1) / C::UNIT);
 #pragma unroll 1
         for (int u = w.u; u < my_end; u++) {
             copies_wait<C::STAGES - 1>();
             __syncwarp();
-            const uint32_t kt = ring + take * C::STAGE, vt = kt + PA_TILE * C::ROW;
+            const uint32_t kt = ring + take * C::STAGE, vt = kt + C::TILE * C::ROW;
             const uint32_t rows = seen[take];
             bool wide = false;                     // (MXFP8) this tile's scales span more than fp16 weights take
             if (FP8) {
-                // the tile's scales: a lane per row and side
-                const uint4 slot = lds128(kt + C::KV + lane * 16);
-                const uint32_t s0 = __funnelshift_r(slot.x, slot.y, slot.w), s1 = __funnelshift_r(slot.y, slot.z, slot.w);
-                const bool is_v = lane >= 16, here = (rows >> (lane & 15)) & 1;
-                uint32_t most = 0u, least = 255u;
-                uint32_t byte[DP / 32];
+                // the tile's scales, a lane a row (and, of 16 rows, a side)
+                uint32_t most = 0u, least = 255u, byte[C::SUB][DP / 32];
+                const bool here = (rows >> (lane & (C::TILE - 1))) & 1;
 #pragma unroll
-                for (int i = 0; i < DP / 32; i++) {
-                    byte[i] = ((i < 4 ? s0 : s1) >> (8 * (i & 3))) & 0xffu;
-                    if (is_v && here && i < row_scales) {
-                        if (byte[i] != 255u) most = max(most, byte[i]);
-                        least = min(least, byte[i]);
+                for (int x = 0; x < C::SUB; x++) {
+                    const uint4 slot = lds128(kt + C::KV + (x * 32 + lane) * 16);
+                    const uint32_t s0 = __funnelshift_r(slot.x, slot.y, slot.w);
+                    const uint32_t s1 = DP == 256 ? __funnelshift_r(slot.y, slot.z, slot.w) : 0u;
+                    const bool is_v = C::SUB == 2 ? x == 1 : lane >= 16;
+#pragma unroll
+                    for (int i = 0; i < DP / 32; i++) {
+                        byte[x][i] = ((i < 4 ? s0 : s1) >> (8 * (i & 3))) & 0xffu;
+                        if (is_v && here && i < row_scales) {
+                            if (byte[x][i] != 255u) most = max(most, byte[x][i]);
+                            least = min(least, byte[x][i]);
+                        }
                     }
                 }
                 most = __reduce_max_sync(FULL, most);
@@ -454,80 +492,94 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                     vref = (int)most;
                 }
                 wide = vref - (int)least > PA_SPREAD;
-                __syncwarp();                      // (nobody reads the last tile's scales any more)
 #pragma unroll
-                for (int i = 0; i < DP / 32; i++) {
-                    if (i >= row_scales) continue;
-                    if (!is_v) {
-                        sts32(prep + (i * PA_TILE + lane) * 4, __float_as_uint(e8m0_value(byte[i])));
-                    } else {
-                        const int x = (int)byte[i] - vref;
-                        uint32_t f = wide ? (uint32_t)max(0, 127 + x) << 7 : (uint32_t)max(0, 15 + x) << 10;
-                        if (byte[i] == 255u) f = wide ? 0x7fc0u : 0x7e00u;
-                        sts16(prep + DP / 32 * PA_TILE * 4 + (i * PA_TILE + (lane - 16)) * 2, f);
+                for (int x = 0; x < C::SUB; x++) {
+                    const bool is_v = C::SUB == 2 ? x == 1 : lane >= 16;
+                    const int row = lane & (C::TILE - 1);
+#pragma unroll
+                    for (int i = 0; i < DP / 32; i++) {
+                        if (i >= row_scales) continue;
+                        if (!is_v) {
+                            sts32(prep + (i * C::TILE + row) * 4, __float_as_uint(e8m0_value(byte[x][i])));
+                        } else {
+                            const int y = (int)byte[x][i] - vref;
+                            uint32_t f = wide ? (uint32_t)max(0, 127 + y) << 7 : (uint32_t)max(0, 15 + y) << 10;
+                            if (byte[x][i] == 255u) f = wide ? 0x7fc0u : 0x7e00u;
+                            sts16(prep + DP / 32 * C::TILE * 4 + (i * C::TILE + row) * 2, f);
+                        }
                     }
                 }
                 __syncwarp();
             }
             // S^T = K Q^T
-            float s[NB][4];
+            float s[C::SUB][NB][4];
 #pragma unroll
-            for (int nb = 0; nb < NB; nb++)
+            for (int x = 0; x < C::SUB; x++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) s[nb][e] = 0.0f;
+                for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) s[x][nb][e] = 0.0f;
             if (!FP8) {
                 const int row = lane & 15;
 #pragma unroll
-                for (int ks = 0; ks < DP / 16; ks++) {
-                    uint32_t f[4];
-                    ldmatrix(f, kt + row * C::ROW + (((2 * ks + (lane >> 4)) ^ (row & 7)) * 16));
+                for (int ks = 0; ks < DP / 16; ks++)
 #pragma unroll
-                    for (int nb = 0; nb < NB; nb++) mma<false>(s[nb], f, qf[nb][ks][0], qf[nb][ks][1]);
-                }
-            } else {
+                    for (int x = 0; x < C::SUB; x++) {
+                        uint32_t f[4];
+                        ldmatrix(f, kt + (x * 16 + row) * C::ROW + (((2 * ks + (lane >> 4)) ^ (row & 7)) * 16));
 #pragma unroll
-                for (int i = 0; i < DP / 32; i++) {
-                    const int sw = DP == 64 ? ((r8 >> 1) & 1) << 1 : (r8 & 3) << 1;           // (row r8 + 8 has the same)
-                    const uint32_t at = kt + r8 * C::ROW + (((2 * i + (j >> 1)) ^ sw) * 16) + (j & 1) * 8;
-                    const uint2 top = lds64(at), bot = lds64(at + 8 * C::ROW);
-                    float part[NB][4];
-                    uint32_t f[4], g[4];
-                    halves(top.x, f[0], f[2]);
-                    halves(bot.x, f[1], f[3]);
-                    halves(top.y, g[0], g[2]);
-                    halves(bot.y, g[1], g[3]);
-                    const float k0 = __uint_as_float(lds32(prep + (i * PA_TILE + r8) * 4));
-                    const float k1 = __uint_as_float(lds32(prep + (i * PA_TILE + r8 + 8) * 4));
-#pragma unroll
-                    for (int nb = 0; nb < NB; nb++) {
-                        part[nb][0] = part[nb][1] = part[nb][2] = part[nb][3] = 0.0f;
-                        mma<true>(part[nb], f, qf[nb][2 * i][0], qf[nb][2 * i][1]);
-                        mma<true>(part[nb], g, qf[nb][2 * i + 1][0], qf[nb][2 * i + 1][1]);
-                        s[nb][0] = fmaf(k0, part[nb][0], s[nb][0]);
-                        s[nb][1] = fmaf(k0, part[nb][1], s[nb][1]);
-                        s[nb][2] = fmaf(k1, part[nb][2], s[nb][2]);
-                        s[nb][3] = fmaf(k1, part[nb][3], s[nb][3]);
+                        for (int nb = 0; nb < NB; nb++) mma<false>(s[x][nb], f, qf[nb][ks][0], qf[nb][ks][1]);
                     }
-                }
+            } else {
+                const int sw = DP == 64 ? ((r8 >> 1) & 1) << 1 : (r8 & 3) << 1;               // (row r8 + 8 has the same)
+#pragma unroll
+                for (int i = 0; i < DP / 32; i++)
+#pragma unroll
+                    for (int x = 0; x < C::SUB; x++) {
+                        const uint32_t at = kt + (x * 16 + r8) * C::ROW + (((2 * i + (j >> 1)) ^ sw) * 16) + (j & 1) * 8;
+                        const uint2 top = lds64(at), bot = lds64(at + 8 * C::ROW);
+                        float part[NB][4];
+                        uint32_t f[4], g[4];
+                        halves(top.x, f[0], f[2]);
+                        halves(bot.x, f[1], f[3]);
+                        halves(top.y, g[0], g[2]);
+                        halves(bot.y, g[1], g[3]);
+                        const float k0 = __uint_as_float(lds32(prep + (i * C::TILE + x * 16 + r8) * 4));
+                        const float k1 = __uint_as_float(lds32(prep + (i * C::TILE + x * 16 + r8 + 8) * 4));
+#pragma unroll
+                        for (int nb = 0; nb < NB; nb++) {
+                            part[nb][0] = part[nb][1] = part[nb][2] = part[nb][3] = 0.0f;
+                            mma<true>(part[nb], f, qf[nb][2 * i][0], qf[nb][2 * i][1]);
+                            mma<true>(part[nb], g, qf[nb][2 * i + 1][0], qf[nb][2 * i + 1][1]);
+                            s[x][nb][0] = fmaf(k0, part[nb][0], s[x][nb][0]);
+                            s[x][nb][1] = fmaf(k0, part[nb][1], s[x][nb][1]);
+                            s[x][nb][2] = fmaf(k1, part[nb][2], s[x][nb][2]);
+                            s[x][nb][3] = fmaf(k1, part[nb][3], s[x][nb][3]);
+                        }
+                    }
             }
             // weights
-            const bool in0 = (rows >> r8) & 1, in1 = (rows >> (r8 + 8)) & 1;
             bool rises = false;
 #pragma unroll
-            for (int nb = 0; nb < NB; nb++)
+            for (int x = 0; x < C::SUB; x++) {
+                const bool in0 = (rows >> (x * 16 + r8)) & 1, in1 = (rows >> (x * 16 + r8 + 8)) & 1;
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    s[nb][e] = in0 ? s[nb][e] * to_s[nb][e] : -INFINITY;
-                    s[nb][2 + e] = in1 ? s[nb][2 + e] * to_s[nb][e] : -INFINITY;
-                    rises = rises || fmaxf(s[nb][e], s[nb][2 + e]) > m[nb][e];
-                }
+                for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        s[x][nb][e] = in0 ? s[x][nb][e] * to_s[nb][e] : -INFINITY;
+                        s[x][nb][2 + e] = in1 ? s[x][nb][2 + e] * to_s[nb][e] : -INFINITY;
+                        rises = rises || fmaxf(s[x][nb][e], s[x][nb][2 + e]) > m[nb][e];
+                    }
+            }
             if (__any_sync(FULL, rises)) {
 #pragma unroll
                 for (int nb = 0; nb < NB; nb++) {
                     float keep[2];
 #pragma unroll
                     for (int e = 0; e < 2; e++) {
-                        float top = fmaxf(s[nb][e], s[nb][2 + e]);
+                        float top = fmaxf(s[0][nb][e], s[0][nb][2 + e]);
+                        if (C::SUB == 2) top = fmaxf(top, fmaxf(s[C::SUB - 1][nb][e], s[C::SUB - 1][nb][2 + e]));
                         top = fmaxf(top, __shfl_xor_sync(FULL, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(FULL, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(FULL, top, 16));
@@ -545,65 +597,78 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                     }
                 }
             }
-            float p[NB][4];
 #pragma unroll
             for (int nb = 0; nb < NB; nb++)
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
                     const float sub = m[nb][e] == -INFINITY ? 0.0f : FP8 ? m[nb][e] - 15.0f : m[nb][e];
-                    p[nb][e] = pow2(s[nb][e] - sub);
-                    p[nb][2 + e] = pow2(s[nb][2 + e] - sub);
-                    l[nb][e] += p[nb][e] + p[nb][2 + e];
+#pragma unroll
+                    for (int x = 0; x < C::SUB; x++) {
+                        s[x][nb][e] = pow2(s[x][nb][e] - sub);
+                        s[x][nb][2 + e] = pow2(s[x][nb][2 + e] - sub);
+                        l[nb][e] += s[x][nb][e] + s[x][nb][2 + e];
+                    }
                 }
             // O^T += V^T P^T
             if (!FP8) {
-                uint32_t b0[NB], b1[NB];
-#pragma unroll
-                for (int nb = 0; nb < NB; nb++) {
-                    b0[nb] = transposed(pack2<false>(p[nb][0], p[nb][1]));
-                    b1[nb] = transposed(pack2<false>(p[nb][2], p[nb][3]));
-                }
                 const int row = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
-                for (int d = 0; d < DP / 16; d++) {
-                    uint32_t f[4];
-                    ldmatrix_t(f, vt + row * C::ROW + (((2 * d + ((lane >> 3) & 1)) ^ (row & 7)) * 16));
+                for (int x = 0; x < C::SUB; x++) {
+                    uint32_t b0[NB], b1[NB];
 #pragma unroll
-                    for (int nb = 0; nb < NB; nb++) mma<false>(o[nb][d], f, b0[nb], b1[nb]);
+                    for (int nb = 0; nb < NB; nb++) {
+                        b0[nb] = transposed(pack2<false>(s[x][nb][0], s[x][nb][1]));
+                        b1[nb] = transposed(pack2<false>(s[x][nb][2], s[x][nb][3]));
+                    }
+#pragma unroll
+                    for (int d = 0; d < DP / 16; d++) {
+                        uint32_t f[4];
+                        ldmatrix_t(f, vt + (x * 16 + row) * C::ROW + (((2 * d + ((lane >> 3) & 1)) ^ (row & 7)) * 16));
+#pragma unroll
+                        for (int nb = 0; nb < NB; nb++) mma<false>(o[nb][d], f, b0[nb], b1[nb]);
+                    }
                 }
             } else {
                 auto values = [&](auto wide_tag) {
                     constexpr bool F16 = !decltype(wide_tag)::value;
-                    uint32_t b0[NB], b1[NB];
 #pragma unroll
-                    for (int nb = 0; nb < NB; nb++) {
-                        b0[nb] = transposed(pack2<F16>(p[nb][0], p[nb][1]));
-                        b1[nb] = transposed(pack2<F16>(p[nb][2], p[nb][3]));
-                    }
+                    for (int x = 0; x < C::SUB; x++) {
+                        uint32_t b0[NB], b1[NB];
 #pragma unroll
-                    for (int i = 0; i < DP / 32; i++) {
-                        const uint32_t fac = prep + DP / 32 * PA_TILE * 4 + (i * PA_TILE + 2 * j) * 2;
-                        const uint32_t f0 = lds32(fac), f1 = lds32(fac + 16);
-                        uint32_t c[4];             // codes 4 r8 .. 4 r8 + 3 of the block, rows 2j, 2j + 1, 2j + 8, 2j + 9
-#pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            const int row = 2 * j + (e & 1) + (e >> 1) * 8;
-                            const int sw = DP == 64 ? ((row >> 1) & 1) << 1 : ((row >> 1) & 3) << 1;
-                            c[e] = lds32(vt + row * C::ROW + (((2 * i + (r8 >> 2)) ^ sw) * 16) + (r8 & 3) * 4);
+                        for (int nb = 0; nb < NB; nb++) {
+                            b0[nb] = transposed(pack2<F16>(s[x][nb][0], s[x][nb][1]));
+                            b1[nb] = transposed(pack2<F16>(s[x][nb][2], s[x][nb][3]));
                         }
 #pragma unroll
-                        for (int h = 0; h < 2; h++) {      // codes 4 r8 + 2h and 4 r8 + 2h + 1: rows r8 and r8 + 8 of the operand
-                            uint32_t f[4];
-                            const uint32_t sel = h ? 0x7362u : 0x5140u;
-                            halves(__byte_perm(c[0], c[1], sel), f[0], f[1]);
-                            halves(__byte_perm(c[2], c[3], sel), f[2], f[3]);
-                            if (!F16) {
+                        for (int i = 0; i < DP / 32; i++) {
+                            const uint32_t fac = prep + DP / 32 * C::TILE * 4 + (i * C::TILE + x * 16 + 2 * j) * 2;
+                            const uint32_t f0 = lds32(fac), f1 = lds32(fac + 16);
+                            uint32_t c[4];         // codes 4 r8 .. 4 r8 + 3 of the block, rows 2j, 2j + 1, 2j + 8, 2j + 9
 #pragma unroll
-                                for (int e = 0; e < 4; e++) f[e] = to_bf16x2(f[e]);
+                            for (int e = 0; e < 4; e++) {
+                                const int row = 2 * j + (e & 1) + (e >> 1) * 8;
+                                const int sw = DP == 64 ? ((row >> 1) & 1) << 1 : ((row >> 1) & 3) << 1;
+                                c[e] = lds32(vt + (x * 16 + row) * C::ROW + (((2 * i + (r8 >> 2)) ^ sw) * 16) + (r8 & 3) * 4);
+                            }
+                            uint32_t p0[NB], p1[NB];
+#pragma unroll
+                            for (int nb = 0; nb < NB; nb++) {
+                                p0[nb] = times2<F16>(b0[nb], f0);
+                                p1[nb] = times2<F16>(b1[nb], f1);
                             }
 #pragma unroll
-                            for (int nb = 0; nb < NB; nb++)
-                                mma<F16>(o[nb][2 * i + h], f, times2<F16>(b0[nb], f0), times2<F16>(b1[nb], f1));
+                            for (int h = 0; h < 2; h++) {  // codes 4 r8 + 2h and 4 r8 + 2h + 1: rows r8 and r8 + 8 of the operand
+                                uint32_t f[4];
+                                const uint32_t sel = h ? 0x7362u : 0x5140u;
+                                halves(__byte_perm(c[0], c[1], sel), f[0], f[1]);
+                                halves(__byte_perm(c[2], c[3], sel), f[2], f[3]);
+                                if (!F16) {
+#pragma unroll
+                                    for (int e = 0; e < 4; e++) f[e] = to_bf16x2(f[e]);
+                                }
+#pragma unroll
+                                for (int nb = 0; nb < NB; nb++) mma<F16>(o[nb][2 * i + h], f, p0[nb], p1[nb]);
+                            }
                         }
                     }
                 };
@@ -615,7 +680,10 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
             issue();
         }
 
-        // -------- the warps' sums joined
+        // -------- the warps' sums joined, while the next segment's heads are on their way
+        const Walk now = w;
+        w.next(a, pairs, C::UNIT);
+        if (w.left > 0) load_q();
 #pragma unroll
         for (int nb = 0; nb < NB; nb++)
 #pragma unroll
@@ -626,8 +694,9 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                 if (r8 == 0) ml[warp * 8 * NB + nb * 8 + 2 * j + e] = make_float2(m[nb][e], l[nb][e]);
             }
         __syncthreads();
-        const bool cut = w.u > 0 || w.u1 < w.units;
-        const int slot = 2 * blockIdx.x + (w.u > 0 ? 0 : 1);
+        const int kv = now.pair / a.tiles_of_heads, h0 = (now.pair - kv * a.tiles_of_heads) * 8 * NB;
+        const bool cut = now.u > 0 || now.u1 < now.units;
+        const int slot = 2 * blockIdx.x + (now.u > 0 ? 0 : 1);
         const float o_scale = FP8 ? pow2((float)(vref - 127)) : 1.0f;
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
@@ -675,7 +744,7 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
                             for (int e = 0; e < 8; e++) v8[e] *= inv;
-                            const long long row = (long long)w.b * a.q_heads + kv * group + head;
+                            const long long row = (long long)now.b * a.q_heads + kv * group + head;
                             *reinterpret_cast<uint4*>(a.out + row * dim + at) = f32_to_bf16x8(v8);
                             if (a.lse && at == 0)
                                 a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum) - (FP8 ? 15.0f : 0.0f)) * 0.69314718055994530942f;
@@ -690,13 +759,12 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                 __syncthreads();
             }
         }
-        if (w.u == 0 && w.u1 < w.units && threadIdx.x == 0) {
-            // the block that has the pair's last unit: the largest whose stretch begins at or before it
-            const long long from = total * (blockIdx.x + 1) / ctas - (w.u1 - w.u), end = from + w.units - 1;
+        if (now.u == 0 && now.u1 < now.units && threadIdx.x == 0) {
+            // the block that has the pair's last step: the largest whose stretch begins at or before it
+            const long long begin = total * (blockIdx.x + 1) / ctas - now.left - now.at, end = begin + PA_BEGIN + now.units - 1;
             const int last = (int)(((end + 1) * ctas - 1) / total);
-            a.cut[blockIdx.x] = make_int4(w.b, w.pair, last - (int)blockIdx.x, 0);
+            a.cut[blockIdx.x] = make_int4(now.b, now.pair, last - (int)blockIdx.x, 0);
         }
-        w.next(a, pairs);
     }
     copies_wait<0>();
 }
@@ -712,14 +780,17 @@ __global__ void __launch_bounds__(DP) attention_join_kernel(const __grid_constan
     const int head = (cut.y - kv * a.tiles_of_heads) * 8 * NB + h, d = threadIdx.x;
     if (head >= group) return;
     const int first = 2 * blockIdx.x + 1;           // its slot; the blocks after it have theirs at 2 (i + k)
+    const int parts = cut.z + 1;
+    auto slot_of = [&](int k) { return (long long)(k ? 2 * (blockIdx.x + k) : first); };
     float top = -INFINITY;
-    for (int k = 0; k <= cut.z; k++) top = fmaxf(top, __ldcg(a.part_ml + (k ? 2 * (blockIdx.x + k) : first) * 8 * NB + h).x);
+    for (int k = lane_id(); k < parts; k += 32) top = fmaxf(top, __ldcg(a.part_ml + slot_of(k) * 8 * NB + h).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
     float sum = 0.0f, v = 0.0f;
-#pragma unroll 4
-    for (int k = 0; k <= cut.z; k++) {
-        const long long slot = k ? 2 * (blockIdx.x + k) : first;
-        const float2 x = __ldcg(a.part_ml + slot * 8 * NB + h);
-        const float y = d < a.c.dim ? __ldcg(a.part + slot * C::SLOT + h * DP + d) : 0.0f;
+#pragma unroll 8
+    for (int k = 0; k < parts; k++) {
+        const float2 x = __ldcg(a.part_ml + slot_of(k) * 8 * NB + h);
+        const float y = d < a.c.dim ? __ldcg(a.part + slot_of(k) * C::SLOT + h * DP + d) : 0.0f;
         const float f = top == -INFINITY ? 1.0f : pow2(x.x - top);
         sum += x.y * f;
         v += y * f;
@@ -748,10 +819,10 @@ moe_status launch(const AttnArgs& a, cudaStream_t s) {
         return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
     });
     if (sms == 0) return MOE_ERR_CUDA;
-    // stretches of at least PA_MIN_UNITS units, as far as the table's room for positions tells
+    // stretches of at least PA_MIN_UNITS steps, as far as the table's room for positions tells
     const long long room = (long long)a.M * a.c.page_size, pairs = (long long)a.B * a.c.heads * a.tiles_of_heads;
-    const long long units = (((a.window > 0 && a.window < room ? a.window : room) + PA_UNIT - 1) / PA_UNIT) * pairs;
-    const long long fill = a.whole ? pairs : (units + PA_MIN_UNITS - 1) / PA_MIN_UNITS;
+    const long long steps = (((a.window > 0 && a.window < room ? a.window : room) + C::UNIT - 1) / C::UNIT + PA_BEGIN) * pairs;
+    const long long fill = a.whole ? pairs : (steps + PA_MIN_UNITS - 1) / PA_MIN_UNITS;
     long long ctas = (long long)sms * C::CTAS;
     if (ctas > PA_MAX_CTAS) ctas = PA_MAX_CTAS;
     if (ctas > fill) ctas = fill;
@@ -805,14 +876,20 @@ extern "C" moe_status moe_paged_attention(const void* q, long long q_stride, int
     if (B == 0) return MOE_OK;
     const int nb = head_blocks(q_heads / heads, dim), dp = padded(dim);
     AttnArgs a = {static_cast<const __nv_bfloat16*>(q), q_stride, B, q_heads, M, window, c, table, lengths, scale,
-                  static_cast<__nv_bfloat16*>(out), lse, nullptr, nullptr, nullptr, 0, 0};
+                  static_cast<__nv_bfloat16*>(out), lse, nullptr, nullptr, nullptr, 0, 0, 0, 0};
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.part = reinterpret_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(ws + part_bytes(nb, dp));
     a.cut = reinterpret_cast<int4*>(ws + part_bytes(nb, dp) + ml_bytes(nb));
     a.tiles_of_heads = (q_heads / heads + 8 * nb - 1) / (8 * nb);
     const long long room = (long long)M * page_size, most = window > 0 && window < room ? window : room;
-    a.whole = most <= 4 * PA_UNIT;
+    a.whole = most <= PA_WHOLE;
+    // division by the page size: with 2^(k-1) < page_size <= 2^k and mul = ceil(2^(31+k) / page_size), p mul / 2^(31+k)
+    // exceeds p / page_size by less than 2^31 2^k / 2^(31+k) / page_size = 1 / page_size for p < 2^31
+    int k = 0;
+    while ((1 << k) < page_size) k++;
+    a.page_mul = k ? (uint32_t)(((1ull << (31 + k)) + (uint32_t)page_size - 1) / (uint32_t)page_size) : 0u;
+    a.page_shift = k ? k - 1 : 0;
     const cudaStream_t s = moe_host::as_stream(stream);
     return dtype == MOE_MXFP8 ? launch_of<true>(a, nb, s) : launch_of<false>(a, nb, s);
 }
