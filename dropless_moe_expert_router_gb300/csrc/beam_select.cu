@@ -3,13 +3,17 @@
 // For every beam lse = ln sum exp(logits), and over a search's beams the K largest score + (logit - lse). The logits
 // are read once: DRAM bounds large vocabularies, two launches small ones. Two kernels:
 //
-// 1. A block holds a chunk of one beam's logits in registers (8192 fp32, 16384 bf16). It leaves the chunk's maximum and sum of
-//    exponentials, and its K largest logits in order (within a beam the order does not depend on lse). For these it
-//    takes the K-th largest of the maxima of 64 groups of four threads, found bit by bit by one warp: no fewer than K logits are
-//    that large, and few more as a rule, which are ranked against each other. Where they are more than the buffer
-//    holds, the K-th largest logit itself is found the same way, and of what ties with it the first ones in order.
-// 2. A block per search, set up while the first kernel runs, joins the sums in 64 bits and the chunks' lists: it drops
-//    what fp32 bounds show to be behind K others, and ranks the rest by its value in 64 bits.
+// 1. All rows' logits, in units of 2048 16-byte pieces, are cut into one equal stretch per block. Every thread copies its
+//    own eight pieces of a unit to a ring in shared memory, two units ahead and across rows, so loads are in flight all
+//    the time and the code is one short loop (eight pieces in registers in line took half as long again: it does not
+//    stay in the instruction cache). For each row of its stretch a block leaves the maximum, the sum of exponentials and its K largest logits in order (within a beam the
+//    order does not depend on lse). What is below a threshold is passed over a piece at a time by the piece's maximum.
+//    The first threshold is the K-th largest of the maxima of 64 groups of four threads in the row's first unit, found bit by bit by one
+//    warp: no fewer than K logits are that large. Later ones are the K-th largest found so far. Where more than the buffer
+//    holds pass, the unit's K-th largest itself is found bit by bit, and of what ties with it the first ones are taken in order.
+// 2. A block per search, set up while the first kernel runs, joins the sums and the lists: it drops
+//    what fp32 bounds show to be behind K others, and ranks the rest by its value in two floats, of 46 bits or more
+//    (this device's 64-bit units are slow: a logarithm and the sums took 5 us in them).
 #include "common.cuh"
 
 #include <math.h>
@@ -18,11 +22,16 @@ namespace moe {
 namespace {
 
 constexpr int BS_THREADS = 256;      // of the first kernel
+constexpr int BS_HELD = 8;           // a thread's 16-byte pieces of a unit
 constexpr int BS_GROUPS = BS_THREADS / 4;
 constexpr int BS_CAP = 1024;         // logits that are ranked against each other
+constexpr int BS_CHECK = 8;          // units between two looks at how many there are
+constexpr int BS_CTAS = 3;           // blocks an SM
+constexpr int BS_RING = 2;           // units on their way or looked at
+constexpr int BS_MAX_CTAS = 1024;    // blocks at most: what the workspace has room for
 constexpr int BS_JOIN = 256;         // threads of the second
 constexpr int BS_BEAM = 8;           // of them that join a beam's sums
-constexpr int BS_EACH = 8;           // list entries a thread of it looks at together
+constexpr int BS_EACH = 4;           // lists a warp of it looks at together
 constexpr int BS_MAX_K = 64;
 constexpr int BS_MAX_W = 64;
 
@@ -30,12 +39,16 @@ struct BeamArgs {
     const void* logits;
     const float* scores;
     const uint8_t* done;
-    int pad, W, V, K, chunks;
+    int pad, W, V, K;
+    int units, segments;             // units of a row; stretches that a row is in at most
+    int ctas;
+    long long total;                 // units of all rows
     float* out_scores;
     int32_t* parents;
     int32_t* tokens;
-    float2* part;                    // [rows, chunks] maximum, sum of exp relative to it
-    unsigned long long* list;        // [rows, chunks, K] order of the logit, then of the lowest token; 0: none
+    // of block g's part of row r, at g + r: no two have the same
+    float2* part;                    // maximum, sum of exp relative to it
+    unsigned long long* list;        // [K] order of the logit, then of the lowest token; 0: none
 };
 
 __device__ __forceinline__ float pow2(float x) {
@@ -74,8 +87,12 @@ __device__ __forceinline__ uint32_t filled(uint32_t t, int lowest_bit) {
 // Of two numbers a lane of one warp, the largest t that at least K have or exceed, or a smaller one that K of them do;
 // its bits from lowest_bit on are looked for, so with more of them it is the smaller the fewer.
 __device__ __forceinline__ uint32_t kth_largest(uint32_t x, uint32_t y, int K, int lowest_bit) {
-    uint32_t t = 0u;
-    for (int bit = 31; bit >= lowest_bit; bit--) {
+    // (the bits that all have in common it has too)
+    const uint32_t any = __reduce_or_sync(FULL, x | y), all = __reduce_and_sync(FULL, x & y), differ = any ^ all;
+    if (differ == 0u) return x;
+    const int first = 31 - __clz(differ);
+    uint32_t t = first == 31 ? 0u : any >> (first + 1) << (first + 1);
+    for (int bit = first; bit >= lowest_bit; bit--) {
         const uint32_t tried = t | (1u << bit);
         const int n = __popc(__ballot_sync(FULL, x >= tried)) + __popc(__ballot_sync(FULL, y >= tried));
         if (n >= K) t = tried;
@@ -87,73 +104,45 @@ __device__ __forceinline__ uint32_t kth_largest(uint32_t x, uint32_t y, int K, i
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// A thread's logits: pieces of 16 bytes, THREADS pieces apart.
+// A piece: 16 bytes of logits.
 template <typename T>
-struct Held;
+struct Piece;
 template <>
-struct Held<float> {
-    static constexpr int VEC = 4, PIECES = 8, LOWEST_BIT = 0;
-    float v[PIECES][VEC];
-    __device__ __forceinline__ float at(int i, int e) const { return v[i][e]; }
-    __device__ __forceinline__ void load(int i, const float* p) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(p));
-        v[i][0] = x.x;
-        v[i][1] = x.y;
-        v[i][2] = x.z;
-        v[i][3] = x.w;
+struct Piece<float> {
+    static constexpr int VEC = 4, LOWEST_BIT = 0;
+    float v[VEC];
+    __device__ __forceinline__ float at(int e) const { return v[e]; }
+    __device__ __forceinline__ void put(const uint4& x) {
+        v[0] = __uint_as_float(x.x);
+        v[1] = __uint_as_float(x.y);
+        v[2] = __uint_as_float(x.z);
+        v[3] = __uint_as_float(x.w);
     }
-    __device__ __forceinline__ void some(int i, const float* p, int first, int end) {
+    // elements [first, end) of it, -inf for the others
+    __device__ __forceinline__ void some(const float* p, int first, int end) {
 #pragma unroll
-        for (int e = 0; e < VEC; e++) v[i][e] = e >= first && e < end ? __ldg(p + e) : -INFINITY;
+        for (int e = 0; e < VEC; e++) v[e] = e >= first && e < end ? __ldg(p + e) : -INFINITY;
     }
-    // f(x, e) for the elements [first, end) of the piece at p, all of them where it is whole
-    template <typename F>
-    static __device__ __forceinline__ void each(const float* p, bool whole, int first, int end, F f) {
-        if (whole) {
-            const float4 x = __ldg(reinterpret_cast<const float4*>(p));
-            f(x.x, 0);
-            f(x.y, 1);
-            f(x.z, 2);
-            f(x.w, 3);
-        } else {
-#pragma unroll 1
-            for (int e = first; e < end; e++) f(__ldg(p + e), e);
-        }
-    }
-    __device__ __forceinline__ float top(int i) const { return fmaxf(fmaxf(v[i][0], v[i][1]), fmaxf(v[i][2], v[i][3])); }
+    __device__ __forceinline__ float top() const { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }
 };
 template <>
-struct Held<__nv_bfloat16> {
-    static constexpr int VEC = 8, PIECES = 8, LOWEST_BIT = 16;
-    uint4 v[PIECES];
-    __device__ __forceinline__ uint32_t word(int i, int w) const { return w == 0 ? v[i].x : w == 1 ? v[i].y : w == 2 ? v[i].z : v[i].w; }
-    __device__ __forceinline__ float at(int i, int e) const {
-        return __uint_as_float(e & 1 ? word(i, e >> 1) & 0xffff0000u : word(i, e >> 1) << 16);
-    }
-    __device__ __forceinline__ void load(int i, const __nv_bfloat16* p) { v[i] = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void some(int i, const __nv_bfloat16* p, int first, int end) {
+struct Piece<__nv_bfloat16> {
+    static constexpr int VEC = 8, LOWEST_BIT = 16;
+    uint4 v;
+    __device__ __forceinline__ uint32_t word(int w) const { return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w; }
+    __device__ __forceinline__ float at(int e) const { return __uint_as_float(e & 1 ? word(e >> 1) & 0xffff0000u : word(e >> 1) << 16); }
+    __device__ __forceinline__ void put(const uint4& x) { v = x; }
+    __device__ __forceinline__ void some(const __nv_bfloat16* p, int first, int end) {
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < VEC; e++) {
             const uint32_t x = e >= first && e < end ? (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + e) : 0xff80u;
             w[e >> 1] = e & 1 ? w[e >> 1] | (x << 16) : x;
         }
-        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        v = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    template <typename F>
-    static __device__ __forceinline__ void each(const __nv_bfloat16* p, bool whole, int first, int end, F f) {
-        if (whole) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < VEC; e++) f(__uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16), e);
-        } else {
-#pragma unroll 1
-            for (int e = first; e < end; e++) f(__bfloat162float(p[e]), e);
-        }
-    }
-    __device__ __forceinline__ float top(int i) const {
-        const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v[i]);
+    __device__ __forceinline__ float top() const {
+        const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
         const float2 f = __bfloat1622float2(__hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
         return fmaxf(f.x, f.y);
     }
@@ -163,12 +152,13 @@ __device__ __forceinline__ unsigned long long key_of(float x, int token) {
     return (unsigned long long)order_of(x + 0.0f) << 32 | (0xffffffffu - (uint32_t)token);
 }
 
-// The K largest of a chunk where many tie, or lie above the groups' threshold: the K-th largest logit is found bit by
+// The K largest of some units where many tie, or are above the threshold: the K-th largest logit is found bit by
 // bit; those above it are fewer than K, and of what ties with it the first K in the tokens' order are taken, piece by piece.
-// The chunk is read again for it (from L2). Returns their number, in buf.
+// The units are read again for it (from L2). They go behind the `kept` in buf; returns how many there are with those.
 template <typename T>
-__device__ __noinline__ int exactly_largest(const T* row, int first, int V, int K, unsigned long long* buf, int* count, int* scan) {
-    using H = Held<T>;
+__device__ __noinline__ int exactly_largest(const T* row, int first, int pieces, int V, int K, unsigned long long* buf, int kept, int* count,
+                                            int* scan) {
+    using P = Piece<T>;
     const int warp = threadIdx.x / 32;
     auto sum = [&](int mine) {
         mine = __reduce_add_sync(FULL, mine);
@@ -180,32 +170,32 @@ __device__ __noinline__ int exactly_largest(const T* row, int first, int V, int 
         return all;
     };
     auto read = [&](int i, int e, int& token, uint32_t& x) {
-        token = first + i * BS_THREADS * H::VEC + e;
+        token = first + i * BS_THREADS * P::VEC + e;
         if ((unsigned)token >= (unsigned)V) return false;
         x = order_of(to_float(row[token]) + 0.0f);
         return true;
     };
     int token;
     uint32_t x, t = 0u;
-    for (int bit = 31; bit >= H::LOWEST_BIT; bit--) {
+    for (int bit = 31; bit >= P::LOWEST_BIT; bit--) {
         const uint32_t tried = t | (1u << bit);
         int mine = 0;
-        for (int i = 0; i < H::PIECES; i++)
-            for (int e = 0; e < H::VEC; e++) mine += read(i, e, token, x) && x >= tried;
+        for (int i = 0; i < pieces; i++)
+            for (int e = 0; e < P::VEC; e++) mine += read(i, e, token, x) && x >= tried;
         if (sum(mine) >= K) t = tried;
     }
-    t = filled(t, H::LOWEST_BIT);
+    t = filled(t, P::LOWEST_BIT);
     __syncthreads();
-    if (threadIdx.x == 0) *count = 0;
+    if (threadIdx.x == 0) *count = kept;
     __syncthreads();
     auto push = [&](uint32_t x, int token) {
         const int slot = atomicAdd(count, 1);
         if (slot < BS_CAP) buf[slot] = (unsigned long long)x << 32 | (0xffffffffu - (uint32_t)token);
     };
     int before = 0;
-    for (int i = 0; i < H::PIECES; i++) {
+    for (int i = 0; i < pieces; i++) {
         int mine = 0;
-        for (int e = 0; e < H::VEC; e++) {
+        for (int e = 0; e < P::VEC; e++) {
             if (!read(i, e, token, x)) continue;
             if (x > t) push(x, token);
             mine += x == t;
@@ -224,212 +214,349 @@ __device__ __noinline__ int exactly_largest(const T* row, int first, int V, int 
             if (w < warp) rank += scan[w];
             before += scan[w];
         }
-        for (int e = 0; e < H::VEC; e++)
+        for (int e = 0; e < P::VEC; e++)
             if (read(i, e, token, x) && x == t && rank++ < K) push(x, token);
     }
     __syncthreads();
     return min(*count, BS_CAP);
 }
 
+// best[rank] = key for the n keys of buf with a rank below K (all keys are different): a warp a key, its lanes the others.
+__device__ __forceinline__ void rank_keys(const unsigned long long* buf, int n, int K, unsigned long long* best) {
+    for (int i = threadIdx.x / 32; i < n; i += BS_THREADS / 32) {
+        const unsigned long long key = buf[i];
+        int above = 0;
+        for (int k = lane_id(); k < n; k += 32) above += buf[k] > key;
+        above = __reduce_add_sync(FULL, above);
+        if (above < K && lane_id() == 0) best[above] = key;
+    }
+}
+
 template <typename T>
-__global__ void __launch_bounds__(BS_THREADS, 4) beam_chunk_kernel(const __grid_constant__ BeamArgs a) {
-    using H = Held<T>;
-    __shared__ unsigned long long buf[BS_CAP];
+__global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __grid_constant__ BeamArgs a) {
+    using P = Piece<T>;
+    extern __shared__ __align__(16) uint4 ring[];                      // [BS_RING][BS_HELD][BS_THREADS]
+    __shared__ unsigned long long buf[BS_CAP], best[BS_MAX_K];
     __shared__ float2 warps[BS_THREADS / 32];
     __shared__ uint32_t groups[BS_GROUPS], threshold;
     __shared__ int count, scan[BS_THREADS / 32];
-    const int chunk = blockIdx.x % a.chunks, warp = threadIdx.x / 32;
-    const long long row = blockIdx.x / a.chunks, start = row * a.V;
-    // pieces are counted from the last 16-byte boundary at or before the row
-    const int skew = (int)(start % H::VEC);
-    const T* const base = static_cast<const T*>(a.logits) + (start - skew);
-    const int p0 = chunk * (BS_THREADS * H::PIECES) + threadIdx.x;
+    constexpr float LOG2E = 1.44269504088896340736f;
+    constexpr int STEP = BS_THREADS * P::VEC, UNIT = BS_HELD * STEP;   // tokens between a thread's pieces, and of a unit
+    const int warp = threadIdx.x / 32;
     pdl_trigger();
-    if (threadIdx.x == 0) count = 0;
+    const long long begin = a.total * blockIdx.x / a.ctas, end = a.total * (blockIdx.x + 1) / a.ctas;
+    long long row = begin / a.units;
+    int u = (int)(begin - row * a.units);
+    // pieces are counted from the last 16-byte boundary at or before the row, which is so many tokens before it
+    auto skew_of = [&](long long r) { return (int)(r * a.V % P::VEC); };
+    auto whole = [&](int t) { return t >= 0 && t + P::VEC <= a.V; };                  // a piece from token t on is all in the row
+    auto all_whole = [&](int v, int skew) { return v * UNIT >= skew && (v + 1) * UNIT - skew <= a.V; };   // unit v is
 
-    H h;
-    float top = -INFINITY, tops[H::PIECES];
-    const int at0 = p0 * H::VEC - skew;                              // token of the first piece's first element
-    const T* const piece0 = base + (at0 + skew);
-    constexpr int STEP = BS_THREADS * H::VEC;                        // tokens between a thread's pieces
-    const int chunk_at = chunk * H::PIECES * STEP - skew;
-    if (chunk_at >= 0 && chunk_at + H::PIECES * STEP <= a.V) {
+    // the loading walk: a unit at a time, copies of what is whole
+    const T* ld_base = static_cast<const T*>(a.logits) + row * a.V;    // token t's logit: base[t]
+    long long ld_row = row, ld_left = end - begin;
+    int ld_u = u, ld_skew = skew_of(row), ld_stage = 0;
+    auto issue = [&]() {
+        if (ld_left > 0) {
+            ld_left--;
+            const int t = ld_u * UNIT + (int)threadIdx.x * P::VEC - ld_skew;
+            const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + ld_stage * (BS_HELD * BS_THREADS) + threadIdx.x);
+            if (all_whole(ld_u, ld_skew)) {
 #pragma unroll
-        for (int i = 0; i < H::PIECES; i++) h.load(i, piece0 + i * STEP);
-    } else {
+                for (int i = 0; i < BS_HELD; i++)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * BS_THREADS * 16), "l"(ld_base + t + i * STEP) : "memory");
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < BS_HELD; i++)
+                    if (whole(t + i * STEP))
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * BS_THREADS * 16), "l"(ld_base + t + i * STEP) : "memory");
+            }
+            if (++ld_u == a.units) {
+                ld_u = 0;
+                ld_row++;
+                ld_base += a.V;
+                ld_skew = skew_of(ld_row);
+            }
+        }
+        ld_stage = ld_stage + 1 == BS_RING ? 0 : ld_stage + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < BS_RING; i++) issue();
+    int stage = 0;
+    const T* base = static_cast<const T*>(a.logits) + row * a.V;
+
+    for (long long at = begin; at < end; row++, base += a.V, u = 0) {
+        const int u0 = u, u1 = (int)min((long long)a.units, u + (end - at)), skew = skew_of(row);
+        at += u1 - u;
+        float least = -INFINITY;
+        // sum of exponentials, relative to m (while that is -inf: 0, or NaN if there is one)
+        float m = -INFINITY, sum = 0.0f;
+        int kept = 0;                                                  // in buf at the last look
+        for (; u < u1; u++) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(BS_RING - 1) : "memory");
+            const int token = u * UNIT + (int)threadIdx.x * P::VEC - skew;            // of the thread's first piece's first element
+            const uint4* const mine = ring + stage * (BS_HELD * BS_THREADS) + threadIdx.x;
+            P p[BS_HELD];
+            if (all_whole(u, skew)) {
 #pragma unroll
-        for (int i = 0; i < H::PIECES; i++) {
-            const int at = at0 + i * STEP;
-            if (at >= 0 && at + H::VEC <= a.V) h.load(i, piece0 + i * STEP);
-            else h.some(i, piece0 + i * STEP, max(0, -at), min(H::VEC, a.V - at));
+                for (int i = 0; i < BS_HELD; i++) p[i].put(mine[i * BS_THREADS]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < BS_HELD; i++) {
+                    const int t = token + i * STEP;
+                    if (whole(t)) p[i].put(mine[i * BS_THREADS]);
+                    else p[i].some(base + t, max(0, -t), min(P::VEC, a.V - t));
+                }
+            }
+            float tops[BS_HELD], top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < BS_HELD; i++) {
+                tops[i] = p[i].top();
+                top = fmaxf(top, tops[i]);
+            }
+            if (u == u0) {
+                // the first threshold, by the first warp while the others sum
+                float four = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
+                four = fmaxf(four, __shfl_xor_sync(FULL, four, 2));
+                if ((threadIdx.x & 3) == 0) groups[threadIdx.x / 4] = order_of(four);
+                if (threadIdx.x == 0) count = 0;
+                __syncthreads();
+                if (warp == 0) {
+                    const uint32_t t = kth_largest(groups[lane_id()], groups[lane_id() + 32], a.K, 12);
+                    if (lane_id() == 0) threshold = t;
+                }
+            }
+            if (top > m) {
+                sum *= m == -INFINITY ? 1.0f : pow2((m - top) * LOG2E);
+                m = top;
+            }
+            {
+                const float sub = m == -INFINITY ? 0.0f : -m;
+                const Two minus(sub, sub), log2e(LOG2E, LOG2E);
+                Two sum0(0.0f, 0.0f), sum1(0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < BS_HELD; i++)
+#pragma unroll
+                    for (int e = 0; e < P::VEC; e += 2) {
+                        Two x(p[i].at(e), p[i].at(e + 1));
+                        x += minus;
+                        x *= log2e;
+                        float x0, x1;
+                        x.get(x0, x1);
+                        (e & 2 ? sum1 : sum0) += Two(pow2(x0), pow2(x1));
+                    }
+                sum0 += sum1;
+                float s0, s1;
+                sum0.get(s0, s1);
+                sum += s0 + s1;
+            }
+            if (u == u0) {
+                __syncthreads();
+                least = of_order(threshold);
+            }
+            // (the few pieces that hold one are read again: a loop's code, not eight pieces' in line)
+            unsigned hits = 0u;
+#pragma unroll
+            for (int i = 0; i < BS_HELD; i++) hits |= (unsigned)(tops[i] >= least) << i;
+            while (hits) {
+                const int i = __ffs(hits) - 1, t = token + i * STEP;
+                hits &= hits - 1;
+                P q;
+                if (whole(t)) q.put(mine[i * BS_THREADS]);
+                else q.some(base + t, max(0, -t), min(P::VEC, a.V - t));
+#pragma unroll
+                for (int e = 0; e < P::VEC; e++) {
+                    const float x = q.at(e);
+                    if (x >= least && (unsigned)(t + e) < (unsigned)a.V) {
+                        const int to = atomicAdd(&count, 1);
+                        if (to < BS_CAP) buf[to] = key_of(x, t + e);
+                    }
+                }
+            }
+            issue();
+            stage = stage + 1 == BS_RING ? 0 : stage + 1;
+            const bool more = u + 1 < u1;
+            if (more && (u - u0) % BS_CHECK != BS_CHECK - 1) continue;
+            // every few units: the K largest so far in order, the last of them the threshold
+            __syncthreads();
+            int n = count;
+            __syncthreads();                                           // (nobody adds to it before all have read it)
+            if (n > BS_CAP) {
+                const int since = (u - u0) % BS_CHECK;
+                n = exactly_largest<T>(base, token - since * UNIT, (since + 1) * BS_HELD, a.V, a.K, buf, kept, &count, scan);
+            }
+            rank_keys(buf, n, a.K, best);
+            n = min(n, a.K);
+            __syncthreads();
+            if ((int)threadIdx.x < n) buf[threadIdx.x] = best[threadIdx.x];
+            if (threadIdx.x == 0) count = n;
+            // (what ties with it comes later in the row, and behind it: the next number up is the least that counts)
+            if (n == a.K) least = of_order((uint32_t)(best[n - 1] >> 32) + 1u);
+            __syncthreads();
+            kept = n;
+        }
+        const long long to = blockIdx.x + row;
+        if ((int)threadIdx.x < a.K) a.list[to * a.K + threadIdx.x] = (int)threadIdx.x < kept ? buf[threadIdx.x] : 0ull;
+        float high = m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) high = fmaxf(high, __shfl_xor_sync(FULL, high, o));
+        if (m != -INFINITY) sum *= pow2((m - high) * LOG2E);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+        if (lane_id() == 0) warps[warp] = make_float2(high, sum);
+        __syncthreads();
+        if (warp == 0) {
+            const float2 x = lane_id() < BS_THREADS / 32 ? warps[lane_id()] : make_float2(-INFINITY, 0.0f);
+            high = x.x;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) high = fmaxf(high, __shfl_xor_sync(FULL, high, o));
+            float v = x.x == -INFINITY ? x.y : x.y * pow2((x.x - high) * LOG2E);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+            if (lane_id() == 0) a.part[to] = make_float2(high, v);
         }
     }
-#pragma unroll
-    for (int i = 0; i < H::PIECES; i++) {
-        tops[i] = h.top(i);
-        top = fmaxf(top, tops[i]);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// A number as the sum of two floats, the first the sum rounded.
+struct Pair {
+    float h, l;
+};
+__device__ __forceinline__ Pair pair_of(float x, float y) {            // x + y exactly (Knuth's two-sum)
+    const float h = __fadd_rn(x, y), z = __fsub_rn(h, x);
+    return {h, __fadd_rn(__fsub_rn(x, __fsub_rn(h, z)), __fsub_rn(y, z))};
+}
+__device__ __forceinline__ Pair plus(Pair x, float y) {
+    const Pair s = pair_of(x.h, y);
+    const float l = __fadd_rn(s.l, x.l), h = __fadd_rn(s.h, l);
+    return {h, isfinite(h) ? __fsub_rn(l, __fsub_rn(h, s.h)) : 0.0f};
+}
+__device__ __forceinline__ Pair plus(Pair x, Pair y) {
+    const Pair s = pair_of(x.h, y.h);
+    const float l = __fadd_rn(s.l, __fadd_rn(x.l, y.l)), h = __fadd_rn(s.h, l);
+    return {h, isfinite(h) ? __fsub_rn(l, __fsub_rn(h, s.h)) : 0.0f};
+}
+
+// ln of a normal positive number: ln(2^k f) = k ln 2 + 2 atanh z with f in [0.7, 1.42), z = (f - 1) / (f + 1) and the series of
+// atanh. Only k ln 2 and 2 z are taken in two floats: the rest is below 2^-8 and the series ends below 2^-35.
+__device__ __forceinline__ Pair ln(Pair x) {
+    const uint32_t u = __float_as_uint(x.h);
+    int k = (int)(u >> 23) - 127;
+    float f = __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
+    if (f > 1.41421356f) {
+        f *= 0.5f;
+        k++;
     }
-    // the threshold, by the first warp while the others sum
-    float four = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
-    four = fmaxf(four, __shfl_xor_sync(FULL, four, 2));
-    if ((threadIdx.x & 3) == 0) groups[threadIdx.x / 4] = order_of(four);
-    __syncthreads();
-    if (warp == 0) {
-        const uint32_t t = kth_largest(groups[lane_id()], groups[lane_id() + 32], a.K, 12);
-        if (lane_id() == 0) threshold = t;
-    }
-    // sum of exponentials, relative to the thread's maximum (where that is -inf: 0, or NaN if there is one)
-    constexpr float LOG2E = 1.44269504088896340736f;
-    {
-        const float sub = top == -INFINITY ? 0.0f : top;
-        const Two minus(-sub, -sub), log2e(LOG2E, LOG2E);
-        Two sum0(0.0f, 0.0f), sum1(0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < H::PIECES; i++)
-#pragma unroll
-            for (int e = 0; e < H::VEC; e += 2) {
-                Two x(h.at(i, e), h.at(i, e + 1));
-                x += minus;
-                x *= log2e;
-                float x0, x1;
-                x.get(x0, x1);
-                (e & 2 ? sum1 : sum0) += Two(pow2(x0), pow2(x1));
-            }
-        sum0 += sum1;
-        float s, s1;
-        sum0.get(s, s1);
-        s += s1;
-        float m = top;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-        if (top != -INFINITY) s *= pow2((top - m) * LOG2E);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-        if (lane_id() == 0) warps[warp] = make_float2(m, s);
-    }
-    __syncthreads();
-    if (warp == BS_THREADS / 32 - 1) {
-        const float2 x = lane_id() < BS_THREADS / 32 ? warps[lane_id()] : make_float2(-INFINITY, 0.0f);
-        float m = x.x;
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-        float v = x.x == -INFINITY ? x.y : x.y * pow2((x.x - m) * LOG2E);
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
-        if (lane_id() == 0) a.part[blockIdx.x] = make_float2(m, v);
-    }
-    const float least = of_order(threshold);
-    // (the few pieces that hold one are read again: a loop's code, not eight pieces' in line)
-    unsigned hits = 0u;
-#pragma unroll
-    for (int i = 0; i < H::PIECES; i++) hits |= (unsigned)(tops[i] >= least) << i;
-    while (hits) {
-        const int i = __ffs(hits) - 1;
-        hits &= hits - 1;
-        const int at = at0 + i * STEP;
-        H::each(piece0 + i * STEP, at >= 0 && at + H::VEC <= a.V, max(0, -at), min(H::VEC, a.V - at), [&](float x, int e) {
-            if (x >= least) {
-                const int slot = atomicAdd(&count, 1);
-                if (slot < BS_CAP) buf[slot] = key_of(x, at + e);
-            }
-        });
-    }
-    __syncthreads();
-    int n = count;
-    if (n > BS_CAP) n = exactly_largest<T>(base + skew, at0, a.V, a.K, buf, &count, scan);
-    unsigned long long* const list = a.list + (long long)blockIdx.x * a.K;
-    for (int i = threadIdx.x; i < n; i += BS_THREADS) {
-        const unsigned long long mine = buf[i];
-        int rank = 0;
-        for (int k = 0; k < n; k++) rank += buf[k] > mine;
-        if (rank < a.K) list[rank] = mine;
-    }
-    for (int k = n + threadIdx.x; k < a.K; k += BS_THREADS) list[k] = 0ull;
+    const float n = __fsub_rn(f, 1.0f);                                // exact
+    const Pair d = pair_of(f, 1.0f);
+    const float z = __fdiv_rn(n, d.h);
+    const float zl = __fdiv_rn(__fsub_rn(__fmaf_rn(-z, d.h, n), __fmul_rn(z, d.l)), d.h);
+    const float w = z * z;
+    const float rest = z * w * (2.0f / 3 + w * (2.0f / 5 + w * (2.0f / 7 + w * (2.0f / 9 + w * (2.0f / 11 + w * (2.0f / 13))))));
+    // ln 2 = 0x1.62e4p-1 + ...: 16 bits, whose product with k is exact, and what is left
+    const Pair a = pair_of(__fmul_rn((float)k, 0x1.62e4p-1f), 2.0f * z);
+    const float l = a.l + ((float)k * (float)(0.69314718055994530942 - 0x1.62e4p-1) + (2.0f * zl + rest + x.l / x.h));
+    const float h = __fadd_rn(a.h, l);
+    return {h, __fsub_rn(l, __fsub_rn(h, a.h))};
 }
 
 struct Joined {
     unsigned long long best[BS_MAX_K];
     int best_at[BS_MAX_K];
-    double lse[BS_MAX_W];            // of a beam that lives
-    float score[BS_MAX_W], off[BS_MAX_W], m[BS_MAX_W];
+    Pair lse[BS_MAX_W];              // of a beam that lives
+    float score[BS_MAX_W], off[BS_MAX_W];
+    int first[BS_MAX_W], parts[BS_MAX_W];
     int state[BS_MAX_W];             // 0: lives, 1: done, 2: has no candidate
-    uint32_t groups[64], threshold;
+    uint32_t low[BS_JOIN], threshold;
     int count;
-    unsigned long long v[BS_JOIN * BS_EACH + BS_MAX_K];
-    int at[BS_JOIN * BS_EACH + BS_MAX_K];
+    unsigned long long v[BS_JOIN * BS_EACH * 2 + BS_MAX_K];
+    int at[BS_JOIN * BS_EACH * 2 + BS_MAX_K];
 };
 
-// Whole numbers in the order of doubles (-0 as +0), and back.
-__device__ __forceinline__ unsigned long long order_of(double x) {
-    const unsigned long long u = (unsigned long long)__double_as_longlong(x == 0.0 ? 0.0 : x);
-    return u >> 63 ? ~u : u | (1ull << 63);
-}
-__device__ __forceinline__ double of_order(unsigned long long u) {
-    return __longlong_as_double((long long)(u >> 63 ? u & ~(1ull << 63) : ~u));
-}
-
-// (What takes 64 bits is slow on this device: a logarithm a beam, all in one warp, and the survivors' values.)
 __global__ void __launch_bounds__(BS_JOIN) beam_join_kernel(const __grid_constant__ BeamArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
     Joined& s = *reinterpret_cast<Joined*>(raw);
     const long long row0 = (long long)blockIdx.x * a.W;
-    const int per_beam = a.chunks * a.K, total = a.W * per_beam;
-    const unsigned long long* const list = a.list + row0 * per_beam;
-    pdl_wait();
-    // the first entries are on their way while the sums are joined
-    unsigned long long ahead[BS_EACH];
-    auto fetch = [&](int i0) {
+    const int lists = a.W * a.segments, warp = threadIdx.x / 32;
+    constexpr int TOGETHER = BS_JOIN / 32 * BS_EACH;
+    // (the scores were there before the first kernel began, which this one runs beside)
+    if ((int)threadIdx.x < a.W) {
+        const long long row = row0 + threadIdx.x, f = row * a.units;
+        const int g0 = (int)(((f + 1) * a.ctas - 1) / a.total), g1 = (int)(((f + a.units) * a.ctas - 1) / a.total);
+        s.first[threadIdx.x] = g0;
+        s.parts[threadIdx.x] = g1 - g0 + 1;
+        s.score[threadIdx.x] = a.scores[row];
+        s.state[threadIdx.x] = a.done && a.done[row];
+    }
+    // the beam and the part of list l, as far as a thread looks at them together
+    int list_w[BS_EACH], list_part[BS_EACH];
+    auto place = [&](int l0) {
 #pragma unroll
         for (int e = 0; e < BS_EACH; e++) {
-            const int i = i0 + e * BS_JOIN + threadIdx.x;
-            ahead[e] = i < total ? __ldcg(list + i) : 0ull;
+            const int l = l0 + e * (BS_JOIN / 32) + warp;
+            list_w[e] = l < lists ? l / a.segments : -1;
+            list_part[e] = l - list_w[e] * a.segments;
         }
     };
-    fetch(0);
+    place(0);
+    __syncthreads();
+    pdl_wait();
+    // the first lists are on their way while the sums are joined: entries lane and lane + 32
+    unsigned long long ahead[BS_EACH][2];
+    auto fetch = [&]() {
+#pragma unroll
+        for (int e = 0; e < BS_EACH; e++) {
+            ahead[e][0] = ahead[e][1] = 0ull;
+            const int w = list_w[e], part = list_part[e];
+            if (w >= 0 && part < s.parts[w]) {
+                const unsigned long long* const list = a.list + (row0 + w + s.first[w] + part) * a.K;
+                if ((int)lane_id() < a.K) ahead[e][0] = __ldcg(list + lane_id());
+                if ((int)lane_id() + 32 < a.K) ahead[e][1] = __ldcg(list + lane_id() + 32);
+            }
+        }
+    };
+    fetch();
     for (int w0 = 0; w0 < a.W; w0 += BS_JOIN / BS_BEAM) {
         const int w = w0 + threadIdx.x / BS_BEAM, l = threadIdx.x % BS_BEAM;
-        const float2* part = a.part + (row0 + min(w, a.W - 1)) * a.chunks;
-        float m = -INFINITY;
-        for (int c = l; c < a.chunks; c += BS_BEAM) m = fmaxf(m, __ldcg(part + c).x);
+        const int parts = w < a.W ? s.parts[w] : 0;
+        const float2* part = a.part + row0 + (w < a.W ? w + s.first[w] : 0);
+        const float2 mine = l < parts ? __ldcg(part + l) : make_float2(-INFINITY, 0.0f);
+        float m = mine.x;
+        for (int c = l + BS_BEAM; c < parts; c += BS_BEAM) m = fmaxf(m, __ldcg(part + c).x);
 #pragma unroll
         for (int o = BS_BEAM / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-        double sum = 0.0;
-        for (int c = l; c < a.chunks; c += BS_BEAM) {
-            const float2 x = __ldcg(part + c);
-            sum += x.x == -INFINITY || x.x == m ? x.y : x.y * expf(x.x - m);
+        Pair sum = {0.0f, 0.0f};
+        for (int c = l; c < parts; c += BS_BEAM) {
+            const float2 x = c == l ? mine : __ldcg(part + c);
+            sum = plus(sum, x.x == -INFINITY || x.x == m ? x.y : x.y * expf(x.x - m));
         }
 #pragma unroll
-        for (int o = BS_BEAM / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+        for (int o = BS_BEAM / 2; o > 0; o >>= 1)
+            sum = plus(sum, Pair{__shfl_xor_sync(FULL, sum.h, o), __shfl_xor_sync(FULL, sum.l, o)});
         if (l == 0 && w < a.W) {
-            s.m[w] = m;
-            s.lse[w] = sum;
+            // (the sum is at least one, where it is one of numbers)
+            const float score = s.score[w];
+            const bool fine = isfinite(score), done = s.state[w], lives = sum.h >= 1.0f && isfinite(sum.h) && isfinite(m);
+            const Pair lse = lives ? plus(ln(sum), m) : Pair{0.0f, 0.0f};
+            s.lse[w] = lse;
+            s.off[w] = score - lse.h;
+            s.state[w] = done && fine ? 1 : !done && fine && lives && isfinite(lse.h) ? 0 : 2;
         }
-    }
-    __syncthreads();
-    if ((int)threadIdx.x < a.W) {
-        const int w = threadIdx.x;
-        const float score = a.scores[row0 + w];
-        const double lse = s.m[w] + log(s.lse[w]);
-        const bool fine = isfinite(score), done = a.done && a.done[row0 + w];
-        s.score[w] = score;
-        s.lse[w] = lse;
-        s.off[w] = (float)(score - lse);
-        s.state[w] = done && fine ? 1 : !done && fine && isfinite(lse) ? 0 : 2;
     }
     __syncthreads();
 
-    // list entry i, its key read: its beam and token, and x, its logit (a done or dead beam's: its score, or -inf); false: none
-    auto entry = [&](int i, unsigned long long key, int& w, int& token, float& x) {
-        if (i >= total) return false;
-        w = i / per_beam;
-        const int k = i - w * per_beam;
+    // entry k of a beam's list, its key read: the token, and x, its logit (a done or dead beam's, in the place of its
+    // first list: its score, or -inf); false: none
+    auto entry = [&](int w, int part, int k, unsigned long long key, int& token, float& x) {
         if (s.state[w] == 0) {
             if (key == 0ull) return false;
             token = (int)(0xffffffffu - (uint32_t)key);
             x = of_order((uint32_t)(key >> 32));
             return true;
         }
-        if (k >= a.K || k >= a.V) return false;
+        if (part > 0 || k >= a.K || k >= a.V) return false;
         token = k;
         x = -INFINITY;
         if (s.state[w] == 1) {
@@ -438,42 +565,73 @@ __global__ void __launch_bounds__(BS_JOIN) beam_join_kernel(const __grid_constan
         }
         return true;
     };
+    // its value as a number in the values' order
     auto value = [&](int w, float x) {
-        return x == -INFINITY ? (double)-INFINITY : s.state[w] ? (double)x : (double)s.score[w] + ((double)x - s.lse[w]);
+        Pair v = {x, 0.0f};
+        if (x != -INFINITY && s.state[w] == 0) {
+            const Pair lse = s.lse[w];
+            v = plus(plus(pair_of(x, -lse.h), -lse.l), s.score[w]);
+        }
+        return (unsigned long long)order_of(v.h + 0.0f) << 32 | order_of(v.l + 0.0f);
     };
     int kept = 0;
-    for (int i0 = 0; i0 < total; i0 += BS_JOIN * BS_EACH) {
-        if (i0) fetch(i0);
-        float hi[BS_EACH];
+    for (int l0 = 0; l0 < lists; l0 += TOGETHER) {
+        if (l0) {
+            place(l0);
+            fetch();
+        }
+        float hi[BS_EACH][2];
         float low = -INFINITY;                                       // the largest lower bound of the thread's entries
         if (threadIdx.x == 0) s.count = 0;
-        const int turns = min(BS_EACH, (total - i0 + BS_JOIN - 1) / BS_JOIN);
 #pragma unroll
         for (int e = 0; e < BS_EACH; e++) {
-            hi[e] = __uint_as_float(0x7fc00000u);
-            if (e >= turns) continue;
-            int w, token;
-            float x;
-            if (!entry(i0 + e * BS_JOIN + threadIdx.x, ahead[e], w, token, x)) continue;
-            float lo = x;
-            hi[e] = x;
-            if (s.state[w] == 0 && x != -INFINITY) {
-                // |value - v| < 2^-22 (|off| + |x|) with the roundings of off and of the sum
-                const float v = s.off[w] + x, eps = (fabsf(s.off[w]) + fabsf(x)) * 0x1p-21f;
-                const bool fine = isfinite(v) && isfinite(eps);
-                lo = fine ? v - eps : -INFINITY;
-                hi[e] = fine ? v + eps : INFINITY;
+            hi[e][0] = hi[e][1] = __uint_as_float(0x7fc00000u);
+            const int w = list_w[e];
+            if (w < 0) continue;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                int token;
+                float x;
+                if (!entry(w, list_part[e], lane_id() + 32 * h, ahead[e][h], token, x)) continue;
+                float lo = x;
+                hi[e][h] = x;
+                if (s.state[w] == 0 && x != -INFINITY) {
+                    // |value - v| < 2^-22 (|off| + |x|) + |lse| 2^-24 with the roundings of off, of lse and of the sum
+                    const float v = s.off[w] + x, eps = (fabsf(s.off[w]) + fabsf(x) + fabsf(s.lse[w].h)) * 0x1p-21f;
+                    const bool fine = isfinite(v) && isfinite(eps);
+                    lo = fine ? v - eps : -INFINITY;
+                    hi[e][h] = fine ? v + eps : INFINITY;
+                }
+                low = fmaxf(low, lo);
             }
-            low = fmaxf(low, lo);
         }
-        if ((int)threadIdx.x < kept) low = fmaxf(low, __double2float_rd(of_order(s.best[threadIdx.x])));
-        low = fmaxf(low, __shfl_xor_sync(FULL, low, 1));
-        low = fmaxf(low, __shfl_xor_sync(FULL, low, 2));
-        if ((threadIdx.x & 3) == 0) s.groups[threadIdx.x / 4] = order_of(low);
+        if ((int)threadIdx.x < kept) {
+            const float best = of_order((uint32_t)(s.best[threadIdx.x] >> 32));
+            low = fmaxf(low, best - fabsf(best) * 0x1p-22f);
+        }
+        s.low[threadIdx.x] = order_of(low);
         __syncthreads();
-        if (threadIdx.x < 32) {
-            const uint32_t t = kth_largest(s.groups[lane_id()], s.groups[lane_id() + 32], a.K, 10);
-            if (lane_id() == 0) s.threshold = t;
+        if (warp == 0) {
+            // the K-th largest of the threads', or a number a little below it: 20 of its bits do
+            uint32_t x[BS_JOIN / 32], any = 0u, all = 0xffffffffu;
+#pragma unroll
+            for (int i = 0; i < BS_JOIN / 32; i++) {
+                x[i] = s.low[i * 32 + lane_id()];
+                any |= x[i];
+                all &= x[i];
+            }
+            const uint32_t differ = __reduce_or_sync(FULL, any) ^ __reduce_and_sync(FULL, all);
+            const int top = differ ? 31 - __clz(differ) : 0;
+            uint32_t t = top == 31 ? 0u : x[0] >> (top + 1) << (top + 1);
+            for (int bit = top; bit >= max(0, top - 20); bit--) {
+                const uint32_t tried = t | (1u << bit);
+                int n = 0;
+#pragma unroll
+                for (int i = 0; i < BS_JOIN / 32; i++) n += __popc(__ballot_sync(FULL, x[i] >= tried));
+                if (n >= a.K) t = tried;
+                if (n == a.K) break;
+            }
+            if (lane_id() == 0) s.threshold = max(t, 0x007fffffu);
         }
         __syncthreads();
         const float least = of_order(s.threshold);
@@ -484,22 +642,26 @@ __global__ void __launch_bounds__(BS_JOIN) beam_join_kernel(const __grid_constan
         };
         if ((int)threadIdx.x < kept) push(s.best[threadIdx.x], s.best_at[threadIdx.x]);
 #pragma unroll
-        for (int e = 0; e < BS_EACH; e++) {
-            if (!(hi[e] >= least)) continue;
-            int w, token;
-            float x;
-            if (entry(i0 + e * BS_JOIN + threadIdx.x, ahead[e], w, token, x)) push(order_of(value(w, x)), w * a.V + token);
-        }
+        for (int e = 0; e < BS_EACH; e++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                if (!(hi[e][h] >= least)) continue;
+                int token;
+                float x;
+                if (entry(list_w[e], list_part[e], lane_id() + 32 * h, ahead[e][h], token, x))
+                    push(value(list_w[e], x), list_w[e] * a.V + token);
+            }
         __syncthreads();
         const int n = s.count;
-        for (int i = threadIdx.x; i < n; i += BS_JOIN) {
+        for (int i = warp; i < n; i += BS_JOIN / 32) {
             const unsigned long long v = s.v[i];
             const int at = s.at[i];
-            int rank = 0;
-            for (int k = 0; k < n; k++) rank += s.v[k] > v || (s.v[k] == v && s.at[k] < at);
-            if (rank < a.K) {
-                s.best[rank] = v;
-                s.best_at[rank] = at;
+            int above = 0;
+            for (int k = lane_id(); k < n; k += 32) above += s.v[k] > v || (s.v[k] == v && s.at[k] < at);
+            above = __reduce_add_sync(FULL, above);
+            if (above < a.K && lane_id() == 0) {
+                s.best[above] = v;
+                s.best_at[above] = at;
             }
         }
         kept = min(n, a.K);
@@ -508,34 +670,47 @@ __global__ void __launch_bounds__(BS_JOIN) beam_join_kernel(const __grid_constan
     if ((int)threadIdx.x < a.K) {
         const long long o = (long long)blockIdx.x * a.K + threadIdx.x;
         const int at = s.best_at[threadIdx.x], w = at / a.V;
-        a.out_scores[o] = (float)of_order(s.best[threadIdx.x]);
+        a.out_scores[o] = of_order((uint32_t)(s.best[threadIdx.x] >> 32));
         a.parents[o] = (int)(row0 + w);
         a.tokens[o] = at - w * a.V;
     }
 }
 
-// Chunks of a row: 16-byte pieces that hold V logits wherever the row begins, in blocks' shares.
+// Units of a row: 16-byte pieces that hold V logits wherever the row begins, in blocks' shares.
 template <typename T>
-int chunks_of(int V) {
-    using H = Held<T>;
-    const int pieces = V % H::VEC ? (V + 2 * H::VEC - 2) / H::VEC : V / H::VEC, share = BS_THREADS * H::PIECES;
+int units_of(int V) {
+    using P = Piece<T>;
+    const int pieces = V % P::VEC ? (V + 2 * P::VEC - 2) / P::VEC : V / P::VEC, share = BS_THREADS * BS_HELD;
     return (pieces + share - 1) / share;
 }
-// (fp32 rows take at least as many as bf16 ones: the workspace is for either)
-int most_chunks(int V) { return chunks_of<float>(V); }
 
 bool refused(int N, int W, int V, int K) {
     return N < 0 || W < 1 || W > BS_MAX_W || V < 1 || V >= (1 << 24) || (long long)N * W >= (1 << 24) || K < 1 ||
-           K > BS_MAX_K || (long long)K > (long long)W * V || (long long)N * W * most_chunks(V) >= (1ll << 31);
+           K > BS_MAX_K || (long long)K > (long long)W * V;
 }
 
-size_t list_bytes(int N, int W, int V, int K) { return (size_t)N * W * most_chunks(V) * K * sizeof(unsigned long long); }
+size_t slots(int N, int W) { return (size_t)N * W + BS_MAX_CTAS; }
 
 template <typename T>
 moe_status launch(BeamArgs a, int N, cudaStream_t s) {
-    static moe_host::PerDevice smem;
-    a.chunks = chunks_of<T>(a.V);
-    beam_chunk_kernel<T><<<(unsigned)((long long)N * a.W * a.chunks), BS_THREADS, 0, s>>>(a);
+    static moe_host::PerDevice ring, smem, sms_of;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    const int sms = sms_of.get(dev, [&] {
+        int n = 0;
+        return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
+    });
+    if (sms == 0) return MOE_ERR_CUDA;
+    a.units = units_of<T>(a.V);
+    a.total = (long long)N * a.W * a.units;
+    const long long most = sms * BS_CTAS < BS_MAX_CTAS ? sms * BS_CTAS : BS_MAX_CTAS;
+    a.ctas = (int)(a.total < most ? a.total : most);
+    // a stretch has at least total / ctas units, rounded down: the stretches that a row's units can lie in
+    const long long least = a.total / a.ctas, parts = (a.units - 1 + least - 1) / least + 1;
+    a.segments = (int)(parts < a.units ? parts : a.units);
+    constexpr int RING = BS_RING * BS_HELD * BS_THREADS * sizeof(uint4);
+    if (!moe_host::allow_smem(beam_rows_kernel<T>, RING, ring)) return MOE_ERR_CUDA;
+    beam_rows_kernel<T><<<a.ctas, BS_THREADS, RING, s>>>(a);
     const moe_status st = moe_host::launch_status();
     if (st != MOE_OK) return st;
     if (!moe_host::allow_smem(beam_join_kernel, sizeof(Joined), smem) ||
@@ -550,8 +725,7 @@ moe_status launch(BeamArgs a, int N, cudaStream_t s) {
 extern "C" size_t moe_beam_select_workspace_size(int N, int W, int V, int K) {
     using namespace moe;
     if (refused(N, W, V, K)) return 0;
-    const size_t rows = (size_t)(N ? N : 1) * W;
-    return list_bytes(N ? N : 1, W, V, K) + rows * most_chunks(V) * sizeof(float2);
+    return slots(N, W) * (K * sizeof(unsigned long long) + sizeof(float2));
 }
 
 extern "C" moe_status moe_beam_select(const void* logits, moe_dtype dtype, const float* scores, const uint8_t* done, int pad,
@@ -568,8 +742,8 @@ extern "C" moe_status moe_beam_select(const void* logits, moe_dtype dtype, const
         !moe_host::aligned(parents, 4) || !moe_host::aligned(tokens, 4) || !moe_host::aligned(workspace, 16))
         return MOE_ERR_ALIGNMENT;
     if (N == 0) return MOE_OK;
-    BeamArgs a = {logits, scores, done, pad, W, V, K, 0, out_scores, parents, tokens, nullptr, nullptr};
+    BeamArgs a = {logits, scores, done, pad, W, V, K, 0, 0, 0, 0, out_scores, parents, tokens, nullptr, nullptr};
     a.list = static_cast<unsigned long long*>(workspace);
-    a.part = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + list_bytes(N, W, V, K));
+    a.part = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + slots(N, W) * K * sizeof(unsigned long long));
     return dtype == MOE_F32 ? launch<float>(a, N, moe_host::as_stream(stream)) : launch<__nv_bfloat16>(a, N, moe_host::as_stream(stream));
 }

@@ -1,7 +1,7 @@
 """Selection of a beam search's step against a plain 64-bit implementation, through the C ABI.
 
 Bars. The sum under a beam's logarithm is of at most 2^11 terms a thread in fp32, each off by 2^-22 of itself
-(exp), and in 64 bits above that; so lse errs by 2^-12 at most. What is compared is ids: they have to be the
+(exp), and in a few levels above that; so lse errs by 2^-12 at most. What is compared is ids: they have to be the
 reference's wherever its candidates are further apart than that, and everywhere in one beam, whose candidates
 all have the same error, and where nothing is rounded (equal beams, finished beams, -inf)."""
 import pytest
@@ -27,7 +27,9 @@ def _plain(logits, scores, K, done=None, pad=0):
     N, W, V = x.shape
     lse = torch.logsumexp(x, -1)
     alive = torch.isfinite(lse) & torch.isfinite(s)
-    c = s[..., None] + (x - torch.where(torch.isfinite(lse), lse, torch.zeros_like(lse))[..., None])
+    # (the maximum first: a row of the type's lowest values has a logarithm that 64 bits would lose beside them)
+    top = torch.where(torch.isfinite(lse), x.amax(-1), torch.zeros_like(lse))[..., None]
+    c = s[..., None] + ((x - top) - torch.log(torch.exp(x - top).sum(-1, keepdim=True)))
     c = torch.where(alive[..., None], c, torch.full_like(c, -INF))
     if done is not None:
         only = torch.full((V,), -INF, dtype=torch.float64)
