@@ -25,7 +25,7 @@ constexpr int BS_THREADS = 256;      // of the first kernel
 constexpr int BS_HELD = 8;           // a thread's 16-byte pieces of a unit
 constexpr int BS_GROUPS = BS_THREADS / 4;
 constexpr int BS_CAP = 1024;         // logits that are ranked against each other
-constexpr int BS_CHECK = 8;          // units between two looks at how many there are
+constexpr int BS_CHECK = 16;         // units between two looks at how many there are, at most
 constexpr int BS_CTAS = 3;           // blocks an SM
 constexpr int BS_RING = 2;           // units on their way or looked at
 constexpr int BS_MAX_CTAS = 1024;    // blocks at most: what the workspace has room for
@@ -41,8 +41,7 @@ struct BeamArgs {
     const uint8_t* done;
     int pad, W, V, K;
     int units, segments;             // units of a row; stretches that a row is in at most
-    int ctas;
-    long long total;                 // units of all rows
+    int ctas, each, longer;          // blocks; units of a block's stretch, one more for the first `longer` of them
     float* out_scores;
     int32_t* parents;
     int32_t* tokens;
@@ -66,9 +65,11 @@ struct Two {
         asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(o.v));
         return *this;
     }
-    __device__ __forceinline__ Two& operator*=(const Two& o) {
-        asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(o.v));
-        return *this;
+    // += 2^((x + shift) scale), 2^((y + shift) scale)
+    __device__ __forceinline__ void add_pow2(float x, float y, const Two& shift, const Two& scale) {
+        asm("{\n .reg .b64 t;\n .reg .f32 a, b;\n mov.b64 t, {%1, %2};\n add.rn.f32x2 t, t, %3;\n mul.rn.f32x2 t, t, %4;\n"
+            " mov.b64 {a, b}, t;\n ex2.approx.ftz.f32 a, a;\n ex2.approx.ftz.f32 b, b;\n mov.b64 t, {a, b};\n add.rn.f32x2 %0, %0, t;\n}"
+            : "+l"(v) : "f"(x), "f"(y), "l"(shift.v), "l"(scale.v));
     }
 };
 
@@ -112,6 +113,7 @@ struct Piece<float> {
     static constexpr int VEC = 4, LOWEST_BIT = 0;
     float v[VEC];
     __device__ __forceinline__ float at(int e) const { return v[e]; }
+    __device__ __forceinline__ float pick(int e) const { return e & 2 ? (e & 1 ? v[3] : v[2]) : (e & 1 ? v[1] : v[0]); }
     __device__ __forceinline__ void put(const uint4& x) {
         v[0] = __uint_as_float(x.x);
         v[1] = __uint_as_float(x.y);
@@ -131,6 +133,10 @@ struct Piece<__nv_bfloat16> {
     uint4 v;
     __device__ __forceinline__ uint32_t word(int w) const { return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w; }
     __device__ __forceinline__ float at(int e) const { return __uint_as_float(e & 1 ? word(e >> 1) & 0xffff0000u : word(e >> 1) << 16); }
+    __device__ __forceinline__ float pick(int e) const {
+        const uint32_t w = e & 4 ? (e & 2 ? v.w : v.z) : (e & 2 ? v.y : v.x);
+        return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+    }
     __device__ __forceinline__ void put(const uint4& x) { v = x; }
     __device__ __forceinline__ void some(const __nv_bfloat16* p, int first, int end) {
         uint32_t w[4];
@@ -221,8 +227,19 @@ __device__ __noinline__ int exactly_largest(const T* row, int first, int pieces,
     return min(*count, BS_CAP);
 }
 
-// best[rank] = key for the n keys of buf with a rank below K (all keys are different): a warp a key, its lanes the others.
+// best[rank] = key for the n keys of buf with a rank below K (all keys are different): a thread a key where they are few,
+// a warp where they are more, its lanes the others.
 __device__ __forceinline__ void rank_keys(const unsigned long long* buf, int n, int K, unsigned long long* best) {
+    if (n <= 64) {
+        if ((int)threadIdx.x < n) {
+            const unsigned long long key = buf[threadIdx.x];
+            int above = 0;
+#pragma unroll 4
+            for (int k = 0; k < n; k++) above += buf[k] > key;
+            if (above < K) best[above] = key;
+        }
+        return;
+    }
     for (int i = threadIdx.x / 32; i < n; i += BS_THREADS / 32) {
         const unsigned long long key = buf[i];
         int above = 0;
@@ -244,9 +261,9 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
     constexpr int STEP = BS_THREADS * P::VEC, UNIT = BS_HELD * STEP;   // tokens between a thread's pieces, and of a unit
     const int warp = threadIdx.x / 32;
     pdl_trigger();
-    const long long begin = a.total * blockIdx.x / a.ctas, end = a.total * (blockIdx.x + 1) / a.ctas;
+    const int begin = (int)blockIdx.x * a.each + min((int)blockIdx.x, a.longer), end = begin + a.each + ((int)blockIdx.x < a.longer);
     long long row = begin / a.units;
-    int u = (int)(begin - row * a.units);
+    int u = begin - (int)row * a.units;
     // pieces are counted from the last 16-byte boundary at or before the row, which is so many tokens before it
     auto skew_of = [&](long long r) { return (int)(r * a.V % P::VEC); };
     auto whole = [&](int t) { return t >= 0 && t + P::VEC <= a.V; };                  // a piece from token t on is all in the row
@@ -254,8 +271,8 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
 
     // the loading walk: a unit at a time, copies of what is whole
     const T* ld_base = static_cast<const T*>(a.logits) + row * a.V;    // token t's logit: base[t]
-    long long ld_row = row, ld_left = end - begin;
-    int ld_u = u, ld_skew = skew_of(row), ld_stage = 0;
+    long long ld_row = row;
+    int ld_left = end - begin, ld_u = u, ld_skew = skew_of(row), ld_stage = 0;
     auto issue = [&]() {
         if (ld_left > 0) {
             ld_left--;
@@ -286,13 +303,13 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
     int stage = 0;
     const T* base = static_cast<const T*>(a.logits) + row * a.V;
 
-    for (long long at = begin; at < end; row++, base += a.V, u = 0) {
-        const int u0 = u, u1 = (int)min((long long)a.units, u + (end - at)), skew = skew_of(row);
+    for (int at = begin; at < end; row++, base += a.V, u = 0) {
+        const int u0 = u, u1 = min(a.units, u + (end - at)), skew = skew_of(row);
         at += u1 - u;
         float least = -INFINITY;
         // sum of exponentials, relative to m (while that is -inf: 0, or NaN if there is one)
         float m = -INFINITY, sum = 0.0f;
-        int kept = 0;                                                  // in buf at the last look
+        int kept = 0, looked = 0;                                      // in buf at the last look, and units before it
         for (; u < u1; u++) {
             asm volatile("cp.async.wait_group %0;" ::"n"(BS_RING - 1) : "memory");
             const int token = u * UNIT + (int)threadIdx.x * P::VEC - skew;            // of the thread's first piece's first element
@@ -338,14 +355,8 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
 #pragma unroll
                 for (int i = 0; i < BS_HELD; i++)
 #pragma unroll
-                    for (int e = 0; e < P::VEC; e += 2) {
-                        Two x(p[i].at(e), p[i].at(e + 1));
-                        x += minus;
-                        x *= log2e;
-                        float x0, x1;
-                        x.get(x0, x1);
-                        (e & 2 ? sum1 : sum0) += Two(pow2(x0), pow2(x1));
-                    }
+                    for (int e = 0; e < P::VEC; e += 2)
+                        (e & 2 ? sum1 : sum0).add_pow2(p[i].at(e), p[i].at(e + 1), minus, log2e);
                 sum0 += sum1;
                 float s0, s1;
                 sum0.get(s0, s1);
@@ -365,26 +376,28 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
                 P q;
                 if (whole(t)) q.put(mine[i * BS_THREADS]);
                 else q.some(base + t, max(0, -t), min(P::VEC, a.V - t));
+                unsigned found = 0u;
 #pragma unroll
-                for (int e = 0; e < P::VEC; e++) {
-                    const float x = q.at(e);
-                    if (x >= least && (unsigned)(t + e) < (unsigned)a.V) {
-                        const int to = atomicAdd(&count, 1);
-                        if (to < BS_CAP) buf[to] = key_of(x, t + e);
-                    }
+                for (int e = 0; e < P::VEC; e++) found |= (unsigned)(q.at(e) >= least) << e;
+                while (found) {
+                    const int e = __ffs(found) - 1;
+                    found &= found - 1;
+                    if ((unsigned)(t + e) >= (unsigned)a.V) continue;
+                    const int to = atomicAdd(&count, 1);
+                    if (to < BS_CAP) buf[to] = key_of(q.pick(e), t + e);
                 }
             }
             issue();
             stage = stage + 1 == BS_RING ? 0 : stage + 1;
             const bool more = u + 1 < u1;
-            if (more && (u - u0) % BS_CHECK != BS_CHECK - 1) continue;
+            const int done = u - u0 + 1;                               // units of the row; looked at after 2, 8, 24, ... of them
+            if (more && done != 2 && done != 8 && done - looked < BS_CHECK) continue;
             // every few units: the K largest so far in order, the last of them the threshold
             __syncthreads();
             int n = count;
             __syncthreads();                                           // (nobody adds to it before all have read it)
             if (n > BS_CAP) {
-                const int since = (u - u0) % BS_CHECK;
-                n = exactly_largest<T>(base, token - since * UNIT, (since + 1) * BS_HELD, a.V, a.K, buf, kept, &count, scan);
+                n = exactly_largest<T>(base, token - (done - looked - 1) * UNIT, (done - looked) * BS_HELD, a.V, a.K, buf, kept, &count, scan);
             }
             rank_keys(buf, n, a.K, best);
             n = min(n, a.K);
@@ -395,6 +408,7 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
             if (n == a.K) least = of_order((uint32_t)(best[n - 1] >> 32) + 1u);
             __syncthreads();
             kept = n;
+            looked = done;
         }
         const long long to = blockIdx.x + row;
         if ((int)threadIdx.x < a.K) a.list[to * a.K + threadIdx.x] = (int)threadIdx.x < kept ? buf[threadIdx.x] : 0ull;
@@ -483,8 +497,13 @@ __global__ void __launch_bounds__(BS_JOIN) beam_join_kernel(const __grid_constan
     constexpr int TOGETHER = BS_JOIN / 32 * BS_EACH;
     // (the scores were there before the first kernel began, which this one runs beside)
     if ((int)threadIdx.x < a.W) {
-        const long long row = row0 + threadIdx.x, f = row * a.units;
-        const int g0 = (int)(((f + 1) * a.ctas - 1) / a.total), g1 = (int)(((f + a.units) * a.ctas - 1) / a.total);
+        // the block that has unit f
+        auto block_of = [&](int f) {
+            const int border = a.longer * (a.each + 1);
+            return f < border ? f / (a.each + 1) : a.longer + (f - border) / a.each;
+        };
+        const long long row = row0 + threadIdx.x;
+        const int f = (int)row * a.units, g0 = block_of(f), g1 = block_of(f + a.units - 1);
         s.first[threadIdx.x] = g0;
         s.parts[threadIdx.x] = g1 - g0 + 1;
         s.score[threadIdx.x] = a.scores[row];
@@ -686,7 +705,7 @@ int units_of(int V) {
 
 bool refused(int N, int W, int V, int K) {
     return N < 0 || W < 1 || W > BS_MAX_W || V < 1 || V >= (1 << 24) || (long long)N * W >= (1 << 24) || K < 1 ||
-           K > BS_MAX_K || (long long)K > (long long)W * V;
+           K > BS_MAX_K || (long long)K > (long long)W * V || (long long)N * W * units_of<float>(V) >= (1ll << 31);
 }
 
 size_t slots(int N, int W) { return (size_t)N * W + BS_MAX_CTAS; }
@@ -702,12 +721,13 @@ moe_status launch(BeamArgs a, int N, cudaStream_t s) {
     });
     if (sms == 0) return MOE_ERR_CUDA;
     a.units = units_of<T>(a.V);
-    a.total = (long long)N * a.W * a.units;
-    const long long most = sms * BS_CTAS < BS_MAX_CTAS ? sms * BS_CTAS : BS_MAX_CTAS;
-    a.ctas = (int)(a.total < most ? a.total : most);
-    // a stretch has at least total / ctas units, rounded down: the stretches that a row's units can lie in
-    const long long least = a.total / a.ctas, parts = (a.units - 1 + least - 1) / least + 1;
-    a.segments = (int)(parts < a.units ? parts : a.units);
+    const int total = N * a.W * a.units, most = sms * BS_CTAS < BS_MAX_CTAS ? sms * BS_CTAS : BS_MAX_CTAS;
+    a.ctas = total < most ? total : most;
+    a.each = total / a.ctas;
+    a.longer = total % a.ctas;
+    // the stretches that a row's units can lie in
+    const int parts = (a.units - 1 + a.each - 1) / a.each + 1;
+    a.segments = parts < a.units ? parts : a.units;
     constexpr int RING = BS_RING * BS_HELD * BS_THREADS * sizeof(uint4);
     if (!moe_host::allow_smem(beam_rows_kernel<T>, RING, ring)) return MOE_ERR_CUDA;
     beam_rows_kernel<T><<<a.ctas, BS_THREADS, RING, s>>>(a);
@@ -742,7 +762,7 @@ extern "C" moe_status moe_beam_select(const void* logits, moe_dtype dtype, const
         !moe_host::aligned(parents, 4) || !moe_host::aligned(tokens, 4) || !moe_host::aligned(workspace, 16))
         return MOE_ERR_ALIGNMENT;
     if (N == 0) return MOE_OK;
-    BeamArgs a = {logits, scores, done, pad, W, V, K, 0, 0, 0, 0, out_scores, parents, tokens, nullptr, nullptr};
+    BeamArgs a = {logits, scores, done, pad, W, V, K, 0, 0, 0, 0, 0, out_scores, parents, tokens, nullptr, nullptr};
     a.list = static_cast<unsigned long long*>(workspace);
     a.part = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + slots(N, W) * K * sizeof(unsigned long long));
     return dtype == MOE_F32 ? launch<float>(a, N, moe_host::as_stream(stream)) : launch<__nv_bfloat16>(a, N, moe_host::as_stream(stream));
