@@ -3,8 +3,9 @@
 //
 // Append and gather move rows between [n, heads, dim] and the pages: every byte once, 8 elements a thread, so
 // DRAM bounds long prompts and one launch a decoding step. Copies of pages are plain copies. Fork and compact
-// are index work on a table and a mark a page, a few hundred kilobytes: latency bounds them. They run as
-// one cluster of blocks whose phases are parted by cluster barriers, so a whole call is one launch.
+// are index work on a table and a mark a page, a few hundred kilobytes: latency bounds them. They run as one block
+// with the marks in shared memory where those fit and the table is not long, else as one cluster of eight blocks with
+// the marks in the workspace, phases parted by cluster barriers. So a whole call is one launch.
 #include "common.cuh"
 #include "paged_cache.cuh"
 
@@ -29,70 +30,78 @@ struct RowsArgs {
     CachePools c;
 };
 
-// The page of token i's position and the offset in it; false: skipped or bad.
-__device__ __forceinline__ bool place_of(const RowsArgs& a, int i, int* page, int* offset) {
+// The line (row of a head's pages, before the head) of token i's position; -1: skipped or bad.
+__device__ __forceinline__ long long line_of(const RowsArgs& a, int i) {
     const int pos = __ldg(a.positions + i);
     const int row = a.rows ? __ldg(a.rows + i) : i;
-    if (pos < 0 || row < 0) return false;
+    if (pos < 0 || row < 0) return -1;
     const int col = pos / a.c.page_size;
     const int p = row < a.S && col < a.M ? __ldg(a.table + (long long)row * a.M + col) : -1;
-    *page = p;
-    *offset = pos - col * a.c.page_size;
-    if ((unsigned)p < (unsigned)a.c.pages) return true;
+    if ((unsigned)p < (unsigned)a.c.pages) return (long long)p * a.c.heads * a.c.page_size + (pos - col * a.c.page_size);
     raise_device_error(MOE_DEVERR_BAD_ID);
-    return false;
+    return -1;
 }
 
-// A thread moves 8 elements of one token, head and side; four neighbours share a 32-element block.
-template <bool FP8, bool WRITE>
+// A thread moves one piece (8 elements of a side and head) of EACH tokens, so what depends on the piece is found once; four
+// neighbours share a 32-element block. A block's threads are a token's pieces (blockIdx.y: 256 of them), or those of
+// several tokens side by side where a token has fewer; its tokens are looked up once, by a thread each.
+template <bool FP8, bool WRITE, int EACH>
 __global__ void __launch_bounds__(RW_THREADS) cache_rows_kernel(const __grid_constant__ RowsArgs a) {
+    __shared__ long long lines[RW_THREADS / 4 * EACH];     // (a token has four pieces at least)
     const int dim8 = a.c.dim / 8, side = a.c.heads * dim8, per_token = 2 * side;
-    const long long total = (long long)a.n * per_token;
-    // (whole warps go round together: the quantiser's lanes exchange their maxima)
-    for (long long base = (long long)blockIdx.x * RW_THREADS; base < total; base += (long long)gridDim.x * RW_THREADS) {
-        const long long at = base + threadIdx.x;
-        const int i = (int)(at / per_token);
-        const int rest = (int)(at - (long long)i * per_token);
-        const bool is_v = rest >= side;
-        const int in_side = is_v ? rest - side : rest;
-        int page = 0, offset = 0;
-        const bool ok = at < total && place_of(a, i, &page, &offset);
-        char* const dense = static_cast<char*>(is_v ? a.v : a.k) + 2 * ((long long)i * (is_v ? a.v_stride : a.k_stride) + 8 * in_side);
-        const int head = in_side / dim8, d8 = in_side - head * dim8;
-        const long long line = ((long long)page * a.c.heads + head) * a.c.page_size + offset;
-        char* const pool = static_cast<char*>(is_v ? a.c.v : a.c.k);
-        if (!FP8) {
-            uint4* const at_pool = reinterpret_cast<uint4*>(pool + 2 * (line * a.c.dim + 8 * d8));
-            if (WRITE) {
-                if (ok) *at_pool = __ldg(reinterpret_cast<const uint4*>(dense));
-            } else if (at < total) {
-                *reinterpret_cast<uint4*>(dense) = ok ? __ldg(at_pool) : make_uint4(0, 0, 0, 0);
-            }
-        } else {
-            uint2* const at_pool = reinterpret_cast<uint2*>(pool + line * a.c.dim + 8 * d8);
-            uint8_t* const at_scale = (is_v ? a.c.v_scales : a.c.k_scales) + line * (a.c.dim / 32) + d8 / 4;
-            float f[8];
-            if (WRITE) {
-                bf16x8_to_f32(ok ? __ldg(reinterpret_cast<const uint4*>(dense)) : make_uint4(0, 0, 0, 0), f);
-                int byte;
-                const uint2 q = quant8_in_quad(f, &byte);
-                if (ok) {
-                    *at_pool = q;
-                    if ((d8 & 3) == 0) *at_scale = (uint8_t)byte;
-                }
-            } else if (at < total) {
-                uint4 out = make_uint4(0, 0, 0, 0);
-                if (ok) {
-                    const uint2 q = __ldg(at_pool);
-                    const float s = e8m0_value(__ldg(at_scale));
-                    e4m3x4_to_f32(q.x, f);
-                    e4m3x4_to_f32(q.y, f + 4);
+    const int beside = max(1, RW_THREADS / per_token);     // tokens side by side
+    const int token0 = blockIdx.x * beside * EACH;
+    if ((int)threadIdx.x < beside * EACH) lines[threadIdx.x] = token0 + (int)threadIdx.x < a.n ? line_of(a, token0 + threadIdx.x) : -1;
+    __syncthreads();
+    const int sub = per_token < RW_THREADS ? (int)threadIdx.x / per_token : 0;
+    const int piece = blockIdx.y * RW_THREADS + threadIdx.x - sub * per_token;
+    const bool mine = sub < beside && piece < per_token, is_v = piece >= side;
+    const int in_side = is_v ? piece - side : piece, head = in_side / dim8, d8 = in_side - head * dim8;
+    const long long stride = 2 * (is_v ? a.v_stride : a.k_stride);
+    char* const dense = static_cast<char*>(is_v ? a.v : a.k) + (long long)(token0 + sub) * stride + 16ll * in_side;
+    const long long line0 = (long long)head * a.c.page_size;
+    char* const pool = static_cast<char*>(is_v ? a.c.v : a.c.k) + (FP8 ? 1 : 2) * (line0 * a.c.dim + 8 * d8);
+    uint8_t* const scale = FP8 ? (is_v ? a.c.v_scales : a.c.k_scales) + line0 * (a.c.dim / 32) + d8 / 4 : nullptr;
+    long long line[EACH];
+    uint4 v[EACH];
 #pragma unroll
-                    for (int e = 0; e < 8; e++) f[e] *= s;
-                    out = f32_to_bf16x8(f);
-                }
-                *reinterpret_cast<uint4*>(dense) = out;
+    for (int e = 0; e < EACH; e++) {
+        line[e] = mine ? lines[e * beside + sub] : -1;
+        v[e] = make_uint4(0, 0, 0, 0);
+        if (line[e] < 0) continue;
+        if (WRITE) {
+            v[e] = __ldg(reinterpret_cast<const uint4*>(dense + e * beside * stride));
+        } else if (FP8) {
+            const uint2 q = __ldg(reinterpret_cast<const uint2*>(pool + line[e] * a.c.dim));
+            v[e] = make_uint4(q.x, q.y, __ldg(scale + line[e] * (a.c.dim / 32)), 0u);
+        } else {
+            v[e] = __ldg(reinterpret_cast<const uint4*>(pool + line[e] * (2 * a.c.dim)));
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < EACH; e++) {
+        float f[8];
+        const bool ok = line[e] >= 0;
+        if (WRITE && FP8) {
+            int byte;
+            bf16x8_to_f32(v[e], f);
+            const uint2 q = quant8_in_quad(f, &byte);
+            if (ok) {
+                *reinterpret_cast<uint2*>(pool + line[e] * a.c.dim) = q;
+                if ((d8 & 3) == 0) scale[line[e] * (a.c.dim / 32)] = (uint8_t)byte;
             }
+        } else if (WRITE) {
+            if (ok) *reinterpret_cast<uint4*>(pool + line[e] * (2 * a.c.dim)) = v[e];
+        } else if (mine && token0 + e * beside + sub < a.n) {
+            if (FP8) {
+                const float s = e8m0_value(v[e].z);
+                e4m3x4_to_f32(v[e].x, f);
+                e4m3x4_to_f32(v[e].y, f + 4);
+#pragma unroll
+                for (int k = 0; k < 8; k++) f[k] *= s;
+                v[e] = ok ? f32_to_bf16x8(f) : make_uint4(0, 0, 0, 0);
+            }
+            *reinterpret_cast<uint4*>(dense + e * beside * stride) = v[e];
         }
     }
 }
@@ -185,7 +194,11 @@ __global__ void __launch_bounds__(CP_THREADS) copy_pages_kernel(const __grid_con
 
 // ------------------------------------------------------------------ fork and compact
 constexpr int PG_THREADS = 1024;
-constexpr int PG_CTAS = 8;           // blocks of the cluster at most
+constexpr int PG_CTAS = 8;           // blocks of the cluster
+constexpr int PG_FLIGHT = 8;         // table entries that a thread has in flight
+constexpr int PG_NEAR = 4096;        // entries of the list of pages that shared memory holds
+constexpr size_t PG_SMEM = 200 * 1024;
+constexpr long long PG_ONE = 16;     // table entries a thread of the single block (32: 20 us against the cluster's 14.5)
 
 // Workspace: marks [pages], list [pages], counts [64] (int32), then for a fork offsets [rows].
 struct PagesWork {
@@ -266,12 +279,56 @@ __device__ __forceinline__ int length_of(const ForkArgs& a, int par) {
     return l < 0 ? 0 : (int)min((long long)l, (long long)a.M * a.page_size);
 }
 
+// The marks and the list of pages given out: in shared memory (ONE: a single block), or in the workspace.
+template <bool ONE>
+struct Marks {
+    uint32_t* m;
+    int32_t* near;                   // ONE: the list's first PG_NEAR entries
+    int32_t* far;
+    __device__ __forceinline__ uint32_t get(int p) const { return ONE ? m[p] : __ldcg(m + p); }
+    __device__ __forceinline__ int32_t* entry(int k) const { return ONE && k < PG_NEAR ? near + k : far + k; }
+    __device__ __forceinline__ int32_t listed(int k) const { return ONE && k < PG_NEAR ? near[k] : __ldcg(far + k); }
+};
+template <bool ONE>
+__device__ __forceinline__ void all_blocks() {
+    if (ONE) __syncthreads();
+    else cg::this_cluster().sync();
+}
+// f(e, i, j) for the entries of rows of M columns, PG_FLIGHT of them at a time by load(i, j) first.
+template <typename Load, typename Use>
+__device__ __forceinline__ void entries(long long total, int M, int thread, int threads, Load load, Use use) {
+    const int di = threads / M, dj = threads - di * M;
+    int i = thread / M, j = thread - i * M;
+    for (long long e = thread; e < total;) {
+        int32_t v[PG_FLIGHT];
+        int vi[PG_FLIGHT], vj[PG_FLIGHT];
+#pragma unroll
+        for (int k = 0; k < PG_FLIGHT; k++) {
+            vi[k] = i;
+            vj[k] = j;
+            v[k] = e + (long long)k * threads < total ? load(i, j) : -1;
+            i += di;
+            j += dj;
+            if (j >= M) {
+                j -= M;
+                i++;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < PG_FLIGHT; k++)
+            if (e + (long long)k * threads < total) use(vi[k], vj[k], v[k]);
+        e += (long long)PG_FLIGHT * threads;
+    }
+}
+
 // What row i, its pages copied and marked, needs: bit 30 a copy of its last page, below it the pages in all.
-__device__ __forceinline__ int needs_of(const ForkArgs& a, int i, int* held_out) {
+template <bool ONE>
+__device__ __forceinline__ int needs_of(const ForkArgs& a, const Marks<ONE>& marks, int i, int* held_out, int* last_out) {
     const int par = parent_of(a, i);
     const int l = length_of(a, par), ps = a.page_size;
     const int held = (l + ps - 1) / ps;
     *held_out = held;
+    *last_out = -1;
     if (par < 0 || par >= a.S) return 0;
     const int room = max(0, a.rooms ? __ldg(a.rooms + i) : a.room);
     if (room == 0) return 0;
@@ -279,99 +336,104 @@ __device__ __forceinline__ int needs_of(const ForkArgs& a, int i, int* held_out)
     int need = (int)end - held;
     if (l % ps) {
         const int page = __ldcg(a.new_table + (long long)i * a.M + held - 1);
+        *last_out = page;
         const uint32_t key = (uint32_t)(l - (held - 1) * ps) * a.S_new + (a.S_new - i);
-        if (page >= 0 && __ldcg(a.w.mark + page) != key) need = (need + 1) | (1 << 30);
+        if (page >= 0 && marks.get(page) != key) need = (need + 1) | (1 << 30);
     }
     return need;
 }
 
+template <bool ONE>
 __global__ void __launch_bounds__(PG_THREADS) cache_fork_kernel(const __grid_constant__ ForkArgs a) {
+    extern __shared__ __align__(16) uint32_t pg_smem[];
     __shared__ int red[PG_THREADS / 32];
-    cg::cluster_group cluster = cg::this_cluster();
+    const Marks<ONE> marks = {ONE ? pg_smem + PG_NEAR : a.w.mark, reinterpret_cast<int32_t*>(pg_smem), a.w.list};
     const int ctas = gridDim.x, b = blockIdx.x, ps = a.page_size;
     const int thread = b * PG_THREADS + threadIdx.x, threads = ctas * PG_THREADS;
-    for (int p = thread; p < a.pages; p += threads) a.w.mark[p] = 0u;
-    cluster.sync();
+    for (int p = thread; p < a.pages; p += threads) marks.m[p] = 0u;
+    all_blocks<ONE>();
 
     // rows: the parents' pages, each marked with the most positions that a row has in it, the first such row
-    for (int i = thread / 32; i < a.S_new; i += threads / 32) {
-        const int par = parent_of(a, i);
-        const bool bad = par < -1 || par >= a.S;
-        const int l = length_of(a, par);
-        if (lane_id() == 0) {
-            a.new_lengths[i] = l;
-            if (bad || (par >= 0 && !bad && __ldg(a.lengths + par) > l)) raise_device_error(MOE_DEVERR_BAD_ID);
-        }
-        for (int j = lane_id(); j < a.M; j += 32) {
-            int page = -1;
-            if ((long long)j * ps < l) {
-                page = __ldg(a.table + (long long)par * a.M + j);
-                if ((unsigned)page < (unsigned)a.pages) {
-                    const uint32_t fill = (uint32_t)min(l - j * ps, ps);
-                    atomicMax(a.w.mark + page, fill * a.S_new + (a.S_new - i));
+    for (int i = thread; i < a.S_new; i += threads) {
+        const int par = parent_of(a, i), l = length_of(a, par);
+        a.new_lengths[i] = l;
+        if (par < -1 || par >= a.S || (par >= 0 && __ldg(a.lengths + par) > l)) raise_device_error(MOE_DEVERR_BAD_ID);
+    }
+    entries((long long)a.S_new * a.M, a.M, thread, threads,
+            [&](int i, int j) {
+                const int par = parent_of(a, i);
+                return par >= 0 && par < a.S ? __ldg(a.table + (long long)par * a.M + j) : -1;
+            },
+            [&](int i, int j, int page) {
+                const int l = length_of(a, parent_of(a, i));
+                if ((long long)j * ps < l) {
+                    if ((unsigned)page < (unsigned)a.pages) {
+                        const uint32_t fill = (uint32_t)min(l - j * ps, ps);
+                        atomicMax(marks.m + page, fill * a.S_new + (a.S_new - i));
+                    } else {
+                        raise_device_error(MOE_DEVERR_BAD_ID);
+                        page = -1;
+                    }
                 } else {
-                    raise_device_error(MOE_DEVERR_BAD_ID);
                     page = -1;
                 }
-            }
-            a.new_table[(long long)i * a.M + j] = page;
-        }
-    }
-    cluster.sync();
+                a.new_table[(long long)i * a.M + j] = page;
+            });
+    all_blocks<ONE>();
 
     // free pages of this block's chunk, and (block 0) where each row's pages start among those that are given out
     int lo, hi;
     chunk_of(a.pages, b, ctas, &lo, &hi);
     int n = 0;
-    for (int p = lo + threadIdx.x; p < hi; p += PG_THREADS) n += __ldcg(a.w.mark + p) == 0u;
+    for (int p = lo + threadIdx.x; p < hi; p += PG_THREADS) n += marks.get(p) == 0u;
     n = block_sum(n, red);
-    if (threadIdx.x == 0) a.w.count[b] = n;
+    if (!ONE && threadIdx.x == 0) a.w.count[b] = n;
+    int wanted = 0, free_before = 0, free_all = n;
     if (b == 0) {
-        int base = 0;
         for (int i0 = 0; i0 < a.S_new; i0 += PG_THREADS) {
             const int i = i0 + threadIdx.x;
-            int held = 0, all;
-            const int need = i < a.S_new ? needs_of(a, i, &held) & ~(1 << 30) : 0;
-            const int at = base + block_scan(need, red, &all);
+            int held = 0, last, all;
+            const int need = i < a.S_new ? needs_of(a, marks, i, &held, &last) & ~(1 << 30) : 0;
+            const int at = wanted + block_scan(need, red, &all);
             if (i < a.S_new) a.w.row[i] = at;
-            base += all;
+            wanted += all;
         }
-        if (threadIdx.x == 0) a.w.count[PG_CTAS] = base;
+        if (!ONE && threadIdx.x == 0) a.w.count[PG_CTAS] = wanted;
     }
-    cluster.sync();
-
+    if (!ONE) {
+        all_blocks<ONE>();
+        wanted = __ldcg(a.w.count + PG_CTAS);
+        free_all = 0;
+        for (int c = 0; c < ctas; c++) {
+            const int f = __ldcg(a.w.count + c);
+            if (c < b) free_before += f;
+            free_all += f;
+        }
+    }
     // the free pages that are given out, in order
-    const int wanted = __ldcg(a.w.count + PG_CTAS);
-    int free_before = 0, free_all = 0;
-    for (int c = 0; c < ctas; c++) {
-        const int f = __ldcg(a.w.count + c);
-        if (c < b) free_before += f;
-        free_all += f;
-    }
     for (int p0 = lo; p0 < hi && free_before < wanted; p0 += PG_THREADS) {
         const int p = p0 + threadIdx.x;
-        const int is_free = p < hi && __ldcg(a.w.mark + p) == 0u;
+        const int is_free = p < hi && marks.get(p) == 0u;
         int all;
         const int at = free_before + block_scan(is_free, red, &all);
-        if (is_free && at < wanted) a.w.list[at] = p;
+        if (is_free && at < wanted) *marks.entry(at) = p;
         free_before += all;
     }
-    cluster.sync();
+    all_blocks<ONE>();
 
     for (int i = thread; i < a.S_new; i += threads) {
-        int held;
-        const int need = needs_of(a, i, &held), pages = need & ~(1 << 30);
+        int held, last;
+        const int need = needs_of(a, marks, i, &held, &last), pages = need & ~(1 << 30);
         const bool copy = need >> 30;
+        const int start = pages ? __ldcg(a.w.row + i) : 0;
         int from = -1, to = -1;
         for (int k = 0; k < pages; k++) {
-            const int at = __ldcg(a.w.row + i) + k;
-            const int page = at < free_all ? __ldcg(a.w.list + at) : -1;
-            int32_t* entry = a.new_table + (long long)i * a.M + held - copy + k;
+            const int page = start + k < free_all ? marks.listed(start + k) : -1;
             if (copy && k == 0) {
-                from = page >= 0 ? __ldcg(entry) : -1;
+                from = page >= 0 ? last : -1;
                 to = page;
             }
-            *entry = page;
+            a.new_table[(long long)i * a.M + held - copy + k] = page;
         }
         a.src[i] = from;
         a.dst[i] = to;
@@ -393,43 +455,46 @@ struct CompactArgs {
     PagesWork w;
 };
 
+template <bool ONE>
 __global__ void __launch_bounds__(PG_THREADS) cache_compact_kernel(const __grid_constant__ CompactArgs a) {
+    extern __shared__ __align__(16) uint32_t pg_smem[];
     __shared__ int red[PG_THREADS / 32];
-    cg::cluster_group cluster = cg::this_cluster();
+    const Marks<ONE> marks = {ONE ? pg_smem + PG_NEAR : a.w.mark, reinterpret_cast<int32_t*>(pg_smem), a.w.list};
     const int ctas = gridDim.x, b = blockIdx.x;
     const int thread = b * PG_THREADS + threadIdx.x, threads = ctas * PG_THREADS;
-    for (int p = thread; p < a.pages; p += threads) a.w.mark[p] = 0u;
-    cluster.sync();
-    for (long long j = thread; j < a.entries; j += threads) {
-        const int page = a.table[j];
-        if ((unsigned)page < (unsigned)a.pages) a.w.mark[page] = 1u;
-        else if (page != -1) raise_device_error(MOE_DEVERR_BAD_ID);
-    }
-    cluster.sync();
+    for (int p = thread; p < a.pages; p += threads) marks.m[p] = 0u;
+    all_blocks<ONE>();
+    entries(a.entries, 1, thread, threads, [&](int i, int) { return a.table[i]; },
+            [&](int, int, int page) {
+                if ((unsigned)page < (unsigned)a.pages) marks.m[page] = 1u;
+                else if (page != -1) raise_device_error(MOE_DEVERR_BAD_ID);
+            });
+    all_blocks<ONE>();
     int lo, hi;
     chunk_of(a.pages, b, ctas, &lo, &hi);
     int n = 0;
-    for (int p = lo + threadIdx.x; p < hi; p += PG_THREADS) n += __ldcg(a.w.mark + p) != 0u;
+    for (int p = lo + threadIdx.x; p < hi; p += PG_THREADS) n += marks.get(p) != 0u;
     n = block_sum(n, red);
-    if (threadIdx.x == 0) a.w.count[b] = n;
-    cluster.sync();
-
-    // live pages in all, before this chunk, and below that number of all
-    int live = 0, before = 0;
-    for (int c = 0; c < ctas; c++) {
-        const int f = __ldcg(a.w.count + c);
-        if (c < b) before += f;
-        live += f;
+    int live = n, before = 0;        // live pages in all, and before this chunk
+    if (!ONE) {
+        if (threadIdx.x == 0) a.w.count[b] = n;
+        all_blocks<ONE>();
+        live = 0;
+        for (int c = 0; c < ctas; c++) {
+            const int f = __ldcg(a.w.count + c);
+            if (c < b) before += f;
+            live += f;
+        }
     }
-    int below = 0;
+    int below = 0;                   // live pages below number `live`
     for (int c = 0; c < ctas; c++) {
         int clo, chi;
         chunk_of(a.pages, c, ctas, &clo, &chi);
         if (chi <= live) {
-            below += __ldcg(a.w.count + c);
+            below += ONE ? n : __ldcg(a.w.count + c);
         } else {
             int m = 0;
-            for (int p = clo + threadIdx.x; p < live; p += PG_THREADS) m += __ldcg(a.w.mark + p) != 0u;
+            for (int p = clo + threadIdx.x; p < live; p += PG_THREADS) m += marks.get(p) != 0u;
             below += block_sum(m, red);
             break;
         }
@@ -438,16 +503,17 @@ __global__ void __launch_bounds__(PG_THREADS) cache_compact_kernel(const __grid_
     // (marks below `live` stay as they are: other blocks may still count them)
     for (int p0 = lo; p0 < hi; p0 += PG_THREADS) {
         const int p = p0 + threadIdx.x;
-        const int is_live = p < hi && __ldcg(a.w.mark + p) != 0u;
+        const int is_live = p < hi && marks.get(p) != 0u;
         int all;
         const int lives = before + block_scan(is_live, red, &all);       // live pages below p
         before += all;
         if (p >= hi) continue;
         if (is_live && p >= live) {
             a.src[lives - below] = p;
-            a.w.mark[p] = 2u + (uint32_t)(lives - below);
+            marks.m[p] = 2u + (uint32_t)(lives - below);
         } else if (!is_live && p < live) {
             a.dst[p - lives] = p;
+            *marks.entry(p - lives) = p;
         }
     }
     for (int j = moved + thread; j < a.moves; j += threads) {
@@ -455,52 +521,62 @@ __global__ void __launch_bounds__(PG_THREADS) cache_compact_kernel(const __grid_
         a.dst[j] = -1;
     }
     if (thread == 0) *a.used = live;
-    cluster.sync();
-    for (long long j = thread; j < a.entries; j += threads) {
-        int page = a.table[j];
-        if ((unsigned)page < (unsigned)a.pages) {
-            const uint32_t m = __ldcg(a.w.mark + page);
-            if (m >= 2u) page = __ldcg(a.dst + (m - 2u));
-        } else {
-            page = -1;
-        }
-        a.new_table[j] = page;
-    }
+    all_blocks<ONE>();
+    entries(a.entries, 1, thread, threads, [&](int i, int) { return a.table[i]; },
+            [&](int i, int, int page) {
+                if ((unsigned)page < (unsigned)a.pages) {
+                    const uint32_t m = marks.get(page);
+                    if (m >= 2u) page = marks.listed((int)(m - 2u));
+                } else {
+                    page = -1;
+                }
+                a.new_table[i] = page;
+            });
 }
 
+// One block where the marks fit its shared memory and its threads have few entries each; a cluster above.
 template <typename Args>
-moe_status launch_cluster(void (*kernel)(const Args), const Args& a, int ctas, cudaStream_t s) {
+moe_status launch_pages(void (*one)(const Args), void (*many)(const Args), moe_host::PerDevice& done, const Args& a, int pages,
+                        long long entries, cudaStream_t s) {
+    const size_t smem = (PG_NEAR + (size_t)pages) * sizeof(uint32_t);
+    if (smem <= PG_SMEM && entries <= PG_ONE * PG_THREADS) {
+        if (!moe_host::allow_smem(one, smem, done)) return MOE_ERR_CUDA;
+        one<<<1, PG_THREADS, smem, s>>>(a);
+        return moe_host::launch_status();
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
+    cfg.gridDim = dim3(PG_CTAS);
     cfg.blockDim = dim3(PG_THREADS);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.x = PG_CTAS;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, many, a) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
     return moe_host::launch_status();
 }
 
-// Blocks of the cluster: one where its threads have a handful of entries each.
-int pages_ctas(long long work) { return work <= 8 * PG_THREADS ? 1 : PG_CTAS; }
-
 moe_status rows_call(RowsArgs a, moe_dtype dtype, bool write, moe_stream_t stream) {
     const long long total = (long long)a.n * 2 * a.c.heads * (a.c.dim / 8);
-    const long long ctas = (total + RW_THREADS - 1) / RW_THREADS;
-    const dim3 grid((unsigned)(ctas < (1 << 20) ? ctas : (1 << 20)));
+    const long long per_token = 2ll * a.c.heads * (a.c.dim / 8), beside = per_token < RW_THREADS ? RW_THREADS / per_token : 1;
+    // four tokens a thread (four loads in flight) where that still fills the device twice over; one, for latency, below
+    const int each = total >= 4ll * RW_THREADS * 2048 ? 4 : 1;
+    const long long ctas = (a.n + beside * each - 1) / (beside * each), rows = (per_token + RW_THREADS - 1) / RW_THREADS;
+    if (rows > 65535) return MOE_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)ctas, (unsigned)rows);
     const cudaStream_t s = moe_host::as_stream(stream);
+    auto go = [&](auto kernel) { kernel<<<grid, RW_THREADS, 0, s>>>(a); };
     if (dtype == MOE_MXFP8) {
-        if (write) cache_rows_kernel<true, true><<<grid, RW_THREADS, 0, s>>>(a);
-        else cache_rows_kernel<true, false><<<grid, RW_THREADS, 0, s>>>(a);
+        if (write) each == 4 ? go(cache_rows_kernel<true, true, 4>) : go(cache_rows_kernel<true, true, 1>);
+        else each == 4 ? go(cache_rows_kernel<true, false, 4>) : go(cache_rows_kernel<true, false, 1>);
     } else {
-        if (write) cache_rows_kernel<false, true><<<grid, RW_THREADS, 0, s>>>(a);
-        else cache_rows_kernel<false, false><<<grid, RW_THREADS, 0, s>>>(a);
+        if (write) each == 4 ? go(cache_rows_kernel<false, true, 4>) : go(cache_rows_kernel<false, true, 1>);
+        else each == 4 ? go(cache_rows_kernel<false, false, 4>) : go(cache_rows_kernel<false, false, 1>);
     }
     return moe_host::launch_status();
 }
@@ -564,7 +640,7 @@ extern "C" moe_status moe_cache_fork(const int32_t* table, const int32_t* length
                                      void* workspace, size_t workspace_bytes, moe_stream_t stream) {
     using namespace moe;
     if (S_new < 0 || S < 0 || M < 1 || pages < 1 || page_size < 1 || page_size > MOE_CACHE_MAX_PAGE ||
-        (long long)M * page_size >= (1ll << 31) || (long long)page_size * S_new >= (1ll << 31) - S_new)
+        (long long)M * page_size >= (1ll << 31) || (long long)page_size * S_new >= (1ll << 31) - S_new || (long long)M * S_new >= (1ll << 31))
         return MOE_ERR_INVALID_ARG;
     if (!parents && S_new != S) return MOE_ERR_INVALID_ARG;
     if ((S > 0 && (!table || !lengths)) || !used) return MOE_ERR_INVALID_ARG;
@@ -576,7 +652,9 @@ extern "C" moe_status moe_cache_fork(const int32_t* table, const int32_t* length
         if (!moe_host::aligned(p, 4)) return MOE_ERR_ALIGNMENT;
     const ForkArgs a = {table, lengths, parents, rooms, S, M, S_new, pages, page_size, room, new_table, new_lengths, src, dst,
                         used, pages_work(workspace, pages)};
-    return launch_cluster(cache_fork_kernel, a, pages_ctas((long long)S_new * M + pages), moe_host::as_stream(stream));
+    static moe_host::PerDevice done;
+    return launch_pages(cache_fork_kernel<true>, cache_fork_kernel<false>, done, a, pages, (long long)S_new * M,
+                        moe_host::as_stream(stream));
 }
 
 extern "C" moe_status moe_cache_compact(const int32_t* table, int S, int M, int pages, int32_t* new_table, int32_t* src,
@@ -590,7 +668,9 @@ extern "C" moe_status moe_cache_compact(const int32_t* table, int S, int M, int 
         if (!moe_host::aligned(p, 4)) return MOE_ERR_ALIGNMENT;
     const long long entries = (long long)S * M;
     const CompactArgs a = {table, pages, pages / 2, entries, new_table, src, dst, used, pages_work(workspace, pages)};
-    return launch_cluster(cache_compact_kernel, a, pages_ctas(entries + pages), moe_host::as_stream(stream));
+    static moe_host::PerDevice done;
+    if (entries >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+    return launch_pages(cache_compact_kernel<true>, cache_compact_kernel<false>, done, a, pages, entries, moe_host::as_stream(stream));
 }
 
 extern "C" moe_status moe_cache_copy_pages(void* const* tensors, const long long* page_bytes, int n_tensors,

@@ -667,7 +667,7 @@ moe_status moe_paged_attention(const void *q, long long q_stride, int B, int q_h
  * rows in ascending order, the copied page first. Pages that no row names any more are free.
  * *used: the pages named in the end, and those that were missing (then *used > pages,
  * MOE_DEVERR_NO_PAGE is set and the entries stay -1). Outputs must not overlap inputs.
- * Requires page_size * S_new < 2^31.
+ * Requires (page_size + 1) * S_new < 2^31, M * S_new < 2^31 (compact: M * S).
  *
  * moe_cache_compact: the named pages renumbered to 0 .. *used - 1: the i-th page at or above
  * *used goes to the i-th hole below it. new_table: the rows with the new numbers; src, dst
