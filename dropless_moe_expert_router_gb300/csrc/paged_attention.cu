@@ -769,35 +769,87 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
     copies_wait<0>();
 }
 
-// Pairs that were cut: block (i, h) joins head h of the one that begins in block i of the first kernel.
+// Pairs that were cut: block (i, g) joins four heads of the one that begins in block i of the first kernel. Its threads
+// take four elements of a head each, in groups that share the pieces out; a piece's loads do not wait for the maxima.
+constexpr int PA_JOIN = 512;
+constexpr int PA_JOIN_HEADS = 4;
+
 template <bool FP8, int DP, int NB>
-__global__ void __launch_bounds__(DP) attention_join_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(PA_JOIN) attention_join_kernel(const __grid_constant__ AttnArgs a) {
     using C = Cfg<FP8, DP, NB>;
+    constexpr int LANES = DP / 4, GROUPS = PA_JOIN / LANES / PA_JOIN_HEADS, AHEAD = 8;
+    __shared__ float factor[PA_JOIN_HEADS][PA_MAX_CTAS], sums[PA_JOIN_HEADS], tops[PA_JOIN_HEADS];
+    __shared__ float4 joined[GROUPS][PA_JOIN_HEADS][LANES];
+    const int lane = threadIdx.x % LANES, at = threadIdx.x / LANES, hh = at % PA_JOIN_HEADS, g = at / PA_JOIN_HEADS;
+    const int h = blockIdx.y * PA_JOIN_HEADS + hh, warp = threadIdx.x / 32;
     pdl_wait();
     const int4 cut = __ldcg(a.cut + blockIdx.x);
     if (cut.x < 0) return;
-    const int kv = cut.y / a.tiles_of_heads, group = a.q_heads / a.c.heads, h = blockIdx.y;
-    const int head = (cut.y - kv * a.tiles_of_heads) * 8 * NB + h, d = threadIdx.x;
-    if (head >= group) return;
-    const int first = 2 * blockIdx.x + 1;           // its slot; the blocks after it have theirs at 2 (i + k)
+    // the first piece is in the block's second slot; the blocks after it have theirs in their first
     const int parts = cut.z + 1;
-    auto slot_of = [&](int k) { return (long long)(k ? 2 * (blockIdx.x + k) : first); };
-    float top = -INFINITY;
-    for (int k = lane_id(); k < parts; k += 32) top = fmaxf(top, __ldcg(a.part_ml + slot_of(k) * 8 * NB + h).x);
+    auto slot_of = [&](int k) { return (long long)(k ? 2 * (blockIdx.x + k) : 2 * blockIdx.x + 1); };
+    auto piece = [&](int k) {
+        return k < parts ? __ldcg(reinterpret_cast<const float4*>(a.part + slot_of(k) * C::SLOT + h * DP) + lane) : make_float4(0, 0, 0, 0);
+    };
+    float4 y[AHEAD];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-    float sum = 0.0f, v = 0.0f;
-#pragma unroll 8
-    for (int k = 0; k < parts; k++) {
-        const float2 x = __ldcg(a.part_ml + slot_of(k) * 8 * NB + h);
-        const float y = d < a.c.dim ? __ldcg(a.part + slot_of(k) * C::SLOT + h * DP + d) : 0.0f;
-        const float f = top == -INFINITY ? 1.0f : pow2(x.x - top);
-        sum += x.y * f;
-        v += y * f;
+    for (int e = 0; e < AHEAD; e++) y[e] = piece(g + e * GROUPS);
+    if (warp < PA_JOIN_HEADS) {
+        const float2* const ml = a.part_ml + blockIdx.y * PA_JOIN_HEADS + warp;
+        float top = -INFINITY, sum = 0.0f;
+        for (int k = lane_id(); k < parts; k += 32) top = fmaxf(top, __ldcg(ml + slot_of(k) * 8 * NB).x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+        for (int k = lane_id(); k < parts; k += 32) {
+            const float2 x = __ldcg(ml + slot_of(k) * 8 * NB);
+            const float f = top == -INFINITY ? 1.0f : pow2(x.x - top);
+            factor[warp][k] = f;
+            sum += x.y * f;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+        if (lane_id() == 0) {
+            tops[warp] = top;
+            sums[warp] = sum;
+        }
+    }
+    __syncthreads();
+    float4 v = make_float4(0, 0, 0, 0);
+    for (int k0 = g; k0 < parts; k0 += AHEAD * GROUPS) {
+#pragma unroll
+        for (int e = 0; e < AHEAD; e++) {
+            const int k = k0 + e * GROUPS;
+            if (k >= parts) break;
+            const float f = factor[hh][k];
+            v.x += y[e].x * f;
+            v.y += y[e].y * f;
+            v.z += y[e].z * f;
+            v.w += y[e].w * f;
+        }
+#pragma unroll
+        for (int e = 0; e < AHEAD; e++) y[e] = piece(k0 + (AHEAD + e) * GROUPS);
+    }
+    joined[g][hh][lane] = v;
+    __syncthreads();
+    const int kv = cut.y / a.tiles_of_heads, group = a.q_heads / a.c.heads, head = (cut.y - kv * a.tiles_of_heads) * 8 * NB + h;
+    if (g > 0 || head >= group) return;
+#pragma unroll
+    for (int e = 1; e < GROUPS; e++) {
+        const float4 o = joined[e][hh][lane];
+        v.x += o.x;
+        v.y += o.y;
+        v.z += o.z;
+        v.w += o.w;
     }
     const long long row = (long long)cut.x * a.q_heads + kv * group + head;
-    if (d < a.c.dim) a.out[row * a.c.dim + d] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : v / sum);
-    if (a.lse && d == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum) - (FP8 ? 15.0f : 0.0f)) * 0.69314718055994530942f;
+    const float sum = sums[hh], inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (lane * 4 < a.c.dim) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv), up = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+        *reinterpret_cast<uint2*>(a.out + row * a.c.dim + lane * 4) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&up));
+    }
+    if (a.lse && lane == 0)
+        a.lse[row] = sum == 0.0f ? -INFINITY : (tops[hh] + log2f(sum) - (FP8 ? 15.0f : 0.0f)) * 0.69314718055994530942f;
 }
 
 // Blocks of 8 query heads that a warp holds at once, by the group: what does not fit is another pass over the cache.
@@ -829,7 +881,7 @@ moe_status launch(const AttnArgs& a, cudaStream_t s) {
     attention_kernel<FP8, DP, NB><<<(unsigned)ctas, PA_THREADS, C::SMEM, s>>>(a);
     const moe_status st = moe_host::launch_status();
     if (st != MOE_OK || a.whole) return st;
-    if (moe_host::launch_pdl(attention_join_kernel<FP8, DP, NB>, dim3((unsigned)ctas, 8 * NB), dim3(DP), 0, s, a) != cudaSuccess)
+    if (moe_host::launch_pdl(attention_join_kernel<FP8, DP, NB>, dim3((unsigned)ctas, 8 * NB / PA_JOIN_HEADS), dim3(PA_JOIN), 0, s, a) != cudaSuccess)
         return MOE_ERR_CUDA;
     return moe_host::launch_status();
 }
