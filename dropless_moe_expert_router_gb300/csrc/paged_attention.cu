@@ -335,30 +335,33 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
             constexpr int PER = 32 / C::CHUNKS;    // rows that an instruction of the warp copies
             const char* const kp = static_cast<const char*>(a.c.k) + ld_chunk * 16;
             const char* const vp = static_cast<const char*>(a.c.v) + ld_chunk * 16;
-            const bool all = rows == (C::TILE == 32 ? FULL : 0xffffu) && row_bytes == C::ROW;
-            const unsigned mine = ld_chunk * 16 < row_bytes ? rows >> ld_row : 0u;
+            // a row's chunk in a tile of keys or values, where the fragments' reads meet all banks
+            auto kx = [&](int row) { return !FP8 ? row & 7 : DP == 64 ? ((row >> 1) & 1) << 1 : (row & 3) << 1; };
+            auto vx = [&](int row) { return !FP8 ? row & 7 : DP == 64 ? ((row >> 1) & 1) << 1 : ((row >> 1) & 3) << 1; };
+            // Sixteen rows that follow one another (a page, or a part of it) need one address.
+            const long long half = __shfl_sync(FULL, line, lane & 16 & (C::TILE - 1));
+            const bool run = __all_sync(FULL, ok && line == half + (lane & 15)) && row_bytes == C::ROW;
+            if (run) {
 #pragma unroll
-            for (int i = 0; i < C::TILE / PER; i++) {
-                const int row = i * PER + ld_row;
-                const long long from = __shfl_sync(FULL, row_at, row);
-                int kx, vx;                        // the chunk's place, so that the fragments' reads meet all banks
-                if (!FP8) {
-                    kx = vx = ld_chunk ^ (row & 7);
-                } else if (DP == 64) {
-                    kx = vx = ld_chunk ^ (((row >> 1) & 1) << 1);
-                } else {
-                    kx = ld_chunk ^ ((row & 3) << 1);
-                    vx = ld_chunk ^ (((row >> 1) & 3) << 1);
+                for (int x = 0; x < C::SUB; x++) {
+                    const long long from = __shfl_sync(FULL, row_at, x * 16) + ld_row * C::ROW;
+#pragma unroll
+                    for (int i = 0; i < 16 / PER; i++) {
+                        const int row = x * 16 + i * PER + ld_row;
+                        copy16(at + row * C::ROW + (ld_chunk ^ kx(row)) * 16, kp + from + i * PER * C::ROW);
+                        copy16(at + (C::TILE + row) * C::ROW + (ld_chunk ^ vx(row)) * 16, vp + from + i * PER * C::ROW);
+                    }
                 }
-                const uint32_t kt = at + row * C::ROW + kx * 16, vt = at + (C::TILE + row) * C::ROW + vx * 16;
-                if (all) {
-                    copy16(kt, kp + from);
-                    copy16(vt, vp + from);
-                } else {
+            } else {
+                const unsigned mine = ld_chunk * 16 < row_bytes ? rows >> ld_row : 0u;
+#pragma unroll
+                for (int i = 0; i < C::TILE / PER; i++) {
+                    const int row = i * PER + ld_row;
+                    const long long from = __shfl_sync(FULL, row_at, row);
                     // (a chunk that is not there is zeros, and its address the pool's first)
                     const bool there = (mine >> (i * PER)) & 1;
-                    copy16(kt, there ? kp + from : static_cast<const char*>(a.c.k), there);
-                    copy16(vt, there ? vp + from : static_cast<const char*>(a.c.v), there);
+                    copy16(at + row * C::ROW + (ld_chunk ^ kx(row)) * 16, there ? kp + from : static_cast<const char*>(a.c.k), there);
+                    copy16(at + (C::TILE + row) * C::ROW + (ld_chunk ^ vx(row)) * 16, there ? vp + from : static_cast<const char*>(a.c.v), there);
                 }
             }
             if (FP8) {
@@ -368,13 +371,18 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                 for (int x = 0; x < C::SUB; x++) {
                     const bool is_v = C::SUB == 2 ? x == 1 : lane >= 16;
                     const uint8_t* const base = (is_v ? a.c.v_scales : a.c.k_scales) + scales_at;
-                    const int skip = (int)(reinterpret_cast<uintptr_t>(base) & 3);
                     const uint32_t slot = at + C::KV + (x * 32 + lane) * 16;
-                    const int words = (skip + row_scales + 3) / 4;
+                    if (row_scales == DP / 32 && DP >= 128) {          // whole words
 #pragma unroll
-                    for (int i = 0; i < (DP / 32 + 6) / 4; i++)
-                        if (i < words) copy4(slot + 4 * i, base - skip + 4 * i, ok);
-                    sts32(slot + 12, ok ? 8u * skip : 0u);
+                        for (int i = 0; i < DP / 128; i++) copy4(slot + 4 * i, base + 4 * i, ok);
+                        sts32(slot + 12, 0u);
+                    } else {
+                        const int skip = (int)(reinterpret_cast<uintptr_t>(base) & 3), words = (skip + row_scales + 3) / 4;
+#pragma unroll
+                        for (int i = 0; i < (DP / 32 + 6) / 4; i++)
+                            if (i < words) copy4(slot + 4 * i, base - skip + 4 * i, ok);
+                        sts32(slot + 12, ok ? 8u * skip : 0u);
+                    }
                 }
             }
             if (lane == 0) seen[fill] = rows;
@@ -500,7 +508,8 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                     for (int i = 0; i < DP / 32; i++) {
                         if (i >= row_scales) continue;
                         if (!is_v) {
-                            sts32(prep + (i * C::TILE + row) * 4, __float_as_uint(e8m0_value(byte[x][i])));
+                            // (2^-127 is half of the least normal number)
+                            sts32(prep + (i * C::TILE + row) * 4, byte[x][i] == 255u ? 0x7fc00000u : max(byte[x][i] << 23, 0x00400000u));
                         } else {
                             const int y = (int)byte[x][i] - vref;
                             uint32_t f = wide ? (uint32_t)max(0, 127 + y) << 7 : (uint32_t)max(0, 15 + y) << 10;
