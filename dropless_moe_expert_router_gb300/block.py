@@ -7,6 +7,9 @@ The block keeps the residual stream and the update apart, as a stack of blocks h
 training step is ``forward``, ``backward``, ``clip_gradients``, an optimiser's update of the parameters
 in place, and ``repack``; serving calls ``step`` with the few tokens of a decoding step. The router's projection is an ordinary dense product and is
 left to torch; the norm, the layer, their backward passes and the clipping are the library's.
+
+A block that serves may begin with attention over a cache (``Attention``): then ``step`` is a whole decoder
+block's, s' = x + delta, delta'' = Attention(LayerNorm(s')), and the MoE part as above on (s', delta'').
 """
 from __future__ import annotations
 
@@ -15,17 +18,50 @@ from typing import Optional
 import torch
 
 from . import api
+from .cache import SequenceCache
 from .layer import MoELayer
+
+
+class Attention:
+    """Pre-norm attention of one new token per sequence over a cache. The two projections are torch's."""
+
+    def __init__(self, qkv: torch.Tensor, out: torch.Tensor, norm_weight: torch.Tensor,
+                 norm_bias: Optional[torch.Tensor] = None, *, q_heads: int, kv_heads: int, scale: Optional[float] = None,
+                 window: int = 0, eps: float = 1e-5):
+        """qkv [(q_heads + 2 kv_heads) * dim, H] bf16 (queries, keys, values), out [H, q_heads * dim] bf16, norm_weight and
+        norm_bias [H]; scale and window are moe_paged_attention's."""
+        rows, H = qkv.shape
+        if kv_heads < 1 or q_heads < 1 or q_heads % kv_heads or rows % (q_heads + 2 * kv_heads):
+            raise ValueError("qkv must be [(q_heads + 2 kv_heads) * dim, H], q_heads a multiple of kv_heads")
+        dim = rows // (q_heads + 2 * kv_heads)
+        if tuple(out.shape) != (H, q_heads * dim) or qkv.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
+            raise ValueError("qkv and out must be bfloat16, out [H, q_heads * dim]")
+        self.qkv, self.out = qkv, out
+        self.norm_weight, self.norm_bias, self.eps = norm_weight, norm_bias, eps
+        self.q_heads, self.kv_heads, self.dim, self.scale, self.window = q_heads, kv_heads, dim, scale, window
+
+    def step(self, x: torch.Tensor, delta: Optional[torch.Tensor], cache: SequenceCache, layer: int):
+        """x (and delta) [t, H], one row a slot of the cache, whose `advance` came before -> (s, delta')."""
+        o = api.moe_layer_norm(x, self.norm_weight, self.norm_bias, self.eps, residual=delta)
+        nq, nkv = self.q_heads, self.kv_heads
+        qkv = torch.mm(o.y, self.qkv.t()).view(x.shape[0], nq + 2 * nkv, self.dim)
+        cache.append(layer, qkv[:, nq:nq + nkv], qkv[:, nq + nkv:])
+        heads = cache.attend(layer, qkv[:, :nq], scale=self.scale, window=self.window)
+        return o.sum, torch.mm(heads.view(x.shape[0], -1), self.out.t())
 
 
 class MoEBlock:
     def __init__(self, w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, router: torch.Tensor,
                  norm_weight: torch.Tensor, norm_bias: Optional[torch.Tensor] = None, *, T: int, K: int,
-                 eps: float = 1e-5, **layer_args):
+                 eps: float = 1e-5, attention: Optional[Attention] = None, index: int = 0, **layer_args):
         """Expert weights as MoELayer takes them, router [E, H] fp32, norm_weight and norm_bias [H];
         the remaining arguments are MoELayer's (precision, renorm, training, score, ...). The block keeps
-        the tensors themselves; the layer also keeps packed copies of w1, w3 and w2 (``repack``)."""
+        the tensors themselves; the layer also keeps packed copies of w1, w3 and w2 (``repack``).
+        attention: what a decoder block's step begins with (serving only); index: the block's layer of the cache."""
         E, H, _ = w1.shape
+        if attention is not None and (attention.qkv.shape[1] != H or layer_args.get("training")):
+            raise ValueError("attention is of the block's width, and in a block that serves")
+        self.attention, self.index = attention, index
         if tuple(router.shape) != (E, H) or router.dtype != torch.float32:
             raise ValueError("router must be [E, H] float32")
         self.layer = MoELayer(w1, w3, w2, T=T, K=K, **layer_args)
@@ -40,15 +76,22 @@ class MoEBlock:
 
     def forward(self, x: torch.Tensor, delta: Optional[torch.Tensor] = None):
         """x (and delta) [T, H] bf16 -> (s [T, H], delta' [T, H], a layer-owned buffer)."""
+        if self.attention is not None:
+            raise ValueError("a block with attention over a cache goes by steps")
         o, logits = self._norm(x, delta)
         out = self.layer.forward(o.y, logits)
         if self.layer.training:
             self._saved = (o, logits)
         return o.sum, out
 
-    def step(self, x: torch.Tensor, delta: Optional[torch.Tensor] = None):
+    def step(self, x: torch.Tensor, delta: Optional[torch.Tensor] = None, cache: Optional[SequenceCache] = None):
         """The block for the few tokens of a decoding step: x (and delta) [t, H], t <= 64. Steps share a
-        workspace (MoELayer.forward_few) and must not overlap on the GPU."""
+        workspace (MoELayer.forward_few) and must not overlap on the GPU. A block with attention wants the cache, and a row
+        for each of its slots."""
+        if (self.attention is None) != (cache is None):
+            raise ValueError("a cache goes with a block that has attention")
+        if cache is not None:
+            x, delta = self.attention.step(x, delta, cache, self.index)
         o, logits = self._norm(x, delta)
         return o.sum, self.layer.forward_few(o.y, logits)
 

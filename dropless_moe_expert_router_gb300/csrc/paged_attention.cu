@@ -35,7 +35,7 @@ constexpr int PA_WARPS = 4;
 constexpr int PA_THREADS = 32 * PA_WARPS;
 constexpr int PA_MAX_CTAS = 512;                  // blocks at most: what the workspace has room for
 constexpr int PA_BEGIN = 2;                       // units that beginning and ending a pair takes as long as
-constexpr int PA_MIN_UNITS = 4;                   // of a block's stretch: a shorter one costs more to join than it saves
+constexpr int PA_MIN_UNITS = 2;                   // of a block's stretch: a shorter one costs more to join than it saves
 constexpr int PA_WHOLE = 256;                     // positions that a pair is not cut for
 constexpr int PA_SPREAD = 6;                      // exponents below the largest scale that fp16 weights take
 
