@@ -1034,36 +1034,44 @@ def cache_buffers(pages: int, heads: int, page_size: int, dim: int, device, prec
 
 def _want_cache(c: PagedCache, dev: int) -> int:
     """The pools have the shape that the cache says, on this device; its type's code."""
-    code = _dt_code(c.precision)
+    precision, pages, heads, page_size, dim, k, k_scales, v, v_scales = c
+    if precision == "bf16":
+        shape = (pages, heads, page_size, dim)
+        # (one expression: a decoding step makes this check a few times a layer)
+        if (k is not None and v is not None and k.dtype is v.dtype is torch.bfloat16 and k.shape == v.shape == shape
+                and k.get_device() == v.get_device() == dev and k.is_contiguous() and v.is_contiguous()):
+            return MOE_BF16
+    code = _dt_code(precision)
     fp8 = code == MOE_MXFP8
-    shape, dtype = (c.pages, c.heads, c.page_size, c.dim), torch.uint8 if fp8 else torch.bfloat16
-    if c.k is None or c.v is None or (fp8 and (c.k_scales is None or c.v_scales is None)):
+    shape, dtype = (pages, heads, page_size, dim), torch.uint8 if fp8 else torch.bfloat16
+    if k is None or v is None or (fp8 and (k_scales is None or v_scales is None)):
         raise ValueError("the cache has no pools")
-    _like(c.k, "cache.k", dtype, shape, dev)
-    _like(c.v, "cache.v", dtype, shape, dev)
+    _like(k, "cache.k", dtype, shape, dev)
+    _like(v, "cache.v", dtype, shape, dev)
     if fp8:
-        shape = shape[:3] + (c.dim // 32,)
-        _like(c.k_scales, "cache.k_scales", torch.uint8, shape, dev)
-        _like(c.v_scales, "cache.v_scales", torch.uint8, shape, dev)
+        shape = shape[:3] + (dim // 32,)
+        _like(k_scales, "cache.k_scales", torch.uint8, shape, dev)
+        _like(v_scales, "cache.v_scales", torch.uint8, shape, dev)
     return code
 
 
 def _table(table: torch.Tensor, dev: int):
-    _like(table, "table", torch.int32, table.shape, dev)
-    if table.dim() != 2:
+    shape = table.shape
+    if len(shape) != 2:
         raise ValueError("table must have 2 dims")
-    return table.shape
+    _like(table, "table", torch.int32, shape, dev)
+    return shape
 
 
 def _tokens(t: torch.Tensor, name: str, shape, dev: int) -> int:
     """t is bf16 of this shape on this device, the last two dimensions without gaps: the stride between tokens
     in elements (0 where there is one)."""
-    if not (t.is_cuda and t.get_device() == dev):
+    if t.get_device() != dev or dev < 0:
         raise ValueError(f"{name} must be on cuda:{dev}, the other tensors' device")
     if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
     n, h, d = shape
-    if tuple(t.shape) != (n, h, d):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {[n, h, d]}")
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d > 1) or (s1 != d and h > 1):
@@ -1195,20 +1203,21 @@ def moe_cache_fork(table: torch.Tensor, lengths: torch.Tensor, parents: Optional
         n = parents.shape[0]
         _like(parents, "parents", torch.int32, (n,), dev)
     rooms = None
-    if isinstance(room, torch.Tensor):
+    if type(room) is not int and isinstance(room, torch.Tensor):
         rooms, room = room, 0
         _like(rooms, "room", torch.int32, (n,), dev)
     elif not 0 <= room < 1 << 31:
         raise ValueError("room must be at least 0")
     i32 = torch.int32
     if out is None:
-        new = [_empty(shape, i32, table.device, stream) for shape in ((n, M), (n,), (n,), (n,), (1,))]
-        out = CacheFork(*new)
+        on = table.device
+        out = CacheFork(_empty((n, M), i32, on, stream), _empty(n, i32, on, stream), _empty(n, i32, on, stream),
+                        _empty(n, i32, on, stream), _empty(1, i32, on, stream))
     else:
         for t, name, shape in zip(out, CacheFork._fields, ((n, M), (n,), (n,), (n,), (1,))):
             _like(t, name, i32, shape, dev)
-        if out.table.data_ptr() == table.data_ptr() and table.numel():
-            raise ValueError("the new table must not be the old one")
+        if n and not {t.data_ptr() for t in out}.isdisjoint([table.data_ptr(), lengths.data_ptr(), _at(parents), _at(rooms)]):
+            raise ValueError("the new table and lists must not be the old ones")
     if workspace is None:
         workspace = moe_cache_pages_workspace(pages, n, table.device, stream)
     else:
@@ -1262,20 +1271,21 @@ def moe_cache_copy_pages(caches, src: torch.Tensor, dst: torch.Tensor, *, stream
     _like(dst, "dst", torch.int32, (n,), dev)
     if dev < 0:
         raise ValueError("src must be a CUDA tensor")
-    pools, sizes = array("q"), array("q")
+    pools, sizes = [], []
     pages = caches[0].pages if caches else 1
     for c in caches:
-        fp8 = _want_cache(c, dev) == MOE_MXFP8
+        code = _want_cache(c, dev)
         if c.pages != pages:
             raise ValueError("the caches must have the same number of pages")
         rows = c.heads * c.page_size
-        pools.extend((c.k.data_ptr(), c.v.data_ptr()))
-        size = rows * c.dim * (1 if fp8 else 2)
-        sizes.extend((size, size))
-        if fp8:
-            pools.extend((c.k_scales.data_ptr(), c.v_scales.data_ptr()))
-            size = rows * (c.dim // 32)
-            sizes.extend((size, size))
+        size = rows * c.dim
+        if code == MOE_BF16:
+            pools += (c.k.data_ptr(), c.v.data_ptr())
+            sizes += (2 * size, 2 * size)
+        else:
+            pools += (c.k.data_ptr(), c.v.data_ptr(), c.k_scales.data_ptr(), c.v_scales.data_ptr())
+            sizes += (size, size, size // 32, size // 32)
+    pools, sizes = array("q", pools), array("q", sizes)
     st = _lib.load().moe_cache_copy_pages(pools.buffer_info()[0], sizes.buffer_info()[0], len(pools), src.data_ptr(),
                                           dst.data_ptr(), n, pages, _raw_stream(stream, src))
     _check("moe_cache_copy_pages", st)

@@ -586,6 +586,7 @@ moe_status rows_check(const void* k, const void* v, long long k_stride, long lon
     if (n < 0 || S < 0) return MOE_ERR_INVALID_ARG;
     const moe_status st = moe_host::check_cache(c, dtype, M);
     if (st != MOE_OK) return st;
+    if (n > 1 << 30) return MOE_ERR_UNSUPPORTED;                       // (tokens are counted in 32 bits)
     if (!rows && n > S) return MOE_ERR_INVALID_ARG;
     if (n > 0 && (!k || !v || !positions || !table)) return MOE_ERR_INVALID_ARG;
     if (k_stride % 8 || v_stride % 8 || !moe_host::aligned(k, 16) || !moe_host::aligned(v, 16) || !moe_host::aligned(rows, 4) ||

@@ -613,7 +613,7 @@ moe_status moe_grad_norm_clip(const void *const *grads, const long long *counts,
  * (multiples of 8; slices of one projection), to position positions[i] of sequence rows[i]
  * (rows NULL: of sequence i, n <= S). A negative position or row is skipped (padding); a
  * position at or past M * page_size or a row >= S is a bad id. The (page, offset) pairs of one
- * call must be distinct. MXFP8 quantises on the way.
+ * call must be distinct. MXFP8 quantises on the way. n <= 2^30.
  * moe_cache_gather: the same positions read back, k, v [n, heads, dim] bf16 contiguous
  * (MXFP8: code times scale, exact), zeros for the positions that are skipped or bad.
  * ------------------------------------------------------------------------ */

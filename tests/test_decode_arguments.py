@@ -42,7 +42,8 @@ def test_rows(lib, call):
     for bad in (dict(dtype=F32), dict(pages=0), dict(heads=0), dict(page=0), dict(dim=0), dict(M=0), dict(kp=None), dict(vp=None)):
         assert call(lib, **bad) == 1, bad
     assert call(lib, dtype=MXFP8, ks=None) == 1 and call(lib, dtype=MXFP8, vs=None) == 1
-    for bad in (dict(dim=40), dict(dim=272), dict(dtype=MXFP8, dim=48), dict(page=4097), dict(M=1 << 28)):
+    for bad in (dict(dim=40), dict(dim=272), dict(dtype=MXFP8, dim=48), dict(page=4097), dict(M=1 << 28),
+                dict(n=(1 << 30) + 1, rows=P)):
         assert call(lib, **bad) == 2, bad
     for name in ("k", "v", "pos", "table"):
         assert call(lib, **{name: None}) == 1

@@ -140,6 +140,35 @@ def test_ascending_and_descending_rows():
         _check(logits, torch.tensor([[0.0, -0.5]], device="cuda"), 64)
 
 
+@pytest.mark.parametrize("dtype,V", [(F32, 32_768), (F32, 30_001), (BF, 70_003)])
+@pytest.mark.parametrize("kind", ["random", "ascending", "equal", "few values"])
+def test_many_rows_a_block(dtype, V, kind):
+    """More units than blocks, so that a block has several of a row and several rows: the threshold that is kept from
+    unit to unit, and more ties and larger logits than the buffer holds."""
+    N, K = 700, 40
+    g = torch.Generator(device="cuda").manual_seed(V)
+    if kind == "random":
+        x = torch.randn((N, V), generator=g, device="cuda") * 2.5
+    elif kind == "ascending":
+        x = torch.linspace(-9, 9, V, device="cuda").expand(N, V) + torch.arange(N, device="cuda")[:, None] * 0.001
+    elif kind == "equal":
+        x = torch.zeros((N, V), device="cuda")
+    else:
+        x = torch.randint(0, 5, (N, V), generator=g, device="cuda").float()
+    logits = x.to(dtype)[:, None].contiguous()
+    del x
+    scores = torch.linspace(-3, 0, N, device="cuda")[:, None].contiguous()
+    o = api.moe_beam_select(logits, scores, K)
+    assert torch.equal(o.parents, torch.arange(N, dtype=I32, device="cuda")[:, None].expand(N, K))
+    rows = logits[:, 0].float()
+    want, at = torch.sort(rows, dim=1, descending=True, stable=True)
+    assert torch.equal(o.tokens.long(), at[:, :K])
+    lse = torch.logsumexp(rows.double(), 1, keepdim=True)
+    ref = scores.double() + want[:, :K].double() - lse
+    assert bool(((o.scores.double() - ref).abs() <= BAR + 2.0 ** -23 * ref.abs()).all())
+    assert api.moe_get_device_errors() == 0
+
+
 def test_repeats_on_any_workspace_stream_and_graph():
     logits, scores = _inputs(3, 6, 40_000, F32, seed=9)
     ref = _check(logits, scores, 12)

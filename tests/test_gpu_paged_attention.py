@@ -178,6 +178,49 @@ def test_an_unattended_outlier_among_the_values(precision):
         _check(q, cache, table, lengths, [(k3.double(), v3.double())], out, lse)
 
 
+@pytest.mark.parametrize("factor", [2.0 ** -40, 1.0, 2.0 ** 40])
+def test_values_of_zeros_beside_small_and_large_ones(factor):
+    """Rows of zeros, whose MXFP8 scale is 1 whatever the others' is, and scales that differ from block to block."""
+    lengths = [150, 33]
+    cache, table, dense = _cache(lengths, 2, 96, 16, "mxfp8")
+    rows = torch.cat([torch.full((n,), b, dtype=I32) for b, n in enumerate(lengths)]).cuda()
+    pos = torch.cat([torch.arange(n, dtype=I32) for n in lengths]).cuda()
+    k, v = api.moe_cache_gather(cache, table, pos, rows=rows)
+    v = v * factor
+    v[::3] = 0
+    v[1::3, :, 32:64] *= 2.0 ** -9
+    v[2::3, 1] *= 2.0 ** 5
+    api.moe_cache_append(k, v, cache, table, pos, rows=rows)
+    k, v = api.moe_cache_gather(cache, table, pos, rows=rows)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q = _randn((2, 6, 96), g).to(BF)
+    out, lse = api.moe_paged_attention(q, cache, table, torch.tensor(lengths, dtype=I32, device="cuda"))
+    dense = [(k[:150].double(), v[:150].double()), (k[150:].double(), v[150:].double())]
+    _check(q, cache, table, lengths, dense, out, lse)
+
+
+def test_a_nan_in_8_bits():
+    lengths = [70]
+    cache, table, dense = _cache(lengths, 1, 64, 16, "mxfp8")
+    q = torch.ones((1, 2, 64), device="cuda", dtype=BF)
+    lens = torch.tensor(lengths, dtype=I32, device="cuda")
+    page, off = int(table[0, 2]), 7                           # position 39
+    for codes, scales in ((cache.v, cache.v_scales), (cache.k, cache.k_scales)):
+        for t, at, bad in ((codes, 40, 0x7f), (codes, 40, 0xff), (scales, 1, 255)):
+            keep = t[page, 0, off, at].clone()
+            t[page, 0, off, at] = bad
+            out, lse = api.moe_paged_attention(q, cache, table, lens)
+            if codes is cache.v:                              # its own elements: a code's one, a scale's 32
+                hit = torch.zeros(64, dtype=torch.bool, device="cuda")
+                hit[40 if at == 40 else slice(32, 64)] = True
+                assert torch.isnan(out[0][:, hit]).all() and torch.isfinite(out[0][:, ~hit]).all() and torch.isfinite(lse).all()
+            else:
+                assert torch.isnan(out).all() and torch.isnan(lse).all()
+            out, lse = api.moe_paged_attention(q, cache, table, lens, window=30)
+            assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+            t[page, 0, off, at] = keep
+
+
 def test_strided_queries_and_given_outputs():
     lengths = [90, 300, 0, 12]
     cache, table, dense = _cache(lengths, 2, 64, 16)

@@ -216,7 +216,7 @@ def _check_fork(table, lengths, parents, pages, page, room, workspace=None):
 
 
 @pytest.mark.parametrize("S,M,page,pages", [(1, 1, 1, 3), (4, 5, 4, 40), (8, 9, 16, 100), (33, 7, 3, 400), (64, 130, 2, 9000),
-                                            (300, 40, 8, 13_000), (5, 3, 16, 70_001)])
+                                            (300, 40, 8, 13_000), (5, 3, 16, 70_001), (300, 100, 2, 31_000), (2, 20_000, 1, 30_000)])
 @pytest.mark.parametrize("room", [0, 1, 5])
 def test_fork(S, M, page, pages, room):
     for seed in range(4):
@@ -263,14 +263,15 @@ def _compact_plain(table, pages):
     live = sorted({t for row in table for t in row if 0 <= t < pages})
     n = len(live)
     movers = [p for p in live if p >= n]
-    holes = [p for p in range(n) if p not in set(live)]
+    named = set(live)
+    holes = [p for p in range(n) if p not in named]
     to = dict(zip(movers, holes))
     pad = [-1] * (pages // 2 - len(movers))
     return [[to.get(t, t) if 0 <= t < pages else -1 for t in row] for row in table], movers + pad, holes + pad, n
 
 
 @pytest.mark.parametrize("S,M,pages", [(1, 1, 1), (1, 1, 2), (4, 5, 40), (9, 9, 81), (33, 7, 400), (64, 130, 9000), (300, 40, 60_000),
-                                       (5, 3, 70_001)])
+                                       (5, 3, 70_001), (300, 100, 29_000), (2, 20_000, 30_000)])
 def test_compact(S, M, pages):
     for seed in range(5):
         r = random.Random(seed * 77 + S)
@@ -404,6 +405,8 @@ def test_refusals():
     with pytest.raises(ValueError):
         f = api.moe_cache_fork(t, l, None, 4, 4)
         api.moe_cache_fork(t, l, None, 4, 4, out=f._replace(table=t))
+    with pytest.raises(ValueError):
+        api.moe_cache_fork(t, l, None, 4, 4, out=f._replace(lengths=l))
     for room in (-1, 1 << 31):
         with pytest.raises(ValueError):
             api.moe_cache_fork(t, l, None, 4, 4, room=room)
