@@ -30,14 +30,14 @@ struct RowsArgs {
     CachePools c;
 };
 
-// The line (row of a head's pages, before the head) of token i's position; -1: skipped or bad.
-__device__ __forceinline__ long long line_of(const RowsArgs& a, int i) {
+// The element of a pool at which token i's position begins in the first head's pages; -1: skipped or bad.
+__device__ __forceinline__ long long place_of(const RowsArgs& a, int i) {
     const int pos = __ldg(a.positions + i);
     const int row = a.rows ? __ldg(a.rows + i) : i;
     if (pos < 0 || row < 0) return -1;
     const int col = pos / a.c.page_size;
     const int p = row < a.S && col < a.M ? __ldg(a.table + (long long)row * a.M + col) : -1;
-    if ((unsigned)p < (unsigned)a.c.pages) return (long long)p * a.c.heads * a.c.page_size + (pos - col * a.c.page_size);
+    if ((unsigned)p < (unsigned)a.c.pages) return ((long long)p * a.c.heads * a.c.page_size + (pos - col * a.c.page_size)) * a.c.dim;
     raise_device_error(MOE_DEVERR_BAD_ID);
     return -1;
 }
@@ -47,51 +47,51 @@ __device__ __forceinline__ long long line_of(const RowsArgs& a, int i) {
 // several tokens side by side where a token has fewer; its tokens are looked up once, by a thread each.
 template <bool FP8, bool WRITE, int EACH>
 __global__ void __launch_bounds__(RW_THREADS) cache_rows_kernel(const __grid_constant__ RowsArgs a) {
-    __shared__ long long lines[RW_THREADS / 4 * EACH];     // (a token has four pieces at least)
+    __shared__ long long places[RW_THREADS / 4 * EACH];    // (a token has four pieces at least)
     const int dim8 = a.c.dim / 8, side = a.c.heads * dim8, per_token = 2 * side;
     const int beside = max(1, RW_THREADS / per_token);     // tokens side by side
     const int token0 = blockIdx.x * beside * EACH;
-    if ((int)threadIdx.x < beside * EACH) lines[threadIdx.x] = token0 + (int)threadIdx.x < a.n ? line_of(a, token0 + threadIdx.x) : -1;
+    if ((int)threadIdx.x < beside * EACH) places[threadIdx.x] = token0 + (int)threadIdx.x < a.n ? place_of(a, token0 + threadIdx.x) : -1;
     __syncthreads();
     const int sub = per_token < RW_THREADS ? (int)threadIdx.x / per_token : 0;
     const int piece = blockIdx.y * RW_THREADS + threadIdx.x - sub * per_token;
     const bool mine = sub < beside && piece < per_token, is_v = piece >= side;
     const int in_side = is_v ? piece - side : piece, head = in_side / dim8, d8 = in_side - head * dim8;
-    const long long stride = 2 * (is_v ? a.v_stride : a.k_stride);
+    const long long stride = 2 * (is_v ? a.v_stride : a.k_stride), step = beside * stride;
     char* const dense = static_cast<char*>(is_v ? a.v : a.k) + (long long)(token0 + sub) * stride + 16ll * in_side;
-    const long long line0 = (long long)head * a.c.page_size;
-    char* const pool = static_cast<char*>(is_v ? a.c.v : a.c.k) + (FP8 ? 1 : 2) * (line0 * a.c.dim + 8 * d8);
-    uint8_t* const scale = FP8 ? (is_v ? a.c.v_scales : a.c.k_scales) + line0 * (a.c.dim / 32) + d8 / 4 : nullptr;
-    long long line[EACH];
+    const long long in_page = (long long)head * a.c.page_size * a.c.dim + 8 * d8;
+    char* const pool = static_cast<char*>(is_v ? a.c.v : a.c.k) + (FP8 ? 1 : 2) * in_page;
+    uint8_t* const scale = FP8 ? (is_v ? a.c.v_scales : a.c.k_scales) + in_page / 32 : nullptr;     // (dim is whole blocks)
+    long long place[EACH];
     uint4 v[EACH];
 #pragma unroll
     for (int e = 0; e < EACH; e++) {
-        line[e] = mine ? lines[e * beside + sub] : -1;
+        place[e] = mine ? places[e * beside + sub] : -1;
         v[e] = make_uint4(0, 0, 0, 0);
-        if (line[e] < 0) continue;
+        if (place[e] < 0) continue;
         if (WRITE) {
-            v[e] = __ldg(reinterpret_cast<const uint4*>(dense + e * beside * stride));
+            v[e] = __ldg(reinterpret_cast<const uint4*>(dense + e * step));
         } else if (FP8) {
-            const uint2 q = __ldg(reinterpret_cast<const uint2*>(pool + line[e] * a.c.dim));
-            v[e] = make_uint4(q.x, q.y, __ldg(scale + line[e] * (a.c.dim / 32)), 0u);
+            const uint2 q = __ldg(reinterpret_cast<const uint2*>(pool + place[e]));
+            v[e] = make_uint4(q.x, q.y, __ldg(scale + (place[e] >> 5)), 0u);
         } else {
-            v[e] = __ldg(reinterpret_cast<const uint4*>(pool + line[e] * (2 * a.c.dim)));
+            v[e] = __ldg(reinterpret_cast<const uint4*>(pool + 2 * place[e]));
         }
     }
 #pragma unroll
     for (int e = 0; e < EACH; e++) {
         float f[8];
-        const bool ok = line[e] >= 0;
+        const bool ok = place[e] >= 0;
         if (WRITE && FP8) {
             int byte;
             bf16x8_to_f32(v[e], f);
             const uint2 q = quant8_in_quad(f, &byte);
             if (ok) {
-                *reinterpret_cast<uint2*>(pool + line[e] * a.c.dim) = q;
-                if ((d8 & 3) == 0) scale[line[e] * (a.c.dim / 32)] = (uint8_t)byte;
+                *reinterpret_cast<uint2*>(pool + place[e]) = q;
+                if ((d8 & 3) == 0) scale[place[e] >> 5] = (uint8_t)byte;
             }
         } else if (WRITE) {
-            if (ok) *reinterpret_cast<uint4*>(pool + line[e] * (2 * a.c.dim)) = v[e];
+            if (ok) *reinterpret_cast<uint4*>(pool + 2 * place[e]) = v[e];
         } else if (mine && token0 + e * beside + sub < a.n) {
             if (FP8) {
                 const float s = e8m0_value(v[e].z);
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(RW_THREADS) cache_rows_kernel(const __grid_con
                 for (int k = 0; k < 8; k++) f[k] *= s;
                 v[e] = ok ? f32_to_bf16x8(f) : make_uint4(0, 0, 0, 0);
             }
-            *reinterpret_cast<uint4*>(dense + e * beside * stride) = v[e];
+            *reinterpret_cast<uint4*>(dense + e * step) = v[e];
         }
     }
 }
