@@ -1152,6 +1152,7 @@ def moe_paged_attention(q: torch.Tensor, cache: PagedCache, table: torch.Tensor,
     S, M = _table(table, dev)
     if S != B:
         raise ValueError(f"table must have {B} rows")
+    window = min(window, (1 << 31) - 1)              # (all positions)
     _like(lengths, "lengths", torch.int32, (B,), dev)
     if out is None:
         out = _empty((B, heads, dim), torch.bfloat16, q.device, stream)
@@ -1208,6 +1209,8 @@ def moe_cache_fork(table: torch.Tensor, lengths: torch.Tensor, parents: Optional
         _like(rooms, "room", torch.int32, (n,), dev)
     elif not 0 <= room < 1 << 31:
         raise ValueError("room must be at least 0")
+    if pages >= 1 << 31 or page_size >= 1 << 31:
+        raise ValueError("pages and page_size must be below 2^31")
     i32 = torch.int32
     if out is None:
         on = table.device
@@ -1243,6 +1246,8 @@ def moe_cache_compact(table: torch.Tensor, pages: int, *, out: Optional[CacheCom
     every layer's pools (moe_cache_copy_pages) before the new table is used. out.table may be the table itself."""
     dev = table.get_device()
     S, M = _table(table, dev)
+    if pages >= 1 << 31:
+        raise ValueError("pages must be below 2^31")
     shapes = ((S, M), (pages // 2,), (pages // 2,), (1,))
     if out is None:
         out = CacheCompact(*[_empty(shape, torch.int32, table.device, stream) for shape in shapes])
@@ -1316,6 +1321,8 @@ def moe_beam_select(logits: torch.Tensor, scores: torch.Tensor, K: int, *, done:
     code = _float_code(logits, "logits")
     _like(scores, "scores", torch.float32, (N, W), dev)
     _like(done, "done", torch.bool, (N, W), dev)
+    if pad >= 1 << 31 or K >= 1 << 31:
+        raise ValueError("pad and K must be below 2^31")
     if out is None:
         out = BeamSelected(_empty((N, K), torch.float32, logits.device, stream),
                            _empty((N, K), torch.int32, logits.device, stream),

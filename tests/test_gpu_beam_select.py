@@ -213,6 +213,9 @@ def test_refusals():
         with pytest.raises(MoeError):
             api.moe_beam_select(logits, scores, K)
     done = torch.zeros((2, 3), dtype=torch.bool, device="cuda")
+    for big in (dict(K=4, pad=1 << 32), dict(K=1 << 32)):        # (not what is left of them in 32 bits)
+        with pytest.raises(ValueError):
+            api.moe_beam_select(logits, scores, done=done, **big)
     for pad in (-1, 50):
         with pytest.raises(MoeError):
             api.moe_beam_select(logits, scores, 4, done=done, pad=pad)

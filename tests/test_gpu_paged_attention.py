@@ -124,7 +124,7 @@ def test_heads_of_a_group(q_heads, precision):
 
 
 @pytest.mark.parametrize("precision", ["bf16", "mxfp8"])
-@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 1000, 100000])
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 1000, 100000, (1 << 32) + 5])
 def test_window(window, precision):
     _run([700, 33, 1, 0, 100, 101], 8, 2, 128, 16, precision, window=window)
 

@@ -407,6 +407,11 @@ def test_refusals():
         api.moe_cache_fork(t, l, None, 4, 4, out=f._replace(table=t))
     with pytest.raises(ValueError):
         api.moe_cache_fork(t, l, None, 4, 4, out=f._replace(lengths=l))
+    for big in ((1 << 32) + 4, 4), (4, (1 << 32) + 4):
+        with pytest.raises(ValueError):
+            api.moe_cache_fork(t, l, None, *big)
+    with pytest.raises(ValueError):
+        api.moe_cache_compact(t, (1 << 32) + 4)
     for room in (-1, 1 << 31):
         with pytest.raises(ValueError):
             api.moe_cache_fork(t, l, None, 4, 4, room=room)
