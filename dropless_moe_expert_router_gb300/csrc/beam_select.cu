@@ -232,17 +232,20 @@ __device__ __noinline__ int exactly_largest(const T* row, int first, int pieces,
     return min(*count, BS_CAP);
 }
 
-// best[rank] = key for the n keys of buf with a rank below K (all keys are different): a thread a key where they are few,
-// a warp where they are more, its lanes the others.
+// best[rank] = key for the n keys of buf with a rank below K (all keys are different): four threads a key where they are
+// few, a warp where they are more, which share the others.
 __device__ __forceinline__ void rank_keys(const unsigned long long* buf, int n, int K, unsigned long long* best) {
     if (n <= 64) {
-        if ((int)threadIdx.x < n) {
-            const unsigned long long key = buf[threadIdx.x];
-            int above = 0;
+        static_assert(BS_THREADS == 4 * 64, "four threads a key");
+        if ((int)(threadIdx.x & ~31u) >= 4 * n) return;                 // (whole warps)
+        const int i = min((int)threadIdx.x / 4, n - 1);
+        const unsigned long long key = buf[i];
+        int above = 0;
 #pragma unroll 4
-            for (int k = 0; k < n; k++) above += buf[k] > key;
-            if (above < K) best[above] = key;
-        }
+        for (int k = threadIdx.x & 3; k < n; k += 4) above += buf[k] > key;
+        above += __shfl_xor_sync(FULL, above, 1);
+        above += __shfl_xor_sync(FULL, above, 2);
+        if ((threadIdx.x & 3) == 0 && (int)threadIdx.x / 4 < n && above < K) best[above] = key;
         return;
     }
     for (int i = threadIdx.x / 32; i < n; i += BS_THREADS / 32) {
