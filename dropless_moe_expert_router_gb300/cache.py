@@ -68,6 +68,11 @@ class SequenceCache:
         them; `grow` follows)."""
         api.moe_cache_append(k, v, self.layers[layer], self.table, positions, rows=rows)
 
+    def read(self, layer: int, rows: torch.Tensor, positions: torch.Tensor):
+        """What the cache holds of positions[i] of slots rows[i]: keys and values [n, heads, dim] bf16 (for the attention of
+        prompts, whose many queries `attend` is not for)."""
+        return api.moe_cache_gather(self.layers[layer], self.table, positions, rows=rows)
+
     def attend(self, layer: int, q: torch.Tensor, *, scale: Optional[float] = None, window: int = 0) -> torch.Tensor:
         """q [sequences, q_heads, dim] bf16 over each slot's positions, the step's among them -> the same shape."""
         heads = q.shape[1]

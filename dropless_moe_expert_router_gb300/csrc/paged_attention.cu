@@ -141,6 +141,29 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
     return r;
 }
+// 2, 4 or 8 floats that begin on a boundary of their size (16 bytes at most).
+template <int N>
+__device__ __forceinline__ void lds_all(uint32_t at, float (&f)[N]) {
+    if (N == 2) {
+        const uint2 x = lds64(at);
+        f[0] = __uint_as_float(x.x);
+        f[1] = __uint_as_float(x.y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; i++) {
+            const uint4 x = lds128(at + 16 * i);
+            f[4 * i] = __uint_as_float(x.x);
+            f[(4 * i + 1) % N] = __uint_as_float(x.y);
+            f[(4 * i + 2) % N] = __uint_as_float(x.z);
+            f[(4 * i + 3) % N] = __uint_as_float(x.w);
+        }
+    }
+}
+__device__ __forceinline__ void sts64(uint32_t at, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+}
+// Whether one of the four bytes is 255.
+__device__ __forceinline__ bool has_255(uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & x & 0x80808080u; }
 __device__ __forceinline__ void sts32(uint32_t at, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
 __device__ __forceinline__ void sts16(uint32_t at, uint32_t v) {
     asm volatile("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n st.shared.b16 [%0], l;\n}" ::"r"(at), "r"(v) : "memory");
@@ -287,8 +310,11 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
     const int warp = threadIdx.x / 32, lane = lane_id(), j = lane & 3, r8 = lane >> 2;
     const int dim = a.c.dim, group = a.q_heads / a.c.heads, pairs = a.c.heads * a.tiles_of_heads;
     const int row_bytes = dim * (FP8 ? 1 : 2), row_scales = dim / 32;
+    // the bytes of a row's scales that there are, four and four
+    const uint32_t keep0 = row_scales >= 4 ? 0xffffffffu : (1u << (8 * row_scales)) - 1u;
+    const uint32_t keep1 = row_scales >= 8 ? 0xffffffffu : row_scales > 4 ? (1u << (8 * (row_scales - 4))) - 1u : 0u;
     const uint32_t ring = saddr(smem) + warp * (C::STAGES * C::STAGE);
-    const uint32_t prep = saddr(smem) + PA_WARPS * C::STAGES * C::STAGE + warp * C::PREP;    // fp32 [DP/32][16], then 16-bit [DP/32][16]
+    const uint32_t prep = saddr(smem) + PA_WARPS * C::STAGES * C::STAGE + warp * C::PREP;    // fp32 [TILE][DP/32], then 16-bit [TILE/2][DP/32][2]
     uint32_t* const seen = reinterpret_cast<uint32_t*>(smem + PA_WARPS * (C::STAGES * C::STAGE + C::PREP)) + warp * 16;  // of a stage's rows
     float* const join = reinterpret_cast<float*>(smem + PA_WARPS * (C::STAGES * C::STAGE + C::PREP + 64));
     float2* const ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(join) + C::JOIN);
@@ -475,26 +501,35 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
             const uint32_t rows = seen[take];
             bool wide = false;                     // (MXFP8) this tile's scales span more than fp16 weights take
             if (FP8) {
-                // the tile's scales, a lane a row (and, of 16 rows, a side)
-                uint32_t most = 0u, least = 255u, byte[C::SUB][DP / 32];
+                // the tile's scales, a lane a row (and, of 16 rows, a side); what a shorter row has not is 0, in least 255
+                constexpr int BLOCKS = DP / 32;
+                uint32_t most = 0u, least = 255u, word[C::SUB][2];
+                bool nan = false;
                 const bool here = (rows >> (lane & (C::TILE - 1))) & 1;
+                auto byte_of = [&](int x, int i) { return (word[x][i >> 2] >> (8 * (i & 3))) & 0xffu; };
 #pragma unroll
                 for (int x = 0; x < C::SUB; x++) {
                     const uint4 slot = lds128(kt + C::KV + (x * 32 + lane) * 16);
-                    const uint32_t s0 = __funnelshift_r(slot.x, slot.y, slot.w);
-                    const uint32_t s1 = DP == 256 ? __funnelshift_r(slot.y, slot.z, slot.w) : 0u;
-                    const bool is_v = C::SUB == 2 ? x == 1 : lane >= 16;
+                    word[x][0] = __funnelshift_r(slot.x, slot.y, slot.w) & keep0;
+                    word[x][1] = DP == 256 ? __funnelshift_r(slot.y, slot.z, slot.w) & keep1 : 0u;
+                    nan = nan || has_255(word[x][0]) || (DP == 256 && has_255(word[x][1]));
+                    if (C::SUB == 2 ? x == 1 : lane >= 16) {
 #pragma unroll
-                    for (int i = 0; i < DP / 32; i++) {
-                        byte[x][i] = ((i < 4 ? s0 : s1) >> (8 * (i & 3))) & 0xffu;
-                        if (is_v && here && i < row_scales) {
-                            if (byte[x][i] != 255u) most = max(most, byte[x][i]);
-                            least = min(least, byte[x][i]);
+                        for (int i = 0; i < BLOCKS; i++) {
+                            most = max(most, byte_of(x, i));
+                            least = min(least, ((i < 4 ? word[x][0] | ~keep0 : word[x][1] | ~keep1) >> (8 * (i & 3))) & 0xffu);
                         }
                     }
                 }
+                nan = __any_sync(FULL, nan);
+                if (nan) {
+                    most = 0u;
+                    for (int x = 0; x < C::SUB; x++)
+                        for (int i = 0; i < BLOCKS; i++)
+                            if ((C::SUB == 2 ? x == 1 : lane >= 16) && byte_of(x, i) != 255u) most = max(most, byte_of(x, i));
+                }
                 most = __reduce_max_sync(FULL, most);
-                least = __reduce_min_sync(FULL, least);
+                least = __reduce_min_sync(FULL, here ? least : 255u);
                 if ((int)most > vref) {
                     const float f = pow2((float)(vref - (int)most));
 #pragma unroll
@@ -506,23 +541,29 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                     vref = (int)most;
                 }
                 wide = vref - (int)least > PA_SPREAD;
+                const int bias = (wide ? 127 : 15) - vref, step = wide ? 7 : 10;
+                const int row = lane & (C::TILE - 1);
+                const uint32_t ks = prep + row * BLOCKS * 4, vs = prep + C::TILE * BLOCKS * 4 + (row >> 1) * BLOCKS * 4 + (row & 1) * 2;
 #pragma unroll
                 for (int x = 0; x < C::SUB; x++) {
-                    const bool is_v = C::SUB == 2 ? x == 1 : lane >= 16;
-                    const int row = lane & (C::TILE - 1);
+                    if (C::SUB == 2 ? x == 0 : lane < 16) {
+                        uint32_t b[BLOCKS];        // (2^-127 is half of the least normal number)
 #pragma unroll
-                    for (int i = 0; i < DP / 32; i++) {
-                        if (i >= row_scales) continue;
-                        if (!is_v) {
-                            // (2^-127 is half of the least normal number)
-                            sts32(prep + (i * C::TILE + row) * 4, byte[x][i] == 255u ? 0x7fc00000u : max(byte[x][i] << 23, 0x00400000u));
-                        } else {
-                            const int y = (int)byte[x][i] - vref;
-                            uint32_t f = wide ? (uint32_t)max(0, 127 + y) << 7 : (uint32_t)max(0, 15 + y) << 10;
-                            if (byte[x][i] == 255u) f = wide ? 0x7fc0u : 0x7e00u;
-                            sts16(prep + DP / 32 * C::TILE * 4 + (i * C::TILE + row) * 2, f);
-                        }
+                        for (int i = 0; i < BLOCKS; i++) b[i] = max(byte_of(x, i) << 23, 0x00400000u);
+#pragma unroll
+                        for (int i = 0; i < BLOCKS; i += 2) sts64(ks + 4 * i, b[i], b[i + 1]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < BLOCKS; i++) sts16(vs + 4 * i, (uint32_t)max(0, bias + (int)byte_of(x, i)) << step);
                     }
+                }
+                if (nan) {
+                    for (int x = 0; x < C::SUB; x++)
+                        for (int i = 0; i < BLOCKS; i++) {
+                            if (byte_of(x, i) != 255u) continue;
+                            if (C::SUB == 2 ? x == 0 : lane < 16) sts32(ks + 4 * i, 0x7fc00000u);
+                            else sts16(vs + 4 * i, wide ? 0x7fc0u : 0x7e00u);
+                        }
                 }
                 __syncwarp();
             }
@@ -548,9 +589,12 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
             } else {
                 const int sw = DP == 64 ? ((r8 >> 1) & 1) << 1 : (r8 & 3) << 1;               // (row r8 + 8 has the same)
 #pragma unroll
-                for (int i = 0; i < DP / 32; i++)
+                for (int x = 0; x < C::SUB; x++) {
+                    float scale0[DP / 32], scale1[DP / 32];
+                    lds_all(prep + (x * 16 + r8) * (DP / 32) * 4, scale0);
+                    lds_all(prep + (x * 16 + r8 + 8) * (DP / 32) * 4, scale1);
 #pragma unroll
-                    for (int x = 0; x < C::SUB; x++) {
+                    for (int i = 0; i < DP / 32; i++) {
                         const uint32_t at = kt + (x * 16 + r8) * C::ROW + (((2 * i + (j >> 1)) ^ sw) * 16) + (j & 1) * 8;
                         const uint2 top = lds64(at), bot = lds64(at + 8 * C::ROW);
                         float part[NB][4];
@@ -559,8 +603,7 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                         halves(bot.x, f[1], f[3]);
                         halves(top.y, g[0], g[2]);
                         halves(bot.y, g[1], g[3]);
-                        const float k0 = __uint_as_float(lds32(prep + (i * C::TILE + x * 16 + r8) * 4));
-                        const float k1 = __uint_as_float(lds32(prep + (i * C::TILE + x * 16 + r8 + 8) * 4));
+                        const float k0 = scale0[i], k1 = scale1[i];
 #pragma unroll
                         for (int nb = 0; nb < NB; nb++) {
                             part[nb][0] = part[nb][1] = part[nb][2] = part[nb][3] = 0.0f;
@@ -572,20 +615,33 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                             s[x][nb][3] = fmaf(k1, part[nb][3], s[x][nb][3]);
                         }
                     }
+                }
             }
             // weights
             bool rises = false;
 #pragma unroll
             for (int x = 0; x < C::SUB; x++) {
-                const bool in0 = (rows >> (x * 16 + r8)) & 1, in1 = (rows >> (x * 16 + r8 + 8)) & 1;
 #pragma unroll
                 for (int nb = 0; nb < NB; nb++)
 #pragma unroll
                     for (int e = 0; e < 2; e++) {
-                        s[x][nb][e] = in0 ? s[x][nb][e] * to_s[nb][e] : -INFINITY;
-                        s[x][nb][2 + e] = in1 ? s[x][nb][2 + e] * to_s[nb][e] : -INFINITY;
-                        rises = rises || fmaxf(s[x][nb][e], s[x][nb][2 + e]) > m[nb][e];
+                        s[x][nb][e] *= to_s[nb][e];
+                        s[x][nb][2 + e] *= to_s[nb][e];
                     }
+                if (rows != (C::TILE == 32 ? FULL : 0xffffu)) {
+                    const bool in0 = (rows >> (x * 16 + r8)) & 1, in1 = (rows >> (x * 16 + r8 + 8)) & 1;
+#pragma unroll
+                    for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            if (!in0) s[x][nb][e] = -INFINITY;
+                            if (!in1) s[x][nb][2 + e] = -INFINITY;
+                        }
+                }
+#pragma unroll
+                for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) rises = rises || fmaxf(s[x][nb][e], s[x][nb][2 + e]) > m[nb][e];
             }
             if (__any_sync(FULL, rises)) {
 #pragma unroll
@@ -654,10 +710,13 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                             b0[nb] = transposed(pack2<F16>(s[x][nb][0], s[x][nb][1]));
                             b1[nb] = transposed(pack2<F16>(s[x][nb][2], s[x][nb][3]));
                         }
+                        float factor0[DP / 32], factor1[DP / 32];      // of rows 2j, 2j + 1 and 2j + 8, 2j + 9, two 16-bit numbers each
+                        const uint32_t factors = prep + C::TILE * (DP / 32) * 4 + (x * 8 + j) * (DP / 32) * 4;
+                        lds_all(factors, factor0);
+                        lds_all(factors + 4 * (DP / 32) * 4, factor1);
 #pragma unroll
                         for (int i = 0; i < DP / 32; i++) {
-                            const uint32_t fac = prep + DP / 32 * C::TILE * 4 + (i * C::TILE + x * 16 + 2 * j) * 2;
-                            const uint32_t f0 = lds32(fac), f1 = lds32(fac + 16);
+                            const uint32_t f0 = __float_as_uint(factor0[i]), f1 = __float_as_uint(factor1[i]);
                             uint32_t c[4];         // codes 4 r8 .. 4 r8 + 3 of the block, rows 2j, 2j + 1, 2j + 8, 2j + 9
 #pragma unroll
                             for (int e = 0; e < 4; e++) {

@@ -190,6 +190,8 @@ def test_prompts_and_slots_that_come_and_go():
     cache.write(0, k, v, rows, pos)
     cache.grow(room)
     assert cache.lengths.tolist() == lens
+    got = cache.read(0, rows, pos)
+    assert torch.equal(got[0], k) and torch.equal(got[1], v)
     full = [[k[0:5], v[0:5]], None, [k[5:13], v[5:13]], [k[13:16], v[13:16]]]
     for parents, src in (([0, 2, 2, -1], [0, 2, 2, None]), ([0, 1, 2, 3], [0, 1, 2, 3]), (None, [0, 1, 2, 3]),
                          ([-1, 1, 1, 1], [None, 1, 1, 1])):
