@@ -126,48 +126,31 @@ __device__ __forceinline__ float pow2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t at) {
-    uint32_t r;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
-    return r;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t at) {
-    uint2 r;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(at) : "memory");
-    return r;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-    uint4 r;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
-    return r;
-}
-// 2, 4 or 8 floats that begin on a boundary of their size (16 bytes at most).
+// Shared memory by pointers: the compiler orders these between the barriers as it likes.
+template <typename T>
+__device__ __forceinline__ T get(const uint8_t* p) { return *reinterpret_cast<const T*>(p); }
+template <typename T>
+__device__ __forceinline__ void put(uint8_t* p, T v) { *reinterpret_cast<T*>(p) = v; }
+// 2, 4 or 8 words that begin on a boundary of their size (16 bytes at most).
 template <int N>
-__device__ __forceinline__ void lds_all(uint32_t at, float (&f)[N]) {
+__device__ __forceinline__ void get_all(const uint8_t* p, uint32_t (&w)[N]) {
     if (N == 2) {
-        const uint2 x = lds64(at);
-        f[0] = __uint_as_float(x.x);
-        f[1] = __uint_as_float(x.y);
+        const uint2 x = get<uint2>(p);
+        w[0] = x.x;
+        w[1] = x.y;
     } else {
 #pragma unroll
         for (int i = 0; i < N / 4; i++) {
-            const uint4 x = lds128(at + 16 * i);
-            f[4 * i] = __uint_as_float(x.x);
-            f[(4 * i + 1) % N] = __uint_as_float(x.y);
-            f[(4 * i + 2) % N] = __uint_as_float(x.z);
-            f[(4 * i + 3) % N] = __uint_as_float(x.w);
+            const uint4 x = get<uint4>(p + 16 * i);
+            w[4 * i] = x.x;
+            w[(4 * i + 1) % N] = x.y;
+            w[(4 * i + 2) % N] = x.z;
+            w[(4 * i + 3) % N] = x.w;
         }
     }
 }
-__device__ __forceinline__ void sts64(uint32_t at, uint32_t x, uint32_t y) {
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
-}
 // Whether one of the four bytes is 255.
 __device__ __forceinline__ bool has_255(uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & x & 0x80808080u; }
-__device__ __forceinline__ void sts32(uint32_t at, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
-__device__ __forceinline__ void sts16(uint32_t at, uint32_t v) {
-    asm volatile("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n st.shared.b16 [%0], l;\n}" ::"r"(at), "r"(v) : "memory");
-}
 // Codes 0 and 1 of a word, codes 2 and 3, as two halves each (exact).
 __device__ __forceinline__ void halves(uint32_t codes, uint32_t& lo, uint32_t& hi) {
     asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
@@ -313,13 +296,14 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
     // the bytes of a row's scales that there are, four and four
     const uint32_t keep0 = row_scales >= 4 ? 0xffffffffu : (1u << (8 * row_scales)) - 1u;
     const uint32_t keep1 = row_scales >= 8 ? 0xffffffffu : row_scales > 4 ? (1u << (8 * (row_scales - 4))) - 1u : 0u;
-    const uint32_t ring = saddr(smem) + warp * (C::STAGES * C::STAGE);
-    const uint32_t prep = saddr(smem) + PA_WARPS * C::STAGES * C::STAGE + warp * C::PREP;    // fp32 [TILE][DP/32], then 16-bit [TILE/2][DP/32][2]
+    uint8_t* const ring_at = smem + warp * (C::STAGES * C::STAGE);
+    const uint32_t ring = saddr(ring_at);
+    uint8_t* const prep = smem + PA_WARPS * C::STAGES * C::STAGE + warp * C::PREP;    // fp32 [TILE][DP/32], then 16-bit [TILE/2][DP/32][2]
     uint32_t* const seen = reinterpret_cast<uint32_t*>(smem + PA_WARPS * (C::STAGES * C::STAGE + C::PREP)) + warp * 16;  // of a stage's rows
     float* const join = reinterpret_cast<float*>(smem + PA_WARPS * (C::STAGES * C::STAGE + C::PREP + 64));
     float2* const ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(join) + C::JOIN);
     if (FP8) {
-        for (int i = lane; i < C::PREP / 4; i += 32) sts32(prep + 4 * i, 0u);
+        for (int i = lane; i < C::PREP / 4; i += 32) put(prep + 4 * i, 0u);
         __syncwarp();
     }
     long long total;
@@ -407,13 +391,13 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                     if (row_scales == DP / 32 && DP >= 128) {          // whole words
 #pragma unroll
                         for (int i = 0; i < DP / 128; i++) copy4(slot + 4 * i, base + 4 * i, ok);
-                        sts32(slot + 12, 0u);
+                            put(ring_at + (slot - ring) + 12, 0u);
                     } else {
                         const int skip = (int)(reinterpret_cast<uintptr_t>(base) & 3), words = (skip + row_scales + 3) / 4;
 #pragma unroll
                         for (int i = 0; i < (DP / 32 + 6) / 4; i++)
                             if (i < words) copy4(slot + 4 * i, base - skip + 4 * i, ok);
-                        sts32(slot + 12, ok ? 8u * skip : 0u);
+                        put(ring_at + (slot - ring) + 12, ok ? 8u * skip : 0u);
                     }
                 }
             }
@@ -497,6 +481,7 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
         for (int u = w.u; u < my_end; u++) {
             copies_wait<C::STAGES - 1>();
             __syncwarp();
+            const uint8_t* const tile = ring_at + take * C::STAGE;
             const uint32_t kt = ring + take * C::STAGE, vt = kt + C::TILE * C::ROW;
             const uint32_t rows = seen[take];
             bool wide = false;                     // (MXFP8) this tile's scales span more than fp16 weights take
@@ -509,7 +494,7 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                 auto byte_of = [&](int x, int i) { return (word[x][i >> 2] >> (8 * (i & 3))) & 0xffu; };
 #pragma unroll
                 for (int x = 0; x < C::SUB; x++) {
-                    const uint4 slot = lds128(kt + C::KV + (x * 32 + lane) * 16);
+                    const uint4 slot = get<uint4>(tile + C::KV + (x * 32 + lane) * 16);
                     word[x][0] = __funnelshift_r(slot.x, slot.y, slot.w) & keep0;
                     word[x][1] = DP == 256 ? __funnelshift_r(slot.y, slot.z, slot.w) & keep1 : 0u;
                     nan = nan || has_255(word[x][0]) || (DP == 256 && has_255(word[x][1]));
@@ -543,7 +528,7 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                 wide = vref - (int)least > PA_SPREAD;
                 const int bias = (wide ? 127 : 15) - vref, step = wide ? 7 : 10;
                 const int row = lane & (C::TILE - 1);
-                const uint32_t ks = prep + row * BLOCKS * 4, vs = prep + C::TILE * BLOCKS * 4 + (row >> 1) * BLOCKS * 4 + (row & 1) * 2;
+                uint8_t *const ks = prep + row * BLOCKS * 4, *const vs = prep + C::TILE * BLOCKS * 4 + (row >> 1) * BLOCKS * 4 + (row & 1) * 2;
 #pragma unroll
                 for (int x = 0; x < C::SUB; x++) {
                     if (C::SUB == 2 ? x == 0 : lane < 16) {
@@ -551,18 +536,18 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
 #pragma unroll
                         for (int i = 0; i < BLOCKS; i++) b[i] = max(byte_of(x, i) << 23, 0x00400000u);
 #pragma unroll
-                        for (int i = 0; i < BLOCKS; i += 2) sts64(ks + 4 * i, b[i], b[i + 1]);
+                        for (int i = 0; i < BLOCKS; i += 2) put(ks + 4 * i, make_uint2(b[i], b[i + 1]));
                     } else {
 #pragma unroll
-                        for (int i = 0; i < BLOCKS; i++) sts16(vs + 4 * i, (uint32_t)max(0, bias + (int)byte_of(x, i)) << step);
+                        for (int i = 0; i < BLOCKS; i++) put(vs + 4 * i, (uint16_t)(max(0, bias + (int)byte_of(x, i)) << step));
                     }
                 }
                 if (nan) {
                     for (int x = 0; x < C::SUB; x++)
                         for (int i = 0; i < BLOCKS; i++) {
                             if (byte_of(x, i) != 255u) continue;
-                            if (C::SUB == 2 ? x == 0 : lane < 16) sts32(ks + 4 * i, 0x7fc00000u);
-                            else sts16(vs + 4 * i, wide ? 0x7fc0u : 0x7e00u);
+                            if (C::SUB == 2 ? x == 0 : lane < 16) put(ks + 4 * i, 0x7fc00000u);
+                            else put(vs + 4 * i, (uint16_t)(wide ? 0x7fc0u : 0x7e00u));
                         }
                 }
                 __syncwarp();
@@ -590,20 +575,20 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                 const int sw = DP == 64 ? ((r8 >> 1) & 1) << 1 : (r8 & 3) << 1;               // (row r8 + 8 has the same)
 #pragma unroll
                 for (int x = 0; x < C::SUB; x++) {
-                    float scale0[DP / 32], scale1[DP / 32];
-                    lds_all(prep + (x * 16 + r8) * (DP / 32) * 4, scale0);
-                    lds_all(prep + (x * 16 + r8 + 8) * (DP / 32) * 4, scale1);
+                    uint32_t scale0[DP / 32], scale1[DP / 32];
+                    get_all(prep + (x * 16 + r8) * (DP / 32) * 4, scale0);
+                    get_all(prep + (x * 16 + r8 + 8) * (DP / 32) * 4, scale1);
 #pragma unroll
                     for (int i = 0; i < DP / 32; i++) {
-                        const uint32_t at = kt + (x * 16 + r8) * C::ROW + (((2 * i + (j >> 1)) ^ sw) * 16) + (j & 1) * 8;
-                        const uint2 top = lds64(at), bot = lds64(at + 8 * C::ROW);
+                        const uint8_t* const at = tile + (x * 16 + r8) * C::ROW + (((2 * i + (j >> 1)) ^ sw) * 16) + (j & 1) * 8;
+                        const uint2 top = get<uint2>(at), bot = get<uint2>(at + 8 * C::ROW);
                         float part[NB][4];
                         uint32_t f[4], g[4];
                         halves(top.x, f[0], f[2]);
                         halves(bot.x, f[1], f[3]);
                         halves(top.y, g[0], g[2]);
                         halves(bot.y, g[1], g[3]);
-                        const float k0 = scale0[i], k1 = scale1[i];
+                        const float k0 = __uint_as_float(scale0[i]), k1 = __uint_as_float(scale1[i]);
 #pragma unroll
                         for (int nb = 0; nb < NB; nb++) {
                             part[nb][0] = part[nb][1] = part[nb][2] = part[nb][3] = 0.0f;
@@ -710,19 +695,19 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                             b0[nb] = transposed(pack2<F16>(s[x][nb][0], s[x][nb][1]));
                             b1[nb] = transposed(pack2<F16>(s[x][nb][2], s[x][nb][3]));
                         }
-                        float factor0[DP / 32], factor1[DP / 32];      // of rows 2j, 2j + 1 and 2j + 8, 2j + 9, two 16-bit numbers each
-                        const uint32_t factors = prep + C::TILE * (DP / 32) * 4 + (x * 8 + j) * (DP / 32) * 4;
-                        lds_all(factors, factor0);
-                        lds_all(factors + 4 * (DP / 32) * 4, factor1);
+                        uint32_t factor0[DP / 32], factor1[DP / 32];   // of rows 2j, 2j + 1 and 2j + 8, 2j + 9, two 16-bit numbers each
+                        const uint8_t* const factors = prep + C::TILE * (DP / 32) * 4 + (x * 8 + j) * (DP / 32) * 4;
+                        get_all(factors, factor0);
+                        get_all(factors + 4 * (DP / 32) * 4, factor1);
 #pragma unroll
                         for (int i = 0; i < DP / 32; i++) {
-                            const uint32_t f0 = __float_as_uint(factor0[i]), f1 = __float_as_uint(factor1[i]);
+                            const uint32_t f0 = factor0[i], f1 = factor1[i];
                             uint32_t c[4];         // codes 4 r8 .. 4 r8 + 3 of the block, rows 2j, 2j + 1, 2j + 8, 2j + 9
 #pragma unroll
                             for (int e = 0; e < 4; e++) {
                                 const int row = 2 * j + (e & 1) + (e >> 1) * 8;
                                 const int sw = DP == 64 ? ((row >> 1) & 1) << 1 : ((row >> 1) & 3) << 1;
-                                c[e] = lds32(vt + (x * 16 + row) * C::ROW + (((2 * i + (r8 >> 2)) ^ sw) * 16) + (r8 & 3) * 4);
+                                c[e] = get<uint32_t>(tile + (C::TILE + x * 16 + row) * C::ROW + (((2 * i + (r8 >> 2)) ^ sw) * 16) + (r8 & 3) * 4);
                             }
                             uint32_t p0[NB], p1[NB];
 #pragma unroll
