@@ -26,9 +26,9 @@
 //
 // Measured (one GB300, GPU time of the call with the join): bf16, 32 x 16384 positions of 8 key heads of 128, 32 query heads
 // 321 us = 6.70 TB/s of the cache's bytes (a plain copy runs at 6.78); one sequence of 131072 90 us, of which the join
-// is 5 to 6; 64 sequences of 1 to 8192 50 us (38 at the copy's rate). MXFP8, the 32 x 16384: 186 us = 5.95 TB/s, bound by the issue of
-// about 770 instructions a warp and 32 positions (conversions, scales, products; 1.8 a cycle of 4 with 8 warps an SM: more
-// warps take 16-row tiles, and 249 us). One sequence of 100: 6.3 us.
+// is 5 to 6; 64 sequences of 1 to 8192 50 us (38 at the copy's rate). MXFP8, the 32 x 16384: 182 us = 6.1 TB/s, near what DRAM gives
+// (about 9 us are the beginning and the join) with 724 instructions a warp and 32 positions, 1.6 a cycle with 8 warps an SM;
+// 12 warps take 16-row tiles, and 249 us; a third stage of the ring changes nothing. One sequence of 100: 6.3 us.
 #include "common.cuh"
 #include "paged_cache.cuh"
 
