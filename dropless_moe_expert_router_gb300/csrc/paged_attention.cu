@@ -750,6 +750,7 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                 l[nb][e] += __shfl_xor_sync(FULL, l[nb][e], 4);
                 l[nb][e] += __shfl_xor_sync(FULL, l[nb][e], 8);
                 l[nb][e] += __shfl_xor_sync(FULL, l[nb][e], 16);
+                if (FP8) l[nb][e] *= 0x1p-15f;         // (from here on without the fp16 weights' factor)
                 if (r8 == 0) ml[warp * 8 * NB + nb * 8 + 2 * j + e] = make_float2(m[nb][e], l[nb][e]);
             }
         __syncthreads();
@@ -759,14 +760,14 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
         const float o_scale = FP8 ? pow2((float)(vref - 127)) : 1.0f;
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
-            float f[2], f2[2];
+            float f[2];
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 float top = -INFINITY;
 #pragma unroll
                 for (int v = 0; v < PA_WARPS; v++) top = fmaxf(top, ml[v * 8 * NB + nb * 8 + 2 * j + e].x);
                 f[e] = top == -INFINITY ? 1.0f : pow2(m[nb][e] - top);
-                f2[e] = o_scale;
+                if (FP8) f[e] *= 0x1p-15f;
             }
 #pragma unroll
             for (int half = 0; half < 2; half++) {
@@ -776,7 +777,7 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         const int at = FP8 ? (d / 2) * 32 + r8 * 4 + (d % 2) * 2 + (e >> 1) : d * 16 + r8 + (e >> 1) * 8;
-                        mine[(2 * j + (e & 1)) * (C::HALF + 4) + at] = o[nb][half * (C::HALF / 16) + d][e] * f[e & 1] * f2[e & 1];
+                        mine[(2 * j + (e & 1)) * (C::HALF + 4) + at] = o[nb][half * (C::HALF / 16) + d][e] * f[e & 1] * o_scale;
                     }
                 __syncthreads();
                 // eight elements of a head a thread and turn
@@ -806,7 +807,7 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                             const long long row = (long long)now.b * a.q_heads + kv * group + head;
                             *reinterpret_cast<uint4*>(a.out + row * dim + at) = f32_to_bf16x8(v8);
                             if (a.lse && at == 0)
-                                a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum) - (FP8 ? 15.0f : 0.0f)) * 0.69314718055994530942f;
+                                a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
                         } else {
                             float* const to = a.part + (long long)slot * C::SLOT + (nb * 8 + h) * DP + at;
                             *reinterpret_cast<float4*>(to) = make_float4(v8[0], v8[1], v8[2], v8[3]);
@@ -908,7 +909,7 @@ __global__ void __launch_bounds__(PA_JOIN) attention_join_kernel(const __grid_co
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&up));
     }
     if (a.lse && lane == 0)
-        a.lse[row] = sum == 0.0f ? -INFINITY : (tops[hh] + log2f(sum) - (FP8 ? 15.0f : 0.0f)) * 0.69314718055994530942f;
+        a.lse[row] = sum == 0.0f ? -INFINITY : (tops[hh] + log2f(sum)) * 0.69314718055994530942f;
 }
 
 // Blocks of 8 query heads that a warp holds at once, by the group: what does not fit is another pass over the cache.

@@ -145,7 +145,7 @@ def test_large_scores_and_scales(precision):
 
 
 @pytest.mark.parametrize("precision", ["bf16", "mxfp8"])
-@pytest.mark.parametrize("factor", [2.0 ** -60, 2.0 ** -20, 2.0 ** 20, 2.0 ** 60])
+@pytest.mark.parametrize("factor", [2.0 ** -60, 2.0 ** -20, 2.0 ** 20, 2.0 ** 60, 2.0 ** 110])
 def test_values_of_any_size(precision, factor):
     """Values by a power of two larger or smaller give outputs by it larger or smaller, bit for bit; one token's
     values 2^20 times the others' leave those where its weight is small."""
