@@ -639,26 +639,36 @@ __global__ void __launch_bounds__(BS_JOIN) beam_join_kernel(const __grid_constan
         s.low[threadIdx.x] = order_of(low);
         __syncthreads();
         if (warp == 0) {
-            // the K-th largest of the threads', or a number a little below it: 20 of its bits do
+            // the K-th largest of the threads', or a number a little below it: 14 bits below the first in which those above
+            // -inf differ
+            constexpr uint32_t NONE = 0x007fffffu;
             uint32_t x[BS_JOIN / 32], any = 0u, all = 0xffffffffu;
+            int some = 0;
 #pragma unroll
             for (int i = 0; i < BS_JOIN / 32; i++) {
                 x[i] = s.low[i * 32 + lane_id()];
-                any |= x[i];
-                all &= x[i];
+                if (x[i] > NONE) {
+                    any |= x[i];
+                    all &= x[i];
+                }
+                some += __popc(__ballot_sync(FULL, x[i] > NONE));
             }
-            const uint32_t differ = __reduce_or_sync(FULL, any) ^ __reduce_and_sync(FULL, all);
-            const int top = differ ? 31 - __clz(differ) : 0;
-            uint32_t t = top == 31 ? 0u : x[0] >> (top + 1) << (top + 1);
-            for (int bit = top; bit >= max(0, top - 20); bit--) {
-                const uint32_t tried = t | (1u << bit);
-                int n = 0;
+            any = __reduce_or_sync(FULL, any);
+            const uint32_t differ = any ^ __reduce_and_sync(FULL, all);
+            uint32_t t = NONE;
+            if (some >= a.K) {
+                const int top = differ ? 31 - __clz(differ) : 0;
+                t = top == 31 ? 0u : any >> (top + 1) << (top + 1);
+                for (int bit = top; bit >= max(0, top - 14); bit--) {
+                    const uint32_t tried = t | (1u << bit);
+                    int n = 0;
 #pragma unroll
-                for (int i = 0; i < BS_JOIN / 32; i++) n += __popc(__ballot_sync(FULL, x[i] >= tried));
-                if (n >= a.K) t = tried;
-                if (n == a.K) break;
+                    for (int i = 0; i < BS_JOIN / 32; i++) n += __popc(__ballot_sync(FULL, x[i] >= tried));
+                    if (n >= a.K) t = tried;
+                    if (n == a.K) break;
+                }
             }
-            if (lane_id() == 0) s.threshold = max(t, 0x007fffffu);
+            if (lane_id() == 0) s.threshold = max(t, NONE);
         }
         __syncthreads();
         const float least = of_order(s.threshold);
