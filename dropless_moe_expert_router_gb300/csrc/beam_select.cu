@@ -15,8 +15,8 @@
 //    what fp32 bounds show to be behind K others, and ranks the rest by its value in two floats, of 46 bits or more
 //    (this device's 64-bit units are slow: a logarithm and the sums took 5 us in them).
 //
-// Measured (one GB300, GPU time): 32 searches of 8 beams over 131072 bf16 logits, K = 16: 26 us (67 MB, 9.9 us at the copy's rate), of
-// which the first kernel takes 19.5, bound by the issue of its instructions (two packed adds, a packed product, two powers and
+// Measured (one GB300, GPU time): 32 searches of 8 beams over 131072 bf16 logits, K = 16: 25.4 us (67 MB, 9.9 us at the copy's rate), of
+// which the first kernel takes 19, bound by the issue of its instructions (two packed adds, a packed product, two powers and
 // two unpackings for two logits are a third of them; thresholds and ranks of each stretch the most of the rest), and the second
 // 6 behind it, a chain of latencies. 1 search of 4 beams over 32000 fp32: 9 us.
 #include "common.cuh"
