@@ -442,13 +442,13 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// A number as the sum of two floats, the first the sum rounded.
+// A number as the sum of two floats, the first the sum rounded; where that is not finite, the second is 0.
 struct Pair {
     float h, l;
 };
 __device__ __forceinline__ Pair pair_of(float x, float y) {            // x + y exactly (Knuth's two-sum)
     const float h = __fadd_rn(x, y), z = __fsub_rn(h, x);
-    return {h, __fadd_rn(__fsub_rn(x, __fsub_rn(h, z)), __fsub_rn(y, z))};
+    return {h, isfinite(h) ? __fadd_rn(__fsub_rn(x, __fsub_rn(h, z)), __fsub_rn(y, z)) : 0.0f};
 }
 __device__ __forceinline__ Pair plus(Pair x, float y) {
     const Pair s = pair_of(x.h, y);

@@ -4,6 +4,8 @@ Bars. The sum under a beam's logarithm is of at most 2^11 terms a thread in fp32
 (exp), and in a few levels above that; so lse errs by 2^-12 at most. What is compared is ids: they have to be the
 reference's wherever its candidates are further apart than that, and everywhere in one beam, whose candidates
 all have the same error, and where nothing is rounded (equal beams, finished beams, -inf)."""
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -222,3 +224,39 @@ def test_refusals():
     with pytest.raises(MoeError):
         api.moe_beam_select(logits, scores, 4, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     assert api.moe_beam_select(logits[:0], scores[:0], 4).tokens.shape == (0, 4)
+
+
+def _ordered(logits, scores, K):
+    """The K best of every search by the definition, as (beam, token) and their scores in 64 bits, compared without rounding
+    (a score of -1e32 swallows a logit in 64 bits). A candidate that fp32 rounds to -inf counts as -inf."""
+    out = []
+    for x, s in zip(logits.double().cpu(), scores.double().cpu()):
+        lp = x - torch.logsumexp(x, -1)[:, None]
+        c = (s[:, None] + lp).float()
+        keys = [(-Fraction(s[w].item()) - Fraction(lp[w, t].item()) if c[w, t] > -INF else INF, w, t)
+                for w in range(x.shape[0]) for t in range(x.shape[1])]
+        out.append([(w, t, -float(v)) for v, w, t in sorted(keys)[:K]])
+    return out
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_sums_below_the_lowest_number(dtype):
+    """Forbidden tokens of the type's lowest value in beams whose score is the lowest number or near it, and a row of both ends
+    of the range: what fp32 cannot hold is -inf, last and in the indices' order. A score is rounded once, 2^-24 of itself, and lse
+    errs by BAR."""
+    logits, _ = _inputs(4, 3, 61, dtype, seed=12)
+    low, lowest = torch.finfo(dtype).min, torch.finfo(F32).min
+    scores = torch.tensor([[-1.0, lowest, -1e32], [lowest, -1e32, lowest], [lowest, lowest, lowest], [0.0, -2.0, lowest]], device="cuda")
+    logits[0, :, 5:] = low                                            # fewer tokens than K are allowed
+    logits[1, :, 3:] = low
+    logits[2, :, :58] = low
+    logits[3, 0] = 0.0
+    logits[3, 0, 7], logits[3, 0, [9, 20]] = 3e38, -3e38
+    for K in (1, 10, 40, 64):
+        o = api.moe_beam_select(logits, scores, K)
+        rows, tokens, got = o.parents.tolist(), o.tokens.tolist(), o.scores.tolist()
+        for n, want in enumerate(_ordered(logits, scores, K)):
+            assert [(r - 3 * n, t) for r, t in zip(rows[n], tokens[n])] == [(w, t) for w, t, _ in want], (n, K)
+            for g, (_, _, v) in zip(got[n], want):
+                assert g == v if v == -INF else abs(g - v) <= BAR + 2.0 ** -23 * abs(v), (n, K, g, v)
+    assert api.moe_get_device_errors() == 0
