@@ -6,17 +6,20 @@
 // 1. All rows' logits, in units of 2048 16-byte pieces, are cut into one equal stretch per block. Every thread copies its
 //    own eight pieces of a unit to a ring in shared memory, two units ahead and across rows, so loads are in flight all
 //    the time and the code is one short loop (eight pieces in registers in line took half as long again: it does not
-//    stay in the instruction cache). For each row of its stretch a block leaves the maximum, the sum of exponentials and its K largest logits in order (within a beam the
-//    order does not depend on lse). What is below a threshold is passed over a piece at a time by the piece's maximum.
+//    stay in the instruction cache). A unit is the same logits of a row wherever the row lies and whichever block has it, and
+//    its maximum and sum of exponentials are its own, so rows with the same logits have the same sums. Where rows begin off 16 bytes
+//    (V no multiple of a piece), the ring holds the aligned pieces around a unit and the threads read theirs across two of them.
+//    Besides, a block leaves for each row of its stretch the K largest logits in order (within a beam the order does not
+//    depend on lse). What is below a threshold is passed over a piece at a time by the piece's maximum.
 //    The first threshold is the K-th largest of the maxima of 64 groups of four threads in the row's first unit, found bit by bit by one
 //    warp: no fewer than K logits are that large. Later ones are the K-th largest found so far. Where more than the buffer
 //    holds pass, the unit's K-th largest itself is found bit by bit, and of what ties with it the first ones are taken in order.
-// 2. A block per search, set up while the first kernel runs, joins the sums and the lists: it drops
+// 2. A block per search, set up while the first kernel runs, joins the units' sums, in their order, and the lists: it drops
 //    what fp32 bounds show to be behind K others, and ranks the rest by its value in two floats, of 46 bits or more
 //    (this device's 64-bit units are slow: a logarithm and the sums took 5 us in them).
 //
-// Measured (one GB300, GPU time): 32 searches of 8 beams over 131072 bf16 logits, K = 16: 25.4 us (67 MB, 9.9 us at the copy's rate), of
-// which the first kernel takes 19, bound by the issue of its instructions (two packed adds, a packed product, two powers and
+// Measured (one GB300, GPU time): 32 searches of 8 beams over 131072 bf16 logits, K = 16: 24.7-25.1 us (67 MB, 9.9 us at the copy's rate;
+// 131071 logits, rows off 16 bytes: 30.8), of which the first kernel takes 19, bound by the issue of its instructions (two packed adds, a packed product, two powers and
 // two unpackings for two logits are a third of them; thresholds and ranks of each stretch the most of the rest), and the second
 // 6 behind it, a chain of latencies. 1 search of 4 beams over 32000 fp32: 9 us.
 #include "common.cuh"
@@ -31,6 +34,7 @@ constexpr int BS_HELD = 8;           // a thread's 16-byte pieces of a unit
 constexpr int BS_GROUPS = BS_THREADS / 4;
 constexpr int BS_CAP = 1024;         // logits that are ranked against each other
 constexpr int BS_CHECK = 16;         // units between two looks at how many there are, at most
+constexpr int BS_STAGE = BS_HELD * BS_THREADS + 1;   // pieces of a unit in the ring, and the one behind
 constexpr int BS_CTAS = 3;           // blocks an SM
 constexpr int BS_RING = 2;           // units on their way or looked at
 constexpr int BS_MAX_CTAS = 1024;    // blocks at most: what the workspace has room for
@@ -47,12 +51,13 @@ struct BeamArgs {
     int pad, W, V, K;
     int units, segments;             // units of a row; stretches that a row is in at most
     int ctas, each, longer;          // blocks; units of a block's stretch, one more for the first `longer` of them
+    long long count;                 // logits in all
     float* out_scores;
     int32_t* parents;
     int32_t* tokens;
-    // of block g's part of row r, at g + r: no two have the same
-    float2* part;                    // maximum, sum of exp relative to it
-    unsigned long long* list;        // [K] order of the logit, then of the lowest token; 0: none
+    float2* part;                    // [row][unit] maximum, sum of exp relative to it
+    // of block g's part of row r, at g + r (no two have the same): [K] order of the logit, then of the lowest token; 0: none
+    unsigned long long* list;
 };
 
 __device__ __forceinline__ float pow2(float x) {
@@ -125,10 +130,17 @@ struct Piece<float> {
         v[2] = __uint_as_float(x.z);
         v[3] = __uint_as_float(x.w);
     }
-    // elements [first, end) of it, -inf for the others
-    __device__ __forceinline__ void some(const float* p, int first, int end) {
+    // the one that begins so many elements behind a boundary (two 16-byte reads: short ones meet the same banks)
+    __device__ __forceinline__ void put_from(const uint4* at, int skew) {
+        const uint4 x = at[0], y = at[1];
+        const bool two = skew & 2, one = skew & 1;
+        const uint32_t w0 = two ? x.z : x.x, w1 = two ? x.w : x.y, w2 = two ? y.x : x.z, w3 = two ? y.y : x.w, w4 = two ? y.z : y.x;
+        put(make_uint4(one ? w1 : w0, one ? w2 : w1, one ? w3 : w2, one ? w4 : w3));
+    }
+    // -inf from element end on
+    __device__ __forceinline__ void cut(int end) {
 #pragma unroll
-        for (int e = 0; e < VEC; e++) v[e] = e >= first && e < end ? __ldg(p + e) : -INFINITY;
+        for (int e = 0; e < VEC; e++) v[e] = e < end ? v[e] : -INFINITY;
     }
     __device__ __forceinline__ float top() const { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }
 };
@@ -143,13 +155,19 @@ struct Piece<__nv_bfloat16> {
         return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
     }
     __device__ __forceinline__ void put(const uint4& x) { v = x; }
-    __device__ __forceinline__ void some(const __nv_bfloat16* p, int first, int end) {
+    __device__ __forceinline__ void put_from(const uint4* at, int skew) {
+        const uint4 x = at[0], y = at[1];
+        const bool four = skew & 4, two = skew & 2;
+        const uint32_t w0 = four ? x.z : x.x, w1 = four ? x.w : x.y, w2 = four ? y.x : x.z, w3 = four ? y.y : x.w, w4 = four ? y.z : y.x,
+                       w5 = four ? y.w : y.y;
+        const uint32_t z0 = two ? w1 : w0, z1 = two ? w2 : w1, z2 = two ? w3 : w2, z3 = two ? w4 : w3, z4 = two ? w5 : w4;
+        const int bits = 16 * (skew & 1);
+        v = make_uint4(__funnelshift_r(z0, z1, bits), __funnelshift_r(z1, z2, bits), __funnelshift_r(z2, z3, bits), __funnelshift_r(z3, z4, bits));
+    }
+    __device__ __forceinline__ void cut(int end) {
         uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < VEC; e++) {
-            const uint32_t x = e >= first && e < end ? (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + e) : 0xff80u;
-            w[e >> 1] = e & 1 ? w[e >> 1] | (x << 16) : x;
-        }
+        for (int i = 0; i < 4; i++) w[i] = 2 * i >= end ? 0xff80ff80u : 2 * i + 1 >= end ? (word(i) & 0xffffu) | 0xff800000u : word(i);
         v = make_uint4(w[0], w[1], w[2], w[3]);
     }
     __device__ __forceinline__ float top() const {
@@ -257,12 +275,13 @@ __device__ __forceinline__ void rank_keys(const unsigned long long* buf, int n, 
     }
 }
 
-template <typename T>
+// APART: rows begin off 16-byte boundaries.
+template <typename T, bool APART>
 __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __grid_constant__ BeamArgs a) {
     using P = Piece<T>;
-    extern __shared__ __align__(16) uint4 ring[];                      // [BS_RING][BS_HELD][BS_THREADS]
+    extern __shared__ __align__(16) uint4 ring[];                      // [BS_RING][BS_STAGE]
     __shared__ unsigned long long buf[BS_CAP], best[BS_MAX_K];
-    __shared__ float2 warps[BS_THREADS / 32];
+    __shared__ float2 sums[BS_CHECK][BS_THREADS / 32];                 // of the units since the last look, a warp's share each
     __shared__ uint32_t groups[BS_GROUPS], threshold;
     __shared__ int count, scan[BS_THREADS / 32];
     constexpr float LOG2E = 1.44269504088896340736f;
@@ -272,12 +291,10 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
     const int begin = (int)blockIdx.x * a.each + min((int)blockIdx.x, a.longer), end = begin + a.each + ((int)blockIdx.x < a.longer);
     long long row = begin / a.units;
     int u = begin - (int)row * a.units;
-    // pieces are counted from the last 16-byte boundary at or before the row, which is so many tokens before it
-    auto skew_of = [&](long long r) { return (int)(r * a.V % P::VEC); };
-    auto whole = [&](int t) { return t >= 0 && t + P::VEC <= a.V; };                  // a piece from token t on is all in the row
-    auto all_whole = [&](int v, int skew) { return v * UNIT >= skew && (v + 1) * UNIT - skew <= a.V; };   // unit v is
+    // tokens from the last 16-byte boundary at or before the row to its first
+    auto skew_of = [&](long long r) { return APART ? (int)(r * a.V % P::VEC) : 0; };
 
-    // the loading walk: a unit at a time, copies of what is whole
+    // the loading walk: a unit at a time, a thread the pieces at its places from the boundary on (APART: and one behind all)
     const T* ld_base = static_cast<const T*>(a.logits) + row * a.V;    // token t's logit: base[t]
     long long ld_row = row;
     int ld_left = end - begin, ld_u = u, ld_skew = skew_of(row), ld_stage = 0;
@@ -285,17 +302,23 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
         if (ld_left > 0) {
             ld_left--;
             const int t = ld_u * UNIT + (int)threadIdx.x * P::VEC - ld_skew;
-            const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + ld_stage * (BS_HELD * BS_THREADS) + threadIdx.x);
-            if (all_whole(ld_u, ld_skew)) {
+            const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + ld_stage * BS_STAGE + threadIdx.x);
+            // what lies behind the logits is zeros and not read, what lies behind the row is not copied
+            auto some = [&](int i) {
+                if (t + i * STEP >= a.V) return;
+                const long long left = a.count - ld_row * a.V - (t + i * STEP);
+                const int bytes = APART ? (int)min(16ll, left * (long long)sizeof(T)) : 16;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * BS_THREADS * 16), "l"(ld_base + t + i * STEP), "r"(bytes) : "memory");
+            };
+            if ((ld_u + 1) * UNIT <= a.V) {
 #pragma unroll
                 for (int i = 0; i < BS_HELD; i++)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * BS_THREADS * 16), "l"(ld_base + t + i * STEP) : "memory");
             } else {
 #pragma unroll 1
-                for (int i = 0; i < BS_HELD; i++)
-                    if (whole(t + i * STEP))
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * BS_THREADS * 16), "l"(ld_base + t + i * STEP) : "memory");
+                for (int i = 0; i < BS_HELD; i++) some(i);
             }
+            if (APART && threadIdx.x == 0) some(BS_HELD);
             if (++ld_u == a.units) {
                 ld_u = 0;
                 ld_row++;
@@ -315,23 +338,24 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
         const int u0 = u, u1 = min(a.units, u + (end - at)), skew = skew_of(row);
         at += u1 - u;
         float least = -INFINITY;
-        // sum of exponentials, relative to m (while that is -inf: 0, or NaN if there is one)
-        float m = -INFINITY, sum = 0.0f;
         int kept = 0, looked = 0;                                      // in buf at the last look, and units before it
         for (; u < u1; u++) {
             asm volatile("cp.async.wait_group %0;" ::"n"(BS_RING - 1) : "memory");
-            const int token = u * UNIT + (int)threadIdx.x * P::VEC - skew;            // of the thread's first piece's first element
-            const uint4* const mine = ring + stage * (BS_HELD * BS_THREADS) + threadIdx.x;
+            if (APART) __syncthreads();                                // (a thread's piece is of two threads' copies)
+            const int token = u * UNIT + (int)threadIdx.x * P::VEC;    // of the thread's first piece's first element
+            const uint4* const mine = ring + stage * BS_STAGE + threadIdx.x;
+            auto read = [&](P& q, int i) {
+                if (APART) q.put_from(mine + i * BS_THREADS, skew);
+                else q.put(mine[i * BS_THREADS]);
+            };
             P p[BS_HELD];
-            if (all_whole(u, skew)) {
 #pragma unroll
-                for (int i = 0; i < BS_HELD; i++) p[i].put(mine[i * BS_THREADS]);
-            } else {
+            for (int i = 0; i < BS_HELD; i++) read(p[i], i);
+            if ((u + 1) * UNIT > a.V) {
 #pragma unroll
-                for (int i = 0; i < BS_HELD; i++) {
-                    const int t = token + i * STEP;
-                    if (whole(t)) p[i].put(mine[i * BS_THREADS]);
-                    else p[i].some(base + t, max(0, -t), min(P::VEC, a.V - t));
+                for (int i = 0; i < BS_HELD; i++) {                    // (cutting what is whole or absent word by word, too: 30.6 us in place of 24.7)
+                    if (APART) p[i].cut(a.V - (token + i * STEP));
+                    else if (token + i * STEP >= a.V) p[i].cut(0);
                 }
             }
             float tops[BS_HELD], top = -INFINITY;
@@ -352,12 +376,10 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
                     if (lane_id() == 0) threshold = t;
                 }
             }
-            if (top > m) {
-                sum *= m == -INFINITY ? 1.0f : pow2((m - top) * LOG2E);
-                m = top;
-            }
+            // the unit's sum, each thread's relative to its own maximum (where that is -inf: 0, or NaN if there is one), then the
+            // warp's, in an order that is the same for all units
             {
-                const float sub = m == -INFINITY ? 0.0f : -m;
+                const float sub = top == -INFINITY ? 0.0f : -top;
                 const Two minus(sub, sub), log2e(LOG2E, LOG2E);
                 Two sum0(0.0f, 0.0f), sum1(0.0f, 0.0f);
 #pragma unroll
@@ -368,7 +390,12 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
                 sum0 += sum1;
                 float s0, s1;
                 sum0.get(s0, s1);
-                sum += s0 + s1;
+                const float high = of_order(__reduce_max_sync(FULL, order_of(top)));
+                float sum = s0 + s1;
+                if (top != -INFINITY) sum *= pow2((top - high) * LOG2E);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+                if (lane_id() == 0) sums[u - u0 - looked][warp] = make_float2(high, sum);
             }
             if (u == u0) {
                 __syncthreads();
@@ -382,8 +409,7 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
                 const int i = __ffs(hits) - 1, t = token + i * STEP;
                 hits &= hits - 1;
                 P q;
-                if (whole(t)) q.put(mine[i * BS_THREADS]);
-                else q.some(base + t, max(0, -t), min(P::VEC, a.V - t));
+                read(q, i);
                 unsigned found = 0u;
 #pragma unroll
                 for (int e = 0; e < P::VEC; e++) found |= (unsigned)(q.at(e) >= least) << e;
@@ -395,6 +421,7 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
                     if (to < BS_CAP) buf[to] = key_of(q.pick(e), t + e);
                 }
             }
+            if (APART) __syncthreads();
             issue();
             stage = stage + 1 == BS_RING ? 0 : stage + 1;
             const bool more = u + 1 < u1;
@@ -403,6 +430,15 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
             // every few units: the K largest so far in order, the last of them the threshold
             __syncthreads();
             int n = count;
+            if ((int)threadIdx.x < done - looked) {                    // the units' sums, of the warps in their order
+                const float2* const x = sums[threadIdx.x];
+                float high = -INFINITY, v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < BS_THREADS / 32; w++) high = fmaxf(high, x[w].x);
+#pragma unroll
+                for (int w = 0; w < BS_THREADS / 32; w++) v += x[w].x == -INFINITY ? x[w].y : x[w].y * pow2((x[w].x - high) * LOG2E);
+                a.part[row * a.units + u0 + looked + threadIdx.x] = make_float2(high, v);
+            }
             __syncthreads();                                           // (nobody adds to it before all have read it)
             if (n > BS_CAP) {
                 n = exactly_largest<T>(base, token - (done - looked - 1) * UNIT, (done - looked) * BS_HELD, a.V, a.K, buf, kept, &count, scan);
@@ -420,24 +456,6 @@ __global__ void __launch_bounds__(BS_THREADS, BS_CTAS) beam_rows_kernel(const __
         }
         const long long to = blockIdx.x + row;
         if ((int)threadIdx.x < a.K) a.list[to * a.K + threadIdx.x] = (int)threadIdx.x < kept ? buf[threadIdx.x] : 0ull;
-        float high = m;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) high = fmaxf(high, __shfl_xor_sync(FULL, high, o));
-        if (m != -INFINITY) sum *= pow2((m - high) * LOG2E);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-        if (lane_id() == 0) warps[warp] = make_float2(high, sum);
-        __syncthreads();
-        if (warp == 0) {
-            const float2 x = lane_id() < BS_THREADS / 32 ? warps[lane_id()] : make_float2(-INFINITY, 0.0f);
-            high = x.x;
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) high = fmaxf(high, __shfl_xor_sync(FULL, high, o));
-            float v = x.x == -INFINITY ? x.y : x.y * pow2((x.x - high) * LOG2E);
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
-            if (lane_id() == 0) a.part[to] = make_float2(high, v);
-        }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
@@ -547,15 +565,15 @@ __global__ void __launch_bounds__(BS_JOIN) beam_join_kernel(const __grid_constan
     fetch();
     for (int w0 = 0; w0 < a.W; w0 += BS_JOIN / BS_BEAM) {
         const int w = w0 + threadIdx.x / BS_BEAM, l = threadIdx.x % BS_BEAM;
-        const int parts = w < a.W ? s.parts[w] : 0;
-        const float2* part = a.part + row0 + (w < a.W ? w + s.first[w] : 0);
-        const float2 mine = l < parts ? __ldcg(part + l) : make_float2(-INFINITY, 0.0f);
+        const int units = w < a.W ? a.units : 0;
+        const float2* part = a.part + (row0 + w) * a.units;
+        const float2 mine = l < units ? __ldcg(part + l) : make_float2(-INFINITY, 0.0f);
         float m = mine.x;
-        for (int c = l + BS_BEAM; c < parts; c += BS_BEAM) m = fmaxf(m, __ldcg(part + c).x);
+        for (int c = l + BS_BEAM; c < units; c += BS_BEAM) m = fmaxf(m, __ldcg(part + c).x);
 #pragma unroll
         for (int o = BS_BEAM / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
         Pair sum = {0.0f, 0.0f};
-        for (int c = l; c < parts; c += BS_BEAM) {
+        for (int c = l; c < units; c += BS_BEAM) {
             const float2 x = c == l ? mine : __ldcg(part + c);
             sum = plus(sum, x.x == -INFINITY || x.x == m ? x.y : x.y * expf(x.x - m));
         }
@@ -713,12 +731,11 @@ __global__ void __launch_bounds__(BS_JOIN) beam_join_kernel(const __grid_constan
     }
 }
 
-// Units of a row: 16-byte pieces that hold V logits wherever the row begins, in blocks' shares.
+// Units of a row: so many 16-byte pieces from its first logit on.
 template <typename T>
 int units_of(int V) {
-    using P = Piece<T>;
-    const int pieces = V % P::VEC ? (V + 2 * P::VEC - 2) / P::VEC : V / P::VEC, share = BS_THREADS * BS_HELD;
-    return (pieces + share - 1) / share;
+    constexpr int UNIT = BS_THREADS * BS_HELD * Piece<T>::VEC;
+    return (V + UNIT - 1) / UNIT;
 }
 
 bool refused(int N, int W, int V, int K) {
@@ -728,7 +745,7 @@ bool refused(int N, int W, int V, int K) {
 
 size_t slots(int N, int W) { return (size_t)N * W + BS_MAX_CTAS; }
 
-template <typename T>
+template <typename T, bool APART>
 moe_status launch(BeamArgs a, int N, cudaStream_t s) {
     static moe_host::PerDevice ring, smem, sms_of;
     int dev = 0;
@@ -746,9 +763,10 @@ moe_status launch(BeamArgs a, int N, cudaStream_t s) {
     // the stretches that a row's units can lie in
     const int parts = (a.units - 1 + a.each - 1) / a.each + 1;
     a.segments = parts < a.units ? parts : a.units;
-    constexpr int RING = BS_RING * BS_HELD * BS_THREADS * sizeof(uint4);
-    if (!moe_host::allow_smem(beam_rows_kernel<T>, RING, ring)) return MOE_ERR_CUDA;
-    beam_rows_kernel<T><<<a.ctas, BS_THREADS, RING, s>>>(a);
+    a.count = (long long)N * a.W * a.V;
+    constexpr int RING = BS_RING * BS_STAGE * sizeof(uint4);
+    if (!moe_host::allow_smem(beam_rows_kernel<T, APART>, RING, ring)) return MOE_ERR_CUDA;
+    beam_rows_kernel<T, APART><<<a.ctas, BS_THREADS, RING, s>>>(a);
     const moe_status st = moe_host::launch_status();
     if (st != MOE_OK) return st;
     if (!moe_host::allow_smem(beam_join_kernel, sizeof(Joined), smem) ||
@@ -757,13 +775,18 @@ moe_status launch(BeamArgs a, int N, cudaStream_t s) {
     return moe_host::launch_status();
 }
 
+template <typename T>
+moe_status launch_of(const BeamArgs& a, int N, cudaStream_t s) {
+    return a.V % Piece<T>::VEC ? launch<T, true>(a, N, s) : launch<T, false>(a, N, s);
+}
+
 }  // namespace
 }  // namespace moe
 
 extern "C" size_t moe_beam_select_workspace_size(int N, int W, int V, int K) {
     using namespace moe;
     if (refused(N, W, V, K)) return 0;
-    return slots(N, W) * (K * sizeof(unsigned long long) + sizeof(float2));
+    return slots(N, W) * K * sizeof(unsigned long long) + (size_t)N * W * units_of<float>(V) * sizeof(float2);
 }
 
 extern "C" moe_status moe_beam_select(const void* logits, moe_dtype dtype, const float* scores, const uint8_t* done, int pad,
@@ -780,8 +803,8 @@ extern "C" moe_status moe_beam_select(const void* logits, moe_dtype dtype, const
         !moe_host::aligned(parents, 4) || !moe_host::aligned(tokens, 4) || !moe_host::aligned(workspace, 16))
         return MOE_ERR_ALIGNMENT;
     if (N == 0) return MOE_OK;
-    BeamArgs a = {logits, scores, done, pad, W, V, K, 0, 0, 0, 0, 0, out_scores, parents, tokens, nullptr, nullptr};
+    BeamArgs a = {logits, scores, done, pad, W, V, K, 0, 0, 0, 0, 0, 0, out_scores, parents, tokens, nullptr, nullptr};
     a.list = static_cast<unsigned long long*>(workspace);
     a.part = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + slots(N, W) * K * sizeof(unsigned long long));
-    return dtype == MOE_F32 ? launch<float>(a, N, moe_host::as_stream(stream)) : launch<__nv_bfloat16>(a, N, moe_host::as_stream(stream));
+    return dtype == MOE_F32 ? launch_of<float>(a, N, moe_host::as_stream(stream)) : launch_of<__nv_bfloat16>(a, N, moe_host::as_stream(stream));
 }

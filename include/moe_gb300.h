@@ -702,9 +702,10 @@ moe_status moe_cache_copy_pages(void *const *tensors, const long long *page_byte
  * beam whose score or lse is not finite: -inf. done [N, W] bytes (NULL: none): a beam that is
  * done has one candidate, token pad with its score as it is, and -inf elsewhere. The K largest in
  * order, ties to the lower w, then the lower t: out_scores [N, K] fp32, parents [N, K] = n * W + w,
- * tokens [N, K]. lse is summed in fp32, each block's share of a row apart; it, the joined sums and
- * the candidates are held in two floats (46 bits or more; a candidate that fp32 rounds to -inf
- * counts as -inf) and rounded once. Requires 1 <= W <= 64, 1 <= V < 2^24,
+ * tokens [N, K]. lse is summed in fp32, the same pieces of a row apart wherever it lies (equal
+ * beams have equal candidates, and a search its scores whatever stands beside it); it, the joined
+ * sums and the candidates are held in two floats (46 bits or more; a candidate that fp32 rounds
+ * to -inf counts as -inf) and rounded once. Requires 1 <= W <= 64, 1 <= V < 2^24,
  * N * W < 2^24, 1 <= K <= 64, K <= W * V, 0 <= pad < V with done. workspace:
  * moe_beam_select_workspace_size bytes (0 for refused sizes), 16-byte aligned, not initialised; calls that
  * share one must not overlap. */

@@ -260,3 +260,32 @@ def test_sums_below_the_lowest_number(dtype):
             for g, (_, _, v) in zip(got[n], want):
                 assert g == v if v == -INF else abs(g - v) <= BAR + 2.0 ** -23 * abs(v), (n, K, g, v)
     assert api.moe_get_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype,N,W,V", [(BF, 32, 8, 131_072), (F32, 32, 8, 65_536), (BF, 32, 8, 50_257), (F32, 32, 8, 30_001),
+                                         (BF, 3, 5, 40_003), (F32, 700, 2, 9_001), (BF, 1, 64, 1_001)])
+def test_equal_beams_of_many_units(dtype, N, W, V):
+    """Beams with the same logits and scores are taken in their order wherever the blocks' stretches cut their rows and
+    wherever the rows begin against 16 bytes: their values are the same bits."""
+    K = 2 * W if W <= 32 else W
+    g = torch.Generator(device="cuda").manual_seed(V)
+    one = (torch.randn((N, 1, V), generator=g, device="cuda") * 2.5).to(dtype)
+    scores = (-8 * torch.rand((N, 1), generator=g, device="cuda")).expand(N, W).contiguous()
+    o = api.moe_beam_select(one.expand(N, W, V).contiguous(), scores, K)
+    for n in range(N):
+        at = torch.sort(one[n].float().expand(W, V).reshape(-1), descending=True, stable=True).indices[:K]
+        assert torch.equal(o.parents[n].long(), n * W + at // V) and torch.equal(o.tokens[n].long(), at % V), n
+    assert api.moe_get_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype,V", [(BF, 131_072), (F32, 20_000), (BF, 50_257), (F32, 33_333), (BF, 333)])
+def test_a_search_does_not_depend_on_its_place(dtype, V):
+    """The same search at every place of a batch, and alone, gives the same bits."""
+    logits, scores = _inputs(1, 5, V, dtype, seed=V)
+    alone = api.moe_beam_select(logits, scores, 16)
+    N = 31
+    o = api.moe_beam_select(logits.expand(N, 5, V).contiguous(), scores.expand(N, 5).contiguous(), 16)
+    base = 5 * torch.arange(N, dtype=I32, device="cuda")[:, None]
+    assert torch.equal(o.scores, alone.scores.expand(N, 16)) and torch.equal(o.tokens, alone.tokens.expand(N, 16))
+    assert torch.equal(o.parents - base, alone.parents.expand(N, 16))
+    assert api.moe_get_device_errors() == 0
