@@ -330,7 +330,7 @@ template <bool ONE>
 __device__ __forceinline__ int needs_of(const ForkArgs& a, const Marks<ONE>& marks, int i, int* held_out, int* last_out) {
     const int par = parent_of(a, i);
     const int l = length_of(a, par), ps = a.page_size;
-    const int held = (l + ps - 1) / ps;
+    const int held = l / ps + (l % ps != 0);               // (l + ps passes 2^31)
     *held_out = held;
     *last_out = -1;
     if (par < 0 || par >= a.S) return 0;

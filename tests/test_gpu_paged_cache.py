@@ -421,3 +421,20 @@ def test_refusals():
         api.moe_cache_copy_pages([cache, api.cache_buffers(5, 2, 4, 32, "cuda")], _i32([0]), _i32([1]))
     with pytest.raises(ValueError):
         api.moe_cache_copy_pages(cache, torch.tensor([0], dtype=I32), torch.tensor([1], dtype=I32))
+
+
+def test_fork_of_sequences_near_two_to_the_31():
+    """2046 * 1049601 = 2^31 - 2 positions a row: lengths whose sum with a page passes 31 bits."""
+    page, M = 2046, 1_049_601
+    table = torch.arange(M, dtype=I32, device="cuda")[None]
+    for n, room in ((page * M - 1, 1), (page * M, 1), (page * M, 0), (page * M - page, 7)):
+        got = api.moe_cache_fork(table, _i32([n]), _i32([0, 0]), M + 2, page, room=room)
+        want = table.expand(2, M).clone()
+        src, dst, used = [-1, -1], [-1, -1], M
+        if n % page:                                                  # the second row's copy of the page that both would write
+            src[1], dst[1], want[1, -1], used = M - 1, M, M, M + 1
+        elif n < page * M:                                            # a page behind for each (M - 1 is free, too)
+            want[:, -1], used = torch.tensor([M - 1, M], dtype=I32, device="cuda"), M + 1
+        assert torch.equal(got.table, want) and got.lengths.tolist() == [n, n]
+        assert got.src.tolist() == src and got.dst.tolist() == dst and got.used.item() == used
+    assert api.moe_get_device_errors() == 0
