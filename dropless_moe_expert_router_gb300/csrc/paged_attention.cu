@@ -194,7 +194,10 @@ __device__ __forceinline__ void range_of(const AttnArgs& a, int b, int& first, i
 }
 // A pair's units: one at least, which writes the output of a sequence without positions. On the line that is cut into
 // stretches PA_BEGIN steps stand before them: what a block takes for a pair however few units it has of it.
-__device__ __forceinline__ int units_of(int first, int n, int unit) { return max(1, (n - first + unit - 1) / unit); }
+// (Positions are counted in 31 bits, those up to a unit's end in 32.)
+__device__ __forceinline__ int units_of(int first, int n, int unit) {
+    return max(1, (int)(((uint32_t)(n - first) + (uint32_t)unit - 1u) / (uint32_t)unit));
+}
 
 struct Walk {
     int b, pair, first, n, units;                 // pair: of a sequence's key heads and tiles of query heads
@@ -326,13 +329,13 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                 ld_kv = ld.pair / a.tiles_of_heads;
                 continue;
             }
-            const int t = ld.first + ld_u * C::UNIT + warp * C::TILE;
+            const uint32_t t = (uint32_t)ld.first + (uint32_t)ld_u * C::UNIT + warp * C::TILE;
             ld_u++;
-            if (t >= ld.n) continue;
-            const int p = t + (lane & (C::TILE - 1));
-            ld_in = p < ld.n;
-            const int col = a.page_mul ? (int)(__umulhi((uint32_t)p, a.page_mul) >> a.page_shift) : p;
-            ld_off = p - col * a.c.page_size;
+            if (t >= (uint32_t)ld.n) continue;
+            const uint32_t p = t + (lane & (C::TILE - 1));
+            ld_in = p < (uint32_t)ld.n;
+            const int col = a.page_mul ? (int)(__umulhi(p, a.page_mul) >> a.page_shift) : (int)p;
+            ld_off = (int)p - col * a.c.page_size;
             ld_page = ld_in ? __ldg(a.table + (long long)ld.b * a.M + col) : -1;
             ld_more = true;
             return;
@@ -476,7 +479,7 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
 #pragma unroll
                 for (int e = 0; e < 4; e++) o[nb][d][e] = 0.0f;
         }
-        const int my_end = min(w.u1, (max(0, w.n - w.first - warp * C::TILE) + C::UNIT - 1) / C::UNIT);
+        const int my_end = min(w.u1, (int)(((uint32_t)max(0, w.n - w.first - warp * C::TILE) + C::UNIT - 1u) / C::UNIT));
 #pragma unroll 1
         for (int u = w.u; u < my_end; u++) {
             copies_wait<C::STAGES - 1>();

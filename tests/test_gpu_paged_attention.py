@@ -5,6 +5,8 @@ e = (dim + 4) u scale sum |q k|; a weight exp(s - m) then errs by 2 e of itself 
 16 bits (at most half a step of bf16, 2^-8) and by 2^-12 for exp, the rescalings and the sums (a thread adds
 fewer than 2^11 terms in a row). With A = sum w |v| the output errs by (2^-8 + 2 e + 2^-12) A and its own
 rounding, 2^-8 of itself; lse by e + 2^-12 and its rounding."""
+import math
+
 import pytest
 import torch
 
@@ -385,3 +387,32 @@ def test_refusals():
         wide = torch.zeros((2, 8 * 64 + 4), device="cuda", dtype=BF)
         call(wide[:, :512].unflatten(1, (8, 64)), cache, table, lens)
     assert api.moe_paged_attention(q[:0], cache, table[:0], lens[:0])[0].shape == (0, 8, 64)
+
+
+@pytest.mark.parametrize("precision", ["bf16", "mxfp8"])
+def test_a_length_near_two_to_the_31(precision):
+    """2^31 - 2 positions, every one of the 1049601 pages of 2046 positions the same: the attention over one page, and lse by
+    ln 1049601 larger. With a block on each of 152 SMs or more, a lane adds to its sums at most 2^31 / (152 * 4 * 16) < 2^18 times in
+    a row (sixteen positions of a warp's at a time). So the sum of weights errs by 2^18 * 2^-24 = 2^-6 at most, which is the bar
+    of lse, and the numerators by 2^-5 (the matrix unit may cut where it adds, 2^-23). The values are between 1 and 2; two more
+    roundings of 2^-8."""
+    page, M = 2046, 1_049_601
+    cache, table, dense = _cache([page], 1, 32, page, precision, spare=0)
+    v = torch.rand((page, 1, 32), generator=torch.Generator(device="cuda").manual_seed(2), device="cuda") + 1
+    k = dense[0][0].to(BF)
+    pos, rows = torch.arange(page, dtype=I32, device="cuda"), torch.zeros(page, dtype=I32, device="cuda")
+    api.moe_cache_append(k, v.to(BF), cache, table, pos, rows=rows)
+    k, v = api.moe_cache_gather(cache, table, pos, rows=rows)
+    q = _randn((1, 2, 32), torch.Generator(device="cuda").manual_seed(3)).to(BF)
+    many = torch.zeros((1, M), dtype=I32, device="cuda")
+    n = torch.tensor([page * M], dtype=I32, device="cuda")
+    out, lse = api.moe_paged_attention(q, cache, many, n)
+    s = q[0].double() @ k[:, 0].double().t() * 32 ** -0.5
+    ref = torch.softmax(s, 1) @ v[:, 0].double()
+    assert bool(((lse[0].double() - torch.logsumexp(s, 1) - math.log(M)).abs() <= 2.0 ** -6 + 2.0 ** -12).all())
+    assert bool(((out[0].double() - ref).abs() <= (2.0 ** -5 + 2.0 ** -6 + 2.0 ** -7) * ref).all())
+    # the last positions of it: one page less its first position
+    out, lse = api.moe_paged_attention(q, cache, many, n, window=page - 1)
+    ref = torch.softmax(s[:, 1:], 1) @ v[1:, 0].double()
+    assert bool(((out[0].double() - ref).abs() <= (2.0 ** -7 + 2.0 ** -11) * ref).all())
+    assert api.moe_get_device_errors() == 0
