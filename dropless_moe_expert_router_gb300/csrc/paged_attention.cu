@@ -126,6 +126,10 @@ __device__ __forceinline__ float pow2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// 2^e for e <= 127, in fp32's subnormals too (ex2.approx.ftz has none).
+__device__ __forceinline__ float two_to(int e) {
+    return __uint_as_float(e >= -126 ? (uint32_t)(e + 127) << 23 : e >= -149 ? 1u << (e + 149) : 0u);
+}
 // Shared memory by pointers: the compiler orders these between the barriers as it likes.
 template <typename T>
 __device__ __forceinline__ T get(const uint8_t* p) { return *reinterpret_cast<const T*>(p); }
@@ -519,7 +523,7 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                 most = __reduce_max_sync(FULL, most);
                 least = __reduce_min_sync(FULL, here ? least : 255u);
                 if ((int)most > vref) {
-                    const float f = pow2((float)(vref - (int)most));
+                    const float f = two_to(vref - (int)most);
 #pragma unroll
                     for (int nb = 0; nb < NB; nb++)
 #pragma unroll
@@ -760,7 +764,7 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
         const int kv = now.pair / a.tiles_of_heads, h0 = (now.pair - kv * a.tiles_of_heads) * 8 * NB;
         const bool cut = now.u > 0 || now.u1 < now.units;
         const int slot = 2 * blockIdx.x + (now.u > 0 ? 0 : 1);
-        const float o_scale = FP8 ? pow2((float)(vref - 127)) : 1.0f;
+        const float o_scale = FP8 ? two_to(vref - 127) : 1.0f;
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
             float f[2];

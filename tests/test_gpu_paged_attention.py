@@ -416,3 +416,25 @@ def test_a_length_near_two_to_the_31(precision):
     ref = torch.softmax(s[:, 1:], 1) @ v[1:, 0].double()
     assert bool(((out[0].double() - ref).abs() <= (2.0 ** -7 + 2.0 ** -11) * ref).all())
     assert api.moe_get_device_errors() == 0
+
+
+@pytest.mark.parametrize("dim,q_heads,heads", [(64, 4, 2), (128, 8, 1), (256, 2, 1), (96, 20, 1)])
+def test_values_of_the_smallest_scale(dim, q_heads, heads):
+    """Values whose scale bytes are 0 (2^-127), alone and beside the next ones. Their codes are 1 and above, so that each is a
+    bf16 number."""
+    lengths = [37, 300, 1]
+    cache, table, _ = _cache(lengths, heads, dim, 16, "mxfp8")
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    cache.v.copy_(torch.randint(0x38, 0x7f, cache.v.shape, generator=g, device="cuda"))
+    q = _randn((3, q_heads, dim), g).to(BF)
+    rows = torch.cat([torch.full((n,), b, dtype=I32) for b, n in enumerate(lengths)]).cuda()
+    pos = torch.cat([torch.arange(n, dtype=I32) for n in lengths]).cuda()
+    for most in (1, 2, 4):
+        cache.v_scales.copy_(torch.randint(0, most, cache.v_scales.shape, generator=g, device="cuda"))
+        k, v = api.moe_cache_gather(cache, table, pos, rows=rows)
+        out, lse = api.moe_paged_attention(q, cache, table, torch.tensor(lengths, dtype=I32, device="cuda"))
+        dense = [(k[rows == b].double(), v[rows == b].double()) for b in range(3)]
+        assert min(d[1].min() for d in dense) >= 2.0 ** -127
+        _check(q, cache, table, lengths, dense, out, lse)
+        # (the bar of _check has 1e-38 for what fp32 cannot hold; these outputs are all well above)
+        assert out.float().min() >= 2.0 ** -127
