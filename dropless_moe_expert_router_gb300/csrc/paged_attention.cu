@@ -31,6 +31,7 @@
 // 12 warps take 16-row tiles, and 249 us; a third stage of the ring changes nothing. One sequence of 100: 6.3 us.
 #include "common.cuh"
 #include "paged_cache.cuh"
+#include "scale_words.h"
 
 #include <math.h>
 
@@ -300,6 +301,7 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
     const int warp = threadIdx.x / 32, lane = lane_id(), j = lane & 3, r8 = lane >> 2;
     const int dim = a.c.dim, group = a.q_heads / a.c.heads, pairs = a.c.heads * a.tiles_of_heads;
     const int row_bytes = dim * (FP8 ? 1 : 2), row_scales = dim / 32;
+    const long long lines = (long long)a.c.pages * a.c.heads * a.c.page_size;
     // the bytes of a row's scales that there are, four and four
     const uint32_t keep0 = row_scales >= 4 ? 0xffffffffu : (1u << (8 * row_scales)) - 1u;
     const uint32_t keep1 = row_scales >= 8 ? 0xffffffffu : row_scales > 4 ? (1u << (8 * (row_scales - 4))) - 1u : 0u;
@@ -395,16 +397,21 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                     const bool is_v = C::SUB == 2 ? x == 1 : lane >= 16;
                     const uint8_t* const base = (is_v ? a.c.v_scales : a.c.k_scales) + scales_at;
                     const uint32_t slot = at + C::KV + (x * 32 + lane) * 16;
+                    uint8_t* const here = ring_at + (slot - ring);
                     if (row_scales == DP / 32 && DP >= 128) {          // whole words
 #pragma unroll
                         for (int i = 0; i < DP / 128; i++) copy4(slot + 4 * i, base + 4 * i, ok);
-                            put(ring_at + (slot - ring) + 12, 0u);
+                        put(here + 12, 0u);
+                    } else if (ok && scales_at_an_end(line, lines)) {
+#pragma unroll 1
+                        for (int i = 0; i < row_scales; i++) put(here + i, __ldg(base + i));
+                        put(here + 12, 0u);
                     } else {
-                        const int skip = (int)(reinterpret_cast<uintptr_t>(base) & 3), words = (skip + row_scales + 3) / 4;
+                        const ScaleWords w = scale_words(reinterpret_cast<uintptr_t>(base), row_scales);
 #pragma unroll
                         for (int i = 0; i < (DP / 32 + 6) / 4; i++)
-                            if (i < words) copy4(slot + 4 * i, base - skip + 4 * i, ok);
-                        put(ring_at + (slot - ring) + 12, ok ? 8u * skip : 0u);
+                            if (i < w.words) copy4(slot + 4 * i, base - w.skip + 4 * i, ok);
+                        put(here + 12, ok ? 8u * w.skip : 0u);
                     }
                 }
             }

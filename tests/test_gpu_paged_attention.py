@@ -438,3 +438,21 @@ def test_values_of_the_smallest_scale(dim, q_heads, heads):
         _check(q, cache, table, lengths, dense, out, lse)
         # (the bar of _check has 1e-38 for what fp32 cannot hold; these outputs are all well above)
         assert out.float().min() >= 2.0 ** -127
+
+
+@pytest.mark.parametrize("dim,offset", [(32, 1), (64, 2), (96, 3), (160, 1), (192, 2), (224, 3)])
+def test_scales_that_begin_off_a_word(dim, offset):
+    """Pools of scales that begin and end inside words whose other bytes are NaN's, every page of them in use: outputs are those of
+    pools of their own, bit for bit."""
+    lengths = [15, 9, 1]
+    cache, table, dense = _cache(lengths, 3, dim, 5, "mxfp8", spare=0)
+    q = _randn((3, 6, dim), torch.Generator(device="cuda").manual_seed(dim)).to(BF)
+    lens = torch.tensor(lengths, dtype=I32, device="cuda")
+    out, lse = api.moe_paged_attention(q, cache, table, lens)
+    _check(q, cache, table, lengths, dense, out, lse)
+    moved = []
+    for t in (cache.k_scales, cache.v_scales):
+        buf = torch.full((t.numel() + 16,), 255, dtype=torch.uint8, device="cuda")
+        moved.append(buf[offset:offset + t.numel()].view(t.shape).copy_(t))
+    o2, l2 = api.moe_paged_attention(q, cache._replace(k_scales=moved[0], v_scales=moved[1]), table, lens)
+    assert torch.equal(o2, out) and torch.equal(l2, lse) and api.moe_get_device_errors() == 0
