@@ -2,6 +2,7 @@
 #pragma once
 
 #include <atomic>
+#include <mutex>
 
 namespace moe_host {
 
@@ -10,11 +11,13 @@ namespace moe_host {
 class PerDevice {
   public:
     // The number reaches value: raise(value) sets it on the current device where it is still smaller, and says
-    // whether that worked.
+    // whether that worked. One thread at a time, so that no smaller value is set behind a larger one.
     template <typename Raise>
     bool reach(int device, int value, Raise raise) {
         if (device < 0 || device >= MOST) return raise(value);
         if (value <= at_[device].load(std::memory_order_acquire)) return true;
+        const std::lock_guard<std::mutex> one(raising_);
+        if (value <= at_[device].load(std::memory_order_relaxed)) return true;
         if (!raise(value)) return false;
         at_[device].store(value, std::memory_order_release);
         return true;
@@ -32,6 +35,7 @@ class PerDevice {
   private:
     static constexpr int MOST = 64;
     std::atomic<int> at_[MOST] = {};
+    std::mutex raising_;
 };
 
 }  // namespace moe_host

@@ -72,3 +72,51 @@ def test_no_launch_remembers_for_the_whole_process():
     for path in glob.glob(os.path.join(CSRC, "*.cu")):
         with open(path) as f:
             assert not re.findall(r"^\s+static (?:bool|int|unsigned|size_t) \w+ = .*", f.read(), re.M), path
+
+
+RACE = """
+#include <chrono>
+#include <thread>
+#include "per_device.h"
+// Two callers want 1000 and 2000 of an attribute; the larger one's setter waits for the smaller one to be through, if it can be.
+extern "C" int lost() {
+    static moe_host::PerDevice smem;
+    std::atomic<int> attribute{0}, larger_sets{0}, smaller_is_through{0};
+    auto until = [](std::atomic<int>& flag) {
+        for (int i = 0; i < 200 && !flag; i++) std::this_thread::sleep_for(std::chrono::milliseconds(1));
+    };
+    std::thread larger([&] {
+        smem.reach(0, 2000, [&](int n) {
+            attribute = n;
+            larger_sets = 1;
+            until(smaller_is_through);
+            return true;
+        });
+    });
+    until(larger_sets);
+    smem.reach(0, 1000, [&](int n) {
+        attribute = n;
+        return true;
+    });
+    smaller_is_through = 1;
+    larger.join();
+    smem.reach(0, 2000, [&](int n) {
+        attribute = n;
+        return true;
+    });
+    return 2000 - attribute;
+}
+"""
+
+
+def test_two_threads_with_different_values(tmp_path):
+    """The attribute is never below what the table says: a smaller value does not come between a larger one's setting and its
+    note (launches that want the larger one would fail from then on)."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    src, so = str(tmp_path / "t.cpp"), str(tmp_path / "t.so")
+    with open(src, "w") as f:
+        f.write(RACE)
+    subprocess.check_call([cxx, "-std=c++17", "-O2", "-shared", "-fPIC", "-pthread", "-I", CSRC, src, "-o", so])
+    assert C.CDLL(so).lost() == 0
