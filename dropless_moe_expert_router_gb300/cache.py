@@ -38,7 +38,9 @@ class SequenceCache:
         moves = [torch.empty(pages // 2, dtype=i32, device=dev) for _ in range(2)]
         self._compact = api.CacheCompact(self.table, *moves, self.used)
         self._own = torch.arange(sequences, dtype=i32, device=dev)
-        self._none, self._zero = torch.full_like(self.lengths, -1), torch.zeros_like(self.lengths)
+        self._none = torch.full_like(self.lengths, -1)
+        self._fits = torch.zeros(1, dtype=torch.bool, device=dev)
+        self._parents, self._src = torch.empty_like(self.lengths), torch.empty_like(self.lengths)
         self._pages_workspace = api.moe_cache_pages_workspace(pages, sequences, dev)
         self._attention_workspace = {}       # by the number of query heads
         self._beam_workspace = {}            # by the logits' shape and type
@@ -47,17 +49,19 @@ class SequenceCache:
         """Slot i goes on from slot parents[i] ([sequences] int32 on the device; -1: no sequence, its pages become free; a slot
         that had none begins an empty one; None: every active slot from itself), with room for `room` more positions (an
         int, or [sequences] int32). Sequences that go on from one parent share its pages but the one they write next. If
-        the pools have too few pages, MOE_DEVERR_NO_PAGE is set and what does not fit is not stored."""
+        the pools have too few pages, MOE_DEVERR_NO_PAGE is set and the step is not made: the cache stays as it was (`used`: the
+        pages that it would take) and no slot is active, so that append, attend and grow do nothing."""
         if parents is None:
             parents = torch.where(self.active, self._own, self._none)
         f = api.moe_cache_fork(self.table, self.lengths, parents, self.pages, self.page_size, room=room, out=self._fork,
                                workspace=self._pages_workspace)
-        api.moe_cache_copy_pages(self.layers, f.src, f.dst)
-        self.table.copy_(f.table)
-        self.lengths.copy_(f.lengths)
-        torch.ge(parents, 0, out=self.active)
+        fits = torch.le(f.used, self.pages, out=self._fits)
+        api.moe_cache_copy_pages(self.layers, torch.where(fits, f.src, self._none, out=self._src), f.dst)
+        torch.where(fits, f.table, self.table, out=self.table)
+        torch.where(fits, f.lengths, self.lengths, out=self.lengths)
+        torch.ge(torch.where(fits, parents, self._none, out=self._parents), 0, out=self.active)
         torch.where(self.active, self.lengths, self._none, out=self.positions)
-        torch.where(self.active, self.lengths + 1, self._zero, out=self.seen)
+        torch.add(self.positions, 1, out=self.seen)
 
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor) -> None:
         """The step's keys and values, [sequences, heads, dim] bf16, slot by slot."""

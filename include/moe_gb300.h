@@ -665,8 +665,10 @@ moe_status moe_paged_attention(const void *q, long long q_stride, int B, int q_h
  * nothing is); the row that keeps a shared page is the one with most positions in it, then the
  * first. The pages behind are free ones too (up to M). Free pages go out in ascending order, to
  * rows in ascending order, the copied page first. Pages that no row names any more are free.
- * *used: the pages named in the end, and those that were missing (then *used > pages,
- * MOE_DEVERR_NO_PAGE is set and the entries stay -1). Outputs must not overlap inputs.
+ * *used: the pages named in the end, and those that were missing: then *used > pages and
+ * MOE_DEVERR_NO_PAGE is set, and the entries are -1, that of a last page that could not be copied
+ * among them, so the new row has lost the positions in it. table and lengths still have all; a caller
+ * that finds *used > pages copies nothing and goes on from those. Outputs must not overlap inputs.
  * Requires (page_size + 1) * S_new < 2^31, M * S_new < 2^31 (compact: M * S).
  *
  * moe_cache_compact: the named pages renumbered to 0 .. *used - 1: the i-th page at or above

@@ -242,3 +242,49 @@ def test_refusals():
         cache.select(torch.zeros((1, 3, V), device="cuda"), torch.zeros((1, 3), device="cuda"))
     with pytest.raises(ValueError):
         cache.append(0, x.view(2, 4, 64), x.view(2, 4, 64))
+
+
+def test_a_step_that_finds_too_few_pages():
+    """Nothing that was stored is lost, nothing is written, and the step is made once there is room."""
+    cache = SequenceCache(2, 3, pages=5, heads=1, page_size=4, dim=32, max_length=16)
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def rand(n):
+        return torch.randn((n, 1, 32), generator=g, device="cuda").to(BF)
+
+    def parents(*p):
+        return torch.tensor(p, dtype=I32, device="cuda")
+    room = parents(6, 3, 0)
+    cache.advance(parents(0, 1, -1), room=room)
+    rows, pos = parents(*[0] * 6 + [1] * 3), parents(*range(6), *range(3))
+    data = [(rand(9), rand(9)) for _ in range(2)]
+    for layer, (k, v) in enumerate(data):
+        cache.write(layer, k, v, rows, pos)
+    cache.grow(room)
+
+    def stored():
+        return all(torch.equal(a, b) for layer in range(2) for a, b in zip(cache.read(layer, rows, pos), data[layer]))
+    assert stored() and cache.lengths.tolist() == [6, 3, 0] and api.moe_get_device_errors() == 0
+    table, pools = cache.table.clone(), [t.clone() for c in cache.layers for t in (c.k, c.v)]
+    # slots 0 and 2 go on from slot 0, slot 1 is given up: of its last page there is to be a copy, and 20 positions more
+    cache.advance(parents(0, -1, 0), room=20)
+    assert api.moe_get_device_errors() == api.MOE_DEVERR_NO_PAGE and cache.used.item() > cache.pages
+    assert torch.equal(cache.table, table) and cache.lengths.tolist() == [6, 3, 0] and not cache.active.any()
+    cache.append(0, rand(3), rand(3))                         # a step that does not know yet
+    assert not cache.attend(0, rand(3)).any()
+    cache.grow()
+    assert cache.lengths.tolist() == [6, 3, 0] and stored()
+    assert all(torch.equal(a, b) for a, b in zip(pools, (t for c in cache.layers for t in (c.k, c.v))))
+    assert api.moe_get_device_errors() == 0
+    cache.advance(parents(0, -1, 0))                          # one position more each: the copy's page is there
+    assert cache.active.tolist() == [True, False, True] and cache.positions.tolist() == [6, -1, 6]
+    new = rand(3)
+    for layer in range(2):
+        cache.append(layer, new, new)
+    cache.grow()
+    assert cache.lengths.tolist() == [7, 0, 7] and api.moe_get_device_errors() == 0
+    for slot in (0, 2):
+        for layer in range(2):
+            k, v = cache.read(layer, parents(*[slot] * 7), parents(*range(7)))
+            assert torch.equal(k, torch.cat([data[layer][0][:6], new[slot:slot + 1]]))
+            assert torch.equal(v, torch.cat([data[layer][1][:6], new[slot:slot + 1]]))
