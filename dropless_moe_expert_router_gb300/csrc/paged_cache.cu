@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(PG_THREADS) cache_fork_kernel(const __grid_con
         a.dst[i] = to;
     }
     if (thread == 0) {
-        *a.used = a.pages - free_all + wanted;
+        *a.used = (int)min((long long)a.pages - free_all + wanted, 0x7fffffffll);
         if (wanted > free_all) raise_device_error(MOE_DEVERR_NO_PAGE);
     }
 }
@@ -635,6 +635,7 @@ extern "C" size_t moe_cache_pages_workspace_size(int pages, int rows) {
 
 static moe_status pages_check(int S, int M, int rows, int pages, const void* workspace, size_t workspace_bytes) {
     if (S < 0 || M < 1 || rows < 0 || pages < 1) return MOE_ERR_INVALID_ARG;
+    if (pages > 1 << 30) return MOE_ERR_UNSUPPORTED;                   // (strides over them are counted in 32 bits)
     if (!workspace || workspace_bytes < moe_cache_pages_workspace_size(pages, rows)) return MOE_ERR_WORKSPACE;
     return moe_host::aligned(workspace, 16) ? MOE_OK : MOE_ERR_ALIGNMENT;
 }

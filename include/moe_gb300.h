@@ -669,7 +669,7 @@ moe_status moe_paged_attention(const void *q, long long q_stride, int B, int q_h
  * MOE_DEVERR_NO_PAGE is set, and the entries are -1, that of a last page that could not be copied
  * among them, so the new row has lost the positions in it. table and lengths still have all; a caller
  * that finds *used > pages copies nothing and goes on from those. Outputs must not overlap inputs.
- * Requires (page_size + 1) * S_new < 2^31, M * S_new < 2^31 (compact: M * S).
+ * Requires (page_size + 1) * S_new < 2^31, M * S_new < 2^31 (compact: M * S), pages <= 2^30.
  *
  * moe_cache_compact: the named pages renumbered to 0 .. *used - 1: the i-th page at or above
  * *used goes to the i-th hole below it. new_table: the rows with the new numbers; src, dst

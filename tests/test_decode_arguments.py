@@ -133,6 +133,12 @@ def test_beams(lib):
     assert size(2, 65, 50, 4) == 0 and size(2, 3, 50, 65) == 0 and size(0, 3, 50, 4) > 0
 
 
+def test_more_pages_than_strides_over_them_can_count(lib):
+    """A stride of 8192 threads would pass 2^31 from the last pages on, and mark what lies before the workspace."""
+    for pages in ((1 << 30) + 1, (1 << 31) - 1):
+        assert _fork(lib, pages=pages) == 2 and _compact(lib, pages=pages) == 2
+
+
 # ------------------------------------------------------------------ devices
 class _Cuda(torch.Tensor):
     """A CPU tensor that says it is on the CUDA device `at`."""
