@@ -685,6 +685,7 @@ extern "C" moe_status moe_cache_copy_pages(void* const* tensors, const long long
     if (n < 0 || n_tensors < 0 || pages < 1) return MOE_ERR_INVALID_ARG;
     if (n > 0 && (!src || !dst)) return MOE_ERR_INVALID_ARG;
     if (n_tensors > 0 && (!tensors || !page_bytes)) return MOE_ERR_INVALID_ARG;
+    if (n > 1 << 30) return MOE_ERR_UNSUPPORTED;                       // (pairs are counted in 32 bits)
     for (int i = 0; i < n_tensors; i++) {
         if (!tensors[i] || page_bytes[i] < 1) return MOE_ERR_INVALID_ARG;
         if (page_bytes[i] > (1ll << 32)) return MOE_ERR_UNSUPPORTED;   // (pieces are counted in 32 bits)

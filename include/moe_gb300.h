@@ -676,7 +676,7 @@ moe_status moe_paged_attention(const void *q, long long q_stride, int B, int q_h
  * [pages / 2]: the moves, in order, -1 behind the last. A bad id in the table becomes -1. new_table
  * may be table.
  *
- * moe_cache_copy_pages: page dst[i] = page src[i] for n pairs, in n_tensors pools (host arrays of
+ * moe_cache_copy_pages: page dst[i] = page src[i] for n <= 2^30 pairs, in n_tensors pools (host arrays of
  * device pointers and bytes a page); pairs with -1 are skipped, ids outside [-1, pages) are
  * skipped and bad. No page may be the destination of two pairs, nor of one and the source of
  * another (the lists of the two calls above are so). The host arrays are read during the call only.

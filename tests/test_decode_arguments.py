@@ -139,6 +139,13 @@ def test_more_pages_than_strides_over_them_can_count(lib):
         assert _fork(lib, pages=pages) == 2 and _compact(lib, pages=pages) == 2
 
 
+def test_more_pairs_than_their_number_can_count(lib):
+    """The list's last 2048 pairs would be followed by those before its beginning."""
+    one = (C.c_void_p * 1)(4096), (C.c_longlong * 1)(64)
+    for n in ((1 << 30) + 1, (1 << 31) - 1):
+        assert lib.moe_cache_copy_pages(*one, 1, P, P, n, 5, None) == 2
+
+
 # ------------------------------------------------------------------ devices
 class _Cuda(torch.Tensor):
     """A CPU tensor that says it is on the CUDA device `at`."""
