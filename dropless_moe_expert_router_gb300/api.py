@@ -105,6 +105,12 @@ def _on(dev: int, t: Optional[torch.Tensor], name: str) -> None:
         raise ValueError(f"{name} must be on cuda:{dev}, the other tensors' device")
 
 
+def _int32(name: str, n: int) -> None:
+    """The library takes n as it is (ctypes would keep the low 32 bits of a larger one)."""
+    if not -0x80000000 <= n <= 0x7fffffff:
+        raise ValueError(f"{name} must be a 32-bit number, got {n}")
+
+
 def _id_code(dtype: torch.dtype) -> int:
     if dtype == torch.int16:
         return MOE_I16
@@ -1130,6 +1136,7 @@ def moe_cache_gather(cache: PagedCache, table: torch.Tensor, positions: torch.Te
 def moe_paged_attention_workspace(cache: PagedCache, B: int, q_heads: int, stream=None) -> torch.Tensor:
     """The workspace of moe_paged_attention for up to B sequences (uninitialised, reusable; stream: the one of the
     first call that uses it)."""
+    _int32("B", B), _int32("q_heads", q_heads)
     n = _lib.load().moe_paged_attention_workspace_size(B, q_heads, cache.heads, cache.dim)
     return _empty(int(n), torch.uint8, cache.k.device, stream)
 
@@ -1153,6 +1160,7 @@ def moe_paged_attention(q: torch.Tensor, cache: PagedCache, table: torch.Tensor,
     if S != B:
         raise ValueError(f"table must have {B} rows")
     window = min(window, (1 << 31) - 1)              # (all positions)
+    _int32("window", window)
     _like(lengths, "lengths", torch.int32, (B,), dev)
     if out is None:
         out = _empty((B, heads, dim), torch.bfloat16, q.device, stream)
@@ -1177,6 +1185,7 @@ def moe_paged_attention(q: torch.Tensor, cache: PagedCache, table: torch.Tensor,
 
 def moe_cache_pages_workspace(pages: int, rows: int, device, stream=None) -> torch.Tensor:
     """The workspace of moe_cache_fork (rows: of the new table) and moe_cache_compact."""
+    _int32("pages", pages), _int32("rows", rows)
     n = _lib.load().moe_cache_pages_workspace_size(pages, rows)
     return _empty(int(n), torch.uint8, torch.device(device), stream)
 
@@ -1209,8 +1218,7 @@ def moe_cache_fork(table: torch.Tensor, lengths: torch.Tensor, parents: Optional
         _like(rooms, "room", torch.int32, (n,), dev)
     elif not 0 <= room < 1 << 31:
         raise ValueError("room must be at least 0")
-    if pages >= 1 << 31 or page_size >= 1 << 31:
-        raise ValueError("pages and page_size must be below 2^31")
+    _int32("pages", pages), _int32("page_size", page_size)
     i32 = torch.int32
     if out is None:
         on = table.device
@@ -1246,8 +1254,7 @@ def moe_cache_compact(table: torch.Tensor, pages: int, *, out: Optional[CacheCom
     every layer's pools (moe_cache_copy_pages) before the new table is used. out.table may be the table itself."""
     dev = table.get_device()
     S, M = _table(table, dev)
-    if pages >= 1 << 31:
-        raise ValueError("pages must be below 2^31")
+    _int32("pages", pages)
     shapes = ((S, M), (pages // 2,), (pages // 2,), (1,))
     if out is None:
         out = CacheCompact(*[_empty(shape, torch.int32, table.device, stream) for shape in shapes])
@@ -1306,6 +1313,7 @@ class BeamSelected(NamedTuple):
 def moe_beam_select_workspace(logits: torch.Tensor, K: int, stream=None) -> torch.Tensor:
     """The workspace of moe_beam_select for logits of this shape (uninitialised, reusable)."""
     N, W, V = logits.shape
+    _int32("K", K)
     return _empty(int(_lib.load().moe_beam_select_workspace_size(N, W, V, K)), torch.uint8, logits.device, stream)
 
 
@@ -1321,8 +1329,7 @@ def moe_beam_select(logits: torch.Tensor, scores: torch.Tensor, K: int, *, done:
     code = _float_code(logits, "logits")
     _like(scores, "scores", torch.float32, (N, W), dev)
     _like(done, "done", torch.bool, (N, W), dev)
-    if pad >= 1 << 31 or K >= 1 << 31:
-        raise ValueError("pad and K must be below 2^31")
+    _int32("pad", pad), _int32("K", K)
     if out is None:
         out = BeamSelected(_empty((N, K), torch.float32, logits.device, stream),
                            _empty((N, K), torch.int32, logits.device, stream),

@@ -219,3 +219,32 @@ def test_devices(no_call):
         logits, scores, 4, done=done, workspace=workspace, out=api.BeamSelected(**{k[1:]: v for k, v in out.items()})),
         dict(logits=_t((2, 3, 50), FL), scores=_t((2, 3), FL), done=_t((2, 3), torch.bool), workspace=_t((64,), U8),
              oscores=_t((2, 4), FL), oparents=_t((2, 4), I32), otokens=_t((2, 4), I32)))
+
+
+@pytest.mark.parametrize("big", [1 << 32, -(1 << 32), (1 << 31), -(1 << 31) - 1])
+def test_numbers_that_32_bits_do_not_hold(no_call, big):
+    """big + 5 would reach the library as 5, or with another sign."""
+    BF, I32, FL = torch.bfloat16, torch.int32, torch.float32
+    n = big + 5 if abs(big) == 1 << 32 else big
+    cache = api.PagedCache("bf16", 5, 2, 4, 32, _t((5, 2, 4, 32), BF), None, _t((5, 2, 4, 32), BF), None)
+    q, table, lengths = _t((3, 4, 32), BF), _t((3, 2), I32), _t((3,), I32)
+    given = dict(out=_t((3, 4, 32), BF), lse=_t((3, 4), FL), workspace=_t((64,), torch.uint8))
+    if n < 0:                                                 # (above: all positions)
+        with pytest.raises(ValueError):
+            api.moe_paged_attention(q, cache, table, lengths, window=n, **given)
+    fork = api.CacheFork(_t((3, 2), I32), *[_t((3,), I32)] * 3, _t((1,), I32))
+    for pages, page_size, room in ((n, 4, 1), (5, n, 1), (5, 4, n)):
+        with pytest.raises(ValueError):
+            api.moe_cache_fork(table, lengths, None, pages, page_size, room=room, out=fork, workspace=given["workspace"])
+    with pytest.raises(ValueError):
+        api.moe_cache_compact(table, n, workspace=given["workspace"])
+    logits, scores = _t((2, 3, 50), FL), _t((2, 3), FL)
+    best = api.BeamSelected(_t((2, 4), FL), _t((2, 4), I32), _t((2, 4), I32))
+    for K, pad in ((4, n), (n, 0)):
+        with pytest.raises(ValueError):
+            api.moe_beam_select(logits, scores, K, pad=pad, out=best, workspace=given["workspace"])
+    for call in (lambda: api.moe_paged_attention_workspace(cache, n, 4), lambda: api.moe_paged_attention_workspace(cache, 3, n),
+                 lambda: api.moe_cache_pages_workspace(n, 3, "cpu"), lambda: api.moe_cache_pages_workspace(5, n, "cpu"),
+                 lambda: api.moe_beam_select_workspace(torch.zeros((2, 3, 50)), n)):
+        with pytest.raises(ValueError):
+            call()
