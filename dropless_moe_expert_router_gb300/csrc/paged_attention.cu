@@ -24,6 +24,11 @@
 // kept relative to; fp16 weights are scaled by 2^15, so that one loses bits only below 2^-29 of the largest. A tile
 // whose scales span more than 2^6 below that takes bf16 values and weights, which have fp32's range.
 //
+// A bf16 weight is 8 bits: rounded to them, weights would add nearly as much to the outputs' error as the outputs' own rounding does
+// (one sequence of 131072: 0.0020 of the outputs, root mean square, in place of 0.0017). So it is two bf16, 16 bits, and two
+// products (that sequence 91.7 -> 92.2 us, 64 of 1 to 8192 50.3 -> 50.9; 32 query heads a key head, which the products bound, 84
+// -> 93). One fp16, 11 bits, adds 0.4 % of that and stays one: the MXFP8 kernel is bound by its instructions.
+//
 // Measured (one GB300, GPU time of the call with the join): bf16, 32 x 16384 positions of 8 key heads of 128, 32 query heads
 // 321 us = 6.70 TB/s of the cache's bytes (a plain copy runs at 6.78); one sequence of 131072 90 us, of which the join
 // is 5 to 6; 64 sequences of 1 to 8192 50 us (38 at the copy's rate). MXFP8, the 32 x 16384: 182 us = 6.1 TB/s, near what DRAM gives
@@ -175,6 +180,14 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
     }
     const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&b);
+}
+// Two weights as two bf16 each, 16 bits of them in all: cut off, and what is left. That is never 0 beside a first part that is
+// not, so that an infinite value times both stays what it is.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& first, uint32_t& left) {
+    const uint32_t cx = __float_as_uint(x) & 0xffff0000u, cy = __float_as_uint(y) & 0xffff0000u;
+    const float fx = __uint_as_float(cx), fy = __uint_as_float(cy);
+    first = (cx >> 16) | cy;
+    left = pack2<false>(fmaxf(x - fx, fx * 0x1p-24f), fmaxf(y - fy, fy * 0x1p-24f));
 }
 template <bool F16>
 __device__ __forceinline__ uint32_t times2(uint32_t x, uint32_t y) {
@@ -684,30 +697,48 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                 const int row = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
                 for (int x = 0; x < C::SUB; x++) {
-                    uint32_t b0[NB], b1[NB];
+                    uint32_t b0[NB][2], b1[NB][2];
 #pragma unroll
                     for (int nb = 0; nb < NB; nb++) {
-                        b0[nb] = transposed(pack2<false>(s[x][nb][0], s[x][nb][1]));
-                        b1[nb] = transposed(pack2<false>(s[x][nb][2], s[x][nb][3]));
+                        split2(s[x][nb][0], s[x][nb][1], b0[nb][0], b0[nb][1]);
+                        split2(s[x][nb][2], s[x][nb][3], b1[nb][0], b1[nb][1]);
+#pragma unroll
+                        for (int w = 0; w < 2; w++) {
+                            b0[nb][w] = transposed(b0[nb][w]);
+                            b1[nb][w] = transposed(b1[nb][w]);
+                        }
                     }
 #pragma unroll
                     for (int d = 0; d < DP / 16; d++) {
                         uint32_t f[4];
                         ldmatrix_t(f, vt + (x * 16 + row) * C::ROW + (((2 * d + ((lane >> 3) & 1)) ^ (row & 7)) * 16));
 #pragma unroll
-                        for (int nb = 0; nb < NB; nb++) mma<false>(o[nb][d], f, b0[nb], b1[nb]);
+                        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                            for (int w = 0; w < 2; w++) mma<false>(o[nb][d], f, b0[nb][w], b1[nb][w]);
                     }
                 }
             } else {
                 auto values = [&](auto wide_tag) {
                     constexpr bool F16 = !decltype(wide_tag)::value;
+                    constexpr int PARTS = F16 ? 1 : 2;                 // of a weight
 #pragma unroll
                     for (int x = 0; x < C::SUB; x++) {
-                        uint32_t b0[NB], b1[NB];
+                        uint32_t b0[NB][PARTS], b1[NB][PARTS];
 #pragma unroll
                         for (int nb = 0; nb < NB; nb++) {
-                            b0[nb] = transposed(pack2<F16>(s[x][nb][0], s[x][nb][1]));
-                            b1[nb] = transposed(pack2<F16>(s[x][nb][2], s[x][nb][3]));
+                            if constexpr (F16) {
+                                b0[nb][0] = pack2<true>(s[x][nb][0], s[x][nb][1]);
+                                b1[nb][0] = pack2<true>(s[x][nb][2], s[x][nb][3]);
+                            } else {
+                                split2(s[x][nb][0], s[x][nb][1], b0[nb][0], b0[nb][1]);
+                                split2(s[x][nb][2], s[x][nb][3], b1[nb][0], b1[nb][1]);
+                            }
+#pragma unroll
+                            for (int w = 0; w < PARTS; w++) {
+                                b0[nb][w] = transposed(b0[nb][w]);
+                                b1[nb][w] = transposed(b1[nb][w]);
+                            }
                         }
                         uint32_t factor0[DP / 32], factor1[DP / 32];   // of rows 2j, 2j + 1 and 2j + 8, 2j + 9, two 16-bit numbers each
                         const uint8_t* const factors = prep + C::TILE * (DP / 32) * 4 + (x * 8 + j) * (DP / 32) * 4;
@@ -723,12 +754,14 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                                 const int sw = DP == 64 ? ((row >> 1) & 1) << 1 : ((row >> 1) & 3) << 1;
                                 c[e] = get<uint32_t>(tile + (C::TILE + x * 16 + row) * C::ROW + (((2 * i + (r8 >> 2)) ^ sw) * 16) + (r8 & 3) * 4);
                             }
-                            uint32_t p0[NB], p1[NB];
+                            uint32_t p0[NB][PARTS], p1[NB][PARTS];
 #pragma unroll
-                            for (int nb = 0; nb < NB; nb++) {
-                                p0[nb] = times2<F16>(b0[nb], f0);
-                                p1[nb] = times2<F16>(b1[nb], f1);
-                            }
+                            for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                                for (int w = 0; w < PARTS; w++) {
+                                    p0[nb][w] = times2<F16>(b0[nb][w], f0);
+                                    p1[nb][w] = times2<F16>(b1[nb][w], f1);
+                                }
 #pragma unroll
                             for (int h = 0; h < 2; h++) {  // codes 4 r8 + 2h and 4 r8 + 2h + 1: rows r8 and r8 + 8 of the operand
                                 uint32_t f[4];
@@ -740,7 +773,9 @@ __global__ void __launch_bounds__(PA_THREADS, (Cfg<FP8, DP, NB>::CTAS)) attentio
                                     for (int e = 0; e < 4; e++) f[e] = to_bf16x2(f[e]);
                                 }
 #pragma unroll
-                                for (int nb = 0; nb < NB; nb++) mma<F16>(o[nb][2 * i + h], f, p0[nb], p1[nb]);
+                                for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                                    for (int w = 0; w < PARTS; w++) mma<F16>(o[nb][2 * i + h], f, p0[nb][w], p1[nb][w]);
                             }
                         }
                     }

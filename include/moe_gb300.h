@@ -637,9 +637,9 @@ moe_status moe_cache_gather(void *k, void *v, int n, const int32_t *rows, const 
  *   lse = m + ln l
  * out [B, q_heads, dim] bf16, lse [B, q_heads] fp32 (NULL to skip). Without a position: out 0,
  * lse -inf. What lies in the pages beside these positions does not matter (NaN among it). Sums,
- * maxima and the joined parts are fp32; the weights exp(s - m) are rounded to 16 bits (bf16
- * beside bf16 values, fp16 beside MXFP8 ones) before they meet the values, l before
- * that. Outputs depend on the sizes, lengths and the device, not on timing. Requires B <= 65535,
+ * maxima and the joined parts are fp32; the weights exp(s - m) meet the values as two bf16 (16 bits)
+ * beside bf16 values and where the scales of MXFP8 ones lie far apart, as fp16 (11 bits) beside other
+ * MXFP8 ones; l is summed before that. Outputs depend on the sizes, lengths and the device, not on timing. Requires B <= 65535,
  * q_heads / heads <= 1024, finite scale, window >= 0. workspace:
  * moe_paged_attention_workspace_size bytes (0 for refused sizes), 16-byte aligned, not
  * initialised; calls that share one must not overlap. */

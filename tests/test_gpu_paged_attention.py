@@ -15,6 +15,7 @@ from dropless_moe_expert_router_gb300.api import MoeError
 
 pytestmark = pytest.mark.gpu
 BF, F32, I32, D64 = torch.bfloat16, torch.float32, torch.int32, torch.float64
+INF = math.inf
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -456,3 +457,56 @@ def test_scales_that_begin_off_a_word(dim, offset):
         moved.append(buf[offset:offset + t.numel()].view(t.shape).copy_(t))
     o2, l2 = api.moe_paged_attention(q, cache._replace(k_scales=moved[0], v_scales=moved[1]), table, lens)
     assert torch.equal(o2, out) and torch.equal(l2, lse) and api.moe_get_device_errors() == 0
+
+
+@pytest.mark.parametrize("precision,apart", [("bf16", False), ("mxfp8", False), ("mxfp8", True)])
+@pytest.mark.parametrize("dim,q_heads", [(64, 1), (128, 12), (256, 3), (128, 20)])
+def test_weights_keep_their_bits(dim, q_heads, precision, apart):
+    """Positions whose weights are all the same, and one whose value takes away what they sum to: a rounding of the weights is
+    all that is left of the output. Bars: those of _check, with the weight's rounding 2^-16 (two bf16) in the place of 2^-8, or 2^-11
+    (fp16). apart: scales of the values further apart than fp16 weights take, which are 16 bits then, too."""
+    lengths = [40, 130, 7, 300, 64, 33, 90, 18, 250, 500] * 2
+    cache, table, _ = _cache(lengths, 1, dim, 16, precision)
+    rows = torch.cat([torch.full((n,), b, dtype=I32) for b, n in enumerate(lengths)]).cuda()
+    pos = torch.cat([torch.arange(n, dtype=I32) for n in lengths]).cuda()
+    first = pos == 0
+    c = 0.02 + 0.011 * rows.float()                           # scores of 0 and -c sqrt(dim): weights 1 and exp(-c sqrt(dim))
+    k = torch.where(first, torch.zeros_like(c), -c)[:, None, None].expand(-1, 1, dim).to(BF).contiguous()
+    w = torch.exp(k[:, 0, 0].double() * dim ** 0.5)
+    n = torch.tensor(lengths, device="cuda")[rows.long()].double()
+    v = torch.where(first, -(n - 1) * torch.exp(-c.to(BF).double() * dim ** 0.5), torch.ones_like(w))
+    v = v[:, None, None].expand(-1, 1, dim).to(BF).contiguous()
+    if apart:
+        v[pos % 5 == 3] *= 2.0 ** -20
+    api.moe_cache_append(k, v, cache, table, pos, rows=rows)
+    k, v = api.moe_cache_gather(cache, table, pos, rows=rows)
+    q = torch.ones((len(lengths), q_heads, dim), dtype=BF, device="cuda")
+    out, lse = api.moe_paged_attention(q, cache, table, torch.tensor(lengths, dtype=I32, device="cuda"))
+    at = 0
+    for b, n in enumerate(lengths):
+        kb, vb = k[at:at + n, 0].double(), v[at:at + n, 0].double()
+        at += n
+        s = q[b].double() @ kb.t() * dim ** -0.5
+        e = (dim + 4) * 2.0 ** -24 * s.abs().amax()
+        p = torch.softmax(s, 1)
+        ref, A = p @ vb, p @ vb.abs()
+        bar = ((2.0 ** -11 if precision == "mxfp8" and not apart else 2.0 ** -16) + 2 * e + 2.0 ** -12) * A + 2.0 ** -8 * ref.abs()
+        assert bool(((out[b].double() - ref).abs() <= bar).all()), b
+    assert api.moe_get_device_errors() == 0
+
+
+def test_infinite_values_stay_infinite():
+    lengths = [100, 300]
+    cache, table, dense = _cache(lengths, 1, 64, 16)
+    q = torch.ones((2, 4, 64), device="cuda", dtype=BF)
+    lens = torch.tensor(lengths, dtype=I32, device="cuda")
+    for at in (0, 7, 53, 99):
+        page, off = int(table[0, at // 16]), at % 16
+        cache.v[page, 0, off, 7], cache.v[page, 0, off, 8] = INF, -INF
+        out, _ = api.moe_paged_attention(q, cache, table, lens)
+        assert bool((out[0, :, 7] == INF).all() and (out[0, :, 8] == -INF).all()) and torch.isfinite(out[1]).all()
+        cache.v[page, 0, off, 7:9] = 0
+    one = _cache([1], 1, 64, 16)                              # (a weight of one: its second part would be 0)
+    one[0].v[one[1][0, 0], 0, 0, 7] = INF
+    out, _ = api.moe_paged_attention(q[:1], one[0], one[1], torch.ones(1, dtype=I32, device="cuda"))
+    assert bool((out[0, :, 7] == INF).all() and torch.isfinite(out[0, :, :7]).all())
