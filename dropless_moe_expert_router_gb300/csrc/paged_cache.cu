@@ -568,8 +568,11 @@ moe_status launch_pages(void (*one)(const Args), void (*many)(const Args), moe_h
 moe_status rows_call(RowsArgs a, moe_dtype dtype, bool write, moe_stream_t stream) {
     const long long total = (long long)a.n * 2 * a.c.heads * (a.c.dim / 8);
     const long long per_token = 2ll * a.c.heads * (a.c.dim / 8), beside = per_token < RW_THREADS ? RW_THREADS / per_token : 1;
-    // four tokens a thread (four loads in flight) where that still fills the device twice over; one, for latency, below
-    const int each = total >= 4ll * RW_THREADS * 2048 ? 4 : 1;
+    // Four tokens a thread (four loads in flight) from 512 blocks of one on; one, for latency, below. One against four, us, of
+    // tokens of 8 heads of 128 into MXFP8 and back: 64 3.1 3.1 / 3.6 3.6, 256 3.2 3.2 / 3.6 3.6, 512 (512 blocks) 3.7 3.6 / 3.6 3.2,
+    // 1024 4.1 4.1 / 3.7 3.7, 4096 11.3 11.5 / 8.7 8.3, 8192 20.4 20.7 / 15.5 13.5; bf16 into bf16: 256 3.1 / 3.1, 1024 3.7 / 3.7,
+    // 4096 11.4 / 8.9.
+    const int each = total >= 512ll * RW_THREADS ? 4 : 1;
     const long long ctas = (a.n + beside * each - 1) / (beside * each), rows = (per_token + RW_THREADS - 1) / RW_THREADS;
     if (rows > 65535) return MOE_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)ctas, (unsigned)rows);
