@@ -438,3 +438,41 @@ def test_fork_of_sequences_near_two_to_the_31():
         assert torch.equal(got.table, want) and got.lengths.tolist() == [n, n]
         assert got.src.tolist() == src and got.dst.tolist() == dst and got.used.item() == used
     assert api.moe_get_device_errors() == 0
+
+
+@pytest.mark.parametrize("precision", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("n,heads,dim,page", [(777, 8, 128, 16), (20_003, 1, 32, 7), (2501, 3, 96, 5), (90, 24, 256, 33), (513, 8, 128, 1)])
+def test_append_and_gather_of_many_tokens(n, heads, dim, page, precision):
+    """Sizes at which a thread has four tokens, the last ones fewer; slices of one projection; padding; other rows as they were."""
+    M = (n + page - 1) // page
+    g = torch.Generator(device="cuda").manual_seed(n)
+    table = torch.randperm(M + 3, generator=g, device="cuda")[:M].to(I32)[None].contiguous()
+    pos = torch.randperm(n, generator=g, device="cuda").to(I32)
+    pos[::7] = -1
+    rows = torch.where(torch.arange(n, device="cuda") % 11 == 3, -1, 0).to(I32)
+    qkv = torch.randn((n, 3 * heads, dim), generator=g, device="cuda").to(BF)
+    k, v = qkv[:, heads:2 * heads], qkv[:, 2 * heads:]
+    cache = api.cache_buffers(M + 3, heads, page, dim, "cuda", precision)
+    want = {}
+    for name in ("k", "v", "k_scales", "v_scales"):
+        t = getattr(cache, name)
+        if t is not None:
+            t.view(U8).random_(0, 100)
+            want[name] = t.clone()
+    api.moe_cache_append(k, v, cache, table, pos, rows=rows)
+    ok = (pos >= 0) & (rows >= 0)
+    p, o = table[0, (pos[ok] // page).long()].long(), (pos[ok] % page).long()
+    back = {}
+    for name, t in (("k", k), ("v", v)):
+        codes, byte = _quant(t) if precision == "mxfp8" else (t, None)
+        want[name][p, :, o] = codes[ok]
+        if byte is not None:
+            want[name + "_scales"][p, :, o] = byte[ok]
+            codes = (codes.view(torch.float8_e4m3fn).float().unflatten(-1, (dim // 32, 32)) *
+                     torch.exp2(byte.float() - 127).unsqueeze(-1)).flatten(-2).to(BF)
+        back[name] = codes.masked_fill(~ok[:, None, None], 0)
+    for name, t in want.items():
+        assert torch.equal(getattr(cache, name).view(U8), t.view(U8)), name
+    gk, gv = api.moe_cache_gather(cache, table, pos, rows=rows)
+    assert torch.equal(gk, back["k"]) and torch.equal(gv, back["v"])
+    assert api.moe_get_device_errors() == 0
