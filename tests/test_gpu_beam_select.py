@@ -289,3 +289,23 @@ def test_a_search_does_not_depend_on_its_place(dtype, V):
     assert torch.equal(o.scores, alone.scores.expand(N, 16)) and torch.equal(o.tokens, alone.tokens.expand(N, 16))
     assert torch.equal(o.parents - base, alone.parents.expand(N, 16))
     assert api.moe_get_device_errors() == 0
+
+
+@pytest.mark.parametrize("N,W,V,dtype", [(260, 1, (1 << 24) - 1, BF), (2, 3, (1 << 24) - 1, F32), (1, 2, (1 << 24) - 8, BF)])
+def test_the_largest_vocabulary(N, W, V, dtype):
+    """Rows of the most logits, off 16 bytes and on them; 260 of them lie past 2^32 logits."""
+    K = 24
+    logits = torch.empty((N, W, V), dtype=dtype, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(N))
+    scores = -8 * torch.rand((N, W), generator=torch.Generator(device="cuda").manual_seed(5), device="cuda")
+    if W > 1:
+        scores[:, 1:] = -1e4                                          # far behind: the first beam's tokens in their order
+    logits[-1, 0, [5, V - 1, V // 2]] = 20.0                          # ties, the row's last logit among them
+    o = api.moe_beam_select(logits, scores, K)
+    for n in sorted({0, 1, N // 2, N - 1} & set(range(N))):
+        x = logits[n, 0].float()
+        want, at = torch.sort(x, descending=True, stable=True)
+        assert torch.equal(o.tokens[n].long(), at[:K]) and bool((o.parents[n] == n * W).all()), n
+        ref = scores[n, 0].double() + want[:K].double() - torch.logsumexp(x.double(), 0)
+        assert bool(((o.scores[n].double() - ref).abs() <= BAR + 2.0 ** -23 * ref.abs()).all()), n
+    assert o.tokens[-1, :3].tolist() == [5, V // 2, V - 1]
+    assert api.moe_get_device_errors() == 0
