@@ -27,20 +27,22 @@ class SequenceCache:
         self.sequences, self.pages, self.page_size = sequences, pages, page_size
         columns = (max_length + page_size - 1) // page_size
         i32 = torch.int32
-        self.table = torch.full((sequences, columns), -1, dtype=i32, device=dev)
-        self.lengths = torch.zeros(sequences, dtype=i32, device=dev)
-        self.active = torch.zeros(sequences, dtype=torch.bool, device=dev)     # sequences that the next step is of
+        # table and lengths side by side, so that a step takes over both at once
+        self._state, self._new = (torch.full((sequences * columns + sequences,), -1, dtype=i32, device=dev) for _ in range(2))
+        (self.table, self.lengths), new = ((t[:-sequences].view(sequences, columns), t[-sequences:]) for t in (self._state, self._new))
+        self.lengths.zero_()
+        self.active = torch.zeros(sequences, dtype=torch.bool, device=dev)     # slots that have a sequence
         self.positions = torch.full((sequences,), -1, dtype=i32, device=dev)   # where it writes (-1: no sequence)
         self.seen = torch.zeros(sequences, dtype=i32, device=dev)              # how far it reads
         self.used = torch.zeros(1, dtype=i32, device=dev)                      # pages, of the last advance or compact
-        new = [torch.empty(shape, dtype=i32, device=dev) for shape in ((sequences, columns),) + ((sequences,),) * 3]
-        self._fork = api.CacheFork(*new, self.used)
+        self._fork = api.CacheFork(*new, *[torch.empty_like(self.lengths) for _ in range(2)], self.used)
         moves = [torch.empty(pages // 2, dtype=i32, device=dev) for _ in range(2)]
         self._compact = api.CacheCompact(self.table, *moves, self.used)
         self._own = torch.arange(sequences, dtype=i32, device=dev)
         self._none = torch.full_like(self.lengths, -1)
         self._fits = torch.zeros(1, dtype=torch.bool, device=dev)
-        self._parents, self._src = torch.empty_like(self.lengths), torch.empty_like(self.lengths)
+        self._goes, self._writes = torch.zeros_like(self.active), torch.zeros_like(self.active)
+        self._src = torch.empty_like(self.lengths)
         self._pages_workspace = api.moe_cache_pages_workspace(pages, sequences, dev)
         self._attention_workspace = {}       # by the number of query heads
         self._beam_workspace = {}            # by the logits' shape and type
@@ -50,17 +52,18 @@ class SequenceCache:
         that had none begins an empty one; None: every active slot from itself), with room for `room` more positions (an
         int, or [sequences] int32). Sequences that go on from one parent share its pages but the one they write next. If
         the pools have too few pages, MOE_DEVERR_NO_PAGE is set and the step is not made: the cache stays as it was (`used`: the
-        pages that it would take) and no slot is active, so that append, attend and grow do nothing."""
+        pages that it would take), and append, attend and grow do nothing until the next one."""
         if parents is None:
             parents = torch.where(self.active, self._own, self._none)
         f = api.moe_cache_fork(self.table, self.lengths, parents, self.pages, self.page_size, room=room, out=self._fork,
                                workspace=self._pages_workspace)
         fits = torch.le(f.used, self.pages, out=self._fits)
         api.moe_cache_copy_pages(self.layers, torch.where(fits, f.src, self._none, out=self._src), f.dst)
-        torch.where(fits, f.table, self.table, out=self.table)
-        torch.where(fits, f.lengths, self.lengths, out=self.lengths)
-        torch.ge(torch.where(fits, parents, self._none, out=self._parents), 0, out=self.active)
-        torch.where(self.active, self.lengths, self._none, out=self.positions)
+        torch.where(fits, self._new, self._state, out=self._state)
+        goes = torch.ge(parents, 0, out=self._goes)
+        torch.where(fits, goes, self.active, out=self.active)
+        torch.logical_and(goes, fits, out=self._writes)
+        torch.where(self._writes, self.lengths, self._none, out=self.positions)
         torch.add(self.positions, 1, out=self.seen)
 
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor) -> None:
@@ -88,8 +91,8 @@ class SequenceCache:
                                        workspace=workspace)[0]
 
     def grow(self, by=1) -> None:
-        """The positions that were written count: one per active slot, or `by` (an int or [sequences] int32)."""
-        torch.where(self.active, self.lengths + by, self.lengths, out=self.lengths)
+        """The positions that were written count: one per slot that the step is of, or `by` (an int or [sequences] int32)."""
+        torch.where(self._writes, self.lengths + by, self.lengths, out=self.lengths)
 
     def select(self, logits: torch.Tensor, scores: torch.Tensor, *, done: Optional[torch.Tensor] = None, pad: int = 0):
         """The beams that go on: logits [N, W, V] of N searches with W beams (N * W slots, a search's side by side), scores

@@ -269,7 +269,7 @@ def test_a_step_that_finds_too_few_pages():
     # slots 0 and 2 go on from slot 0, slot 1 is given up: of its last page there is to be a copy, and 20 positions more
     cache.advance(parents(0, -1, 0), room=20)
     assert api.moe_get_device_errors() == api.MOE_DEVERR_NO_PAGE and cache.used.item() > cache.pages
-    assert torch.equal(cache.table, table) and cache.lengths.tolist() == [6, 3, 0] and not cache.active.any()
+    assert torch.equal(cache.table, table) and cache.lengths.tolist() == [6, 3, 0] and cache.positions.tolist() == [-1] * 3
     cache.append(0, rand(3), rand(3))                         # a step that does not know yet
     assert not cache.attend(0, rand(3)).any()
     cache.grow()
@@ -288,3 +288,31 @@ def test_a_step_that_finds_too_few_pages():
             k, v = cache.read(layer, parents(*[slot] * 7), parents(*range(7)))
             assert torch.equal(k, torch.cat([data[layer][0][:6], new[slot:slot + 1]]))
             assert torch.equal(v, torch.cat([data[layer][1][:6], new[slot:slot + 1]]))
+
+
+def test_steps_of_every_slot_that_find_too_few_pages():
+    """Slots that go on from themselves find no page for a step or more, and all go on where they were when one is free."""
+    cache = SequenceCache(1, 3, pages=3, heads=1, page_size=2, dim=32, max_length=8)
+
+    def parents(*p):
+        return torch.tensor(p, dtype=I32, device="cuda")
+    cache.advance(parents(0, 1, 2))
+    kv = torch.randn((3, 1, 32), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(BF)
+    for n in (1, 2):
+        cache.append(0, kv, kv)
+        cache.grow()
+        if n == 1:
+            cache.advance()
+    for _ in range(3):                                        # three pages more are wanted, none is free
+        cache.advance()
+        assert api.moe_get_device_errors() == api.MOE_DEVERR_NO_PAGE
+        cache.append(0, kv, kv)
+        cache.grow()
+        assert cache.lengths.tolist() == [2, 2, 2] and cache.active.all() and cache.used.item() == 6
+    cache.advance(parents(0, -1, -1))
+    cache.append(0, kv, kv)
+    cache.grow()
+    assert cache.lengths.tolist() == [3, 0, 0] and cache.active.tolist() == [True, False, False]
+    k, v = cache.read(0, parents(0, 0, 0), parents(0, 1, 2))
+    assert torch.equal(k, kv[:1].expand(3, 1, 32)) and torch.equal(v, k)
+    assert api.moe_get_device_errors() == 0
