@@ -45,7 +45,7 @@ class SequenceCache:
         self._src = torch.empty_like(self.lengths)
         self._pages_workspace = api.moe_cache_pages_workspace(pages, sequences, dev)
         self._attention_workspace = {}       # by the number of query heads
-        self._beam_workspace = {}            # by the logits' shape and type
+        self._beam_workspace = {}            # by the logits' shape (its size is the same for both types)
 
     def advance(self, parents: Optional[torch.Tensor] = None, room=1) -> None:
         """Slot i goes on from slot parents[i] ([sequences] int32 on the device; -1: no sequence, its pages become free; a slot

@@ -19,9 +19,10 @@
 //    (this device's 64-bit units are slow: a logarithm and the sums took 5 us in them).
 //
 // Measured (one GB300, GPU time): 32 searches of 8 beams over 131072 bf16 logits, K = 16: 24.7-25.1 us (67 MB, 9.9 us at the copy's rate;
-// 131071 logits, rows off 16 bytes: 30.8), of which the first kernel takes 19, bound by the issue of its instructions (two packed adds, a packed product, two powers and
-// two unpackings for two logits are a third of them; thresholds and ranks of each stretch the most of the rest), and the second
-// 6 behind it, a chain of latencies. 1 search of 4 beams over 32000 fp32: 9 us.
+// 131071 logits, rows off 16 bytes: 31), of which the first kernel takes 19 and the second 6 behind it, a chain of latencies. The first issues 2.1 instructions a cycle of
+// 4; a fifth of its warps' waits are at the block's barriers (two a row for the threshold, three a look), the rest is spread over
+// reads of the ring, powers and fixed latencies. Two packed adds, a packed product, two powers and two unpackings for two logits are a third
+// of its instructions, thresholds and ranks of each stretch the most of the rest. 1 search of 4 beams over 32000 fp32: 9 us.
 #include "common.cuh"
 
 #include <math.h>

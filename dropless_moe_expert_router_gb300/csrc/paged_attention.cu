@@ -10,8 +10,8 @@
 // that is cut, each block leaves m, l and the unnormalised output in the workspace, and a second kernel, set up
 // while the first one runs, joins them in the blocks' order. So outputs do not depend on timing.
 //
-// A block's four warps work alone, 16 positions of a unit each: a ring of three tiles or more per warp is filled by 16-byte
-// asynchronous copies (rows anywhere, so pages may end inside a tile; absent rows are filled with zeros).
+// A block's four warps work alone, a tile of 16 or 32 positions of a unit each: a ring of tiles per warp (two of MXFP8 rows of 128
+// or 256, three to six of the others: what 24 KB hold) is filled by 16-byte asynchronous copies (rows anywhere, so pages may end inside a tile; absent rows are filled with zeros).
 // The products take the cache as the 16-row operand and the heads as the 8 columns, S^T = K Q^T and
 // O^T = V^T P^T, so that a key or value passes through one fragment once, whatever the group, and the running
 // maximum and scale of a head sit in the lanes that hold its column. P^T is the transpose of the fragment that S^T comes
@@ -30,9 +30,9 @@
 // -> 93). One fp16, 11 bits, adds 0.4 % of that and stays one: the MXFP8 kernel is bound by its instructions.
 //
 // Measured (one GB300, GPU time of the call with the join): bf16, 32 x 16384 positions of 8 key heads of 128, 32 query heads
-// 321 us = 6.70 TB/s of the cache's bytes (a plain copy runs at 6.78); one sequence of 131072 90 us, of which the join
-// is 5 to 6; 64 sequences of 1 to 8192 50 us (38 at the copy's rate). MXFP8, the 32 x 16384: 182 us = 6.1 TB/s, near what DRAM gives
-// (about 9 us are the beginning and the join) with 724 instructions a warp and 32 positions, 1.6 a cycle with 8 warps an SM;
+// 321-324 us = 6.63-6.69 TB/s of the cache's bytes (a plain copy runs at 6.78); one sequence of 131072 92 us, of which the join
+// is 5 to 6; 64 sequences of 1 to 8192 51 us (38 at the copy's rate). MXFP8, the 32 x 16384: 183 us = 6.0 TB/s, near what DRAM gives
+// (about 9 us are the beginning and the join) with 731 instructions a warp and 32 positions, 1.7 a cycle with 8 warps an SM;
 // 12 warps take 16-row tiles, and 249 us; a third stage of the ring changes nothing. One sequence of 100: 6.3 us.
 #include "common.cuh"
 #include "paged_cache.cuh"
@@ -79,6 +79,7 @@ struct Cfg {
     static constexpr int KV = 2 * TILE * ROW;
     static constexpr int STAGE = KV + (FP8 ? 2 * TILE * 16 : 0);   // and a 16-byte slot for each row's scales
     static constexpr int STAGES = DP == 256 && !FP8 ? 3 : (96 * 1024 / PA_WARPS) / STAGE > 6 ? 6 : (96 * 1024 / PA_WARPS) / STAGE;
+    static_assert(STAGES >= 2, "a tile is on its way while another is taken");
     static constexpr int PREP = FP8 ? DP / 32 * TILE * (4 + 2) : 0;  // a tile's scales as the products take them
     static constexpr int HALF = DP / 2;                        // elements joined at a time
     static constexpr int JOIN = PA_WARPS * 8 * (HALF + 4) * 4;

@@ -7,8 +7,9 @@
 // with the marks in shared memory where those fit and the table is not long, else as one cluster of eight blocks with
 // the marks in the workspace, phases parted by cluster barriers. So a whole call is one launch.
 //
-// Measured (one GB300): append of 64 tokens 2.8 us; 8192 tokens of 8 heads of 128 into MXFP8 13.4 us and back 13 us (7.5 us of bytes each
-// at the copy's rate; two waves of blocks, each a chain of position, table and row); fork of 4 beams 6 us, of 32 x 8 beams over
+// Measured (one GB300): append of 64 tokens 2.8 us; 8192 tokens of 8 heads of 128 into MXFP8 13.4 to 15.5 us and back 13 us (7.5 us of
+// bytes each at the copy's rate; 3.4 waves of blocks for the append, whose 52 registers let four of them on an SM, and 2.2 for the
+// gather, each a chain of position, table and row), bf16 14.0 and 14.3 (9.9); fork of 4 beams 6 us, of 32 x 8 beams over
 // 33,000 table entries 14.5 us; the copies of 88 pages in four layers 9 us, of 2,100 pages in two 24 to 33 us.
 #include "common.cuh"
 #include "paged_cache.cuh"

@@ -615,7 +615,8 @@ moe_status moe_grad_norm_clip(const void *const *grads, const long long *counts,
  * position at or past M * page_size or a row >= S is a bad id. The (page, offset) pairs of one
  * call must be distinct. MXFP8 quantises on the way. n <= 2^30.
  * moe_cache_gather: the same positions read back, k, v [n, heads, dim] bf16 contiguous
- * (MXFP8: code times scale, exact), zeros for the positions that are skipped or bad.
+ * (MXFP8: code times scale, exact within bf16's range), zeros for the positions that are skipped or
+ * bad.
  * ------------------------------------------------------------------------ */
 moe_status moe_cache_append(const void *k, const void *v, long long k_stride, long long v_stride,
                             int n, const int32_t *rows, const int32_t *positions,
@@ -639,7 +640,8 @@ moe_status moe_cache_gather(void *k, void *v, int n, const int32_t *rows, const 
  * lse -inf. What lies in the pages beside these positions does not matter (NaN among it). Sums,
  * maxima and the joined parts are fp32; the weights exp(s - m) meet the values as two bf16 (16 bits)
  * beside bf16 values and where the scales of MXFP8 ones lie far apart, as fp16 (11 bits) beside other
- * MXFP8 ones; l is summed before that. Outputs depend on the sizes, lengths and the device, not on timing. Requires B <= 65535,
+ * MXFP8 ones; l is summed before that. Sums of exp(s - m) |v| beyond fp32's range give infinities.
+ * Outputs depend on the sizes, lengths and the device, not on timing. Requires B <= 65535,
  * q_heads / heads <= 1024, finite scale, window >= 0. workspace:
  * moe_paged_attention_workspace_size bytes (0 for refused sizes), 16-byte aligned, not
  * initialised; calls that share one must not overlap. */
