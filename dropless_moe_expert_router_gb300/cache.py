@@ -32,7 +32,7 @@ class SequenceCache:
         (self.table, self.lengths), new = ((t[:-sequences].view(sequences, columns), t[-sequences:]) for t in (self._state, self._new))
         self.lengths.zero_()
         self.active = torch.zeros(sequences, dtype=torch.bool, device=dev)     # slots that have a sequence
-        self.positions = torch.full((sequences,), -1, dtype=i32, device=dev)   # where it writes (-1: no sequence)
+        self.positions = torch.full((sequences,), -1, dtype=i32, device=dev)   # where a step writes (-1: nowhere)
         self.seen = torch.zeros(sequences, dtype=i32, device=dev)              # how far it reads
         self.used = torch.zeros(1, dtype=i32, device=dev)                      # pages, of the last advance or compact
         self._fork = api.CacheFork(*new, *[torch.empty_like(self.lengths) for _ in range(2)], self.used)
